@@ -5,10 +5,13 @@ CUDA library.  There is no CPU fallback; if the library is missing this
 module raises instead of computing anything.
 
 Entry points keep the C names: ``treewy_verify``, ``treewy_commit``,
-``treewy_storeall_verify``, ``treewy_storeall_commit``, ``treewy_last_error``
-and ``treewy_version``.  ``TreewyBatch`` mirrors ``struct treewy_batch``;
+``treewy_storeall_verify``, ``treewy_storeall_commit``, ``treewy_extend``,
+``treewy_qk_norm``, ``treewy_copy_slots``, ``treewy_last_error`` and
+``treewy_version``.  ``TreewyBatch`` mirrors ``struct treewy_batch``;
 ``make_batch`` fills one from torch tensors (device memory and streams are
-PyTorch's; the library only receives raw pointers).
+PyTorch's; the library only receives raw pointers), as ``make_seqs``,
+``make_qk`` and ``make_slots`` fill the arguments of the three calls around
+verification.
 """
 from __future__ import annotations
 
@@ -30,11 +33,15 @@ STATUS_BAD_ACCEPTED = 4
 STATUS_BAD_SLOT = 8
 STATUS_TIMEOUT = 16
 STATUS_COMMIT_REFUSED = 32
+STATUS_BAD_POSITION = 64
+STATUS_SLOT_CLASH = 128
 
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
 FLAG_FORCE_GENERIC = 1
 FLAG_STATE_BF16 = 2
+NORM_L2 = 0
+NORM_RMS = 1
 MAX_NODES = 64
 
 
@@ -72,11 +79,35 @@ class TreewyBatch(ctypes.Structure):
     ]
 
 
+class TreewySeqs(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in
+                ("R", "H", "Hk", "dk", "dv", "max_len", "qkv_dtype", "o_dtype")] + [
+        (f, ctypes.c_int64) for f in ("T", "num_slots", "q_stride", "k_stride", "v_stride")] + [
+        (f, ctypes.c_void_p) for f in
+        ("seq_offset", "q", "k", "v", "alpha", "beta", "state", "state_slot", "fresh", "o", "status")] + [
+        ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class TreewyQk(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64)] + [(f, ctypes.c_int32) for f in
+                ("Hq", "Hk", "d", "dtype", "norm", "rope_dims", "interleaved", "q_repeat", "k_repeat")] + [
+        (f, ctypes.c_float) for f in ("eps", "q_scale", "k_scale")] + [
+        (f, ctypes.c_int64) for f in ("q_stride", "k_stride", "rope_rows")] + [
+        (f, ctypes.c_void_p) for f in
+        ("q", "k", "q_weight", "k_weight", "rope", "position", "q_out", "k_out", "status")]
+
+
+class TreewySlots(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("layers", ctypes.c_int32)] + [
+        (f, ctypes.c_int64) for f in ("num_slots", "slot_bytes", "layer_stride")] + [
+        (f, ctypes.c_void_p) for f in ("state", "src", "dst", "status")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 ENTRY_POINTS = ("treewy_verify", "treewy_commit", "treewy_commit_verify", "treewy_storeall_verify",
-                "treewy_storeall_commit", "treewy_selftest_wait_timeout", "treewy_last_error",
-                "treewy_version")
+                "treewy_storeall_commit", "treewy_extend", "treewy_qk_norm", "treewy_copy_slots",
+                "treewy_selftest_wait_timeout", "treewy_last_error", "treewy_version")
 
 
 def load(path: Optional[str] = None) -> ctypes.CDLL:
@@ -97,9 +128,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.treewy_commit_verify.argtypes = [bp, vp, bp, vp]
     lib.treewy_storeall_verify.argtypes = [bp, vp, vp]
     lib.treewy_storeall_commit.argtypes = [bp, vp, vp, vp]
+    lib.treewy_extend.argtypes = [ctypes.POINTER(TreewySeqs), vp]
+    lib.treewy_qk_norm.argtypes = [ctypes.POINTER(TreewyQk), vp]
+    lib.treewy_copy_slots.argtypes = [ctypes.POINTER(TreewySlots), vp]
     lib.treewy_selftest_wait_timeout.argtypes = [vp, ctypes.c_uint32, vp]
     for name in ("treewy_verify", "treewy_commit", "treewy_commit_verify", "treewy_storeall_verify",
-                 "treewy_storeall_commit", "treewy_selftest_wait_timeout"):
+                 "treewy_storeall_commit", "treewy_extend", "treewy_qk_norm", "treewy_copy_slots",
+                 "treewy_selftest_wait_timeout"):
         getattr(lib, name).restype = ctypes.c_int
     lib.treewy_last_error.argtypes = []
     lib.treewy_last_error.restype = ctypes.c_char_p
@@ -175,6 +210,21 @@ def treewy_storeall_commit(batch: TreewyBatch, snapshots, accepted, stream=None)
                                          _stream_handle(stream)))
 
 
+def treewy_extend(seqs: TreewySeqs, stream=None) -> None:
+    """The gated delta rule over every sequence's new tokens, from and into its state slot."""
+    _check(load().treewy_extend(ctypes.byref(seqs), _stream_handle(stream)))
+
+
+def treewy_qk_norm(qk: TreewyQk, stream=None) -> None:
+    """Norm, weight, scale and rotation of every query and key head."""
+    _check(load().treewy_qk_norm(ctypes.byref(qk), _stream_handle(stream)))
+
+
+def treewy_copy_slots(slots: TreewySlots, stream=None) -> None:
+    """Copy, fork, compact and clear slots of the state pools of all layers."""
+    _check(load().treewy_copy_slots(ctypes.byref(slots), _stream_handle(stream)))
+
+
 def make_batch(*, node_offset, parent, q, k, v, alpha, beta, state, state_slot, o, U, status,
                gamma=None, max_nodes: int = MAX_NODES, T: Optional[int] = None,
                flags: int = 0) -> TreewyBatch:
@@ -222,6 +272,170 @@ def make_batch(*, node_offset, parent, q, k, v, alpha, beta, state, state_slot, 
     b.flags = int(flags)
     b._keep = (node_offset, parent, q, k, v, alpha, beta, state, state_slot, o, U, gamma, status)
     return b
+
+
+def _dtype_code(x, name: str) -> int:
+    import torch
+    if x.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if x.dtype == torch.float32:
+        return DTYPE_F32
+    raise TypeError(f"{name} dtype {x.dtype} is not bf16 or fp32")
+
+
+def _need(x, name: str, dtype, shape=None) -> None:
+    """``x`` is contiguous, of this type and, where given, of this shape; None passes."""
+    if x is None:
+        return
+    if x.dtype != dtype:
+        raise TypeError(f"{name} dtype {x.dtype} is not {dtype}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, not {tuple(shape)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _one_device(**tensors) -> None:
+    found = {x.device for x in tensors.values() if x is not None}
+    if len(found) > 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, found))}")
+
+
+def _token_stride(x, name: str) -> int:
+    """Elements between the token rows of ``x`` [T][heads][d], whose heads are
+    contiguous within a row (a slice of a fused projection has longer rows)."""
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [T][heads][d]")
+    T, heads, d = x.shape
+    if (d > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if T <= 1 or heads * d == 0:
+        return heads * d
+    if x.stride(0) < heads * d:
+        raise ValueError(f"{name}: token rows overlap")
+    return int(x.stride(0))
+
+
+def make_seqs(*, seq_offset, q, k, v, alpha, beta, state, state_slot, o, status, max_len: int, fresh=None,
+              flags: int = 0) -> TreewySeqs:
+    """Fill a TreewySeqs from torch tensors (shapes as in include/treewy.h; the
+    token rows of q, k and v may be strided).  ``max_len`` bounds every
+    sequence's number of new tokens.  The structure keeps the tensors alive.
+    """
+    import torch
+    strides = [_token_stride(x, n) for n, x in (("q", q), ("k", k), ("v", v))]
+    T, Hk, dk = q.shape
+    H, dv = int(v.shape[1]), int(v.shape[2])
+    R = int(seq_offset.numel()) - 1
+    if tuple(k.shape) != (T, Hk, dk) or v.shape[0] != T:
+        raise ValueError("k must have q's shape, and v as many tokens")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must have one dtype")
+    i32 = torch.int32
+    _need(seq_offset, "seq_offset", i32, (R + 1,))
+    _need(state_slot, "state_slot", i32, (R,))
+    _need(status, "status", i32, (R,))
+    _need(fresh, "fresh", torch.uint8, (R,))
+    _need(alpha, "alpha", torch.float32, (T, H))
+    _need(beta, "beta", torch.float32, (T, H))
+    _need(o, "o", o.dtype, (T, H, dv))
+    _need(state, "state", state.dtype, (state.shape[0], H, dv, dk))
+    _one_device(seq_offset=seq_offset, q=q, k=k, v=v, alpha=alpha, beta=beta, state=state,
+                state_slot=state_slot, o=o, status=status, fresh=fresh)
+    s = TreewySeqs()
+    s.R, s.H, s.Hk, s.dk, s.dv, s.max_len = R, H, int(Hk), int(dk), dv, int(max_len)
+    s.qkv_dtype, s.o_dtype = _dtype_code(q, "q/k/v"), _dtype_code(o, "o")
+    s.T, s.num_slots = int(T), int(state.shape[0])
+    s.q_stride, s.k_stride, s.v_stride = strides
+    s.seq_offset, s.q, s.k, s.v = _ptr(seq_offset), _ptr(q), _ptr(k), _ptr(v)
+    s.alpha, s.beta, s.state, s.state_slot = _ptr(alpha), _ptr(beta), _ptr(state), _ptr(state_slot)
+    s.fresh, s.o, s.status = _ptr(fresh), _ptr(o), _ptr(status)
+    s.flags = int(flags) | (FLAG_STATE_BF16 if _dtype_code(state, "state") == DTYPE_BF16 else 0)
+    s._keep = (seq_offset, q, k, v, alpha, beta, state, state_slot, fresh, o, status)
+    return s
+
+
+def make_qk(*, q=None, k=None, q_out=None, k_out=None, norm: str = "l2", eps: float = 1e-6, q_weight=None,
+            k_weight=None, q_scale: float = 1.0, k_scale: float = 1.0, rope=None, position=None,
+            interleaved: bool = False, status=None) -> TreewyQk:
+    """Fill a TreewyQk from torch tensors: q [T][Hq][d], k [T][Hk][d] (strided
+    token rows allowed; either may be left out), outputs with a multiple of
+    their heads, ``norm`` "l2" or "rms", ``rope`` f32 [rows][rotated dims].
+    """
+    import torch
+    if q is None and k is None:
+        raise ValueError("q or k is needed")
+    if norm not in ("l2", "rms"):
+        raise ValueError(f"norm {norm!r} is not 'l2' or 'rms'")
+    x = q if q is not None else k
+    T, d = int(x.shape[0]), int(x.shape[2])
+    a = TreewyQk()
+    a.T, a.d, a.dtype = T, d, _dtype_code(x, "q/k")
+    a.norm = NORM_L2 if norm == "l2" else NORM_RMS
+    a.q_repeat = a.k_repeat = 1
+    for name, src, out, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
+        if src is None:
+            continue
+        stride = _token_stride(src, name)
+        heads = int(src.shape[1])
+        if (int(src.shape[0]), int(src.shape[2]), src.dtype) != (T, d, x.dtype):
+            raise ValueError("q and k must agree on tokens, head size and dtype")
+        if out is None:
+            raise ValueError(f"{name}_out is needed")
+        repeat = int(out.shape[1]) // heads if heads else 1
+        _need(out, f"{name}_out", x.dtype, (T, heads * repeat, d))
+        _need(w, f"{name}_weight", torch.float32, (d,))
+        if repeat < 1 and heads:
+            raise ValueError(f"{name}_out has fewer heads than {name}")
+        setattr(a, "Hq" if name == "q" else "Hk", heads)
+        setattr(a, f"{name}_repeat", max(repeat, 1))
+        setattr(a, f"{name}_stride", stride)
+        setattr(a, name, _ptr(src))
+        setattr(a, f"{name}_out", _ptr(out))
+        setattr(a, f"{name}_weight", _ptr(w))
+    if rope is not None:
+        _need(rope, "rope", torch.float32, (rope.shape[0], rope.shape[1]))
+        if position is None or status is None:
+            raise ValueError("position and status are needed with rope")
+        _need(position, "position", torch.int32, (T,))
+        a.rope_rows, a.rope_dims = int(rope.shape[0]), int(rope.shape[1])
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _one_device(q=q, k=k, q_out=q_out, k_out=k_out, q_weight=q_weight, k_weight=k_weight, rope=rope,
+                position=position, status=status)
+    a.eps, a.q_scale, a.k_scale, a.interleaved = float(eps), float(q_scale), float(k_scale), int(interleaved)
+    a.rope, a.position, a.status = _ptr(rope), _ptr(position), _ptr(status)
+    a._keep = (q, k, q_out, k_out, q_weight, k_weight, rope, position, status)
+    return a
+
+
+def make_slots(*, state, src, dst, status, layers: Optional[int] = None) -> TreewySlots:
+    """Fill a TreewySlots: ``state`` is one pool [num_slots][...] or, with
+    ``layers`` given, [layers][num_slots][...] (each layer's pool contiguous);
+    src, dst and status are int32 of one length, src -1 clears a slot.
+    """
+    import torch
+    for name, x in (("src", src), ("dst", dst), ("status", status)):
+        _need(x, name, torch.int32, (int(src.numel()),))
+    pool = state if layers is None else state[0] if layers else None
+    if layers is not None and int(state.shape[0]) != layers:
+        raise ValueError(f"state has {int(state.shape[0])} layers, not {layers}")
+    if pool is not None and not pool.is_contiguous():
+        raise ValueError("a layer's pool must be contiguous")
+    shape = state.shape[1:] if layers is not None else state.shape
+    if len(shape) < 2:
+        raise ValueError("state must be [num_slots][...] or [layers][num_slots][...]")
+    per = 1
+    for n in shape[1:]:
+        per *= int(n)
+    _one_device(state=state, src=src, dst=dst, status=status)
+    a = TreewySlots()
+    a.n, a.layers = int(src.numel()), 1 if layers is None else int(layers)
+    a.num_slots, a.slot_bytes = int(shape[0]), per * state.element_size()
+    a.layer_stride = int(state.stride(0)) * state.element_size() if layers is not None and layers > 1 else 0
+    a.state, a.src, a.dst, a.status = _ptr(state), _ptr(src), _ptr(dst), _ptr(status)
+    a._keep = (state, src, dst, status)
+    return a
 
 
 class TreeVerifier:

@@ -1,0 +1,378 @@
+// extend_scan.cu -- the gated delta rule token by token on CUDA cores
+// (TreeWY paper §1 Eq. (1)), for any head size dk, dv <= 128:
+//
+//   u_t = beta_t (v_t - alpha_t S k_t),  S <- alpha_t S + u_t k_t^T,
+//   o_t = S q_t = alpha_t (S_old q_t) + (k_t . q_t) u_t,
+//
+// so that S k_t and S q_t are both taken of the old state in one sweep over
+// it, and the state is touched once per token.
+//
+// The state lives in registers, f32 whatever the pool's type: eight lanes
+// share a row of S (each holds 16 of its dk columns, in pieces of 16 bytes of
+// the pool, so that a warp's load covers whole 128-byte lines), a warp holds
+// four rows per register row, and dot products over a row are three shuffles.
+//
+// decode_kernel: at most one token per sequence.  Its time is the state's
+// way in and out of HBM (2 x 64 KB per f32 head against 1.3 KB of everything
+// else); nothing depends on the state's load but the token's own arithmetic.
+//
+// scan_kernel: any number of tokens, staged 16 at a time in shared memory
+// while the loads of the next 16 are in flight.  Every token costs a sweep of
+// the registers, so it is bound by FMA issue and serves the sizes and types
+// that the chunked kernel does not take.
+#include "treewy_device.cuh"
+#include "treewy_internal.h"
+
+namespace treewy {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStage = 16;  // tokens staged at a time
+constexpr unsigned kFull = 0xffffffffu;
+
+struct Seq {
+  int64_t tok0;
+  int len, slot, flags;
+  bool fresh;
+};
+
+// Sequence r's range and slot, and the status bits of what is wrong with them.
+__device__ __forceinline__ Seq load_seq(const treewy_seqs& a, int r) {
+  const int lo = __ldg(a.seq_offset + r), hi = __ldg(a.seq_offset + r + 1);
+  Seq s;
+  s.slot = __ldg(a.state_slot + r);
+  s.fresh = a.fresh != nullptr && __ldg(a.fresh + r) != 0;
+  const int64_t len = static_cast<int64_t>(hi) - lo;
+  s.flags = 0;
+  if (len < 0 || len > a.max_len) s.flags |= TREEWY_STATUS_TOO_MANY_NODES;
+  else if (lo < 0 || hi > a.T) s.flags |= TREEWY_STATUS_BAD_TREE;
+  if (s.slot < 0 || s.slot >= a.num_slots) s.flags |= TREEWY_STATUS_BAD_SLOT;
+  s.tok0 = lo;
+  s.len = static_cast<int>(len);
+  return s;
+}
+
+// First column of piece i of lane l (0..7) of a row group: pieces of V columns.
+template <int V>
+__device__ __forceinline__ int piece_col(int l, int i) {
+  return V * (l + 8 * i);
+}
+
+// The 16 columns of lane l of a row of n elements, zero beyond it.  WIDE: the
+// row starts on a 16-byte boundary of the pool's type (a q/k row on a
+// boundary of V elements) and n is a multiple of V.
+template <int V, bool WIDE>
+__device__ __forceinline__ void load_row(const void* base, bool bf16, int64_t at, int n, int l,
+                                         float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16 / V; ++i) {
+    const int c0 = piece_col<V>(l, i);
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[V * i + e] = 0.f;
+    if constexpr (WIDE) {
+      if (c0 < n) {
+        if (bf16) {
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at + c0;
+          uint32_t w[V / 2];
+          if constexpr (V == 8) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p);
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            w[0] = u.x; w[1] = u.y;
+          }
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            x[V * i + 2 * e] = __uint_as_float(w[e] << 16);
+            x[V * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+          }
+        } else {
+          const float* p = reinterpret_cast<const float*>(base) + at + c0;
+#pragma unroll
+          for (int e = 0; e < V; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(p + e);
+            x[V * i + e] = f.x;
+            x[V * i + e + 1] = f.y;
+            x[V * i + e + 2] = f.z;
+            x[V * i + e + 3] = f.w;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (c0 + e < n) {
+          x[V * i + e] = bf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(base)[at + c0 + e])
+                              : reinterpret_cast<const float*>(base)[at + c0 + e];
+        }
+      }
+    }
+  }
+}
+
+// The same columns back to the pool; a bf16 pool rounds to nearest even.
+template <int V, bool WIDE>
+__device__ __forceinline__ void store_row(void* base, bool bf16, int64_t at, int n, int l,
+                                          const float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16 / V; ++i) {
+    const int c0 = piece_col<V>(l, i);
+    if constexpr (WIDE) {
+      if (c0 < n) {
+        if (bf16) {
+          uint32_t w[V / 2];
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x[V * i + 2 * e], x[V * i + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          uint16_t* p = reinterpret_cast<uint16_t*>(base) + at + c0;
+          if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+          else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        } else {
+          float* p = reinterpret_cast<float*>(base) + at + c0;
+#pragma unroll
+          for (int e = 0; e < V; e += 4)
+            *reinterpret_cast<float4*>(p + e) = make_float4(x[V * i + e], x[V * i + e + 1],
+                                                            x[V * i + e + 2], x[V * i + e + 3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (c0 + e < n) {
+          if (bf16) reinterpret_cast<__nv_bfloat16*>(base)[at + c0 + e] = __float2bfloat16_rn(x[V * i + e]);
+          else reinterpret_cast<float*>(base)[at + c0 + e] = x[V * i + e];
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float sum8(float x) {
+  x += __shfl_xor_sync(kFull, x, 4);
+  x += __shfl_xor_sync(kFull, x, 2);
+  x += __shfl_xor_sync(kFull, x, 1);
+  return x;
+}
+
+__device__ __forceinline__ void store_o(const treewy_seqs& a, int64_t at, float x) {
+  if (a.o_dtype == TREEWY_DTYPE_BF16) reinterpret_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(x);
+  else reinterpret_cast<float*>(a.o)[at] = x;
+}
+
+// Row of register row j of this lane's group: a warp's four groups hold
+// neighbouring rows.
+template <int RPT>
+__device__ __forceinline__ int group_row(int j) {
+  const int warp = threadIdx.x >> 5, grp = (threadIdx.x & 31) >> 3;
+  return static_cast<int>(blockIdx.y) * (32 * RPT) + 4 * (warp * RPT + j) + grp;
+}
+
+// One (sequence, head) and 32 RPT of its rows per CTA, one token at most.
+template <int RPT, int V, bool WIDE>
+__global__ void __launch_bounds__(kThreads) decode_kernel(const treewy_seqs a) {
+  const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
+  const int l = threadIdx.x & 7;
+  const bool sb = (a.flags & TREEWY_FLAG_STATE_BF16) != 0;
+  const bool qb = a.qkv_dtype == TREEWY_DTYPE_BF16;
+  const Seq s = load_seq(a, r);
+  if (s.flags) {
+    if (threadIdx.x == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
+    return;
+  }
+  if (s.len == 0 && !s.fresh) return;
+  const int64_t block = (static_cast<int64_t>(s.slot) * a.H + h) * a.dv;
+  float S[RPT][16];
+#pragma unroll
+  for (int j = 0; j < RPT; ++j) {
+    const int row = group_row<RPT>(j);
+    if (!s.fresh && row < a.dv) {
+      load_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) S[j][c] = 0.f;
+    }
+  }
+  if (s.len > 0) {
+    const int64_t t = s.tok0;
+    const int hk = h / (a.H / a.Hk);
+    float k[16], q[16], v[RPT];
+    load_row<V, WIDE>(a.k, qb, t * a.k_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, k);
+    load_row<V, WIDE>(a.q, qb, t * a.q_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, q);
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+      const int row = group_row<RPT>(j);
+      v[j] = row < a.dv ? load_qkv(a.v, t * a.v_stride + static_cast<int64_t>(h) * a.dv + row, qb) : 0.f;
+    }
+    const float alpha = __ldg(a.alpha + t * a.H + h), beta = __ldg(a.beta + t * a.H + h);
+    float kq = 0.f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) kq = fmaf(k[c], q[c], kq);
+    kq = sum8(kq);
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+      float sk = 0.f, sq = 0.f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        sk = fmaf(S[j][c], k[c], sk);
+        sq = fmaf(S[j][c], q[c], sq);
+      }
+      sk = sum8(sk);
+      sq = sum8(sq);
+      const float u = beta * (v[j] - alpha * sk);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) S[j][c] = fmaf(u, k[c], alpha * S[j][c]);
+      const int row = group_row<RPT>(j);
+      if (l == 0 && row < a.dv) store_o(a, (t * a.H + h) * a.dv + row, fmaf(kq, u, alpha * sq));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < RPT; ++j) {
+    const int row = group_row<RPT>(j);
+    if (row < a.dv) store_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
+  }
+}
+
+// Staged tokens, f32, columns beyond dk (rows beyond dv) zero.
+struct Stage {
+  float k[kStage][128];
+  float q[kStage][128];
+  float v[kStage][128];
+  float alpha[kStage], beta[kStage];
+};
+
+// One (sequence, head) and 32 RPT of its rows per CTA, any number of tokens.
+template <int RPT, int V, bool WIDE>
+__global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
+  __shared__ __align__(16) Stage st;
+  const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
+  const int tid = threadIdx.x, l = tid & 7;
+  const bool sb = (a.flags & TREEWY_FLAG_STATE_BF16) != 0;
+  const bool qb = a.qkv_dtype == TREEWY_DTYPE_BF16;
+  const Seq s = load_seq(a, r);
+  if (s.flags) {
+    if (tid == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
+    return;
+  }
+  if (s.len == 0 && !s.fresh) return;
+  const int64_t block = (static_cast<int64_t>(s.slot) * a.H + h) * a.dv;
+  float S[RPT][16];
+#pragma unroll
+  for (int j = 0; j < RPT; ++j) {
+    const int row = group_row<RPT>(j);
+    if (!s.fresh && row < a.dv) {
+      load_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) S[j][c] = 0.f;
+    }
+  }
+
+  const int hk = h / (a.H / a.Hk);
+  constexpr int kPer = kStage * 128 / kThreads;  // staged elements of k (q, v) per thread
+  float nk[kPer], nq[kPer], nv[kPer], ngate = 0.f;
+  auto fetch = [&](int t0) {  // the stage from token t0 on, into registers
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + i * kThreads, n = e >> 7, c = e & 127;
+      const int64_t t = s.tok0 + t0 + n;
+      const bool live = t0 + n < s.len;
+      nk[i] = nq[i] = nv[i] = 0.f;
+      if (live && c < a.dk) {
+        nk[i] = load_qkv(a.k, t * a.k_stride + static_cast<int64_t>(hk) * a.dk + c, qb);
+        nq[i] = load_qkv(a.q, t * a.q_stride + static_cast<int64_t>(hk) * a.dk + c, qb);
+      }
+      if (live && c < a.dv) nv[i] = load_qkv(a.v, t * a.v_stride + static_cast<int64_t>(h) * a.dv + c, qb);
+    }
+    if (tid < 2 * kStage) {
+      const int n = tid & (kStage - 1);
+      const float* g = tid < kStage ? a.alpha : a.beta;
+      if (t0 + n < s.len) ngate = __ldg(g + (s.tok0 + t0 + n) * a.H + h);
+    }
+  };
+  fetch(0);
+  for (int t0 = 0; t0 < s.len; t0 += kStage) {
+    __syncthreads();  // the last stage has been read
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + i * kThreads;
+      (&st.k[0][0])[e] = nk[i];
+      (&st.q[0][0])[e] = nq[i];
+      (&st.v[0][0])[e] = nv[i];
+    }
+    if (tid < kStage) st.alpha[tid] = ngate;
+    else if (tid < 2 * kStage) st.beta[tid - kStage] = ngate;
+    __syncthreads();
+    fetch(t0 + kStage);
+    const int m = min(kStage, s.len - t0);
+    for (int n = 0; n < m; ++n) {
+      float k[16], q[16];
+      load_row<V, true>(st.k[n], false, 0, 128, l, k);
+      load_row<V, true>(st.q[n], false, 0, 128, l, q);
+      const float alpha = st.alpha[n], beta = st.beta[n];
+      float kq = 0.f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) kq = fmaf(k[c], q[c], kq);
+      kq = sum8(kq);
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) {
+        const int row = group_row<RPT>(j);
+        float sk = 0.f, sq = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          sk = fmaf(S[j][c], k[c], sk);
+          sq = fmaf(S[j][c], q[c], sq);
+        }
+        sk = sum8(sk);
+        sq = sum8(sq);
+        const float u = beta * (st.v[n][row] - alpha * sk);  // row < 128
+#pragma unroll
+        for (int c = 0; c < 16; ++c) S[j][c] = fmaf(u, k[c], alpha * S[j][c]);
+        if (l == 0 && row < a.dv)
+          store_o(a, ((s.tok0 + t0 + n) * a.H + h) * a.dv + row, fmaf(kq, u, alpha * sq));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < RPT; ++j) {
+    const int row = group_row<RPT>(j);
+    if (row < a.dv) store_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
+  }
+}
+
+template <int RPT, int V, bool WIDE>
+cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
+                  static_cast<unsigned>((a.dv + 32 * RPT - 1) / (32 * RPT)));
+  if (a.max_len <= 1) decode_kernel<RPT, V, WIDE><<<grid, kThreads, 0, stream>>>(a);
+  else scan_kernel<RPT, V, WIDE><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int RPT>
+cudaError_t launch_rows(const treewy_seqs& a, cudaStream_t stream) {
+  // pieces of 16 bytes of the pool's type; wide loads where every row of the
+  // state, and of q and k for the single-token kernel, starts on a piece
+  const int e = a.qkv_dtype == TREEWY_DTYPE_BF16 ? 2 : 4;
+  auto rows_on = [&](const void* p, int64_t stride, int64_t piece) {
+    return (reinterpret_cast<uintptr_t>(p) % piece) == 0 && (stride * e) % piece == 0;
+  };
+  const bool sb = (a.flags & TREEWY_FLAG_STATE_BF16) != 0;
+  const int v = sb ? 8 : 4;
+  const int64_t piece = (v * e < 16) ? v * e : 16;
+  const bool wide = a.dk % v == 0 && rows_on(a.q, a.q_stride, piece) && rows_on(a.k, a.k_stride, piece);
+  if (sb) return wide ? launch<RPT, 8, true>(a, stream) : launch<RPT, 8, false>(a, stream);
+  return wide ? launch<RPT, 4, true>(a, stream) : launch<RPT, 4, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_extend_scan(const treewy_seqs& a, cudaStream_t stream) {
+  // a whole head per CTA, or a quarter of one while that leaves SMs idle
+  const int64_t heads = static_cast<int64_t>(a.R) * a.H;
+  return heads >= 304 ? launch_rows<4>(a, stream) : launch_rows<1>(a, stream);
+}
+
+}  // namespace treewy

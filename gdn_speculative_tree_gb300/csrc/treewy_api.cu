@@ -12,8 +12,12 @@
 #include "treewy_internal.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+namespace treewy {
+
+void clear_error() { g_last_error.clear(); }
 
 treewy_status fail(treewy_status code, const char* fmt, ...) {
   char buf[512];
@@ -28,6 +32,29 @@ treewy_status fail(treewy_status code, const char* fmt, ...) {
 treewy_status cuda_fail(cudaError_t err, const char* what) {
   return fail(TREEWY_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(err), cudaGetErrorString(err));
 }
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess) {
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+  });
+  return fn;
+}
+
+}  // namespace treewy
+
+namespace {
+
+using treewy::cuda_fail;
+using treewy::encode_fn;
+using treewy::fail;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -85,21 +112,6 @@ treewy_status validate(const treewy_batch* b, bool need_qv, bool need_outputs, b
 bool use_tensor_cores(const treewy_batch* b) {
   return b->dk == 128 && b->dv == 128 && b->qkv_dtype == TREEWY_DTYPE_BF16 &&
          (b->flags & TREEWY_FLAG_FORCE_GENERIC) == 0;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess) {
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-  });
-  return fn;
 }
 
 // State pool of a dk = dv = 128 batch as rows [slots*H*128][128]; one box =

@@ -6,11 +6,21 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "treewy.h"
 
 namespace treewy {
+
+// The calling thread's last error (treewy_last_error): cleared at every entry
+// point, set with the code that is returned.
+void clear_error();
+treewy_status fail(treewy_status code, const char* fmt, ...);
+treewy_status cuda_fail(cudaError_t err, const char* what);
+
+// cuTensorMapEncodeTiled of the loaded driver, or NULL.
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 // Runs `set` (a cudaFuncSetAttribute call) once per device: the attributes
 // are per device and function, so a process driving several GPUs needs them
@@ -102,6 +112,13 @@ cudaError_t launch_commit_tma(const treewy_batch& b, const CUtensorMap& state_ma
 cudaError_t launch_storeall_verify(const treewy_batch& b, float* snapshots, cudaStream_t stream);
 cudaError_t launch_storeall_commit(const treewy_batch& b, const float* snapshots,
                                    const int32_t* accepted, cudaStream_t stream);
+
+// The gated delta rule token by token (extend_scan.cu), and its form for at
+// most one token per sequence.
+cudaError_t launch_extend_scan(const treewy_seqs& s, cudaStream_t stream);
+
+cudaError_t launch_qk_norm(const treewy_qk& a, cudaStream_t stream);
+cudaError_t launch_copy_slots(const treewy_slots& a, cudaStream_t stream);
 
 // One thread waiting for a barrier phase nothing completes (bounded).
 cudaError_t launch_wait_selftest(int32_t* status, uint32_t limit_us, cudaStream_t stream);

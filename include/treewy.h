@@ -19,6 +19,11 @@
  *   commit (paper §3 "Reconstruct on commit", review Eq. (6)):
  *       S_a = gamma_a S0 + sum_{i on the root-to-a path} (gamma_a/gamma_i) u_i k_i^T
  *
+ * Around it, for a server's pool of states: treewy_extend (the same rule over
+ * a prompt's or a decode step's tokens), treewy_qk_norm (the normed q and k
+ * that all of these read) and treewy_copy_slots (forking and compacting the
+ * pool).
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - All pointers in treewy_batch are DEVICE pointers to memory the caller
@@ -64,10 +69,15 @@ enum {
   TREEWY_STATUS_BAD_SLOT = 8,       /* state_slot[r] outside [0, num_slots) */
   TREEWY_STATUS_TIMEOUT = 16,       /* an internal wait gave up after ~1 s; that
                                        (request, head) was skipped */
-  TREEWY_STATUS_COMMIT_REFUSED = 32 /* treewy_commit_verify only: the previous
+  TREEWY_STATUS_COMMIT_REFUSED = 32, /* treewy_commit_verify only: the previous
                                        round's commit of this request was refused
                                        (its state is unchanged); the bits beside
                                        it say why */
+  TREEWY_STATUS_BAD_POSITION = 64,  /* treewy_qk_norm: a position outside the
+                                       rotation table */
+  TREEWY_STATUS_SLOT_CLASH = 128    /* treewy_copy_slots: the move's destination
+                                       is written by another move too, or its
+                                       source is another move's destination */
 };
 
 /* Element type of q, k and v. */
@@ -251,6 +261,173 @@ treewy_status treewy_storeall_commit(const treewy_batch* batch, const float* sna
  */
 treewy_status treewy_selftest_wait_timeout(int32_t* status, uint32_t limit_us,
                                            cudaStream_t stream);
+
+/*
+ * One GDN layer's new tokens for a batch of sequences (treewy_extend).
+ *
+ * Sizes: R >= 0 sequences, H >= 1 value heads, Hk >= 1 key heads with H a
+ * multiple of Hk (value head h reads q and k of head h / (H / Hk)),
+ * 1 <= dk, dv <= 128, T >= seq_offset[R] token rows, max_len >= 0 a bound on
+ * every sequence's number of new tokens that the host knows (it chooses the
+ * kernel: 1 where every sequence brings at most one token), num_slots >= 1,
+ * R * H < 2^31.
+ *
+ * Layouts (device memory; innermost index last):
+ *   seq_offset  int32 [R+1], non-decreasing: sequence r's tokens, in their
+ *               order, are rows seq_offset[r] .. seq_offset[r+1]-1 (it may
+ *               have none)
+ *   q, k        bf16|f32, token t's row of [Hk][dk] at element t * q_stride
+ *               (k_stride); strides 0 mean dense rows, others are at least
+ *               Hk * dk (a slice of a fused projection)
+ *   v           the same type, rows of [H][dv], stride v_stride
+ *   alpha, beta f32 [T][H]: decay in [0, 1] and write strength
+ *   state       the pool [num_slots][H][dv][dk] of treewy_batch: f32, or bf16
+ *               with TREEWY_FLAG_STATE_BF16; 16-byte aligned
+ *   state_slot  int32 [R], distinct (two sequences on one slot race)
+ *   fresh       uint8 [R] or NULL: non-zero where the sequence starts from the
+ *               zero state, which is then not read
+ *   o           f32 or bf16 (o_dtype) [T][H][dv]
+ *   status      int32 [R], bits OR-ed in
+ * q, k, v and o are aligned to their element size only; rows and bases that
+ * are multiples of 16 bytes take the wide loads.
+ */
+typedef struct treewy_seqs {
+  int32_t R;
+  int32_t H;
+  int32_t Hk;
+  int32_t dk;
+  int32_t dv;
+  int32_t max_len;
+  int32_t qkv_dtype;
+  int32_t o_dtype;
+  int64_t T;
+  int64_t num_slots;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* seq_offset;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* alpha;
+  const float* beta;
+  void* state;
+  const int32_t* state_slot;
+  const uint8_t* fresh;
+  void* o;
+  int32_t* status;
+  uint32_t flags;                 /* TREEWY_FLAG_FORCE_GENERIC, TREEWY_FLAG_STATE_BF16 */
+  uint32_t reserved;
+} treewy_seqs;
+
+/*
+ * treewy_extend -- the gated delta rule over every sequence's new tokens
+ * (paper §1 Eq. (1)): from S = state[state_slot[r]] (zero where fresh),
+ *   S_t = alpha_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,  o_t = S_t q_t,
+ * for the tokens of sequence r in order; o gets every o_t and the slot the
+ * last state (rounded to nearest for a bf16 pool; S is f32 in between).  One
+ * token per sequence is a decode step without a draft, many are a prompt or
+ * a chunk of one.  A sequence without tokens keeps its state, or gets the
+ * zero state where fresh.
+ *
+ * A token range outside [0, T) sets TREEWY_STATUS_BAD_TREE, a length that is
+ * negative or above max_len TREEWY_STATUS_TOO_MANY_NODES, a slot outside the
+ * pool TREEWY_STATUS_BAD_SLOT; that sequence's outputs and state stay as they
+ * are.
+ */
+treewy_status treewy_extend(const treewy_seqs* seqs, cudaStream_t stream);
+
+/* Norms of treewy_qk_norm. */
+enum {
+  TREEWY_NORM_L2 = 0,   /* x / sqrt(sum x^2 + eps) */
+  TREEWY_NORM_RMS = 1   /* x / sqrt(mean x^2 + eps) */
+};
+
+/*
+ * Queries and keys of T tokens for treewy_qk_norm.
+ *
+ * q (k): token t's row of [Hq][d] ([Hk][d]) at element t * q_stride
+ * (k_stride), bf16 or f32; stride 0 means dense.  q_out, k_out: the same
+ * type, dense rows of [Hq * q_repeat][d] ([Hk * k_repeat][d]): output heads
+ * j * repeat .. j * repeat + repeat - 1 are head j, so that GDN layers whose
+ * key heads are shared get the one row per value head that treewy_verify
+ * reads.  q_out may be q itself where q_repeat is 1 and q is dense (k_out
+ * likewise); other overlaps are not allowed.  Either side may be left out
+ * (Hq = 0 or Hk = 0).  1 <= d <= 256.
+ *   q_weight, k_weight  f32 [d] or NULL (ones)
+ *   rope      f32 [rope_rows][rope_dims]: cosines of the rope_dims / 2 pairs,
+ *             then their sines; rope_dims even, 0 .. d, 0 for no rotation
+ *   position  int32 [T], rows of rope
+ *   status    int32 [1]; TREEWY_STATUS_BAD_POSITION is OR-ed into it where a
+ *             position is outside the table, and that token's outputs stay
+ *             as they are.  May be NULL where rope_dims = 0.
+ */
+typedef struct treewy_qk {
+  int64_t T;
+  int32_t Hq;
+  int32_t Hk;
+  int32_t d;
+  int32_t dtype;                  /* TREEWY_DTYPE_BF16 or TREEWY_DTYPE_F32 */
+  int32_t norm;
+  int32_t rope_dims;
+  int32_t interleaved;            /* pairs (2i, 2i+1) instead of (i, i + rope_dims / 2) */
+  int32_t q_repeat;
+  int32_t k_repeat;
+  float eps;
+  float q_scale;                  /* factors of the normed rows, 1 for none */
+  float k_scale;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t rope_rows;
+  const void* q;
+  const void* k;
+  const float* q_weight;
+  const float* k_weight;
+  const float* rope;
+  const int32_t* position;
+  void* q_out;
+  void* k_out;
+  int32_t* status;
+} treewy_qk;
+
+/*
+ * treewy_qk_norm -- every query and key head's norm, weight, scale and
+ * position rotation in one pass, in f32 with one rounding at the end:
+ *   y = scale w x / sqrt(sum or mean of x^2 + eps),
+ *   (a, b) <- (a cos - b sin, b cos + a sin) for each rotated pair.
+ */
+treewy_status treewy_qk_norm(const treewy_qk* qk, cudaStream_t stream);
+
+/*
+ * Moves between slots of `layers` state pools for treewy_copy_slots: layer
+ * l's pool starts at state + l * layer_stride bytes and holds num_slots
+ * blocks of slot_bytes bytes.  src, dst: int32 [n] (device).  status: int32
+ * [n], bits OR-ed in per move.
+ */
+typedef struct treewy_slots {
+  int32_t n;
+  int32_t layers;
+  int64_t num_slots;
+  int64_t slot_bytes;
+  int64_t layer_stride;           /* bytes; 0: num_slots * slot_bytes */
+  void* state;
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t* status;
+} treewy_slots;
+
+/*
+ * treewy_copy_slots -- copies block src[i] to block dst[i] in every layer's
+ * pool, byte for byte; src[i] = -1 fills block dst[i] with zeros (a request's
+ * states forked to samples of it, live slots moved into holes, slots
+ * cleared).  A source may serve several moves; moves with src[i] = dst[i]
+ * leave the block as it is.  Moves must not meet: where dst[i] is another
+ * move's destination too, or src[i] another move's destination,
+ * TREEWY_STATUS_SLOT_CLASH is set in status[i] and move i is not made.  An
+ * index outside the pool sets TREEWY_STATUS_BAD_SLOT and the move is not
+ * made (it still counts as a destination or source of its other index).
+ */
+treewy_status treewy_copy_slots(const treewy_slots* slots, cudaStream_t stream);
 
 /* Message for the last non-OK return on the calling host thread ("" if none). */
 const char* treewy_last_error(void);
