@@ -1,0 +1,841 @@
+// extend_chunk.cu -- the gated delta rule over long sequences in chunks of 64
+// tokens on the 5th-generation tensor cores (tcgen05, TMEM, TMA), for bf16
+// q/k/v and head sizes that are multiples of 8 up to 128 (smaller heads are
+// zero-padded to 128 by the tensor maps).
+//
+// Within a chunk, with g_t the product of its decays up to token t, the
+// recurrence S_t = a_t S_{t-1} (I - b_t k_t k_t^T) + b_t v_t k_t^T unrolls to
+//
+//   (I + A) U = W,  A[n,i] = b_n (g_n/g_i) k_n.k_i (i < n),  W_i = b_i (v_i - g_i S k_i),
+//   o_n = g_n S q_n + sum_{i<=n} M[n,i] u_i,  M[n,i] = (g_n/g_i) q_n.k_i,
+//   S'  = g_C S + sum_n (g_C/g_n) u_n k_n^T.
+//
+// With T = (I + A)^-1 neither sum needs U:
+//
+//   o_n = g_n S q_n + ((M T) W)_n,   S' = g_C S + sum_i W_i kt_i^T,
+//   kt_i = sum_n T[n,i] (g_C/g_n) k_n,
+//
+// and T, M T and kt depend on the tokens alone.  So the chain from one
+// chunk's state to the next is two products long, S k and W kt; everything
+// else is prepared one chunk ahead or follows behind.
+//
+// One CTA per (sequence, head).  Value rows are TMEM lanes throughout: S, W
+// and their products are [dv = 128 lanes][columns], so that a thread owns a
+// row, and the left operands S and W go back to TMEM as bf16 without passing
+// through shared memory.
+//
+//   warps 0-7   state: two threads per row (64 of S's columns and 32 tokens
+//               each); S stays in f32 registers for the whole sequence
+//   warps 8-11  preparation of the next chunk: gates, [K;Q] K^T, T, M T, kt
+//   warp 12     issues the chain's products
+//   warp 13     loads K, Q and V, two chunks in flight
+//
+// Every product takes an f32 operand as two bf16 terms x = hi + lo (16
+// significant bits; lo times lo is left out), accumulates in f32, and keys,
+// queries and values are exact, so a result is within a few 2^-17 of the
+// recurrence's.  The decays are handled as powers of two with an integer and
+// a small f32 part, so that a ratio g_n/g_i is right to f32 rounding however
+// small the products have become, a decay of zero included.
+#include "treewy_device.cuh"
+#include "treewy_internal.h"
+
+namespace treewy {
+namespace {
+
+constexpr int kC = 64;                       // tokens per chunk
+constexpr int kStateThreads = 256;
+constexpr int kPrepThreads = 128;
+constexpr int kThreads = kStateThreads + kPrepThreads + 64;
+constexpr int kMmaWarp = 12, kLoadWarp = 13;
+
+// TMEM columns
+constexpr uint32_t kColS = 0;                // S: hi in 64 columns, lo in 64 (bf16 pairs)
+constexpr uint32_t kColW = 128;              // S k, then W (32 columns per half of the tokens: hi 16, lo 16)
+constexpr uint32_t kColO = 192;              // S q, then (M T) W
+constexpr uint32_t kColD = 256;              // sum W kt^T
+constexpr uint32_t kColG = 384;              // [K;Q] K^T, then M T
+constexpr uint32_t kColK = 448;              // kt^T
+constexpr uint32_t kTmemCols = 512;
+
+// Shared memory.  A stage holds K and Q as 64-column boxes of 64 rows in the
+// order K0 Q0 K1 Q1 (8 KB each, 128-byte swizzle; so [K;Q] is one operand of
+// 128 rows), then V as plain rows.
+constexpr uint32_t kBox = 8192;
+constexpr uint32_t kStageBytes = 6 * kBox;
+constexpr uint32_t kOffKt = 2 * kStageBytes;      // kt^T: 128 rows (dk) of 64 tokens, hi then lo
+constexpr uint32_t kOffMT = kOffKt + 4 * kBox;    // M T: 64 rows of 64 tokens, hi then lo
+constexpr uint32_t kOffM = kOffMT + 2 * kBox;     // M, hi then lo
+constexpr uint32_t kOffT = kOffM + 2 * kBox;      // T hi, lo, then (g_C/g_n) T hi, lo
+constexpr uint32_t kOffA = kOffT + 4 * kBox;      // A, then T: f32, 64 rows
+constexpr int kPitchA = 68;
+constexpr uint32_t kSmemBytes = kOffA + kC * kPitchA * 4 + 1024;
+
+struct Gates {
+  float bb[kC], bg[kC], gam[kC];  // b, b g, g of every token
+  float gC;
+};
+
+struct ChunkSmem {
+  Gates gates[2];
+  int gE[kC];                     // g_n = 2^(gE + gF)
+  float gF[kC], dec[kC];          // dec: g_C / g_n
+  uint64_t full[2], stage_free[2], gates_ready[2], o_read[2];
+  uint64_t fix, gram_done, prep_done, kt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done, drain[2];
+  uint32_t tmem;
+  int fail;
+};
+
+// A bounded wait that also gives up once any other wait of the CTA has.
+__device__ __forceinline__ bool wait(ChunkSmem& cs, uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity & 1u)) return true;
+    if ((it & 31u) == 31u) {
+      if (*reinterpret_cast<volatile int*>(&cs.fail)) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile int*>(&cs.fail) = 1;
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// D(tmem) (+)= A(tmem, bf16 pairs) * B(smem desc)^T
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of an operand whose rows run along the contraction (MN-major),
+// 128-byte swizzle: blocks of 64 columns `lbo` bytes apart, groups of eight
+// rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = smem_desc_sw128(saddr, 1024);
+  d &= ~(static_cast<uint64_t>(0x3FFFu) << 16);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  return d;
+}
+constexpr uint32_t kAmajorMN = 1u << 15, kBmajorMN = 1u << 16;
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 consecutive columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&a)[16], uint32_t (&b)[16]) {
+  tmem_ld16_async(taddr, a);
+  tmem_ld16_async(taddr + 16, b);
+  tmem_wait16(a);
+  tmem_wait16(b);
+}
+
+// a = 2^(e + f) with e whole and f in [-1/2, 1/2); zero as 2^-16384.
+__device__ __forceinline__ void log2_split(float a, int& e, float& f) {
+  if (a == 0.f) {
+    e = -16384;
+    f = 0.f;
+    return;
+  }
+  int shift = 0;
+  if (a < 1.17549435e-38f) {  // below the normal numbers
+    a *= 4294967296.f;
+    shift = 32;
+  }
+  const uint32_t bits = __float_as_uint(a);
+  e = static_cast<int>((bits >> 23) & 255u) - 127;
+  float m = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);  // the sign stays: a negative decay becomes NaN
+  if (m > 1.41421356f) {
+    m *= 0.5f;
+    ++e;
+  }
+  if (((bits >> 23) & 255u) == 255u) m = a;  // infinite or NaN
+  e -= shift;
+  f = log2f(m);
+}
+
+// Row `row`, 16-byte piece `j` of a K-major operand with 128-byte rows.
+__device__ __forceinline__ uint4* operand_piece(unsigned char* tile, int row, int j) {
+  return reinterpret_cast<uint4*>(tile + row * 128 + ((j ^ (row & 7)) << 4));
+}
+
+// Eight values as hi and lo pieces.
+__device__ __forceinline__ void put_piece(unsigned char* hi, unsigned char* lo, int row, int j, const float (&x)[8]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) split_pair(x[2 * e], x[2 * e + 1], h[e], l[e]);
+  *operand_piece(hi, row, j) = make_uint4(h[0], h[1], h[2], h[3]);
+  *operand_piece(lo, row, j) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+__device__ __forceinline__ void prep_sync() { named_bar_sync<1, kPrepThreads>(); }
+
+// T = (I + A)^-1 in place of A (unit lower triangular, 64 x 64 f32, zeros
+// above): the two diagonal blocks of 32 by substitution, a column per lane,
+// then T21 = -T22 (A21 T11).
+__device__ __forceinline__ void invert(float* A, int p) {
+  const int w = p >> 5, j = p & 31;
+  if (w < 2) {
+    float* B = A + 32 * w * kPitchA + 32 * w;
+    float x[32];
+#pragma unroll
+    for (int n = 0; n < 32; ++n) {
+      float acc0 = n == j ? 1.f : 0.f, acc1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < n; i += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(B + n * kPitchA + i);
+        acc0 = fmaf(-a.x, x[i], acc0);
+        if (i + 1 < n) acc1 = fmaf(-a.y, x[i + 1], acc1);
+        if (i + 2 < n) acc0 = fmaf(-a.z, x[i + 2], acc0);
+        if (i + 3 < n) acc1 = fmaf(-a.w, x[i + 3], acc1);
+      }
+      x[n] = acc0 + acc1;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < 32; ++n) B[n * kPitchA + j] = x[n];
+  }
+  prep_sync();
+  float acc[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) acc[r] = 0.f;
+  const float* rows = A + (32 + 8 * w) * kPitchA;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float t0 = A[i * kPitchA + j], t1 = A[(i + 1) * kPitchA + j], t2 = A[(i + 2) * kPitchA + j],
+                t3 = A[(i + 3) * kPitchA + j];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float4 a = *reinterpret_cast<const float4*>(rows + r * kPitchA + i);
+      acc[r] = fmaf(a.x, t0, fmaf(a.y, t1, fmaf(a.z, t2, fmaf(a.w, t3, acc[r]))));
+    }
+  }
+  prep_sync();
+  float* out = A + (32 + 8 * w) * kPitchA + j;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    out[r * kPitchA] = acc[r];
+    acc[r] = 0.f;
+  }
+  prep_sync();
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float* W = A + 32 * kPitchA + j;
+    const float t0 = W[i * kPitchA], t1 = W[(i + 1) * kPitchA], t2 = W[(i + 2) * kPitchA], t3 = W[(i + 3) * kPitchA];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float4 a = *reinterpret_cast<const float4*>(rows + r * kPitchA + 32 + i);
+      acc[r] = fmaf(a.x, t0, fmaf(a.y, t1, fmaf(a.z, t2, fmaf(a.w, t3, acc[r]))));
+    }
+  }
+  prep_sync();
+#pragma unroll
+  for (int r = 0; r < 8; ++r) out[r * kPitchA] = -acc[r];
+  prep_sync();
+}
+
+struct SeqInfo {
+  int64_t tok0;
+  int len, slot;
+  bool fresh;
+};
+
+// 64 columns of a row of S (from column 64 half) of the pool.
+template <bool SB>
+__device__ __forceinline__ void load_state(const treewy_seqs& a, int64_t row, int half, float (&S)[64]) {
+#pragma unroll
+  for (int i = 0; i < 64; i += 8) {
+    const int c = 64 * half + i;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) S[i + e] = 0.f;
+    if (c < a.dk) {
+      if constexpr (SB) {
+        const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.state) + row * a.dk + c);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          S[i + 2 * e] = __uint_as_float(w[e] << 16);
+          S[i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+      } else {
+        const float* p = reinterpret_cast<const float*>(a.state) + row * a.dk + c;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(p + e);
+          S[i + e] = f.x;
+          S[i + e + 1] = f.y;
+          S[i + e + 2] = f.z;
+          S[i + e + 3] = f.w;
+        }
+      }
+    }
+  }
+}
+
+template <bool SB>
+__device__ __forceinline__ void store_state(const treewy_seqs& a, int64_t row, int half, const float (&S)[64]) {
+#pragma unroll
+  for (int i = 0; i < 64; i += 8) {
+    const int c = 64 * half + i;
+    if (c < a.dk) {
+      if constexpr (SB) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(S[i + 2 * e], S[i + 2 * e + 1]);
+          w[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.state) + row * a.dk + c) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        float* p = reinterpret_cast<float*>(a.state) + row * a.dk + c;
+        *reinterpret_cast<float4*>(p) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(S[i + 4], S[i + 5], S[i + 6], S[i + 7]);
+      }
+    }
+  }
+}
+
+// Columns 32 b .. 32 b + 31 of this thread's half of S as the left operand.
+__device__ __forceinline__ void put_state(uint32_t tm, int half, int b, const float (&S)[64]) {
+  uint32_t hi[16], lo[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) split_pair(S[32 * b + 2 * e], S[32 * b + 2 * e + 1], hi[e], lo[e]);
+  tmem_st16(tm + kColS + 32 * half + 16 * b, hi);
+  tmem_st16(tm + kColS + 64 + 32 * half + 16 * b, lo);
+}
+
+// The state warps.
+template <bool SB, bool OF32>
+__device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, unsigned char* base, const SeqInfo& q,
+                                          int h, int nchunk) {
+  const int t = threadIdx.x, d = t & 127, half = t >> 7;
+  const uint32_t tm = cs.tmem + (static_cast<uint32_t>(d & 96) << 16);
+  const int64_t row = (static_cast<int64_t>(q.slot) * a.H + h) * a.dv + d;
+  float S[64];
+  if (d < a.dv && !q.fresh) {
+    load_state<SB>(a, row, half, S);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) S[i] = 0.f;
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) put_state(tm, half, b, S);
+  tmem_wait_st();
+  tc_fence_before_sync();
+  arrive(&cs.s_ready[half]);
+  bool ok = true;
+  for (int c = 0; c < nchunk; ++c) {
+    const int sg = c & 1;
+    const uint32_t ph2 = c >> 1;
+    const Gates& g = cs.gates[sg];
+    const int n0 = 32 * half, left = q.len - c * kC - n0;  // tokens of this thread's half
+    ok = wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.full[sg], ph2) && wait(cs, &cs.d1_done, c);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after_sync();
+    uint32_t x0[16], x1[16];
+    {
+      // W = b v - b g (S k), zero past the sequence's end
+      tmem_ld32(tm + kColW + n0, x0, x1);
+      const uint16_t* V = reinterpret_cast<const uint16_t*>(base + sg * kStageBytes + 4 * kBox) + n0 * 128 + d;
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int n = 2 * e + k;
+          const float sk = __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
+          const float v = bf16_bits_to_float(V[n * 128]);
+          w[k] = n < left ? fmaf(-g.bg[n0 + n], sk, g.bb[n0 + n] * v) : 0.f;
+        }
+        split_pair(w[0], w[1], hi[e], lo[e]);
+      }
+      tmem_st16(tm + kColW + n0, hi);
+      tmem_st16(tm + kColW + n0 + 16, lo);
+    }
+    tmem_wait_st();
+    tc_fence_before_sync();
+    arrive(&cs.rhs_ready);
+    arrive(&cs.stage_free[sg]);
+    // S q of this thread's tokens, scaled, before its columns are written again
+    float o[32];
+    ok = wait(cs, &cs.qs_done, c);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after_sync();
+    tmem_ld32(tm + kColO + n0, x0, x1);
+    tc_fence_before_sync();
+    arrive(&cs.qs_read);
+#pragma unroll
+    for (int n = 0; n < 32; ++n) o[n] = g.gam[n0 + n] * __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
+    // S' = g_C S + W kt
+    const float gC = g.gC;
+    ok = wait(cs, &cs.d2_done[half], c);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after_sync();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      tmem_ld32(tm + kColD + 64 * half + 32 * b, x0, x1);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        S[32 * b + e] = fmaf(gC, S[32 * b + e], __uint_as_float(x0[e]));
+        S[32 * b + 16 + e] = fmaf(gC, S[32 * b + 16 + e], __uint_as_float(x1[e]));
+      }
+      if (c + 1 < nchunk) put_state(tm, half, b, S);
+    }
+    if (c + 1 < nchunk) {
+      tmem_wait_st();
+      tc_fence_before_sync();
+      arrive(&cs.s_ready[half]);
+    }
+    ok = wait(cs, &cs.o2_done, c);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after_sync();
+    tmem_ld32(tm + kColO + n0, x0, x1);
+    tc_fence_before_sync();
+    arrive(&cs.o_read[sg]);
+    if (d < a.dv) {
+      const int64_t at = ((q.tok0 + c * kC + n0) * a.H + h) * static_cast<int64_t>(a.dv) + d;
+      const int64_t step = static_cast<int64_t>(a.H) * a.dv;
+#pragma unroll
+      for (int n = 0; n < 32; ++n) {
+        if (n < left) {
+          const float y = o[n] + __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
+          if constexpr (OF32) reinterpret_cast<float*>(a.o)[at + n * step] = y;
+          else reinterpret_cast<__nv_bfloat16*>(a.o)[at + n * step] = __float2bfloat16_rn(y);
+        }
+      }
+    }
+  }
+  if (ok && d < a.dv) store_state<SB>(a, row, half, S);
+}
+
+// The preparation warps: T, M T and kt of every chunk, one chunk ahead of the state.
+__device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, unsigned char* base, const SeqInfo& q,
+                                         int h, int nchunk) {
+  const int p = threadIdx.x - kStateThreads, lane = p & 31, n = p & 63;
+  const uint32_t tm = cs.tmem + (static_cast<uint32_t>(p & 96) << 16);
+  float* A = reinterpret_cast<float*>(base + kOffA);
+  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
+  // gates of tokens `lane` and `lane + 32` of the chunk, requested one chunk ahead
+  float al[2], be[2];
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = c * kC + lane + 32 * k;
+      al[k] = 1.f;
+      be[k] = 0.f;
+      if (i < q.len) {
+        al[k] = __ldg(a.alpha + (q.tok0 + i) * a.H + h);
+        be[k] = __ldg(a.beta + (q.tok0 + i) * a.H + h);
+      }
+    }
+  };
+  fetch(0);
+  bool ok = true;
+  for (int c = 0; c < nchunk; ++c) {
+    const int sg = c & 1;
+    const uint32_t ph2 = c >> 1;
+    const int nt = min(kC, q.len - c * kC);
+    unsigned char* st = base + sg * kStageBytes;
+    if (c >= 2) ok = wait(cs, &cs.o_read[sg], ph2 - 1);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    // inclusive sums of log2 of the decays: every warp for itself, the first writes
+    int e[2];
+    float f[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      log2_split(al[k], e[k], f[k]);
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int ey = __shfl_up_sync(0xffffffffu, e[k], s);
+        const float fy = __shfl_up_sync(0xffffffffu, f[k], s);
+        if (lane >= s) {
+          e[k] += ey;
+          f[k] += fy;
+        }
+      }
+    }
+    e[1] += __shfl_sync(0xffffffffu, e[0], 31);
+    f[1] += __shfl_sync(0xffffffffu, f[0], 31);
+    const int eC = __shfl_sync(0xffffffffu, e[1], 31);
+    const float fC = __shfl_sync(0xffffffffu, f[1], 31);
+    if (p < 32) {
+      Gates& g = cs.gates[sg];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        const float gam = exp2f(static_cast<float>(e[k]) + f[k]);
+        g.bb[i] = be[k];
+        g.bg[i] = be[k] * gam;
+        g.gam[i] = gam;
+        cs.gE[i] = e[k];
+        cs.gF[i] = f[k];
+        cs.dec[i] = exp2f(static_cast<float>(eC - e[k]) + (fC - f[k]));
+      }
+      if (lane == 0) g.gC = exp2f(static_cast<float>(eC) + fC);
+    }
+    arrive(&cs.gates_ready[sg]);
+    if (c + 1 < nchunk) fetch(c + 1);
+    ok = wait(cs, &cs.full[sg], ph2);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    if (nt < kC) {
+      // rows of K past the sequence's end (the next one's) become zero
+      for (int i = nt * 128 + 16 * p; i < static_cast<int>(kBox); i += 16 * kPrepThreads) {
+        *reinterpret_cast<uint4*>(st + i) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(st + 2 * kBox + i) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      arrive(&cs.fix);
+    }
+    prep_sync();
+    if (p == 0) {
+      tc_fence_after_sync();
+      constexpr uint32_t id = idesc_bf16_f32(128, kC);
+      const uint32_t s0 = smem_addr(st);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t at = s0 + (k >> 2) * 2 * kBox + (k & 3) * 32;
+        mma_bf16(cs.tmem + kColG, smem_desc_sw128(at, 1024), smem_desc_sw128(at, 1024), id, k > 0);
+      }
+      mma_commit(&cs.gram_done);
+    }
+    ok = wait(cs, &cs.gram_done, c);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after_sync();
+    {
+      // lanes 0-63: rows of A (f32), lanes 64-127: rows of M (hi and lo)
+      const bool isM = p >= 64;
+      const int en = cs.gE[n];
+      const float fn = cs.gF[n], scale = isM ? 1.f : cs.gates[sg].bb[n];
+      const int last = isM ? n + 1 : n;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t x0[16], x1[16];
+        tmem_ld32(tm + kColG + 32 * b, x0, x1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int i = 32 * b + 8 * j + k;
+            const float x = __uint_as_float(8 * j + k < 16 ? x0[(8 * j + k) & 15] : x1[(8 * j + k) & 15]);
+            y[k] = i < last ? scale * exp2f(static_cast<float>(en - cs.gE[i]) + (fn - cs.gF[i])) * x : 0.f;
+          }
+          if (isM) {
+            put_piece(mb, mb + kBox, n, 4 * b + j, y);
+          } else {
+            float4* r = reinterpret_cast<float4*>(A + n * kPitchA + 32 * b + 8 * j);
+            r[0] = make_float4(y[0], y[1], y[2], y[3]);
+            r[1] = make_float4(y[4], y[5], y[6], y[7]);
+          }
+        }
+      }
+    }
+    tc_fence_before_sync();
+    prep_sync();
+    invert(A, p);
+    {
+      // T and (g_C/g_n) T as operands [n][i]: two threads per row
+      const int r = p >> 1, hb = p & 1;
+      const float dec = cs.dec[r];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4* src = reinterpret_cast<const float4*>(A + r * kPitchA + 32 * hb + 8 * j);
+        const float4 u = src[0], v = src[1];
+        float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        put_piece(tb, tb + kBox, r, 4 * hb + j, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] *= dec;
+        put_piece(tb + 2 * kBox, tb + 3 * kBox, r, 4 * hb + j, y);
+      }
+    }
+    fence_proxy_async_smem();
+    prep_sync();
+    if (p == 0) {
+      tc_fence_after_sync();
+      // kt^T[dk][i] = sum_n K[n][dk] (g_C/g_n) T[n][i]; M T (rows 64.. of its
+      // left operand only fill lanes that nothing reads)
+      constexpr uint32_t idk = idesc_bf16_f32(128, kC) | kAmajorMN | kBmajorMN;
+      constexpr uint32_t idm = idesc_bf16_f32(128, kC) | kBmajorMN;
+      const uint32_t k0 = smem_addr(st), t0 = smem_addr(tb), m0 = smem_addr(mb);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t kd = smem_desc_sw128_mn(k0 + k * 2048, 2 * kBox);
+        mma_bf16(cs.tmem + kColK, kd, smem_desc_sw128_mn(t0 + 2 * kBox + k * 2048, kBox), idk, k > 0);
+        mma_bf16(cs.tmem + kColK, kd, smem_desc_sw128_mn(t0 + 3 * kBox + k * 2048, kBox), idk, 1u);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t th = smem_desc_sw128_mn(t0 + k * 2048, kBox), tl = smem_desc_sw128_mn(t0 + kBox + k * 2048, kBox);
+        const uint64_t mh = smem_desc_sw128(m0 + 32 * k, 1024), ml = smem_desc_sw128(m0 + kBox + 32 * k, 1024);
+        mma_bf16(cs.tmem + kColG, mh, th, idm, k > 0);
+        mma_bf16(cs.tmem + kColG, mh, tl, idm, 1u);
+        mma_bf16(cs.tmem + kColG, ml, th, idm, 1u);
+      }
+      mma_commit(&cs.prep_done);
+    }
+    ok = wait(cs, &cs.prep_done, c);
+    // the last chunk's kt and M T have been read
+    if (ok && c > 0) ok = wait(cs, &cs.o2_done, c - 1);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after_sync();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t x0[16], x1[16];
+      tmem_ld32(tm + kColK + 32 * b, x0, x1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(8 * j + k < 16 ? x0[(8 * j + k) & 15] : x1[(8 * j + k) & 15]);
+        put_piece(ktb, ktb + 2 * kBox, p, 4 * b + j, y);
+      }
+    }
+    if (p < 64) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t x0[16], x1[16];
+        tmem_ld32(tm + kColG + 32 * b, x0, x1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(8 * j + k < 16 ? x0[(8 * j + k) & 15] : x1[(8 * j + k) & 15]);
+          put_piece(mtb, mtb + kBox, p, 4 * b + j, y);
+        }
+      }
+    }
+    tc_fence_before_sync();
+    fence_proxy_async_smem();
+    arrive(&cs.kt_ready);
+    arrive(&cs.stage_free[sg]);
+  }
+}
+
+// The products that this thread has issued are done (or the limit is over)
+// before the CTA frees its TMEM, also after a wait that gave up.
+__device__ __forceinline__ void drain(uint64_t* bar) {
+  mma_commit(bar);
+  mbar_wait(bar, 0);
+}
+
+// One thread: the chain's products.
+__device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int len, int nchunk) {
+  constexpr uint32_t id = idesc_bf16_f32(128, kC);
+  const uint32_t tm = cs.tmem;
+  const uint32_t kt = smem_addr(base + kOffKt), mt = smem_addr(base + kOffMT);
+  for (int c = 0; c < nchunk; ++c) {
+    const int sg = c & 1;
+    const uint32_t s0 = smem_addr(base + sg * kStageBytes);
+    if (!wait(cs, &cs.full[sg], c >> 1)) return;
+    if (len - c * kC < kC && !wait(cs, &cs.fix, 0)) return;
+    // W's columns have been read by the last chunk's products
+    if (c > 0 && !wait(cs, &cs.o2_done, c - 1)) return;
+    // S k, half of the columns of S at a time
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (!wait(cs, &cs.s_ready[half], c)) return;
+      tc_fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t kd = smem_desc_sw128(s0 + half * 2 * kBox + 32 * k, 1024);
+        mma_bf16_ts(tm + kColW, tm + kColS + 32 * half + 8 * k, kd, id, half > 0 || k > 0);
+        mma_bf16_ts(tm + kColW, tm + kColS + 64 + 32 * half + 8 * k, kd, id, 1u);
+      }
+    }
+    mma_commit(&cs.d1_done);
+    // S q
+    if (c > 0 && !wait(cs, &cs.o_read[sg ^ 1], (c - 1) >> 1)) return;
+    tc_fence_after_sync();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint64_t qd = smem_desc_sw128(s0 + (k >> 2) * 2 * kBox + kBox + 32 * (k & 3), 1024);
+      mma_bf16_ts(tm + kColO, tm + kColS + 8 * k, qd, id, k > 0);
+      mma_bf16_ts(tm + kColO, tm + kColS + 64 + 8 * k, qd, id, 1u);
+    }
+    mma_commit(&cs.qs_done);
+    mma_commit(&cs.stage_free[sg]);
+    // W kt, half of its columns at a time
+    if (!wait(cs, &cs.kt_ready, c) || !wait(cs, &cs.rhs_ready, c)) return;
+    tc_fence_after_sync();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t wh = tm + kColW + 32 * (k >> 1) + 8 * (k & 1);
+        const uint64_t kh = smem_desc_sw128(kt + half * kBox + 32 * k, 1024);
+        const uint64_t kl = smem_desc_sw128(kt + 2 * kBox + half * kBox + 32 * k, 1024);
+        mma_bf16_ts(tm + kColD + 64 * half, wh, kh, id, k > 0);
+        mma_bf16_ts(tm + kColD + 64 * half, wh, kl, id, 1u);
+        mma_bf16_ts(tm + kColD + 64 * half, wh + 16, kh, id, 1u);
+      }
+      mma_commit(&cs.d2_done[half]);
+    }
+    // (M T) W over the columns of S q
+    if (!wait(cs, &cs.qs_read, c)) return;
+    tc_fence_after_sync();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t wh = tm + kColW + 32 * (k >> 1) + 8 * (k & 1);
+      const uint64_t mh = smem_desc_sw128(mt + 32 * k, 1024), ml = smem_desc_sw128(mt + kBox + 32 * k, 1024);
+      mma_bf16_ts(tm + kColO, wh, mh, id, k > 0);
+      mma_bf16_ts(tm + kColO, wh, ml, id, 1u);
+      mma_bf16_ts(tm + kColO, wh + 16, mh, id, 1u);
+    }
+    mma_commit(&cs.o2_done);
+  }
+}
+
+// One thread: K, Q and V of every chunk, two in flight.
+__device__ __forceinline__ void run_load(const CUtensorMap* map_q, const CUtensorMap* map_k, const CUtensorMap* map_v,
+                                         ChunkSmem& cs, unsigned char* base, const SeqInfo& q, int hk, int h,
+                                         int nchunk) {
+  int issued = 0;
+  for (int c = 0; c < nchunk; ++c) {
+    const int sg = c & 1;
+    if (c >= 2 && !wait(cs, &cs.stage_free[sg], (c >> 1) - 1)) break;
+    unsigned char* st = base + sg * kStageBytes;
+    const int tok = static_cast<int>(q.tok0) + c * kC;
+    mbar_arrive_expect_tx(&cs.full[sg], kStageBytes);
+    tma_load_3d(st, map_k, &cs.full[sg], 0, hk, tok);
+    tma_load_3d(st + 2 * kBox, map_k, &cs.full[sg], 64, hk, tok);
+    tma_load_3d(st + kBox, map_q, &cs.full[sg], 0, hk, tok);
+    tma_load_3d(st + 3 * kBox, map_q, &cs.full[sg], 64, hk, tok);
+    tma_load_3d(st + 4 * kBox, map_v, &cs.full[sg], 0, h, tok);
+    ++issued;
+  }
+  // no copy targets this CTA's memory once it has ended
+  for (int c = max(0, issued - 2); c < issued; ++c) mbar_wait(&cs.full[c & 1], (c >> 1) & 1);
+}
+
+template <bool SB, bool OF32>
+__global__ void __launch_bounds__(kThreads, 1)
+    extend_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const treewy_seqs a) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ ChunkSmem cs;
+  unsigned char* base =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) & ~uintptr_t(1023));
+  const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
+  const int t = threadIdx.x, warp = t >> 5;
+
+  const int lo = __ldg(a.seq_offset + r), hi = __ldg(a.seq_offset + r + 1);
+  SeqInfo q;
+  q.slot = __ldg(a.state_slot + r);
+  q.fresh = a.fresh != nullptr && __ldg(a.fresh + r) != 0;
+  const int64_t len = static_cast<int64_t>(hi) - lo;
+  int flags = 0;
+  if (len < 0 || len > a.max_len) flags |= TREEWY_STATUS_TOO_MANY_NODES;
+  else if (lo < 0 || hi > a.T) flags |= TREEWY_STATUS_BAD_TREE;
+  if (q.slot < 0 || q.slot >= a.num_slots) flags |= TREEWY_STATUS_BAD_SLOT;
+  q.tok0 = lo;
+  q.len = static_cast<int>(len);
+  if (flags) {
+    if (t == 0 && h == 0) atomicOr(a.status + r, flags);
+    return;
+  }
+  if (q.len == 0) {
+    if (q.fresh && t < kStateThreads && (t & 127) < a.dv) {
+      float S[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) S[i] = 0.f;
+      store_state<SB>(a, (static_cast<int64_t>(q.slot) * a.H + h) * a.dv + (t & 127), t >> 7, S);
+    }
+    return;
+  }
+  const int nchunk = (q.len + kC - 1) / kC;
+
+  if (t == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&cs.full[i], 1);
+      mbar_init(&cs.stage_free[i], 1 + kStateThreads + kPrepThreads);
+      mbar_init(&cs.gates_ready[i], kPrepThreads);
+      mbar_init(&cs.o_read[i], kStateThreads);
+      mbar_init(&cs.s_ready[i], kStateThreads / 2);
+      mbar_init(&cs.d2_done[i], 1);
+      mbar_init(&cs.drain[i], 1);
+    }
+    mbar_init(&cs.fix, kPrepThreads);
+    mbar_init(&cs.gram_done, 1);
+    mbar_init(&cs.prep_done, 1);
+    mbar_init(&cs.kt_ready, kPrepThreads);
+    mbar_init(&cs.d1_done, 1);
+    mbar_init(&cs.qs_done, 1);
+    mbar_init(&cs.rhs_ready, kStateThreads);
+    mbar_init(&cs.qs_read, kStateThreads);
+    mbar_init(&cs.o2_done, 1);
+    cs.fail = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&cs.tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+
+  if (warp < kStateThreads / 32) {
+    run_state<SB, OF32>(a, cs, base, q, h, nchunk);
+  } else if (warp < kMmaWarp) {
+    run_prep(a, cs, base, q, h, nchunk);
+    if (t == kStateThreads) drain(&cs.drain[1]);
+  } else if (warp == kMmaWarp) {
+    if ((t & 31) == 0) {
+      run_mma(cs, base, q.len, nchunk);
+      drain(&cs.drain[0]);
+    }
+  } else if ((t & 31) == 0) {
+    run_load(&map_q, &map_k, &map_v, cs, base, q, h / (a.H / a.Hk), h, nchunk);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (t == 0 && cs.fail) atomicOr(a.status + r, TREEWY_STATUS_TIMEOUT);
+  if (warp == kMmaWarp) tmem_dealloc(cs.tmem, kTmemCols);
+}
+
+template <bool SB, bool OF32>
+cudaError_t launch(const treewy_seqs& a, const ExtendMaps& m, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  const cudaError_t attr = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(extend_chunk_kernel<SB, OF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kSmemBytes));
+  });
+  if (attr != cudaSuccess) return attr;
+  const unsigned grid = static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H);
+  extend_chunk_kernel<SB, OF32><<<grid, kThreads, kSmemBytes, stream>>>(m.q, m.k, m.v, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_extend_chunk(const treewy_seqs& a, const ExtendMaps& m, cudaStream_t stream) {
+  const bool f32 = a.o_dtype == TREEWY_DTYPE_F32;
+  if (a.flags & TREEWY_FLAG_STATE_BF16)
+    return f32 ? launch<true, true>(a, m, stream) : launch<true, false>(a, m, stream);
+  return f32 ? launch<false, true>(a, m, stream) : launch<false, false>(a, m, stream);
+}
+
+}  // namespace treewy

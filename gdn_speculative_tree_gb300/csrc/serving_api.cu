@@ -62,6 +62,44 @@ treewy_status validate_seqs(const treewy_seqs* s) {
   return TREEWY_OK;
 }
 
+// Batches whose longest sequence has at least this many tokens run in chunks.
+constexpr int kChunkedLen = 17;
+
+// Whether the chunked kernel takes the batch (s: strides resolved).
+bool use_chunks(const treewy_seqs& s) {
+  auto rows_on16 = [](const void* p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; };
+  return s.qkv_dtype == TREEWY_DTYPE_BF16 && s.dk % 8 == 0 && s.dv % 8 == 0 && s.T > 0 &&
+         s.max_len >= kChunkedLen && (s.flags & TREEWY_FLAG_FORCE_GENERIC) == 0 &&
+         rows_on16(s.q, s.q_stride) && rows_on16(s.k, s.k_stride) && rows_on16(s.v, s.v_stride);
+}
+
+treewy_status make_extend_maps(const treewy_seqs& s, treewy::ExtendMaps* m) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = treewy::encode_fn();
+  if (enc == nullptr) return fail(TREEWY_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint32_t ones[3] = {1, 1, 1};
+  struct {
+    CUtensorMap* map;
+    const void* p;
+    int heads, d;
+    int64_t stride;
+    cuuint32_t cols;
+  } const of[3] = {{&m->q, s.q, s.Hk, s.dk, s.q_stride, 64},
+                   {&m->k, s.k, s.Hk, s.dk, s.k_stride, 64},
+                   {&m->v, s.v, s.H, s.dv, s.v_stride, 128}};
+  for (const auto& x : of) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(x.d), static_cast<cuuint64_t>(x.heads),
+                                static_cast<cuuint64_t>(s.T)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.d) * 2, static_cast<cuuint64_t>(x.stride) * 2};
+    const cuuint32_t box[3] = {x.cols, 1, 64};
+    const CUresult rc = enc(x.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, box,
+                            ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            x.cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (rc != CUDA_SUCCESS) return fail(TREEWY_ERR_CUDA, "tensor map for q, k or v failed (%d)", (int)rc);
+  }
+  return TREEWY_OK;
+}
+
 treewy_status validate_qk(const treewy_qk* a) {
   if (a == nullptr) return fail(TREEWY_ERR_INVALID_ARG, "qk is NULL");
   if (a->T < 0 || a->T > kMax31)
@@ -143,7 +181,15 @@ treewy_status treewy_extend(const treewy_seqs* seqs, cudaStream_t stream) {
   s.q_stride = stride_or(s.q_stride, int64_t(s.Hk) * s.dk);
   s.k_stride = stride_or(s.k_stride, int64_t(s.Hk) * s.dk);
   s.v_stride = stride_or(s.v_stride, int64_t(s.H) * s.dv);
-  const cudaError_t err = treewy::launch_extend_scan(s, stream);
+  cudaError_t err;
+  if (use_chunks(s)) {
+    treewy::ExtendMaps maps;
+    st = make_extend_maps(s, &maps);
+    if (st != TREEWY_OK) return st;
+    err = treewy::launch_extend_chunk(s, maps, stream);
+  } else {
+    err = treewy::launch_extend_scan(s, stream);
+  }
   return err == cudaSuccess ? TREEWY_OK : cuda_fail(err, "treewy_extend launch");
 }
 

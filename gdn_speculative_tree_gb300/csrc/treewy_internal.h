@@ -117,6 +117,15 @@ cudaError_t launch_storeall_commit(const treewy_batch& b, const float* snapshots
 // most one token per sequence.
 cudaError_t launch_extend_scan(const treewy_seqs& s, cudaStream_t stream);
 
+// Tensor maps of the chunked kernel: q and k as boxes of 64 tokens x 64
+// columns (128B swizzle), v as boxes of 64 tokens x 128 columns (plain rows).
+struct ExtendMaps {
+  CUtensorMap q, k, v;
+};
+// The same in chunks of 64 tokens on the tensor cores (extend_chunk.cu): bf16
+// q/k/v whose rows start on 16 bytes, dk and dv multiples of 8.
+cudaError_t launch_extend_chunk(const treewy_seqs& s, const ExtendMaps& maps, cudaStream_t stream);
+
 cudaError_t launch_qk_norm(const treewy_qk& a, cudaStream_t stream);
 cudaError_t launch_copy_slots(const treewy_slots& a, cudaStream_t stream);
 
