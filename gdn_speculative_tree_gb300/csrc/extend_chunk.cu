@@ -33,9 +33,9 @@
 // Every product takes an f32 operand as two bf16 terms x = hi + lo (16
 // significant bits; lo times lo is left out), accumulates in f32, and keys,
 // queries and values are exact, so a result is within a few 2^-17 of the
-// recurrence's.  The decays are handled as powers of two with an integer and
-// a small f32 part, so that a ratio g_n/g_i is right to f32 rounding however
-// small the products have become, a decay of zero included.
+// recurrence's.  Ratios g_n/g_i are running products of the decays between i
+// and n, never quotients, so they are right however small g has become, a
+// decay of zero included.
 #include "treewy_device.cuh"
 #include "treewy_internal.h"
 
@@ -70,17 +70,16 @@ constexpr uint32_t kOffA = kOffT + 4 * kBox;      // A, then T: f32, 64 rows
 constexpr int kPitchA = 68;
 constexpr uint32_t kSmemBytes = kOffA + kC * kPitchA * 4 + 1024;
 
-struct Gates {
-  float bb[kC], bg[kC], gam[kC];  // b, b g, g of every token
+struct __align__(16) Gates {
+  float a[kC], b[kC], bg[kC], g[kC];  // decay a, b, b g and g (the product of the decays up to it) of every token
+  float dec[kC];                      // g_C / g_n: the product of the decays behind token n
   float gC;
 };
 
 struct ChunkSmem {
   Gates gates[2];
-  int gE[kC];                     // g_n = 2^(gE + gF)
-  float gF[kC], dec[kC];          // dec: g_C / g_n
-  uint64_t full[2], stage_free[2], gates_ready[2], o_read[2];
-  uint64_t fix, gram_done, prep_done, kt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done, drain[2];
+  uint64_t full[2], full_v[2], stage_free[2], v_free[2], gates_ready[2], o_read[2];
+  uint64_t fix, gram_done, prep_done, kt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done, o_tile, drain[2];
   uint32_t tmem;
   int fail;
 };
@@ -148,30 +147,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&a)[16], uin
   tmem_wait16(b);
 }
 
-// a = 2^(e + f) with e whole and f in [-1/2, 1/2); zero as 2^-16384.
-__device__ __forceinline__ void log2_split(float a, int& e, float& f) {
-  if (a == 0.f) {
-    e = -16384;
-    f = 0.f;
-    return;
-  }
-  int shift = 0;
-  if (a < 1.17549435e-38f) {  // below the normal numbers
-    a *= 4294967296.f;
-    shift = 32;
-  }
-  const uint32_t bits = __float_as_uint(a);
-  e = static_cast<int>((bits >> 23) & 255u) - 127;
-  float m = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);  // the sign stays: a negative decay becomes NaN
-  if (m > 1.41421356f) {
-    m *= 0.5f;
-    ++e;
-  }
-  if (((bits >> 23) & 255u) == 255u) m = a;  // infinite or NaN
-  e -= shift;
-  f = log2f(m);
-}
-
 // Row `row`, 16-byte piece `j` of a K-major operand with 128-byte rows.
 __device__ __forceinline__ uint4* operand_piece(unsigned char* tile, int row, int j) {
   return reinterpret_cast<uint4*>(tile + row * 128 + ((j ^ (row & 7)) << 4));
@@ -187,69 +162,157 @@ __device__ __forceinline__ void put_piece(unsigned char* hi, unsigned char* lo, 
 }
 
 __device__ __forceinline__ void prep_sync() { named_bar_sync<1, kPrepThreads>(); }
+// The same, and whether a wait of any preparation thread has given up: all of
+// them leave together, so that none is left at a barrier.
+__device__ __forceinline__ bool prep_failed(bool ok) { return named_bar_or<1, kPrepThreads>(!ok); }
 
-// T = (I + A)^-1 in place of A (unit lower triangular, 64 x 64 f32, zeros
-// above): the two diagonal blocks of 32 by substitution, a column per lane,
-// then T21 = -T22 (A21 T11).
-__device__ __forceinline__ void invert(float* A, int p) {
-  const int w = p >> 5, j = p & 31;
-  if (w < 2) {
-    float* B = A + 32 * w * kPitchA + 32 * w;
-    float x[32];
+// D += A B of one 16 x 8 x 16 warp-level tile with f32 operands as hi and lo.
+struct Frag4 {
+  uint32_t hi[4], lo[4];
+};
+struct Frag2 {
+  uint32_t hi[2], lo[2];
+};
+__device__ __forceinline__ void mma_split(float (&d)[4], const Frag4& a, const Frag2& b) {
+  mma16816_bf16_nv(d, a.lo[0], a.lo[1], a.lo[2], a.lo[3], b.hi[0], b.hi[1]);
+  mma16816_bf16_nv(d, a.hi[0], a.hi[1], a.hi[2], a.hi[3], b.lo[0], b.lo[1]);
+  mma16816_bf16_nv(d, a.hi[0], a.hi[1], a.hi[2], a.hi[3], b.hi[0], b.hi[1]);
+}
+// 16 x 16 left operand at X, 16 x 8 right operand at X (rows the contraction).
+__device__ __forceinline__ Frag4 left_frag(const float* X, int lane) {
+  const float* x = X + (lane >> 2) * kPitchA + 2 * (lane & 3);
+  Frag4 f;
 #pragma unroll
-    for (int n = 0; n < 32; ++n) {
-      float acc0 = n == j ? 1.f : 0.f, acc1 = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = *reinterpret_cast<const float2*>(x + (i & 1) * 8 * kPitchA + (i >> 1) * 8);
+    split_pair(v.x, v.y, f.hi[i], f.lo[i]);
+  }
+  return f;
+}
+__device__ __forceinline__ Frag2 right_frag(const float* X, int lane) {
+  const float* x = X + 2 * (lane & 3) * kPitchA + (lane >> 2);
+  Frag2 f;
 #pragma unroll
-      for (int i = 0; i < n; i += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(B + n * kPitchA + i);
-        acc0 = fmaf(-a.x, x[i], acc0);
-        if (i + 1 < n) acc1 = fmaf(-a.y, x[i + 1], acc1);
-        if (i + 2 < n) acc0 = fmaf(-a.z, x[i + 2], acc0);
-        if (i + 3 < n) acc1 = fmaf(-a.w, x[i + 3], acc1);
-      }
-      x[n] = acc0 + acc1;
+  for (int i = 0; i < 2; ++i) split_pair(x[8 * i * kPitchA], x[(8 * i + 1) * kPitchA], f.hi[i], f.lo[i]);
+  return f;
+}
+// Two neighbouring result tiles as the next product's left operand.
+__device__ __forceinline__ Frag4 left_of(const float (&d0)[4], const float (&d1)[4]) {
+  Frag4 f;
+  split_pair(d0[0], d0[1], f.hi[0], f.lo[0]);
+  split_pair(d0[2], d0[3], f.hi[1], f.lo[1]);
+  split_pair(d1[0], d1[1], f.hi[2], f.lo[2]);
+  split_pair(d1[2], d1[3], f.hi[3], f.lo[3]);
+  return f;
+}
+
+// The operands T and T'' = diag(g_C/g_n) T of T = (I + A)^-1, with A's lower
+// triangle in X (overwritten): the diagonal blocks of 16 by substitution, a
+// column per lane; then blocks of 32 and of 64 by T21 = -(T22 A21) T11 on
+// warp-level MMAs, whose result layout is the next product's left operand.
+// The operands' upper right quarter is zero and not written.
+__device__ __forceinline__ void invert(float* X, const float* dec, unsigned char* tb, int p) {
+  const int w = p >> 5, lane = p & 31;
+  {
+    float* B = X + 16 * w * (kPitchA + 1);
+    const int j = lane & 15;
+    float x[16];
+#pragma unroll
+    for (int n = 0; n < 16; ++n) x[n] = n == j ? 1.f : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      float4 a[16];
+#pragma unroll
+      for (int n = i + 1; n < 16; ++n) a[n] = *reinterpret_cast<const float4*>(B + n * kPitchA + i);
+#pragma unroll
+      for (int n = i + 1; n < 16; ++n) x[n] = fmaf(-a[n].x, x[i], x[n]);
+#pragma unroll
+      for (int n = i + 2; n < 16; ++n) x[n] = fmaf(-a[n].y, x[i + 1], x[n]);
+#pragma unroll
+      for (int n = i + 3; n < 16; ++n) x[n] = fmaf(-a[n].z, x[i + 2], x[n]);
+#pragma unroll
+      for (int n = i + 4; n < 16; ++n) x[n] = fmaf(-a[n].w, x[i + 3], x[n]);
     }
     __syncwarp();
+    if (lane < 16) {
 #pragma unroll
-    for (int n = 0; n < 32; ++n) B[n * kPitchA + j] = x[n];
-  }
-  prep_sync();
-  float acc[8];
-#pragma unroll
-  for (int r = 0; r < 8; ++r) acc[r] = 0.f;
-  const float* rows = A + (32 + 8 * w) * kPitchA;
-#pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const float t0 = A[i * kPitchA + j], t1 = A[(i + 1) * kPitchA + j], t2 = A[(i + 2) * kPitchA + j],
-                t3 = A[(i + 3) * kPitchA + j];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float4 a = *reinterpret_cast<const float4*>(rows + r * kPitchA + i);
-      acc[r] = fmaf(a.x, t0, fmaf(a.y, t1, fmaf(a.z, t2, fmaf(a.w, t3, acc[r]))));
+      for (int n = 0; n < 16; ++n) B[n * kPitchA + j] = x[n];
     }
   }
   prep_sync();
-  float* out = A + (32 + 8 * w) * kPitchA + j;
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    out[r * kPitchA] = acc[r];
-    acc[r] = 0.f;
+  {
+    // blocks of 32: two warps each, 8 columns of T21 per warp
+    float* R = X + 32 * (w >> 1) * (kPitchA + 1);
+    float* A21 = R + 16 * kPitchA;
+    float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+    const Frag4 t22 = left_frag(A21 + 16, lane);
+    mma_split(d0, t22, right_frag(A21, lane));
+    mma_split(d1, t22, right_frag(A21 + 8, lane));
+    mma_split(d, left_of(d0, d1), right_frag(R + 8 * (w & 1), lane));
+    prep_sync();
+    float* out = A21 + (lane >> 2) * kPitchA + 8 * (w & 1) + 2 * (lane & 3);
+    *reinterpret_cast<float2*>(out) = make_float2(-d[0], -d[1]);
+    *reinterpret_cast<float2*>(out + 8 * kPitchA) = make_float2(-d[2], -d[3]);
   }
   prep_sync();
+  {
+    // T's diagonal blocks of 32 as operands: half of a row per thread
+    const int r = p >> 1, c0 = (r & 32) + 16 * (p & 1);
+    const float f = dec[r];
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const float* W = A + 32 * kPitchA + j;
-    const float t0 = W[i * kPitchA], t1 = W[(i + 1) * kPitchA], t2 = W[(i + 2) * kPitchA], t3 = W[(i + 3) * kPitchA];
+    for (int j = 0; j < 2; ++j) {
+      const float4* src = reinterpret_cast<const float4*>(X + r * kPitchA + c0 + 8 * j);
+      const float4 u = src[0], v = src[1];
+      float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+      put_piece(tb, tb + kBox, r, c0 / 8 + j, y);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float4 a = *reinterpret_cast<const float4*>(rows + r * kPitchA + 32 + i);
-      acc[r] = fmaf(a.x, t0, fmaf(a.y, t1, fmaf(a.z, t2, fmaf(a.w, t3, acc[r]))));
+      for (int k = 0; k < 8; ++k) y[k] *= f;
+      put_piece(tb + 2 * kBox, tb + 3 * kBox, r, c0 / 8 + j, y);
     }
   }
-  prep_sync();
+  {
+    // the lower left quarter: 16 rows and 16 columns of it per warp
+    const int m = w & 1, nh = w >> 1;
+    const float* A21 = X + 32 * kPitchA;
+    const float* T22 = A21 + 32 + 16 * m * kPitchA;
+    float pr[4][4], d[2][4];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) out[r * kPitchA] = -acc[r];
-  prep_sync();
+    for (int t = 0; t < 4; ++t) pr[t][0] = pr[t][1] = pr[t][2] = pr[t][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k <= m) {  // T22 is lower triangular
+        const Frag4 t22 = left_frag(T22 + 16 * k, lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) mma_split(pr[t], t22, right_frag(A21 + 16 * k * kPitchA + 8 * t, lane));
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k >= nh) {  // T11 too
+        const Frag4 l = left_of(pr[2 * k], pr[2 * k + 1]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) mma_split(d[t], l, right_frag(X + 16 * k * kPitchA + 16 * nh + 8 * t, lane));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 32 + 16 * m + 8 * e + (lane >> 2);
+      const float f = -dec[r];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t at = sw128_off(r, 16 * nh + 8 * t + 2 * (lane & 3));
+        uint32_t h, l;
+        split_pair(-d[t][2 * e], -d[t][2 * e + 1], h, l);
+        *reinterpret_cast<uint32_t*>(tb + at) = h;
+        *reinterpret_cast<uint32_t*>(tb + kBox + at) = l;
+        split_pair(f * d[t][2 * e], f * d[t][2 * e + 1], h, l);
+        *reinterpret_cast<uint32_t*>(tb + 2 * kBox + at) = h;
+        *reinterpret_cast<uint32_t*>(tb + 3 * kBox + at) = l;
+      }
+    }
+  }
 }
 
 struct SeqInfo {
@@ -348,26 +411,30 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
     const uint32_t ph2 = c >> 1;
     const Gates& g = cs.gates[sg];
     const int n0 = 32 * half, left = q.len - c * kC - n0;  // tokens of this thread's half
-    ok = wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.full[sg], ph2) && wait(cs, &cs.d1_done, c);
+    ok = wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.full_v[sg], ph2) && wait(cs, &cs.d1_done, c);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after_sync();
     uint32_t x0[16], x1[16];
+    unsigned char* vt = base + sg * kStageBytes + 4 * kBox + n0 * 256 + 2 * d;  // column d of V's rows, then of o's
     {
       // W = b v - b g (S k), zero past the sequence's end
       tmem_ld32(tm + kColW + n0, x0, x1);
-      const uint16_t* V = reinterpret_cast<const uint16_t*>(base + sg * kStageBytes + 4 * kBox) + n0 * 128 + d;
       uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float w[2];
+      for (int j = 0; j < 8; ++j) {
+        const float4 b = *reinterpret_cast<const float4*>(g.b + n0 + 4 * j);
+        const float4 bg = *reinterpret_cast<const float4*>(g.bg + n0 + 4 * j);
+        const float bs[4] = {b.x, b.y, b.z, b.w}, bgs[4] = {bg.x, bg.y, bg.z, bg.w};
+        float w[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int n = 2 * e + k;
+        for (int k = 0; k < 4; ++k) {
+          const int n = 4 * j + k;
           const float sk = __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
-          const float v = bf16_bits_to_float(V[n * 128]);
-          w[k] = n < left ? fmaf(-g.bg[n0 + n], sk, g.bb[n0 + n] * v) : 0.f;
+          const float v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + n * 256));
+          w[k] = n < left ? fmaf(-bgs[k], sk, bs[k] * v) : 0.f;
         }
-        split_pair(w[0], w[1], hi[e], lo[e]);
+        split_pair(w[0], w[1], hi[2 * j], lo[2 * j]);
+        split_pair(w[2], w[3], hi[2 * j + 1], lo[2 * j + 1]);
       }
       tmem_st16(tm + kColW + n0, hi);
       tmem_st16(tm + kColW + n0 + 16, lo);
@@ -375,7 +442,6 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
     tmem_wait_st();
     tc_fence_before_sync();
     arrive(&cs.rhs_ready);
-    arrive(&cs.stage_free[sg]);
     // S q of this thread's tokens, scaled, before its columns are written again
     float o[32];
     ok = wait(cs, &cs.qs_done, c);
@@ -385,7 +451,13 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
     tc_fence_before_sync();
     arrive(&cs.qs_read);
 #pragma unroll
-    for (int n = 0; n < 32; ++n) o[n] = g.gam[n0 + n] * __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
+    for (int j = 0; j < 8; ++j) {
+      const float4 f = *reinterpret_cast<const float4*>(g.g + n0 + 4 * j);
+      o[4 * j] = f.x * __uint_as_float(j < 4 ? x0[(4 * j) & 15] : x1[(4 * j) & 15]);
+      o[4 * j + 1] = f.y * __uint_as_float(j < 4 ? x0[(4 * j + 1) & 15] : x1[(4 * j + 1) & 15]);
+      o[4 * j + 2] = f.z * __uint_as_float(j < 4 ? x0[(4 * j + 2) & 15] : x1[(4 * j + 2) & 15]);
+      o[4 * j + 3] = f.w * __uint_as_float(j < 4 ? x0[(4 * j + 3) & 15] : x1[(4 * j + 3) & 15]);
+    }
     // S' = g_C S + W kt
     const float gC = g.gC;
     ok = wait(cs, &cs.d2_done[half], c);
@@ -412,17 +484,38 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
     tmem_ld32(tm + kColO + n0, x0, x1);
     tc_fence_before_sync();
     arrive(&cs.o_read[sg]);
-    if (d < a.dv) {
-      const int64_t at = ((q.tok0 + c * kC + n0) * a.H + h) * static_cast<int64_t>(a.dv) + d;
-      const int64_t step = static_cast<int64_t>(a.H) * a.dv;
+    const int64_t step = static_cast<int64_t>(a.H) * a.dv;
+    const int64_t at0 = ((q.tok0 + c * kC) * a.H + h) * static_cast<int64_t>(a.dv);
+    if constexpr (OF32) {
+      arrive(&cs.v_free[sg]);
+      float* out = reinterpret_cast<float*>(a.o) + at0 + n0 * step + d;
 #pragma unroll
       for (int n = 0; n < 32; ++n) {
-        if (n < left) {
-          const float y = o[n] + __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
-          if constexpr (OF32) reinterpret_cast<float*>(a.o)[at + n * step] = y;
-          else reinterpret_cast<__nv_bfloat16*>(a.o)[at + n * step] = __float2bfloat16_rn(y);
+        if (n < left && d < a.dv) out[n * step] = o[n] + __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
+      }
+    } else {
+      // bf16: the values of o take the place of the thread's own values of V,
+      // and leave from there in pieces of 16 bytes
+#pragma unroll
+      for (int n = 0; n < 32; ++n)
+        *reinterpret_cast<__nv_bfloat16*>(vt + n * 256) =
+            __float2bfloat16_rn(o[n] + __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]));
+      arrive(&cs.o_tile);
+      ok = wait(cs, &cs.o_tile, c);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const unsigned char* tile = base + sg * kStageBytes + 4 * kBox;
+      const int piece = t & 15, rows = min(kC, q.len - c * kC);
+      if (8 * piece < a.dv) {
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + at0 + 8 * piece;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = (t >> 4) + 16 * i;
+          if (n < rows)
+            *reinterpret_cast<uint4*>(out + n * step) = *reinterpret_cast<const uint4*>(tile + n * 256 + 16 * piece);
         }
       }
+      fence_proxy_async_smem();
+      arrive(&cs.v_free[sg]);
     }
   }
   if (ok && d < a.dv) store_state<SB>(a, row, half, S);
@@ -435,8 +528,12 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
   const uint32_t tm = cs.tmem + (static_cast<uint32_t>(p & 96) << 16);
   float* A = reinterpret_cast<float*>(base + kOffA);
   unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
-  // gates of tokens `lane` and `lane + 32` of the chunk, requested one chunk ahead
-  float al[2], be[2];
+  // the upper right quarters of M, T and T'' stay zero
+  for (int i = 16 * p; i < static_cast<int>(6 * kBox); i += 16 * kPrepThreads)
+    *reinterpret_cast<uint4*>(mb + i) = make_uint4(0u, 0u, 0u, 0u);
+  // gates of tokens `lane` and `lane + 32` of the chunk, requested one chunk
+  // ahead by the first warp
+  float al[2] = {1.f, 1.f}, be[2] = {0.f, 0.f};
   auto fetch = [&](int c) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -449,54 +546,46 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
       }
     }
   };
-  fetch(0);
+  if (p < 32) fetch(0);
   bool ok = true;
   for (int c = 0; c < nchunk; ++c) {
     const int sg = c & 1;
     const uint32_t ph2 = c >> 1;
     const int nt = min(kC, q.len - c * kC);
     unsigned char* st = base + sg * kStageBytes;
-    if (c >= 2) ok = wait(cs, &cs.o_read[sg], ph2 - 1);
-    if (!__all_sync(0xffffffffu, ok)) break;
-    // inclusive sums of log2 of the decays: every warp for itself, the first writes
-    int e[2];
-    float f[2];
+    Gates& g = cs.gates[sg];
+    if (p < 32) {
+      if (c >= 2 && !wait(cs, &cs.o_read[sg], ph2 - 1)) ok = false;
+      __syncwarp();
+      // products of the decays up to and behind every token, by doubling
+      float up[2] = {al[0], al[1]}, down[2] = {al[0], al[1]};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      log2_split(al[k], e[k], f[k]);
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
-        const int ey = __shfl_up_sync(0xffffffffu, e[k], s);
-        const float fy = __shfl_up_sync(0xffffffffu, f[k], s);
-        if (lane >= s) {
-          e[k] += ey;
-          f[k] += fy;
+        for (int s = 1; s < 32; s <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, up[k], s), z = __shfl_down_sync(0xffffffffu, down[k], s);
+          if (lane >= s) up[k] *= y;
+          if (lane + s < 32) down[k] *= z;
         }
       }
-    }
-    e[1] += __shfl_sync(0xffffffffu, e[0], 31);
-    f[1] += __shfl_sync(0xffffffffu, f[0], 31);
-    const int eC = __shfl_sync(0xffffffffu, e[1], 31);
-    const float fC = __shfl_sync(0xffffffffu, f[1], 31);
-    if (p < 32) {
-      Gates& g = cs.gates[sg];
+      up[1] *= __shfl_sync(0xffffffffu, up[0], 31);
+      const float half = __shfl_sync(0xffffffffu, down[1], 0);
+      const float next0 = __shfl_down_sync(0xffffffffu, down[0], 1), next1 = __shfl_down_sync(0xffffffffu, down[1], 1);
+      const float dec[2] = {lane < 31 ? next0 * half : half, lane < 31 ? next1 : 1.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int i = lane + 32 * k;
-        const float gam = exp2f(static_cast<float>(e[k]) + f[k]);
-        g.bb[i] = be[k];
-        g.bg[i] = be[k] * gam;
-        g.gam[i] = gam;
-        cs.gE[i] = e[k];
-        cs.gF[i] = f[k];
-        cs.dec[i] = exp2f(static_cast<float>(eC - e[k]) + (fC - f[k]));
+        g.a[i] = al[k];
+        g.b[i] = be[k];
+        g.bg[i] = be[k] * up[k];
+        g.g[i] = up[k];
+        g.dec[i] = dec[k];
       }
-      if (lane == 0) g.gC = exp2f(static_cast<float>(eC) + fC);
+      if (lane == 31) g.gC = up[1];
+      arrive(&cs.gates_ready[sg]);
+      if (c + 1 < nchunk) fetch(c + 1);
     }
-    arrive(&cs.gates_ready[sg]);
-    if (c + 1 < nchunk) fetch(c + 1);
-    ok = wait(cs, &cs.full[sg], ph2);
-    if (!__all_sync(0xffffffffu, ok)) break;
+    if (!wait(cs, &cs.full[sg], ph2)) ok = false;
     if (nt < kC) {
       // rows of K past the sequence's end (the next one's) become zero
       for (int i = nt * 128 + 16 * p; i < static_cast<int>(kBox); i += 16 * kPrepThreads) {
@@ -506,7 +595,7 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
       fence_proxy_async_smem();
       arrive(&cs.fix);
     }
-    prep_sync();
+    if (prep_failed(ok)) break;
     if (p == 0) {
       tc_fence_after_sync();
       constexpr uint32_t id = idesc_bf16_f32(128, kC);
@@ -518,27 +607,31 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
       }
       mma_commit(&cs.gram_done);
     }
-    ok = wait(cs, &cs.gram_done, c);
-    if (!__all_sync(0xffffffffu, ok)) break;
+    if (!wait(cs, &cs.gram_done, c)) ok = false;
+    __syncwarp();
     tc_fence_after_sync();
     {
-      // lanes 0-63: rows of A (f32), lanes 64-127: rows of M (hi and lo)
+      // lanes 0-63: rows of A (f32), lanes 64-127: rows of M (hi and lo), from
+      // the diagonal leftwards; f is b_n (for A) times the decays passed
       const bool isM = p >= 64;
-      const int en = cs.gE[n];
-      const float fn = cs.gF[n], scale = isM ? 1.f : cs.gates[sg].bb[n];
-      const int last = isM ? n + 1 : n;
+      float f = isM ? 1.f : g.b[n];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 1; b >= 0; --b) {
+        if (b == 1 && n < 32) continue;  // a whole warp: the upper right quarter
         uint32_t x0[16], x1[16];
         tmem_ld32(tm + kColG + 32 * b, x0, x1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 3; j >= 0; --j) {
+          const float4 u = *reinterpret_cast<const float4*>(g.a + 32 * b + 8 * j);
+          const float4 v = *reinterpret_cast<const float4*>(g.a + 32 * b + 8 * j + 4);
+          const float as[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
           float y[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 7; k >= 0; --k) {
             const int i = 32 * b + 8 * j + k;
             const float x = __uint_as_float(8 * j + k < 16 ? x0[(8 * j + k) & 15] : x1[(8 * j + k) & 15]);
-            y[k] = i < last ? scale * exp2f(static_cast<float>(en - cs.gE[i]) + (fn - cs.gF[i])) * x : 0.f;
+            y[k] = (isM ? i <= n : i < n) ? f * x : 0.f;
+            if (i <= n) f *= as[k];
           }
           if (isM) {
             put_piece(mb, mb + kBox, n, 4 * b + j, y);
@@ -551,23 +644,8 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
       }
     }
     tc_fence_before_sync();
-    prep_sync();
-    invert(A, p);
-    {
-      // T and (g_C/g_n) T as operands [n][i]: two threads per row
-      const int r = p >> 1, hb = p & 1;
-      const float dec = cs.dec[r];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4* src = reinterpret_cast<const float4*>(A + r * kPitchA + 32 * hb + 8 * j);
-        const float4 u = src[0], v = src[1];
-        float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-        put_piece(tb, tb + kBox, r, 4 * hb + j, y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] *= dec;
-        put_piece(tb + 2 * kBox, tb + 3 * kBox, r, 4 * hb + j, y);
-      }
-    }
+    if (prep_failed(ok)) break;
+    invert(A, g.dec, tb, p);
     fence_proxy_async_smem();
     prep_sync();
     if (p == 0) {
@@ -593,10 +671,10 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
       }
       mma_commit(&cs.prep_done);
     }
-    ok = wait(cs, &cs.prep_done, c);
+    if (!wait(cs, &cs.prep_done, c)) ok = false;
     // the last chunk's kt and M T have been read
-    if (ok && c > 0) ok = wait(cs, &cs.o2_done, c - 1);
-    if (!__all_sync(0xffffffffu, ok)) break;
+    if (c > 0 && !wait(cs, &cs.o2_done, c - 1)) ok = false;
+    __syncwarp();
     tc_fence_after_sync();
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -709,22 +787,26 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
 __device__ __forceinline__ void run_load(const CUtensorMap* map_q, const CUtensorMap* map_k, const CUtensorMap* map_v,
                                          ChunkSmem& cs, unsigned char* base, const SeqInfo& q, int hk, int h,
                                          int nchunk) {
-  int issued = 0;
+  int issued = 0, issued_v = 0;
   for (int c = 0; c < nchunk; ++c) {
     const int sg = c & 1;
     if (c >= 2 && !wait(cs, &cs.stage_free[sg], (c >> 1) - 1)) break;
     unsigned char* st = base + sg * kStageBytes;
     const int tok = static_cast<int>(q.tok0) + c * kC;
-    mbar_arrive_expect_tx(&cs.full[sg], kStageBytes);
+    mbar_arrive_expect_tx(&cs.full[sg], 4 * kBox);
     tma_load_3d(st, map_k, &cs.full[sg], 0, hk, tok);
     tma_load_3d(st + 2 * kBox, map_k, &cs.full[sg], 64, hk, tok);
     tma_load_3d(st + kBox, map_q, &cs.full[sg], 0, hk, tok);
     tma_load_3d(st + 3 * kBox, map_q, &cs.full[sg], 64, hk, tok);
-    tma_load_3d(st + 4 * kBox, map_v, &cs.full[sg], 0, h, tok);
     ++issued;
+    if (c >= 2 && !wait(cs, &cs.v_free[sg], (c >> 1) - 1)) break;
+    mbar_arrive_expect_tx(&cs.full_v[sg], 2 * kBox);
+    tma_load_3d(st + 4 * kBox, map_v, &cs.full_v[sg], 0, h, tok);
+    ++issued_v;
   }
   // no copy targets this CTA's memory once it has ended
   for (int c = max(0, issued - 2); c < issued; ++c) mbar_wait(&cs.full[c & 1], (c >> 1) & 1);
+  for (int c = max(0, issued_v - 2); c < issued_v; ++c) mbar_wait(&cs.full_v[c & 1], (c >> 1) & 1);
 }
 
 template <bool SB, bool OF32>
@@ -768,8 +850,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cs.full[i], 1);
-      mbar_init(&cs.stage_free[i], 1 + kStateThreads + kPrepThreads);
-      mbar_init(&cs.gates_ready[i], kPrepThreads);
+      mbar_init(&cs.full_v[i], 1);
+      mbar_init(&cs.stage_free[i], 1 + kPrepThreads);
+      mbar_init(&cs.v_free[i], kStateThreads);
+      mbar_init(&cs.gates_ready[i], 32);
       mbar_init(&cs.o_read[i], kStateThreads);
       mbar_init(&cs.s_ready[i], kStateThreads / 2);
       mbar_init(&cs.d2_done[i], 1);
@@ -784,6 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&cs.rhs_ready, kStateThreads);
     mbar_init(&cs.qs_read, kStateThreads);
     mbar_init(&cs.o2_done, 1);
+    mbar_init(&cs.o_tile, kStateThreads);
     cs.fail = 0;
     fence_mbarrier_init();
   }

@@ -70,7 +70,8 @@ bool use_chunks(const treewy_seqs& s) {
   auto rows_on16 = [](const void* p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; };
   return s.qkv_dtype == TREEWY_DTYPE_BF16 && s.dk % 8 == 0 && s.dv % 8 == 0 && s.T > 0 &&
          s.max_len >= kChunkedLen && (s.flags & TREEWY_FLAG_FORCE_GENERIC) == 0 &&
-         rows_on16(s.q, s.q_stride) && rows_on16(s.k, s.k_stride) && rows_on16(s.v, s.v_stride);
+         rows_on16(s.q, s.q_stride) && rows_on16(s.k, s.k_stride) && rows_on16(s.v, s.v_stride) &&
+         aligned(s.o, 16);
 }
 
 treewy_status make_extend_maps(const treewy_seqs& s, treewy::ExtendMaps* m) {
