@@ -24,11 +24,13 @@
 // row, and the left operands S and W go back to TMEM as bf16 without passing
 // through shared memory.
 //
-//   warps 0-7   state: two threads per row (64 of S's columns and 32 tokens
-//               each); S stays in f32 registers for the whole sequence
-//   warps 8-11  preparation of the next chunk: gates, [K;Q] K^T, T, M T, kt
-//   warp 12     issues the chain's products
-//   warp 13     loads K, Q and V, two chunks in flight
+//   warps 0-7    state: two threads per row (64 of S's columns and 32 tokens
+//                each); S stays in f32 registers for the whole sequence
+//   warps 8-15   preparation of the next chunk: [K;Q] K^T, T, M T, kt
+//   warps 16-19  o
+//   warp 20      issues the chain's products
+//   warp 21      loads K, Q and V, two chunks in flight
+//   warp 22      gates
 //
 // Every product takes an f32 operand as two bf16 terms x = hi + lo (16
 // significant bits; lo times lo is left out), accumulates in f32, and keys,
@@ -43,14 +45,19 @@ namespace treewy {
 namespace {
 
 constexpr int kC = 64;                       // tokens per chunk
-constexpr int kStateThreads = 256;
-constexpr int kPrepThreads = 128;
-constexpr int kThreads = kStateThreads + kPrepThreads + 64;
-constexpr int kMmaWarp = 12, kLoadWarp = 13;
+constexpr int kStateWarps = 8, kPrepWarps = 8, kOutWarps = 4;
+constexpr int kPrepWarp = kStateWarps, kOutWarp = kPrepWarp + kPrepWarps, kMmaWarp = kOutWarp + kOutWarps,
+              kLoadWarp = kMmaWarp + 1, kGateWarp = kLoadWarp + 1;
+constexpr int kPrepThreads = 32 * kPrepWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 4);
+// Registers per thread: 80 at launch; the state warps take what the others
+// give back (2 x 112 + 2 x 64 + 96 + 32 = 6 x 80 per 128 threads).
+constexpr int kStateRegs = 112, kPrepRegs = 64, kOutRegs = 96, kMiscRegs = 32;
+static_assert(2 * kStateRegs + 2 * kPrepRegs + kOutRegs + kMiscRegs == 6 * 80, "the launch's registers");
 
 // TMEM columns
 constexpr uint32_t kColS = 0;                // S: hi in 64 columns, lo in 64 (bf16 pairs)
-constexpr uint32_t kColW = 128;              // S k, then W (32 columns per half of the tokens: hi 16, lo 16)
+constexpr uint32_t kColW = 128;              // S k, then W (16 columns per 16 tokens: hi 8, lo 8)
 constexpr uint32_t kColO = 192;              // S q, then (M T) W
 constexpr uint32_t kColD = 256;              // sum W kt^T
 constexpr uint32_t kColG = 384;              // [K;Q] K^T, then M T
@@ -73,13 +80,16 @@ constexpr uint32_t kSmemBytes = kOffA + kC * kPitchA * 4 + 1024;
 struct __align__(16) Gates {
   float a[kC], b[kC], bg[kC], g[kC];  // decay a, b, b g and g (the product of the decays up to it) of every token
   float dec[kC];                      // g_C / g_n: the product of the decays behind token n
+  float mid[kC];                      // product of the decays from token 32 to n (1 for n < 32)
   float gC;
 };
 
+// Barriers count warps (lane 0 arrives for its warp) or commits of products.
 struct ChunkSmem {
   Gates gates[2];
-  uint64_t full[2], full_v[2], stage_free[2], v_free[2], gates_ready[2], o_read[2];
-  uint64_t fix, gram_done, prep_done, kt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done, o_tile, drain[2];
+  uint64_t full[2], full_v[2], stage_free[2], v_free[2], gates_ready[2], gates_free[2];
+  uint64_t fix, gram_done, prep_done, kt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done,
+      o_read, o_tile, drain[2];
   uint32_t tmem;
   int fail;
 };
@@ -102,19 +112,48 @@ __device__ __forceinline__ bool wait(ChunkSmem& cs, uint64_t* bar, uint32_t pari
   }
 }
 
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+// One arrival for the warp, after everything its threads have done.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// D(tmem) (+)= A(tmem, bf16 pairs) * B(smem desc)^T
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Products are issued by whole warps, converged, with all but one lane
+// predicated off: descriptors then stay in uniform registers.
+// D(tmem) (+)= A(smem desc or tmem, bf16 pairs) * B(smem desc)^T
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+  if (lead) mma_commit(bar);
+  __syncwarp();
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Descriptor of an operand whose rows run along the contraction (MN-major),
@@ -128,24 +167,13 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t 
 }
 constexpr uint32_t kAmajorMN = 1u << 15, kBmajorMN = 1u << 16;
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
-      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// 32 consecutive columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&a)[16], uint32_t (&b)[16]) {
-  tmem_ld16_async(taddr, a);
-  tmem_ld16_async(taddr + 16, b);
-  tmem_wait16(a);
-  tmem_wait16(b);
-}
 
 // Row `row`, 16-byte piece `j` of a K-major operand with 128-byte rows.
 __device__ __forceinline__ uint4* operand_piece(unsigned char* tile, int row, int j) {
@@ -209,11 +237,11 @@ __device__ __forceinline__ Frag4 left_of(const float (&d0)[4], const float (&d1)
 // The operands T and T'' = diag(g_C/g_n) T of T = (I + A)^-1, with A's lower
 // triangle in X (overwritten): the diagonal blocks of 16 by substitution, a
 // column per lane; then blocks of 32 and of 64 by T21 = -(T22 A21) T11 on
-// warp-level MMAs, whose result layout is the next product's left operand.
-// The operands' upper right quarter is zero and not written.
+// warp-level MMAs, a tile per warp.  The operands' upper right quarter is zero
+// and not written; X's takes T22 A21.
 __device__ __forceinline__ void invert(float* X, const float* dec, unsigned char* tb, int p) {
   const int w = p >> 5, lane = p & 31;
-  {
+  if (w < 4) {
     float* B = X + 16 * w * (kPitchA + 1);
     const int j = lane & 15;
     float x[16];
@@ -221,17 +249,14 @@ __device__ __forceinline__ void invert(float* X, const float* dec, unsigned char
     for (int n = 0; n < 16; ++n) x[n] = n == j ? 1.f : 0.f;
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
-      float4 a[16];
 #pragma unroll
-      for (int n = i + 1; n < 16; ++n) a[n] = *reinterpret_cast<const float4*>(B + n * kPitchA + i);
-#pragma unroll
-      for (int n = i + 1; n < 16; ++n) x[n] = fmaf(-a[n].x, x[i], x[n]);
-#pragma unroll
-      for (int n = i + 2; n < 16; ++n) x[n] = fmaf(-a[n].y, x[i + 1], x[n]);
-#pragma unroll
-      for (int n = i + 3; n < 16; ++n) x[n] = fmaf(-a[n].z, x[i + 2], x[n]);
-#pragma unroll
-      for (int n = i + 4; n < 16; ++n) x[n] = fmaf(-a[n].w, x[i + 3], x[n]);
+      for (int n = i + 1; n < 16; ++n) {
+        const float4 a = *reinterpret_cast<const float4*>(B + n * kPitchA + i);
+        x[n] = fmaf(-a.x, x[i], x[n]);
+        if (n > i + 1) x[n] = fmaf(-a.y, x[i + 1], x[n]);
+        if (n > i + 2) x[n] = fmaf(-a.z, x[i + 2], x[n]);
+        if (n > i + 3) x[n] = fmaf(-a.w, x[i + 3], x[n]);
+      }
     }
     __syncwarp();
     if (lane < 16) {
@@ -241,76 +266,73 @@ __device__ __forceinline__ void invert(float* X, const float* dec, unsigned char
   }
   prep_sync();
   {
-    // blocks of 32: two warps each, 8 columns of T21 per warp
-    float* R = X + 32 * (w >> 1) * (kPitchA + 1);
+    // blocks of 32: 8 columns of T21 per warp
+    float* R = X + 32 * (w >> 2) * (kPitchA + 1);
     float* A21 = R + 16 * kPitchA;
+    const int t = w & 3;
     float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
-    const Frag4 t22 = left_frag(A21 + 16, lane);
-    mma_split(d0, t22, right_frag(A21, lane));
-    mma_split(d1, t22, right_frag(A21 + 8, lane));
-    mma_split(d, left_of(d0, d1), right_frag(R + 8 * (w & 1), lane));
+    if (t < 2) {
+      const Frag4 t22 = left_frag(A21 + 16, lane);
+      mma_split(d0, t22, right_frag(A21, lane));
+      mma_split(d1, t22, right_frag(A21 + 8, lane));
+      mma_split(d, left_of(d0, d1), right_frag(R + 8 * t, lane));
+    }
     prep_sync();
-    float* out = A21 + (lane >> 2) * kPitchA + 8 * (w & 1) + 2 * (lane & 3);
-    *reinterpret_cast<float2*>(out) = make_float2(-d[0], -d[1]);
-    *reinterpret_cast<float2*>(out + 8 * kPitchA) = make_float2(-d[2], -d[3]);
+    if (t < 2) {
+      float* out = A21 + (lane >> 2) * kPitchA + 8 * t + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(out) = make_float2(-d[0], -d[1]);
+      *reinterpret_cast<float2*>(out + 8 * kPitchA) = make_float2(-d[2], -d[3]);
+    }
+  }
+  prep_sync();
+  // the lower left quarter: 16 rows and 8 columns of it per warp
+  const int m = w & 1, t = w >> 1;
+  float* P = X + 32;
+  {
+    const float* A21 = X + 32 * kPitchA;
+    const float* T22 = A21 + 32 + 16 * m * kPitchA;
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k <= m)  // T22 is lower triangular
+        mma_split(d, left_frag(T22 + 16 * k, lane), right_frag(A21 + 16 * k * kPitchA + 8 * t, lane));
+    }
+    float* out = P + (16 * m + (lane >> 2)) * kPitchA + 8 * t + 2 * (lane & 3);
+    *reinterpret_cast<float2*>(out) = make_float2(d[0], d[1]);
+    *reinterpret_cast<float2*>(out + 8 * kPitchA) = make_float2(d[2], d[3]);
+  }
+  {
+    // T's diagonal blocks of 32 as operands: eight values per thread
+    const int r = p >> 2, c0 = (r & 32) + 8 * (p & 3);
+    const float f = dec[r];
+    const float4* src = reinterpret_cast<const float4*>(X + r * kPitchA + c0);
+    const float4 u = src[0], v = src[1];
+    float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    put_piece(tb, tb + kBox, r, c0 / 8, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] *= f;
+    put_piece(tb + 2 * kBox, tb + 3 * kBox, r, c0 / 8, y);
   }
   prep_sync();
   {
-    // T's diagonal blocks of 32 as operands: half of a row per thread
-    const int r = p >> 1, c0 = (r & 32) + 16 * (p & 1);
-    const float f = dec[r];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float4* src = reinterpret_cast<const float4*>(X + r * kPitchA + c0 + 8 * j);
-      const float4 u = src[0], v = src[1];
-      float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-      put_piece(tb, tb + kBox, r, c0 / 8 + j, y);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] *= f;
-      put_piece(tb + 2 * kBox, tb + 3 * kBox, r, c0 / 8 + j, y);
-    }
-  }
-  {
-    // the lower left quarter: 16 rows and 16 columns of it per warp
-    const int m = w & 1, nh = w >> 1;
-    const float* A21 = X + 32 * kPitchA;
-    const float* T22 = A21 + 32 + 16 * m * kPitchA;
-    float pr[4][4], d[2][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) pr[t][0] = pr[t][1] = pr[t][2] = pr[t][3] = 0.f;
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (k <= m) {  // T22 is lower triangular
-        const Frag4 t22 = left_frag(T22 + 16 * k, lane);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) mma_split(pr[t], t22, right_frag(A21 + 16 * k * kPitchA + 8 * t, lane));
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k >= nh) {  // T11 too
-        const Frag4 l = left_of(pr[2 * k], pr[2 * k + 1]);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) mma_split(d[t], l, right_frag(X + 16 * k * kPitchA + 16 * nh + 8 * t, lane));
-      }
+      if (k >= (t >> 1))  // T11 is lower triangular
+        mma_split(d, left_frag(P + 16 * m * kPitchA + 16 * k, lane), right_frag(X + 16 * k * kPitchA + 8 * t, lane));
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 32 + 16 * m + 8 * e + (lane >> 2);
       const float f = -dec[r];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t at = sw128_off(r, 16 * nh + 8 * t + 2 * (lane & 3));
-        uint32_t h, l;
-        split_pair(-d[t][2 * e], -d[t][2 * e + 1], h, l);
-        *reinterpret_cast<uint32_t*>(tb + at) = h;
-        *reinterpret_cast<uint32_t*>(tb + kBox + at) = l;
-        split_pair(f * d[t][2 * e], f * d[t][2 * e + 1], h, l);
-        *reinterpret_cast<uint32_t*>(tb + 2 * kBox + at) = h;
-        *reinterpret_cast<uint32_t*>(tb + 3 * kBox + at) = l;
-      }
+      const uint32_t at = sw128_off(r, 8 * t + 2 * (lane & 3));
+      uint32_t h, l;
+      split_pair(-d[2 * e], -d[2 * e + 1], h, l);
+      *reinterpret_cast<uint32_t*>(tb + at) = h;
+      *reinterpret_cast<uint32_t*>(tb + kBox + at) = l;
+      split_pair(f * d[2 * e], f * d[2 * e + 1], h, l);
+      *reinterpret_cast<uint32_t*>(tb + 2 * kBox + at) = h;
+      *reinterpret_cast<uint32_t*>(tb + 3 * kBox + at) = l;
     }
   }
 }
@@ -377,17 +399,17 @@ __device__ __forceinline__ void store_state(const treewy_seqs& a, int64_t row, i
   }
 }
 
-// Columns 32 b .. 32 b + 31 of this thread's half of S as the left operand.
-__device__ __forceinline__ void put_state(uint32_t tm, int half, int b, const float (&S)[64]) {
-  uint32_t hi[16], lo[16];
+// Columns 16 b .. 16 b + 15 of this thread's half of S as the left operand.
+__device__ __forceinline__ void put_state16(uint32_t tm, int half, int b, const float (&S)[64]) {
+  uint32_t hi[8], lo[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) split_pair(S[32 * b + 2 * e], S[32 * b + 2 * e + 1], hi[e], lo[e]);
-  tmem_st16(tm + kColS + 32 * half + 16 * b, hi);
-  tmem_st16(tm + kColS + 64 + 32 * half + 16 * b, lo);
+  for (int e = 0; e < 8; ++e) split_pair(S[16 * b + 2 * e], S[16 * b + 2 * e + 1], hi[e], lo[e]);
+  tmem_st8(tm + kColS + 32 * half + 8 * b, hi);
+  tmem_st8(tm + kColS + 64 + 32 * half + 8 * b, lo);
 }
 
 // The state warps.
-template <bool SB, bool OF32>
+template <bool SB>
 __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, unsigned char* base, const SeqInfo& q,
                                           int h, int nchunk) {
   const int t = threadIdx.x, d = t & 127, half = t >> 7;
@@ -401,140 +423,159 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
     for (int i = 0; i < 64; ++i) S[i] = 0.f;
   }
 #pragma unroll
-  for (int b = 0; b < 2; ++b) put_state(tm, half, b, S);
+  for (int b = 0; b < 4; ++b) put_state16(tm, half, b, S);
   tmem_wait_st();
   tc_fence_before_sync();
-  arrive(&cs.s_ready[half]);
+  warp_arrive(&cs.s_ready[half]);
   bool ok = true;
+  const int n0 = 32 * half;
   for (int c = 0; c < nchunk; ++c) {
     const int sg = c & 1;
     const uint32_t ph2 = c >> 1;
     const Gates& g = cs.gates[sg];
-    const int n0 = 32 * half, left = q.len - c * kC - n0;  // tokens of this thread's half
+    const int left = q.len - c * kC - n0;  // tokens of this thread's half
     ok = wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.full_v[sg], ph2) && wait(cs, &cs.d1_done, c);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after_sync();
-    uint32_t x0[16], x1[16];
-    unsigned char* vt = base + sg * kStageBytes + 4 * kBox + n0 * 256 + 2 * d;  // column d of V's rows, then of o's
     {
       // W = b v - b g (S k), zero past the sequence's end
-      tmem_ld32(tm + kColW + n0, x0, x1);
-      uint32_t hi[16], lo[16];
+      const unsigned char* vt = base + sg * kStageBytes + 4 * kBox + n0 * 256 + 2 * d;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 b = *reinterpret_cast<const float4*>(g.b + n0 + 4 * j);
-        const float4 bg = *reinterpret_cast<const float4*>(g.bg + n0 + 4 * j);
-        const float bs[4] = {b.x, b.y, b.z, b.w}, bgs[4] = {bg.x, bg.y, bg.z, bg.w};
-        float w[4];
+      for (int b = 0; b < 2; ++b) {
+        uint32_t x[16], hi[8], lo[8];
+        tmem_ld16_async(tm + kColW + n0 + 16 * b, x);
+        tmem_wait16(x);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int n = 4 * j + k;
-          const float sk = __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
-          const float v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + n * 256));
-          w[k] = n < left ? fmaf(-bgs[k], sk, bs[k] * v) : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          const int n = 16 * b + 4 * j;
+          const float4 fb = *reinterpret_cast<const float4*>(g.b + n0 + n);
+          const float4 fg = *reinterpret_cast<const float4*>(g.bg + n0 + n);
+          const float bs[4] = {fb.x, fb.y, fb.z, fb.w}, bgs[4] = {fg.x, fg.y, fg.z, fg.w};
+          float w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + (n + k) * 256));
+            w[k] = n + k < left ? fmaf(-bgs[k], __uint_as_float(x[4 * j + k]), bs[k] * v) : 0.f;
+          }
+          split_pair(w[0], w[1], hi[2 * j], lo[2 * j]);
+          split_pair(w[2], w[3], hi[2 * j + 1], lo[2 * j + 1]);
         }
-        split_pair(w[0], w[1], hi[2 * j], lo[2 * j]);
-        split_pair(w[2], w[3], hi[2 * j + 1], lo[2 * j + 1]);
+        // 16 tokens: hi in 8 columns, lo in 8, in place of what was just read
+        tmem_st8(tm + kColW + n0 + 16 * b, hi);
+        tmem_st8(tm + kColW + n0 + 16 * b + 8, lo);
       }
-      tmem_st16(tm + kColW + n0, hi);
-      tmem_st16(tm + kColW + n0 + 16, lo);
     }
     tmem_wait_st();
     tc_fence_before_sync();
-    arrive(&cs.rhs_ready);
-    // S q of this thread's tokens, scaled, before its columns are written again
-    float o[32];
-    ok = wait(cs, &cs.qs_done, c);
-    if (!__all_sync(0xffffffffu, ok)) break;
-    tc_fence_after_sync();
-    tmem_ld32(tm + kColO + n0, x0, x1);
-    tc_fence_before_sync();
-    arrive(&cs.qs_read);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 f = *reinterpret_cast<const float4*>(g.g + n0 + 4 * j);
-      o[4 * j] = f.x * __uint_as_float(j < 4 ? x0[(4 * j) & 15] : x1[(4 * j) & 15]);
-      o[4 * j + 1] = f.y * __uint_as_float(j < 4 ? x0[(4 * j + 1) & 15] : x1[(4 * j + 1) & 15]);
-      o[4 * j + 2] = f.z * __uint_as_float(j < 4 ? x0[(4 * j + 2) & 15] : x1[(4 * j + 2) & 15]);
-      o[4 * j + 3] = f.w * __uint_as_float(j < 4 ? x0[(4 * j + 3) & 15] : x1[(4 * j + 3) & 15]);
-    }
+    warp_arrive(&cs.rhs_ready);
     // S' = g_C S + W kt
     const float gC = g.gC;
     ok = wait(cs, &cs.d2_done[half], c);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after_sync();
+    const bool more = c + 1 < nchunk;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      tmem_ld32(tm + kColD + 64 * half + 32 * b, x0, x1);
+    for (int b = 0; b < 4; ++b) {
+      uint32_t x[16];
+      tmem_ld16_async(tm + kColD + 64 * half + 16 * b, x);
+      tmem_wait16(x);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        S[32 * b + e] = fmaf(gC, S[32 * b + e], __uint_as_float(x0[e]));
-        S[32 * b + 16 + e] = fmaf(gC, S[32 * b + 16 + e], __uint_as_float(x1[e]));
-      }
-      if (c + 1 < nchunk) put_state(tm, half, b, S);
+      for (int e = 0; e < 16; ++e) S[16 * b + e] = fmaf(gC, S[16 * b + e], __uint_as_float(x[e]));
+      if (more) put_state16(tm, half, b, S);
     }
-    if (c + 1 < nchunk) {
+    if (more) {
       tmem_wait_st();
       tc_fence_before_sync();
-      arrive(&cs.s_ready[half]);
+      warp_arrive(&cs.s_ready[half]);
     }
+    warp_arrive(&cs.gates_free[sg]);
+  }
+  if (ok && d < a.dv) store_state<SB>(a, row, half, S);
+}
+
+// The output warps: o = g (S q) + (M T) W, a row of 64 tokens per thread.
+template <bool OF32>
+__device__ __forceinline__ void run_out(const treewy_seqs& a, ChunkSmem& cs, unsigned char* base, const SeqInfo& q,
+                                        int h, int nchunk) {
+  const int t = threadIdx.x - 32 * kOutWarp, d = t;
+  const uint32_t tm = cs.tmem + (static_cast<uint32_t>(d & 96) << 16);
+  const int64_t step = static_cast<int64_t>(a.H) * a.dv;
+  for (int c = 0; c < nchunk; ++c) {
+    const int sg = c & 1;
+    const uint32_t ph2 = c >> 1;
+    const Gates& g = cs.gates[sg];
+    float o[64];
+    bool ok = wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.qs_done, c);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    tc_fence_after_sync();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      uint32_t x[16];
+      tmem_ld16_async(tm + kColO + 16 * b, x);
+      tmem_wait16(x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 f = *reinterpret_cast<const float4*>(g.g + 16 * b + 4 * j);
+        o[16 * b + 4 * j] = f.x * __uint_as_float(x[4 * j]);
+        o[16 * b + 4 * j + 1] = f.y * __uint_as_float(x[4 * j + 1]);
+        o[16 * b + 4 * j + 2] = f.z * __uint_as_float(x[4 * j + 2]);
+        o[16 * b + 4 * j + 3] = f.w * __uint_as_float(x[4 * j + 3]);
+      }
+    }
+    tc_fence_before_sync();
+    warp_arrive(&cs.qs_read);
+    warp_arrive(&cs.gates_free[sg]);
     ok = wait(cs, &cs.o2_done, c);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after_sync();
-    tmem_ld32(tm + kColO + n0, x0, x1);
-    tc_fence_before_sync();
-    arrive(&cs.o_read[sg]);
-    const int64_t step = static_cast<int64_t>(a.H) * a.dv;
+    const int rows = min(kC, q.len - c * kC);
     const int64_t at0 = ((q.tok0 + c * kC) * a.H + h) * static_cast<int64_t>(a.dv);
-    if constexpr (OF32) {
-      arrive(&cs.v_free[sg]);
-      float* out = reinterpret_cast<float*>(a.o) + at0 + n0 * step + d;
+    // bf16: o takes V's place (the state warps have read it: W is made) and
+    // leaves from there in pieces of 16 bytes
+    unsigned char* tile = base + sg * kStageBytes + 4 * kBox;
 #pragma unroll
-      for (int n = 0; n < 32; ++n) {
-        if (n < left && d < a.dv) out[n * step] = o[n] + __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]);
+    for (int b = 0; b < 4; ++b) {
+      uint32_t x[16];
+      tmem_ld16_async(tm + kColO + 16 * b, x);
+      tmem_wait16(x);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int n = 16 * b + e;
+        const float y = o[n] + __uint_as_float(x[e]);
+        if constexpr (OF32) {
+          if (n < rows && d < a.dv) reinterpret_cast<float*>(a.o)[at0 + n * step + d] = y;
+        } else {
+          *reinterpret_cast<__nv_bfloat16*>(tile + n * 256 + 2 * d) = __float2bfloat16_rn(y);
+        }
       }
-    } else {
-      // bf16: the values of o take the place of the thread's own values of V,
-      // and leave from there in pieces of 16 bytes
-#pragma unroll
-      for (int n = 0; n < 32; ++n)
-        *reinterpret_cast<__nv_bfloat16*>(vt + n * 256) =
-            __float2bfloat16_rn(o[n] + __uint_as_float(n < 16 ? x0[n & 15] : x1[n & 15]));
-      arrive(&cs.o_tile);
+    }
+    tc_fence_before_sync();
+    warp_arrive(&cs.o_read);
+    if constexpr (!OF32) {
+      warp_arrive(&cs.o_tile);
       ok = wait(cs, &cs.o_tile, c);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const unsigned char* tile = base + sg * kStageBytes + 4 * kBox;
-      const int piece = t & 15, rows = min(kC, q.len - c * kC);
+      const int piece = t & 15;
       if (8 * piece < a.dv) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + at0 + 8 * piece;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = (t >> 4) + 16 * i;
+        for (int i = 0; i < 8; ++i) {
+          const int n = (t >> 4) + 8 * i;
           if (n < rows)
             *reinterpret_cast<uint4*>(out + n * step) = *reinterpret_cast<const uint4*>(tile + n * 256 + 16 * piece);
         }
       }
       fence_proxy_async_smem();
-      arrive(&cs.v_free[sg]);
     }
+    warp_arrive(&cs.v_free[sg]);
   }
-  if (ok && d < a.dv) store_state<SB>(a, row, half, S);
 }
 
-// The preparation warps: T, M T and kt of every chunk, one chunk ahead of the state.
-__device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, unsigned char* base, const SeqInfo& q,
-                                         int h, int nchunk) {
-  const int p = threadIdx.x - kStateThreads, lane = p & 31, n = p & 63;
-  const uint32_t tm = cs.tmem + (static_cast<uint32_t>(p & 96) << 16);
-  float* A = reinterpret_cast<float*>(base + kOffA);
-  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
-  // the upper right quarters of M, T and T'' stay zero
-  for (int i = 16 * p; i < static_cast<int>(6 * kBox); i += 16 * kPrepThreads)
-    *reinterpret_cast<uint4*>(mb + i) = make_uint4(0u, 0u, 0u, 0u);
-  // gates of tokens `lane` and `lane + 32` of the chunk, requested one chunk
-  // ahead by the first warp
-  float al[2] = {1.f, 1.f}, be[2] = {0.f, 0.f};
-  auto fetch = [&](int c) {
+// One warp: the gates of every chunk.
+__device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, const SeqInfo& q, int h, int nchunk) {
+  const int lane = threadIdx.x & 31;
+  float al[2], be[2];
+  auto fetch = [&](int c) {  // tokens `lane` and `lane + 32`; past the end they change nothing
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = c * kC + lane + 32 * k;
@@ -546,46 +587,66 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
       }
     }
   };
-  if (p < 32) fetch(0);
+  fetch(0);
+  for (int c = 0; c < nchunk; ++c) {
+    const int sg = c & 1;
+    // products of the decays up to and behind every token, by doubling
+    float up[2] = {al[0], al[1]}, down[2] = {al[0], al[1]};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, up[k], s), z = __shfl_down_sync(0xffffffffu, down[k], s);
+        if (lane >= s) up[k] *= y;
+        if (lane + s < 32) down[k] *= z;
+      }
+    }
+    const float mid = up[1];
+    up[1] *= __shfl_sync(0xffffffffu, up[0], 31);
+    const float half = __shfl_sync(0xffffffffu, down[1], 0);
+    const float next0 = __shfl_down_sync(0xffffffffu, down[0], 1), next1 = __shfl_down_sync(0xffffffffu, down[1], 1);
+    const float dec[2] = {lane < 31 ? next0 * half : half, lane < 31 ? next1 : 1.f};
+    const bool ok = c < 2 || wait(cs, &cs.gates_free[sg], (c >> 1) - 1);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    Gates& g = cs.gates[sg];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = lane + 32 * k;
+      g.a[i] = al[k];
+      g.b[i] = be[k];
+      g.bg[i] = be[k] * up[k];
+      g.g[i] = up[k];
+      g.dec[i] = dec[k];
+      g.mid[i] = k ? mid : 1.f;
+    }
+    if (lane == 31) g.gC = up[1];
+    warp_arrive(&cs.gates_ready[sg]);
+    if (c + 1 < nchunk) fetch(c + 1);
+  }
+}
+
+// The preparation warps: T, M T and kt of every chunk, one chunk ahead of the
+// state.  Warps p and p + 4 share a quarter of the lanes (rows), half of the
+// columns each.
+__device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int len, int nchunk) {
+  const int p = threadIdx.x - 32 * kPrepWarp, row = p & 127, n = p & 63, hh = p >> 7;
+  const bool first = p < 32;
+  const uint32_t lead = p == 0;
+  const uint32_t tm = cs.tmem + (static_cast<uint32_t>(p & 96) << 16);
+  float* A = reinterpret_cast<float*>(base + kOffA);
+  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
+  // the upper right quarters of M, T and T'' stay zero
+  for (int i = 16 * p; i < static_cast<int>(6 * kBox); i += 16 * kPrepThreads)
+    *reinterpret_cast<uint4*>(mb + i) = make_uint4(0u, 0u, 0u, 0u);
   bool ok = true;
   for (int c = 0; c < nchunk; ++c) {
     const int sg = c & 1;
     const uint32_t ph2 = c >> 1;
-    const int nt = min(kC, q.len - c * kC);
+    const int nt = min(kC, len - c * kC);
     unsigned char* st = base + sg * kStageBytes;
-    Gates& g = cs.gates[sg];
-    if (p < 32) {
-      if (c >= 2 && !wait(cs, &cs.o_read[sg], ph2 - 1)) ok = false;
-      __syncwarp();
-      // products of the decays up to and behind every token, by doubling
-      float up[2] = {al[0], al[1]}, down[2] = {al[0], al[1]};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-          const float y = __shfl_up_sync(0xffffffffu, up[k], s), z = __shfl_down_sync(0xffffffffu, down[k], s);
-          if (lane >= s) up[k] *= y;
-          if (lane + s < 32) down[k] *= z;
-        }
-      }
-      up[1] *= __shfl_sync(0xffffffffu, up[0], 31);
-      const float half = __shfl_sync(0xffffffffu, down[1], 0);
-      const float next0 = __shfl_down_sync(0xffffffffu, down[0], 1), next1 = __shfl_down_sync(0xffffffffu, down[1], 1);
-      const float dec[2] = {lane < 31 ? next0 * half : half, lane < 31 ? next1 : 1.f};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int i = lane + 32 * k;
-        g.a[i] = al[k];
-        g.b[i] = be[k];
-        g.bg[i] = be[k] * up[k];
-        g.g[i] = up[k];
-        g.dec[i] = dec[k];
-      }
-      if (lane == 31) g.gC = up[1];
-      arrive(&cs.gates_ready[sg]);
-      if (c + 1 < nchunk) fetch(c + 1);
-    }
+    const Gates& g = cs.gates[sg];
     if (!wait(cs, &cs.full[sg], ph2)) ok = false;
+    __syncwarp();
     if (nt < kC) {
       // rows of K past the sequence's end (the next one's) become zero
       for (int i = nt * 128 + 16 * p; i < static_cast<int>(kBox); i += 16 * kPrepThreads) {
@@ -593,50 +654,51 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
         *reinterpret_cast<uint4*>(st + 2 * kBox + i) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
-      arrive(&cs.fix);
+      warp_arrive(&cs.fix);
     }
     if (prep_failed(ok)) break;
-    if (p == 0) {
+    if (first) {
       tc_fence_after_sync();
       constexpr uint32_t id = idesc_bf16_f32(128, kC);
-      const uint32_t s0 = smem_addr(st);
+      const uint64_t s0 = smem_desc_sw128(smem_addr(st), 1024);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint32_t at = s0 + (k >> 2) * 2 * kBox + (k & 3) * 32;
-        mma_bf16(cs.tmem + kColG, smem_desc_sw128(at, 1024), smem_desc_sw128(at, 1024), id, k > 0);
+        const uint64_t at = s0 + (((k >> 2) * 2 * kBox + (k & 3) * 32) >> 4);
+        mma_ss(lead, cs.tmem + kColG, at, at, id, k > 0);
       }
-      mma_commit(&cs.gram_done);
+      commit(lead, &cs.gram_done);
     }
-    if (!wait(cs, &cs.gram_done, c)) ok = false;
+    if (!wait(cs, &cs.gates_ready[sg], ph2) || !wait(cs, &cs.gram_done, c)) ok = false;
     __syncwarp();
     tc_fence_after_sync();
-    {
+    if (hh == 0 || (n & 32) != 0) {  // whole warps; the upper right quarter stays
       // lanes 0-63: rows of A (f32), lanes 64-127: rows of M (hi and lo), from
-      // the diagonal leftwards; f is b_n (for A) times the decays passed
-      const bool isM = p >= 64;
-      float f = isM ? 1.f : g.b[n];
+      // the diagonal (or column 31) leftwards; f is b_n (for A) times the
+      // decays passed
+      const bool isM = row >= 64;
+      float f = (isM ? 1.f : g.b[n]) * (hh == 0 ? g.mid[n] : 1.f);
+      const int last = (isM ? n : n - 1) - 32 * hh, dl = n - 32 * hh;
 #pragma unroll
       for (int b = 1; b >= 0; --b) {
-        if (b == 1 && n < 32) continue;  // a whole warp: the upper right quarter
-        uint32_t x0[16], x1[16];
-        tmem_ld32(tm + kColG + 32 * b, x0, x1);
+        uint32_t x[16];
+        tmem_ld16_async(tm + kColG + 32 * hh + 16 * b, x);
+        tmem_wait16(x);
 #pragma unroll
-        for (int j = 3; j >= 0; --j) {
-          const float4 u = *reinterpret_cast<const float4*>(g.a + 32 * b + 8 * j);
-          const float4 v = *reinterpret_cast<const float4*>(g.a + 32 * b + 8 * j + 4);
+        for (int j = 1; j >= 0; --j) {
+          const int i0 = 16 * b + 8 * j;
+          const float4 u = *reinterpret_cast<const float4*>(g.a + 32 * hh + i0);
+          const float4 v = *reinterpret_cast<const float4*>(g.a + 32 * hh + i0 + 4);
           const float as[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
           float y[8];
 #pragma unroll
           for (int k = 7; k >= 0; --k) {
-            const int i = 32 * b + 8 * j + k;
-            const float x = __uint_as_float(8 * j + k < 16 ? x0[(8 * j + k) & 15] : x1[(8 * j + k) & 15]);
-            y[k] = (isM ? i <= n : i < n) ? f * x : 0.f;
-            if (i <= n) f *= as[k];
+            y[k] = i0 + k <= last ? f * __uint_as_float(x[8 * j + k]) : 0.f;
+            if (i0 + k <= dl) f *= as[k];
           }
           if (isM) {
-            put_piece(mb, mb + kBox, n, 4 * b + j, y);
+            put_piece(mb, mb + kBox, n, 4 * hh + 2 * b + j, y);
           } else {
-            float4* r = reinterpret_cast<float4*>(A + n * kPitchA + 32 * b + 8 * j);
+            float4* r = reinterpret_cast<float4*>(A + n * kPitchA + 32 * hh + i0);
             r[0] = make_float4(y[0], y[1], y[2], y[3]);
             r[1] = make_float4(y[4], y[5], y[6], y[7]);
           }
@@ -646,30 +708,31 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
     tc_fence_before_sync();
     if (prep_failed(ok)) break;
     invert(A, g.dec, tb, p);
+    warp_arrive(&cs.gates_free[sg]);
     fence_proxy_async_smem();
     prep_sync();
-    if (p == 0) {
+    if (first) {
       tc_fence_after_sync();
       // kt^T[dk][i] = sum_n K[n][dk] (g_C/g_n) T[n][i]; M T (rows 64.. of its
       // left operand only fill lanes that nothing reads)
       constexpr uint32_t idk = idesc_bf16_f32(128, kC) | kAmajorMN | kBmajorMN;
       constexpr uint32_t idm = idesc_bf16_f32(128, kC) | kBmajorMN;
-      const uint32_t k0 = smem_addr(st), t0 = smem_addr(tb), m0 = smem_addr(mb);
+      const uint64_t k0 = smem_desc_sw128_mn(smem_addr(st), 2 * kBox);
+      const uint64_t t0 = smem_desc_sw128_mn(smem_addr(tb), kBox);
+      const uint64_t m0 = smem_desc_sw128(smem_addr(mb), 1024);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint64_t kd = smem_desc_sw128_mn(k0 + k * 2048, 2 * kBox);
-        mma_bf16(cs.tmem + kColK, kd, smem_desc_sw128_mn(t0 + 2 * kBox + k * 2048, kBox), idk, k > 0);
-        mma_bf16(cs.tmem + kColK, kd, smem_desc_sw128_mn(t0 + 3 * kBox + k * 2048, kBox), idk, 1u);
+        mma_ss(lead, cs.tmem + kColK, k0 + k * 128, t0 + ((2 * kBox) >> 4) + k * 128, idk, k > 0);
+        mma_ss(lead, cs.tmem + kColK, k0 + k * 128, t0 + ((3 * kBox) >> 4) + k * 128, idk, 1u);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint64_t th = smem_desc_sw128_mn(t0 + k * 2048, kBox), tl = smem_desc_sw128_mn(t0 + kBox + k * 2048, kBox);
-        const uint64_t mh = smem_desc_sw128(m0 + 32 * k, 1024), ml = smem_desc_sw128(m0 + kBox + 32 * k, 1024);
-        mma_bf16(cs.tmem + kColG, mh, th, idm, k > 0);
-        mma_bf16(cs.tmem + kColG, mh, tl, idm, 1u);
-        mma_bf16(cs.tmem + kColG, ml, th, idm, 1u);
+        const uint64_t th = t0 + k * 128, tl = th + (kBox >> 4), mh = m0 + 2 * k, ml = mh + (kBox >> 4);
+        mma_ss(lead, cs.tmem + kColG, mh, th, idm, k > 0);
+        mma_ss(lead, cs.tmem + kColG, mh, tl, idm, 1u);
+        mma_ss(lead, cs.tmem + kColG, ml, th, idm, 1u);
       }
-      mma_commit(&cs.prep_done);
+      commit(lead, &cs.prep_done);
     }
     if (!wait(cs, &cs.prep_done, c)) ok = false;
     // the last chunk's kt and M T have been read
@@ -678,108 +741,117 @@ __device__ __forceinline__ void run_prep(const treewy_seqs& a, ChunkSmem& cs, un
     tc_fence_after_sync();
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      uint32_t x0[16], x1[16];
-      tmem_ld32(tm + kColK + 32 * b, x0, x1);
+      uint32_t x[16];
+      tmem_ld16_async(tm + kColK + 32 * hh + 16 * b, x);
+      tmem_wait16(x);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         float y[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(8 * j + k < 16 ? x0[(8 * j + k) & 15] : x1[(8 * j + k) & 15]);
-        put_piece(ktb, ktb + 2 * kBox, p, 4 * b + j, y);
+        for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(x[8 * j + k]);
+        put_piece(ktb, ktb + 2 * kBox, row, 4 * hh + 2 * b + j, y);
       }
     }
-    if (p < 64) {
+    if (row < 64) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        uint32_t x0[16], x1[16];
-        tmem_ld32(tm + kColG + 32 * b, x0, x1);
+        uint32_t x[16];
+        tmem_ld16_async(tm + kColG + 32 * hh + 16 * b, x);
+        tmem_wait16(x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
           float y[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(8 * j + k < 16 ? x0[(8 * j + k) & 15] : x1[(8 * j + k) & 15]);
-          put_piece(mtb, mtb + kBox, p, 4 * b + j, y);
+          for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(x[8 * j + k]);
+          put_piece(mtb, mtb + kBox, row, 4 * hh + 2 * b + j, y);
         }
       }
     }
     tc_fence_before_sync();
     fence_proxy_async_smem();
-    arrive(&cs.kt_ready);
-    arrive(&cs.stage_free[sg]);
+    warp_arrive(&cs.kt_ready);
+    warp_arrive(&cs.stage_free[sg]);
   }
 }
 
-// The products that this thread has issued are done (or the limit is over)
+// The products that this warp has issued are done (or the limit is over)
 // before the CTA frees its TMEM, also after a wait that gave up.
 __device__ __forceinline__ void drain(uint64_t* bar) {
-  mma_commit(bar);
+  __syncwarp();
+  commit((threadIdx.x & 31) == 0, bar);
   mbar_wait(bar, 0);
+  __syncwarp();
 }
 
-// One thread: the chain's products.
+// One warp: the chain's products.
 __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int len, int nchunk) {
   constexpr uint32_t id = idesc_bf16_f32(128, kC);
+  const uint32_t lead = (threadIdx.x & 31) == 0;
   const uint32_t tm = cs.tmem;
-  const uint32_t kt = smem_addr(base + kOffKt), mt = smem_addr(base + kOffMT);
+  const uint64_t kt = smem_desc_sw128(smem_addr(base + kOffKt), 1024);
+  const uint64_t mt = smem_desc_sw128(smem_addr(base + kOffMT), 1024);
+  auto held = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = wait(cs, bar, parity);
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
   for (int c = 0; c < nchunk; ++c) {
     const int sg = c & 1;
-    const uint32_t s0 = smem_addr(base + sg * kStageBytes);
-    if (!wait(cs, &cs.full[sg], c >> 1)) return;
-    if (len - c * kC < kC && !wait(cs, &cs.fix, 0)) return;
+    const uint64_t s0 = smem_desc_sw128(smem_addr(base + sg * kStageBytes), 1024);
+    if (!held(&cs.full[sg], c >> 1)) return;
+    if (len - c * kC < kC && !held(&cs.fix, 0)) return;
     // W's columns have been read by the last chunk's products
-    if (c > 0 && !wait(cs, &cs.o2_done, c - 1)) return;
+    if (c > 0 && !held(&cs.o2_done, c - 1)) return;
     // S k, half of the columns of S at a time
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (!wait(cs, &cs.s_ready[half], c)) return;
+      if (!held(&cs.s_ready[half], c)) return;
       tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        const uint64_t kd = smem_desc_sw128(s0 + half * 2 * kBox + 32 * k, 1024);
-        mma_bf16_ts(tm + kColW, tm + kColS + 32 * half + 8 * k, kd, id, half > 0 || k > 0);
-        mma_bf16_ts(tm + kColW, tm + kColS + 64 + 32 * half + 8 * k, kd, id, 1u);
+        const uint64_t kd = s0 + ((half * 2 * kBox + 32 * k) >> 4);
+        mma_ts(lead, tm + kColW, tm + kColS + 32 * half + 8 * k, kd, id, half > 0 || k > 0);
+        mma_ts(lead, tm + kColW, tm + kColS + 64 + 32 * half + 8 * k, kd, id, 1u);
       }
     }
-    mma_commit(&cs.d1_done);
+    commit(lead, &cs.d1_done);
     // S q
-    if (c > 0 && !wait(cs, &cs.o_read[sg ^ 1], (c - 1) >> 1)) return;
+    if (c > 0 && !held(&cs.o_read, c - 1)) return;
     tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < 8; ++k) {
-      const uint64_t qd = smem_desc_sw128(s0 + (k >> 2) * 2 * kBox + kBox + 32 * (k & 3), 1024);
-      mma_bf16_ts(tm + kColO, tm + kColS + 8 * k, qd, id, k > 0);
-      mma_bf16_ts(tm + kColO, tm + kColS + 64 + 8 * k, qd, id, 1u);
+      const uint64_t qd = s0 + (((k >> 2) * 2 * kBox + kBox + 32 * (k & 3)) >> 4);
+      mma_ts(lead, tm + kColO, tm + kColS + 8 * k, qd, id, k > 0);
+      mma_ts(lead, tm + kColO, tm + kColS + 64 + 8 * k, qd, id, 1u);
     }
-    mma_commit(&cs.qs_done);
-    mma_commit(&cs.stage_free[sg]);
+    commit(lead, &cs.qs_done);
+    commit(lead, &cs.stage_free[sg]);
     // W kt, half of its columns at a time
-    if (!wait(cs, &cs.kt_ready, c) || !wait(cs, &cs.rhs_ready, c)) return;
+    if (!held(&cs.kt_ready, c) || !held(&cs.rhs_ready, c)) return;
     tc_fence_after_sync();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        const uint32_t wh = tm + kColW + 32 * (k >> 1) + 8 * (k & 1);
-        const uint64_t kh = smem_desc_sw128(kt + half * kBox + 32 * k, 1024);
-        const uint64_t kl = smem_desc_sw128(kt + 2 * kBox + half * kBox + 32 * k, 1024);
-        mma_bf16_ts(tm + kColD + 64 * half, wh, kh, id, k > 0);
-        mma_bf16_ts(tm + kColD + 64 * half, wh, kl, id, 1u);
-        mma_bf16_ts(tm + kColD + 64 * half, wh + 16, kh, id, 1u);
+        const uint32_t wh = tm + kColW + 16 * k;
+        const uint64_t kh = kt + ((half * kBox + 32 * k) >> 4), kl = kh + ((2 * kBox) >> 4);
+        mma_ts(lead, tm + kColD + 64 * half, wh, kh, id, k > 0);
+        mma_ts(lead, tm + kColD + 64 * half, wh, kl, id, 1u);
+        mma_ts(lead, tm + kColD + 64 * half, wh + 8, kh, id, 1u);
       }
-      mma_commit(&cs.d2_done[half]);
+      commit(lead, &cs.d2_done[half]);
     }
     // (M T) W over the columns of S q
-    if (!wait(cs, &cs.qs_read, c)) return;
+    if (!held(&cs.qs_read, c)) return;
     tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < 4; ++k) {
-      const uint32_t wh = tm + kColW + 32 * (k >> 1) + 8 * (k & 1);
-      const uint64_t mh = smem_desc_sw128(mt + 32 * k, 1024), ml = smem_desc_sw128(mt + kBox + 32 * k, 1024);
-      mma_bf16_ts(tm + kColO, wh, mh, id, k > 0);
-      mma_bf16_ts(tm + kColO, wh, ml, id, 1u);
-      mma_bf16_ts(tm + kColO, wh + 16, mh, id, 1u);
+      const uint32_t wh = tm + kColW + 16 * k;
+      const uint64_t mh = mt + 2 * k, ml = mh + (kBox >> 4);
+      mma_ts(lead, tm + kColO, wh, mh, id, k > 0);
+      mma_ts(lead, tm + kColO, wh, ml, id, 1u);
+      mma_ts(lead, tm + kColO, wh + 8, mh, id, 1u);
     }
-    mma_commit(&cs.o2_done);
+    commit(lead, &cs.o2_done);
   }
 }
 
@@ -836,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (q.len == 0) {
-    if (q.fresh && t < kStateThreads && (t & 127) < a.dv) {
+    if (q.fresh && warp < kStateWarps && (t & 127) < a.dv) {
       float S[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) S[i] = 0.f;
@@ -851,24 +923,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cs.full[i], 1);
       mbar_init(&cs.full_v[i], 1);
-      mbar_init(&cs.stage_free[i], 1 + kPrepThreads);
-      mbar_init(&cs.v_free[i], kStateThreads);
-      mbar_init(&cs.gates_ready[i], 32);
-      mbar_init(&cs.o_read[i], kStateThreads);
-      mbar_init(&cs.s_ready[i], kStateThreads / 2);
+      mbar_init(&cs.stage_free[i], 1 + kPrepWarps);
+      mbar_init(&cs.v_free[i], kOutWarps);
+      mbar_init(&cs.gates_ready[i], 1);
+      mbar_init(&cs.gates_free[i], kStateWarps + kPrepWarps + kOutWarps);
+      mbar_init(&cs.s_ready[i], kStateWarps / 2);
       mbar_init(&cs.d2_done[i], 1);
       mbar_init(&cs.drain[i], 1);
     }
-    mbar_init(&cs.fix, kPrepThreads);
+    mbar_init(&cs.fix, kPrepWarps);
     mbar_init(&cs.gram_done, 1);
     mbar_init(&cs.prep_done, 1);
-    mbar_init(&cs.kt_ready, kPrepThreads);
+    mbar_init(&cs.kt_ready, kPrepWarps);
     mbar_init(&cs.d1_done, 1);
     mbar_init(&cs.qs_done, 1);
-    mbar_init(&cs.rhs_ready, kStateThreads);
-    mbar_init(&cs.qs_read, kStateThreads);
+    mbar_init(&cs.rhs_ready, kStateWarps);
+    mbar_init(&cs.qs_read, kOutWarps);
     mbar_init(&cs.o2_done, 1);
-    mbar_init(&cs.o_tile, kStateThreads);
+    mbar_init(&cs.o_read, kOutWarps);
+    mbar_init(&cs.o_tile, kOutWarps);
     cs.fail = 0;
     fence_mbarrier_init();
   }
@@ -880,18 +953,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
 
-  if (warp < kStateThreads / 32) {
-    run_state<SB, OF32>(a, cs, base, q, h, nchunk);
+  if (warp < kPrepWarp) {
+    set_regs_up<kStateRegs>();
+    run_state<SB>(a, cs, base, q, h, nchunk);
+  } else if (warp < kOutWarp) {
+    set_regs_down<kPrepRegs>();
+    run_prep(cs, base, q.len, nchunk);
+    if (warp == kPrepWarp) drain(&cs.drain[1]);
   } else if (warp < kMmaWarp) {
-    run_prep(a, cs, base, q, h, nchunk);
-    if (t == kStateThreads) drain(&cs.drain[1]);
-  } else if (warp == kMmaWarp) {
-    if ((t & 31) == 0) {
+    set_regs_up<kOutRegs>();
+    run_out<OF32>(a, cs, base, q, h, nchunk);
+  } else {
+    set_regs_down<kMiscRegs>();
+    if (warp == kMmaWarp) {
       run_mma(cs, base, q.len, nchunk);
       drain(&cs.drain[0]);
+    } else if (warp == kLoadWarp) {
+      if ((t & 31) == 0) run_load(&map_q, &map_k, &map_v, cs, base, q, h / (a.H / a.Hk), h, nchunk);
+    } else if (warp == kGateWarp) {
+      run_gates(a, cs, q, h, nchunk);
     }
-  } else if ((t & 31) == 0) {
-    run_load(&map_q, &map_k, &map_v, cs, base, q, h / (a.H / a.Hk), h, nchunk);
   }
   __syncwarp();
   tc_fence_before_sync();
