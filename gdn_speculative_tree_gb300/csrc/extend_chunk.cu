@@ -50,10 +50,12 @@ constexpr int kPrepWarp = kStateWarps, kOutWarp = kPrepWarp + kPrepWarps, kMmaWa
               kLoadWarp = kMmaWarp + 1, kGateWarp = kLoadWarp + 1;
 constexpr int kPrepThreads = 32 * kPrepWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 4);
-// Registers per thread: 80 at launch; the state warps take what the others
-// give back (2 x 112 + 2 x 64 + 96 + 32 = 6 x 80 per 128 threads).
-constexpr int kStateRegs = 112, kPrepRegs = 64, kOutRegs = 96, kMiscRegs = 32;
-static_assert(2 * kStateRegs + 2 * kPrepRegs + kOutRegs + kMiscRegs == 6 * 80, "the launch's registers");
+// Registers per thread: kLaunchRegs at launch (six warps share the 512 x 32 of
+// a quarter of the SM); the state and output warps take what the others give
+// back.  An increase waits for registers of the launch, so the shares must not
+// add up to more than it has: launch() holds the compiled kernel to it.
+constexpr int kLaunchRegs = 80, kStateRegs = 112, kPrepRegs = 64, kOutRegs = 96, kMiscRegs = 32;
+static_assert(2 * kStateRegs + 2 * kPrepRegs + kOutRegs + kMiscRegs <= 6 * kLaunchRegs, "the launch's registers");
 
 // TMEM columns
 constexpr uint32_t kColS = 0;                // S: hi in 64 columns, lo in 64 (bf16 pairs)
@@ -119,32 +121,25 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Products are issued by whole warps, converged, with all but one lane
-// predicated off: descriptors then stay in uniform registers.
-// D(tmem) (+)= A(smem desc or tmem, bf16 pairs) * B(smem desc)^T
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// One lane of a converged warp.  Products are issued by the lane that this
+// elects: the compiler knows that branch to be taken by one lane and keeps the
+// descriptors in uniform registers (a 128 x 64 x 16 product every 37 cycles,
+// against 56 from a branch on the lane number and 76 under a predicate).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// D(tmem) (+)= A(tmem, bf16 pairs) * B(smem desc)^T
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
-  if (lead) mma_commit(bar);
-  __syncwarp();
 }
 
 template <int N>
@@ -631,7 +626,6 @@ __device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, c
 __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int len, int nchunk) {
   const int p = threadIdx.x - 32 * kPrepWarp, row = p & 127, n = p & 63, hh = p >> 7;
   const bool first = p < 32;
-  const uint32_t lead = p == 0;
   const uint32_t tm = cs.tmem + (static_cast<uint32_t>(p & 96) << 16);
   float* A = reinterpret_cast<float*>(base + kOffA);
   unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
@@ -657,17 +651,18 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
       warp_arrive(&cs.fix);
     }
     if (prep_failed(ok)) break;
-    if (first) {
+    if (first && elect_one()) {
       tc_fence_after_sync();
       constexpr uint32_t id = idesc_bf16_f32(128, kC);
       const uint64_t s0 = smem_desc_sw128(smem_addr(st), 1024);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint64_t at = s0 + (((k >> 2) * 2 * kBox + (k & 3) * 32) >> 4);
-        mma_ss(lead, cs.tmem + kColG, at, at, id, k > 0);
+        mma_bf16(cs.tmem + kColG, at, at, id, k > 0);
       }
-      commit(lead, &cs.gram_done);
+      mma_commit(&cs.gram_done);
     }
+    __syncwarp();
     if (!wait(cs, &cs.gates_ready[sg], ph2) || !wait(cs, &cs.gram_done, c)) ok = false;
     __syncwarp();
     tc_fence_after_sync();
@@ -711,7 +706,7 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
     warp_arrive(&cs.gates_free[sg]);
     fence_proxy_async_smem();
     prep_sync();
-    if (first) {
+    if (first && elect_one()) {
       tc_fence_after_sync();
       // kt^T[dk][i] = sum_n K[n][dk] (g_C/g_n) T[n][i]; M T (rows 64.. of its
       // left operand only fill lanes that nothing reads)
@@ -722,18 +717,19 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
       const uint64_t m0 = smem_desc_sw128(smem_addr(mb), 1024);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        mma_ss(lead, cs.tmem + kColK, k0 + k * 128, t0 + ((2 * kBox) >> 4) + k * 128, idk, k > 0);
-        mma_ss(lead, cs.tmem + kColK, k0 + k * 128, t0 + ((3 * kBox) >> 4) + k * 128, idk, 1u);
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + ((2 * kBox) >> 4) + k * 128, idk, k > 0);
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + ((3 * kBox) >> 4) + k * 128, idk, 1u);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint64_t th = t0 + k * 128, tl = th + (kBox >> 4), mh = m0 + 2 * k, ml = mh + (kBox >> 4);
-        mma_ss(lead, cs.tmem + kColG, mh, th, idm, k > 0);
-        mma_ss(lead, cs.tmem + kColG, mh, tl, idm, 1u);
-        mma_ss(lead, cs.tmem + kColG, ml, th, idm, 1u);
+        mma_bf16(cs.tmem + kColG, mh, th, idm, k > 0);
+        mma_bf16(cs.tmem + kColG, mh, tl, idm, 1u);
+        mma_bf16(cs.tmem + kColG, ml, th, idm, 1u);
       }
-      commit(lead, &cs.prep_done);
+      mma_commit(&cs.prep_done);
     }
+    __syncwarp();
     if (!wait(cs, &cs.prep_done, c)) ok = false;
     // the last chunk's kt and M T have been read
     if (c > 0 && !wait(cs, &cs.o2_done, c - 1)) ok = false;
@@ -778,7 +774,7 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
 // before the CTA frees its TMEM, also after a wait that gave up.
 __device__ __forceinline__ void drain(uint64_t* bar) {
   __syncwarp();
-  commit((threadIdx.x & 31) == 0, bar);
+  if (elect_one()) mma_commit(bar);
   mbar_wait(bar, 0);
   __syncwarp();
 }
@@ -786,7 +782,6 @@ __device__ __forceinline__ void drain(uint64_t* bar) {
 // One warp: the chain's products.
 __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int len, int nchunk) {
   constexpr uint32_t id = idesc_bf16_f32(128, kC);
-  const uint32_t lead = (threadIdx.x & 31) == 0;
   const uint32_t tm = cs.tmem;
   const uint64_t kt = smem_desc_sw128(smem_addr(base + kOffKt), 1024);
   const uint64_t mt = smem_desc_sw128(smem_addr(base + kOffMT), 1024);
@@ -805,28 +800,35 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if (!held(&cs.s_ready[half], c)) return;
+      if (elect_one()) {
       tc_fence_after_sync();
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const uint64_t kd = s0 + ((half * 2 * kBox + 32 * k) >> 4);
-        mma_ts(lead, tm + kColW, tm + kColS + 32 * half + 8 * k, kd, id, half > 0 || k > 0);
-        mma_ts(lead, tm + kColW, tm + kColS + 64 + 32 * half + 8 * k, kd, id, 1u);
+        mma_ts(tm + kColW, tm + kColS + 32 * half + 8 * k, kd, id, half > 0 || k > 0);
+        mma_ts(tm + kColW, tm + kColS + 64 + 32 * half + 8 * k, kd, id, 1u);
       }
+      if (half == 1) mma_commit(&cs.d1_done);
+      }
+      __syncwarp();
     }
-    commit(lead, &cs.d1_done);
     // S q
     if (c > 0 && !held(&cs.o_read, c - 1)) return;
+    if (elect_one()) {
     tc_fence_after_sync();
 #pragma unroll 1
     for (int k = 0; k < 8; ++k) {
       const uint64_t qd = s0 + (((k >> 2) * 2 * kBox + kBox + 32 * (k & 3)) >> 4);
-      mma_ts(lead, tm + kColO, tm + kColS + 8 * k, qd, id, k > 0);
-      mma_ts(lead, tm + kColO, tm + kColS + 64 + 8 * k, qd, id, 1u);
+      mma_ts(tm + kColO, tm + kColS + 8 * k, qd, id, k > 0);
+      mma_ts(tm + kColO, tm + kColS + 64 + 8 * k, qd, id, 1u);
     }
-    commit(lead, &cs.qs_done);
-    commit(lead, &cs.stage_free[sg]);
+    mma_commit(&cs.qs_done);
+    mma_commit(&cs.stage_free[sg]);
+    }
+    __syncwarp();
     // W kt, half of its columns at a time
     if (!held(&cs.kt_ready, c) || !held(&cs.rhs_ready, c)) return;
+    if (elect_one()) {
     tc_fence_after_sync();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -834,24 +836,29 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
       for (int k = 0; k < 4; ++k) {
         const uint32_t wh = tm + kColW + 16 * k;
         const uint64_t kh = kt + ((half * kBox + 32 * k) >> 4), kl = kh + ((2 * kBox) >> 4);
-        mma_ts(lead, tm + kColD + 64 * half, wh, kh, id, k > 0);
-        mma_ts(lead, tm + kColD + 64 * half, wh, kl, id, 1u);
-        mma_ts(lead, tm + kColD + 64 * half, wh + 8, kh, id, 1u);
+        mma_ts(tm + kColD + 64 * half, wh, kh, id, k > 0);
+        mma_ts(tm + kColD + 64 * half, wh, kl, id, 1u);
+        mma_ts(tm + kColD + 64 * half, wh + 8, kh, id, 1u);
       }
-      commit(lead, &cs.d2_done[half]);
+      mma_commit(&cs.d2_done[half]);
     }
+    }
+    __syncwarp();
     // (M T) W over the columns of S q
     if (!held(&cs.qs_read, c)) return;
+    if (elect_one()) {
     tc_fence_after_sync();
 #pragma unroll 1
     for (int k = 0; k < 4; ++k) {
       const uint32_t wh = tm + kColW + 16 * k;
       const uint64_t mh = mt + 2 * k, ml = mh + (kBox >> 4);
-      mma_ts(lead, tm + kColO, wh, mh, id, k > 0);
-      mma_ts(lead, tm + kColO, wh, ml, id, 1u);
-      mma_ts(lead, tm + kColO, wh + 8, mh, id, 1u);
+      mma_ts(tm + kColO, wh, mh, id, k > 0);
+      mma_ts(tm + kColO, wh, ml, id, 1u);
+      mma_ts(tm + kColO, wh + 8, mh, id, 1u);
     }
-    commit(lead, &cs.o2_done);
+    mma_commit(&cs.o2_done);
+    }
+    __syncwarp();
   }
 }
 
@@ -986,6 +993,10 @@ template <bool SB, bool OF32>
 cudaError_t launch(const treewy_seqs& a, const ExtendMaps& m, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_done{0};
   const cudaError_t attr = once_per_device(attr_done, [] {
+    cudaFuncAttributes f;
+    const cudaError_t e = cudaFuncGetAttributes(&f, extend_chunk_kernel<SB, OF32>);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(extend_chunk_kernel<SB, OF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kSmemBytes));
   });
