@@ -150,10 +150,25 @@ def _check(code: int) -> None:
         raise TreewyError(code, treewy_last_error())
 
 
+_current_raw_stream = None
+
+
+def _current_stream_handle() -> int:
+    """The current stream's handle, by the call that makes no Stream object
+    where this PyTorch has it (a small call's time is mostly the host's)."""
+    global _current_raw_stream
+    if _current_raw_stream is None:
+        import torch
+        torch.cuda.current_stream()  # initialises CUDA
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        _current_raw_stream = ((lambda: raw(device())) if raw is not None and device is not None
+                               else (lambda: torch.cuda.current_stream().cuda_stream))
+    return _current_raw_stream()
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream_handle()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -27,7 +27,7 @@ namespace treewy {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kDecodeWarps = 1, kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kStage = 16;  // tokens staged at a time
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -111,7 +111,8 @@ __device__ __forceinline__ void load_row(const void* base, bool bf16, int64_t at
   }
 }
 
-// The same columns back to the pool; a bf16 pool rounds to nearest even.
+// The same columns back to the pool, which the next layers' pools push out of
+// L2 before it is read again; a bf16 pool rounds to nearest even.
 template <int V, bool WIDE>
 __device__ __forceinline__ void store_row(void* base, bool bf16, int64_t at, int n, int l,
                                           const float (&x)[16]) {
@@ -128,14 +129,14 @@ __device__ __forceinline__ void store_row(void* base, bool bf16, int64_t at, int
             w[e] = *reinterpret_cast<const uint32_t*>(&p);
           }
           uint16_t* p = reinterpret_cast<uint16_t*>(base) + at + c0;
-          if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-          else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+          if constexpr (V == 8) __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+          else __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
         } else {
           float* p = reinterpret_cast<float*>(base) + at + c0;
 #pragma unroll
           for (int e = 0; e < V; e += 4)
-            *reinterpret_cast<float4*>(p + e) = make_float4(x[V * i + e], x[V * i + e + 1],
-                                                            x[V * i + e + 2], x[V * i + e + 3]);
+            __stcs(reinterpret_cast<float4*>(p + e), make_float4(x[V * i + e], x[V * i + e + 1],
+                                                                 x[V * i + e + 2], x[V * i + e + 3]));
         }
       }
     } else {
@@ -162,20 +163,46 @@ __device__ __forceinline__ void store_o(const treewy_seqs& a, int64_t at, float 
   else reinterpret_cast<float*>(a.o)[at] = x;
 }
 
-// Row of register row j of this lane's group: a warp's four groups hold
-// neighbouring rows.
+// Row of register row j of this lane's group, `first` the CTA's first row: a
+// warp's four groups hold neighbouring rows.
 template <int RPT>
-__device__ __forceinline__ int group_row(int j) {
+__device__ __forceinline__ int group_row(int first, int j) {
   const int warp = threadIdx.x >> 5, grp = (threadIdx.x & 31) >> 3;
-  return static_cast<int>(blockIdx.y) * (32 * RPT) + 4 * (warp * RPT + j) + grp;
+  return first + 4 * (warp * RPT + j) + grp;
 }
 
-// One (sequence, head) and 32 RPT of its rows per CTA, one token at most.
-template <int RPT, int V, bool WIDE>
-__global__ void __launch_bounds__(kThreads) decode_kernel(const treewy_seqs a) {
+// The 16 columns of a row as they are stored: pieces of 16 bytes.
+template <bool SB>
+struct RawRow {
+  uint4 w[SB ? 2 : 4];
+};
+template <bool SB>
+__device__ __forceinline__ void unpack_row(const RawRow<SB>& r, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < (SB ? 2 : 4); ++i) {
+    const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (SB) {
+        x[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+        x[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      } else {
+        x[4 * i + e] = __uint_as_float(w[e]);
+      }
+    }
+  }
+}
+
+// One (sequence, head) and 4 kDecodeWarps RPT of its rows per CTA, one token
+// at most.  WIDE: every load of the state, q and k is a whole piece; the rows
+// then wait in registers as they are stored, all of them in flight at once,
+// and are taken one after the other.
+template <int RPT, bool SB, bool WIDE>
+__global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seqs a) {
+  constexpr int V = SB ? 8 : 4;
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int l = threadIdx.x & 7;
-  const bool sb = (a.flags & TREEWY_FLAG_STATE_BF16) != 0;
+  const int first = static_cast<int>(blockIdx.y) * (4 * kDecodeWarps * RPT);
   const bool qb = a.qkv_dtype == TREEWY_DTYPE_BF16;
   const Seq s = load_seq(a, r);
   if (s.flags) {
@@ -184,54 +211,64 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const treewy_seqs a) {
   }
   if (s.len == 0 && !s.fresh) return;
   const int64_t block = (static_cast<int64_t>(s.slot) * a.H + h) * a.dv;
-  float S[RPT][16];
+  RawRow<SB> raw[RPT];
+  if constexpr (WIDE) {
+    const unsigned char* p = reinterpret_cast<const unsigned char*>(a.state);
 #pragma unroll
-  for (int j = 0; j < RPT; ++j) {
-    const int row = group_row<RPT>(j);
-    if (!s.fresh && row < a.dv) {
-      load_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
-    } else {
+    for (int j = 0; j < RPT; ++j) {
+      const int row = group_row<RPT>(first, j);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) S[j][c] = 0.f;
+      for (int i = 0; i < 16 / V; ++i) {
+        raw[j].w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (!s.fresh && row < a.dv && piece_col<V>(l, i) < a.dk)
+          raw[j].w[i] = __ldcs(reinterpret_cast<const uint4*>(p + ((block + row) * a.dk + piece_col<V>(l, i)) * (SB ? 2 : 4)));
+      }
     }
   }
+  const int64_t t = s.tok0;
+  float k[16], q[16], v[RPT], alpha = 1.f, beta = 0.f, kq = 0.f;
   if (s.len > 0) {
-    const int64_t t = s.tok0;
     const int hk = h / (a.H / a.Hk);
-    float k[16], q[16], v[RPT];
     load_row<V, WIDE>(a.k, qb, t * a.k_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, k);
     load_row<V, WIDE>(a.q, qb, t * a.q_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, q);
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
-      const int row = group_row<RPT>(j);
+      const int row = group_row<RPT>(first, j);
       v[j] = row < a.dv ? load_qkv(a.v, t * a.v_stride + static_cast<int64_t>(h) * a.dv + row, qb) : 0.f;
     }
-    const float alpha = __ldg(a.alpha + t * a.H + h), beta = __ldg(a.beta + t * a.H + h);
-    float kq = 0.f;
+    alpha = __ldg(a.alpha + t * a.H + h);
+    beta = __ldg(a.beta + t * a.H + h);
 #pragma unroll
     for (int c = 0; c < 16; ++c) kq = fmaf(k[c], q[c], kq);
     kq = sum8(kq);
+  }
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) {
+  for (int j = 0; j < RPT; ++j) {
+    const int row = group_row<RPT>(first, j);
+    float S[16];
+    if constexpr (WIDE) {
+      unpack_row<SB>(raw[j], S);
+    } else if (!s.fresh && row < a.dv) {
+      load_row<V, false>(a.state, SB, (block + row) * a.dk, a.dk, l, S);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) S[c] = 0.f;
+    }
+    if (s.len > 0) {
       float sk = 0.f, sq = 0.f;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        sk = fmaf(S[j][c], k[c], sk);
-        sq = fmaf(S[j][c], q[c], sq);
+        sk = fmaf(S[c], k[c], sk);
+        sq = fmaf(S[c], q[c], sq);
       }
       sk = sum8(sk);
       sq = sum8(sq);
       const float u = beta * (v[j] - alpha * sk);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) S[j][c] = fmaf(u, k[c], alpha * S[j][c]);
-      const int row = group_row<RPT>(j);
+      for (int c = 0; c < 16; ++c) S[c] = fmaf(u, k[c], alpha * S[c]);
       if (l == 0 && row < a.dv) store_o(a, (t * a.H + h) * a.dv + row, fmaf(kq, u, alpha * sq));
     }
-  }
-#pragma unroll
-  for (int j = 0; j < RPT; ++j) {
-    const int row = group_row<RPT>(j);
-    if (row < a.dv) store_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
+    if (row < a.dv) store_row<V, WIDE>(a.state, SB, (block + row) * a.dk, a.dk, l, S);
   }
 }
 
@@ -258,10 +295,11 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
   }
   if (s.len == 0 && !s.fresh) return;
   const int64_t block = (static_cast<int64_t>(s.slot) * a.H + h) * a.dv;
+  const int first = static_cast<int>(blockIdx.y) * (32 * RPT);
   float S[RPT][16];
 #pragma unroll
   for (int j = 0; j < RPT; ++j) {
-    const int row = group_row<RPT>(j);
+    const int row = group_row<RPT>(first, j);
     if (!s.fresh && row < a.dv) {
       load_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
     } else {
@@ -318,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
       kq = sum8(kq);
 #pragma unroll
       for (int j = 0; j < RPT; ++j) {
-        const int row = group_row<RPT>(j);
+        const int row = group_row<RPT>(first, j);
         float sk = 0.f, sq = 0.f;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -337,22 +375,40 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
   }
 #pragma unroll
   for (int j = 0; j < RPT; ++j) {
-    const int row = group_row<RPT>(j);
+    const int row = group_row<RPT>(first, j);
     if (row < a.dv) store_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
   }
 }
 
-template <int RPT, int V, bool WIDE>
-cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
+template <int RPT, bool SB, bool WIDE>
+cudaError_t launch_decode(const treewy_seqs& a, cudaStream_t stream) {
+  constexpr int kRows = 4 * kDecodeWarps * RPT;
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
-                  static_cast<unsigned>((a.dv + 32 * RPT - 1) / (32 * RPT)));
-  if (a.max_len <= 1) decode_kernel<RPT, V, WIDE><<<grid, kThreads, 0, stream>>>(a);
-  else scan_kernel<RPT, V, WIDE><<<grid, kThreads, 0, stream>>>(a);
+                  static_cast<unsigned>((a.dv + kRows - 1) / kRows));
+  decode_kernel<RPT, SB, WIDE><<<grid, kDecodeThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <int RPT>
-cudaError_t launch_rows(const treewy_seqs& a, cudaStream_t stream) {
+template <int RPT, bool SB, bool WIDE>
+cudaError_t launch_scan(const treewy_seqs& a, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
+                  static_cast<unsigned>((a.dv + 32 * RPT - 1) / (32 * RPT)));
+  scan_kernel<RPT, SB ? 8 : 4, WIDE><<<grid, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool SB, bool WIDE>
+cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
+  const int64_t heads = static_cast<int64_t>(a.R) * a.H;
+  if (a.max_len <= 1)  // a quarter of a head per CTA, or less while that leaves SMs idle
+    return 4 * heads >= 304 ? launch_decode<4, SB, WIDE>(a, stream) : launch_decode<1, SB, WIDE>(a, stream);
+  // a whole head per CTA, or a quarter of one while that leaves SMs idle
+  return heads >= 304 ? launch_scan<4, SB, WIDE>(a, stream) : launch_scan<1, SB, WIDE>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_extend_scan(const treewy_seqs& a, cudaStream_t stream) {
   // pieces of 16 bytes of the pool's type; wide loads where every row of the
   // state, and of q and k for the single-token kernel, starts on a piece
   const int e = a.qkv_dtype == TREEWY_DTYPE_BF16 ? 2 : 4;
@@ -363,16 +419,8 @@ cudaError_t launch_rows(const treewy_seqs& a, cudaStream_t stream) {
   const int v = sb ? 8 : 4;
   const int64_t piece = (v * e < 16) ? v * e : 16;
   const bool wide = a.dk % v == 0 && rows_on(a.q, a.q_stride, piece) && rows_on(a.k, a.k_stride, piece);
-  if (sb) return wide ? launch<RPT, 8, true>(a, stream) : launch<RPT, 8, false>(a, stream);
-  return wide ? launch<RPT, 4, true>(a, stream) : launch<RPT, 4, false>(a, stream);
-}
-
-}  // namespace
-
-cudaError_t launch_extend_scan(const treewy_seqs& a, cudaStream_t stream) {
-  // a whole head per CTA, or a quarter of one while that leaves SMs idle
-  const int64_t heads = static_cast<int64_t>(a.R) * a.H;
-  return heads >= 304 ? launch_rows<4>(a, stream) : launch_rows<1>(a, stream);
+  if (sb) return wide ? launch<true, true>(a, stream) : launch<true, false>(a, stream);
+  return wide ? launch<false, true>(a, stream) : launch<false, false>(a, stream);
 }
 
 }  // namespace treewy

@@ -9,7 +9,9 @@
 // rounding at the store.  A head's row is held by d / 8 neighbouring lanes
 // (rounded up to a power of two), so that the sum of squares is a few shuffles
 // and the other element of a rotated pair is one shuffle away or in the same
-// lane.  Rows that this does not fit (odd sizes, unaligned rows, pairs that
+// lane.  A warp takes several heads of one token and side (q or k), so that
+// the weights and the token's cosines and sines are loaded once for all of
+// them.  Rows that this does not fit (odd sizes, unaligned rows, pairs that
 // cross an eight at an odd place) go to one warp each, element by element.
 #include "treewy_device.cuh"
 #include "treewy_internal.h"
@@ -64,118 +66,167 @@ __device__ __forceinline__ const float* table_row(const treewy_qk& a, int64_t t,
   return a.rope + static_cast<int64_t>(p) * a.rope_dims;
 }
 
-__device__ __forceinline__ float inv_norm(const treewy_qk& a, float sum) {
-  return 1.0f / sqrtf((a.norm == TREEWY_NORM_RMS ? sum / static_cast<float>(a.d) : sum) + a.eps);
+// 1 / sqrt: the hardware's reciprocal root, right to two units of f32's last
+// place, against the 2^-9 or 2^-24 of the outputs' rounding.  mean: 1 / d for
+// the RMS norm, 1 for L2.
+__device__ __forceinline__ float inv_norm(float sum, float mean, float eps) {
+  return rsqrtf(fmaf(sum, mean, eps));
 }
 
-// LANES lanes per row, eight elements each; UNROLL rows of a lane in flight.
-template <typename T, int LANES, int UNROLL>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const treewy_qk a) {
-  constexpr bool kBf16 = sizeof(T) == 2;
-  constexpr int kGroups = kThreads / LANES;           // rows per pass of a CTA
-  const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  const int heads = a.Hq + a.Hk;
-  const int64_t rows = a.T * heads;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGroups * UNROLL);
-  const int64_t t_first = first / heads;
-  const int h_first = static_cast<int>(first - t_first * heads);
+// Eight elements of a row as they are stored.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+    const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (sizeof(T) == 2) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      } else {
+        x[4 * i + e] = __uint_as_float(w[e]);
+      }
+    }
+  }
+}
+__device__ __forceinline__ void load8_f32(const float* p, float (&x)[8]) {
+  const float4 f = *reinterpret_cast<const float4*>(p), g = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+  x[4] = g.x; x[5] = g.y; x[6] = g.z; x[7] = g.w;
+}
+
+// LANES lanes per head, eight elements each; a warp takes UNROLL passes of
+// 32 / LANES heads of one token's q or k, all loaded before the first is used.
+template <typename T, int LANES, int UNROLL, int THREADS>
+__global__ void __launch_bounds__(THREADS, 896 / THREADS)
+    qk_norm_kernel(const treewy_qk a, int q_units, int units, float mean) {
+  constexpr int kPass = 32 / LANES;                   // heads per pass
+  const int lane = threadIdx.x % LANES, grp = (threadIdx.x & 31) / LANES;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;                               // a whole warp
+  const float* tab = nullptr;
+  if (a.rope_dims > 0) {
+    tab = table_row(a, t, blockIdx.y == 0 && (threadIdx.x & 31) == 0);
+    if (tab == nullptr) return;                       // a whole warp
+  }
   const int c0 = 8 * lane;
   const bool mine = c0 < a.d;
-
-  float x[UNROLL][8];
-  Row row[UNROLL];
-  bool live[UNROLL];
+  // half is a multiple of 8: a pair's other eight are half / 8 lanes on
+  const int half = a.rope_dims / 2;
+  const bool in_rope = c0 < a.rope_dims, low = c0 < half;
+  const int other = in_rope ? (low ? lane + half / 8 : lane - half / 8) : lane;
+  for (int part = blockIdx.y; part < units; part += gridDim.y) {
+    const bool isq = part < q_units;
+    const int heads = isq ? a.Hq : a.Hk, repeat = isq ? a.q_repeat : a.k_repeat;
+    const int h0 = (isq ? part : part - q_units) * (UNROLL * kPass) + grp;
+    const unsigned char* in =
+        reinterpret_cast<const unsigned char*>(isq ? a.q : a.k) +
+        (t * (isq ? a.q_stride : a.k_stride) + static_cast<int64_t>(h0) * a.d + c0) * static_cast<int64_t>(sizeof(T));
+    const int step = kPass * a.d * static_cast<int>(sizeof(T));
+    Raw8<T> raw[UNROLL];
 #pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
-    const int local = i * kGroups + grp;
-    live[i] = first + local < rows;
-    const int at = h_first + (live[i] ? local : 0);
-    row[i] = row_of(a, t_first + at / heads, at % heads, sizeof(T));
+    for (int i = 0; i < UNROLL; ++i) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-    if (live[i] && mine) {
-      if constexpr (kBf16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(row[i].in + 2 * c0);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[i][2 * e] = __uint_as_float(w[e] << 16);
-          x[i][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(row[i].in + 4 * (c0 + e));
-          x[i][e] = f.x; x[i][e + 1] = f.y; x[i][e + 2] = f.z; x[i][e + 3] = f.w;
-        }
+      for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) {
+        raw[i].w[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (h0 + i * kPass < heads && mine)
+          raw[i].w[k] = *reinterpret_cast<const uint4*>(in + static_cast<int64_t>(i) * step + 16 * k);
       }
     }
-  }
+    // y = f (x wc + x' ws) with x' the pair's other element (ws = 0: no pair)
+    float wc[8], ws[8];
+    const float* weight = isq ? a.q_weight : a.k_weight;
+    const float scale = isq ? a.q_scale : a.k_scale;
 #pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(x[i][e], x[i][e], sum);
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    const float f = row[i].scale * inv_norm(a, sum);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[i][e] *= f;
-    if (row[i].w != nullptr && mine) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] *= __ldg(row[i].w + c0 + e);
-    }
-    if (a.rope_dims > 0) {
-      const float* tab = live[i] ? table_row(a, row[i].token, lane == 0) : nullptr;
-      if (tab == nullptr) live[i] = false;
-      const int half = a.rope_dims / 2;
+    for (int e = 0; e < 8; ++e) wc[e] = scale, ws[e] = 0.f;
+    if (in_rope) {
+      float cs[8], sn[8], v[8];
       if (a.interleaved) {
-        if (tab != nullptr) {
+        const float4 c = *reinterpret_cast<const float4*>(tab + c0 / 2);
+        const float4 s = *reinterpret_cast<const float4*>(tab + half + c0 / 2);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            if (c0 + e < a.rope_dims) {
-              const float c = __ldg(tab + (c0 + e) / 2), s = __ldg(tab + half + (c0 + e) / 2);
-              const float u = x[i][e], v = x[i][e + 1];
-              x[i][e] = u * c - v * s;
-              x[i][e + 1] = v * c + u * s;
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          cs[e] = cc[e / 2];
+          sn[e] = (e & 1) ? ss[e / 2] : -ss[e / 2];
         }
       } else {
-        // half is a multiple of 8: the pair's other eight are half / 8 lanes on
-        const bool low = c0 < half, in = c0 < a.rope_dims;
-        const int other = low ? lane + half / 8 : lane - half / 8;
-        float y[8];
+        load8_f32(tab + (low ? c0 : c0 - half), cs);
+        load8_f32(tab + half + (low ? c0 : c0 - half), sn);
+        if (low) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(kFull, x[i][e], in ? other : lane, LANES);
-        if (in && tab != nullptr) {
-          const int j = low ? c0 : c0 - half;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float c = __ldg(tab + j + e), s = __ldg(tab + half + j + e);
-            x[i][e] = low ? x[i][e] * c - y[e] * s : x[i][e] * c + y[e] * s;
-          }
+          for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
         }
       }
-    }
-  }
+      if (weight != nullptr) load8_f32(weight + (a.interleaved ? c0 : 8 * other), v);
 #pragma unroll
-  for (int i = 0; i < UNROLL; ++i) {
-    if (!live[i] || !mine) continue;
-    unsigned char* out = row[i].out + c0 * sizeof(T);
-    if constexpr (kBf16) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(x[i][2 * e], x[i][2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t*>(&p);
+      for (int e = 0; e < 8; ++e) {
+        wc[e] *= cs[e];
+        ws[e] = scale * sn[e] * (weight != nullptr ? v[a.interleaved ? e ^ 1 : e] : 1.f);
       }
-      for (int c = 0; c < row[i].repeat; ++c, out += a.d * sizeof(T))
-        *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      for (int c = 0; c < row[i].repeat; ++c, out += a.d * sizeof(T)) {
-        *reinterpret_cast<float4*>(out) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
-        *reinterpret_cast<float4*>(out + 16) = make_float4(x[i][4], x[i][5], x[i][6], x[i][7]);
+    }
+    if (weight != nullptr && mine) {
+      float v[8];
+      load8_f32(weight + c0, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wc[e] *= v[e];
+    }
+    unsigned char* out = reinterpret_cast<unsigned char*>(isq ? a.q_out : a.k_out) +
+                         ((t * heads + h0) * repeat * static_cast<int64_t>(a.d) + c0) * static_cast<int64_t>(sizeof(T));
+    const int copy = a.d * static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      if (i > 0 && h0 - grp + i * kPass >= heads) break;  // a whole warp
+      float x[8];
+      unpack8<T>(raw[i], x);
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      const float f = inv_norm(sum, mean, a.eps);
+      if (a.rope_dims > 0) {
+        Raw8<T> pair = raw[i];
+        if (!a.interleaved) {
+#pragma unroll
+          for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) {
+            pair.w[k].x = __shfl_sync(kFull, pair.w[k].x, other, LANES);
+            pair.w[k].y = __shfl_sync(kFull, pair.w[k].y, other, LANES);
+            pair.w[k].z = __shfl_sync(kFull, pair.w[k].z, other, LANES);
+            pair.w[k].w = __shfl_sync(kFull, pair.w[k].w, other, LANES);
+          }
+        }
+        float y[8], z[8];
+        unpack8<T>(pair, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = f * fmaf(a.interleaved ? y[e ^ 1] : y[e], ws[e], x[e] * wc[e]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = z[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= f * wc[e];
+      }
+      if (h0 + i * kPass < heads && mine) {
+        unsigned char* o = out + static_cast<int64_t>(i) * step * repeat;
+        if constexpr (sizeof(T) == 2) {
+          uint32_t p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+            p[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          for (int c = 0; c < repeat; ++c, o += copy) *reinterpret_cast<uint4*>(o) = make_uint4(p[0], p[1], p[2], p[3]);
+        } else {
+          for (int c = 0; c < repeat; ++c, o += copy) {
+            *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(o + 16) = make_float4(x[4], x[5], x[6], x[7]);
+          }
+        }
       }
     }
   }
@@ -202,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(const treewy_qk a
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  const float f = row.scale * inv_norm(a, sum);
+  const float f = row.scale * inv_norm(sum, a.norm == TREEWY_NORM_RMS ? 1.0f / static_cast<float>(a.d) : 1.f, a.eps);
   for (int c = lane; c < a.d; c += 32) y[c] *= row.w != nullptr ? f * __ldg(row.w + c) : f;
   __syncwarp();
   if (a.rope_dims > 0) {
@@ -223,13 +274,26 @@ __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(const treewy_qk a
     for (int e = lane; e < a.d; e += 32) out[c * a.d + e] = static_cast<T>(y[e]);
 }
 
-template <typename T, int LANES>
-cudaError_t launch(const treewy_qk& a, int64_t rows, cudaStream_t stream) {
-  constexpr int kUnroll = 4;
-  constexpr int kRows = kThreads / LANES;
-  const int64_t wide = (rows + kRows * kUnroll - 1) / (kRows * kUnroll);
-  qk_norm_kernel<T, LANES, kUnroll><<<static_cast<unsigned>(wide), kThreads, 0, stream>>>(a);
+template <typename T, int LANES, int UNROLL, int THREADS>
+cudaError_t launch_passes(const treewy_qk& a, cudaStream_t stream) {
+  constexpr int kHeads = UNROLL * 32 / LANES;
+  const int q_units = (a.Hq + kHeads - 1) / kHeads, units = q_units + (a.Hk + kHeads - 1) / kHeads;
+  const dim3 grid(static_cast<unsigned>((a.T + THREADS / 32 - 1) / (THREADS / 32)),
+                  static_cast<unsigned>(units < 65535 ? units : 65535));
+  const float mean = a.norm == TREEWY_NORM_RMS ? 1.0f / static_cast<float>(a.d) : 1.f;
+  qk_norm_kernel<T, LANES, UNROLL, THREADS><<<grid, THREADS, 0, stream>>>(a, q_units, units, mean);
   return cudaGetLastError();
+}
+
+template <typename T, int LANES>
+cudaError_t launch(const treewy_qk& a, cudaStream_t stream) {
+  // Many rows: as many heads per warp as its registers hold, and a warp per
+  // CTA, so that a warp's place is filled as soon as it is done (32768 tokens
+  // of 18 bf16 heads of 256: 122 us, 143 us with two warps per CTA).  Few: the
+  // rows spread over more warps (256 tokens of 32 heads of 128: 2.3 us).
+  constexpr int kMany = sizeof(T) == 2 ? 8 : 4;
+  return a.T * (a.Hq + a.Hk) >= int64_t(152) * 64 * (32 / LANES) ? launch_passes<T, LANES, kMany, 32>(a, stream)
+                                                               : launch_passes<T, LANES, 2, 64>(a, stream);
 }
 
 template <typename T>
@@ -238,7 +302,9 @@ cudaError_t launch_typed(const treewy_qk& a, cudaStream_t stream) {
   auto on16 = [](const void* p, int64_t stride) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (stride * sizeof(T)) % 16 == 0;
   };
-  bool wide = a.d % 8 == 0 && (a.interleaved || a.rope_dims % 16 == 0);
+  bool wide = a.d % 8 == 0 && a.rope_dims % (a.interleaved ? 8 : 16) == 0 &&
+              reinterpret_cast<uintptr_t>(a.rope) % 16 == 0 && reinterpret_cast<uintptr_t>(a.q_weight) % 16 == 0 &&
+              reinterpret_cast<uintptr_t>(a.k_weight) % 16 == 0;
   if (a.Hq > 0) wide = wide && on16(a.q, a.q_stride) && on16(a.q_out, 0);
   if (a.Hk > 0) wide = wide && on16(a.k, a.k_stride) && on16(a.k_out, 0);
   if (!wide) {
@@ -246,9 +312,9 @@ cudaError_t launch_typed(const treewy_qk& a, cudaStream_t stream) {
     qk_norm_any_kernel<T><<<static_cast<unsigned>((rows + kRows - 1) / kRows), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  if (a.d <= 64) return launch<T, 8>(a, rows, stream);
-  if (a.d <= 128) return launch<T, 16>(a, rows, stream);
-  return launch<T, 32>(a, rows, stream);
+  if (a.d <= 64) return launch<T, 8>(a, stream);
+  if (a.d <= 128) return launch<T, 16>(a, stream);
+  return launch<T, 32>(a, stream);
 }
 
 }  // namespace
