@@ -894,8 +894,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap map_v, const treewy_seqs a) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ ChunkSmem cs;
-  unsigned char* base =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) & ~uintptr_t(1023));
+  // by an offset, so that the compiler still knows the pointer to be a shared one
+  unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int t = threadIdx.x, warp = t >> 5;
 
