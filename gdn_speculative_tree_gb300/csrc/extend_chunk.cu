@@ -6,16 +6,16 @@
 // Within a chunk, with g_t the product of its decays up to token t, the
 // recurrence S_t = a_t S_{t-1} (I - b_t k_t k_t^T) + b_t v_t k_t^T unrolls to
 //
-//   (I + A) U = W,  A[n,i] = b_n (g_n/g_i) k_n.k_i (i < n),  W_i = b_i (v_i - g_i S k_i),
+//   (I + A) U = diag(b) W,  A[n,i] = b_n (g_n/g_i) k_n.k_i (i < n),  W_i = v_i - g_i S k_i,
 //   o_n = g_n S q_n + sum_{i<=n} M[n,i] u_i,  M[n,i] = (g_n/g_i) q_n.k_i,
 //   S'  = g_C S + sum_n (g_C/g_n) u_n k_n^T.
 //
 // With T = (I + A)^-1 neither sum needs U:
 //
-//   o_n = g_n S q_n + ((M T) W)_n,   S' = g_C S + sum_i W_i kt_i^T,
-//   kt_i = sum_n T[n,i] (g_C/g_n) k_n,
+//   o_n = g_n S q_n + (MT W)_n,   S' = g_C S + sum_i W_i kt_i^T,
+//   MT = M T diag(b),   kt_i = b_i sum_n T[n,i] (g_C/g_n) k_n,
 //
-// and T, M T and kt depend on the tokens alone.  So the chain from one
+// and MT and kt depend on the tokens alone.  So the chain from one
 // chunk's state to the next is two products long, S k and W kt; everything
 // else is prepared one chunk ahead or follows behind.
 //
@@ -26,7 +26,7 @@
 //
 //   warps 0-7    state: two threads per row (64 of S's columns and 32 tokens
 //                each); S stays in f32 registers for the whole sequence
-//   warps 8-15   preparation of the next chunk: [K;Q] K^T, T, M T, kt
+//   warps 8-15   preparation of the next chunk: [K;Q] K^T, T, MT, kt
 //   warps 16-19  o
 //   warp 20      issues the chain's products
 //   warp 21      loads K, Q and V, two chunks in flight
@@ -60,9 +60,9 @@ static_assert(2 * kStateRegs + 2 * kPrepRegs + kOutRegs + kMiscRegs <= 6 * kLaun
 // TMEM columns
 constexpr uint32_t kColS = 0;                // S: hi in 64 columns, lo in 64 (bf16 pairs)
 constexpr uint32_t kColW = 128;              // S k, then W (16 columns per 16 tokens: hi 8, lo 8)
-constexpr uint32_t kColO = 192;              // S q, then (M T) W
+constexpr uint32_t kColO = 192;              // S q, then MT W
 constexpr uint32_t kColD = 256;              // sum W kt^T
-constexpr uint32_t kColG = 384;              // [K;Q] K^T, then M T
+constexpr uint32_t kColG = 384;              // [K;Q] K^T
 constexpr uint32_t kColK = 448;              // kt^T
 constexpr uint32_t kTmemCols = 512;
 
@@ -72,15 +72,16 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBox = 8192;
 constexpr uint32_t kStageBytes = 6 * kBox;
 constexpr uint32_t kOffKt = 2 * kStageBytes;      // kt^T: 128 rows (dk) of 64 tokens, hi then lo
-constexpr uint32_t kOffMT = kOffKt + 4 * kBox;    // M T: 64 rows of 64 tokens, hi then lo
+constexpr uint32_t kOffMT = kOffKt + 4 * kBox;    // MT: 64 rows of 64 tokens, hi then lo
 constexpr uint32_t kOffM = kOffMT + 2 * kBox;     // M, hi then lo
-constexpr uint32_t kOffT = kOffM + 2 * kBox;      // T hi, lo, then (g_C/g_n) T hi, lo
-constexpr uint32_t kOffA = kOffT + 4 * kBox;      // A, then T: f32, 64 rows
-constexpr int kPitchA = 68;
-constexpr uint32_t kSmemBytes = kOffA + kC * kPitchA * 4 + 1024;
+constexpr uint32_t kOffT = kOffM + 2 * kBox;      // T hi, lo, then T'' = diag(g_C/g_n) T diag(b) hi, lo
+constexpr uint32_t kOffA = kOffT + 4 * kBox;      // A left of its diagonal blocks of 16, hi then lo
+constexpr uint32_t kOffD = kOffA + 2 * kBox;      // A's diagonal blocks of 16: f32, rows of 20
+constexpr int kPitchD = 20;
+constexpr uint32_t kSmemBytes = kOffD + kC * kPitchD * 4 + 1024;
 
 struct __align__(16) Gates {
-  float a[kC], b[kC], bg[kC], g[kC];  // decay a, b, b g and g (the product of the decays up to it) of every token
+  float a[kC], b[kC], g[kC];          // decay, write strength and the product of the decays up to every token
   float dec[kC];                      // g_C / g_n: the product of the decays behind token n
   float mid[kC];                      // product of the decays from token 32 to n (1 for n < 32)
   float gC;
@@ -189,34 +190,36 @@ __device__ __forceinline__ void prep_sync() { named_bar_sync<1, kPrepThreads>();
 // them leave together, so that none is left at a barrier.
 __device__ __forceinline__ bool prep_failed(bool ok) { return named_bar_or<1, kPrepThreads>(!ok); }
 
-// D += A B of one 16 x 8 x 16 warp-level tile with f32 operands as hi and lo.
+// D += A B of one 16 x 8 x 16 warp-level tile with operands as hi and lo.
 struct Frag4 {
   uint32_t hi[4], lo[4];
 };
-struct Frag2 {
-  uint32_t hi[2], lo[2];
-};
-__device__ __forceinline__ void mma_split(float (&d)[4], const Frag4& a, const Frag2& b) {
-  mma16816_bf16_nv(d, a.lo[0], a.lo[1], a.lo[2], a.lo[3], b.hi[0], b.hi[1]);
-  mma16816_bf16_nv(d, a.hi[0], a.hi[1], a.hi[2], a.hi[3], b.lo[0], b.lo[1]);
-  mma16816_bf16_nv(d, a.hi[0], a.hi[1], a.hi[2], a.hi[3], b.hi[0], b.hi[1]);
+__device__ __forceinline__ void mma_split(float (&d)[4], const Frag4& a, uint32_t bh0, uint32_t bh1, uint32_t bl0,
+                                          uint32_t bl1) {
+  mma16816_bf16_nv(d, a.lo[0], a.lo[1], a.lo[2], a.lo[3], bh0, bh1);
+  mma16816_bf16_nv(d, a.hi[0], a.hi[1], a.hi[2], a.hi[3], bl0, bl1);
+  mma16816_bf16_nv(d, a.hi[0], a.hi[1], a.hi[2], a.hi[3], bh0, bh1);
 }
-// 16 x 16 left operand at X, 16 x 8 right operand at X (rows the contraction).
-__device__ __forceinline__ Frag4 left_frag(const float* X, int lane) {
-  const float* x = X + (lane >> 2) * kPitchA + 2 * (lane & 3);
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_addr(p)));
+}
+// The 16 x 16 block at (row, col) of an operand's hi and lo tiles as a left
+// operand, and as two right operands of 8 columns each (rows the contraction:
+// hi and lo of the first in [0..1], of the second in [2..3]).
+__device__ __forceinline__ Frag4 left_frag(const unsigned char* hi, const unsigned char* lo, int row, int col, int lane) {
+  const uint32_t at = sw128_off(row + (lane & 15), col + 8 * (lane >> 4));
   Frag4 f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = *reinterpret_cast<const float2*>(x + (i & 1) * 8 * kPitchA + (i >> 1) * 8);
-    split_pair(v.x, v.y, f.hi[i], f.lo[i]);
-  }
+  ldsm_x4(f.hi, hi + at);
+  ldsm_x4(f.lo, lo + at);
   return f;
 }
-__device__ __forceinline__ Frag2 right_frag(const float* X, int lane) {
-  const float* x = X + 2 * (lane & 3) * kPitchA + (lane >> 2);
-  Frag2 f;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) split_pair(x[8 * i * kPitchA], x[(8 * i + 1) * kPitchA], f.hi[i], f.lo[i]);
+__device__ __forceinline__ Frag4 right_frags(const unsigned char* hi, const unsigned char* lo, int row, int col, int lane) {
+  const uint32_t at = sw128_off(row + (lane & 15), col + 8 * (lane >> 4));
+  Frag4 f;
+  ldsm_x4_trans(f.hi, hi + at);
+  ldsm_x4_trans(f.lo, lo + at);
   return f;
 }
 // Two neighbouring result tiles as the next product's left operand.
@@ -228,16 +231,34 @@ __device__ __forceinline__ Frag4 left_of(const float (&d0)[4], const float (&d1)
   split_pair(d1[2], d1[3], f.hi[3], f.lo[3]);
   return f;
 }
+// A result tile at (row, col) of T, negated, and of T''.
+__device__ __forceinline__ void put_t(unsigned char* tb, const Gates& g, int row, int col, const float (&d)[4], int lane) {
+  const int c = col + 2 * (lane & 3);
+  const float2 b = *reinterpret_cast<const float2*>(g.b + c);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = row + 8 * e + (lane >> 2);
+    const float f = -g.dec[r];
+    const uint32_t at = sw128_off(r, c);
+    uint32_t h, l;
+    split_pair(-d[2 * e], -d[2 * e + 1], h, l);
+    *reinterpret_cast<uint32_t*>(tb + at) = h;
+    *reinterpret_cast<uint32_t*>(tb + kBox + at) = l;
+    split_pair(f * b.x * d[2 * e], f * b.y * d[2 * e + 1], h, l);
+    *reinterpret_cast<uint32_t*>(tb + 2 * kBox + at) = h;
+    *reinterpret_cast<uint32_t*>(tb + 3 * kBox + at) = l;
+  }
+}
 
-// The operands T and T'' = diag(g_C/g_n) T of T = (I + A)^-1, with A's lower
-// triangle in X (overwritten): the diagonal blocks of 16 by substitution, a
-// column per lane; then blocks of 32 and of 64 by T21 = -(T22 A21) T11 on
-// warp-level MMAs, a tile per warp.  The operands' upper right quarter is zero
-// and not written; X's takes T22 A21.
-__device__ __forceinline__ void invert(float* X, const float* dec, unsigned char* tb, int p) {
+// The operands T = (I + A)^-1 and T'' = diag(g_C/g_n) T diag(b): the diagonal
+// blocks of 16 by substitution, a column per lane; then blocks of 32 and of 64
+// by T21 = -(T22 A21) T11 on warp-level MMAs.  Blocks right of the diagonal
+// ones stay as they are (zero).  Every preparation thread; ends without a
+// barrier.
+__device__ __forceinline__ void invert(const float* D, const unsigned char* ab, unsigned char* tb, const Gates& g, int p) {
   const int w = p >> 5, lane = p & 31;
   if (w < 4) {
-    float* B = X + 16 * w * (kPitchA + 1);
+    const float* B = D + 16 * w * kPitchD;
     const int j = lane & 15;
     float x[16];
 #pragma unroll
@@ -246,89 +267,94 @@ __device__ __forceinline__ void invert(float* X, const float* dec, unsigned char
     for (int i = 0; i < 16; i += 4) {
 #pragma unroll
       for (int n = i + 1; n < 16; ++n) {
-        const float4 a = *reinterpret_cast<const float4*>(B + n * kPitchA + i);
+        const float4 a = *reinterpret_cast<const float4*>(B + n * kPitchD + i);
         x[n] = fmaf(-a.x, x[i], x[n]);
         if (n > i + 1) x[n] = fmaf(-a.y, x[i + 1], x[n]);
         if (n > i + 2) x[n] = fmaf(-a.z, x[i + 2], x[n]);
         if (n > i + 3) x[n] = fmaf(-a.w, x[i + 3], x[n]);
       }
     }
-    __syncwarp();
-    if (lane < 16) {
+    // lanes 0-15 write the columns of T, lanes 16-31 those of T''
+    const bool second = lane >= 16;
+    const float b = g.b[16 * w + j];
+    unsigned char* out = tb + (second ? 2 * kBox : 0u);
 #pragma unroll
-      for (int n = 0; n < 16; ++n) B[n * kPitchA + j] = x[n];
+    for (int n = 0; n < 16; ++n) {
+      const float y = second ? x[n] * b * g.dec[16 * w + n] : x[n];
+      const __nv_bfloat16 h = __float2bfloat16_rn(y), l = __float2bfloat16_rn(y - __bfloat162float(h));
+      const uint32_t at = sw128_off(16 * w + n, 16 * w + j);
+      *reinterpret_cast<__nv_bfloat16*>(out + at) = h;
+      *reinterpret_cast<__nv_bfloat16*>(out + kBox + at) = l;
     }
   }
   prep_sync();
-  {
+  if ((w & 3) < 2) {
     // blocks of 32: 8 columns of T21 per warp
-    float* R = X + 32 * (w >> 2) * (kPitchA + 1);
-    float* A21 = R + 16 * kPitchA;
-    const int t = w & 3;
+    const int r0 = 32 * (w >> 2), t = w & 3;
     float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
-    if (t < 2) {
-      const Frag4 t22 = left_frag(A21 + 16, lane);
-      mma_split(d0, t22, right_frag(A21, lane));
-      mma_split(d1, t22, right_frag(A21 + 8, lane));
-      mma_split(d, left_of(d0, d1), right_frag(R + 8 * t, lane));
-    }
-    prep_sync();
-    if (t < 2) {
-      float* out = A21 + (lane >> 2) * kPitchA + 8 * t + 2 * (lane & 3);
-      *reinterpret_cast<float2*>(out) = make_float2(-d[0], -d[1]);
-      *reinterpret_cast<float2*>(out + 8 * kPitchA) = make_float2(-d[2], -d[3]);
-    }
-  }
-  prep_sync();
-  // the lower left quarter: 16 rows and 8 columns of it per warp
-  const int m = w & 1, t = w >> 1;
-  float* P = X + 32;
-  {
-    const float* A21 = X + 32 * kPitchA;
-    const float* T22 = A21 + 32 + 16 * m * kPitchA;
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k <= m)  // T22 is lower triangular
-        mma_split(d, left_frag(T22 + 16 * k, lane), right_frag(A21 + 16 * k * kPitchA + 8 * t, lane));
-    }
-    float* out = P + (16 * m + (lane >> 2)) * kPitchA + 8 * t + 2 * (lane & 3);
-    *reinterpret_cast<float2*>(out) = make_float2(d[0], d[1]);
-    *reinterpret_cast<float2*>(out + 8 * kPitchA) = make_float2(d[2], d[3]);
-  }
-  {
-    // T's diagonal blocks of 32 as operands: eight values per thread
-    const int r = p >> 2, c0 = (r & 32) + 8 * (p & 3);
-    const float f = dec[r];
-    const float4* src = reinterpret_cast<const float4*>(X + r * kPitchA + c0);
-    const float4 u = src[0], v = src[1];
-    float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    put_piece(tb, tb + kBox, r, c0 / 8, y);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] *= f;
-    put_piece(tb + 2 * kBox, tb + 3 * kBox, r, c0 / 8, y);
+    const Frag4 t22 = left_frag(tb, tb + kBox, r0 + 16, r0 + 16, lane);
+    const Frag4 a21 = right_frags(ab, ab + kBox, r0 + 16, r0, lane);
+    const Frag4 t11 = right_frags(tb, tb + kBox, r0, r0, lane);
+    mma_split(d0, t22, a21.hi[0], a21.hi[1], a21.lo[0], a21.lo[1]);
+    mma_split(d1, t22, a21.hi[2], a21.hi[3], a21.lo[2], a21.lo[3]);
+    const Frag4 l = left_of(d0, d1);
+    if (t == 0) mma_split(d, l, t11.hi[0], t11.hi[1], t11.lo[0], t11.lo[1]);
+    else mma_split(d, l, t11.hi[2], t11.hi[3], t11.lo[2], t11.lo[3]);
+    put_t(tb, g, r0 + 16, r0 + 8 * t, d, lane);
   }
   prep_sync();
   {
+    // the lower left quarter: 16 rows (m) and 8 columns (t) of it per warp.
+    // T22 and T11 are lower triangular: only blocks k <= m of the one, k >= t/2
+    // of the other.
+    const int m = w & 1, t = w >> 1;
     float d[4] = {0.f, 0.f, 0.f, 0.f};
+    Frag4 t22[2];
+    t22[0] = left_frag(tb, tb + kBox, 32 + 16 * m, 32, lane);
+    if (m == 1) t22[1] = left_frag(tb, tb + kBox, 48, 48, lane);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (k >= (t >> 1))  // T11 is lower triangular
-        mma_split(d, left_frag(P + 16 * m * kPitchA + 16 * k, lane), right_frag(X + 16 * k * kPitchA + 8 * t, lane));
-    }
+      if (k >= (t >> 1)) {
+        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 32 + 16 * m + 8 * e + (lane >> 2);
-      const float f = -dec[r];
-      const uint32_t at = sw128_off(r, 8 * t + 2 * (lane & 3));
-      uint32_t h, l;
-      split_pair(-d[2 * e], -d[2 * e + 1], h, l);
-      *reinterpret_cast<uint32_t*>(tb + at) = h;
-      *reinterpret_cast<uint32_t*>(tb + kBox + at) = l;
-      split_pair(f * d[2 * e], f * d[2 * e + 1], h, l);
-      *reinterpret_cast<uint32_t*>(tb + 2 * kBox + at) = h;
-      *reinterpret_cast<uint32_t*>(tb + 3 * kBox + at) = l;
+        for (int kk = 0; kk < 2; ++kk) {
+          if (kk <= m) {
+            const Frag4 a21 = right_frags(ab, ab + kBox, 32 + 16 * kk, 16 * k, lane);
+            mma_split(d0, t22[kk], a21.hi[0], a21.hi[1], a21.lo[0], a21.lo[1]);
+            mma_split(d1, t22[kk], a21.hi[2], a21.hi[3], a21.lo[2], a21.lo[3]);
+          }
+        }
+        const Frag4 l = left_of(d0, d1);
+        const Frag4 t11 = right_frags(tb, tb + kBox, 16 * k, 16 * (t >> 1), lane);
+        if ((t & 1) == 0) mma_split(d, l, t11.hi[0], t11.hi[1], t11.lo[0], t11.lo[1]);
+        else mma_split(d, l, t11.hi[2], t11.hi[3], t11.lo[2], t11.lo[3]);
+      }
     }
+    put_t(tb, g, 32 + 16 * m, 8 * t, d, lane);
+  }
+}
+
+// The 16 x 8 tile (row 16 m, column 8 t) of MT = M T diag(b).
+__device__ __forceinline__ void put_mt(unsigned char* mtb, const unsigned char* mb, const unsigned char* tb,
+                                       const Gates& g, int m, int t, int lane) {
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k = t >> 1; k <= m; ++k) {
+    const Frag4 l = left_frag(mb, mb + kBox, 16 * m, 16 * k, lane);
+    // k rows of 8 columns: lanes 0-15 address the hi tile, 16-31 the lo tile
+    uint32_t r[4];
+    ldsm_x4_trans(r, tb + (lane >> 4) * kBox + sw128_off(16 * k + (lane & 15), 8 * t));
+    mma_split(d, l, r[0], r[1], r[2], r[3]);
+  }
+  const int c = 8 * t + 2 * (lane & 3);
+  const float2 b = *reinterpret_cast<const float2*>(g.b + c);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t at = sw128_off(16 * m + 8 * e + (lane >> 2), c);
+    uint32_t h, l;
+    split_pair(b.x * d[2 * e], b.y * d[2 * e + 1], h, l);
+    *reinterpret_cast<uint32_t*>(mtb + at) = h;
+    *reinterpret_cast<uint32_t*>(mtb + kBox + at) = l;
   }
 }
 
@@ -429,12 +455,28 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
     const uint32_t ph2 = c >> 1;
     const Gates& g = cs.gates[sg];
     const int left = q.len - c * kC - n0;  // tokens of this thread's half
-    ok = wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.full_v[sg], ph2) && wait(cs, &cs.d1_done, c);
+    // this thread's values of V, while S k is under way: zero past the end
+    uint32_t v[16];
+    ok = wait(cs, &cs.full_v[sg], ph2);
+    {
+      const unsigned char* vt = base + sg * kStageBytes + 4 * kBox + n0 * 256 + 2 * d;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t v0 = *reinterpret_cast<const uint16_t*>(vt + 2 * e * 256);
+        const uint32_t v1 = *reinterpret_cast<const uint16_t*>(vt + (2 * e + 1) * 256);
+        v[e] = v0 | (v1 << 16);
+      }
+      if (left < 32) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          v[e] = 2 * e + 1 < left ? v[e] : (2 * e < left ? v[e] & 0xffffu : 0u);
+      }
+    }
+    ok = ok && wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.d1_done, c);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after_sync();
     {
-      // W = b v - b g (S k), zero past the sequence's end
-      const unsigned char* vt = base + sg * kStageBytes + 4 * kBox + n0 * 256 + 2 * d;
+      // W = v - g (S k)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         uint32_t x[16], hi[8], lo[8];
@@ -442,18 +484,13 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
         tmem_wait16(x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int n = 16 * b + 4 * j;
-          const float4 fb = *reinterpret_cast<const float4*>(g.b + n0 + n);
-          const float4 fg = *reinterpret_cast<const float4*>(g.bg + n0 + n);
-          const float bs[4] = {fb.x, fb.y, fb.z, fb.w}, bgs[4] = {fg.x, fg.y, fg.z, fg.w};
-          float w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float v = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + (n + k) * 256));
-            w[k] = n + k < left ? fmaf(-bgs[k], __uint_as_float(x[4 * j + k]), bs[k] * v) : 0.f;
-          }
-          split_pair(w[0], w[1], hi[2 * j], lo[2 * j]);
-          split_pair(w[2], w[3], hi[2 * j + 1], lo[2 * j + 1]);
+          const float4 f = *reinterpret_cast<const float4*>(g.g + n0 + 16 * b + 4 * j);
+          const uint32_t va = v[8 * b + 2 * j], vb = v[8 * b + 2 * j + 1];
+          split_pair(fmaf(-f.x, __uint_as_float(x[4 * j]), __uint_as_float(va << 16)),
+                     fmaf(-f.y, __uint_as_float(x[4 * j + 1]), __uint_as_float(va & 0xffff0000u)), hi[2 * j], lo[2 * j]);
+          split_pair(fmaf(-f.z, __uint_as_float(x[4 * j + 2]), __uint_as_float(vb << 16)),
+                     fmaf(-f.w, __uint_as_float(x[4 * j + 3]), __uint_as_float(vb & 0xffff0000u)), hi[2 * j + 1],
+                     lo[2 * j + 1]);
         }
         // 16 tokens: hi in 8 columns, lo in 8, in place of what was just read
         tmem_st8(tm + kColW + n0 + 16 * b, hi);
@@ -488,7 +525,7 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
   if (ok && d < a.dv) store_state<SB>(a, row, half, S);
 }
 
-// The output warps: o = g (S q) + (M T) W, a row of 64 tokens per thread.
+// The output warps: o = g (S q) + MT W, a row of 64 tokens per thread.
 template <bool OF32>
 __device__ __forceinline__ void run_out(const treewy_seqs& a, ChunkSmem& cs, unsigned char* base, const SeqInfo& q,
                                         int h, int nchunk) {
@@ -609,7 +646,6 @@ __device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, c
       const int i = lane + 32 * k;
       g.a[i] = al[k];
       g.b[i] = be[k];
-      g.bg[i] = be[k] * up[k];
       g.g[i] = up[k];
       g.dec[i] = dec[k];
       g.mid[i] = k ? mid : 1.f;
@@ -620,29 +656,27 @@ __device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, c
   }
 }
 
-// The preparation warps: T, M T and kt of every chunk, one chunk ahead of the
-// state.  Warps p and p + 4 share a quarter of the lanes (rows), half of the
-// columns each.
+// The preparation warps: T, MT and kt of every chunk, one chunk ahead of the
+// state, and [K;Q] K^T one more chunk ahead.  Warps p and p + 4 share a quarter
+// of the lanes (rows), half of the columns each.
 __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int len, int nchunk) {
   const int p = threadIdx.x - 32 * kPrepWarp, row = p & 127, n = p & 63, hh = p >> 7;
+  const int w = p >> 5, lane = p & 31;
   const bool first = p < 32;
   const uint32_t tm = cs.tmem + (static_cast<uint32_t>(p & 96) << 16);
-  float* A = reinterpret_cast<float*>(base + kOffA);
-  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
-  // the upper right quarters of M, T and T'' stay zero
-  for (int i = 16 * p; i < static_cast<int>(6 * kBox); i += 16 * kPrepThreads)
-    *reinterpret_cast<uint4*>(mb + i) = make_uint4(0u, 0u, 0u, 0u);
-  bool ok = true;
-  for (int c = 0; c < nchunk; ++c) {
-    const int sg = c & 1;
-    const uint32_t ph2 = c >> 1;
-    const int nt = min(kC, len - c * kC);
-    unsigned char* st = base + sg * kStageBytes;
-    const Gates& g = cs.gates[sg];
-    if (!wait(cs, &cs.full[sg], ph2)) ok = false;
+  float* D = reinterpret_cast<float*>(base + kOffD);
+  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT, *ab = base + kOffA;
+  // what lies right of the diagonal blocks of MT, M, T and T'' stays zero
+  for (int i = 16 * p; i < static_cast<int>(8 * kBox); i += 16 * kPrepThreads)
+    *reinterpret_cast<uint4*>(mtb + i) = make_uint4(0u, 0u, 0u, 0u);
+  // K and Q of chunk c are there; rows of K past the sequence's end (the next
+  // one's) become zero
+  auto stage_in = [&](int c) {
+    const bool there = wait(cs, &cs.full[c & 1], c >> 1);
     __syncwarp();
+    const int nt = len - c * kC;
     if (nt < kC) {
-      // rows of K past the sequence's end (the next one's) become zero
+      unsigned char* st = base + (c & 1) * kStageBytes;
       for (int i = nt * 128 + 16 * p; i < static_cast<int>(kBox); i += 16 * kPrepThreads) {
         *reinterpret_cast<uint4*>(st + i) = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(st + 2 * kBox + i) = make_uint4(0u, 0u, 0u, 0u);
@@ -650,29 +684,41 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
       fence_proxy_async_smem();
       warp_arrive(&cs.fix);
     }
-    if (prep_failed(ok)) break;
-    if (first && elect_one()) {
-      tc_fence_after_sync();
-      constexpr uint32_t id = idesc_bf16_f32(128, kC);
-      const uint64_t s0 = smem_desc_sw128(smem_addr(st), 1024);
+    return there;
+  };
+  auto issue_gram = [&](int c) {  // one elected lane
+    constexpr uint32_t id = idesc_bf16_f32(128, kC);
+    const uint64_t s0 = smem_desc_sw128(smem_addr(base + (c & 1) * kStageBytes), 1024);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint64_t at = s0 + (((k >> 2) * 2 * kBox + (k & 3) * 32) >> 4);
-        mma_bf16(cs.tmem + kColG, at, at, id, k > 0);
-      }
-      mma_commit(&cs.gram_done);
+    for (int k = 0; k < 8; ++k) {
+      const uint64_t at = s0 + (((k >> 2) * 2 * kBox + (k & 3) * 32) >> 4);
+      mma_bf16(cs.tmem + kColG, at, at, id, k > 0);
     }
-    __syncwarp();
+    mma_commit(&cs.gram_done);
+  };
+  bool ok = stage_in(0);
+  if (prep_failed(ok)) return;
+  if (first && elect_one()) {
+    tc_fence_after_sync();
+    issue_gram(0);
+  }
+  __syncwarp();
+  for (int c = 0; c < nchunk; ++c) {
+    const int sg = c & 1;
+    const uint32_t ph2 = c >> 1;
+    unsigned char* st = base + sg * kStageBytes;
+    const Gates& g = cs.gates[sg];
     if (!wait(cs, &cs.gates_ready[sg], ph2) || !wait(cs, &cs.gram_done, c)) ok = false;
-    __syncwarp();
+    prep_sync();  // the last chunk's M has been read
     tc_fence_after_sync();
     if (hh == 0 || (n & 32) != 0) {  // whole warps; the upper right quarter stays
-      // lanes 0-63: rows of A (f32), lanes 64-127: rows of M (hi and lo), from
-      // the diagonal (or column 31) leftwards; f is b_n (for A) times the
-      // decays passed
+      // lanes 0-63: rows of A, lanes 64-127: rows of M, from the diagonal (or
+      // column 31) leftwards; f is b_n (for A) times the decays passed.  (A's
+      // diagonal is never read.)
       const bool isM = row >= 64;
-      float f = (isM ? 1.f : g.b[n]) * (hh == 0 ? g.mid[n] : 1.f);
-      const int last = (isM ? n : n - 1) - 32 * hh, dl = n - 32 * hh;
+      const float f0 = isM ? 1.f : g.b[n];
+      const int dl = n - 32 * hh;  // the diagonal's column, at most 31 in a diagonal block of 32
+      float f = dl > 31 ? f0 * g.mid[n] : 0.f;
 #pragma unroll
       for (int b = 1; b >= 0; --b) {
         uint32_t x[16];
@@ -687,13 +733,16 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
           float y[8];
 #pragma unroll
           for (int k = 7; k >= 0; --k) {
-            y[k] = i0 + k <= last ? f * __uint_as_float(x[8 * j + k]) : 0.f;
-            if (i0 + k <= dl) f *= as[k];
+            if (i0 + k == dl) f = f0;
+            y[k] = f * __uint_as_float(x[8 * j + k]);
+            f *= as[k];
           }
           if (isM) {
             put_piece(mb, mb + kBox, n, 4 * hh + 2 * b + j, y);
-          } else {
-            float4* r = reinterpret_cast<float4*>(A + n * kPitchA + 32 * hh + i0);
+          } else if (2 * hh + b < (n >> 4)) {
+            put_piece(ab, ab + kBox, n, 4 * hh + 2 * b + j, y);
+          } else if (2 * hh + b == (n >> 4)) {
+            float4* r = reinterpret_cast<float4*>(D + n * kPitchD + 8 * j);
             r[0] = make_float4(y[0], y[1], y[2], y[3]);
             r[1] = make_float4(y[4], y[5], y[6], y[7]);
           }
@@ -702,37 +751,42 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
     }
     tc_fence_before_sync();
     if (prep_failed(ok)) break;
-    invert(A, g.dec, tb, p);
-    warp_arrive(&cs.gates_free[sg]);
+    invert(D, ab, tb, g, p);
+    if (c + 1 < nchunk && !stage_in(c + 1)) ok = false;
     fence_proxy_async_smem();
     prep_sync();
     if (first && elect_one()) {
       tc_fence_after_sync();
-      // kt^T[dk][i] = sum_n K[n][dk] (g_C/g_n) T[n][i]; M T (rows 64.. of its
-      // left operand only fill lanes that nothing reads)
+      // kt^T[dk][i] = sum_n K[n][dk] T''[n][i]; then the next chunk's [K;Q] K^T
       constexpr uint32_t idk = idesc_bf16_f32(128, kC) | kAmajorMN | kBmajorMN;
-      constexpr uint32_t idm = idesc_bf16_f32(128, kC) | kBmajorMN;
       const uint64_t k0 = smem_desc_sw128_mn(smem_addr(st), 2 * kBox);
-      const uint64_t t0 = smem_desc_sw128_mn(smem_addr(tb), kBox);
-      const uint64_t m0 = smem_desc_sw128(smem_addr(mb), 1024);
+      const uint64_t t0 = smem_desc_sw128_mn(smem_addr(tb + 2 * kBox), kBox);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + ((2 * kBox) >> 4) + k * 128, idk, k > 0);
-        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + ((3 * kBox) >> 4) + k * 128, idk, 1u);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint64_t th = t0 + k * 128, tl = th + (kBox >> 4), mh = m0 + 2 * k, ml = mh + (kBox >> 4);
-        mma_bf16(cs.tmem + kColG, mh, th, idm, k > 0);
-        mma_bf16(cs.tmem + kColG, mh, tl, idm, 1u);
-        mma_bf16(cs.tmem + kColG, ml, th, idm, 1u);
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + k * 128, idk, k > 0);
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + (kBox >> 4) + k * 128, idk, 1u);
       }
       mma_commit(&cs.prep_done);
+      if (c + 1 < nchunk) issue_gram(c + 1);
     }
     __syncwarp();
-    if (!wait(cs, &cs.prep_done, c)) ok = false;
-    // the last chunk's kt and M T have been read
+    // the last chunk's kt and MT have been read
     if (c > 0 && !wait(cs, &cs.o2_done, c - 1)) ok = false;
+    __syncwarp();
+    // MT: the rows of tiles 3 and 0, and 2 and 1, on four warps each, by their
+    // number of steps
+    const int u = w & 3;
+    if (w < 4) {
+      put_mt(mtb, mb, tb, g, 3, u, lane);
+      put_mt(mtb, mb, tb, g, 3, u + 4, lane);
+      if (u >= 2) put_mt(mtb, mb, tb, g, 0, u - 2, lane);
+    } else {
+      put_mt(mtb, mb, tb, g, 2, u, lane);
+      if (u < 2) put_mt(mtb, mb, tb, g, 2, u + 4, lane);
+      put_mt(mtb, mb, tb, g, 1, u ^ 2, lane);
+    }
+    warp_arrive(&cs.gates_free[sg]);
+    if (!wait(cs, &cs.prep_done, c)) ok = false;
     __syncwarp();
     tc_fence_after_sync();
 #pragma unroll
@@ -746,21 +800,6 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(x[8 * j + k]);
         put_piece(ktb, ktb + 2 * kBox, row, 4 * hh + 2 * b + j, y);
-      }
-    }
-    if (row < 64) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint32_t x[16];
-        tmem_ld16_async(tm + kColG + 32 * hh + 16 * b, x);
-        tmem_wait16(x);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float y[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(x[8 * j + k]);
-          put_piece(mtb, mtb + kBox, row, 4 * hh + 2 * b + j, y);
-        }
       }
     }
     tc_fence_before_sync();
@@ -844,7 +883,7 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
     }
     }
     __syncwarp();
-    // (M T) W over the columns of S q
+    // MT W over the columns of S q
     if (!held(&cs.qs_read, c)) return;
     if (elect_one()) {
     tc_fence_after_sync();
