@@ -31,6 +31,7 @@
 //   warp 20      issues the chain's products
 //   warp 21      loads K, Q and V, two chunks in flight
 //   warp 22      gates
+//   warp 23      issues the preparation's products
 //
 // Every product takes an f32 operand as two bf16 terms x = hi + lo (16
 // significant bits; lo times lo is left out), accumulates in f32, and keys,
@@ -47,9 +48,9 @@ namespace {
 constexpr int kC = 64;                       // tokens per chunk
 constexpr int kStateWarps = 8, kPrepWarps = 8, kOutWarps = 4;
 constexpr int kPrepWarp = kStateWarps, kOutWarp = kPrepWarp + kPrepWarps, kMmaWarp = kOutWarp + kOutWarps,
-              kLoadWarp = kMmaWarp + 1, kGateWarp = kLoadWarp + 1;
+              kLoadWarp = kMmaWarp + 1, kGateWarp = kLoadWarp + 1, kWarps = kGateWarp + 2;
 constexpr int kPrepThreads = 32 * kPrepWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);
+constexpr int kThreads = 32 * kWarps;
 // Registers per thread: kLaunchRegs at launch (six warps share the 512 x 32 of
 // a quarter of the SM); the state and output warps take what the others give
 // back.  An increase waits for registers of the launch, so the shares must not
@@ -92,7 +93,7 @@ struct ChunkSmem {
   Gates gates[2];
   uint64_t full[2], full_v[2], stage_free[2], v_free[2], gates_ready[2], gates_free[2];
   uint64_t fix, gram_done, prep_done, kt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done,
-      o_read, o_tile, drain[2];
+      o_read, o_tile, t_ready, drain[3];
   uint32_t tmem;
   int fail;
 };
@@ -176,30 +177,30 @@ __device__ __forceinline__ uint4* operand_piece(unsigned char* tile, int row, in
   return reinterpret_cast<uint4*>(tile + row * 128 + ((j ^ (row & 7)) << 4));
 }
 
-// Eight values as hi and lo pieces.
-__device__ __forceinline__ void put_piece(unsigned char* hi, unsigned char* lo, int row, int j, const float (&x)[8]) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) split_pair(x[2 * e], x[2 * e + 1], h[e], l[e]);
-  *operand_piece(hi, row, j) = make_uint4(h[0], h[1], h[2], h[3]);
-  *operand_piece(lo, row, j) = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
 __device__ __forceinline__ void prep_sync() { named_bar_sync<1, kPrepThreads>(); }
 // The same, and whether a wait of any preparation thread has given up: all of
 // them leave together, so that none is left at a barrier.
 __device__ __forceinline__ bool prep_failed(bool ok) { return named_bar_or<1, kPrepThreads>(!ok); }
 
-// D += A B of one 16 x 8 x 16 warp-level tile with operands as hi and lo.
+// A 16 x 8 result tile of warp-level products whose operands are hi and lo:
+// one accumulator per product of terms, so that they need not wait for one
+// another.
 struct Frag4 {
   uint32_t hi[4], lo[4];
 };
-__device__ __forceinline__ void mma_split(float (&d)[4], const Frag4& a, uint32_t bh0, uint32_t bh1, uint32_t bl0,
-                                          uint32_t bl1) {
-  mma16816_bf16_nv(d, a.lo[0], a.lo[1], a.lo[2], a.lo[3], bh0, bh1);
-  mma16816_bf16_nv(d, a.hi[0], a.hi[1], a.hi[2], a.hi[3], bl0, bl1);
-  mma16816_bf16_nv(d, a.hi[0], a.hi[1], a.hi[2], a.hi[3], bh0, bh1);
-}
+struct Tile {
+  float hh[4], hl[4], lh[4];
+  __device__ __forceinline__ Tile() {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) hh[e] = hl[e] = lh[e] = 0.f;
+  }
+  __device__ __forceinline__ void add(const Frag4& a, uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1) {
+    mma16816_bf16_nv(lh, a.lo[0], a.lo[1], a.lo[2], a.lo[3], bh0, bh1);
+    mma16816_bf16_nv(hl, a.hi[0], a.hi[1], a.hi[2], a.hi[3], bl0, bl1);
+    mma16816_bf16_nv(hh, a.hi[0], a.hi[1], a.hi[2], a.hi[3], bh0, bh1);
+  }
+  __device__ __forceinline__ float at(int e) const { return hh[e] + (hl[e] + lh[e]); }
+};
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], const void* p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -223,50 +224,53 @@ __device__ __forceinline__ Frag4 right_frags(const unsigned char* hi, const unsi
   return f;
 }
 // Two neighbouring result tiles as the next product's left operand.
-__device__ __forceinline__ Frag4 left_of(const float (&d0)[4], const float (&d1)[4]) {
+__device__ __forceinline__ Frag4 left_of(const Tile& d0, const Tile& d1) {
   Frag4 f;
-  split_pair(d0[0], d0[1], f.hi[0], f.lo[0]);
-  split_pair(d0[2], d0[3], f.hi[1], f.lo[1]);
-  split_pair(d1[0], d1[1], f.hi[2], f.lo[2]);
-  split_pair(d1[2], d1[3], f.hi[3], f.lo[3]);
+  split_pair(d0.at(0), d0.at(1), f.hi[0], f.lo[0]);
+  split_pair(d0.at(2), d0.at(3), f.hi[1], f.lo[1]);
+  split_pair(d1.at(0), d1.at(1), f.hi[2], f.lo[2]);
+  split_pair(d1.at(2), d1.at(3), f.hi[3], f.lo[3]);
   return f;
 }
-// A result tile at (row, col) of T, negated, and of T''.
-__device__ __forceinline__ void put_t(unsigned char* tb, const Gates& g, int row, int col, const float (&d)[4], int lane) {
-  const int c = col + 2 * (lane & 3);
+// A result tile at (row, col) of T, negated, and of T''.  (Here and below
+// everything is read before the first store: the compiler keeps the order of
+// a store and the loads behind it.)
+__device__ __forceinline__ void put_t(unsigned char* tb, const Gates& g, int row, int col, const Tile& d, int lane) {
+  const int c = col + 2 * (lane & 3), r = row + (lane >> 2);
   const float2 b = *reinterpret_cast<const float2*>(g.b + c);
+  const float f[2] = {-g.dec[r], -g.dec[r + 8]};
+  uint32_t h[4], l[4];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int r = row + 8 * e + (lane >> 2);
-    const float f = -g.dec[r];
-    const uint32_t at = sw128_off(r, c);
-    uint32_t h, l;
-    split_pair(-d[2 * e], -d[2 * e + 1], h, l);
-    *reinterpret_cast<uint32_t*>(tb + at) = h;
-    *reinterpret_cast<uint32_t*>(tb + kBox + at) = l;
-    split_pair(f * b.x * d[2 * e], f * b.y * d[2 * e + 1], h, l);
-    *reinterpret_cast<uint32_t*>(tb + 2 * kBox + at) = h;
-    *reinterpret_cast<uint32_t*>(tb + 3 * kBox + at) = l;
+    const float x = d.at(2 * e), y = d.at(2 * e + 1);
+    split_pair(-x, -y, h[e], l[e]);
+    split_pair(f[e] * b.x * x, f[e] * b.y * y, h[2 + e], l[2 + e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    unsigned char* t = tb + (e >> 1) * 2 * kBox + sw128_off(r + 8 * (e & 1), c);
+    *reinterpret_cast<uint32_t*>(t) = h[e];
+    *reinterpret_cast<uint32_t*>(t + kBox) = l[e];
   }
 }
 
-// The operands T = (I + A)^-1 and T'' = diag(g_C/g_n) T diag(b): the diagonal
-// blocks of 16 by substitution, a column per lane; then blocks of 32 and of 64
-// by T21 = -(T22 A21) T11 on warp-level MMAs.  Blocks right of the diagonal
-// ones stay as they are (zero).  Every preparation thread; ends without a
-// barrier.
-__device__ __forceinline__ void invert(const float* D, const unsigned char* ab, unsigned char* tb, const Gates& g, int p) {
+// The operands T = (I + A)^-1 and T'' = diag(g_C/g_n) T diag(b): diagonal
+// blocks of 8 by substitution, a column per lane; blocks of 16 by
+// T21 = -T22 (A21 T11), a value per lane; blocks of 32 and of 64 by
+// -(T22 A21) T11 on warp-level MMAs.  What lies right of the diagonal blocks
+// stays as it is (zero).  Every preparation thread; ends without a barrier.
+__device__ __forceinline__ void invert(float* D, const unsigned char* ab, unsigned char* tb, const Gates& g, int p) {
   const int w = p >> 5, lane = p & 31;
-  if (w < 4) {
-    const float* B = D + 16 * w * kPitchD;
-    const int j = lane & 15;
-    float x[16];
+  const int j = lane & 7, q = lane >> 3;
+  {
+    float* B = D + 8 * w * kPitchD + 8 * (w & 1);
+    float x[8];
 #pragma unroll
-    for (int n = 0; n < 16; ++n) x[n] = n == j ? 1.f : 0.f;
+    for (int n = 0; n < 8; ++n) x[n] = n == j ? 1.f : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
+    for (int i = 0; i < 8; i += 4) {
 #pragma unroll
-      for (int n = i + 1; n < 16; ++n) {
+      for (int n = i + 1; n < 8; ++n) {
         const float4 a = *reinterpret_cast<const float4*>(B + n * kPitchD + i);
         x[n] = fmaf(-a.x, x[i], x[n]);
         if (n > i + 1) x[n] = fmaf(-a.y, x[i + 1], x[n]);
@@ -274,32 +278,73 @@ __device__ __forceinline__ void invert(const float* D, const unsigned char* ab, 
         if (n > i + 3) x[n] = fmaf(-a.w, x[i + 3], x[n]);
       }
     }
-    // lanes 0-15 write the columns of T, lanes 16-31 those of T''
-    const bool second = lane >= 16;
-    const float b = g.b[16 * w + j];
-    unsigned char* out = tb + (second ? 2 * kBox : 0u);
+    __syncwarp();
+    // f32 for the next step; and each group of eight lanes fills one tile
+    const float b = q < 2 ? 1.f : g.b[8 * w + j];
+    const float4 u = *reinterpret_cast<const float4*>(g.dec + 8 * w), v = *reinterpret_cast<const float4*>(g.dec + 8 * w + 4);
+    const float dec[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    __nv_bfloat16 y[8];
 #pragma unroll
-    for (int n = 0; n < 16; ++n) {
-      const float y = second ? x[n] * b * g.dec[16 * w + n] : x[n];
-      const __nv_bfloat16 h = __float2bfloat16_rn(y), l = __float2bfloat16_rn(y - __bfloat162float(h));
-      const uint32_t at = sw128_off(16 * w + n, 16 * w + j);
-      *reinterpret_cast<__nv_bfloat16*>(out + at) = h;
-      *reinterpret_cast<__nv_bfloat16*>(out + kBox + at) = l;
+    for (int n = 0; n < 8; ++n) {
+      const float f = q < 2 ? x[n] : x[n] * b * dec[n];
+      y[n] = __float2bfloat16_rn(f);
+      if (q & 1) y[n] = __float2bfloat16_rn(f - __bfloat162float(y[n]));
     }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      if (q == 0) B[n * kPitchD + j] = x[n];
+      *reinterpret_cast<__nv_bfloat16*>(tb + q * kBox + sw128_off(8 * w + n, 8 * w + j)) = y[n];
+    }
+  }
+  prep_sync();
+  {
+    // rows 8 + 4 (w mod 2) .. of block w / 2, left half: lane (q, j) forms
+    // rows q and q + 4 of A21 T11, then its own row of T21
+    const float* R = D + 16 * (w >> 1) * kPitchD;
+    float p0 = 0.f, p1 = 0.f, t = 0.f;
+    const float* r0 = R + (8 + q) * kPitchD;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(r0 + i);
+      const float4 c = *reinterpret_cast<const float4*>(r0 + 4 * kPitchD + i);
+      const float as[4] = {a.x, a.y, a.z, a.w}, cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float y = R[(i + e) * kPitchD + j];
+        p0 = fmaf(as[e], y, p0);
+        p1 = fmaf(cs[e], y, p1);
+      }
+    }
+    const int row = 8 + 4 * (w & 1) + q;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(R + row * kPitchD + 8 + i);
+      const float as[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t = fmaf(-as[e], __shfl_sync(0xffffffffu, i == 0 ? p0 : p1, 8 * e + j), t);
+    }
+    const int r = 16 * (w >> 1) + row, c = 16 * (w >> 1) + j;
+    const float t2 = t * g.b[c] * g.dec[r];
+    const __nv_bfloat16 h = __float2bfloat16_rn(t), h2 = __float2bfloat16_rn(t2);
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(tb + sw128_off(r, c));
+    out[0] = h;
+    out[kBox / 2] = __float2bfloat16_rn(t - __bfloat162float(h));
+    out[kBox] = h2;
+    out[3 * kBox / 2] = __float2bfloat16_rn(t2 - __bfloat162float(h2));
   }
   prep_sync();
   if ((w & 3) < 2) {
     // blocks of 32: 8 columns of T21 per warp
     const int r0 = 32 * (w >> 2), t = w & 3;
-    float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+    Tile d0, d1, d;
     const Frag4 t22 = left_frag(tb, tb + kBox, r0 + 16, r0 + 16, lane);
     const Frag4 a21 = right_frags(ab, ab + kBox, r0 + 16, r0, lane);
     const Frag4 t11 = right_frags(tb, tb + kBox, r0, r0, lane);
-    mma_split(d0, t22, a21.hi[0], a21.hi[1], a21.lo[0], a21.lo[1]);
-    mma_split(d1, t22, a21.hi[2], a21.hi[3], a21.lo[2], a21.lo[3]);
+    d0.add(t22, a21.hi[0], a21.hi[1], a21.lo[0], a21.lo[1]);
+    d1.add(t22, a21.hi[2], a21.hi[3], a21.lo[2], a21.lo[3]);
     const Frag4 l = left_of(d0, d1);
-    if (t == 0) mma_split(d, l, t11.hi[0], t11.hi[1], t11.lo[0], t11.lo[1]);
-    else mma_split(d, l, t11.hi[2], t11.hi[3], t11.lo[2], t11.lo[3]);
+    if (t == 0) d.add(l, t11.hi[0], t11.hi[1], t11.lo[0], t11.lo[1]);
+    else d.add(l, t11.hi[2], t11.hi[3], t11.lo[2], t11.lo[3]);
     put_t(tb, g, r0 + 16, r0 + 8 * t, d, lane);
   }
   prep_sync();
@@ -308,53 +353,67 @@ __device__ __forceinline__ void invert(const float* D, const unsigned char* ab, 
     // T22 and T11 are lower triangular: only blocks k <= m of the one, k >= t/2
     // of the other.
     const int m = w & 1, t = w >> 1;
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    Tile d;
     Frag4 t22[2];
     t22[0] = left_frag(tb, tb + kBox, 32 + 16 * m, 32, lane);
     if (m == 1) t22[1] = left_frag(tb, tb + kBox, 48, 48, lane);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (k >= (t >> 1)) {
-        float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+        Tile d0, d1;
+        const Frag4 t11 = right_frags(tb, tb + kBox, 16 * k, 16 * (t >> 1), lane);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
           if (kk <= m) {
             const Frag4 a21 = right_frags(ab, ab + kBox, 32 + 16 * kk, 16 * k, lane);
-            mma_split(d0, t22[kk], a21.hi[0], a21.hi[1], a21.lo[0], a21.lo[1]);
-            mma_split(d1, t22[kk], a21.hi[2], a21.hi[3], a21.lo[2], a21.lo[3]);
+            d0.add(t22[kk], a21.hi[0], a21.hi[1], a21.lo[0], a21.lo[1]);
+            d1.add(t22[kk], a21.hi[2], a21.hi[3], a21.lo[2], a21.lo[3]);
           }
         }
         const Frag4 l = left_of(d0, d1);
-        const Frag4 t11 = right_frags(tb, tb + kBox, 16 * k, 16 * (t >> 1), lane);
-        if ((t & 1) == 0) mma_split(d, l, t11.hi[0], t11.hi[1], t11.lo[0], t11.lo[1]);
-        else mma_split(d, l, t11.hi[2], t11.hi[3], t11.lo[2], t11.lo[3]);
+        if ((t & 1) == 0) d.add(l, t11.hi[0], t11.hi[1], t11.lo[0], t11.lo[1]);
+        else d.add(l, t11.hi[2], t11.hi[3], t11.lo[2], t11.lo[3]);
       }
     }
     put_t(tb, g, 32 + 16 * m, 8 * t, d, lane);
   }
 }
 
-// The 16 x 8 tile (row 16 m, column 8 t) of MT = M T diag(b).
+// The 16 x 8 tiles (row 16 m, columns 8 t and 8 t + 32) of MT = M T diag(b);
+// the second only where it reaches the diagonal blocks.
 __device__ __forceinline__ void put_mt(unsigned char* mtb, const unsigned char* mb, const unsigned char* tb,
                                        const Gates& g, int m, int t, int lane) {
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int k = t >> 1; k <= m; ++k) {
+  Tile d[2];
+  const int second = t + 4 <= 2 * m + 1 ? (t + 4) >> 1 : 4;  // its first block of the contraction
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k < (t >> 1) || k > m) continue;
     const Frag4 l = left_frag(mb, mb + kBox, 16 * m, 16 * k, lane);
     // k rows of 8 columns: lanes 0-15 address the hi tile, 16-31 the lo tile
+    const unsigned char* at = tb + (lane >> 4) * kBox;
     uint32_t r[4];
-    ldsm_x4_trans(r, tb + (lane >> 4) * kBox + sw128_off(16 * k + (lane & 15), 8 * t));
-    mma_split(d, l, r[0], r[1], r[2], r[3]);
+    ldsm_x4_trans(r, at + sw128_off(16 * k + (lane & 15), 8 * t));
+    if (k >= second) {
+      uint32_t r2[4];
+      ldsm_x4_trans(r2, at + sw128_off(16 * k + (lane & 15), 8 * t + 32));
+      d[1].add(l, r2[0], r2[1], r2[2], r2[3]);
+    }
+    d[0].add(l, r[0], r[1], r[2], r[3]);
   }
-  const int c = 8 * t + 2 * (lane & 3);
-  const float2 b = *reinterpret_cast<const float2*>(g.b + c);
+  const int c = 8 * t + 2 * (lane & 3), row = 16 * m + (lane >> 2);
+  const float2 b0 = *reinterpret_cast<const float2*>(g.b + c), b1 = *reinterpret_cast<const float2*>(g.b + c + 32);
+  uint32_t h[4], l[4];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const uint32_t at = sw128_off(16 * m + 8 * e + (lane >> 2), c);
-    uint32_t h, l;
-    split_pair(b.x * d[2 * e], b.y * d[2 * e + 1], h, l);
-    *reinterpret_cast<uint32_t*>(mtb + at) = h;
-    *reinterpret_cast<uint32_t*>(mtb + kBox + at) = l;
+  for (int e = 0; e < 4; ++e) {
+    const float2 b = e < 2 ? b0 : b1;
+    split_pair(b.x * d[e >> 1].at(2 * (e & 1)), b.y * d[e >> 1].at(2 * (e & 1) + 1), h[e], l[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (e >= 2 && second == 4) continue;
+    unsigned char* out = mtb + sw128_off(row + 8 * (e & 1), c + 32 * (e >> 1));
+    *reinterpret_cast<uint32_t*>(out) = h[e];
+    *reinterpret_cast<uint32_t*>(out + kBox) = l[e];
   }
 }
 
@@ -507,13 +566,21 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
     tc_fence_after_sync();
     const bool more = c + 1 < nchunk;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      uint32_t x[16];
+    for (int b = 0; b < 4; b += 2) {
+      uint32_t x[16], y[16];
       tmem_ld16_async(tm + kColD + 64 * half + 16 * b, x);
+      tmem_ld16_async(tm + kColD + 64 * half + 16 * b + 16, y);
       tmem_wait16(x);
+      tmem_wait16(y);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) S[16 * b + e] = fmaf(gC, S[16 * b + e], __uint_as_float(x[e]));
-      if (more) put_state16(tm, half, b, S);
+      for (int e = 0; e < 16; ++e) {
+        S[16 * b + e] = fmaf(gC, S[16 * b + e], __uint_as_float(x[e]));
+        S[16 * b + 16 + e] = fmaf(gC, S[16 * b + 16 + e], __uint_as_float(y[e]));
+      }
+      if (more) {
+        put_state16(tm, half, b, S);
+        put_state16(tm, half, b + 1, S);
+      }
     }
     if (more) {
       tmem_wait_st();
@@ -656,6 +723,42 @@ __device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, c
   }
 }
 
+// [K;Q] K^T of chunk c (one elected lane).
+__device__ __forceinline__ void issue_gram(ChunkSmem& cs, unsigned char* base, int c) {
+  constexpr uint32_t id = idesc_bf16_f32(128, kC);
+  const uint64_t s0 = smem_desc_sw128(smem_addr(base + (c & 1) * kStageBytes), 1024);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint64_t at = s0 + (((k >> 2) * 2 * kBox + (k & 3) * 32) >> 4);
+    mma_bf16(cs.tmem + kColG, at, at, id, k > 0);
+  }
+  mma_commit(&cs.gram_done);
+}
+
+// One warp: the preparation's other products, once T and the next chunk's K
+// and Q are there.
+__device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, int nchunk) {
+  constexpr uint32_t idk = idesc_bf16_f32(128, kC) | kAmajorMN | kBmajorMN;
+  const uint64_t t0 = smem_desc_sw128_mn(smem_addr(base + kOffT + 2 * kBox), kBox);
+  for (int c = 0; c < nchunk; ++c) {
+    const uint64_t k0 = smem_desc_sw128_mn(smem_addr(base + (c & 1) * kStageBytes), 2 * kBox);
+    const bool ok = wait(cs, &cs.t_ready, c);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    if (elect_one()) {
+      tc_fence_after_sync();
+      // kt^T[dk][i] = sum_n K[n][dk] T''[n][i]
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + k * 128, idk, k > 0);
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + (kBox >> 4) + k * 128, idk, 1u);
+      }
+      mma_commit(&cs.prep_done);
+      if (c + 1 < nchunk) issue_gram(cs, base, c + 1);
+    }
+    __syncwarp();
+  }
+}
+
 // The preparation warps: T, MT and kt of every chunk, one chunk ahead of the
 // state, and [K;Q] K^T one more chunk ahead.  Warps p and p + 4 share a quarter
 // of the lanes (rows), half of the columns each.
@@ -686,27 +789,16 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
     }
     return there;
   };
-  auto issue_gram = [&](int c) {  // one elected lane
-    constexpr uint32_t id = idesc_bf16_f32(128, kC);
-    const uint64_t s0 = smem_desc_sw128(smem_addr(base + (c & 1) * kStageBytes), 1024);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint64_t at = s0 + (((k >> 2) * 2 * kBox + (k & 3) * 32) >> 4);
-      mma_bf16(cs.tmem + kColG, at, at, id, k > 0);
-    }
-    mma_commit(&cs.gram_done);
-  };
   bool ok = stage_in(0);
   if (prep_failed(ok)) return;
   if (first && elect_one()) {
     tc_fence_after_sync();
-    issue_gram(0);
+    issue_gram(cs, base, 0);
   }
   __syncwarp();
   for (int c = 0; c < nchunk; ++c) {
     const int sg = c & 1;
     const uint32_t ph2 = c >> 1;
-    unsigned char* st = base + sg * kStageBytes;
     const Gates& g = cs.gates[sg];
     if (!wait(cs, &cs.gates_ready[sg], ph2) || !wait(cs, &cs.gram_done, c)) ok = false;
     prep_sync();  // the last chunk's M has been read
@@ -724,28 +816,33 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
         uint32_t x[16];
         tmem_ld16_async(tm + kColG + 32 * hh + 16 * b, x);
         tmem_wait16(x);
+        float as[16], y[16];
 #pragma unroll
-        for (int j = 1; j >= 0; --j) {
-          const int i0 = 16 * b + 8 * j;
-          const float4 u = *reinterpret_cast<const float4*>(g.a + 32 * hh + i0);
-          const float4 v = *reinterpret_cast<const float4*>(g.a + 32 * hh + i0 + 4);
-          const float as[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-          float y[8];
+        for (int j = 0; j < 4; ++j) {
+          const float4 u = *reinterpret_cast<const float4*>(g.a + 32 * hh + 16 * b + 4 * j);
+          as[4 * j] = u.x, as[4 * j + 1] = u.y, as[4 * j + 2] = u.z, as[4 * j + 3] = u.w;
+        }
 #pragma unroll
-          for (int k = 7; k >= 0; --k) {
-            if (i0 + k == dl) f = f0;
-            y[k] = f * __uint_as_float(x[8 * j + k]);
-            f *= as[k];
+        for (int k = 15; k >= 0; --k) {
+          if (16 * b + k == dl) f = f0;
+          y[k] = f * __uint_as_float(x[k]);
+          f *= as[k];
+        }
+        if (isM || 2 * hh + b < (n >> 4)) {
+          unsigned char* tile = isM ? mb : ab;
+          uint32_t h[8], l[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) split_pair(y[2 * k], y[2 * k + 1], h[k], l[k]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint4* out = operand_piece(tile, n, 4 * hh + 2 * b + j);
+            *out = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+            out[kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
           }
-          if (isM) {
-            put_piece(mb, mb + kBox, n, 4 * hh + 2 * b + j, y);
-          } else if (2 * hh + b < (n >> 4)) {
-            put_piece(ab, ab + kBox, n, 4 * hh + 2 * b + j, y);
-          } else if (2 * hh + b == (n >> 4)) {
-            float4* r = reinterpret_cast<float4*>(D + n * kPitchD + 8 * j);
-            r[0] = make_float4(y[0], y[1], y[2], y[3]);
-            r[1] = make_float4(y[4], y[5], y[6], y[7]);
-          }
+        } else if (2 * hh + b == (n >> 4)) {
+          float4* r = reinterpret_cast<float4*>(D + n * kPitchD);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
         }
       }
     }
@@ -754,22 +851,8 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
     invert(D, ab, tb, g, p);
     if (c + 1 < nchunk && !stage_in(c + 1)) ok = false;
     fence_proxy_async_smem();
+    warp_arrive(&cs.t_ready);
     prep_sync();
-    if (first && elect_one()) {
-      tc_fence_after_sync();
-      // kt^T[dk][i] = sum_n K[n][dk] T''[n][i]; then the next chunk's [K;Q] K^T
-      constexpr uint32_t idk = idesc_bf16_f32(128, kC) | kAmajorMN | kBmajorMN;
-      const uint64_t k0 = smem_desc_sw128_mn(smem_addr(st), 2 * kBox);
-      const uint64_t t0 = smem_desc_sw128_mn(smem_addr(tb + 2 * kBox), kBox);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + k * 128, idk, k > 0);
-        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + (kBox >> 4) + k * 128, idk, 1u);
-      }
-      mma_commit(&cs.prep_done);
-      if (c + 1 < nchunk) issue_gram(c + 1);
-    }
-    __syncwarp();
     // the last chunk's kt and MT have been read
     if (c > 0 && !wait(cs, &cs.o2_done, c - 1)) ok = false;
     __syncwarp();
@@ -778,11 +861,9 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
     const int u = w & 3;
     if (w < 4) {
       put_mt(mtb, mb, tb, g, 3, u, lane);
-      put_mt(mtb, mb, tb, g, 3, u + 4, lane);
       if (u >= 2) put_mt(mtb, mb, tb, g, 0, u - 2, lane);
     } else {
       put_mt(mtb, mb, tb, g, 2, u, lane);
-      if (u < 2) put_mt(mtb, mb, tb, g, 2, u + 4, lane);
       put_mt(mtb, mb, tb, g, 1, u ^ 2, lane);
     }
     warp_arrive(&cs.gates_free[sg]);
@@ -794,12 +875,14 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
       uint32_t x[16];
       tmem_ld16_async(tm + kColK + 32 * hh + 16 * b, x);
       tmem_wait16(x);
+      uint32_t h[8], l[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) split_pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), h[k], l[k]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float y[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(x[8 * j + k]);
-        put_piece(ktb, ktb + 2 * kBox, row, 4 * hh + 2 * b + j, y);
+        uint4* out = operand_piece(ktb, row, 4 * hh + 2 * b + j);
+        *out = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+        out[2 * kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
       }
     }
     tc_fence_before_sync();
@@ -975,8 +1058,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&cs.gates_free[i], kStateWarps + kPrepWarps + kOutWarps);
       mbar_init(&cs.s_ready[i], kStateWarps / 2);
       mbar_init(&cs.d2_done[i], 1);
-      mbar_init(&cs.drain[i], 1);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(&cs.drain[i], 1);
+    mbar_init(&cs.t_ready, kPrepWarps);
     mbar_init(&cs.fix, kPrepWarps);
     mbar_init(&cs.gram_done, 1);
     mbar_init(&cs.prep_done, 1);
@@ -1018,6 +1102,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((t & 31) == 0) run_load(&map_q, &map_k, &map_v, cs, base, q, h / (a.H / a.Hk), h, nchunk);
     } else if (warp == kGateWarp) {
       run_gates(a, cs, q, h, nchunk);
+    } else {
+      run_issue(cs, base, nchunk);
+      drain(&cs.drain[2]);
     }
   }
   __syncwarp();
