@@ -62,7 +62,7 @@ static_assert(2 * kStateRegs + 2 * kPrepRegs + kOutRegs + kMiscRegs <= 6 * kLaun
 constexpr uint32_t kColS = 0;                // S: hi in 64 columns, lo in 64 (bf16 pairs)
 constexpr uint32_t kColW = 128;              // S k, then W (16 columns per 16 tokens: hi 8, lo 8)
 constexpr uint32_t kColO = 192;              // S q, then MT W
-constexpr uint32_t kColD = 256;              // sum W kt^T
+constexpr uint32_t kColD = 256;              // sum W kt^T; before that MT (lanes 64-127)
 constexpr uint32_t kColG = 384;              // [K;Q] K^T
 constexpr uint32_t kColK = 448;              // kt^T
 constexpr uint32_t kTmemCols = 512;
@@ -76,10 +76,10 @@ constexpr uint32_t kOffKt = 2 * kStageBytes;      // kt^T: 128 rows (dk) of 64 t
 constexpr uint32_t kOffMT = kOffKt + 4 * kBox;    // MT: 64 rows of 64 tokens, hi then lo
 constexpr uint32_t kOffM = kOffMT + 2 * kBox;     // M, hi then lo
 constexpr uint32_t kOffT = kOffM + 2 * kBox;      // T hi, lo, then T'' = diag(g_C/g_n) T diag(b) hi, lo
-constexpr uint32_t kOffA = kOffT + 4 * kBox;      // A left of its diagonal blocks of 16, hi then lo
-constexpr uint32_t kOffD = kOffA + 2 * kBox;      // A's diagonal blocks of 16: f32, rows of 20
-constexpr int kPitchD = 20;
-constexpr uint32_t kSmemBytes = kOffD + kC * kPitchD * 4 + 1024;
+constexpr uint32_t kOffA = kOffT + 4 * kBox;      // A21, hi then lo: rows 32-63; rows 0-31 take T22 A21
+constexpr uint32_t kOffX = kOffA + 2 * kBox;      // A's, then T's diagonal blocks of 32, f32
+constexpr int kPitchX = 36;
+constexpr uint32_t kSmemBytes = kOffX + kC * kPitchX * 4 + 1024;
 
 struct __align__(16) Gates {
   float a[kC], b[kC], g[kC];          // decay, write strength and the product of the decays up to every token
@@ -182,6 +182,98 @@ __device__ __forceinline__ void prep_sync() { named_bar_sync<1, kPrepThreads>();
 // them leave together, so that none is left at a barrier.
 __device__ __forceinline__ bool prep_failed(bool ok) { return named_bar_or<1, kPrepThreads>(!ok); }
 
+// out (row r, columns c ..) = sum over N of left (row r of L) times right
+// (rows of R, columns c ..), N a multiple of 4, V = 4 or 8 columns per lane;
+// all f32 in shared memory.
+template <int N, int V>
+__device__ __forceinline__ void dot_rows(const float* L, const float* R, float (&acc)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(L + i);
+    const float ls[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(R + (i + k) * kPitchX + e);
+        acc[e] = fmaf(ls[k], y.x, acc[e]);
+        acc[e + 1] = fmaf(ls[k], y.y, acc[e + 1]);
+        acc[e + 2] = fmaf(ls[k], y.z, acc[e + 2]);
+        acc[e + 3] = fmaf(ls[k], y.w, acc[e + 3]);
+      }
+    }
+  }
+}
+
+// The diagonal block of 32 at X (unit lower triangular, zeros above) becomes
+// its inverse, by one warp: blocks of 8 by substitution, a column per lane;
+// then of 16 and of 32 by T21 = -T22 (A21 T11).
+__device__ __forceinline__ void solve32(float* X, int lane) {
+  {
+    const int j = lane & 7;
+    float* B = X + 8 * (lane >> 3) * (kPitchX + 1);
+    float x[8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) x[n] = n == j ? 1.f : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      float4 a[8];
+#pragma unroll
+      for (int n = i + 1; n < 8; ++n) a[n] = *reinterpret_cast<const float4*>(B + n * kPitchX + i);
+#pragma unroll
+      for (int n = i + 1; n < 8; ++n) {
+        x[n] = fmaf(-a[n].x, x[i], x[n]);
+        if (n > i + 1) x[n] = fmaf(-a[n].y, x[i + 1], x[n]);
+        if (n > i + 2) x[n] = fmaf(-a[n].z, x[i + 2], x[n]);
+        if (n > i + 3) x[n] = fmaf(-a[n].w, x[i + 3], x[n]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < 8; ++n) B[n * kPitchX + j] = x[n];
+  }
+  __syncwarp();
+  {
+    const int r = 8 + ((lane & 15) >> 1), c = 4 * (lane & 1);
+    float* B = X + 16 * (lane >> 4) * (kPitchX + 1);
+    float4* out = reinterpret_cast<float4*>(B + r * kPitchX + c);
+    float t[4];
+    dot_rows<8, 4>(B + r * kPitchX, B + c, t);
+    __syncwarp();
+    *out = make_float4(t[0], t[1], t[2], t[3]);
+    __syncwarp();
+    dot_rows<8, 4>(B + r * kPitchX + 8, B + 8 * kPitchX + c, t);
+    __syncwarp();
+    *out = make_float4(-t[0], -t[1], -t[2], -t[3]);
+  }
+  __syncwarp();
+  {
+    const int r = 16 + (lane >> 1), c = 8 * (lane & 1);
+    float4* out = reinterpret_cast<float4*>(X + r * kPitchX + c);
+    float t[8];
+    dot_rows<16, 8>(X + r * kPitchX, X + c, t);
+    __syncwarp();
+    out[0] = make_float4(t[0], t[1], t[2], t[3]);
+    out[1] = make_float4(t[4], t[5], t[6], t[7]);
+    __syncwarp();
+    dot_rows<16, 8>(X + r * kPitchX + 16, X + 16 * kPitchX + c, t);
+    __syncwarp();
+    out[0] = make_float4(-t[0], -t[1], -t[2], -t[3]);
+    out[1] = make_float4(-t[4], -t[5], -t[6], -t[7]);
+  }
+}
+
+__device__ __forceinline__ void put_piece(unsigned char* hi, int row, int j, const float (&x)[8]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) split_pair(x[2 * e], x[2 * e + 1], h[e], l[e]);
+  uint4* out = operand_piece(hi, row, j);
+  out[0] = make_uint4(h[0], h[1], h[2], h[3]);
+  out[kBox / 16] = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 // A 16 x 8 result tile of warp-level products whose operands are hi and lo:
 // one accumulator per product of terms, so that they need not wait for one
 // another.
@@ -207,213 +299,85 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], const void* p) {
                : "r"(smem_addr(p)));
 }
 // The 16 x 16 block at (row, col) of an operand's hi and lo tiles as a left
-// operand, and as two right operands of 8 columns each (rows the contraction:
-// hi and lo of the first in [0..1], of the second in [2..3]).
-__device__ __forceinline__ Frag4 left_frag(const unsigned char* hi, const unsigned char* lo, int row, int col, int lane) {
+// operand; 16 rows (the contraction) and 8 columns of it as a right operand
+// (hi in [0..1], lo in [2..3]).
+__device__ __forceinline__ Frag4 left_frag(const unsigned char* hi, int row, int col, int lane) {
   const uint32_t at = sw128_off(row + (lane & 15), col + 8 * (lane >> 4));
   Frag4 f;
   ldsm_x4(f.hi, hi + at);
-  ldsm_x4(f.lo, lo + at);
+  ldsm_x4(f.lo, hi + kBox + at);
   return f;
 }
-__device__ __forceinline__ Frag4 right_frags(const unsigned char* hi, const unsigned char* lo, int row, int col, int lane) {
-  const uint32_t at = sw128_off(row + (lane & 15), col + 8 * (lane >> 4));
-  Frag4 f;
-  ldsm_x4_trans(f.hi, hi + at);
-  ldsm_x4_trans(f.lo, lo + at);
-  return f;
-}
-// Two neighbouring result tiles as the next product's left operand.
-__device__ __forceinline__ Frag4 left_of(const Tile& d0, const Tile& d1) {
-  Frag4 f;
-  split_pair(d0.at(0), d0.at(1), f.hi[0], f.lo[0]);
-  split_pair(d0.at(2), d0.at(3), f.hi[1], f.lo[1]);
-  split_pair(d1.at(0), d1.at(1), f.hi[2], f.lo[2]);
-  split_pair(d1.at(2), d1.at(3), f.hi[3], f.lo[3]);
-  return f;
-}
-// A result tile at (row, col) of T, negated, and of T''.  (Here and below
-// everything is read before the first store: the compiler keeps the order of
-// a store and the loads behind it.)
-__device__ __forceinline__ void put_t(unsigned char* tb, const Gates& g, int row, int col, const Tile& d, int lane) {
-  const int c = col + 2 * (lane & 3), r = row + (lane >> 2);
-  const float2 b = *reinterpret_cast<const float2*>(g.b + c);
-  const float f[2] = {-g.dec[r], -g.dec[r + 8]};
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float x = d.at(2 * e), y = d.at(2 * e + 1);
-    split_pair(-x, -y, h[e], l[e]);
-    split_pair(f[e] * b.x * x, f[e] * b.y * y, h[2 + e], l[2 + e]);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    unsigned char* t = tb + (e >> 1) * 2 * kBox + sw128_off(r + 8 * (e & 1), c);
-    *reinterpret_cast<uint32_t*>(t) = h[e];
-    *reinterpret_cast<uint32_t*>(t + kBox) = l[e];
-  }
+__device__ __forceinline__ void right_frag(uint32_t (&r)[4], const unsigned char* hi, int row, int col, int lane) {
+  ldsm_x4_trans(r, hi + (lane >> 4) * kBox + sw128_off(row + (lane & 15), col));
 }
 
-// The operands T = (I + A)^-1 and T'' = diag(g_C/g_n) T diag(b): diagonal
-// blocks of 8 by substitution, a column per lane; blocks of 16 by
-// T21 = -T22 (A21 T11), a value per lane; blocks of 32 and of 64 by
-// -(T22 A21) T11 on warp-level MMAs.  What lies right of the diagonal blocks
-// stays as it is (zero).  Every preparation thread; ends without a barrier.
-__device__ __forceinline__ void invert(float* D, const unsigned char* ab, unsigned char* tb, const Gates& g, int p) {
-  const int w = p >> 5, lane = p & 31;
-  const int j = lane & 7, q = lane >> 3;
+// The operands T and T'' = diag(g_C/g_n) T diag(b) from T's diagonal blocks of
+// 32 (in X) and A21: the lower left quarter T21 = -(T22 A21) T11 by warp-level
+// MMAs, a tile of 16 x 8 per warp.  (These take turns with the tcgen05
+// products; on FMAs the two products took 4500 cycles against 1500.)  The upper
+// right quarter stays zero in the tiles.
+__device__ __forceinline__ void solve64(const float* X, unsigned char* ab, unsigned char* tb, const Gates& g, int p) {
   {
-    float* B = D + 8 * w * kPitchD + 8 * (w & 1);
-    float x[8];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) x[n] = n == j ? 1.f : 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-#pragma unroll
-      for (int n = i + 1; n < 8; ++n) {
-        const float4 a = *reinterpret_cast<const float4*>(B + n * kPitchD + i);
-        x[n] = fmaf(-a.x, x[i], x[n]);
-        if (n > i + 1) x[n] = fmaf(-a.y, x[i + 1], x[n]);
-        if (n > i + 2) x[n] = fmaf(-a.z, x[i + 2], x[n]);
-        if (n > i + 3) x[n] = fmaf(-a.w, x[i + 3], x[n]);
-      }
-    }
-    __syncwarp();
-    // f32 for the next step; and each group of eight lanes fills one tile
-    const float b = q < 2 ? 1.f : g.b[8 * w + j];
-    const float4 u = *reinterpret_cast<const float4*>(g.dec + 8 * w), v = *reinterpret_cast<const float4*>(g.dec + 8 * w + 4);
-    const float dec[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    __nv_bfloat16 y[8];
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const float f = q < 2 ? x[n] : x[n] * b * dec[n];
-      y[n] = __float2bfloat16_rn(f);
-      if (q & 1) y[n] = __float2bfloat16_rn(f - __bfloat162float(y[n]));
-    }
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      if (q == 0) B[n * kPitchD + j] = x[n];
-      *reinterpret_cast<__nv_bfloat16*>(tb + q * kBox + sw128_off(8 * w + n, 8 * w + j)) = y[n];
-    }
+    // the diagonal blocks: eight values per thread
+    const int r = p >> 2, c = 8 * (p & 3), col = (r & 32) + c;
+    const float dec = g.dec[r];
+    const float4 u = *reinterpret_cast<const float4*>(X + r * kPitchX + c);
+    const float4 v = *reinterpret_cast<const float4*>(X + r * kPitchX + c + 4);
+    const float4 b0 = *reinterpret_cast<const float4*>(g.b + col), b1 = *reinterpret_cast<const float4*>(g.b + col + 4);
+    const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    const float y[8] = {dec * b0.x * u.x, dec * b0.y * u.y, dec * b0.z * u.z, dec * b0.w * u.w,
+                        dec * b1.x * v.x, dec * b1.y * v.y, dec * b1.z * v.z, dec * b1.w * v.w};
+    put_piece(tb, r, col / 8, x);
+    put_piece(tb + 2 * kBox, r, col / 8, y);
   }
   prep_sync();
+  // T22 and T11 are lower triangular: only blocks k <= m of the one, k >= t/2
+  // of the other
+  const int lane = p & 31, m = (p >> 5) & 1, t = p >> 6;
+  const int at = lane >> 2, c = 8 * t + 2 * (lane & 3);
   {
-    // rows 8 + 4 (w mod 2) .. of block w / 2, left half: lane (q, j) forms
-    // rows q and q + 4 of A21 T11, then its own row of T21
-    const float* R = D + 16 * (w >> 1) * kPitchD;
-    float p0 = 0.f, p1 = 0.f, t = 0.f;
-    const float* r0 = R + (8 + q) * kPitchD;
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(r0 + i);
-      const float4 c = *reinterpret_cast<const float4*>(r0 + 4 * kPitchD + i);
-      const float as[4] = {a.x, a.y, a.z, a.w}, cs[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float y = R[(i + e) * kPitchD + j];
-        p0 = fmaf(as[e], y, p0);
-        p1 = fmaf(cs[e], y, p1);
-      }
-    }
-    const int row = 8 + 4 * (w & 1) + q;
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(R + row * kPitchD + 8 + i);
-      const float as[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t = fmaf(-as[e], __shfl_sync(0xffffffffu, i == 0 ? p0 : p1, 8 * e + j), t);
-    }
-    const int r = 16 * (w >> 1) + row, c = 16 * (w >> 1) + j;
-    const float t2 = t * g.b[c] * g.dec[r];
-    const __nv_bfloat16 h = __float2bfloat16_rn(t), h2 = __float2bfloat16_rn(t2);
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(tb + sw128_off(r, c));
-    out[0] = h;
-    out[kBox / 2] = __float2bfloat16_rn(t - __bfloat162float(h));
-    out[kBox] = h2;
-    out[3 * kBox / 2] = __float2bfloat16_rn(t2 - __bfloat162float(h2));
-  }
-  prep_sync();
-  if ((w & 3) < 2) {
-    // blocks of 32: 8 columns of T21 per warp
-    const int r0 = 32 * (w >> 2), t = w & 3;
-    Tile d0, d1, d;
-    const Frag4 t22 = left_frag(tb, tb + kBox, r0 + 16, r0 + 16, lane);
-    const Frag4 a21 = right_frags(ab, ab + kBox, r0 + 16, r0, lane);
-    const Frag4 t11 = right_frags(tb, tb + kBox, r0, r0, lane);
-    d0.add(t22, a21.hi[0], a21.hi[1], a21.lo[0], a21.lo[1]);
-    d1.add(t22, a21.hi[2], a21.hi[3], a21.lo[2], a21.lo[3]);
-    const Frag4 l = left_of(d0, d1);
-    if (t == 0) d.add(l, t11.hi[0], t11.hi[1], t11.lo[0], t11.lo[1]);
-    else d.add(l, t11.hi[2], t11.hi[3], t11.lo[2], t11.lo[3]);
-    put_t(tb, g, r0 + 16, r0 + 8 * t, d, lane);
-  }
-  prep_sync();
-  {
-    // the lower left quarter: 16 rows (m) and 8 columns (t) of it per warp.
-    // T22 and T11 are lower triangular: only blocks k <= m of the one, k >= t/2
-    // of the other.
-    const int m = w & 1, t = w >> 1;
     Tile d;
-    Frag4 t22[2];
-    t22[0] = left_frag(tb, tb + kBox, 32 + 16 * m, 32, lane);
-    if (m == 1) t22[1] = left_frag(tb, tb + kBox, 48, 48, lane);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (k >= (t >> 1)) {
-        Tile d0, d1;
-        const Frag4 t11 = right_frags(tb, tb + kBox, 16 * k, 16 * (t >> 1), lane);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          if (kk <= m) {
-            const Frag4 a21 = right_frags(ab, ab + kBox, 32 + 16 * kk, 16 * k, lane);
-            d0.add(t22[kk], a21.hi[0], a21.hi[1], a21.lo[0], a21.lo[1]);
-            d1.add(t22[kk], a21.hi[2], a21.hi[3], a21.lo[2], a21.lo[3]);
-          }
-        }
-        const Frag4 l = left_of(d0, d1);
-        if ((t & 1) == 0) d.add(l, t11.hi[0], t11.hi[1], t11.lo[0], t11.lo[1]);
-        else d.add(l, t11.hi[2], t11.hi[3], t11.lo[2], t11.lo[3]);
-      }
+      if (k > m) continue;
+      uint32_t r[4];
+      right_frag(r, ab, 32 + 16 * k, 8 * t, lane);
+      d.add(left_frag(tb, 32 + 16 * m, 32 + 16 * k, lane), r[0], r[1], r[2], r[3]);
     }
-    put_t(tb, g, 32 + 16 * m, 8 * t, d, lane);
-  }
-}
-
-// The 16 x 8 tiles (row 16 m, columns 8 t and 8 t + 32) of MT = M T diag(b);
-// the second only where it reaches the diagonal blocks.
-__device__ __forceinline__ void put_mt(unsigned char* mtb, const unsigned char* mb, const unsigned char* tb,
-                                       const Gates& g, int m, int t, int lane) {
-  Tile d[2];
-  const int second = t + 4 <= 2 * m + 1 ? (t + 4) >> 1 : 4;  // its first block of the contraction
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (k < (t >> 1) || k > m) continue;
-    const Frag4 l = left_frag(mb, mb + kBox, 16 * m, 16 * k, lane);
-    // k rows of 8 columns: lanes 0-15 address the hi tile, 16-31 the lo tile
-    const unsigned char* at = tb + (lane >> 4) * kBox;
-    uint32_t r[4];
-    ldsm_x4_trans(r, at + sw128_off(16 * k + (lane & 15), 8 * t));
-    if (k >= second) {
-      uint32_t r2[4];
-      ldsm_x4_trans(r2, at + sw128_off(16 * k + (lane & 15), 8 * t + 32));
-      d[1].add(l, r2[0], r2[1], r2[2], r2[3]);
+    for (int e = 0; e < 2; ++e) {
+      uint32_t h, l;
+      split_pair(d.at(2 * e), d.at(2 * e + 1), h, l);
+      unsigned char* out = ab + sw128_off(16 * m + 8 * e + at, c);
+      *reinterpret_cast<uint32_t*>(out) = h;
+      *reinterpret_cast<uint32_t*>(out + kBox) = l;
     }
-    d[0].add(l, r[0], r[1], r[2], r[3]);
   }
-  const int c = 8 * t + 2 * (lane & 3), row = 16 * m + (lane >> 2);
-  const float2 b0 = *reinterpret_cast<const float2*>(g.b + c), b1 = *reinterpret_cast<const float2*>(g.b + c + 32);
-  uint32_t h[4], l[4];
+  prep_sync();
+  {
+    const float2 b = *reinterpret_cast<const float2*>(g.b + c);
+    const float dec[2] = {-g.dec[32 + 16 * m + at], -g.dec[40 + 16 * m + at]};
+    Tile d;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 b = e < 2 ? b0 : b1;
-    split_pair(b.x * d[e >> 1].at(2 * (e & 1)), b.y * d[e >> 1].at(2 * (e & 1) + 1), h[e], l[e]);
-  }
+    for (int k = 0; k < 2; ++k) {
+      if (k < (t >> 1)) continue;
+      uint32_t r[4];
+      right_frag(r, tb, 16 * k, 8 * t, lane);
+      d.add(left_frag(ab, 16 * m, 16 * k, lane), r[0], r[1], r[2], r[3]);
+    }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (e >= 2 && second == 4) continue;
-    unsigned char* out = mtb + sw128_off(row + 8 * (e & 1), c + 32 * (e >> 1));
-    *reinterpret_cast<uint32_t*>(out) = h[e];
-    *reinterpret_cast<uint32_t*>(out + kBox) = l[e];
+    for (int e = 0; e < 2; ++e) {
+      const float x = d.at(2 * e), y = d.at(2 * e + 1);
+      uint32_t h, l, h2, l2;
+      split_pair(-x, -y, h, l);
+      split_pair(dec[e] * b.x * x, dec[e] * b.y * y, h2, l2);
+      unsigned char* out = tb + sw128_off(32 + 16 * m + 8 * e + at, c);
+      *reinterpret_cast<uint32_t*>(out) = h;
+      *reinterpret_cast<uint32_t*>(out + kBox) = l;
+      *reinterpret_cast<uint32_t*>(out + 2 * kBox) = h2;
+      *reinterpret_cast<uint32_t*>(out + 3 * kBox) = l2;
+    }
   }
 }
 
@@ -727,7 +691,7 @@ __device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, c
 __device__ __forceinline__ void issue_gram(ChunkSmem& cs, unsigned char* base, int c) {
   constexpr uint32_t id = idesc_bf16_f32(128, kC);
   const uint64_t s0 = smem_desc_sw128(smem_addr(base + (c & 1) * kStageBytes), 1024);
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < 8; ++k) {
     const uint64_t at = s0 + (((k >> 2) * 2 * kBox + (k & 3) * 32) >> 4);
     mma_bf16(cs.tmem + kColG, at, at, id, k > 0);
@@ -739,18 +703,33 @@ __device__ __forceinline__ void issue_gram(ChunkSmem& cs, unsigned char* base, i
 // and Q are there.
 __device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, int nchunk) {
   constexpr uint32_t idk = idesc_bf16_f32(128, kC) | kAmajorMN | kBmajorMN;
-  const uint64_t t0 = smem_desc_sw128_mn(smem_addr(base + kOffT + 2 * kBox), kBox);
+  constexpr uint32_t idm = idesc_bf16_f32(128, kC) | kBmajorMN;
+  const uint64_t t1 = smem_desc_sw128_mn(smem_addr(base + kOffT), kBox), t2 = t1 + ((2 * kBox) >> 4);
+  const uint64_t m0 = smem_desc_sw128(smem_addr(base + kOffM - kBox), 1024);
   for (int c = 0; c < nchunk; ++c) {
     const uint64_t k0 = smem_desc_sw128_mn(smem_addr(base + (c & 1) * kStageBytes), 2 * kBox);
     const bool ok = wait(cs, &cs.t_ready, c);
     if (!__all_sync(0xffffffffu, ok)) return;
+    // MT goes where the last chunk's sum W kt^T has been taken in
+    const bool free = wait(cs, &cs.s_ready[0], c) && wait(cs, &cs.s_ready[1], c);
+    if (!__all_sync(0xffffffffu, free)) return;
     if (elect_one()) {
       tc_fence_after_sync();
       // kt^T[dk][i] = sum_n K[n][dk] T''[n][i]
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + k * 128, idk, k > 0);
-        mma_bf16(cs.tmem + kColK, k0 + k * 128, t0 + (kBox >> 4) + k * 128, idk, 1u);
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t2 + k * 128, idk, k > 0);
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t2 + (kBox >> 4) + k * 128, idk, 1u);
+      }
+      mma_commit(&cs.stage_free[c & 1]);
+      // M T in lanes 64-127: rows 64.. of the left operand are M's (hi, then
+      // lo), the tile before them fills lanes that nothing reads
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t mh = m0 + 2 * k, ml = mh + (kBox >> 4), th = t1 + 128 * k, tl = th + (kBox >> 4);
+        mma_bf16(cs.tmem + kColD, mh, th, idm, k > 0);
+        mma_bf16(cs.tmem + kColD, mh, tl, idm, 1u);
+        mma_bf16(cs.tmem + kColD, ml, th, idm, 1u);
       }
       mma_commit(&cs.prep_done);
       if (c + 1 < nchunk) issue_gram(cs, base, c + 1);
@@ -759,19 +738,117 @@ __device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, in
   }
 }
 
+// 32 columns (from 32 cb) of row n of A or M from [K;Q] K^T: entry i times the
+// decays between i and n (and b_n for A), from the diagonal (or column
+// 32 cb + 31) leftwards; zero right of the diagonal.  A's diagonal blocks go to
+// `row` in f32 (their diagonal is never read), the others to a tile.
+__device__ __forceinline__ void form32(uint32_t tm_row, const Gates& g, bool isM, int n, int cb, unsigned char* tile,
+                                       float* out_row) {
+  const float f0 = isM ? 1.f : g.b[n];
+  const int dl = n - 32 * cb;
+  float f = dl > 31 ? f0 * g.mid[n] : 0.f;
+#pragma unroll
+  for (int b = 1; b >= 0; --b) {
+    float as[16], y[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 u = *reinterpret_cast<const float4*>(g.a + 32 * cb + 16 * b + 4 * j);
+      as[4 * j] = u.x, as[4 * j + 1] = u.y, as[4 * j + 2] = u.z, as[4 * j + 3] = u.w;
+    }
+    uint32_t x[16];
+    tmem_ld16_async(tm_row + kColG + 32 * cb + 16 * b, x);
+    tmem_wait16(x);
+#pragma unroll
+    for (int k = 15; k >= 0; --k) {
+      if (16 * b + k == dl) f = f0;
+      y[k] = 16 * b + k <= dl ? f * __uint_as_float(x[k]) : 0.f;
+      f *= as[k];
+    }
+    if (out_row == nullptr) {
+      uint32_t h[8], l[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) split_pair(y[2 * k], y[2 * k + 1], h[k], l[k]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint4* out = operand_piece(tile, n, 4 * cb + 2 * b + j);
+        out[0] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+        out[kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+      }
+    } else {
+      float4* r = reinterpret_cast<float4*>(out_row + 16 * b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+    }
+  }
+}
+
+// 32 columns (from 32 cb) of a row of kt^T as operands.
+__device__ __forceinline__ void put_kt(uint32_t tm_row, unsigned char* ktb, int row, int cb) {
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t x[16], h[8], l[8];
+    tmem_ld16_async(tm_row + kColK + 32 * cb + 16 * b, x);
+    tmem_wait16(x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) split_pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), h[k], l[k]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint4* out = operand_piece(ktb, row, 4 * cb + 2 * b + j);
+      out[0] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+      out[2 * kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+    }
+  }
+}
+
+// The same of row n of MT = M T diag(b).
+__device__ __forceinline__ void put_mt(uint32_t tm_row, unsigned char* mtb, const Gates& g, int n, int cb) {
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    float bs[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 u = *reinterpret_cast<const float4*>(g.b + 32 * cb + 16 * b + 4 * j);
+      bs[4 * j] = u.x, bs[4 * j + 1] = u.y, bs[4 * j + 2] = u.z, bs[4 * j + 3] = u.w;
+    }
+    uint32_t x[16], h[8], l[8];
+    tmem_ld16_async(tm_row + kColD + 32 * cb + 16 * b, x);
+    tmem_wait16(x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      split_pair(bs[2 * k] * __uint_as_float(x[2 * k]), bs[2 * k + 1] * __uint_as_float(x[2 * k + 1]), h[k], l[k]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint4* out = operand_piece(mtb, n, 4 * cb + 2 * b + j);
+      out[0] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+      out[kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+    }
+  }
+}
+
 // The preparation warps: T, MT and kt of every chunk, one chunk ahead of the
-// state, and [K;Q] K^T one more chunk ahead.  Warps p and p + 4 share a quarter
-// of the lanes (rows), half of the columns each.
+// state, and [K;Q] K^T one more chunk ahead.  The way from a chunk's
+// [K;Q] K^T to its T is the longest, so two warps (0 and 5, whose TMEM lanes
+// hold the rows of A's diagonal blocks of 32) do nothing else, and the others
+// finish the chunk before and form the rest of A and M beside them:
+//
+//   0, 5          A's diagonal blocks of chunk c, then T's
+//   1             A21 of c; kt of c - 1 (64 columns)
+//   4             kt of c - 1 (64 columns)
+//   2, 3, 6, 7    kt and MT of c - 1 (32 columns each); 2, 3, 7: M of c
+//
+// then all of them T21 of c, and kt^T and MT of c and [K;Q] K^T of c + 1 are
+// issued.
 __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int len, int nchunk) {
-  const int p = threadIdx.x - 32 * kPrepWarp, row = p & 127, n = p & 63, hh = p >> 7;
-  const int w = p >> 5, lane = p & 31;
-  const bool first = p < 32;
-  const uint32_t tm = cs.tmem + (static_cast<uint32_t>(p & 96) << 16);
-  float* D = reinterpret_cast<float*>(base + kOffD);
-  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT, *ab = base + kOffA;
-  // what lies right of the diagonal blocks of MT, M, T and T'' stays zero
-  for (int i = 16 * p; i < static_cast<int>(8 * kBox); i += 16 * kPrepThreads)
-    *reinterpret_cast<uint4*>(mtb + i) = make_uint4(0u, 0u, 0u, 0u);
+  const int p = threadIdx.x - 32 * kPrepWarp, lane = p & 31, w = p >> 5;
+  const int quad = w & 3, row = 32 * quad + lane, n = row & 63;
+  const uint32_t tm = cs.tmem + (static_cast<uint32_t>(32 * quad) << 16);
+  const bool solver = w == 0 || w == 5;
+  float* X = reinterpret_cast<float*>(base + kOffX);
+  unsigned char* ab = base + kOffA;
+  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
+  // the upper right quarters of M, T and T'' stay zero
+  for (int i = 16 * p; i < static_cast<int>(6 * kBox); i += 16 * kPrepThreads)
+    *reinterpret_cast<uint4*>(mb + i) = make_uint4(0u, 0u, 0u, 0u);
   // K and Q of chunk c are there; rows of K past the sequence's end (the next
   // one's) become zero
   auto stage_in = [&](int c) {
@@ -791,104 +868,47 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
   };
   bool ok = stage_in(0);
   if (prep_failed(ok)) return;
-  if (first && elect_one()) {
+  if (w == 0 && elect_one()) {
     tc_fence_after_sync();
     issue_gram(cs, base, 0);
   }
   __syncwarp();
-  for (int c = 0; c < nchunk; ++c) {
-    const int sg = c & 1;
-    const uint32_t ph2 = c >> 1;
-    const Gates& g = cs.gates[sg];
-    if (!wait(cs, &cs.gates_ready[sg], ph2) || !wait(cs, &cs.gram_done, c)) ok = false;
-    prep_sync();  // the last chunk's M has been read
+  for (int c = 0; c <= nchunk; ++c) {
+    const bool cur = c < nchunk;
+    const Gates& g = cs.gates[c & 1];
+    // kt and MT of c - 1: their products are done, and the operands of c - 2
+    // have been read.  (M and T'' are written again only after that.)
+    if (c > 0 && !wait(cs, &cs.prep_done, c - 1)) ok = false;
+    if (!solver && c > 1 && !wait(cs, &cs.o2_done, c - 2)) ok = false;
+    __syncwarp();
     tc_fence_after_sync();
-    if (hh == 0 || (n & 32) != 0) {  // whole warps; the upper right quarter stays
-      // lanes 0-63: rows of A, lanes 64-127: rows of M, from the diagonal (or
-      // column 31) leftwards; f is b_n (for A) times the decays passed.  (A's
-      // diagonal is never read.)
-      const bool isM = row >= 64;
-      const float f0 = isM ? 1.f : g.b[n];
-      const int dl = n - 32 * hh;  // the diagonal's column, at most 31 in a diagonal block of 32
-      float f = dl > 31 ? f0 * g.mid[n] : 0.f;
-#pragma unroll
-      for (int b = 1; b >= 0; --b) {
-        uint32_t x[16];
-        tmem_ld16_async(tm + kColG + 32 * hh + 16 * b, x);
-        tmem_wait16(x);
-        float as[16], y[16];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 u = *reinterpret_cast<const float4*>(g.a + 32 * hh + 16 * b + 4 * j);
-          as[4 * j] = u.x, as[4 * j + 1] = u.y, as[4 * j + 2] = u.z, as[4 * j + 3] = u.w;
-        }
-#pragma unroll
-        for (int k = 15; k >= 0; --k) {
-          if (16 * b + k == dl) f = f0;
-          y[k] = f * __uint_as_float(x[k]);
-          f *= as[k];
-        }
-        if (isM || 2 * hh + b < (n >> 4)) {
-          unsigned char* tile = isM ? mb : ab;
-          uint32_t h[8], l[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) split_pair(y[2 * k], y[2 * k + 1], h[k], l[k]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint4* out = operand_piece(tile, n, 4 * hh + 2 * b + j);
-            *out = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-            out[kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
-          }
-        } else if (2 * hh + b == (n >> 4)) {
-          float4* r = reinterpret_cast<float4*>(D + n * kPitchD);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) r[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-        }
-      }
+    if (!solver && c > 0) {
+      if (w != 6 && w != 7) put_kt(tm, ktb, row, 0);
+      if (w != 2 && w != 3) put_kt(tm, ktb, row, 1);
+      if (w == 2 || w == 3) put_mt(tm, mtb, cs.gates[(c - 1) & 1], n, 0);
+      if (w == 6 || w == 7) put_mt(tm, mtb, cs.gates[(c - 1) & 1], n, 1);
+      tc_fence_before_sync();
+      fence_proxy_async_smem();
+      warp_arrive(&cs.kt_ready);
     }
+    if (c > 0) warp_arrive(&cs.gates_free[(c - 1) & 1]);
+    if (!cur) break;
+    if (!wait(cs, &cs.gates_ready[c & 1], c >> 1) || !wait(cs, &cs.gram_done, c)) ok = false;
+    __syncwarp();
+    tc_fence_after_sync();
+    if (w != 4 && w != 6)
+      form32(tm, g, quad >= 2, n, w == 5 || w == 7, quad >= 2 ? mb : ab, solver ? X + n * kPitchX : nullptr);
     tc_fence_before_sync();
-    if (prep_failed(ok)) break;
-    invert(D, ab, tb, g, p);
+    if (solver) {
+      __syncwarp();
+      solve32(X + (w == 5 ? 32 * kPitchX : 0), lane);
+    }
     if (c + 1 < nchunk && !stage_in(c + 1)) ok = false;
+    if (prep_failed(ok)) break;
+    solve64(X, ab, tb, g, p);
     fence_proxy_async_smem();
     warp_arrive(&cs.t_ready);
-    prep_sync();
-    // the last chunk's kt and MT have been read
-    if (c > 0 && !wait(cs, &cs.o2_done, c - 1)) ok = false;
-    __syncwarp();
-    // MT: the rows of tiles 3 and 0, and 2 and 1, on four warps each, by their
-    // number of steps
-    const int u = w & 3;
-    if (w < 4) {
-      put_mt(mtb, mb, tb, g, 3, u, lane);
-      if (u >= 2) put_mt(mtb, mb, tb, g, 0, u - 2, lane);
-    } else {
-      put_mt(mtb, mb, tb, g, 2, u, lane);
-      put_mt(mtb, mb, tb, g, 1, u ^ 2, lane);
-    }
-    warp_arrive(&cs.gates_free[sg]);
-    if (!wait(cs, &cs.prep_done, c)) ok = false;
-    __syncwarp();
-    tc_fence_after_sync();
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t x[16];
-      tmem_ld16_async(tm + kColK + 32 * hh + 16 * b, x);
-      tmem_wait16(x);
-      uint32_t h[8], l[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) split_pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), h[k], l[k]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint4* out = operand_piece(ktb, row, 4 * hh + 2 * b + j);
-        *out = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-        out[2 * kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
-      }
-    }
-    tc_fence_before_sync();
-    fence_proxy_async_smem();
-    warp_arrive(&cs.kt_ready);
-    warp_arrive(&cs.stage_free[sg]);
+    prep_sync();  // X may be written again
   }
 }
 
@@ -1052,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cs.full[i], 1);
       mbar_init(&cs.full_v[i], 1);
-      mbar_init(&cs.stage_free[i], 1 + kPrepWarps);
+      mbar_init(&cs.stage_free[i], 2);
       mbar_init(&cs.v_free[i], kOutWarps);
       mbar_init(&cs.gates_ready[i], 1);
       mbar_init(&cs.gates_free[i], kStateWarps + kPrepWarps + kOutWarps);
@@ -1064,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&cs.fix, kPrepWarps);
     mbar_init(&cs.gram_done, 1);
     mbar_init(&cs.prep_done, 1);
-    mbar_init(&cs.kt_ready, kPrepWarps);
+    mbar_init(&cs.kt_ready, kPrepWarps - 2);
     mbar_init(&cs.d1_done, 1);
     mbar_init(&cs.qs_done, 1);
     mbar_init(&cs.rhs_ready, kStateWarps);
