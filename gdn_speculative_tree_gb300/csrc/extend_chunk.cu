@@ -94,26 +94,23 @@ struct ChunkSmem {
   uint64_t full[2], full_v[2], stage_free[2], v_free[2], gates_ready[2], gates_free[2];
   uint64_t fix, gram_done, prep_done, kt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done,
       o_read, o_tile, t_ready, drain[3];
+  uint64_t deadline;
   uint32_t tmem;
   int fail;
 };
 
-// A bounded wait that also gives up once any other wait of the CTA has.
+// A bounded wait: every wait of the CTA gives up at the same time, a second
+// and 100 us per chunk (fifteen times what one takes) after its start, or once
+// another one has.  Kept short: the roles' code together is several times the
+// instruction cache, and its size is what the chunks' time went down with.
 __device__ __forceinline__ bool wait(ChunkSmem& cs, uint64_t* bar, uint32_t parity) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait(bar, parity & 1u)) return true;
-    if ((it & 31u) == 31u) {
-      if (*reinterpret_cast<volatile int*>(&cs.fail)) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > kWaitLimitNs) {
-        *reinterpret_cast<volatile int*>(&cs.fail) = 1;
-        return false;
-      }
+  while (!mbar_try_wait(bar, parity & 1u)) {
+    if (*reinterpret_cast<volatile int*>(&cs.fail) || globaltimer_ns() > cs.deadline) {
+      *reinterpret_cast<volatile int*>(&cs.fail) = 1;
+      return false;
     }
   }
+  return true;
 }
 
 // One arrival for the warp, after everything its threads have done.
@@ -182,28 +179,47 @@ __device__ __forceinline__ void prep_sync() { named_bar_sync<1, kPrepThreads>();
 // them leave together, so that none is left at a barrier.
 __device__ __forceinline__ bool prep_failed(bool ok) { return named_bar_or<1, kPrepThreads>(!ok); }
 
-// out (row r, columns c ..) = sum over N of left (row r of L) times right
-// (rows of R, columns c ..), N a multiple of 4, V = 4 or 8 columns per lane;
-// all f32 in shared memory.
+// acc = sum over N of left (a row L) times right (rows of R, V columns from
+// there), N a multiple of 4; all f32 in shared memory.
 template <int N, int V>
 __device__ __forceinline__ void dot_rows(const float* L, const float* R, float (&acc)[V]) {
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < N; i += 4) {
     const float4 l = *reinterpret_cast<const float4*>(L + i);
     const float ls[4] = {l.x, l.y, l.z, l.w};
+    float4 y[V];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < V; ++k)
+      y[k] = *reinterpret_cast<const float4*>(R + (i + k / (V / 4)) * kPitchX + 4 * (k % (V / 4)));
 #pragma unroll
-      for (int e = 0; e < V; e += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(R + (i + k) * kPitchX + e);
-        acc[e] = fmaf(ls[k], y.x, acc[e]);
-        acc[e + 1] = fmaf(ls[k], y.y, acc[e + 1]);
-        acc[e + 2] = fmaf(ls[k], y.z, acc[e + 2]);
-        acc[e + 3] = fmaf(ls[k], y.w, acc[e + 3]);
-      }
+    for (int k = 0; k < V; ++k) {
+      const int e = 4 * (k % (V / 4));
+      const float f = ls[k / (V / 4)];
+      acc[e] = fmaf(f, y[k].x, acc[e]);
+      acc[e + 1] = fmaf(f, y[k].y, acc[e + 1]);
+      acc[e + 2] = fmaf(f, y[k].z, acc[e + 2]);
+      acc[e + 3] = fmaf(f, y[k].w, acc[e + 3]);
     }
+  }
+}
+
+// T21 = -T22 (A21 T11) for the block of 2 N at B (A21 and then T21 at row N,
+// T22 at row and column N), V columns per lane: row r, from column c.
+template <int N, int V>
+__device__ __forceinline__ void merge(float* B, int r, int c) {
+  float4* out = reinterpret_cast<float4*>(B + (N + r) * kPitchX + c);
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    float t[V];
+    dot_rows<N, V>(B + (N + r) * kPitchX + pass * N, B + pass * N * kPitchX + c, t);
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < V; e += 4)
+      out[e / 4] = pass ? make_float4(-t[e], -t[e + 1], -t[e + 2], -t[e + 3])
+                        : make_float4(t[e], t[e + 1], t[e + 2], t[e + 3]);
+    __syncwarp();
   }
 }
 
@@ -235,34 +251,8 @@ __device__ __forceinline__ void solve32(float* X, int lane) {
     for (int n = 0; n < 8; ++n) B[n * kPitchX + j] = x[n];
   }
   __syncwarp();
-  {
-    const int r = 8 + ((lane & 15) >> 1), c = 4 * (lane & 1);
-    float* B = X + 16 * (lane >> 4) * (kPitchX + 1);
-    float4* out = reinterpret_cast<float4*>(B + r * kPitchX + c);
-    float t[4];
-    dot_rows<8, 4>(B + r * kPitchX, B + c, t);
-    __syncwarp();
-    *out = make_float4(t[0], t[1], t[2], t[3]);
-    __syncwarp();
-    dot_rows<8, 4>(B + r * kPitchX + 8, B + 8 * kPitchX + c, t);
-    __syncwarp();
-    *out = make_float4(-t[0], -t[1], -t[2], -t[3]);
-  }
-  __syncwarp();
-  {
-    const int r = 16 + (lane >> 1), c = 8 * (lane & 1);
-    float4* out = reinterpret_cast<float4*>(X + r * kPitchX + c);
-    float t[8];
-    dot_rows<16, 8>(X + r * kPitchX, X + c, t);
-    __syncwarp();
-    out[0] = make_float4(t[0], t[1], t[2], t[3]);
-    out[1] = make_float4(t[4], t[5], t[6], t[7]);
-    __syncwarp();
-    dot_rows<16, 8>(X + r * kPitchX + 16, X + 16 * kPitchX + c, t);
-    __syncwarp();
-    out[0] = make_float4(-t[0], -t[1], -t[2], -t[3]);
-    out[1] = make_float4(-t[4], -t[5], -t[6], -t[7]);
-  }
+  merge<8, 4>(X + 16 * (lane >> 4) * (kPitchX + 1), (lane & 15) >> 1, 4 * (lane & 1));
+  merge<16, 8>(X, lane >> 1, 8 * (lane & 1));
 }
 
 __device__ __forceinline__ void put_piece(unsigned char* hi, int row, int j, const float (&x)[8]) {
@@ -747,8 +737,9 @@ __device__ __forceinline__ void form32(uint32_t tm_row, const Gates& g, bool isM
   const float f0 = isM ? 1.f : g.b[n];
   const int dl = n - 32 * cb;
   float f = dl > 31 ? f0 * g.mid[n] : 0.f;
-#pragma unroll
+#pragma unroll 1
   for (int b = 1; b >= 0; --b) {
+    const int db = dl - 16 * b;
     float as[16], y[16];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -760,8 +751,8 @@ __device__ __forceinline__ void form32(uint32_t tm_row, const Gates& g, bool isM
     tmem_wait16(x);
 #pragma unroll
     for (int k = 15; k >= 0; --k) {
-      if (16 * b + k == dl) f = f0;
-      y[k] = 16 * b + k <= dl ? f * __uint_as_float(x[k]) : 0.f;
+      if (k == db) f = f0;
+      y[k] = k <= db ? f * __uint_as_float(x[k]) : 0.f;
       f *= as[k];
     }
     if (out_row == nullptr) {
@@ -782,45 +773,35 @@ __device__ __forceinline__ void form32(uint32_t tm_row, const Gates& g, bool isM
   }
 }
 
-// 32 columns (from 32 cb) of a row of kt^T as operands.
-__device__ __forceinline__ void put_kt(uint32_t tm_row, unsigned char* ktb, int row, int cb) {
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uint32_t x[16], h[8], l[8];
-    tmem_ld16_async(tm_row + kColK + 32 * cb + 16 * b, x);
-    tmem_wait16(x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) split_pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), h[k], l[k]);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint4* out = operand_piece(ktb, row, 4 * cb + 2 * b + j);
-      out[0] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-      out[2 * kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
-    }
-  }
-}
-
-// The same of row n of MT = M T diag(b).
-__device__ __forceinline__ void put_mt(uint32_t tm_row, unsigned char* mtb, const Gates& g, int n, int cb) {
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
+// Columns 16 b .. of a row of kt^T (MT false) or of MT = M T diag(b) as
+// operands, for b from b0 to b1 - 1; `lo` bytes from the hi to the lo tile.
+template <bool MT>
+__device__ __forceinline__ void put_rows(uint32_t tm_cols, unsigned char* tile, uint32_t lo, const Gates& g, int row,
+                                         int b0, int b1) {
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
     float bs[16];
+    if constexpr (MT) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 u = *reinterpret_cast<const float4*>(g.b + 32 * cb + 16 * b + 4 * j);
-      bs[4 * j] = u.x, bs[4 * j + 1] = u.y, bs[4 * j + 2] = u.z, bs[4 * j + 3] = u.w;
+      for (int j = 0; j < 4; ++j) {
+        const float4 u = *reinterpret_cast<const float4*>(g.b + 16 * b + 4 * j);
+        bs[4 * j] = u.x, bs[4 * j + 1] = u.y, bs[4 * j + 2] = u.z, bs[4 * j + 3] = u.w;
+      }
     }
     uint32_t x[16], h[8], l[8];
-    tmem_ld16_async(tm_row + kColD + 32 * cb + 16 * b, x);
+    tmem_ld16_async(tm_cols + 16 * b, x);
     tmem_wait16(x);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      split_pair(bs[2 * k] * __uint_as_float(x[2 * k]), bs[2 * k + 1] * __uint_as_float(x[2 * k + 1]), h[k], l[k]);
+    for (int k = 0; k < 8; ++k) {
+      const float u = __uint_as_float(x[2 * k]), v = __uint_as_float(x[2 * k + 1]);
+      if constexpr (MT) split_pair(bs[2 * k] * u, bs[2 * k + 1] * v, h[k], l[k]);
+      else split_pair(u, v, h[k], l[k]);
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      uint4* out = operand_piece(mtb, n, 4 * cb + 2 * b + j);
-      out[0] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-      out[kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+      unsigned char* out = reinterpret_cast<unsigned char*>(operand_piece(tile, row, 2 * b + j));
+      *reinterpret_cast<uint4*>(out) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+      *reinterpret_cast<uint4*>(out + lo) = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
     }
   }
 }
@@ -883,10 +864,9 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
     __syncwarp();
     tc_fence_after_sync();
     if (!solver && c > 0) {
-      if (w != 6 && w != 7) put_kt(tm, ktb, row, 0);
-      if (w != 2 && w != 3) put_kt(tm, ktb, row, 1);
-      if (w == 2 || w == 3) put_mt(tm, mtb, cs.gates[(c - 1) & 1], n, 0);
-      if (w == 6 || w == 7) put_mt(tm, mtb, cs.gates[(c - 1) & 1], n, 1);
+      const int b0 = w == 6 || w == 7 ? 2 : 0, b1 = w == 2 || w == 3 ? 2 : 4;
+      put_rows<false>(tm + kColK, ktb, 2 * kBox, g, row, b0, b1);
+      if (quad >= 2) put_rows<true>(tm + kColD, mtb, kBox, cs.gates[(c - 1) & 1], n, b0, b1);
       tc_fence_before_sync();
       fence_proxy_async_smem();
       warp_arrive(&cs.kt_ready);
@@ -1093,6 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&cs.o_read, kOutWarps);
     mbar_init(&cs.o_tile, kOutWarps);
     cs.fail = 0;
+    cs.deadline = globaltimer_ns() + kWaitLimitNs + 100000ull * static_cast<uint64_t>(nchunk);
     fence_mbarrier_init();
   }
   if (warp == kMmaWarp) {
