@@ -61,8 +61,8 @@ static_assert(2 * kStateRegs + 2 * kPrepRegs + kOutRegs + kMiscRegs <= 6 * kLaun
 // TMEM columns
 constexpr uint32_t kColS = 0;                // S: hi in 64 columns, lo in 64 (bf16 pairs)
 constexpr uint32_t kColW = 128;              // S k, then W (16 columns per 16 tokens: hi 8, lo 8)
-constexpr uint32_t kColO = 192;              // S q, then MT W
-constexpr uint32_t kColD = 256;              // sum W kt^T; before that MT (lanes 64-127)
+constexpr uint32_t kColO = 192;              // S q, then MT (lanes 64-127), then MT W
+constexpr uint32_t kColD = 256;              // sum W kt^T
 constexpr uint32_t kColG = 384;              // [K;Q] K^T
 constexpr uint32_t kColK = 448;              // kt^T
 constexpr uint32_t kTmemCols = 512;
@@ -85,6 +85,7 @@ struct __align__(16) Gates {
   float a[kC], b[kC], g[kC];          // decay, write strength and the product of the decays up to every token
   float dec[kC];                      // g_C / g_n: the product of the decays behind token n
   float mid[kC];                      // product of the decays from token 32 to n (1 for n < 32)
+  float mid16[32];                    // product of the decays from token 16 to n (16 <= n < 32)
   float gC;
 };
 
@@ -92,7 +93,7 @@ struct __align__(16) Gates {
 struct ChunkSmem {
   Gates gates[2];
   uint64_t full[2], full_v[2], stage_free[2], v_free[2], gates_ready[2], gates_free[2];
-  uint64_t fix, gram_done, prep_done, kt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done,
+  uint64_t fix, gram_done, kt_done, mt_done, kt_ready, mt_ready, s_ready[2], d1_done, qs_done, rhs_ready, qs_read, d2_done[2], o2_done,
       o_read, o_tile, t_ready, drain[3];
   uint64_t deadline;
   uint32_t tmem;
@@ -185,7 +186,7 @@ template <int N, int V>
 __device__ __forceinline__ void dot_rows(const float* L, const float* R, float (&acc)[V]) {
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
   for (int i = 0; i < N; i += 4) {
     const float4 l = *reinterpret_cast<const float4*>(L + i);
     const float ls[4] = {l.x, l.y, l.z, l.w};
@@ -627,34 +628,42 @@ __device__ __forceinline__ void run_out(const treewy_seqs& a, ChunkSmem& cs, uns
 // One warp: the gates of every chunk.
 __device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, const SeqInfo& q, int h, int nchunk) {
   const int lane = threadIdx.x & 31;
-  float al[2], be[2];
-  auto fetch = [&](int c) {  // tokens `lane` and `lane + 32`; past the end they change nothing
+  float na[2] = {1.f, 1.f}, nb[2] = {0.f, 0.f};
+  // one turn ahead: turn c works on what turn c - 1 has requested
+#pragma unroll 1
+  for (int c = -1; c < nchunk; ++c) {
+    const float al[2] = {na[0], na[1]}, be[2] = {nb[0], nb[1]};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = c * kC + lane + 32 * k;
-      al[k] = 1.f;
-      be[k] = 0.f;
+    for (int k = 0; k < 2; ++k) {  // tokens `lane` and `lane + 32`; past the end they change nothing
+      const int i = (c + 1) * kC + lane + 32 * k;
+      na[k] = 1.f;
+      nb[k] = 0.f;
       if (i < q.len) {
-        al[k] = __ldg(a.alpha + (q.tok0 + i) * a.H + h);
-        be[k] = __ldg(a.beta + (q.tok0 + i) * a.H + h);
+        na[k] = __ldg(a.alpha + (q.tok0 + i) * a.H + h);
+        nb[k] = __ldg(a.beta + (q.tok0 + i) * a.H + h);
       }
     }
-  };
-  fetch(0);
-  for (int c = 0; c < nchunk; ++c) {
+    if (c < 0) continue;
     const int sg = c & 1;
     // products of the decays up to and behind every token, by doubling
     float up[2] = {al[0], al[1]}, down[2] = {al[0], al[1]};
+#pragma unroll 1
+    for (int s = 1; s < 32; s <<= 1) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) {
+      for (int k = 0; k < 2; ++k) {
         const float y = __shfl_up_sync(0xffffffffu, up[k], s), z = __shfl_down_sync(0xffffffffu, down[k], s);
         if (lane >= s) up[k] *= y;
         if (lane + s < 32) down[k] *= z;
       }
     }
     const float mid = up[1];
+    // within tokens 16-31: by doubling over 16 lanes
+    float mid16 = al[0];
+#pragma unroll 1
+    for (int s = 1; s < 16; s <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, mid16, s, 16);
+      if ((lane & 15) >= s) mid16 *= y;
+    }
     up[1] *= __shfl_sync(0xffffffffu, up[0], 31);
     const float half = __shfl_sync(0xffffffffu, down[1], 0);
     const float next0 = __shfl_down_sync(0xffffffffu, down[0], 1), next1 = __shfl_down_sync(0xffffffffu, down[1], 1);
@@ -671,9 +680,9 @@ __device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, c
       g.dec[i] = dec[k];
       g.mid[i] = k ? mid : 1.f;
     }
+    g.mid16[lane] = mid16;
     if (lane == 31) g.gC = up[1];
     warp_arrive(&cs.gates_ready[sg]);
-    if (c + 1 < nchunk) fetch(c + 1);
   }
 }
 
@@ -700,45 +709,53 @@ __device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, in
     const uint64_t k0 = smem_desc_sw128_mn(smem_addr(base + (c & 1) * kStageBytes), 2 * kBox);
     const bool ok = wait(cs, &cs.t_ready, c);
     if (!__all_sync(0xffffffffu, ok)) return;
-    // MT goes where the last chunk's sum W kt^T has been taken in
-    const bool free = wait(cs, &cs.s_ready[0], c) && wait(cs, &cs.s_ready[1], c);
-    if (!__all_sync(0xffffffffu, free)) return;
     if (elect_one()) {
       tc_fence_after_sync();
+      // the next chunk's [K;Q] K^T first: the way from there to T is the longest
+      if (c + 1 < nchunk) issue_gram(cs, base, c + 1);
       // kt^T[dk][i] = sum_n K[n][dk] T''[n][i]
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         mma_bf16(cs.tmem + kColK, k0 + k * 128, t2 + k * 128, idk, k > 0);
         mma_bf16(cs.tmem + kColK, k0 + k * 128, t2 + (kBox >> 4) + k * 128, idk, 1u);
       }
+      mma_commit(&cs.kt_done);
       mma_commit(&cs.stage_free[c & 1]);
+    }
+    __syncwarp();
+    // MT takes the place of the chunk's S q for a while
+    const bool free = wait(cs, &cs.qs_read, c);
+    if (!__all_sync(0xffffffffu, free)) return;
+    if (elect_one()) {
+      tc_fence_after_sync();
       // M T in lanes 64-127: rows 64.. of the left operand are M's (hi, then
       // lo), the tile before them fills lanes that nothing reads
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const uint64_t mh = m0 + 2 * k, ml = mh + (kBox >> 4), th = t1 + 128 * k, tl = th + (kBox >> 4);
-        mma_bf16(cs.tmem + kColD, mh, th, idm, k > 0);
-        mma_bf16(cs.tmem + kColD, mh, tl, idm, 1u);
-        mma_bf16(cs.tmem + kColD, ml, th, idm, 1u);
+        mma_bf16(cs.tmem + kColO, mh, th, idm, k > 0);
+        mma_bf16(cs.tmem + kColO, mh, tl, idm, 1u);
+        mma_bf16(cs.tmem + kColO, ml, th, idm, 1u);
       }
-      mma_commit(&cs.prep_done);
-      if (c + 1 < nchunk) issue_gram(cs, base, c + 1);
+      mma_commit(&cs.mt_done);
     }
     __syncwarp();
   }
 }
 
-// 32 columns (from 32 cb) of row n of A or M from [K;Q] K^T: entry i times the
+// Columns 16 b .. of the 32 from 32 cb, for b from b1 - 1 down to b0, of row n
+// of A or M from [K;Q] K^T: entry i times the
 // decays between i and n (and b_n for A), from the diagonal (or column
 // 32 cb + 31) leftwards; zero right of the diagonal.  A's diagonal blocks go to
 // `row` in f32 (their diagonal is never read), the others to a tile.
-__device__ __forceinline__ void form32(uint32_t tm_row, const Gates& g, bool isM, int n, int cb, unsigned char* tile,
-                                       float* out_row) {
+__device__ __forceinline__ void form_row(uint32_t tm_row, const Gates& g, bool isM, int n, int cb, int b0, int b1,
+                                         unsigned char* tile, float* out_row) {
   const float f0 = isM ? 1.f : g.b[n];
   const int dl = n - 32 * cb;
   float f = dl > 31 ? f0 * g.mid[n] : 0.f;
+  if (b1 == 1) f = dl > 15 ? f0 * g.mid16[n] : 0.f;
 #pragma unroll 1
-  for (int b = 1; b >= 0; --b) {
+  for (int b = b1 - 1; b >= b0; --b) {
     const int db = dl - 16 * b;
     float as[16], y[16];
 #pragma unroll
@@ -813,12 +830,13 @@ __device__ __forceinline__ void put_rows(uint32_t tm_cols, unsigned char* tile, 
 // finish the chunk before and form the rest of A and M beside them:
 //
 //   0, 5          A's diagonal blocks of chunk c, then T's
-//   1             A21 of c; kt of c - 1 (64 columns)
+//   1             kt of c - 1 (64 columns); A21 of c
 //   4             kt of c - 1 (64 columns)
-//   2, 3, 6, 7    kt and MT of c - 1 (32 columns each); 2, 3, 7: M of c
+//   2, 3, 6, 7    kt of c - 1 (32 columns each), MT of c - 1 and M of c (2, 6: rows
+//                 0-31, 16 columns each; 3, 7: rows 32-63, 32 columns each)
 //
-// then all of them T21 of c, and kt^T and MT of c and [K;Q] K^T of c + 1 are
-// issued.
+// then all of them T21 of c, and [K;Q] K^T of c + 1, kt^T and MT of c are
+// issued.  kt is what the chain waits for, so it comes first.
 __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int len, int nchunk) {
   const int p = threadIdx.x - 32 * kPrepWarp, lane = p & 31, w = p >> 5;
   const int quad = w & 3, row = 32 * quad + lane, n = row & 63;
@@ -827,9 +845,9 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
   float* X = reinterpret_cast<float*>(base + kOffX);
   unsigned char* ab = base + kOffA;
   unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
-  // the upper right quarters of M, T and T'' stay zero
-  for (int i = 16 * p; i < static_cast<int>(6 * kBox); i += 16 * kPrepThreads)
-    *reinterpret_cast<uint4*>(mb + i) = make_uint4(0u, 0u, 0u, 0u);
+  // the upper right quarters of MT, M, T and T'' stay zero
+  for (int i = 16 * p; i < static_cast<int>(8 * kBox); i += 16 * kPrepThreads)
+    *reinterpret_cast<uint4*>(mtb + i) = make_uint4(0u, 0u, 0u, 0u);
   // K and Q of chunk c are there; rows of K past the sequence's end (the next
   // one's) become zero
   auto stage_in = [&](int c) {
@@ -857,27 +875,38 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
   for (int c = 0; c <= nchunk; ++c) {
     const bool cur = c < nchunk;
     const Gates& g = cs.gates[c & 1];
-    // kt and MT of c - 1: their products are done, and the operands of c - 2
-    // have been read.  (M and T'' are written again only after that.)
-    if (c > 0 && !wait(cs, &cs.prep_done, c - 1)) ok = false;
-    if (!solver && c > 1 && !wait(cs, &cs.o2_done, c - 2)) ok = false;
-    __syncwarp();
-    tc_fence_after_sync();
     if (!solver && c > 0) {
+      // the operands of c - 2 have been read, the products of c - 1 are done
+      if (c > 1 && !wait(cs, &cs.o2_done, c - 2)) ok = false;
+      if (!wait(cs, &cs.kt_done, c - 1)) ok = false;
+      __syncwarp();
+      tc_fence_after_sync();
       const int b0 = w == 6 || w == 7 ? 2 : 0, b1 = w == 2 || w == 3 ? 2 : 4;
       put_rows<false>(tm + kColK, ktb, 2 * kBox, g, row, b0, b1);
-      if (quad >= 2) put_rows<true>(tm + kColD, mtb, kBox, cs.gates[(c - 1) & 1], n, b0, b1);
       tc_fence_before_sync();
       fence_proxy_async_smem();
       warp_arrive(&cs.kt_ready);
+      // and M and T of c - 1 have been read
+      if (!wait(cs, &cs.mt_done, c - 1)) ok = false;
+      __syncwarp();
+      if (quad >= 2) {
+        tc_fence_after_sync();
+        const int m0 = quad == 2 ? (w == 6) : b0, m1 = quad == 2 ? m0 + 1 : b1;
+        put_rows<true>(tm + kColO, mtb, kBox, cs.gates[(c - 1) & 1], n, m0, m1);
+        tc_fence_before_sync();
+        fence_proxy_async_smem();
+        warp_arrive(&cs.mt_ready);
+      }
     }
     if (c > 0) warp_arrive(&cs.gates_free[(c - 1) & 1]);
     if (!cur) break;
     if (!wait(cs, &cs.gates_ready[c & 1], c >> 1) || !wait(cs, &cs.gram_done, c)) ok = false;
     __syncwarp();
     tc_fence_after_sync();
-    if (w != 4 && w != 6)
-      form32(tm, g, quad >= 2, n, w == 5 || w == 7, quad >= 2 ? mb : ab, solver ? X + n * kPitchX : nullptr);
+    // rows 0-31 of M end in column 31: 16 columns each for warps 2 and 6
+    if (w != 4)
+      form_row(tm, g, quad >= 2, n, w == 5 || w == 7, w == 2, w == 6 ? 1 : 2, quad >= 2 ? mb : ab,
+               solver ? X + n * kPitchX : nullptr);
     tc_fence_before_sync();
     if (solver) {
       __syncwarp();
@@ -919,7 +948,7 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
     // W's columns have been read by the last chunk's products
     if (c > 0 && !held(&cs.o2_done, c - 1)) return;
     // S k, half of the columns of S at a time
-#pragma unroll
+#pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       if (!held(&cs.s_ready[half], c)) return;
       if (elect_one()) {
@@ -952,7 +981,7 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
     if (!held(&cs.kt_ready, c) || !held(&cs.rhs_ready, c)) return;
     if (elect_one()) {
     tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
     for (int half = 0; half < 2; ++half) {
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
@@ -967,7 +996,7 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
     }
     __syncwarp();
     // MT W over the columns of S q
-    if (!held(&cs.qs_read, c)) return;
+    if (!held(&cs.mt_ready, c)) return;
     if (elect_one()) {
     tc_fence_after_sync();
 #pragma unroll 1
@@ -989,6 +1018,7 @@ __device__ __forceinline__ void run_load(const CUtensorMap* map_q, const CUtenso
                                          ChunkSmem& cs, unsigned char* base, const SeqInfo& q, int hk, int h,
                                          int nchunk) {
   int issued = 0, issued_v = 0;
+#pragma unroll 1
   for (int c = 0; c < nchunk; ++c) {
     const int sg = c & 1;
     if (c >= 2 && !wait(cs, &cs.stage_free[sg], (c >> 1) - 1)) break;
@@ -1063,7 +1093,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&cs.t_ready, kPrepWarps);
     mbar_init(&cs.fix, kPrepWarps);
     mbar_init(&cs.gram_done, 1);
-    mbar_init(&cs.prep_done, 1);
+    mbar_init(&cs.kt_done, 1);
+    mbar_init(&cs.mt_done, 1);
+    mbar_init(&cs.mt_ready, 4);
     mbar_init(&cs.kt_ready, kPrepWarps - 2);
     mbar_init(&cs.d1_done, 1);
     mbar_init(&cs.qs_done, 1);
