@@ -277,7 +277,7 @@ struct Stage {
   float k[kStage][128];
   float q[kStage][128];
   float v[kStage][128];
-  float alpha[kStage], beta[kStage];
+  float alpha[kStage], beta[kStage], kq[kStage];
 };
 
 // One (sequence, head) and 32 RPT of its rows per CTA, any number of tokens.
@@ -344,32 +344,53 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
     else if (tid < 2 * kStage) st.beta[tid - kStage] = ngate;
     __syncthreads();
     fetch(t0 + kStage);
-    const int m = min(kStage, s.len - t0);
-    for (int n = 0; n < m; ++n) {
-      float k[16], q[16];
-      load_row<V, true>(st.k[n], false, 0, 128, l, k);
-      load_row<V, true>(st.q[n], false, 0, 128, l, q);
-      const float alpha = st.alpha[n], beta = st.beta[n];
-      float kq = 0.f;
+    if (tid < 8 * kStage) {  // k . q, eight lanes per token
+      float k[16], q[16], kq = 0.f;
+      load_row<V, true>(st.k[tid >> 3], false, 0, 128, l, k);
+      load_row<V, true>(st.q[tid >> 3], false, 0, 128, l, q);
 #pragma unroll
       for (int c = 0; c < 16; ++c) kq = fmaf(k[c], q[c], kq);
       kq = sum8(kq);
+      if (l == 0) st.kq[tid >> 3] = kq;
+    }
+    __syncthreads();
+    const int m = min(kStage, s.len - t0);
+    // a token's way through the state is a chain of four FMAs, three shuffles
+    // and an update per row; the next token's k and q are on their way meanwhile
+    float k[16], q[16], kn[16], qn[16], vn[RPT];
+    auto next = [&](int n) {
+      load_row<V, true>(st.k[n], false, 0, 128, l, kn);
+      load_row<V, true>(st.q[n], false, 0, 128, l, qn);
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) vn[j] = st.v[n][group_row<RPT>(first, j)];  // rows below 128
+    };
+    next(0);
+#pragma unroll 1
+    for (int n = 0; n < m; ++n) {
+      float v[RPT];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) k[c] = kn[c], q[c] = qn[c];
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) v[j] = vn[j];
+      const float alpha = st.alpha[n], beta = st.beta[n], kq = st.kq[n];
+      next(n + 1 < m ? n + 1 : n);
 #pragma unroll
       for (int j = 0; j < RPT; ++j) {
-        const int row = group_row<RPT>(first, j);
-        float sk = 0.f, sq = 0.f;
+        float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          sk = fmaf(S[j][c], k[c], sk);
-          sq = fmaf(S[j][c], q[c], sq);
+          sk[c & 3] = fmaf(S[j][c], k[c], sk[c & 3]);
+          sq[c & 3] = fmaf(S[j][c], q[c], sq[c & 3]);
+          S[j][c] *= alpha;
         }
-        sk = sum8(sk);
-        sq = sum8(sq);
-        const float u = beta * (st.v[n][row] - alpha * sk);  // row < 128
+        const float skt = sum8((sk[0] + sk[1]) + (sk[2] + sk[3]));
+        const float sqt = sum8((sq[0] + sq[1]) + (sq[2] + sq[3]));
+        const float u = beta * (v[j] - alpha * skt);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) S[j][c] = fmaf(u, k[c], alpha * S[j][c]);
+        for (int c = 0; c < 16; ++c) S[j][c] = fmaf(u, k[c], S[j][c]);
+        const int row = group_row<RPT>(first, j);
         if (l == 0 && row < a.dv)
-          store_o(a, ((s.tok0 + t0 + n) * a.H + h) * a.dv + row, fmaf(kq, u, alpha * sq));
+          store_o(a, ((s.tok0 + t0 + n) * a.H + h) * a.dv + row, fmaf(kq, u, alpha * sqt));
       }
     }
   }
