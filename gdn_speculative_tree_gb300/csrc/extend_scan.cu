@@ -199,6 +199,7 @@ __device__ __forceinline__ void unpack_row(const RawRow<SB>& r, float (&x)[16]) 
 // and are taken one after the other.
 template <int RPT, bool SB, bool WIDE>
 __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seqs a) {
+  after_previous();
   constexpr int V = SB ? 8 : 4;
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int l = threadIdx.x & 7;
@@ -284,6 +285,7 @@ struct Stage {
 template <int RPT, int V, bool WIDE>
 __global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
   __shared__ __align__(16) Stage st;
+  after_previous();
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int tid = threadIdx.x, l = tid & 7;
   const bool sb = (a.flags & TREEWY_FLAG_STATE_BF16) != 0;
@@ -406,16 +408,14 @@ cudaError_t launch_decode(const treewy_seqs& a, cudaStream_t stream) {
   constexpr int kRows = 4 * kDecodeWarps * RPT;
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
                   static_cast<unsigned>((a.dv + kRows - 1) / kRows));
-  decode_kernel<RPT, SB, WIDE><<<grid, kDecodeThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(decode_kernel<RPT, SB, WIDE>, grid, kDecodeThreads, stream, a);
 }
 
 template <int RPT, bool SB, bool WIDE>
 cudaError_t launch_scan(const treewy_seqs& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
                   static_cast<unsigned>((a.dv + 32 * RPT - 1) / (32 * RPT)));
-  scan_kernel<RPT, SB ? 8 : 4, WIDE><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(scan_kernel<RPT, SB ? 8 : 4, WIDE>, grid, kThreads, stream, a);
 }
 
 template <bool SB, bool WIDE>

@@ -105,6 +105,7 @@ __device__ __forceinline__ void load8_f32(const float* p, float (&x)[8]) {
 template <typename T, int LANES, int UNROLL, int THREADS>
 __global__ void __launch_bounds__(THREADS, 896 / THREADS)
     qk_norm_kernel(const treewy_qk a, int q_units, int units, float mean) {
+  after_previous();
   constexpr int kPass = 32 / LANES;                   // heads per pass
   const int lane = threadIdx.x % LANES, grp = (threadIdx.x & 31) / LANES;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
 // memory so that a pair's two elements may sit anywhere.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(const treewy_qk a) {
+  after_previous();
   __shared__ float buf[kThreads / 32][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int heads = a.Hq + a.Hk;
@@ -281,8 +283,7 @@ cudaError_t launch_passes(const treewy_qk& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.T + THREADS / 32 - 1) / (THREADS / 32)),
                   static_cast<unsigned>(units < 65535 ? units : 65535));
   const float mean = a.norm == TREEWY_NORM_RMS ? 1.0f / static_cast<float>(a.d) : 1.f;
-  qk_norm_kernel<T, LANES, UNROLL, THREADS><<<grid, THREADS, 0, stream>>>(a, q_units, units, mean);
-  return cudaGetLastError();
+  return launch_after(qk_norm_kernel<T, LANES, UNROLL, THREADS>, grid, THREADS, stream, a, q_units, units, mean);
 }
 
 template <typename T, int LANES>
@@ -309,8 +310,7 @@ cudaError_t launch_typed(const treewy_qk& a, cudaStream_t stream) {
   if (a.Hk > 0) wide = wide && on16(a.k, a.k_stride) && on16(a.k_out, 0);
   if (!wide) {
     constexpr int kRows = kThreads / 32;
-    qk_norm_any_kernel<T><<<static_cast<unsigned>((rows + kRows - 1) / kRows), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(qk_norm_any_kernel<T>, dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)), kThreads, stream, a);
   }
   if (a.d <= 64) return launch<T, 8>(a, stream);
   if (a.d <= 128) return launch<T, 16>(a, stream);

@@ -18,6 +18,7 @@ constexpr int kWords = 8;  // words of a thread per piece
 template <typename W>
 __global__ void __launch_bounds__(kThreads)
     copy_slots_kernel(const treewy_slots a, int64_t words, int pieces, int64_t layer_stride) {
+  after_previous();
   // pieces of one block are neighbours, then layers, then moves
   const int piece = static_cast<int>(blockIdx.x % pieces);
   const unsigned rest = blockIdx.x / pieces;
@@ -63,9 +64,8 @@ cudaError_t launch(const treewy_slots& a, int64_t layer_stride, cudaStream_t str
   const int64_t pieces = (words + kThreads * kWords - 1) / (kThreads * kWords);
   const int64_t grid = pieces * a.layers * a.n;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  copy_slots_kernel<W><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(
-      a, words, static_cast<int>(pieces), layer_stride);
-  return cudaGetLastError();
+  return launch_after(copy_slots_kernel<W>, dim3(static_cast<unsigned>(grid)), kThreads, stream, a, words,
+                      static_cast<int>(pieces), layer_stride);
 }
 
 }  // namespace

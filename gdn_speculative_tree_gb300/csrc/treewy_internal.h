@@ -38,6 +38,24 @@ cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& set) {
   return e;
 }
 
+// Launches a kernel that may be set up while the kernel before it on the stream
+// still runs (programmatic dependent launch): it calls after_previous() before
+// it touches memory, which holds it until that kernel is done.  A small call's
+// time between its neighbours is mostly that set-up.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Tensor maps the tensor-core verify kernel reads through (built on the host
 // per call; passed by value as kernel parameters).
 struct VerifyMaps {
