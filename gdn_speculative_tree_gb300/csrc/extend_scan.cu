@@ -26,7 +26,6 @@
 namespace treewy {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kDecodeWarps = 1, kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kStage = 16;  // tokens staged at a time
 constexpr unsigned kFull = 0xffffffffu;
@@ -59,14 +58,14 @@ __device__ __forceinline__ int piece_col(int l, int i) {
   return V * (l + 8 * i);
 }
 
-// The 16 columns of lane l of a row of n elements, zero beyond it.  WIDE: the
+// The CL columns (16 of up to 128, 8 of up to 64) of lane l of a row of n elements, zero beyond it.  WIDE: the
 // row starts on a 16-byte boundary of the pool's type (a q/k row on a
 // boundary of V elements) and n is a multiple of V.
-template <int V, bool WIDE>
+template <int V, bool WIDE, int CL>
 __device__ __forceinline__ void load_row(const void* base, bool bf16, int64_t at, int n, int l,
-                                         float (&x)[16]) {
+                                         float (&x)[CL]) {
 #pragma unroll
-  for (int i = 0; i < 16 / V; ++i) {
+  for (int i = 0; i < CL / V; ++i) {
     const int c0 = piece_col<V>(l, i);
 #pragma unroll
     for (int e = 0; e < V; ++e) x[V * i + e] = 0.f;
@@ -113,11 +112,11 @@ __device__ __forceinline__ void load_row(const void* base, bool bf16, int64_t at
 
 // The same columns back to the pool, which the next layers' pools push out of
 // L2 before it is read again; a bf16 pool rounds to nearest even.
-template <int V, bool WIDE>
+template <int V, bool WIDE, int CL>
 __device__ __forceinline__ void store_row(void* base, bool bf16, int64_t at, int n, int l,
-                                          const float (&x)[16]) {
+                                          const float (&x)[CL]) {
 #pragma unroll
-  for (int i = 0; i < 16 / V; ++i) {
+  for (int i = 0; i < CL / V; ++i) {
     const int c0 = piece_col<V>(l, i);
     if constexpr (WIDE) {
       if (c0 < n) {
@@ -273,22 +272,25 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seq
   }
 }
 
-// Staged tokens, f32, columns beyond dk (rows beyond dv) zero.
+// Staged tokens, f32: 8 CL columns of k and q (zero beyond dk) and the CTA's
+// rows of v (zero beyond dv).
+template <int CL, int ROWS>
 struct Stage {
-  float k[kStage][128];
-  float q[kStage][128];
-  float v[kStage][128];
+  float k[kStage][8 * CL];
+  float q[kStage][8 * CL];
+  float v[kStage][ROWS];
   float alpha[kStage], beta[kStage], kq[kStage];
 };
 
-// One (sequence, head) and 32 RPT of its rows per CTA, any number of tokens.
-template <int RPT, int V, bool WIDE>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
-  __shared__ __align__(16) Stage st;
+// One (sequence, head) and THREADS / 8 x RPT of its rows per CTA, CL columns
+// of a row per lane, any number of tokens.
+template <int RPT, bool SB, bool WIDE, int CL, int THREADS>
+__global__ void __launch_bounds__(THREADS) scan_kernel(const treewy_seqs a) {
+  constexpr int V = SB ? 8 : 4, kRows = THREADS / 8 * RPT, kCols = 8 * CL;
+  __shared__ __align__(16) Stage<CL, kRows> st;
   after_previous();
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int tid = threadIdx.x, l = tid & 7;
-  const bool sb = (a.flags & TREEWY_FLAG_STATE_BF16) != 0;
   const bool qb = a.qkv_dtype == TREEWY_DTYPE_BF16;
   const Seq s = load_seq(a, r);
   if (s.flags) {
@@ -297,34 +299,40 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
   }
   if (s.len == 0 && !s.fresh) return;
   const int64_t block = (static_cast<int64_t>(s.slot) * a.H + h) * a.dv;
-  const int first = static_cast<int>(blockIdx.y) * (32 * RPT);
-  float S[RPT][16];
+  const int first = static_cast<int>(blockIdx.y) * kRows;
+  float S[RPT][CL];
 #pragma unroll
   for (int j = 0; j < RPT; ++j) {
     const int row = group_row<RPT>(first, j);
     if (!s.fresh && row < a.dv) {
-      load_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
+      load_row<V, WIDE>(a.state, SB, (block + row) * a.dk, a.dk, l, S[j]);
     } else {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) S[j][c] = 0.f;
+      for (int c = 0; c < CL; ++c) S[j][c] = 0.f;
     }
   }
 
   const int hk = h / (a.H / a.Hk);
-  constexpr int kPer = kStage * 128 / kThreads;  // staged elements of k (q, v) per thread
-  float nk[kPer], nq[kPer], nv[kPer], ngate = 0.f;
+  constexpr int kPer = kStage * kCols / THREADS;  // staged elements of k (and q) per thread
+  constexpr int kPerV = kStage * kRows / THREADS;
+  float nk[kPer], nq[kPer], nv[kPerV], ngate = 0.f;
   auto fetch = [&](int t0) {  // the stage from token t0 on, into registers
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int e = tid + i * kThreads, n = e >> 7, c = e & 127;
+      const int e = tid + i * THREADS, n = e / kCols, c = e % kCols;
       const int64_t t = s.tok0 + t0 + n;
-      const bool live = t0 + n < s.len;
-      nk[i] = nq[i] = nv[i] = 0.f;
-      if (live && c < a.dk) {
+      nk[i] = nq[i] = 0.f;
+      if (t0 + n < s.len && c < a.dk) {
         nk[i] = load_qkv(a.k, t * a.k_stride + static_cast<int64_t>(hk) * a.dk + c, qb);
         nq[i] = load_qkv(a.q, t * a.q_stride + static_cast<int64_t>(hk) * a.dk + c, qb);
       }
-      if (live && c < a.dv) nv[i] = load_qkv(a.v, t * a.v_stride + static_cast<int64_t>(h) * a.dv + c, qb);
+    }
+#pragma unroll
+    for (int i = 0; i < kPerV; ++i) {
+      const int e = tid + i * THREADS, n = e / kRows, c = first + e % kRows;
+      nv[i] = 0.f;
+      if (t0 + n < s.len && c < a.dv)
+        nv[i] = load_qkv(a.v, (s.tok0 + t0 + n) * a.v_stride + static_cast<int64_t>(h) * a.dv + c, qb);
     }
     if (tid < 2 * kStage) {
       const int n = tid & (kStage - 1);
@@ -337,69 +345,70 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const treewy_seqs a) {
     __syncthreads();  // the last stage has been read
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int e = tid + i * kThreads;
-      (&st.k[0][0])[e] = nk[i];
-      (&st.q[0][0])[e] = nq[i];
-      (&st.v[0][0])[e] = nv[i];
+      (&st.k[0][0])[tid + i * THREADS] = nk[i];
+      (&st.q[0][0])[tid + i * THREADS] = nq[i];
     }
+#pragma unroll
+    for (int i = 0; i < kPerV; ++i) (&st.v[0][0])[tid + i * THREADS] = nv[i];
     if (tid < kStage) st.alpha[tid] = ngate;
     else if (tid < 2 * kStage) st.beta[tid - kStage] = ngate;
     __syncthreads();
     fetch(t0 + kStage);
     if (tid < 8 * kStage) {  // k . q, eight lanes per token
-      float k[16], q[16], kq = 0.f;
-      load_row<V, true>(st.k[tid >> 3], false, 0, 128, l, k);
-      load_row<V, true>(st.q[tid >> 3], false, 0, 128, l, q);
+      float k[CL], q[CL], kq = 0.f;
+      load_row<V, true>(st.k[tid >> 3], false, 0, kCols, l, k);
+      load_row<V, true>(st.q[tid >> 3], false, 0, kCols, l, q);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) kq = fmaf(k[c], q[c], kq);
+      for (int c = 0; c < CL; ++c) kq = fmaf(k[c], q[c], kq);
       kq = sum8(kq);
       if (l == 0) st.kq[tid >> 3] = kq;
     }
     __syncthreads();
     const int m = min(kStage, s.len - t0);
-    // a token's way through the state is a chain of four FMAs, three shuffles
-    // and an update per row; the next token's k and q are on their way meanwhile
-    float k[16], q[16], kn[16], qn[16], vn[RPT];
-    auto next = [&](int n) {
-      load_row<V, true>(st.k[n], false, 0, 128, l, kn);
-      load_row<V, true>(st.q[n], false, 0, 128, l, qn);
+    // A token's way through the state is a chain of CL / 4 FMAs, three shuffles
+    // and an update per row; the next token's k, q and v are on their way
+    // meanwhile.
+    float k[2][CL], q[2][CL], v[2][RPT];
+    auto next = [&](int n, int slot) {
+      load_row<V, true>(st.k[n], false, 0, kCols, l, k[slot]);
+      load_row<V, true>(st.q[n], false, 0, kCols, l, q[slot]);
 #pragma unroll
-      for (int j = 0; j < RPT; ++j) vn[j] = st.v[n][group_row<RPT>(first, j)];  // rows below 128
+      for (int j = 0; j < RPT; ++j) v[slot][j] = st.v[n][group_row<RPT>(0, j)];
     };
-    next(0);
+    next(0, 0);
 #pragma unroll 1
-    for (int n = 0; n < m; ++n) {
-      float v[RPT];
+    for (int n0 = 0; n0 < m; n0 += 2) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) k[c] = kn[c], q[c] = qn[c];
+      for (int p = 0; p < 2; ++p) {
+        const int n = n0 + p;
+        if (n >= m) break;
+        const float alpha = st.alpha[n], beta = st.beta[n], kq = st.kq[n];
+        next(min(n + 1, kStage - 1), p ^ 1);
 #pragma unroll
-      for (int j = 0; j < RPT; ++j) v[j] = vn[j];
-      const float alpha = st.alpha[n], beta = st.beta[n], kq = st.kq[n];
-      next(n + 1 < m ? n + 1 : n);
+        for (int j = 0; j < RPT; ++j) {
+          float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < RPT; ++j) {
-        float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int c = 0; c < CL; ++c) {
+            sk[c & 3] = fmaf(S[j][c], k[p][c], sk[c & 3]);
+            sq[c & 3] = fmaf(S[j][c], q[p][c], sq[c & 3]);
+            S[j][c] *= alpha;
+          }
+          const float skt = sum8((sk[0] + sk[1]) + (sk[2] + sk[3]));
+          const float sqt = sum8((sq[0] + sq[1]) + (sq[2] + sq[3]));
+          const float u = beta * (v[p][j] - alpha * skt);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          sk[c & 3] = fmaf(S[j][c], k[c], sk[c & 3]);
-          sq[c & 3] = fmaf(S[j][c], q[c], sq[c & 3]);
-          S[j][c] *= alpha;
+          for (int c = 0; c < CL; ++c) S[j][c] = fmaf(u, k[p][c], S[j][c]);
+          const int row = group_row<RPT>(first, j);
+          if (l == 0 && row < a.dv)
+            store_o(a, ((s.tok0 + t0 + n) * a.H + h) * a.dv + row, fmaf(kq, u, alpha * sqt));
         }
-        const float skt = sum8((sk[0] + sk[1]) + (sk[2] + sk[3]));
-        const float sqt = sum8((sq[0] + sq[1]) + (sq[2] + sq[3]));
-        const float u = beta * (v[j] - alpha * skt);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) S[j][c] = fmaf(u, k[c], S[j][c]);
-        const int row = group_row<RPT>(first, j);
-        if (l == 0 && row < a.dv)
-          store_o(a, ((s.tok0 + t0 + n) * a.H + h) * a.dv + row, fmaf(kq, u, alpha * sqt));
       }
     }
   }
 #pragma unroll
   for (int j = 0; j < RPT; ++j) {
     const int row = group_row<RPT>(first, j);
-    if (row < a.dv) store_row<V, WIDE>(a.state, sb, (block + row) * a.dk, a.dk, l, S[j]);
+    if (row < a.dv) store_row<V, WIDE>(a.state, SB, (block + row) * a.dk, a.dk, l, S[j]);
   }
 }
 
@@ -411,11 +420,12 @@ cudaError_t launch_decode(const treewy_seqs& a, cudaStream_t stream) {
   return launch_after(decode_kernel<RPT, SB, WIDE>, grid, kDecodeThreads, stream, a);
 }
 
-template <int RPT, bool SB, bool WIDE>
+template <int RPT, bool SB, bool WIDE, int CL, int THREADS>
 cudaError_t launch_scan(const treewy_seqs& a, cudaStream_t stream) {
+  constexpr int kRows = THREADS / 8 * RPT;
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
-                  static_cast<unsigned>((a.dv + 32 * RPT - 1) / (32 * RPT)));
-  return launch_after(scan_kernel<RPT, SB ? 8 : 4, WIDE>, grid, kThreads, stream, a);
+                  static_cast<unsigned>((a.dv + kRows - 1) / kRows));
+  return launch_after(scan_kernel<RPT, SB, WIDE, CL, THREADS>, grid, THREADS, stream, a);
 }
 
 template <bool SB, bool WIDE>
@@ -423,8 +433,12 @@ cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
   const int64_t heads = static_cast<int64_t>(a.R) * a.H;
   if (a.max_len <= 1)  // a quarter of a head per CTA, or less while that leaves SMs idle
     return 4 * heads >= 304 ? launch_decode<4, SB, WIDE>(a, stream) : launch_decode<1, SB, WIDE>(a, stream);
-  // a whole head per CTA, or a quarter of one while that leaves SMs idle
-  return heads >= 304 ? launch_scan<4, SB, WIDE>(a, stream) : launch_scan<1, SB, WIDE>(a, stream);
+  // A whole head per CTA, or 16 of its rows while that leaves SMs idle (the
+  // chain of a row is then alone on its quarter of an SM); half as many columns
+  // per lane for small keys.
+  if (heads >= 304)
+    return a.dk <= 64 ? launch_scan<4, SB, WIDE, 8, 256>(a, stream) : launch_scan<4, SB, WIDE, 16, 256>(a, stream);
+  return a.dk <= 64 ? launch_scan<1, SB, WIDE, 8, 128>(a, stream) : launch_scan<1, SB, WIDE, 16, 128>(a, stream);
 }
 
 }  // namespace
