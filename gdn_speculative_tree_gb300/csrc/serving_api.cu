@@ -63,13 +63,18 @@ treewy_status validate_seqs(const treewy_seqs* s) {
 }
 
 // Batches whose longest sequence has at least this many tokens run in chunks.
-constexpr int kChunkedLen = 17;
+// A chunk costs a CTA about 15 us whatever its length, a token of the other
+// kernel 0.4 us (128 x 128 heads), and that kernel spreads a head over eight
+// CTAs, which helps it until the SMs are full: 24 tokens x 32 heads take 16.7
+// and 16.9 us, 8 tokens x 128 heads 16.7 and 20.2 us, 17 x 1024 heads 93 and
+// 151 us.
+int chunked_len(const treewy_seqs& s) { return int64_t(s.R) * s.H >= 128 ? 9 : 24; }
 
 // Whether the chunked kernel takes the batch (s: strides resolved).
 bool use_chunks(const treewy_seqs& s) {
   auto rows_on16 = [](const void* p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; };
   return s.qkv_dtype == TREEWY_DTYPE_BF16 && s.dk % 8 == 0 && s.dv % 8 == 0 && s.T > 0 &&
-         s.max_len >= kChunkedLen && (s.flags & TREEWY_FLAG_FORCE_GENERIC) == 0 &&
+         s.max_len >= chunked_len(s) && (s.flags & TREEWY_FLAG_FORCE_GENERIC) == 0 &&
          rows_on16(s.q, s.q_stride) && rows_on16(s.k, s.k_stride) && rows_on16(s.v, s.v_stride) &&
          aligned(s.o, 16);
 }
