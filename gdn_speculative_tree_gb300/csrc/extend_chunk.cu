@@ -26,8 +26,8 @@
 //
 //   warps 0-7    state: two threads per row (64 of S's columns and 32 tokens
 //                each); S stays in f32 registers for the whole sequence
-//   warps 8-15   preparation of the next chunk: [K;Q] K^T, T, MT, kt
-//   warps 16-19  o
+//   warps 8-15   preparation of the next chunk: [K;Q] K^T, T, kt
+//   warps 16-19  o; 18 and 19 also MT
 //   warp 20      issues the chain's products
 //   warp 21      loads K, Q and V, two chunks in flight
 //   warp 22      gates
@@ -165,6 +165,14 @@ constexpr uint32_t kAmajorMN = 1u << 15, kBmajorMN = 1u << 16;
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// As tmem_wait16 for one array of eight.
+__device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
                : "memory");
 }
 
@@ -578,6 +586,29 @@ __device__ __forceinline__ void run_out(const treewy_seqs& a, ChunkSmem& cs, uns
     }
     tc_fence_before_sync();
     warp_arrive(&cs.qs_read);
+    if (d >= 64) {
+      // MT = M T diag(b), in lanes 64-127, as an operand while these warps have
+      // nothing else to do; rows 0-31 of it end in column 31
+      ok = wait(cs, &cs.mt_done, c);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after_sync();
+      unsigned char* mtb = base + kOffMT;
+      const int last = d < 96 ? 4 : 8;
+#pragma unroll 1
+      for (int j = 0; j < last; ++j) {
+        const float4 u = *reinterpret_cast<const float4*>(g.b + 8 * j), v = *reinterpret_cast<const float4*>(g.b + 8 * j + 4);
+        uint32_t x[8];
+        tmem_ld8_async(tm + kColO + 8 * j, x);
+        tmem_wait8(x);
+        const float y[8] = {u.x * __uint_as_float(x[0]), u.y * __uint_as_float(x[1]), u.z * __uint_as_float(x[2]),
+                            u.w * __uint_as_float(x[3]), v.x * __uint_as_float(x[4]), v.y * __uint_as_float(x[5]),
+                            v.z * __uint_as_float(x[6]), v.w * __uint_as_float(x[7])};
+        put_piece(mtb, d - 64, j, y);
+      }
+      tc_fence_before_sync();
+      fence_proxy_async_smem();
+      warp_arrive(&cs.mt_ready);
+    }
     warp_arrive(&cs.gates_free[sg]);
     ok = wait(cs, &cs.o2_done, c);
     if (!__all_sync(0xffffffffu, ok)) break;
@@ -711,8 +742,6 @@ __device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, in
     if (!__all_sync(0xffffffffu, ok)) return;
     if (elect_one()) {
       tc_fence_after_sync();
-      // the next chunk's [K;Q] K^T first: the way from there to T is the longest
-      if (c + 1 < nchunk) issue_gram(cs, base, c + 1);
       // kt^T[dk][i] = sum_n K[n][dk] T''[n][i]
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
@@ -721,6 +750,7 @@ __device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, in
       }
       mma_commit(&cs.kt_done);
       mma_commit(&cs.stage_free[c & 1]);
+      if (c + 1 < nchunk) issue_gram(cs, base, c + 1);
     }
     __syncwarp();
     // MT takes the place of the chunk's S q for a while
@@ -790,40 +820,25 @@ __device__ __forceinline__ void form_row(uint32_t tm_row, const Gates& g, bool i
   }
 }
 
-// Columns 16 b .. of a row of kt^T (MT false) or of MT = M T diag(b) as
-// operands, for b from b0 to b1 - 1; `lo` bytes from the hi to the lo tile.
-template <bool MT>
-__device__ __forceinline__ void put_rows(uint32_t tm_cols, unsigned char* tile, uint32_t lo, const Gates& g, int row,
-                                         int b0, int b1) {
+// Columns 16 b .. of a row of kt^T as operands, for b from b0 to b1 - 1.
+__device__ __forceinline__ void put_kt(uint32_t tm_row, unsigned char* ktb, int row, int b0, int b1) {
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    float bs[16];
-    if constexpr (MT) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 u = *reinterpret_cast<const float4*>(g.b + 16 * b + 4 * j);
-        bs[4 * j] = u.x, bs[4 * j + 1] = u.y, bs[4 * j + 2] = u.z, bs[4 * j + 3] = u.w;
-      }
-    }
     uint32_t x[16], h[8], l[8];
-    tmem_ld16_async(tm_cols + 16 * b, x);
+    tmem_ld16_async(tm_row + kColK + 16 * b, x);
     tmem_wait16(x);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float u = __uint_as_float(x[2 * k]), v = __uint_as_float(x[2 * k + 1]);
-      if constexpr (MT) split_pair(bs[2 * k] * u, bs[2 * k + 1] * v, h[k], l[k]);
-      else split_pair(u, v, h[k], l[k]);
-    }
+    for (int k = 0; k < 8; ++k) split_pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), h[k], l[k]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      unsigned char* out = reinterpret_cast<unsigned char*>(operand_piece(tile, row, 2 * b + j));
-      *reinterpret_cast<uint4*>(out) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-      *reinterpret_cast<uint4*>(out + lo) = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+      uint4* out = operand_piece(ktb, row, 2 * b + j);
+      out[0] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+      out[2 * kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
     }
   }
 }
 
-// The preparation warps: T, MT and kt of every chunk, one chunk ahead of the
+// The preparation warps: M, T and kt of every chunk, one chunk ahead of the
 // state, and [K;Q] K^T one more chunk ahead.  The way from a chunk's
 // [K;Q] K^T to its T is the longest, so two warps (0 and 5, whose TMEM lanes
 // hold the rows of A's diagonal blocks of 32) do nothing else, and the others
@@ -832,8 +847,8 @@ __device__ __forceinline__ void put_rows(uint32_t tm_cols, unsigned char* tile, 
 //   0, 5          A's diagonal blocks of chunk c, then T's
 //   1             kt of c - 1 (64 columns); A21 of c
 //   4             kt of c - 1 (64 columns)
-//   2, 3, 6, 7    kt of c - 1 (32 columns each), MT of c - 1 and M of c (2, 6: rows
-//                 0-31, 16 columns each; 3, 7: rows 32-63, 32 columns each)
+//   2, 3, 6, 7    kt of c - 1 (32 columns each); M of c (2, 6: rows 0-31, 16 columns
+//                 each; 3, 7: rows 32-63, 32 columns each)
 //
 // then all of them T21 of c, and [K;Q] K^T of c + 1, kt^T and MT of c are
 // issued.  kt is what the chain waits for, so it comes first.
@@ -882,21 +897,12 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
       __syncwarp();
       tc_fence_after_sync();
       const int b0 = w == 6 || w == 7 ? 2 : 0, b1 = w == 2 || w == 3 ? 2 : 4;
-      put_rows<false>(tm + kColK, ktb, 2 * kBox, g, row, b0, b1);
+      put_kt(tm, ktb, row, b0, b1);
       tc_fence_before_sync();
       fence_proxy_async_smem();
       warp_arrive(&cs.kt_ready);
-      // and M and T of c - 1 have been read
+      // M and T of c - 1 have been read
       if (!wait(cs, &cs.mt_done, c - 1)) ok = false;
-      __syncwarp();
-      if (quad >= 2) {
-        tc_fence_after_sync();
-        const int m0 = quad == 2 ? (w == 6) : b0, m1 = quad == 2 ? m0 + 1 : b1;
-        put_rows<true>(tm + kColO, mtb, kBox, cs.gates[(c - 1) & 1], n, m0, m1);
-        tc_fence_before_sync();
-        fence_proxy_async_smem();
-        warp_arrive(&cs.mt_ready);
-      }
     }
     if (c > 0) warp_arrive(&cs.gates_free[(c - 1) & 1]);
     if (!cur) break;
@@ -1095,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&cs.gram_done, 1);
     mbar_init(&cs.kt_done, 1);
     mbar_init(&cs.mt_done, 1);
-    mbar_init(&cs.mt_ready, 4);
+    mbar_init(&cs.mt_ready, kOutWarps / 2);
     mbar_init(&cs.kt_ready, kPrepWarps - 2);
     mbar_init(&cs.d1_done, 1);
     mbar_init(&cs.qs_done, 1);
