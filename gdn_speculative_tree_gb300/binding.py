@@ -304,16 +304,16 @@ def _need(x, name: str, dtype, shape=None) -> None:
         return
     if x.dtype != dtype:
         raise TypeError(f"{name} dtype {x.dtype} is not {dtype}")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+    if shape is not None and x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, not {tuple(shape)}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _one_device(**tensors) -> None:
-    found = {x.device for x in tensors.values() if x is not None}
+def _one_device(tensors) -> None:
+    found = {x.get_device() for x in tensors if x is not None}
     if len(found) > 1:
-        raise ValueError(f"tensors on several devices: {sorted(map(str, found))}")
+        raise ValueError(f"tensors on several devices: {sorted(found)} (-1: the CPU)")
 
 
 def _token_stride(x, name: str) -> int:
@@ -322,13 +322,14 @@ def _token_stride(x, name: str) -> int:
     if x.dim() != 3:
         raise ValueError(f"{name} must be [T][heads][d]")
     T, heads, d = x.shape
-    if (d > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != d):
+    st, sh, sd = x.stride()
+    if (d > 1 and sd != 1) or (heads > 1 and sh != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if T <= 1 or heads * d == 0:
         return heads * d
-    if x.stride(0) < heads * d:
+    if st < heads * d:
         raise ValueError(f"{name}: token rows overlap")
-    return int(x.stride(0))
+    return st
 
 
 def make_seqs(*, seq_offset, q, k, v, alpha, beta, state, state_slot, o, status, max_len: int, fresh=None,
@@ -340,33 +341,29 @@ def make_seqs(*, seq_offset, q, k, v, alpha, beta, state, state_slot, o, status,
     import torch
     strides = [_token_stride(x, n) for n, x in (("q", q), ("k", k), ("v", v))]
     T, Hk, dk = q.shape
-    H, dv = int(v.shape[1]), int(v.shape[2])
-    R = int(seq_offset.numel()) - 1
-    if tuple(k.shape) != (T, Hk, dk) or v.shape[0] != T:
+    Tv, H, dv = v.shape
+    R = seq_offset.numel() - 1
+    if k.shape != q.shape or Tv != T:
         raise ValueError("k must have q's shape, and v as many tokens")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k and v must have one dtype")
-    i32 = torch.int32
+    i32, f32 = torch.int32, torch.float32
+    num_slots = state.shape[0]
     _need(seq_offset, "seq_offset", i32, (R + 1,))
     _need(state_slot, "state_slot", i32, (R,))
     _need(status, "status", i32, (R,))
     _need(fresh, "fresh", torch.uint8, (R,))
-    _need(alpha, "alpha", torch.float32, (T, H))
-    _need(beta, "beta", torch.float32, (T, H))
+    _need(alpha, "alpha", f32, (T, H))
+    _need(beta, "beta", f32, (T, H))
     _need(o, "o", o.dtype, (T, H, dv))
-    _need(state, "state", state.dtype, (state.shape[0], H, dv, dk))
-    _one_device(seq_offset=seq_offset, q=q, k=k, v=v, alpha=alpha, beta=beta, state=state,
-                state_slot=state_slot, o=o, status=status, fresh=fresh)
-    s = TreewySeqs()
-    s.R, s.H, s.Hk, s.dk, s.dv, s.max_len = R, H, int(Hk), int(dk), dv, int(max_len)
-    s.qkv_dtype, s.o_dtype = _dtype_code(q, "q/k/v"), _dtype_code(o, "o")
-    s.T, s.num_slots = int(T), int(state.shape[0])
-    s.q_stride, s.k_stride, s.v_stride = strides
-    s.seq_offset, s.q, s.k, s.v = _ptr(seq_offset), _ptr(q), _ptr(k), _ptr(v)
-    s.alpha, s.beta, s.state, s.state_slot = _ptr(alpha), _ptr(beta), _ptr(state), _ptr(state_slot)
-    s.fresh, s.o, s.status = _ptr(fresh), _ptr(o), _ptr(status)
-    s.flags = int(flags) | (FLAG_STATE_BF16 if _dtype_code(state, "state") == DTYPE_BF16 else 0)
-    s._keep = (seq_offset, q, k, v, alpha, beta, state, state_slot, fresh, o, status)
+    _need(state, "state", state.dtype, (num_slots, H, dv, dk))
+    keep = (seq_offset, q, k, v, alpha, beta, state, state_slot, fresh, o, status)
+    _one_device(keep)
+    if _dtype_code(state, "state") == DTYPE_BF16:
+        flags |= FLAG_STATE_BF16
+    s = TreewySeqs(R, H, Hk, dk, dv, int(max_len), _dtype_code(q, "q/k/v"), _dtype_code(o, "o"), T, num_slots,
+                   *strides, *map(_ptr, keep), int(flags), 0)
+    s._keep = keep
     return s
 
 
@@ -416,11 +413,11 @@ def make_qk(*, q=None, k=None, q_out=None, k_out=None, norm: str = "l2", eps: fl
         a.rope_rows, a.rope_dims = int(rope.shape[0]), int(rope.shape[1])
     if status is not None:
         _need(status, "status", torch.int32)
-    _one_device(q=q, k=k, q_out=q_out, k_out=k_out, q_weight=q_weight, k_weight=k_weight, rope=rope,
-                position=position, status=status)
+    keep = (q, k, q_out, k_out, q_weight, k_weight, rope, position, status)
+    _one_device(keep)
     a.eps, a.q_scale, a.k_scale, a.interleaved = float(eps), float(q_scale), float(k_scale), int(interleaved)
     a.rope, a.position, a.status = _ptr(rope), _ptr(position), _ptr(status)
-    a._keep = (q, k, q_out, k_out, q_weight, k_weight, rope, position, status)
+    a._keep = keep
     return a
 
 
@@ -443,7 +440,7 @@ def make_slots(*, state, src, dst, status, layers: Optional[int] = None) -> Tree
     per = 1
     for n in shape[1:]:
         per *= int(n)
-    _one_device(state=state, src=src, dst=dst, status=status)
+    _one_device((state, src, dst, status))
     a = TreewySlots()
     a.n, a.layers = int(src.numel()), 1 if layers is None else int(layers)
     a.num_slots, a.slot_bytes = int(shape[0]), per * state.element_size()
