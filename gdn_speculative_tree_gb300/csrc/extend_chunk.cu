@@ -465,54 +465,43 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
 #pragma unroll
     for (int i = 0; i < 64; ++i) S[i] = 0.f;
   }
-#pragma unroll
-  for (int b = 0; b < 4; ++b) put_state16(tm, half, b, S);
-  tmem_wait_st();
-  tc_fence_before_sync();
-  warp_arrive(&cs.s_ready[half]);
   bool ok = true;
   const int n0 = 32 * half;
   for (int c = 0; c < nchunk; ++c) {
+    // the state as the left operand of S k and S q
+#pragma unroll
+    for (int b = 0; b < 4; ++b) put_state16(tm, half, b, S);
+    tmem_wait_st();
+    tc_fence_before_sync();
+    warp_arrive(&cs.s_ready[half]);
     const int sg = c & 1;
     const uint32_t ph2 = c >> 1;
     const Gates& g = cs.gates[sg];
     const int left = q.len - c * kC - n0;  // tokens of this thread's half
-    // this thread's values of V, while S k is under way: zero past the end
-    uint32_t v[16];
-    ok = wait(cs, &cs.full_v[sg], ph2);
-    {
-      const unsigned char* vt = base + sg * kStageBytes + 4 * kBox + n0 * 256 + 2 * d;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const uint32_t v0 = *reinterpret_cast<const uint16_t*>(vt + 2 * e * 256);
-        const uint32_t v1 = *reinterpret_cast<const uint16_t*>(vt + (2 * e + 1) * 256);
-        v[e] = v0 | (v1 << 16);
-      }
-      if (left < 32) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          v[e] = 2 * e + 1 < left ? v[e] : (2 * e < left ? v[e] & 0xffffu : 0u);
-      }
-    }
-    ok = ok && wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.d1_done, c);
+    ok = wait(cs, &cs.full_v[sg], ph2) && wait(cs, &cs.gates_ready[sg], ph2) && wait(cs, &cs.d1_done, c);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after_sync();
     {
-      // W = v - g (S k)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      // W = v - g (S k), with v zero past the sequence's end (each thread reads,
+      // and clears, only its own column of its half's rows)
+      unsigned char* vt = base + sg * kStageBytes + 4 * kBox + n0 * 256 + 2 * d;
+      for (int n = max(left, 0); n < 32; ++n) *reinterpret_cast<uint16_t*>(vt + n * 256) = 0;
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b, vt += 16 * 256) {
         uint32_t x[16], hi[8], lo[8];
         tmem_ld16_async(tm + kColW + n0 + 16 * b, x);
         tmem_wait16(x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float4 f = *reinterpret_cast<const float4*>(g.g + n0 + 16 * b + 4 * j);
-          const uint32_t va = v[8 * b + 2 * j], vb = v[8 * b + 2 * j + 1];
-          split_pair(fmaf(-f.x, __uint_as_float(x[4 * j]), __uint_as_float(va << 16)),
-                     fmaf(-f.y, __uint_as_float(x[4 * j + 1]), __uint_as_float(va & 0xffff0000u)), hi[2 * j], lo[2 * j]);
-          split_pair(fmaf(-f.z, __uint_as_float(x[4 * j + 2]), __uint_as_float(vb << 16)),
-                     fmaf(-f.w, __uint_as_float(x[4 * j + 3]), __uint_as_float(vb & 0xffff0000u)), hi[2 * j + 1],
-                     lo[2 * j + 1]);
+          const float fs[4] = {f.x, f.y, f.z, f.w};
+          float w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = fmaf(-fs[k], __uint_as_float(x[4 * j + k]),
+                        bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + (4 * j + k) * 256)));
+          split_pair(w[0], w[1], hi[2 * j], lo[2 * j]);
+          split_pair(w[2], w[3], hi[2 * j + 1], lo[2 * j + 1]);
         }
         // 16 tokens: hi in 8 columns, lo in 8, in place of what was just read
         tmem_st8(tm + kColW + n0 + 16 * b, hi);
@@ -527,28 +516,13 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
     ok = wait(cs, &cs.d2_done[half], c);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after_sync();
-    const bool more = c + 1 < nchunk;
 #pragma unroll
-    for (int b = 0; b < 4; b += 2) {
-      uint32_t x[16], y[16];
+    for (int b = 0; b < 4; ++b) {
+      uint32_t x[16];
       tmem_ld16_async(tm + kColD + 64 * half + 16 * b, x);
-      tmem_ld16_async(tm + kColD + 64 * half + 16 * b + 16, y);
       tmem_wait16(x);
-      tmem_wait16(y);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        S[16 * b + e] = fmaf(gC, S[16 * b + e], __uint_as_float(x[e]));
-        S[16 * b + 16 + e] = fmaf(gC, S[16 * b + 16 + e], __uint_as_float(y[e]));
-      }
-      if (more) {
-        put_state16(tm, half, b, S);
-        put_state16(tm, half, b + 1, S);
-      }
-    }
-    if (more) {
-      tmem_wait_st();
-      tc_fence_before_sync();
-      warp_arrive(&cs.s_ready[half]);
+      for (int e = 0; e < 16; ++e) S[16 * b + e] = fmaf(gC, S[16 * b + e], __uint_as_float(x[e]));
     }
     warp_arrive(&cs.gates_free[sg]);
   }
@@ -643,12 +617,9 @@ __device__ __forceinline__ void run_out(const treewy_seqs& a, ChunkSmem& cs, uns
       const int piece = t & 15;
       if (8 * piece < a.dv) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + at0 + 8 * piece;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int n = (t >> 4) + 8 * i;
-          if (n < rows)
-            *reinterpret_cast<uint4*>(out + n * step) = *reinterpret_cast<const uint4*>(tile + n * 256 + 16 * piece);
-        }
+#pragma unroll 2
+        for (int n = t >> 4; n < rows; n += 8)
+          *reinterpret_cast<uint4*>(out + n * step) = *reinterpret_cast<const uint4*>(tile + n * 256 + 16 * piece);
       }
       fence_proxy_async_smem();
     }
@@ -1073,11 +1044,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (q.len == 0) {
-    if (q.fresh && warp < kStateWarps && (t & 127) < a.dv) {
-      float S[64];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) S[i] = 0.f;
-      store_state<SB>(a, (static_cast<int64_t>(q.slot) * a.H + h) * a.dv + (t & 127), t >> 7, S);
+    if (q.fresh) {
+      const int64_t at = (static_cast<int64_t>(q.slot) * a.H + h) * a.dv * a.dk;
+      for (int i = t; i < a.dv * a.dk; i += kThreads) {
+        if constexpr (SB) reinterpret_cast<uint16_t*>(a.state)[at + i] = 0;
+        else reinterpret_cast<float*>(a.state)[at + i] = 0.f;
+      }
     }
     return;
   }
