@@ -101,13 +101,13 @@ struct ChunkSmem {
 };
 
 // A bounded wait: every wait of the CTA gives up at the same time, a second
-// and 100 us per chunk (fifteen times what one takes) after its start, or once
-// another one has.  Kept short: the roles' code together is several times the
-// instruction cache, and its size is what the chunks' time went down with.
+// and 100 us per chunk (fifteen times what one takes) after its start.  Kept
+// short: the roles' code together outgrows the instruction cache, and its size
+// is what a chunk's time has gone down with.
 __device__ __forceinline__ bool wait(ChunkSmem& cs, uint64_t* bar, uint32_t parity) {
   while (!mbar_try_wait(bar, parity & 1u)) {
-    if (*reinterpret_cast<volatile int*>(&cs.fail) || globaltimer_ns() > cs.deadline) {
-      *reinterpret_cast<volatile int*>(&cs.fail) = 1;
+    if (globaltimer_ns() > cs.deadline) {
+      cs.fail = 1;
       return false;
     }
   }
