@@ -1146,10 +1146,9 @@ cudaError_t launch(const treewy_seqs& a, const ExtendMaps& m, cudaStream_t strea
 }  // namespace
 
 cudaError_t launch_extend_chunk(const treewy_seqs& a, const ExtendMaps& m, cudaStream_t stream) {
-  const bool f32 = a.o_dtype == TREEWY_DTYPE_F32;
-  if (a.flags & TREEWY_FLAG_STATE_BF16)
-    return f32 ? launch<true, true>(a, m, stream) : launch<true, false>(a, m, stream);
-  return f32 ? launch<false, true>(a, m, stream) : launch<false, false>(a, m, stream);
+  if (a.flags & TREEWY_FLAG_STATE_BF16)  // with bf16 outputs only
+    return a.o_dtype == TREEWY_DTYPE_F32 ? cudaErrorInvalidValue : launch<true, false>(a, m, stream);
+  return a.o_dtype == TREEWY_DTYPE_F32 ? launch<false, true>(a, m, stream) : launch<false, false>(a, m, stream);
 }
 
 }  // namespace treewy

@@ -70,10 +70,17 @@ treewy_status validate_seqs(const treewy_seqs* s) {
 // 151 us.
 int chunked_len(const treewy_seqs& s) { return int64_t(s.R) * s.H >= 128 ? 9 : 24; }
 
-// Whether the chunked kernel takes the batch (s: strides resolved).
+// Whether the chunked kernel takes the batch (s: strides resolved).  f32
+// outputs over a bf16 pool go token by token: a product of split operands is
+// a few 2^-18 off, so that one value in 500 of the next call's state rounds to
+// the other side, 2^-8 away, and its f32 outputs (70 tokens, decays above
+// 0.97) differ by 7e-5 in the norm, where f32 sums throughout keep them within
+// 6e-5 (a flip in 10^4).  It costs time: 3191 us against 355 for 4096 tokens of
+// 32 heads of 128, 97 against 36 for 300 tokens of 8 heads of 64.
 bool use_chunks(const treewy_seqs& s) {
+  const bool rounded_state = (s.flags & TREEWY_FLAG_STATE_BF16) != 0 && s.o_dtype == TREEWY_DTYPE_F32;
   auto rows_on16 = [](const void* p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; };
-  return s.qkv_dtype == TREEWY_DTYPE_BF16 && s.dk % 8 == 0 && s.dv % 8 == 0 && s.T > 0 &&
+  return s.qkv_dtype == TREEWY_DTYPE_BF16 && s.dk % 8 == 0 && s.dv % 8 == 0 && s.T > 0 && !rounded_state &&
          s.max_len >= chunked_len(s) && (s.flags & TREEWY_FLAG_FORCE_GENERIC) == 0 &&
          rows_on16(s.q, s.q_stride) && rows_on16(s.k, s.k_stride) && rows_on16(s.v, s.v_stride) &&
          aligned(s.o, 16);

@@ -289,7 +289,8 @@ treewy_status treewy_selftest_wait_timeout(int32_t* status, uint32_t limit_us,
  *   o           f32 or bf16 (o_dtype) [T][H][dv]
  *   status      int32 [R], bits OR-ed in
  * q, k, v and o are aligned to their element size only; rows and bases that
- * are multiples of 16 bytes take the wide loads.
+ * are multiples of 16 bytes take the wide loads.  o and status overlap nothing
+ * else.
  */
 typedef struct treewy_seqs {
   int32_t R;
@@ -334,6 +335,15 @@ typedef struct treewy_seqs {
  * negative or above max_len TREEWY_STATUS_TOO_MANY_NODES, a slot outside the
  * pool TREEWY_STATUS_BAD_SLOT; that sequence's outputs and state stay as they
  * are.
+ *
+ * Long sequences of bf16 q, k and v with 16-byte rows run in chunks of 64
+ * tokens on the tensor cores, f32 operands as two bf16 terms each (a result
+ * is a few 2^-17 off); other calls run token by token in f32, and so do f32
+ * outputs over a bf16 pool, where such differences would turn roundings of
+ * the next call's state.  In a chunk a NaN or an infinity among a token's
+ * inputs can reach the outputs of that sequence and head from up to 63 tokens
+ * before it on.  TREEWY_STATUS_TIMEOUT: a wait of the kernel gave up; the
+ * sequence's outputs are partly written and its state may be too.
  */
 treewy_status treewy_extend(const treewy_seqs* seqs, cudaStream_t stream);
 

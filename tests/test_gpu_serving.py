@@ -306,6 +306,26 @@ def test_extend_feeds_verification(cuda_lib):
     assert_near(c.pool, f64(d.pool), 1e-3)
 
 
+@pytest.mark.parametrize("n", [1, 26, 70])
+def test_extend_f32_outputs_over_a_rounded_state(cuda_lib, n):
+    """A second call on the bf16 state that the first one rounded, its outputs in f32.
+
+    An error e of the state lets a share e / 2^-8 of its values, doubled, round the other way, each 2^-8 off:
+    eight f32 roundings, e = 2^-21 at most and 2^-22 in the mean, give sqrt(2^-13) 2^-8 of the state, and of the
+    outputs read from it, in the norm: 2^-14.5, below 2^-14."""
+    c = Case([n, n], H=8, alpha=(0.97, 0.999), out="f32", pool="bf16", seed=17)
+    S = f64(c.pool)
+    ref = np.zeros(tuple(c.o.shape))
+    for _ in range(2):
+        c.run()
+        for r in range(2):
+            s, rows = int(c.slot[r]), slice(r * n, (r + 1) * n)
+            ref[rows], new = orc.extend(S[s], f64(c.q[rows]), f64(c.k[rows]), f64(c.v[rows]), f64(c.alpha[rows]),
+                                        f64(c.beta[rows]))
+            S[s] = f64(torch.from_numpy(new).to(torch.bfloat16))
+    assert np.linalg.norm(f64(c.o) - ref) <= 2.0 ** -14 * np.linalg.norm(ref)
+
+
 # ------------------------------------------------------------------ qk_norm
 
 def qk_case(T, Hq, Hk, d, dtype="bf16", norm="l2", rope=0, interleaved=False, repeat=(1, 1), pad=0, shift=0,
