@@ -11,8 +11,9 @@
 // and the other element of a rotated pair is one shuffle away or in the same
 // lane.  A warp takes several heads of one token and side (q or k), so that
 // the weights and the token's cosines and sines are loaded once for all of
-// them.  Rows that this does not fit (odd sizes, unaligned rows, pairs that
-// cross an eight at an odd place) go to one warp each, element by element.
+// them.  Where a pair's elements are not a multiple of eight apart (ODD), the
+// other one is loaded by itself.  Rows that this does not fit (odd sizes,
+// unaligned rows) go to one warp each, element by element.
 #include "treewy_device.cuh"
 #include "treewy_internal.h"
 
@@ -100,9 +101,16 @@ __device__ __forceinline__ void load8_f32(const float* p, float (&x)[8]) {
   x[4] = g.x; x[5] = g.y; x[6] = g.z; x[7] = g.w;
 }
 
+// From element c of a rotated pair to the other one.
+__device__ __forceinline__ int pair_step(const treewy_qk& a, int c) {
+  if (a.interleaved) return (c & 1) ? -1 : 1;
+  return c < a.rope_dims / 2 ? a.rope_dims / 2 : -(a.rope_dims / 2);
+}
+
 // LANES lanes per head, eight elements each; a warp takes UNROLL passes of
 // 32 / LANES heads of one token's q or k, all loaded before the first is used.
-template <typename T, int LANES, int UNROLL, int THREADS>
+// ODD: pairs at any distance, eights that the rotation ends within.
+template <typename T, int LANES, int UNROLL, int THREADS, bool ODD>
 __global__ void __launch_bounds__(THREADS, 896 / THREADS)
     qk_norm_kernel(const treewy_qk a, int q_units, int units, float mean) {
   after_previous();
@@ -117,7 +125,7 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
   }
   const int c0 = 8 * lane;
   const bool mine = c0 < a.d;
-  // half is a multiple of 8: a pair's other eight are half / 8 lanes on
+  // half is a multiple of 8 (but where ODD): a pair's other eight are half / 8 lanes on
   const int half = a.rope_dims / 2;
   const bool in_rope = c0 < a.rope_dims, low = c0 < half;
   const int other = in_rope ? (low ? lane + half / 8 : lane - half / 8) : lane;
@@ -130,8 +138,17 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
         (t * (isq ? a.q_stride : a.k_stride) + static_cast<int64_t>(h0) * a.d + c0) * static_cast<int64_t>(sizeof(T));
     const int step = kPass * a.d * static_cast<int>(sizeof(T));
     Raw8<T> raw[UNROLL];
+    T far[ODD ? UNROLL : 1][8];                       // ODD: the pairs' other elements
 #pragma unroll
     for (int i = 0; i < UNROLL; ++i) {
+      if constexpr (ODD) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          far[i][e] = static_cast<T>(0.f);
+          if (h0 + i * kPass < heads && c0 + e < a.rope_dims)
+            far[i][e] = reinterpret_cast<const T*>(in + static_cast<int64_t>(i) * step)[pair_step(a, c0 + e) + e];
+        }
+      }
 #pragma unroll
       for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) {
         raw[i].w[k] = make_uint4(0u, 0u, 0u, 0u);
@@ -145,7 +162,16 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
     const float scale = isq ? a.q_scale : a.k_scale;
 #pragma unroll
     for (int e = 0; e < 8; ++e) wc[e] = scale, ws[e] = 0.f;
-    if (in_rope) {
+    if (ODD) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (c0 + e >= a.rope_dims) continue;
+        const int by = pair_step(a, c0 + e), i = a.interleaved ? (c0 + e) / 2 : by > 0 ? c0 + e : c0 + e - half;
+        const float sn = by > 0 ? -tab[half + i] : tab[half + i];
+        wc[e] *= tab[i];
+        ws[e] = scale * sn * (weight != nullptr ? weight[c0 + e + by] : 1.f);
+      }
+    } else if (in_rope) {
       float cs[8], sn[8], v[8];
       if (a.interleaved) {
         const float4 c = *reinterpret_cast<const float4*>(tab + c0 / 2);
@@ -191,7 +217,10 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
       const float f = inv_norm(sum, mean, a.eps);
-      if (a.rope_dims > 0) {
+      if constexpr (ODD) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = f * fmaf(static_cast<float>(far[i][e]), ws[e], x[e] * wc[e]);
+      } else if (a.rope_dims > 0) {
         Raw8<T> pair = raw[i];
         if (!a.interleaved) {
 #pragma unroll
@@ -276,14 +305,14 @@ __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(const treewy_qk a
     for (int e = lane; e < a.d; e += 32) out[c * a.d + e] = static_cast<T>(y[e]);
 }
 
-template <typename T, int LANES, int UNROLL, int THREADS>
+template <typename T, int LANES, int UNROLL, int THREADS, bool ODD>
 cudaError_t launch_passes(const treewy_qk& a, cudaStream_t stream) {
   constexpr int kHeads = UNROLL * 32 / LANES;
   const int q_units = (a.Hq + kHeads - 1) / kHeads, units = q_units + (a.Hk + kHeads - 1) / kHeads;
   const dim3 grid(static_cast<unsigned>((a.T + THREADS / 32 - 1) / (THREADS / 32)),
                   static_cast<unsigned>(units < 65535 ? units : 65535));
   const float mean = a.norm == TREEWY_NORM_RMS ? 1.0f / static_cast<float>(a.d) : 1.f;
-  return launch_after(qk_norm_kernel<T, LANES, UNROLL, THREADS>, grid, THREADS, stream, a, q_units, units, mean);
+  return launch_after(qk_norm_kernel<T, LANES, UNROLL, THREADS, ODD>, grid, THREADS, stream, a, q_units, units, mean);
 }
 
 template <typename T, int LANES>
@@ -292,9 +321,13 @@ cudaError_t launch(const treewy_qk& a, cudaStream_t stream) {
   // CTA, so that a warp's place is filled as soon as it is done (32768 tokens
   // of 18 bf16 heads of 256: 122 us, 143 us with two warps per CTA).  Few: the
   // rows spread over more warps (256 tokens of 32 heads of 128: 2.3 us).
+  // Odd pairs: one shape for both (8001 tokens of 24 bf16 heads of 80, 20 of
+  // them rotated: 45 us, 67 us element by element; more heads per warp 40 to
+  // 42, but f32 53 to 70 for 47).
   constexpr int kMany = sizeof(T) == 2 ? 8 : 4;
-  return a.T * (a.Hq + a.Hk) >= int64_t(152) * 64 * (32 / LANES) ? launch_passes<T, LANES, kMany, 32>(a, stream)
-                                                               : launch_passes<T, LANES, 2, 64>(a, stream);
+  if (a.rope_dims % (a.interleaved ? 8 : 16) != 0) return launch_passes<T, LANES, 2, 64, true>(a, stream);
+  return a.T * (a.Hq + a.Hk) >= int64_t(152) * 64 * (32 / LANES) ? launch_passes<T, LANES, kMany, 32, false>(a, stream)
+                                                               : launch_passes<T, LANES, 2, 64, false>(a, stream);
 }
 
 template <typename T>
@@ -303,7 +336,7 @@ cudaError_t launch_typed(const treewy_qk& a, cudaStream_t stream) {
   auto on16 = [](const void* p, int64_t stride) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (stride * sizeof(T)) % 16 == 0;
   };
-  bool wide = a.d % 8 == 0 && a.rope_dims % (a.interleaved ? 8 : 16) == 0 &&
+  bool wide = a.d % 8 == 0 &&
               reinterpret_cast<uintptr_t>(a.rope) % 16 == 0 && reinterpret_cast<uintptr_t>(a.q_weight) % 16 == 0 &&
               reinterpret_cast<uintptr_t>(a.k_weight) % 16 == 0;
   if (a.Hq > 0) wide = wide && on16(a.q, a.q_stride) && on16(a.q_out, 0);
