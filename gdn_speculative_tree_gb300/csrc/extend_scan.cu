@@ -20,6 +20,8 @@
 // while the loads of the next 16 are in flight.  Every token costs a sweep of
 // the registers, so it is bound by FMA issue and serves the sizes and types
 // that the chunked kernel does not take.
+#include <type_traits>
+
 #include "treewy_device.cuh"
 #include "treewy_internal.h"
 
@@ -28,6 +30,7 @@ namespace {
 
 constexpr int kDecodeWarps = 1, kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kStage = 16;  // tokens staged at a time
+constexpr int kBlock = 4;   // tokens that take one sweep of the state
 constexpr unsigned kFull = 0xffffffffu;
 
 struct Seq {
@@ -196,14 +199,13 @@ __device__ __forceinline__ void unpack_row(const RawRow<SB>& r, float (&x)[16]) 
 // at most.  WIDE: every load of the state, q and k is a whole piece; the rows
 // then wait in registers as they are stored, all of them in flight at once,
 // and are taken one after the other.
-template <int RPT, bool SB, bool WIDE>
+template <int RPT, bool SB, bool QB, bool WIDE>
 __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seqs a) {
   after_previous();
   constexpr int V = SB ? 8 : 4;
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int l = threadIdx.x & 7;
   const int first = static_cast<int>(blockIdx.y) * (4 * kDecodeWarps * RPT);
-  const bool qb = a.qkv_dtype == TREEWY_DTYPE_BF16;
   const Seq s = load_seq(a, r);
   if (s.flags) {
     if (threadIdx.x == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
@@ -229,12 +231,12 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seq
   float k[16], q[16], v[RPT], alpha = 1.f, beta = 0.f, kq = 0.f;
   if (s.len > 0) {
     const int hk = h / (a.H / a.Hk);
-    load_row<V, WIDE>(a.k, qb, t * a.k_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, k);
-    load_row<V, WIDE>(a.q, qb, t * a.q_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, q);
+    load_row<V, WIDE>(a.k, QB, t * a.k_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, k);
+    load_row<V, WIDE>(a.q, QB, t * a.q_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, q);
 #pragma unroll
     for (int j = 0; j < RPT; ++j) {
       const int row = group_row<RPT>(first, j);
-      v[j] = row < a.dv ? load_qkv(a.v, t * a.v_stride + static_cast<int64_t>(h) * a.dv + row, qb) : 0.f;
+      v[j] = row < a.dv ? load_qkv(a.v, t * a.v_stride + static_cast<int64_t>(h) * a.dv + row, QB) : 0.f;
     }
     alpha = __ldg(a.alpha + t * a.H + h);
     beta = __ldg(a.beta + t * a.H + h);
@@ -273,25 +275,47 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seq
 }
 
 // Staged tokens, f32: 8 CL columns of k and q (zero beyond dk) and the CTA's
-// rows of v (zero beyond dv).
+// rows of v (zero beyond dv); behind the sequence's end k, q, v and beta are
+// zero and alpha is one.  The factors of a block of kBlock tokens, with G_n the
+// product of the decays from the block's first token to n:
 template <int CL, int ROWS>
 struct Stage {
   float k[kStage][8 * CL];
   float q[kStage][8 * CL];
   float v[kStage][ROWS];
-  float alpha[kStage], beta[kStage], kq[kStage];
+  float kk[kStage][kBlock];    // beta_n (G_n / G_j) k_n . k_j   (j < n)
+  float kq[kStage][kBlock];    // (G_n / G_j) q_n . k_j          (j <= n)
+  float dec[kStage];           // G of the block's last token / G_n
+  float gate[kStage];          // G_n
+  float alpha[kStage], beta[kStage];
 };
+
+// Sums over the eight lanes of a row group of eight values: lane l gets value l's.
+__device__ __forceinline__ float sum8_each(const float (&x)[8], int l) {
+  float y[4], z[2];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float mine = (l & 4) ? x[e + 4] : x[e], other = (l & 4) ? x[e] : x[e + 4];
+    y[e] = mine + __shfl_xor_sync(kFull, other, 4);
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float mine = (l & 2) ? y[e + 2] : y[e], other = (l & 2) ? y[e] : y[e + 2];
+    z[e] = mine + __shfl_xor_sync(kFull, other, 2);
+  }
+  const float mine = (l & 1) ? z[1] : z[0], other = (l & 1) ? z[0] : z[1];
+  return mine + __shfl_xor_sync(kFull, other, 1);
+}
 
 // One (sequence, head) and THREADS / 8 x RPT of its rows per CTA, CL columns
 // of a row per lane, any number of tokens.
-template <int RPT, bool SB, bool WIDE, int CL, int THREADS>
+template <int RPT, bool SB, bool QB, bool WIDE, int CL, int THREADS>
 __global__ void __launch_bounds__(THREADS) scan_kernel(const treewy_seqs a) {
-  constexpr int V = SB ? 8 : 4, kRows = THREADS / 8 * RPT, kCols = 8 * CL;
+  constexpr int V = 4, kRows = THREADS / 8 * RPT, kCols = 8 * CL;
   __shared__ __align__(16) Stage<CL, kRows> st;
   after_previous();
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int tid = threadIdx.x, l = tid & 7;
-  const bool qb = a.qkv_dtype == TREEWY_DTYPE_BF16;
   const Seq s = load_seq(a, r);
   if (s.flags) {
     if (tid == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
@@ -315,27 +339,36 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const treewy_seqs a) {
   const int hk = h / (a.H / a.Hk);
   constexpr int kPer = kStage * kCols / THREADS;  // staged elements of k (and q) per thread
   constexpr int kPerV = kStage * kRows / THREADS;
-  float nk[kPer], nq[kPer], nv[kPerV], ngate = 0.f;
+  // as they are stored: a conversion here would wait for its load
+  using Raw = std::conditional_t<QB, uint16_t, float>;
+  const Raw *pk = static_cast<const Raw*>(a.k), *pq = static_cast<const Raw*>(a.q), *pv = static_cast<const Raw*>(a.v);
+  auto value = [](Raw x) {
+    if constexpr (QB) return bf16_bits_to_float(x);
+    else return x;
+  };
+  Raw nk[kPer], nq[kPer], nv[kPerV];
+  float ngate = 0.f;
   auto fetch = [&](int t0) {  // the stage from token t0 on, into registers
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = tid + i * THREADS, n = e / kCols, c = e % kCols;
       const int64_t t = s.tok0 + t0 + n;
-      nk[i] = nq[i] = 0.f;
+      nk[i] = nq[i] = 0;
       if (t0 + n < s.len && c < a.dk) {
-        nk[i] = load_qkv(a.k, t * a.k_stride + static_cast<int64_t>(hk) * a.dk + c, qb);
-        nq[i] = load_qkv(a.q, t * a.q_stride + static_cast<int64_t>(hk) * a.dk + c, qb);
+        nk[i] = __ldg(pk + t * a.k_stride + static_cast<int64_t>(hk) * a.dk + c);
+        nq[i] = __ldg(pq + t * a.q_stride + static_cast<int64_t>(hk) * a.dk + c);
       }
     }
 #pragma unroll
     for (int i = 0; i < kPerV; ++i) {
       const int e = tid + i * THREADS, n = e / kRows, c = first + e % kRows;
-      nv[i] = 0.f;
+      nv[i] = 0;
       if (t0 + n < s.len && c < a.dv)
-        nv[i] = load_qkv(a.v, (s.tok0 + t0 + n) * a.v_stride + static_cast<int64_t>(h) * a.dv + c, qb);
+        nv[i] = __ldg(pv + (s.tok0 + t0 + n) * a.v_stride + static_cast<int64_t>(h) * a.dv + c);
     }
     if (tid < 2 * kStage) {
       const int n = tid & (kStage - 1);
+      ngate = tid < kStage ? 1.f : 0.f;
       const float* g = tid < kStage ? a.alpha : a.beta;
       if (t0 + n < s.len) ngate = __ldg(g + (s.tok0 + t0 + n) * a.H + h);
     }
@@ -345,62 +378,97 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const treewy_seqs a) {
     __syncthreads();  // the last stage has been read
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      (&st.k[0][0])[tid + i * THREADS] = nk[i];
-      (&st.q[0][0])[tid + i * THREADS] = nq[i];
+      (&st.k[0][0])[tid + i * THREADS] = value(nk[i]);
+      (&st.q[0][0])[tid + i * THREADS] = value(nq[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kPerV; ++i) (&st.v[0][0])[tid + i * THREADS] = nv[i];
+    for (int i = 0; i < kPerV; ++i) (&st.v[0][0])[tid + i * THREADS] = value(nv[i]);
     if (tid < kStage) st.alpha[tid] = ngate;
     else if (tid < 2 * kStage) st.beta[tid - kStage] = ngate;
     __syncthreads();
     fetch(t0 + kStage);
-    if (tid < 8 * kStage) {  // k . q, eight lanes per token
-      float k[CL], q[CL], kq = 0.f;
-      load_row<V, true>(st.k[tid >> 3], false, 0, kCols, l, k);
-      load_row<V, true>(st.q[tid >> 3], false, 0, kCols, l, q);
+    const int m = min(kStage, s.len - t0);
+    // The blocks' factors: 10 products q_n . k_j and 6 k_n . k_j each, eight lanes per product.
+#pragma unroll 1
+    for (int p = tid >> 3; p < kStage / kBlock * 16; p += THREADS / 8) {
+      const int b = p / 16 * kBlock, e = p % 16;
+      if (b >= m) break;  // whole warps: 4 products of one block each
+      const bool isq = e < 10;
+      const int f = isq ? e : e - 10;
+      const int n = isq ? (f >= 6 ? 3 : f >= 3 ? 2 : f >= 1 ? 1 : 0) : (f >= 3 ? 3 : f >= 1 ? 2 : 1);
+      const int j = f - (isq ? n * (n + 1) / 2 : n * (n - 1) / 2);
+      float x[CL], y[CL], sum[2] = {0.f, 0.f};
+      load_row<V, true>(isq ? st.q[b + n] : st.k[b + n], false, 0, kCols, l, x);
+      load_row<V, true>(st.k[b + j], false, 0, kCols, l, y);
 #pragma unroll
-      for (int c = 0; c < CL; ++c) kq = fmaf(k[c], q[c], kq);
-      kq = sum8(kq);
-      if (l == 0) st.kq[tid >> 3] = kq;
+      for (int c = 0; c < CL; ++c) sum[c & 1] = fmaf(x[c], y[c], sum[c & 1]);
+      float z = sum8(sum[0] + sum[1]);
+      if (!isq) z *= st.beta[b + n];
+      for (int i = j + 1; i <= n; ++i) z *= st.alpha[b + i];
+      if (l == 0) (isq ? st.kq : st.kk)[b + n][j] = z;
+    }
+    if (tid < kStage) {
+      const int b = tid & ~(kBlock - 1);
+      float g = st.alpha[b], d = 1.f;
+      for (int i = b + 1; i < b + kBlock; ++i) {
+        if (i <= tid) g *= st.alpha[i];
+        else d *= st.alpha[i];
+      }
+      st.gate[tid] = g;
+      st.dec[tid] = d;
     }
     __syncthreads();
-    const int m = min(kStage, s.len - t0);
-    // A token's way through the state is a chain of CL / 4 FMAs, three shuffles
-    // and an update per row; the next token's k, q and v are on their way
-    // meanwhile.
-    float k[2][CL], q[2][CL], v[2][RPT];
-    auto next = [&](int n, int slot) {
-      load_row<V, true>(st.k[n], false, 0, kCols, l, k[slot]);
-      load_row<V, true>(st.q[n], false, 0, kCols, l, q[slot]);
-#pragma unroll
-      for (int j = 0; j < RPT; ++j) v[slot][j] = st.v[n][group_row<RPT>(0, j)];
-    };
-    next(0, 0);
 #pragma unroll 1
-    for (int n0 = 0; n0 < m; n0 += 2) {
+    for (int b = 0; b < m; b += kBlock) {
+      float dot[RPT][2 * kBlock];  // S k_n, then S q_n: this lane's columns
+      float k[kBlock][CL];
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int n = n0 + p;
-        if (n >= m) break;
-        const float alpha = st.alpha[n], beta = st.beta[n], kq = st.kq[n];
-        next(min(n + 1, kStage - 1), p ^ 1);
+      for (int n = 0; n < kBlock; ++n) {
+        float q[CL];
+        load_row<V, true>(st.k[b + n], false, 0, kCols, l, k[n]);
+        load_row<V, true>(st.q[b + n], false, 0, kCols, l, q);
 #pragma unroll
         for (int j = 0; j < RPT; ++j) {
-          float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f};
+          dot[j][n] = S[j][0] * k[n][0];
+          dot[j][kBlock + n] = S[j][0] * q[0];
 #pragma unroll
-          for (int c = 0; c < CL; ++c) {
-            sk[c & 3] = fmaf(S[j][c], k[p][c], sk[c & 3]);
-            sq[c & 3] = fmaf(S[j][c], q[p][c], sq[c & 3]);
-            S[j][c] *= alpha;
+          for (int c = 1; c < CL; ++c) {
+            dot[j][n] = fmaf(S[j][c], k[n][c], dot[j][n]);
+            dot[j][kBlock + n] = fmaf(S[j][c], q[c], dot[j][kBlock + n]);
           }
-          const float skt = sum8((sk[0] + sk[1]) + (sk[2] + sk[3]));
-          const float sqt = sum8((sq[0] + sq[1]) + (sq[2] + sq[3]));
-          const float u = beta * (v[p][j] - alpha * skt);
+        }
+      }
+      // lane l < 4: token l's S k, the others token l - 4's S q
+      const int mine = b + (l & (kBlock - 1));
+      const float gate = st.gate[mine], beta = st.beta[mine], last = st.gate[b + kBlock - 1];
+      const float4 m4 = *reinterpret_cast<const float4*>(st.kq[mine]);
+      const float mq[kBlock] = {m4.x, m4.y, m4.z, m4.w};
+      float u[RPT][kBlock];
 #pragma unroll
-          for (int c = 0; c < CL; ++c) S[j][c] = fmaf(u, k[p][c], S[j][c]);
-          const int row = group_row<RPT>(first, j);
-          if (l == 0 && row < a.dv)
-            store_o(a, ((s.tok0 + t0 + n) * a.H + h) * a.dv + row, fmaf(kq, u, alpha * sqt));
+      for (int j = 0; j < RPT; ++j) {
+        float y = gate * sum8_each(dot[j], l);
+        const float rhs = mine < m ? beta * (st.v[mine][group_row<RPT>(0, j)] - y) : 0.f;
+#pragma unroll
+        for (int n = 0; n < kBlock; ++n) {
+          u[j][n] = __shfl_sync(kFull, rhs, n, 8);
+          if (b + n < m) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) u[j][n] = fmaf(-st.kk[b + n][i], u[j][i], u[j][n]);
+          }
+          if (n <= (l & (kBlock - 1))) y = fmaf(mq[n], u[j][n], y);
+        }
+        const int row = group_row<RPT>(first, j);
+        if (l >= kBlock && mine < m && row < a.dv)
+          store_o(a, ((s.tok0 + t0 + mine) * a.H + h) * a.dv + row, y);
+      }
+#pragma unroll
+      for (int n = 0; n < kBlock; ++n) {
+        const float dec = st.dec[b + n];
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+          const float w = dec * u[j][n];
+#pragma unroll
+          for (int c = 0; c < CL; ++c) S[j][c] = fmaf(w, k[n][c], n == 0 ? last * S[j][c] : S[j][c]);
         }
       }
     }
@@ -412,33 +480,33 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const treewy_seqs a) {
   }
 }
 
-template <int RPT, bool SB, bool WIDE>
+template <int RPT, bool SB, bool QB, bool WIDE>
 cudaError_t launch_decode(const treewy_seqs& a, cudaStream_t stream) {
   constexpr int kRows = 4 * kDecodeWarps * RPT;
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
                   static_cast<unsigned>((a.dv + kRows - 1) / kRows));
-  return launch_after(decode_kernel<RPT, SB, WIDE>, grid, kDecodeThreads, stream, a);
+  return launch_after(decode_kernel<RPT, SB, QB, WIDE>, grid, kDecodeThreads, stream, a);
 }
 
-template <int RPT, bool SB, bool WIDE, int CL, int THREADS>
+template <int RPT, bool SB, bool QB, bool WIDE, int CL, int THREADS>
 cudaError_t launch_scan(const treewy_seqs& a, cudaStream_t stream) {
   constexpr int kRows = THREADS / 8 * RPT;
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
                   static_cast<unsigned>((a.dv + kRows - 1) / kRows));
-  return launch_after(scan_kernel<RPT, SB, WIDE, CL, THREADS>, grid, THREADS, stream, a);
+  return launch_after(scan_kernel<RPT, SB, QB, WIDE, CL, THREADS>, grid, THREADS, stream, a);
 }
 
-template <bool SB, bool WIDE>
+template <bool SB, bool QB, bool WIDE>
 cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
   const int64_t heads = static_cast<int64_t>(a.R) * a.H;
   if (a.max_len <= 1)  // a quarter of a head per CTA, or less while that leaves SMs idle
-    return 4 * heads >= 304 ? launch_decode<4, SB, WIDE>(a, stream) : launch_decode<1, SB, WIDE>(a, stream);
+    return 4 * heads >= 304 ? launch_decode<4, SB, QB, WIDE>(a, stream) : launch_decode<1, SB, QB, WIDE>(a, stream);
   // A whole head per CTA, or 16 of its rows while that leaves SMs idle (the
   // chain of a row is then alone on its quarter of an SM); half as many columns
   // per lane for small keys.
   if (heads >= 304)
-    return a.dk <= 64 ? launch_scan<4, SB, WIDE, 8, 256>(a, stream) : launch_scan<4, SB, WIDE, 16, 256>(a, stream);
-  return a.dk <= 64 ? launch_scan<1, SB, WIDE, 8, 128>(a, stream) : launch_scan<1, SB, WIDE, 16, 128>(a, stream);
+    return a.dk <= 64 ? launch_scan<4, SB, QB, WIDE, 8, 256>(a, stream) : launch_scan<4, SB, QB, WIDE, 16, 256>(a, stream);
+  return a.dk <= 64 ? launch_scan<1, SB, QB, WIDE, 8, 128>(a, stream) : launch_scan<1, SB, QB, WIDE, 16, 128>(a, stream);
 }
 
 }  // namespace
@@ -454,8 +522,12 @@ cudaError_t launch_extend_scan(const treewy_seqs& a, cudaStream_t stream) {
   const int v = sb ? 8 : 4;
   const int64_t piece = (v * e < 16) ? v * e : 16;
   const bool wide = a.dk % v == 0 && rows_on(a.q, a.q_stride, piece) && rows_on(a.k, a.k_stride, piece);
-  if (sb) return wide ? launch<true, true>(a, stream) : launch<true, false>(a, stream);
-  return wide ? launch<false, true>(a, stream) : launch<false, false>(a, stream);
+  if (e == 2) {
+    if (sb) return wide ? launch<true, true, true>(a, stream) : launch<true, true, false>(a, stream);
+    return wide ? launch<false, true, true>(a, stream) : launch<false, true, false>(a, stream);
+  }
+  if (sb) return wide ? launch<true, false, true>(a, stream) : launch<true, false, false>(a, stream);
+  return wide ? launch<false, false, true>(a, stream) : launch<false, false, false>(a, stream);
 }
 
 }  // namespace treewy
