@@ -11,15 +11,32 @@
 // share a row of S (each holds 16 of its dk columns, in pieces of 16 bytes of
 // the pool, so that a warp's load covers whole 128-byte lines), a warp holds
 // four rows per register row, and dot products over a row are three shuffles.
+// The type of q, k and v is a template argument: behind a branch on it every
+// load would be followed by its conversion, one load's latency after the other
+// (64 tokens x 32 heads on a bf16 pool: 25 us, 32 with the branch).
 //
-// decode_kernel: at most one token per sequence.  Its time is the state's
-// way in and out of HBM (2 x 64 KB per f32 head against 1.3 KB of everything
-// else); nothing depends on the state's load but the token's own arithmetic.
+// decode_kernel: at most one token per sequence, a warp per CTA and 16 rows
+// per warp.  Its time is the state's way in and out of HBM (2 x 64 KB per f32
+// head against 1.3 KB of everything else); nothing depends on the state's load
+// but the token's own arithmetic.  256 tokens x 32 heads, f32: 178 us, 6.1 TB/s.
 //
-// scan_kernel: any number of tokens, staged 16 at a time in shared memory
-// while the loads of the next 16 are in flight.  Every token costs a sweep of
-// the registers, so it is bound by FMA issue and serves the sizes and types
-// that the chunked kernel does not take.
+// few_kernel: the same for up to 16 tokens (2048 heads x 4 tokens: 78 us, 92
+// to 126 us by the staged kernel below), bound by the chain of shuffles.
+//
+// scan_kernel: any number of tokens, for the sizes and types that the chunked
+// kernel does not take.  Four tokens take one sweep of the state: with G_n the
+// product of the decays from the first of them to n,
+//
+//   u_n = beta_n (v_n - G_n S k_n) - sum_{j<n} beta_n (G_n/G_j) (k_n . k_j) u_j,
+//   o_n = G_n S q_n + sum_{j<=n} (G_n/G_j) (q_n . k_j) u_j,
+//   S <- G_4 S + sum_j (G_4/G_j) u_j k_j^T
+//
+// (the quotients as products of the decays between, so that a decay of zero is
+// right), which turns eight sums over a row's lanes into seven shuffles for
+// all four tokens and one chain per four tokens.  Four warps of a CTA stage
+// the next 16 tokens and their blocks' products meanwhile.  Bound by issue and
+// by the reads of k and q from shared memory: 4096 tokens of 32 heads 1133 us
+// (3262 us a token at a time, staged by the warps that use it).
 #include <type_traits>
 
 #include "treewy_device.cuh"
@@ -30,6 +47,7 @@ namespace {
 
 constexpr int kDecodeWarps = 1, kDecodeThreads = 32 * kDecodeWarps;
 constexpr int kStage = 16;  // tokens staged at a time
+constexpr int kPrep = 128;  // threads that stage them
 constexpr int kBlock = 4;   // tokens that take one sweep of the state
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -274,6 +292,85 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seq
   }
 }
 
+// The same split for a few tokens: S in f32 registers over all of them, the
+// next token's rows on their way meanwhile.
+template <int RPT, bool SB, bool QB, bool WIDE>
+__global__ void __launch_bounds__(kDecodeThreads) few_kernel(const treewy_seqs a) {
+  after_previous();
+  constexpr int V = SB ? 8 : 4;
+  const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
+  const int l = threadIdx.x & 7;
+  const int first = static_cast<int>(blockIdx.y) * (4 * kDecodeWarps * RPT);
+  const Seq s = load_seq(a, r);
+  if (s.flags) {
+    if (threadIdx.x == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
+    return;
+  }
+  if (s.len == 0 && !s.fresh) return;
+  const int64_t block = (static_cast<int64_t>(s.slot) * a.H + h) * a.dv;
+  float S[RPT][16];
+#pragma unroll
+  for (int j = 0; j < RPT; ++j) {
+    const int row = group_row<RPT>(first, j);
+    if (!s.fresh && row < a.dv) {
+      load_row<V, WIDE>(a.state, SB, (block + row) * a.dk, a.dk, l, S[j]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) S[j][c] = 0.f;
+    }
+  }
+  const int hk = h / (a.H / a.Hk);
+  float k[2][16], q[2][16], v[2][RPT], alpha[2], beta[2];
+  auto next = [&](int n, int slot) {
+    const int64_t t = s.tok0 + n;
+    load_row<V, WIDE>(a.k, QB, t * a.k_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, k[slot]);
+    load_row<V, WIDE>(a.q, QB, t * a.q_stride + static_cast<int64_t>(hk) * a.dk, a.dk, l, q[slot]);
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) {
+      const int row = group_row<RPT>(first, j);
+      v[slot][j] = row < a.dv ? load_qkv(a.v, t * a.v_stride + static_cast<int64_t>(h) * a.dv + row, QB) : 0.f;
+    }
+    alpha[slot] = __ldg(a.alpha + t * a.H + h);
+    beta[slot] = __ldg(a.beta + t * a.H + h);
+  };
+  if (s.len > 0) next(0, 0);
+#pragma unroll 1
+  for (int n0 = 0; n0 < s.len; n0 += 2) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int n = n0 + p;
+      if (n >= s.len) break;
+      if (n + 1 < s.len) next(n + 1, p ^ 1);
+      float kq = 0.f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) kq = fmaf(k[p][c], q[p][c], kq);
+      kq = sum8(kq);
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) {
+        float sk = 0.f, sq = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          sk = fmaf(S[j][c], k[p][c], sk);
+          sq = fmaf(S[j][c], q[p][c], sq);
+          S[j][c] *= alpha[p];
+        }
+        sk = sum8(sk);
+        sq = sum8(sq);
+        const float u = beta[p] * (v[p][j] - alpha[p] * sk);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) S[j][c] = fmaf(u, k[p][c], S[j][c]);
+        const int row = group_row<RPT>(first, j);
+        if (l == 0 && row < a.dv) store_o(a, ((s.tok0 + n) * a.H + h) * a.dv + row, fmaf(kq, u, alpha[p] * sq));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < RPT; ++j) {
+    const int row = group_row<RPT>(first, j);
+    if (row < a.dv) store_row<V, WIDE>(a.state, SB, (block + row) * a.dk, a.dk, l, S[j]);
+  }
+}
+
 // Staged tokens, f32: 8 CL columns of k and q (zero beyond dk) and the CTA's
 // rows of v (zero beyond dv); behind the sequence's end k, q, v and beta are
 // zero and alpha is one.  The factors of a block of kBlock tokens, with G_n the
@@ -307,23 +404,117 @@ __device__ __forceinline__ float sum8_each(const float (&x)[8], int l) {
   return mine + __shfl_xor_sync(kFull, other, 1);
 }
 
+template <int ID, int N>
+__device__ __forceinline__ void bar_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
+}
+
 // One (sequence, head) and THREADS / 8 x RPT of its rows per CTA, CL columns
-// of a row per lane, any number of tokens.
+// of a row per lane, any number of tokens.  kPrep more threads stage the next
+// tokens and their blocks' factors meanwhile.
 template <int RPT, bool SB, bool QB, bool WIDE, int CL, int THREADS>
-__global__ void __launch_bounds__(THREADS) scan_kernel(const treewy_seqs a) {
-  constexpr int V = 4, kRows = THREADS / 8 * RPT, kCols = 8 * CL;
-  __shared__ __align__(16) Stage<CL, kRows> st;
+__global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs a) {
+  constexpr int V = 4, kRows = THREADS / 8 * RPT, kCols = 8 * CL, kAll = THREADS + kPrep;
+  __shared__ __align__(16) Stage<CL, kRows> stages[2];
   after_previous();
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
-  const int tid = threadIdx.x, l = tid & 7;
+  const int l = threadIdx.x & 7;
   const Seq s = load_seq(a, r);
   if (s.flags) {
-    if (tid == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
+    if (threadIdx.x == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
     return;
   }
   if (s.len == 0 && !s.fresh) return;
-  const int64_t block = (static_cast<int64_t>(s.slot) * a.H + h) * a.dv;
   const int first = static_cast<int>(blockIdx.y) * kRows;
+
+  if (threadIdx.x >= THREADS) {
+    const int tid = threadIdx.x - THREADS, hk = h / (a.H / a.Hk);
+    constexpr int kPer = kStage * kCols / kPrep;  // staged elements of k (and q) per thread
+    constexpr int kPerV = kStage * kRows / kPrep;
+    // as they are stored: a conversion here would wait for its load
+    using Raw = std::conditional_t<QB, uint16_t, float>;
+    const Raw *pk = static_cast<const Raw*>(a.k), *pq = static_cast<const Raw*>(a.q), *pv = static_cast<const Raw*>(a.v);
+    auto value = [](Raw x) {
+      if constexpr (QB) return bf16_bits_to_float(x);
+      else return x;
+    };
+    Raw nk[kPer], nq[kPer], nv[kPerV];
+    float ngate = 0.f;
+    auto fetch = [&](int t0) {  // the stage from token t0 on, into registers
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = tid + i * kPrep, n = e / kCols, c = e % kCols;
+        const int64_t t = s.tok0 + t0 + n;
+        nk[i] = nq[i] = 0;
+        if (t0 + n < s.len && c < a.dk) {
+          nk[i] = __ldg(pk + t * a.k_stride + static_cast<int64_t>(hk) * a.dk + c);
+          nq[i] = __ldg(pq + t * a.q_stride + static_cast<int64_t>(hk) * a.dk + c);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kPerV; ++i) {
+        const int e = tid + i * kPrep, n = e / kRows, c = first + e % kRows;
+        nv[i] = 0;
+        if (t0 + n < s.len && c < a.dv)
+          nv[i] = __ldg(pv + (s.tok0 + t0 + n) * a.v_stride + static_cast<int64_t>(h) * a.dv + c);
+      }
+      if (tid < 2 * kStage) {
+        const int n = tid & (kStage - 1);
+        ngate = tid < kStage ? 1.f : 0.f;
+        const float* g = tid < kStage ? a.alpha : a.beta;
+        if (t0 + n < s.len) ngate = __ldg(g + (s.tok0 + t0 + n) * a.H + h);
+      }
+    };
+    fetch(0);
+    for (int t0 = 0; t0 < s.len; t0 += kStage) {
+      Stage<CL, kRows>& st = stages[t0 / kStage & 1];  // its last tokens were done before the last barrier
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        (&st.k[0][0])[tid + i * kPrep] = value(nk[i]);
+        (&st.q[0][0])[tid + i * kPrep] = value(nq[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kPerV; ++i) (&st.v[0][0])[tid + i * kPrep] = value(nv[i]);
+      if (tid < kStage) st.alpha[tid] = ngate;
+      else if (tid < 2 * kStage) st.beta[tid - kStage] = ngate;
+      bar_sync<1, kPrep>();
+      fetch(t0 + kStage);
+      const int m = min(kStage, s.len - t0);
+      // 10 products q_n . k_j and 6 k_n . k_j of each block, eight lanes per product
+#pragma unroll 1
+      for (int p = tid >> 3; p < kStage / kBlock * 16; p += kPrep / 8) {
+        const int b = p / 16 * kBlock, e = p % 16;
+        if (b >= m) break;  // whole warps: 4 products of one block each
+        const bool isq = e < 10;
+        const int f = isq ? e : e - 10;
+        const int n = isq ? (f >= 6 ? 3 : f >= 3 ? 2 : f >= 1 ? 1 : 0) : (f >= 3 ? 3 : f >= 1 ? 2 : 1);
+        const int j = f - (isq ? n * (n + 1) / 2 : n * (n - 1) / 2);
+        float x[CL], y[CL], sum[2] = {0.f, 0.f};
+        load_row<V, true>(isq ? st.q[b + n] : st.k[b + n], false, 0, kCols, l, x);
+        load_row<V, true>(st.k[b + j], false, 0, kCols, l, y);
+#pragma unroll
+        for (int c = 0; c < CL; ++c) sum[c & 1] = fmaf(x[c], y[c], sum[c & 1]);
+        float z = sum8(sum[0] + sum[1]);
+        if (!isq) z *= st.beta[b + n];
+        for (int i = j + 1; i <= n; ++i) z *= st.alpha[b + i];
+        if (l == 0) (isq ? st.kq : st.kk)[b + n][j] = z;
+      }
+      if (tid < kStage) {
+        const int b = tid & ~(kBlock - 1);
+        float g = st.alpha[b], d = 1.f;
+        for (int i = b + 1; i < b + kBlock; ++i) {
+          if (i <= tid) g *= st.alpha[i];
+          else d *= st.alpha[i];
+        }
+        st.gate[tid] = g;
+        st.dec[tid] = d;
+      }
+      bar_sync<0, kAll>();
+    }
+    return;
+  }
+
+  const int64_t block = (static_cast<int64_t>(s.slot) * a.H + h) * a.dv;
   float S[RPT][CL];
 #pragma unroll
   for (int j = 0; j < RPT; ++j) {
@@ -335,89 +526,10 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const treewy_seqs a) {
       for (int c = 0; c < CL; ++c) S[j][c] = 0.f;
     }
   }
-
-  const int hk = h / (a.H / a.Hk);
-  constexpr int kPer = kStage * kCols / THREADS;  // staged elements of k (and q) per thread
-  constexpr int kPerV = kStage * kRows / THREADS;
-  // as they are stored: a conversion here would wait for its load
-  using Raw = std::conditional_t<QB, uint16_t, float>;
-  const Raw *pk = static_cast<const Raw*>(a.k), *pq = static_cast<const Raw*>(a.q), *pv = static_cast<const Raw*>(a.v);
-  auto value = [](Raw x) {
-    if constexpr (QB) return bf16_bits_to_float(x);
-    else return x;
-  };
-  Raw nk[kPer], nq[kPer], nv[kPerV];
-  float ngate = 0.f;
-  auto fetch = [&](int t0) {  // the stage from token t0 on, into registers
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid + i * THREADS, n = e / kCols, c = e % kCols;
-      const int64_t t = s.tok0 + t0 + n;
-      nk[i] = nq[i] = 0;
-      if (t0 + n < s.len && c < a.dk) {
-        nk[i] = __ldg(pk + t * a.k_stride + static_cast<int64_t>(hk) * a.dk + c);
-        nq[i] = __ldg(pq + t * a.q_stride + static_cast<int64_t>(hk) * a.dk + c);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kPerV; ++i) {
-      const int e = tid + i * THREADS, n = e / kRows, c = first + e % kRows;
-      nv[i] = 0;
-      if (t0 + n < s.len && c < a.dv)
-        nv[i] = __ldg(pv + (s.tok0 + t0 + n) * a.v_stride + static_cast<int64_t>(h) * a.dv + c);
-    }
-    if (tid < 2 * kStage) {
-      const int n = tid & (kStage - 1);
-      ngate = tid < kStage ? 1.f : 0.f;
-      const float* g = tid < kStage ? a.alpha : a.beta;
-      if (t0 + n < s.len) ngate = __ldg(g + (s.tok0 + t0 + n) * a.H + h);
-    }
-  };
-  fetch(0);
   for (int t0 = 0; t0 < s.len; t0 += kStage) {
-    __syncthreads();  // the last stage has been read
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      (&st.k[0][0])[tid + i * THREADS] = value(nk[i]);
-      (&st.q[0][0])[tid + i * THREADS] = value(nq[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kPerV; ++i) (&st.v[0][0])[tid + i * THREADS] = value(nv[i]);
-    if (tid < kStage) st.alpha[tid] = ngate;
-    else if (tid < 2 * kStage) st.beta[tid - kStage] = ngate;
-    __syncthreads();
-    fetch(t0 + kStage);
+    const Stage<CL, kRows>& st = stages[t0 / kStage & 1];
     const int m = min(kStage, s.len - t0);
-    // The blocks' factors: 10 products q_n . k_j and 6 k_n . k_j each, eight lanes per product.
-#pragma unroll 1
-    for (int p = tid >> 3; p < kStage / kBlock * 16; p += THREADS / 8) {
-      const int b = p / 16 * kBlock, e = p % 16;
-      if (b >= m) break;  // whole warps: 4 products of one block each
-      const bool isq = e < 10;
-      const int f = isq ? e : e - 10;
-      const int n = isq ? (f >= 6 ? 3 : f >= 3 ? 2 : f >= 1 ? 1 : 0) : (f >= 3 ? 3 : f >= 1 ? 2 : 1);
-      const int j = f - (isq ? n * (n + 1) / 2 : n * (n - 1) / 2);
-      float x[CL], y[CL], sum[2] = {0.f, 0.f};
-      load_row<V, true>(isq ? st.q[b + n] : st.k[b + n], false, 0, kCols, l, x);
-      load_row<V, true>(st.k[b + j], false, 0, kCols, l, y);
-#pragma unroll
-      for (int c = 0; c < CL; ++c) sum[c & 1] = fmaf(x[c], y[c], sum[c & 1]);
-      float z = sum8(sum[0] + sum[1]);
-      if (!isq) z *= st.beta[b + n];
-      for (int i = j + 1; i <= n; ++i) z *= st.alpha[b + i];
-      if (l == 0) (isq ? st.kq : st.kk)[b + n][j] = z;
-    }
-    if (tid < kStage) {
-      const int b = tid & ~(kBlock - 1);
-      float g = st.alpha[b], d = 1.f;
-      for (int i = b + 1; i < b + kBlock; ++i) {
-        if (i <= tid) g *= st.alpha[i];
-        else d *= st.alpha[i];
-      }
-      st.gate[tid] = g;
-      st.dec[tid] = d;
-    }
-    __syncthreads();
+    bar_sync<0, kAll>();
 #pragma unroll 1
     for (int b = 0; b < m; b += kBlock) {
       float dot[RPT][2 * kBlock];  // S k_n, then S q_n: this lane's columns
@@ -488,12 +600,20 @@ cudaError_t launch_decode(const treewy_seqs& a, cudaStream_t stream) {
   return launch_after(decode_kernel<RPT, SB, QB, WIDE>, grid, kDecodeThreads, stream, a);
 }
 
+template <int RPT, bool SB, bool QB, bool WIDE>
+cudaError_t launch_few(const treewy_seqs& a, cudaStream_t stream) {
+  constexpr int kRows = 4 * kDecodeWarps * RPT;
+  const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
+                  static_cast<unsigned>((a.dv + kRows - 1) / kRows));
+  return launch_after(few_kernel<RPT, SB, QB, WIDE>, grid, kDecodeThreads, stream, a);
+}
+
 template <int RPT, bool SB, bool QB, bool WIDE, int CL, int THREADS>
 cudaError_t launch_scan(const treewy_seqs& a, cudaStream_t stream) {
   constexpr int kRows = THREADS / 8 * RPT;
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
                   static_cast<unsigned>((a.dv + kRows - 1) / kRows));
-  return launch_after(scan_kernel<RPT, SB, QB, WIDE, CL, THREADS>, grid, THREADS, stream, a);
+  return launch_after(scan_kernel<RPT, SB, QB, WIDE, CL, THREADS>, grid, THREADS + kPrep, stream, a);
 }
 
 template <bool SB, bool QB, bool WIDE>
@@ -501,11 +621,12 @@ cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
   const int64_t heads = static_cast<int64_t>(a.R) * a.H;
   if (a.max_len <= 1)  // a quarter of a head per CTA, or less while that leaves SMs idle
     return 4 * heads >= 304 ? launch_decode<4, SB, QB, WIDE>(a, stream) : launch_decode<1, SB, QB, WIDE>(a, stream);
-  // A whole head per CTA, or 16 of its rows while that leaves SMs idle (the
-  // chain of a row is then alone on its quarter of an SM); half as many columns
-  // per lane for small keys.
-  if (heads >= 304)
-    return a.dk <= 64 ? launch_scan<4, SB, QB, WIDE, 8, 256>(a, stream) : launch_scan<4, SB, QB, WIDE, 16, 256>(a, stream);
+  if (a.max_len <= 16)
+    return 4 * heads >= 304 ? launch_few<2, SB, QB, WIDE>(a, stream) : launch_few<1, SB, QB, WIDE>(a, stream);
+  // 16 rows of a head per CTA while two CTAs per SM hold them all, then 64;
+  // half as many columns per lane for small keys.
+  if (8 * heads > 304)
+    return a.dk <= 64 ? launch_scan<2, SB, QB, WIDE, 8, 256>(a, stream) : launch_scan<2, SB, QB, WIDE, 16, 256>(a, stream);
   return a.dk <= 64 ? launch_scan<1, SB, QB, WIDE, 8, 128>(a, stream) : launch_scan<1, SB, QB, WIDE, 16, 128>(a, stream);
 }
 
