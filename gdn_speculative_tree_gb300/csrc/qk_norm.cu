@@ -11,7 +11,7 @@
 // and the other element of a rotated pair is one shuffle away or in the same
 // lane.  A warp takes several heads of one token and side (q or k), so that
 // the weights and the token's cosines and sines are loaded once for all of
-// them.  Where a pair's elements are not a multiple of eight apart (ODD), the
+// them.  Where a pair's elements are not a multiple of eight apart (kOdd), the
 // other one is loaded by itself.  Rows that this does not fit (odd sizes,
 // unaligned rows) go to one warp each, element by element.
 #include "treewy_device.cuh"
@@ -57,9 +57,8 @@ __device__ __forceinline__ Row row_of(const treewy_qk& a, int64_t t, int head, i
   return r;
 }
 
-// The rotation table's row of token t, or NULL with the status bit set.
-__device__ __forceinline__ const float* table_row(const treewy_qk& a, int64_t t, bool report) {
-  const int p = __ldg(a.position + t);
+// The rotation table's row of position p, or NULL with the status bit set.
+__device__ __forceinline__ const float* table_row(const treewy_qk& a, int p, bool report) {
   if (p < 0 || p >= a.rope_rows) {
     if (report) atomicOr(a.status, TREEWY_STATUS_BAD_POSITION);
     return nullptr;
@@ -107,29 +106,60 @@ __device__ __forceinline__ int pair_step(const treewy_qk& a, int c) {
   return c < a.rope_dims / 2 ? a.rope_dims / 2 : -(a.rope_dims / 2);
 }
 
+// Two f32 at a time (one instruction): a b + c, a b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Many rows outgrow L2: they pass through it as a stream.
+template <bool STREAM>
+__device__ __forceinline__ uint4 get(const void* p) {
+  const uint4* q = static_cast<const uint4*>(p);
+  return STREAM ? __ldcs(q) : *q;
+}
+template <bool STREAM, typename V>
+__device__ __forceinline__ void put(void* p, V x) {
+  if (STREAM) __stcs(static_cast<V*>(p), x);
+  else *static_cast<V*>(p) = x;
+}
+
 // LANES lanes per head, eight elements each; a warp takes UNROLL passes of
 // 32 / LANES heads of one token's q or k, all loaded before the first is used.
-// ODD: pairs at any distance, eights that the rotation ends within.
-template <typename T, int LANES, int UNROLL, int THREADS, bool ODD>
+// PAIRS: the two elements of a pair are half / 8 lanes apart, neighbours, or at
+// any distance with the rotation ending anywhere.
+enum Pairs { kLanes, kNeighbours, kOdd };
+template <typename T, int LANES, int UNROLL, int THREADS, Pairs PAIRS>
 __global__ void __launch_bounds__(THREADS, 896 / THREADS)
-    qk_norm_kernel(const treewy_qk a, int q_units, int units, float mean) {
+    qk_norm_kernel(const treewy_qk a, int q_units, int units, unsigned parts, float mean) {
   after_previous();
+  constexpr bool ODD = PAIRS == kOdd, NEXT = PAIRS == kNeighbours, kStream = UNROLL > 2;
   constexpr int kPass = 32 / LANES;                   // heads per pass
   const int lane = threadIdx.x % LANES, grp = (threadIdx.x & 31) / LANES;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+  const int64_t t = static_cast<int64_t>(blockIdx.x / parts) * (THREADS / 32) + (threadIdx.x >> 5);
   if (t >= a.T) return;                               // a whole warp
-  const float* tab = nullptr;
-  if (a.rope_dims > 0) {
-    tab = table_row(a, t, blockIdx.y == 0 && (threadIdx.x & 31) == 0);
-    if (tab == nullptr) return;                       // a whole warp
-  }
+  const int position = a.rope_dims > 0 ? __ldg(a.position + t) : 0;
   const int c0 = 8 * lane;
   const bool mine = c0 < a.d;
   // half is a multiple of 8 (but where ODD): a pair's other eight are half / 8 lanes on
   const int half = a.rope_dims / 2;
   const bool in_rope = c0 < a.rope_dims, low = c0 < half;
   const int other = in_rope ? (low ? lane + half / 8 : lane - half / 8) : lane;
-  for (int part = blockIdx.y; part < units; part += gridDim.y) {
+  for (int part = blockIdx.x % parts; part < units; part += parts) {
     const bool isq = part < q_units;
     const int heads = isq ? a.Hq : a.Hk, repeat = isq ? a.q_repeat : a.k_repeat;
     const int h0 = (isq ? part : part - q_units) * (UNROLL * kPass) + grp;
@@ -153,8 +183,13 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
       for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) {
         raw[i].w[k] = make_uint4(0u, 0u, 0u, 0u);
         if (h0 + i * kPass < heads && mine)
-          raw[i].w[k] = *reinterpret_cast<const uint4*>(in + static_cast<int64_t>(i) * step + 16 * k);
+          raw[i].w[k] = get<kStream>(in + static_cast<int64_t>(i) * step + 16 * k);
       }
+    }
+    const float* tab = nullptr;                       // looked up while the rows are on their way
+    if (a.rope_dims > 0) {
+      tab = table_row(a, position, part == 0 && (threadIdx.x & 31) == 0);
+      if (tab == nullptr) return;                     // a whole warp
     }
     // y = f (x wc + x' ws) with x' the pair's other element (ws = 0: no pair)
     float wc[8], ws[8];
@@ -173,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
       }
     } else if (in_rope) {
       float cs[8], sn[8], v[8];
-      if (a.interleaved) {
+      if constexpr (NEXT) {
         const float4 c = *reinterpret_cast<const float4*>(tab + c0 / 2);
         const float4 s = *reinterpret_cast<const float4*>(tab + half + c0 / 2);
         const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
@@ -190,11 +225,11 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
           for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
         }
       }
-      if (weight != nullptr) load8_f32(weight + (a.interleaved ? c0 : 8 * other), v);
+      if (weight != nullptr) load8_f32(weight + (NEXT ? c0 : 8 * other), v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         wc[e] *= cs[e];
-        ws[e] = scale * sn[e] * (weight != nullptr ? v[a.interleaved ? e ^ 1 : e] : 1.f);
+        ws[e] = scale * sn[e] * (weight != nullptr ? v[NEXT ? e ^ 1 : e] : 1.f);
       }
     }
     if (weight != nullptr && mine) {
@@ -211,18 +246,20 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
       if (i > 0 && h0 - grp + i * kPass >= heads) break;  // a whole warp
       float x[8];
       unpack8<T>(raw[i], x);
-      float sum = 0.f;
+      float2 sums = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+      for (int e = 0; e < 8; e += 2) sums = fma2(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), sums);
+      float sum = sums.x + sums.y;
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
       const float f = inv_norm(sum, mean, a.eps);
+      float y[8];
       if constexpr (ODD) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = f * fmaf(static_cast<float>(far[i][e]), ws[e], x[e] * wc[e]);
+        for (int e = 0; e < 8; ++e) y[e] = static_cast<float>(far[i][e]);
       } else if (a.rope_dims > 0) {
         Raw8<T> pair = raw[i];
-        if (!a.interleaved) {
+        if (!NEXT) {
 #pragma unroll
           for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) {
             pair.w[k].x = __shfl_sync(kFull, pair.w[k].x, other, LANES);
@@ -231,15 +268,18 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
             pair.w[k].w = __shfl_sync(kFull, pair.w[k].w, other, LANES);
           }
         }
-        float y[8], z[8];
-        unpack8<T>(pair, y);
+        float z[8];
+        unpack8<T>(pair, z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = f * fmaf(a.interleaved ? y[e ^ 1] : y[e], ws[e], x[e] * wc[e]);
+        for (int e = 0; e < 8; ++e) y[e] = NEXT ? z[e ^ 1] : z[e];
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = z[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= f * wc[e];
+      for (int e = 0; e < 8; e += 2) {
+        float2 z = mul2(make_float2(x[e], x[e + 1]), make_float2(wc[e], wc[e + 1]));
+        if (ODD || a.rope_dims > 0) z = fma2(make_float2(y[e], y[e + 1]), make_float2(ws[e], ws[e + 1]), z);
+        z = mul2(z, make_float2(f, f));
+        x[e] = z.x;
+        x[e + 1] = z.y;
       }
       if (h0 + i * kPass < heads && mine) {
         unsigned char* o = out + static_cast<int64_t>(i) * step * repeat;
@@ -250,11 +290,13 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
             const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
             p[e] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          for (int c = 0; c < repeat; ++c, o += copy) *reinterpret_cast<uint4*>(o) = make_uint4(p[0], p[1], p[2], p[3]);
+          const uint4 w = make_uint4(p[0], p[1], p[2], p[3]);
+          put<kStream>(o, w);
+          for (int c = 1; c < repeat; ++c) put<kStream>(o += copy, w);
         } else {
           for (int c = 0; c < repeat; ++c, o += copy) {
-            *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(o + 16) = make_float4(x[4], x[5], x[6], x[7]);
+            put<kStream>(o, make_float4(x[0], x[1], x[2], x[3]));
+            put<kStream>(o + 16, make_float4(x[4], x[5], x[6], x[7]));
           }
         }
       }
@@ -288,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(const treewy_qk a
   for (int c = lane; c < a.d; c += 32) y[c] *= row.w != nullptr ? f * __ldg(row.w + c) : f;
   __syncwarp();
   if (a.rope_dims > 0) {
-    const float* tab = table_row(a, t, lane == 0);
+    const float* tab = table_row(a, __ldg(a.position + t), lane == 0);
     if (tab == nullptr) return;
     const int half = a.rope_dims / 2;
     for (int i = lane; i < half; i += 32) {
@@ -305,29 +347,35 @@ __global__ void __launch_bounds__(kThreads) qk_norm_any_kernel(const treewy_qk a
     for (int e = lane; e < a.d; e += 32) out[c * a.d + e] = static_cast<T>(y[e]);
 }
 
-template <typename T, int LANES, int UNROLL, int THREADS, bool ODD>
+template <typename T, int LANES, int UNROLL, int THREADS, Pairs PAIRS>
 cudaError_t launch_passes(const treewy_qk& a, cudaStream_t stream) {
   constexpr int kHeads = UNROLL * 32 / LANES;
   const int q_units = (a.Hq + kHeads - 1) / kHeads, units = q_units + (a.Hk + kHeads - 1) / kHeads;
-  const dim3 grid(static_cast<unsigned>((a.T + THREADS / 32 - 1) / (THREADS / 32)),
-                  static_cast<unsigned>(units < 65535 ? units : 65535));
+  const int64_t ctas = (a.T + THREADS / 32 - 1) / (THREADS / 32);
+  const unsigned parts = static_cast<unsigned>(min(int64_t(units), max(int64_t(1), int64_t(0x7fffffff) / ctas)));
+  const dim3 grid(static_cast<unsigned>(ctas * parts));
   const float mean = a.norm == TREEWY_NORM_RMS ? 1.0f / static_cast<float>(a.d) : 1.f;
-  return launch_after(qk_norm_kernel<T, LANES, UNROLL, THREADS, ODD>, grid, THREADS, stream, a, q_units, units, mean);
+  return launch_after(qk_norm_kernel<T, LANES, UNROLL, THREADS, PAIRS>, grid, THREADS, stream, a, q_units, units, parts, mean);
 }
 
 template <typename T, int LANES>
 cudaError_t launch(const treewy_qk& a, cudaStream_t stream) {
   // Many rows: as many heads per warp as its registers hold, and a warp per
-  // CTA, so that a warp's place is filled as soon as it is done (32768 tokens
-  // of 18 bf16 heads of 256: 122 us, 143 us with two warps per CTA).  Few: the
-  // rows spread over more warps (256 tokens of 32 heads of 128: 2.3 us).
+  // CTA, so that a warp's place is filled as soon as it is done, a token's
+  // parts one after the other (32768 tokens of 18 bf16 heads of 256: 106 us,
+  // 5.8 TB/s; 112 us without the streaming hints, 122 us with all tokens' first
+  // parts first, 143 us with two warps per CTA).  Few: the rows spread over
+  // more warps (256 tokens of 32 heads of 128: 2.3 us).
   // Odd pairs: one shape for both (8001 tokens of 24 bf16 heads of 80, 20 of
-  // them rotated: 45 us, 67 us element by element; more heads per warp 40 to
-  // 42, but f32 53 to 70 for 47).
+  // them rotated: 48 us, 67 us element by element; more heads per warp save
+  // 4 us and cost f32 6 to 20).
   constexpr int kMany = sizeof(T) == 2 ? 8 : 4;
-  if (a.rope_dims % (a.interleaved ? 8 : 16) != 0) return launch_passes<T, LANES, 2, 64, true>(a, stream);
-  return a.T * (a.Hq + a.Hk) >= int64_t(152) * 64 * (32 / LANES) ? launch_passes<T, LANES, kMany, 32, false>(a, stream)
-                                                               : launch_passes<T, LANES, 2, 64, false>(a, stream);
+  if (a.rope_dims % (a.interleaved ? 8 : 16) != 0) return launch_passes<T, LANES, 2, 64, kOdd>(a, stream);
+  const bool many = a.T * (a.Hq + a.Hk) >= int64_t(152) * 64 * (32 / LANES);
+  if (a.interleaved)
+    return many ? launch_passes<T, LANES, kMany, 32, kNeighbours>(a, stream)
+                : launch_passes<T, LANES, 2, 64, kNeighbours>(a, stream);
+  return many ? launch_passes<T, LANES, kMany, 32, kLanes>(a, stream) : launch_passes<T, LANES, 2, 64, kLanes>(a, stream);
 }
 
 template <typename T>
