@@ -176,6 +176,16 @@ __device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8]) {
                : "memory");
 }
 
+// x = hi + lo in bf16 terms, as split_pair, two elements per instruction.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const float2 d = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), make_float2(-1.f, -1.f),
+                        make_float2(x0, x1));
+  const __nv_bfloat162 l = __floats2bfloat162_rn(d.x, d.y);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Row `row`, 16-byte piece `j` of a K-major operand with 128-byte rows.
@@ -267,7 +277,7 @@ __device__ __forceinline__ void solve32(float* X, int lane) {
 __device__ __forceinline__ void put_piece(unsigned char* hi, int row, int j, const float (&x)[8]) {
   uint32_t h[4], l[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) split_pair(x[2 * e], x[2 * e + 1], h[e], l[e]);
+  for (int e = 0; e < 4; ++e) split2(x[2 * e], x[2 * e + 1], h[e], l[e]);
   uint4* out = operand_piece(hi, row, j);
   out[0] = make_uint4(h[0], h[1], h[2], h[3]);
   out[kBox / 16] = make_uint4(l[0], l[1], l[2], l[3]);
@@ -347,7 +357,7 @@ __device__ __forceinline__ void solve64(const float* X, unsigned char* ab, unsig
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       uint32_t h, l;
-      split_pair(d.at(2 * e), d.at(2 * e + 1), h, l);
+      split2(d.at(2 * e), d.at(2 * e + 1), h, l);
       unsigned char* out = ab + sw128_off(16 * m + 8 * e + at, c);
       *reinterpret_cast<uint32_t*>(out) = h;
       *reinterpret_cast<uint32_t*>(out + kBox) = l;
@@ -369,8 +379,8 @@ __device__ __forceinline__ void solve64(const float* X, unsigned char* ab, unsig
     for (int e = 0; e < 2; ++e) {
       const float x = d.at(2 * e), y = d.at(2 * e + 1);
       uint32_t h, l, h2, l2;
-      split_pair(-x, -y, h, l);
-      split_pair(dec[e] * b.x * x, dec[e] * b.y * y, h2, l2);
+      split2(-x, -y, h, l);
+      split2(dec[e] * b.x * x, dec[e] * b.y * y, h2, l2);
       unsigned char* out = tb + sw128_off(32 + 16 * m + 8 * e + at, c);
       *reinterpret_cast<uint32_t*>(out) = h;
       *reinterpret_cast<uint32_t*>(out + kBox) = l;
@@ -446,7 +456,7 @@ __device__ __forceinline__ void store_state(const treewy_seqs& a, int64_t row, i
 __device__ __forceinline__ void put_state16(uint32_t tm, int half, int b, const float (&S)[64]) {
   uint32_t hi[8], lo[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) split_pair(S[16 * b + 2 * e], S[16 * b + 2 * e + 1], hi[e], lo[e]);
+  for (int e = 0; e < 8; ++e) split2(S[16 * b + 2 * e], S[16 * b + 2 * e + 1], hi[e], lo[e]);
   tmem_st8(tm + kColS + 32 * half + 8 * b, hi);
   tmem_st8(tm + kColS + 64 + 32 * half + 8 * b, lo);
 }
@@ -489,19 +499,23 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
 #pragma unroll 1
       for (int b = 0; b < 2; ++b, vt += 16 * 256) {
         uint32_t x[16], hi[8], lo[8];
-        tmem_ld16_async(tm + kColW + n0 + 16 * b, x);
+        tmem_ld16_async(tm + kColD + n0 + 16 * b, x);
         tmem_wait16(x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float4 f = *reinterpret_cast<const float4*>(g.g + n0 + 16 * b + 4 * j);
           const float fs[4] = {f.x, f.y, f.z, f.w};
-          float w[4];
+          float v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w[k] = fmaf(-fs[k], __uint_as_float(x[4 * j + k]),
-                        bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + (4 * j + k) * 256)));
-          split_pair(w[0], w[1], hi[2 * j], lo[2 * j]);
-          split_pair(w[2], w[3], hi[2 * j + 1], lo[2 * j + 1]);
+            v[k] = bf16_bits_to_float(*reinterpret_cast<const uint16_t*>(vt + (4 * j + k) * 256));
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const float2 w = fma2(make_float2(-fs[k], -fs[k + 1]),
+                                  make_float2(__uint_as_float(x[4 * j + k]), __uint_as_float(x[4 * j + k + 1])),
+                                  make_float2(v[k], v[k + 1]));
+            split2(w.x, w.y, hi[2 * j + k / 2], lo[2 * j + k / 2]);
+          }
         }
         // 16 tokens: hi in 8 columns, lo in 8, in place of what was just read
         tmem_st8(tm + kColW + n0 + 16 * b, hi);
@@ -522,7 +536,12 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
       tmem_ld16_async(tm + kColD + 64 * half + 16 * b, x);
       tmem_wait16(x);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) S[16 * b + e] = fmaf(gC, S[16 * b + e], __uint_as_float(x[e]));
+      for (int e = 0; e < 16; e += 2) {
+        const float2 y = fma2(make_float2(gC, gC), make_float2(S[16 * b + e], S[16 * b + e + 1]),
+                              make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+        S[16 * b + e] = y.x;
+        S[16 * b + e + 1] = y.y;
+      }
     }
     warp_arrive(&cs.gates_free[sg]);
   }
@@ -552,10 +571,10 @@ __device__ __forceinline__ void run_out(const treewy_seqs& a, ChunkSmem& cs, uns
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float4 f = *reinterpret_cast<const float4*>(g.g + 16 * b + 4 * j);
-        o[16 * b + 4 * j] = f.x * __uint_as_float(x[4 * j]);
-        o[16 * b + 4 * j + 1] = f.y * __uint_as_float(x[4 * j + 1]);
-        o[16 * b + 4 * j + 2] = f.z * __uint_as_float(x[4 * j + 2]);
-        o[16 * b + 4 * j + 3] = f.w * __uint_as_float(x[4 * j + 3]);
+        const float2 y = mul2(make_float2(f.x, f.y), make_float2(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])));
+        const float2 z = mul2(make_float2(f.z, f.w), make_float2(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])));
+        o[16 * b + 4 * j] = y.x, o[16 * b + 4 * j + 1] = y.y;
+        o[16 * b + 4 * j + 2] = z.x, o[16 * b + 4 * j + 3] = z.y;
       }
     }
     tc_fence_before_sync();
@@ -776,7 +795,7 @@ __device__ __forceinline__ void form_row(uint32_t tm_row, const Gates& g, bool i
     if (out_row == nullptr) {
       uint32_t h[8], l[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) split_pair(y[2 * k], y[2 * k + 1], h[k], l[k]);
+      for (int k = 0; k < 8; ++k) split2(y[2 * k], y[2 * k + 1], h[k], l[k]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint4* out = operand_piece(tile, n, 4 * cb + 2 * b + j);
@@ -799,7 +818,7 @@ __device__ __forceinline__ void put_kt(uint32_t tm_row, unsigned char* ktb, int 
     tmem_ld16_async(tm_row + kColK + 16 * b, x);
     tmem_wait16(x);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) split_pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), h[k], l[k]);
+    for (int k = 0; k < 8; ++k) split2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]), h[k], l[k]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint4* out = operand_piece(ktb, row, 2 * b + j);
@@ -922,9 +941,7 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
     const uint64_t s0 = smem_desc_sw128(smem_addr(base + sg * kStageBytes), 1024);
     if (!held(&cs.full[sg], c >> 1)) return;
     if (len - c * kC < kC && !held(&cs.fix, 0)) return;
-    // W's columns have been read by the last chunk's products
-    if (c > 0 && !held(&cs.o2_done, c - 1)) return;
-    // S k, half of the columns of S at a time
+    // S k in the columns of W kt, half of the columns of S at a time
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       if (!held(&cs.s_ready[half], c)) return;
@@ -933,13 +950,16 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const uint64_t kd = s0 + ((half * 2 * kBox + 32 * k) >> 4);
-        mma_ts(tm + kColW, tm + kColS + 32 * half + 8 * k, kd, id, half > 0 || k > 0);
-        mma_ts(tm + kColW, tm + kColS + 64 + 32 * half + 8 * k, kd, id, 1u);
+        mma_ts(tm + kColD, tm + kColS + 32 * half + 8 * k, kd, id, half > 0 || k > 0);
+        mma_ts(tm + kColD, tm + kColS + 64 + 32 * half + 8 * k, kd, id, 1u);
       }
-      if (half == 1) mma_commit(&cs.d1_done);
       }
       __syncwarp();
     }
+    // the columns of W may be written again
+    if (c > 0 && !held(&cs.o2_done, c - 1)) return;
+    if (elect_one()) mma_commit(&cs.d1_done);
+    __syncwarp();
     // S q
     if (c > 0 && !held(&cs.o_read, c - 1)) return;
     if (elect_one()) {
