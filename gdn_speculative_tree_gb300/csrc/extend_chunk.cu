@@ -202,8 +202,9 @@ __device__ __forceinline__ bool prep_failed(bool ok) { return named_bar_or<1, kP
 // there), N a multiple of 4; all f32 in shared memory.
 template <int N, int V>
 __device__ __forceinline__ void dot_rows(const float* L, const float* R, float (&acc)[V]) {
+  float2 sum[V / 2];
 #pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int e = 0; e < V / 2; ++e) sum[e] = make_float2(0.f, 0.f);
 #pragma unroll 2
   for (int i = 0; i < N; i += 4) {
     const float4 l = *reinterpret_cast<const float4*>(L + i);
@@ -214,14 +215,14 @@ __device__ __forceinline__ void dot_rows(const float* L, const float* R, float (
       y[k] = *reinterpret_cast<const float4*>(R + (i + k / (V / 4)) * kPitchX + 4 * (k % (V / 4)));
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int e = 4 * (k % (V / 4));
-      const float f = ls[k / (V / 4)];
-      acc[e] = fmaf(f, y[k].x, acc[e]);
-      acc[e + 1] = fmaf(f, y[k].y, acc[e + 1]);
-      acc[e + 2] = fmaf(f, y[k].z, acc[e + 2]);
-      acc[e + 3] = fmaf(f, y[k].w, acc[e + 3]);
+      const int e = 2 * (k % (V / 4));
+      const float2 f = make_float2(ls[k / (V / 4)], ls[k / (V / 4)]);
+      sum[e] = fma2(f, make_float2(y[k].x, y[k].y), sum[e]);
+      sum[e + 1] = fma2(f, make_float2(y[k].z, y[k].w), sum[e + 1]);
     }
   }
+#pragma unroll
+  for (int e = 0; e < V; e += 2) acc[e] = sum[e / 2].x, acc[e + 1] = sum[e / 2].y;
 }
 
 // T21 = -T22 (A21 T11) for the block of 2 N at B (A21 and then T21 at row N,
@@ -335,8 +336,13 @@ __device__ __forceinline__ void solve64(const float* X, unsigned char* ab, unsig
     const float4 v = *reinterpret_cast<const float4*>(X + r * kPitchX + c + 4);
     const float4 b0 = *reinterpret_cast<const float4*>(g.b + col), b1 = *reinterpret_cast<const float4*>(g.b + col + 4);
     const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    const float y[8] = {dec * b0.x * u.x, dec * b0.y * u.y, dec * b0.z * u.z, dec * b0.w * u.w,
-                        dec * b1.x * v.x, dec * b1.y * v.y, dec * b1.z * v.z, dec * b1.w * v.w};
+    const float bs[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float2 z = mul2(mul2(make_float2(dec, dec), make_float2(bs[e], bs[e + 1])), make_float2(x[e], x[e + 1]));
+      y[e] = z.x, y[e + 1] = z.y;
+    }
     put_piece(tb, r, col / 8, x);
     put_piece(tb + 2 * kBox, r, col / 8, y);
   }
@@ -593,9 +599,13 @@ __device__ __forceinline__ void run_out(const treewy_seqs& a, ChunkSmem& cs, uns
         uint32_t x[8];
         tmem_ld8_async(tm + kColO + 8 * j, x);
         tmem_wait8(x);
-        const float y[8] = {u.x * __uint_as_float(x[0]), u.y * __uint_as_float(x[1]), u.z * __uint_as_float(x[2]),
-                            u.w * __uint_as_float(x[3]), v.x * __uint_as_float(x[4]), v.y * __uint_as_float(x[5]),
-                            v.z * __uint_as_float(x[6]), v.w * __uint_as_float(x[7])};
+        const float bs[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 z = mul2(make_float2(bs[e], bs[e + 1]), make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+          y[e] = z.x, y[e + 1] = z.y;
+        }
         put_piece(mtb, d - 64, j, y);
       }
       tc_fence_before_sync();
