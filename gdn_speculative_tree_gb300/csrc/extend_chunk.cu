@@ -205,7 +205,7 @@ __device__ __forceinline__ void dot_rows(const float* L, const float* R, float (
   float2 sum[V / 2];
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) sum[e] = make_float2(0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 1
   for (int i = 0; i < N; i += 4) {
     const float4 l = *reinterpret_cast<const float4*>(L + i);
     const float ls[4] = {l.x, l.y, l.z, l.w};
@@ -627,13 +627,18 @@ __device__ __forceinline__ void run_out(const treewy_seqs& a, ChunkSmem& cs, uns
       tmem_ld16_async(tm + kColO + 16 * b, x);
       tmem_wait16(x);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < 16; e += 2) {
         const int n = 16 * b + e;
-        const float y = o[n] + __uint_as_float(x[e]);
+        const float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(1.f, 1.f),
+                              make_float2(o[n], o[n + 1]));
         if constexpr (OF32) {
-          if (n < rows && d < a.dv) reinterpret_cast<float*>(a.o)[at0 + n * step + d] = y;
+          float* out = reinterpret_cast<float*>(a.o) + at0 + n * step + d;
+          if (n < rows && d < a.dv) out[0] = y.x;
+          if (n + 1 < rows && d < a.dv) out[step] = y.y;
         } else {
-          *reinterpret_cast<__nv_bfloat16*>(tile + n * 256 + 2 * d) = __float2bfloat16_rn(y);
+          const __nv_bfloat162 p = __floats2bfloat162_rn(y.x, y.y);
+          *reinterpret_cast<__nv_bfloat16*>(tile + n * 256 + 2 * d) = p.x;
+          *reinterpret_cast<__nv_bfloat16*>(tile + (n + 1) * 256 + 2 * d) = p.y;
         }
       }
     }
