@@ -36,9 +36,21 @@
 // Every product takes an f32 operand as two bf16 terms x = hi + lo (16
 // significant bits; lo times lo is left out), accumulates in f32, and keys,
 // queries and values are exact, so a result is within a few 2^-17 of the
-// recurrence's.  Ratios g_n/g_i are running products of the decays between i
-// and n, never quotients, so they are right however small g has become, a
-// decay of zero included.
+// recurrence's (measured: 4e-6 to 5e-6 of the state's norm, where sums in f32
+// token by token give 2e-7; one bf16 term would give 2e-3, and three half as
+// many products again).  Ratios g_n/g_i are running products of the decays
+// between i and n, never quotients, so they are right however small g has
+// become, a decay of zero included.
+//
+// Bound by what a CTA's warps issue between the products, not by the products
+// or by HBM: a chunk takes about 8000 cycles, of which [K;Q] K^T, T, kt and
+// the tiles for the products are the longest way, and the SM's tensor pipe is
+// busy for a third and its issue slots for half of them.  The roles' code
+// together (76 KB) does not fit the instruction cache, so that its size shows
+// in every figure (a full batch of 16 prompts x 32 heads of 4096 tokens: 125 KB
+// 1684 us, 92 KB 1294 us, 83 KB 1205 us, 76 KB 1090 us): loops stay rolled
+// where the registers allow it, and f32 work is packed in pairs.  4096 tokens
+// of 32 heads 271 us (15 us of HBM time), the full batch 1063 us (243 us).
 #include "treewy_device.cuh"
 #include "treewy_internal.h"
 
@@ -60,9 +72,9 @@ static_assert(2 * kStateRegs + 2 * kPrepRegs + kOutRegs + kMiscRegs <= 6 * kLaun
 
 // TMEM columns
 constexpr uint32_t kColS = 0;                // S: hi in 64 columns, lo in 64 (bf16 pairs)
-constexpr uint32_t kColW = 128;              // S k, then W (16 columns per 16 tokens: hi 8, lo 8)
+constexpr uint32_t kColW = 128;              // W (16 columns per 16 tokens: hi 8, lo 8)
 constexpr uint32_t kColO = 192;              // S q, then MT (lanes 64-127), then MT W
-constexpr uint32_t kColD = 256;              // sum W kt^T
+constexpr uint32_t kColD = 256;              // S k in the first 64, then sum W kt^T
 constexpr uint32_t kColG = 384;              // [K;Q] K^T
 constexpr uint32_t kColK = 448;              // kt^T
 constexpr uint32_t kTmemCols = 512;
@@ -523,7 +535,7 @@ __device__ __forceinline__ void run_state(const treewy_seqs& a, ChunkSmem& cs, u
             split2(w.x, w.y, hi[2 * j + k / 2], lo[2 * j + k / 2]);
           }
         }
-        // 16 tokens: hi in 8 columns, lo in 8, in place of what was just read
+        // 16 tokens: hi in 8 columns, lo in 8
         tmem_st8(tm + kColW + n0 + 16 * b, hi);
         tmem_st8(tm + kColW + n0 + 16 * b + 8, lo);
       }
@@ -726,10 +738,11 @@ __device__ __forceinline__ void run_gates(const treewy_seqs& a, ChunkSmem& cs, c
 __device__ __forceinline__ void issue_gram(ChunkSmem& cs, unsigned char* base, int c) {
   constexpr uint32_t id = idesc_bf16_f32(128, kC);
   const uint64_t s0 = smem_desc_sw128(smem_addr(base + (c & 1) * kStageBytes), 1024);
-#pragma unroll 1
+  uint64_t at = s0;
+#pragma unroll 2
   for (int k = 0; k < 8; ++k) {
-    const uint64_t at = s0 + (((k >> 2) * 2 * kBox + (k & 3) * 32) >> 4);
     mma_bf16(cs.tmem + kColG, at, at, id, k > 0);
+    at += k == 3 ? (2 * kBox - 96) >> 4 : 2;
   }
   mma_commit(&cs.gram_done);
 }
@@ -962,7 +975,7 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
       if (!held(&cs.s_ready[half], c)) return;
       if (elect_one()) {
       tc_fence_after_sync();
-#pragma unroll 1
+#pragma unroll 2
       for (int k = 0; k < 4; ++k) {
         const uint64_t kd = s0 + ((half * 2 * kBox + 32 * k) >> 4);
         mma_ts(tm + kColD, tm + kColS + 32 * half + 8 * k, kd, id, half > 0 || k > 0);
@@ -979,9 +992,9 @@ __device__ __forceinline__ void run_mma(ChunkSmem& cs, unsigned char* base, int 
     if (c > 0 && !held(&cs.o_read, c - 1)) return;
     if (elect_one()) {
     tc_fence_after_sync();
+    uint64_t qd = s0 + (kBox >> 4);
 #pragma unroll 1
-    for (int k = 0; k < 8; ++k) {
-      const uint64_t qd = s0 + (((k >> 2) * 2 * kBox + kBox + 32 * (k & 3)) >> 4);
+    for (int k = 0; k < 8; ++k, qd += k == 4 ? (2 * kBox - 96) >> 4 : 2) {
       mma_ts(tm + kColO, tm + kColS + 8 * k, qd, id, k > 0);
       mma_ts(tm + kColO, tm + kColS + 64 + 8 * k, qd, id, 1u);
     }
