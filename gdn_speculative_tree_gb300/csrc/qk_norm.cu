@@ -125,21 +125,24 @@ __device__ __forceinline__ void put(void* p, V x) {
 enum Pairs { kLanes, kNeighbours, kOdd };
 template <typename T, int LANES, int UNROLL, int THREADS, Pairs PAIRS>
 __global__ void __launch_bounds__(THREADS, 896 / THREADS)
-    qk_norm_kernel(const treewy_qk a, int q_units, int units, unsigned parts, float mean) {
+    qk_norm_kernel(const treewy_qk a, int q_units, int units, float mean) {
   after_previous();
   constexpr bool ODD = PAIRS == kOdd, NEXT = PAIRS == kNeighbours, kStream = UNROLL > 2;
   constexpr int kPass = 32 / LANES;                   // heads per pass
   const int lane = threadIdx.x % LANES, grp = (threadIdx.x & 31) / LANES;
-  const int64_t t = static_cast<int64_t>(blockIdx.x / parts) * (THREADS / 32) + (threadIdx.x >> 5);
-  if (t >= a.T) return;                               // a whole warp
-  const int position = a.rope_dims > 0 ? __ldg(a.position + t) : 0;
   const int c0 = 8 * lane;
   const bool mine = c0 < a.d;
   // half is a multiple of 8 (but where ODD): a pair's other eight are half / 8 lanes on
   const int half = a.rope_dims / 2;
   const bool in_rope = c0 < a.rope_dims, low = c0 < half;
   const int other = in_rope ? (low ? lane + half / 8 : lane - half / 8) : lane;
-  for (int part = blockIdx.x % parts; part < units; part += parts) {
+  // a warp's first token and part, and the way to its next ones
+  const unsigned at = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), warps = gridDim.x * (THREADS / 32);
+  int64_t t = at / static_cast<unsigned>(units);
+  int part = static_cast<int>(at % static_cast<unsigned>(units));
+  const int hop = static_cast<int>(warps / units), step = static_cast<int>(warps % units);
+  for (; t < a.T; t += hop + (part + step >= units), part = part + step - (part + step >= units ? units : 0)) {
+    const int position = a.rope_dims > 0 ? __ldg(a.position + t) : 0;
     const bool isq = part < q_units;
     const int heads = isq ? a.Hq : a.Hk, repeat = isq ? a.q_repeat : a.k_repeat;
     const int h0 = (isq ? part : part - q_units) * (UNROLL * kPass) + grp;
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
     const float* tab = nullptr;                       // looked up while the rows are on their way
     if (a.rope_dims > 0) {
       tab = table_row(a, position, part == 0 && (threadIdx.x & 31) == 0);
-      if (tab == nullptr) return;                     // a whole warp
+      if (tab == nullptr) continue;                   // a whole warp
     }
     // y = f (x wc + x' ws) with x' the pair's other element (ws = 0: no pair)
     float wc[8], ws[8];
@@ -177,14 +180,20 @@ __global__ void __launch_bounds__(THREADS, 896 / THREADS)
     const float scale = isq ? a.q_scale : a.k_scale;
 #pragma unroll
     for (int e = 0; e < 8; ++e) wc[e] = scale, ws[e] = 0.f;
-    if (ODD) {
+    if constexpr (ODD) {
+      float cs[8], sn[8], v[8];                       // all on their way before the first is used
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (c0 + e >= a.rope_dims) continue;
-        const int by = pair_step(a, c0 + e), i = a.interleaved ? (c0 + e) / 2 : by > 0 ? c0 + e : c0 + e - half;
-        const float sn = by > 0 ? -tab[half + i] : tab[half + i];
-        wc[e] *= tab[i];
-        ws[e] = scale * sn * (weight != nullptr ? weight[c0 + e + by] : 1.f);
+        const int c = c0 + e, by = pair_step(a, c), i = a.interleaved ? c / 2 : by > 0 ? c : c - half;
+        const bool pair = c < a.rope_dims;
+        cs[e] = pair ? tab[i] : 1.f;
+        sn[e] = pair ? tab[half + i] : 0.f;
+        v[e] = pair && weight != nullptr ? weight[c + by] : 1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        wc[e] *= cs[e];
+        ws[e] = scale * (pair_step(a, c0 + e) > 0 ? -sn[e] : sn[e]) * v[e];
       }
     } else if (in_rope) {
       float cs[8], sn[8], v[8];
@@ -331,26 +340,25 @@ template <typename T, int LANES, int UNROLL, int THREADS, Pairs PAIRS>
 cudaError_t launch_passes(const treewy_qk& a, cudaStream_t stream) {
   constexpr int kHeads = UNROLL * 32 / LANES;
   const int q_units = (a.Hq + kHeads - 1) / kHeads, units = q_units + (a.Hk + kHeads - 1) / kHeads;
-  const int64_t ctas = (a.T + THREADS / 32 - 1) / (THREADS / 32);
-  const unsigned parts = static_cast<unsigned>(min(int64_t(units), max(int64_t(1), int64_t(0x7fffffff) / ctas)));
-  const dim3 grid(static_cast<unsigned>(ctas * parts));
+  // as many warps as the GPU holds (a CTA costs about a nanosecond of the whole
+  // GPU's time to start), each with every so many-th token and part
+  const int64_t ctas = (a.T * units + THREADS / 32 - 1) / (THREADS / 32);
+  const dim3 grid(static_cast<unsigned>(min(ctas, int64_t(152 * 896 / THREADS))));
   const float mean = a.norm == TREEWY_NORM_RMS ? 1.0f / static_cast<float>(a.d) : 1.f;
-  return launch_after(qk_norm_kernel<T, LANES, UNROLL, THREADS, PAIRS>, grid, THREADS, stream, a, q_units, units, parts, mean);
+  return launch_after(qk_norm_kernel<T, LANES, UNROLL, THREADS, PAIRS>, grid, THREADS, stream, a, q_units, units, mean);
 }
 
 template <typename T, int LANES>
 cudaError_t launch(const treewy_qk& a, cudaStream_t stream) {
   // Many rows: as many heads per warp as its registers hold, and a warp per
-  // CTA, so that a warp's place is filled as soon as it is done, a token's
-  // parts one after the other (32768 tokens of 18 bf16 heads of 256: 106 us,
-  // 5.8 TB/s; 112 us without the streaming hints, 122 us with all tokens' first
-  // parts first, 143 us with two warps per CTA).  Few: the rows spread over
-  // more warps (256 tokens of 32 heads of 128: 2.3 us).
-  // Odd pairs: one shape for both (8001 tokens of 24 bf16 heads of 80, 20 of
-  // them rotated: 48 us, 67 us element by element; more heads per warp save
-  // 4 us and cost f32 6 to 20).
+  // CTA, a token's parts one after the other (32768 tokens of 18 bf16 heads of
+  // 256: 102 us, 6.0 TB/s; 106 us with a CTA per token and part, 118 us without
+  // the streaming hints, 128 us with all tokens' first parts first).  Few: the
+  // rows spread over more warps (256 tokens of 32 heads of 128: 2.3 us).  Odd
+  // pairs: one shape for both (8001 tokens of 24 bf16 heads of 80, 20 of them
+  // rotated: 40 us, 67 us element by element).
   constexpr int kMany = sizeof(T) == 2 ? 8 : 4;
-  if (a.rope_dims % (a.interleaved ? 8 : 16) != 0) return launch_passes<T, LANES, 2, 64, kOdd>(a, stream);
+  if (a.rope_dims % (a.interleaved ? 8 : 16) != 0) return launch_passes<T, LANES, 4, 32, kOdd>(a, stream);
   const bool many = a.T * (a.Hq + a.Hk) >= int64_t(152) * 64 * (32 / LANES);
   if (a.interleaved)
     return many ? launch_passes<T, LANES, kMany, 32, kNeighbours>(a, stream)
