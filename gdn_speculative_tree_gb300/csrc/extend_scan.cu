@@ -15,10 +15,10 @@
 // load would be followed by its conversion, one load's latency after the other
 // (64 tokens x 32 heads on a bf16 pool: 25 us, 32 with the branch).
 //
-// decode_kernel: at most one token per sequence, a warp per CTA and 16 rows
-// per warp.  Its time is the state's way in and out of HBM (2 x 64 KB per f32
+// decode_kernel: at most one token per sequence, 16 rows per warp.  Its time is the state's way in and out of HBM (2 x 64 KB per f32
 // head against 1.3 KB of everything else); nothing depends on the state's load
-// but the token's own arithmetic.  256 tokens x 32 heads, f32: 178 us, 6.1 TB/s.
+// but the token's own arithmetic.  256 tokens x 32 heads, f32: 159 us, 6.8 TB/s,
+// the rate of a plain copy.
 //
 // few_kernel: the same for up to 16 tokens (2048 heads x 4 tokens: 78 us, 92
 // to 126 us by the staged kernel below), bound by the chain of shuffles.
@@ -45,7 +45,7 @@
 namespace treewy {
 namespace {
 
-constexpr int kDecodeWarps = 1, kDecodeThreads = 32 * kDecodeWarps;
+constexpr int kFewWarps = 1, kFewThreads = 32 * kFewWarps;
 constexpr int kStage = 16;  // tokens staged at a time
 constexpr int kPrep = 128;  // threads that stage them
 constexpr int kBlock = 4;   // tokens that take one sweep of the state
@@ -213,17 +213,17 @@ __device__ __forceinline__ void unpack_row(const RawRow<SB>& r, float (&x)[16]) 
   }
 }
 
-// One (sequence, head) and 4 kDecodeWarps RPT of its rows per CTA, one token
+// One (sequence, head) and 4 WARPS RPT of its rows per CTA, one token
 // at most.  WIDE: every load of the state, q and k is a whole piece; the rows
 // then wait in registers as they are stored, all of them in flight at once,
 // and are taken one after the other.
-template <int RPT, bool SB, bool QB, bool WIDE>
-__global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seqs a) {
+template <int RPT, int WARPS, bool SB, bool QB, bool WIDE>
+__global__ void __launch_bounds__(32 * WARPS) decode_kernel(const treewy_seqs a) {
   after_previous();
   constexpr int V = SB ? 8 : 4;
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int l = threadIdx.x & 7;
-  const int first = static_cast<int>(blockIdx.y) * (4 * kDecodeWarps * RPT);
+  const int first = static_cast<int>(blockIdx.y) * (4 * WARPS * RPT);
   const Seq s = load_seq(a, r);
   if (s.flags) {
     if (threadIdx.x == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
@@ -295,12 +295,12 @@ __global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const treewy_seq
 // The same split for a few tokens: S in f32 registers over all of them, the
 // next token's rows on their way meanwhile.
 template <int RPT, bool SB, bool QB, bool WIDE>
-__global__ void __launch_bounds__(kDecodeThreads) few_kernel(const treewy_seqs a) {
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const treewy_seqs a) {
   after_previous();
   constexpr int V = SB ? 8 : 4;
   const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
   const int l = threadIdx.x & 7;
-  const int first = static_cast<int>(blockIdx.y) * (4 * kDecodeWarps * RPT);
+  const int first = static_cast<int>(blockIdx.y) * (4 * kFewWarps * RPT);
   const Seq s = load_seq(a, r);
   if (s.flags) {
     if (threadIdx.x == 0 && blockIdx.y == 0 && h == 0) atomicOr(a.status + r, s.flags);
@@ -592,20 +592,20 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
   }
 }
 
-template <int RPT, bool SB, bool QB, bool WIDE>
+template <int RPT, int WARPS, bool SB, bool QB, bool WIDE>
 cudaError_t launch_decode(const treewy_seqs& a, cudaStream_t stream) {
-  constexpr int kRows = 4 * kDecodeWarps * RPT;
+  constexpr int kRows = 4 * WARPS * RPT;
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
                   static_cast<unsigned>((a.dv + kRows - 1) / kRows));
-  return launch_after(decode_kernel<RPT, SB, QB, WIDE>, grid, kDecodeThreads, stream, a);
+  return launch_after(decode_kernel<RPT, WARPS, SB, QB, WIDE>, grid, 32 * WARPS, stream, a);
 }
 
 template <int RPT, bool SB, bool QB, bool WIDE>
 cudaError_t launch_few(const treewy_seqs& a, cudaStream_t stream) {
-  constexpr int kRows = 4 * kDecodeWarps * RPT;
+  constexpr int kRows = 4 * kFewWarps * RPT;
   const dim3 grid(static_cast<unsigned>(a.R) * static_cast<unsigned>(a.H),
                   static_cast<unsigned>((a.dv + kRows - 1) / kRows));
-  return launch_after(few_kernel<RPT, SB, QB, WIDE>, grid, kDecodeThreads, stream, a);
+  return launch_after(few_kernel<RPT, SB, QB, WIDE>, grid, kFewThreads, stream, a);
 }
 
 template <int RPT, bool SB, bool QB, bool WIDE, int CL, int THREADS>
@@ -619,8 +619,12 @@ cudaError_t launch_scan(const treewy_seqs& a, cudaStream_t stream) {
 template <bool SB, bool QB, bool WIDE>
 cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
   const int64_t heads = static_cast<int64_t>(a.R) * a.H;
-  if (a.max_len <= 1)  // a quarter of a head per CTA, or less while that leaves SMs idle
-    return 4 * heads >= 304 ? launch_decode<4, SB, QB, WIDE>(a, stream) : launch_decode<1, SB, QB, WIDE>(a, stream);
+  // Up to 75 heads spread over as many CTAs as they have rows for; more take 16
+  // rows per warp and 64 per CTA (32 on a bf16 pool): 8192 heads 159 us, 177 us
+  // with 16 per CTA, 159 us with all 128; on a bf16 pool 94, 94 and 100 us.
+  if (a.max_len <= 1)
+    return 4 * heads >= 304 ? launch_decode<4, SB ? 2 : 4, SB, QB, WIDE>(a, stream)
+                            : launch_decode<1, 1, SB, QB, WIDE>(a, stream);
   if (a.max_len <= 16)
     return 4 * heads >= 304 ? launch_few<2, SB, QB, WIDE>(a, stream) : launch_few<1, SB, QB, WIDE>(a, stream);
   // 16 rows of a head per CTA while two CTAs per SM hold them all, then 64;
