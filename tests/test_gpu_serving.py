@@ -326,6 +326,45 @@ def test_extend_f32_outputs_over_a_rounded_state(cuda_lib, n):
     assert np.linalg.norm(f64(c.o) - ref) <= 2.0 ** -14 * np.linalg.norm(ref)
 
 
+@pytest.mark.parametrize("lens", [[5, 0, 9, 16], [17, 3, 0, 38]])
+@pytest.mark.parametrize("H", [1, 24])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (52, 71)])
+@pytest.mark.parametrize("qkv,pool", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+def test_extend_token_by_token_splits(cuda_lib, lens, H, dk, dv, qkv, pool):
+    """Few and many heads, below and above the lengths that are staged."""
+    Case(lens, H=H, dk=dk, dv=dv, qkv=qkv, pool=pool, fresh=(2,), seed=18).run(binding.FLAG_FORCE_GENERIC).check()
+
+
+@pytest.mark.parametrize("n", [9, 30])
+@pytest.mark.parametrize("what", ["k", "v", "alpha"])
+@pytest.mark.parametrize("at", [4, 6, 8])
+def test_extend_token_by_token_nan_goes_forward_only(cuda_lib, n, what, at):
+    ok = Case([n], H=2, seed=19).run(binding.FLAG_FORCE_GENERIC)
+    c = Case([n], H=2, seed=19)
+    getattr(c, what)[at] = float("nan")
+    c.run(binding.FLAG_FORCE_GENERIC)
+    assert torch.equal(c.o[:at], ok.o[:at]) and torch.isnan(c.o[at:]).all()
+
+
+@pytest.mark.parametrize("n", [3, 18])
+def test_extend_token_by_token_infinite_last_token(cuda_lib, n):
+    """What fills a block of tokens up behind a sequence's end adds nothing, not even to an infinite state."""
+    c = Case([n], H=1, seed=20)
+    c.alpha[n - 1], c.beta[n - 1], c.v[n - 1] = 1.0, 1.0, float("inf")
+    c.k[n - 1] = 0
+    c.k[n - 1, :, 5] = 1.0
+    before = Case([n - 1], H=1, seed=20)
+    for x in ("q", "k", "v", "alpha", "beta"):
+        getattr(before, x).copy_(getattr(c, x)[:n - 1])
+    before.pool.copy_(c.before)
+    before.slot = c.slot
+    before.run(binding.FLAG_FORCE_GENERIC)
+    c.run(binding.FLAG_FORCE_GENERIC)
+    got, ref = c.pool[c.slot[0].long(), 0], before.pool[c.slot[0].long(), 0]
+    assert torch.isinf(got[:, 5]).all() and torch.isnan(got[:, [4, 6]]).all()
+    assert torch.isfinite(ref).all()
+
+
 # ------------------------------------------------------------------ qk_norm
 
 def qk_case(T, Hq, Hk, d, dtype="bf16", norm="l2", rope=0, interleaved=False, repeat=(1, 1), pad=0, shift=0,
