@@ -20,8 +20,8 @@
 // but the token's own arithmetic.  256 tokens x 32 heads, f32: 159 us, 6.8 TB/s,
 // the rate of a plain copy.
 //
-// few_kernel: the same for up to 16 tokens (2048 heads x 4 tokens: 78 us, 92
-// to 126 us by the staged kernel below), bound by the chain of shuffles.
+// few_kernel: the same for up to 12 or 16 tokens (2048 heads x 4 tokens: 78 us,
+// 92 to 126 us by the staged kernel below), bound by the chain of shuffles.
 //
 // scan_kernel: any number of tokens, for the sizes and types that the chunked
 // kernel does not take.  Four tokens take one sweep of the state: with G_n the
@@ -35,8 +35,9 @@
 // right), which turns eight sums over a row's lanes into seven shuffles for
 // all four tokens and one chain per four tokens.  Four warps of a CTA stage
 // the next 16 tokens and their blocks' products meanwhile.  Bound by issue and
-// by the reads of k and q from shared memory: 4096 tokens of 32 heads 1133 us
-// (3262 us a token at a time, staged by the warps that use it).
+// by the reads of k and q from shared memory: 4096 tokens of 32 heads 996 us
+// (3262 us a token at a time, staged by the warps that use it); with one head
+// per eight SMs by the staging, 0.15 us a token.
 #include <type_traits>
 
 #include "treewy_device.cuh"
@@ -387,21 +388,27 @@ struct Stage {
   float alpha[kStage], beta[kStage];
 };
 
-// Sums over the eight lanes of a row group of eight values: lane l gets value l's.
-__device__ __forceinline__ float sum8_each(const float (&x)[8], int l) {
-  float y[4], z[2];
+// Sums over the eight lanes of a row group of eight values per row: lane l gets
+// value l's.  Step by step for all rows, so that one's shuffle need not wait
+// for another's.
+template <int RPT>
+__device__ __forceinline__ void sum8_each(const float (&x)[RPT][8], int l, float (&out)[RPT]) {
+  float y[RPT][4], z[RPT][2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float mine = (l & 4) ? x[e + 4] : x[e], other = (l & 4) ? x[e] : x[e + 4];
-    y[e] = mine + __shfl_xor_sync(kFull, other, 4);
+  for (int j = 0; j < RPT; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      y[j][e] = ((l & 4) ? x[j][e + 4] : x[j][e]) + __shfl_xor_sync(kFull, (l & 4) ? x[j][e] : x[j][e + 4], 4);
   }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float mine = (l & 2) ? y[e + 2] : y[e], other = (l & 2) ? y[e] : y[e + 2];
-    z[e] = mine + __shfl_xor_sync(kFull, other, 2);
+  for (int j = 0; j < RPT; ++j) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      z[j][e] = ((l & 2) ? y[j][e + 2] : y[j][e]) + __shfl_xor_sync(kFull, (l & 2) ? y[j][e] : y[j][e + 2], 2);
   }
-  const float mine = (l & 1) ? z[1] : z[0], other = (l & 1) ? z[0] : z[1];
-  return mine + __shfl_xor_sync(kFull, other, 1);
+#pragma unroll
+  for (int j = 0; j < RPT; ++j)
+    out[j] = ((l & 1) ? z[j][1] : z[j][0]) + __shfl_xor_sync(kFull, (l & 1) ? z[j][0] : z[j][1], 1);
 }
 
 template <int ID, int N>
@@ -441,14 +448,18 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
     Raw nk[kPer], nq[kPer], nv[kPerV];
     float ngate = 0.f;
     auto fetch = [&](int t0) {  // the stage from token t0 on, into registers
+      {
+        constexpr int kHop = kPrep / kCols;  // tokens between a thread's elements, all of one column
+        const int n0 = tid / kCols, c = tid % kCols;
+        const Raw* k = pk + (s.tok0 + t0 + n0) * a.k_stride + static_cast<int64_t>(hk) * a.dk + c;
+        const Raw* q = pq + (s.tok0 + t0 + n0) * a.q_stride + static_cast<int64_t>(hk) * a.dk + c;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = tid + i * kPrep, n = e / kCols, c = e % kCols;
-        const int64_t t = s.tok0 + t0 + n;
-        nk[i] = nq[i] = 0;
-        if (t0 + n < s.len && c < a.dk) {
-          nk[i] = __ldg(pk + t * a.k_stride + static_cast<int64_t>(hk) * a.dk + c);
-          nq[i] = __ldg(pq + t * a.q_stride + static_cast<int64_t>(hk) * a.dk + c);
+        for (int i = 0; i < kPer; ++i, k += kHop * a.k_stride, q += kHop * a.q_stride) {
+          nk[i] = nq[i] = 0;
+          if (t0 + n0 + i * kHop < s.len && c < a.dk) {
+            nk[i] = __ldg(k);
+            nq[i] = __ldg(q);
+          }
         }
       }
 #pragma unroll
@@ -481,7 +492,7 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
       fetch(t0 + kStage);
       const int m = min(kStage, s.len - t0);
       // 10 products q_n . k_j and 6 k_n . k_j of each block, eight lanes per product
-#pragma unroll 1
+#pragma unroll 2
       for (int p = tid >> 3; p < kStage / kBlock * 16; p += kPrep / 8) {
         const int b = p / 16 * kBlock, e = p % 16;
         if (b >= m) break;  // whole warps: 4 products of one block each
@@ -489,23 +500,23 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
         const int f = isq ? e : e - 10;
         const int n = isq ? (f >= 6 ? 3 : f >= 3 ? 2 : f >= 1 ? 1 : 0) : (f >= 3 ? 3 : f >= 1 ? 2 : 1);
         const int j = f - (isq ? n * (n + 1) / 2 : n * (n - 1) / 2);
-        float x[CL], y[CL], sum[2] = {0.f, 0.f};
+        float x[CL], y[CL];
+        float2 sum = make_float2(0.f, 0.f);
         load_row<V, true>(isq ? st.q[b + n] : st.k[b + n], false, 0, kCols, l, x);
         load_row<V, true>(st.k[b + j], false, 0, kCols, l, y);
 #pragma unroll
-        for (int c = 0; c < CL; ++c) sum[c & 1] = fmaf(x[c], y[c], sum[c & 1]);
-        float z = sum8(sum[0] + sum[1]);
-        if (!isq) z *= st.beta[b + n];
-        for (int i = j + 1; i <= n; ++i) z *= st.alpha[b + i];
+        for (int c = 0; c < CL; c += 2) sum = fma2(make_float2(x[c], x[c + 1]), make_float2(y[c], y[c + 1]), sum);
+        const float4 al = *reinterpret_cast<const float4*>(st.alpha + b);
+        const float beta = st.beta[b + n];
+        const float a1 = j < 1 && n >= 1 ? al.y : 1.f, a2 = j < 2 && n >= 2 ? al.z : 1.f, a3 = n >= 3 && j < 3 ? al.w : 1.f;
+        const float z = sum8(sum.x + sum.y) * (isq ? 1.f : beta) * (a1 * a2 * a3);
         if (l == 0) (isq ? st.kq : st.kk)[b + n][j] = z;
       }
       if (tid < kStage) {
-        const int b = tid & ~(kBlock - 1);
-        float g = st.alpha[b], d = 1.f;
-        for (int i = b + 1; i < b + kBlock; ++i) {
-          if (i <= tid) g *= st.alpha[i];
-          else d *= st.alpha[i];
-        }
+        const int n = tid & (kBlock - 1);
+        const float4 al = *reinterpret_cast<const float4*>(st.alpha + tid - n);
+        const float g = al.x * (n >= 1 ? al.y : 1.f) * (n >= 2 ? al.z : 1.f) * (n >= 3 ? al.w : 1.f);
+        const float d = (n < 1 ? al.y : 1.f) * (n < 2 ? al.z : 1.f) * (n < 3 ? al.w : 1.f);
         st.gate[tid] = g;
         st.dec[tid] = d;
       }
@@ -526,6 +537,8 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
       for (int c = 0; c < CL; ++c) S[j][c] = 0.f;
     }
   }
+  // row 0's output of this lane's token of the first block
+  const int64_t at0 = ((s.tok0 + (l & (kBlock - 1))) * a.H + h) * a.dv + group_row<RPT>(first, 0);
   for (int t0 = 0; t0 < s.len; t0 += kStage) {
     const Stage<CL, kRows>& st = stages[t0 / kStage & 1];
     const int m = min(kStage, s.len - t0);
@@ -541,13 +554,16 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
         load_row<V, true>(st.q[b + n], false, 0, kCols, l, q);
 #pragma unroll
         for (int j = 0; j < RPT; ++j) {
-          dot[j][n] = S[j][0] * k[n][0];
-          dot[j][kBlock + n] = S[j][0] * q[0];
+          const float2 s0 = make_float2(S[j][0], S[j][1]);
+          float2 x = mul2(s0, make_float2(k[n][0], k[n][1])), y = mul2(s0, make_float2(q[0], q[1]));
 #pragma unroll
-          for (int c = 1; c < CL; ++c) {
-            dot[j][n] = fmaf(S[j][c], k[n][c], dot[j][n]);
-            dot[j][kBlock + n] = fmaf(S[j][c], q[c], dot[j][kBlock + n]);
+          for (int c = 2; c < CL; c += 2) {
+            const float2 sc = make_float2(S[j][c], S[j][c + 1]);
+            x = fma2(sc, make_float2(k[n][c], k[n][c + 1]), x);
+            y = fma2(sc, make_float2(q[c], q[c + 1]), y);
           }
+          dot[j][n] = x.x + x.y;
+          dot[j][kBlock + n] = y.x + y.y;
         }
       }
       // lane l < 4: token l's S k, the others token l - 4's S q
@@ -555,23 +571,34 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
       const float gate = st.gate[mine], beta = st.beta[mine], last = st.gate[b + kBlock - 1];
       const float4 m4 = *reinterpret_cast<const float4*>(st.kq[mine]);
       const float mq[kBlock] = {m4.x, m4.y, m4.z, m4.w};
-      float u[RPT][kBlock];
+      const float4 k1 = *reinterpret_cast<const float4*>(st.kk[b + 1]), k2 = *reinterpret_cast<const float4*>(st.kk[b + 2]),
+                   k3 = *reinterpret_cast<const float4*>(st.kk[b + 3]);
+      float v[RPT], y[RPT], u[RPT][kBlock];
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) v[j] = st.v[mine][group_row<RPT>(0, j)];
+      // the rows' chains side by side
+      sum8_each<RPT>(dot, l, y);
 #pragma unroll
       for (int j = 0; j < RPT; ++j) {
-        float y = gate * sum8_each(dot[j], l);
-        const float rhs = mine < m ? beta * (st.v[mine][group_row<RPT>(0, j)] - y) : 0.f;
+        y[j] *= gate;
+        const float rhs = mine < m ? beta * (v[j] - y[j]) : 0.f;
+#pragma unroll
+        for (int n = 0; n < kBlock; ++n) u[j][n] = __shfl_sync(kFull, rhs, n, 8);
+      }
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) {
+        u[j][1] = b + 1 < m ? fmaf(-k1.x, u[j][0], u[j][1]) : 0.f;
+        u[j][2] = b + 2 < m ? fmaf(-k2.y, u[j][1], fmaf(-k2.x, u[j][0], u[j][2])) : 0.f;
+        u[j][3] = b + 3 < m ? fmaf(-k3.z, u[j][2], fmaf(-k3.y, u[j][1], fmaf(-k3.x, u[j][0], u[j][3]))) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) {
 #pragma unroll
         for (int n = 0; n < kBlock; ++n) {
-          u[j][n] = __shfl_sync(kFull, rhs, n, 8);
-          if (b + n < m) {
-#pragma unroll
-            for (int i = 0; i < n; ++i) u[j][n] = fmaf(-st.kk[b + n][i], u[j][i], u[j][n]);
-          }
-          if (n <= (l & (kBlock - 1))) y = fmaf(mq[n], u[j][n], y);
+          if (n <= (l & (kBlock - 1))) y[j] = fmaf(mq[n], u[j][n], y[j]);
         }
         const int row = group_row<RPT>(first, j);
-        if (l >= kBlock && mine < m && row < a.dv)
-          store_o(a, ((s.tok0 + t0 + mine) * a.H + h) * a.dv + row, y);
+        if (l >= kBlock && mine < m && row < a.dv) store_o(a, at0 + (t0 + b) * static_cast<int64_t>(a.H) * a.dv + 4 * j, y[j]);
       }
 #pragma unroll
       for (int n = 0; n < kBlock; ++n) {
@@ -580,7 +607,13 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
         for (int j = 0; j < RPT; ++j) {
           const float w = dec * u[j][n];
 #pragma unroll
-          for (int c = 0; c < CL; ++c) S[j][c] = fmaf(w, k[n][c], n == 0 ? last * S[j][c] : S[j][c]);
+          for (int c = 0; c < CL; c += 2) {
+            float2 x = make_float2(S[j][c], S[j][c + 1]);
+            if (n == 0) x = mul2(make_float2(last, last), x);
+            x = fma2(make_float2(w, w), make_float2(k[n][c], k[n][c + 1]), x);
+            S[j][c] = x.x;
+            S[j][c + 1] = x.y;
+          }
         }
       }
     }
@@ -625,7 +658,9 @@ cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
   if (a.max_len <= 1)
     return 4 * heads >= 304 ? launch_decode<4, SB ? 2 : 4, SB, QB, WIDE>(a, stream)
                             : launch_decode<1, 1, SB, QB, WIDE>(a, stream);
-  if (a.max_len <= 16)
+  // 12 tokens of 32 heads 8.0 us, 16 10.0 us, 20 staged 8.7 us; of 2048 heads 16
+  // 238 us, 20 staged 256 us
+  if (a.max_len <= (4 * heads >= 304 ? 16 : 12))
     return 4 * heads >= 304 ? launch_few<2, SB, QB, WIDE>(a, stream) : launch_few<1, SB, QB, WIDE>(a, stream);
   // 16 rows of a head per CTA while two CTAs per SM hold them all, then 64;
   // half as many columns per lane for small keys.
