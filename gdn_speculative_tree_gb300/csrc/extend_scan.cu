@@ -20,7 +20,7 @@
 // but the token's own arithmetic.  256 tokens x 32 heads, f32: 159 us, 6.8 TB/s,
 // the rate of a plain copy.
 //
-// few_kernel: the same for up to 12 or 16 tokens (2048 heads x 4 tokens: 78 us,
+// few_kernel: the same for up to 12 or 16 tokens (2048 heads x 4 tokens: 67 us,
 // 92 to 126 us by the staged kernel below), bound by the chain of shuffles.
 //
 // scan_kernel: any number of tokens, for the sizes and types that the chunked
@@ -342,26 +342,45 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const treewy_seqs a) {
       const int n = n0 + p;
       if (n >= s.len) break;
       if (n + 1 < s.len) next(n + 1, p ^ 1);
-      float kq = 0.f;
+      float2 prod = make_float2(0.f, 0.f), sk[RPT], sq[RPT];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) kq = fmaf(k[p][c], q[p][c], kq);
-      kq = sum8(kq);
+      for (int j = 0; j < RPT; ++j) sk[j] = sq[j] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 16; c += 2) {
+        const float2 kc = make_float2(k[p][c], k[p][c + 1]), qc = make_float2(q[p][c], q[p][c + 1]);
+        prod = fma2(kc, qc, prod);
+#pragma unroll
+        for (int j = 0; j < RPT; ++j) {
+          const float2 s2 = make_float2(S[j][c], S[j][c + 1]);
+          sk[j] = fma2(s2, kc, sk[j]);
+          sq[j] = fma2(s2, qc, sq[j]);
+        }
+      }
+      const float kq = sum8(prod.x + prod.y);
+      // lanes 0-3 of a row get S k, the others S q
+      float x[RPT], u[RPT];
 #pragma unroll
       for (int j = 0; j < RPT; ++j) {
-        float sk = 0.f, sq = 0.f;
+        const float y = sk[j].x + sk[j].y, z = sq[j].x + sq[j].y;
+        x[j] = ((l & 4) ? z : y) + __shfl_xor_sync(kFull, (l & 4) ? y : z, 4);
+      }
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          sk = fmaf(S[j][c], k[p][c], sk);
-          sq = fmaf(S[j][c], q[p][c], sq);
-          S[j][c] *= alpha[p];
+      for (int j = 0; j < RPT; ++j) x[j] += __shfl_xor_sync(kFull, x[j], 2);
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) x[j] = alpha[p] * (x[j] + __shfl_xor_sync(kFull, x[j], 1));
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) u[j] = __shfl_sync(kFull, beta[p] * (v[p][j] - x[j]), 0, 8);
+#pragma unroll
+      for (int j = 0; j < RPT; ++j) {
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+          const float2 y = fma2(make_float2(u[j], u[j]), make_float2(k[p][c], k[p][c + 1]),
+                                mul2(make_float2(alpha[p], alpha[p]), make_float2(S[j][c], S[j][c + 1])));
+          S[j][c] = y.x;
+          S[j][c + 1] = y.y;
         }
-        sk = sum8(sk);
-        sq = sum8(sq);
-        const float u = beta[p] * (v[p][j] - alpha[p] * sk);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) S[j][c] = fmaf(u, k[p][c], S[j][c]);
         const int row = group_row<RPT>(first, j);
-        if (l == 0 && row < a.dv) store_o(a, ((s.tok0 + n) * a.H + h) * a.dv + row, fmaf(kq, u, alpha[p] * sq));
+        if (l == 4 && row < a.dv) store_o(a, ((s.tok0 + n) * a.H + h) * a.dv + row, fmaf(kq, u[j], x[j]));
       }
     }
   }
@@ -659,7 +678,7 @@ cudaError_t launch(const treewy_seqs& a, cudaStream_t stream) {
     return 4 * heads >= 304 ? launch_decode<4, SB ? 2 : 4, SB, QB, WIDE>(a, stream)
                             : launch_decode<1, 1, SB, QB, WIDE>(a, stream);
   // 12 tokens of 32 heads 8.0 us, 16 10.0 us, 20 staged 8.7 us; of 2048 heads 16
-  // 238 us, 20 staged 256 us
+  // 210 us, 20 staged 256 us
   if (a.max_len <= (4 * heads >= 304 ? 16 : 12))
     return 4 * heads >= 304 ? launch_few<2, SB, QB, WIDE>(a, stream) : launch_few<1, SB, QB, WIDE>(a, stream);
   // 16 rows of a head per CTA while two CTAs per SM hold them all, then 64;

@@ -66,10 +66,10 @@ treewy_status validate_seqs(const treewy_seqs* s) {
 // A chunk takes 13 (bf16 pool) to 17 us whatever its length; token by token it
 // is 0.2 to 0.3 us a token (128 x 128 heads) while a head's rows have the SMs
 // to themselves, more when heads share them.  Chunks against tokens: 32 tokens
-// of 40 heads 13.0 and 13.3 us (16.7 and 13.4 us on an f32 pool), 40 tokens
-// 13.5 and 15.8 (16.7 and 16.2); 12 tokens of 80 heads 13.8 and 12.2 (16.7 and
-// 14.9), 16 tokens 14.4 and 15.2 (16.7 and 18.9); 12 tokens of 2048 heads 148
-// and 191 (187 and 181), 10 tokens 148 and 165 (186 and 155).
+// of 40 heads 13.3 and 13.2 us (16.7 and 13.4 us on an f32 pool), 40 tokens
+// 13.4 and 15.8 (16.7 and 15.9); 12 tokens of 80 heads 13.6 and 11.8 (16.8 and
+// 13.0), 16 tokens 13.9 and 14.8 (16.7 and 16.5); 10 tokens of 2048 heads 148
+// and 156 (186 and 132), 16 tokens 150 and 235 (187 and 211).
 int chunked_len(const treewy_seqs& s) { return int64_t(s.R) * s.H > 64 ? 13 : 33; }
 
 // Whether the chunked kernel takes the batch (s: strides resolved).  f32
@@ -77,8 +77,8 @@ int chunked_len(const treewy_seqs& s) { return int64_t(s.R) * s.H > 64 ? 13 : 33
 // a few 2^-18 off, so that one value in 500 of the next call's state rounds to
 // the other side, 2^-8 away, and its f32 outputs (70 tokens, decays above
 // 0.97) differ by 7e-5 in the norm, where f32 sums throughout keep them within
-// 6e-5 (a flip in 10^4).  It costs time: 996 us against 271 for 4096 tokens of
-// 32 heads of 128; 300 tokens of 8 heads of 64 take 34 us either way.
+// 6e-5 (a flip in 10^4).  It costs time: 996 us for 4096 tokens of 32 heads of
+// 128, where chunks with bf16 outputs take 271 us.
 bool use_chunks(const treewy_seqs& s) {
   const bool rounded_state = (s.flags & TREEWY_FLAG_STATE_BF16) != 0 && s.o_dtype == TREEWY_DTYPE_F32;
   auto rows_on16 = [](const void* p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; };
