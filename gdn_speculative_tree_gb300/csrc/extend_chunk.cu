@@ -50,7 +50,8 @@
 // in every figure (a full batch of 16 prompts x 32 heads of 4096 tokens: 125 KB
 // 1684 us, 92 KB 1294 us, 83 KB 1205 us, 76 KB 1090 us): loops stay rolled
 // where the registers allow it, and f32 work is packed in pairs.  4096 tokens
-// of 32 heads 271 us (15 us of HBM time), the full batch 1063 us (243 us).
+// of 32 heads 268 us (15 us of HBM time), the full batch 1050 us (243 us).
+#include "serving_device.cuh"
 #include "treewy_device.cuh"
 #include "treewy_internal.h"
 
@@ -1073,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ ChunkSmem cs;
   // by an offset, so that the compiler still knows the pointer to be a shared one
   unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
+  const int idx = blockIdx.x / a.H, h = blockIdx.x - idx * a.H, r = longest_first(a, idx);
   const int t = threadIdx.x, warp = t >> 5;
 
   const int lo = __ldg(a.seq_offset + r), hi = __ldg(a.seq_offset + r + 1);

@@ -40,6 +40,7 @@
 // per eight SMs by the staging, 0.15 us a token.
 #include <type_traits>
 
+#include "serving_device.cuh"
 #include "treewy_device.cuh"
 #include "treewy_internal.h"
 
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(THREADS + kPrep) scan_kernel(const treewy_seqs
   constexpr int V = 4, kRows = THREADS / 8 * RPT, kCols = 8 * CL, kAll = THREADS + kPrep;
   __shared__ __align__(16) Stage<CL, kRows> stages[2];
   after_previous();
-  const int r = blockIdx.x / a.H, h = blockIdx.x - r * a.H;
+  const int idx = blockIdx.x / a.H, h = blockIdx.x - idx * a.H, r = longest_first(a, idx);
   const int l = threadIdx.x & 7;
   const Seq s = load_seq(a, r);
   if (s.flags) {

@@ -326,6 +326,17 @@ def test_extend_f32_outputs_over_a_rounded_state(cuda_lib, n):
     assert np.linalg.norm(f64(c.o) - ref) <= 2.0 ** -14 * np.linalg.norm(ref)
 
 
+@pytest.mark.parametrize("R", [128, 129])
+@pytest.mark.parametrize("qkv", ["bf16", "f32"])
+def test_extend_order_of_sequences(cuda_lib, R, qkv):
+    """Equal, empty and refused lengths among as many sequences as are put in order, and one more."""
+    lens = [int(x) for x in np.random.RandomState(2).choice([0, 1, 7, 40, 40, 66], R)]
+    c = Case(lens, H=1, dk=32, dv=32, qkv=qkv, seed=21, max_len=60).run()
+    bad = [r for r, n in enumerate(lens) if n > 60]
+    c.check(skip=bad)
+    assert c.status.tolist() == [binding.STATUS_TOO_MANY_NODES if r in bad else 0 for r in range(R)]
+
+
 @pytest.mark.parametrize("lens", [[5, 0, 9, 16], [17, 3, 0, 38]])
 @pytest.mark.parametrize("H", [1, 24])
 @pytest.mark.parametrize("dk,dv", [(128, 128), (52, 71)])
