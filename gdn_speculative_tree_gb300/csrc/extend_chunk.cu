@@ -33,24 +33,37 @@
 //   warp 22      gates
 //   warp 23      issues the preparation's products
 //
-// Every product takes an f32 operand as two bf16 terms x = hi + lo (16
-// significant bits; lo times lo is left out), accumulates in f32, and keys,
-// queries and values are exact, so a result is within a few 2^-17 of the
-// recurrence's (measured: 4e-6 to 5e-6 of the state's norm, where sums in f32
-// token by token give 2e-7; one bf16 term would give 2e-3, and three half as
-// many products again).  Ratios g_n/g_i are running products of the decays
-// between i and n, never quotients, so they are right however small g has
-// become, a decay of zero included.
+// Products accumulate in f32; keys, queries and values are exact operands, and
+// an f32 operand is two bf16 terms x = hi + lo, lo times lo left out: S, W, kt,
+// M and MT, each 2^-17 off at most (a third term of all five has no room in
+// TMEM and shared memory).  T21 and what it is made from, T and T'' have three
+// terms and all products that count: where keys are alike, they are large and
+// cancel in what they are multiplied by.  Errors against 64 bits, in the norm
+// (512 tokens, heads of 128; sums in f32 token by token: 1e-7 to 1e-6):
+//
+//   cosine of the keys, b, decay     o (f32)  S       (two terms throughout)
+//   0.08, 0 to 1, 0.9 to 1           5e-6     4e-6    (5e-6, 5e-6)
+//   0.9, 1, 1                        7e-6     6e-6    (2e-5, 2e-5)
+//   0.99, 1, 1                       1e-5     6e-6    (3e-5, 3e-5)
+//   0.9, 1.9, 1                      1e-5     1e-5    (1e-4, 1e-4)
+//   0.99, 2, 1                       5e-5     5e-5    (1e-3, 1e-3)
+//
+// bf16 outputs leave M T's smallest products out: up to 2e-4 in the last two
+// lines, against the 2^-9 of their own rounding (290 against 306 us for 4096
+// tokens of 32 heads; the state does not depend on it).  Ratios g_n/g_i are
+// running products of the decays between i and n, never quotients, so they are
+// right however small g has become, a decay of zero included.
 //
 // Bound by what a CTA's warps issue between the products, not by the products
-// or by HBM: a chunk takes about 8000 cycles, of which [K;Q] K^T, T, kt and
+// or by HBM: a chunk takes about 8700 cycles, of which [K;Q] K^T, T, kt and
 // the tiles for the products are the longest way, and the SM's tensor pipe is
 // busy for a third and its issue slots for half of them.  The roles' code
-// together (76 KB) does not fit the instruction cache, so that its size shows
-// in every figure (a full batch of 16 prompts x 32 heads of 4096 tokens: 125 KB
-// 1684 us, 92 KB 1294 us, 83 KB 1205 us, 76 KB 1090 us): loops stay rolled
-// where the registers allow it, and f32 work is packed in pairs.  4096 tokens
-// of 32 heads 268 us (15 us of HBM time), the full batch 1050 us (243 us).
+// together (81 KB) does not fit the instruction cache, so that its size shows
+// in every figure (a full batch of 16 prompts x 32 heads of 4096 tokens, with
+// two terms throughout: 125 KB 1684 us, 92 KB 1294 us, 83 KB 1205 us, 76 KB
+// 1050 us): loops stay rolled where the registers allow it, and f32 work is
+// packed in pairs.  4096 tokens of 32 heads 289 us (15 us of HBM time; 268 us
+// with two terms), the full batch 1152 us (243 us; 1050 us).
 #include "serving_device.cuh"
 #include "treewy_device.cuh"
 #include "treewy_internal.h"
@@ -89,10 +102,13 @@ constexpr uint32_t kOffKt = 2 * kStageBytes;      // kt^T: 128 rows (dk) of 64 t
 constexpr uint32_t kOffMT = kOffKt + 4 * kBox;    // MT: 64 rows of 64 tokens, hi then lo
 constexpr uint32_t kOffM = kOffMT + 2 * kBox;     // M, hi then lo
 constexpr uint32_t kOffT = kOffM + 2 * kBox;      // T hi, lo, then T'' = diag(g_C/g_n) T diag(b) hi, lo
-constexpr uint32_t kOffA = kOffT + 4 * kBox;      // A21, hi then lo: rows 32-63; rows 0-31 take T22 A21
-constexpr uint32_t kOffX = kOffA + 2 * kBox;      // A's, then T's diagonal blocks of 32, f32
+constexpr uint32_t kOffT3 = kOffT + 4 * kBox;     // T's third term; A21's hi in its lower left quarter until T21 is there
+constexpr uint32_t kOffA = kOffT3 + kBox;         // A21's lo and third term (rows 32-63), T22 A21's lo (rows 0-31)
+constexpr uint32_t kOffX = kOffA + kBox;          // A's, then T's diagonal blocks of 32, f32; then the third term of T''
 constexpr int kPitchX = 36;
-constexpr uint32_t kSmemBytes = kOffX + kC * kPitchX * 4 + 1024;
+constexpr uint32_t kOffY = kOffX + kC * kPitchX * 4;  // T22 A21's hi and third term
+constexpr uint32_t kSmemBytes = kOffY + kBox / 2 + 1024;
+static_assert(kC * kPitchX * 4 >= kBox && kOffY % 1024 == 0, "a tile in the place of the diagonal blocks");
 
 struct __align__(16) Gates {
   float a[kC], b[kC], g[kC];          // decay, write strength and the product of the decays up to every token
@@ -199,6 +215,19 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+// x = hi + lo + third, to 2^-26 of x.
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t& hi, uint32_t& lo, uint32_t& third) {
+  const float2 minus = make_float2(-1.f, -1.f);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const float2 d = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), minus, make_float2(x0, x1));
+  const __nv_bfloat162 l = __floats2bfloat162_rn(d.x, d.y);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  const float2 e = fma2(make_float2(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u)), minus, d);
+  const __nv_bfloat162 t = __floats2bfloat162_rn(e.x, e.y);
+  third = *reinterpret_cast<const uint32_t*>(&t);
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Row `row`, 16-byte piece `j` of a K-major operand with 128-byte rows.
@@ -297,50 +326,81 @@ __device__ __forceinline__ void put_piece(unsigned char* hi, int row, int j, con
   out[kBox / 16] = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// A 16 x 8 result tile of warp-level products whose operands are hi and lo:
-// one accumulator per product of terms, so that they need not wait for one
-// another.
-struct Frag4 {
-  uint32_t hi[4], lo[4];
+// The same, and the third term.
+__device__ __forceinline__ uint4 put_piece3(unsigned char* hi, int row, int j, const float (&x)[8]) {
+  uint32_t h[4], l[4], t[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) split3(x[2 * e], x[2 * e + 1], h[e], l[e], t[e]);
+  uint4* out = operand_piece(hi, row, j);
+  out[0] = make_uint4(h[0], h[1], h[2], h[3]);
+  out[kBox / 16] = make_uint4(l[0], l[1], l[2], l[3]);
+  return make_uint4(t[0], t[1], t[2], t[3]);
+}
+
+// A 16 x 8 result tile of warp-level products whose operands are three terms
+// each, products below 2^-25 of the largest left out; three accumulators of
+// two products each, so that they need not all wait for one another.
+struct Left {
+  uint32_t hi[4], lo[4], third[4];
+};
+struct Right {
+  uint32_t hl[4], third[2];  // hi in hl[0..1], lo in hl[2..3]
 };
 struct Tile {
-  float hh[4], hl[4], lh[4];
+  float x[4], y[4], z[4];
   __device__ __forceinline__ Tile() {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) hh[e] = hl[e] = lh[e] = 0.f;
+    for (int e = 0; e < 4; ++e) x[e] = y[e] = z[e] = 0.f;
   }
-  __device__ __forceinline__ void add(const Frag4& a, uint32_t bh0, uint32_t bh1, uint32_t bl0, uint32_t bl1) {
-    mma16816_bf16_nv(lh, a.lo[0], a.lo[1], a.lo[2], a.lo[3], bh0, bh1);
-    mma16816_bf16_nv(hl, a.hi[0], a.hi[1], a.hi[2], a.hi[3], bl0, bl1);
-    mma16816_bf16_nv(hh, a.hi[0], a.hi[1], a.hi[2], a.hi[3], bh0, bh1);
+  __device__ __forceinline__ void add(const Left& a, const Right& b) {
+    mma16816_bf16_nv(z, a.third[0], a.third[1], a.third[2], a.third[3], b.hl[0], b.hl[1]);
+    mma16816_bf16_nv(y, a.lo[0], a.lo[1], a.lo[2], a.lo[3], b.hl[0], b.hl[1]);
+    mma16816_bf16_nv(x, a.hi[0], a.hi[1], a.hi[2], a.hi[3], b.hl[0], b.hl[1]);
+    mma16816_bf16_nv(z, a.hi[0], a.hi[1], a.hi[2], a.hi[3], b.third[0], b.third[1]);
+    mma16816_bf16_nv(y, a.hi[0], a.hi[1], a.hi[2], a.hi[3], b.hl[2], b.hl[3]);
+    mma16816_bf16_nv(x, a.lo[0], a.lo[1], a.lo[2], a.lo[3], b.hl[2], b.hl[3]);
   }
-  __device__ __forceinline__ float at(int e) const { return hh[e] + (hl[e] + lh[e]); }
+  __device__ __forceinline__ float at(int e) const { return x[e] + (y[e] + z[e]); }
 };
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], const void* p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(smem_addr(p)));
 }
-// The 16 x 16 block at (row, col) of an operand's hi and lo tiles as a left
-// operand; 16 rows (the contraction) and 8 columns of it as a right operand
-// (hi in [0..1], lo in [2..3]).
-__device__ __forceinline__ Frag4 left_frag(const unsigned char* hi, int row, int col, int lane) {
+__device__ __forceinline__ void ldsm_x2_trans(uint32_t (&r)[2], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];\n"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(smem_addr(p)));
+}
+// The 16 x 16 block at (row, col) of an operand's tiles as a left operand, the
+// third term's from column col3 of its tile.
+__device__ __forceinline__ Left left_frag(const unsigned char* hi, const unsigned char* lo, const unsigned char* third,
+                                          int row, int col, int col3, int lane) {
   const uint32_t at = sw128_off(row + (lane & 15), col + 8 * (lane >> 4));
-  Frag4 f;
+  Left f;
   ldsm_x4(f.hi, hi + at);
-  ldsm_x4(f.lo, hi + kBox + at);
+  ldsm_x4(f.lo, lo + at);
+  ldsm_x4(f.third, third + sw128_off(row + (lane & 15), col3 + 8 * (lane >> 4)));
   return f;
 }
-__device__ __forceinline__ void right_frag(uint32_t (&r)[4], const unsigned char* hi, int row, int col, int lane) {
-  ldsm_x4_trans(r, hi + (lane >> 4) * kBox + sw128_off(row + (lane & 15), col));
+// 16 rows (the contraction) and 8 columns as a right operand; lo is a tile
+// behind hi.
+__device__ __forceinline__ Right right_frag(const unsigned char* hi, const unsigned char* third, int row, int col,
+                                            int col3, int lane) {
+  Right f;
+  ldsm_x4_trans(f.hl, hi + (lane >> 4) * kBox + sw128_off(row + (lane & 15), col));
+  ldsm_x2_trans(f.third, third + sw128_off(row + (lane & 15), col3));
+  return f;
 }
 
 // The operands T and T'' = diag(g_C/g_n) T diag(b) from T's diagonal blocks of
 // 32 (in X) and A21: the lower left quarter T21 = -(T22 A21) T11 by warp-level
 // MMAs, a tile of 16 x 8 per warp.  (These take turns with the tcgen05
-// products; on FMAs the two products took 4500 cycles against 1500.)  The upper
-// right quarter stays zero in the tiles.
-__device__ __forceinline__ void solve64(const float* X, unsigned char* ab, unsigned char* tb, const Gates& g, int p) {
+// products; on FMAs the two products took 4500 cycles against 1500 with two
+// terms.)  The upper right quarter stays zero in the tiles.
+__device__ __forceinline__ void solve64(unsigned char* base, const Gates& g, int p) {
+  float* X = reinterpret_cast<float*>(base + kOffX);
+  unsigned char *tb = base + kOffT, *t3 = base + kOffT3, *ab = base + kOffA, *u3 = base + kOffX, *yb = base + kOffY;
   {
     // the diagonal blocks: eight values per thread
     const int r = p >> 2, c = 8 * (p & 3), col = (r & 32) + c;
@@ -356,10 +416,13 @@ __device__ __forceinline__ void solve64(const float* X, unsigned char* ab, unsig
       const float2 z = mul2(mul2(make_float2(dec, dec), make_float2(bs[e], bs[e + 1])), make_float2(x[e], x[e + 1]));
       y[e] = z.x, y[e + 1] = z.y;
     }
-    put_piece(tb, r, col / 8, x);
-    put_piece(tb + 2 * kBox, r, col / 8, y);
+    *operand_piece(t3, r, col / 8) = put_piece3(tb, r, col / 8, x);
+    const uint4 late = put_piece3(tb + 2 * kBox, r, col / 8, y);
+    prep_sync();
+    // X has been read: the third term of T'' takes its place
+    *operand_piece(u3, r, col / 8) = late;
+    if (r < 32) *operand_piece(u3, r, 4 + (p & 3)) = make_uint4(0u, 0u, 0u, 0u);
   }
-  prep_sync();
   // T22 and T11 are lower triangular: only blocks k <= m of the one, k >= t/2
   // of the other
   const int lane = p & 31, m = (p >> 5) & 1, t = p >> 6;
@@ -369,17 +432,17 @@ __device__ __forceinline__ void solve64(const float* X, unsigned char* ab, unsig
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (k > m) continue;
-      uint32_t r[4];
-      right_frag(r, ab, 32 + 16 * k, 8 * t, lane);
-      d.add(left_frag(tb, 32 + 16 * m, 32 + 16 * k, lane), r[0], r[1], r[2], r[3]);
+      d.add(left_frag(tb, tb + kBox, t3, 32 + 16 * m, 32 + 16 * k, 32 + 16 * k, lane),
+            right_frag(t3, ab, 32 + 16 * k, 8 * t, 32 + 8 * t, lane));
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      uint32_t h, l;
-      split2(d.at(2 * e), d.at(2 * e + 1), h, l);
-      unsigned char* out = ab + sw128_off(16 * m + 8 * e + at, c);
-      *reinterpret_cast<uint32_t*>(out) = h;
-      *reinterpret_cast<uint32_t*>(out + kBox) = l;
+      uint32_t h, l, h3;
+      split3(d.at(2 * e), d.at(2 * e + 1), h, l, h3);
+      const uint32_t to = sw128_off(16 * m + 8 * e + at, c);
+      *reinterpret_cast<uint32_t*>(yb + to) = h;
+      *reinterpret_cast<uint32_t*>(ab + to) = l;
+      *reinterpret_cast<uint32_t*>(yb + sw128_off(16 * m + 8 * e + at, 32 + c)) = h3;
     }
   }
   prep_sync();
@@ -390,21 +453,22 @@ __device__ __forceinline__ void solve64(const float* X, unsigned char* ab, unsig
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (k < (t >> 1)) continue;
-      uint32_t r[4];
-      right_frag(r, tb, 16 * k, 8 * t, lane);
-      d.add(left_frag(ab, 16 * m, 16 * k, lane), r[0], r[1], r[2], r[3]);
+      d.add(left_frag(yb, ab, yb, 16 * m, 16 * k, 32 + 16 * k, lane), right_frag(tb, t3, 16 * k, 8 * t, 8 * t, lane));
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float x = d.at(2 * e), y = d.at(2 * e + 1);
-      uint32_t h, l, h2, l2;
-      split2(-x, -y, h, l);
-      split2(dec[e] * b.x * x, dec[e] * b.y * y, h2, l2);
-      unsigned char* out = tb + sw128_off(32 + 16 * m + 8 * e + at, c);
+      uint32_t h, l, h3, h2, l2, h23;
+      split3(-x, -y, h, l, h3);
+      split3(dec[e] * b.x * x, dec[e] * b.y * y, h2, l2, h23);
+      const uint32_t to = sw128_off(32 + 16 * m + 8 * e + at, c);
+      unsigned char* out = tb + to;
       *reinterpret_cast<uint32_t*>(out) = h;
       *reinterpret_cast<uint32_t*>(out + kBox) = l;
       *reinterpret_cast<uint32_t*>(out + 2 * kBox) = h2;
       *reinterpret_cast<uint32_t*>(out + 3 * kBox) = l2;
+      *reinterpret_cast<uint32_t*>(t3 + to) = h3;
+      *reinterpret_cast<uint32_t*>(u3 + to) = h23;
     }
   }
 }
@@ -750,6 +814,7 @@ __device__ __forceinline__ void issue_gram(ChunkSmem& cs, unsigned char* base, i
 
 // One warp: the preparation's other products, once T and the next chunk's K
 // and Q are there.
+template <bool OF32>
 __device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, int nchunk) {
   constexpr uint32_t idk = idesc_bf16_f32(128, kC) | kAmajorMN | kBmajorMN;
   constexpr uint32_t idm = idesc_bf16_f32(128, kC) | kBmajorMN;
@@ -766,6 +831,7 @@ __device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, in
       for (int k = 0; k < 4; ++k) {
         mma_bf16(cs.tmem + kColK, k0 + k * 128, t2 + k * 128, idk, k > 0);
         mma_bf16(cs.tmem + kColK, k0 + k * 128, t2 + (kBox >> 4) + k * 128, idk, 1u);
+        mma_bf16(cs.tmem + kColK, k0 + k * 128, t1 + ((kOffX - kOffT) >> 4) + k * 128, idk, 1u);
       }
       mma_commit(&cs.kt_done);
       mma_commit(&cs.stage_free[c & 1]);
@@ -785,6 +851,10 @@ __device__ __forceinline__ void run_issue(ChunkSmem& cs, unsigned char* base, in
         mma_bf16(cs.tmem + kColO, mh, th, idm, k > 0);
         mma_bf16(cs.tmem + kColO, mh, tl, idm, 1u);
         mma_bf16(cs.tmem + kColO, ml, th, idm, 1u);
+        if constexpr (OF32) {
+          mma_bf16(cs.tmem + kColO, ml, tl, idm, 1u);
+          mma_bf16(cs.tmem + kColO, mh, th + ((kOffT3 - kOffT) >> 4), idm, 1u);
+        }
       }
       mma_commit(&cs.mt_done);
     }
@@ -830,6 +900,18 @@ __device__ __forceinline__ void form_row(uint32_t tm_row, const Gates& g, bool i
         uint4* out = operand_piece(tile, n, 4 * cb + 2 * b + j);
         out[0] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
         out[kBox / 16] = make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+      }
+      if (!isM) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t t[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t hh, ll;
+            split3(y[8 * j + 2 * k], y[8 * j + 2 * k + 1], hh, ll, t[k]);
+          }
+          *operand_piece(tile + kBox, n, 4 + 2 * b + j) = make_uint4(t[0], t[1], t[2], t[3]);
+        }
       }
     } else {
       float4* r = reinterpret_cast<float4*>(out_row + 16 * b);
@@ -877,10 +959,9 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
   const uint32_t tm = cs.tmem + (static_cast<uint32_t>(32 * quad) << 16);
   const bool solver = w == 0 || w == 5;
   float* X = reinterpret_cast<float*>(base + kOffX);
-  unsigned char* ab = base + kOffA;
-  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM, *tb = base + kOffT;
-  // the upper right quarters of MT, M, T and T'' stay zero
-  for (int i = 16 * p; i < static_cast<int>(8 * kBox); i += 16 * kPrepThreads)
+  unsigned char *ktb = base + kOffKt, *mtb = base + kOffMT, *mb = base + kOffM;
+  // the upper right quarters of MT, M, T, T'' and T's third term stay zero
+  for (int i = 16 * p; i < static_cast<int>(9 * kBox); i += 16 * kPrepThreads)
     *reinterpret_cast<uint4*>(mtb + i) = make_uint4(0u, 0u, 0u, 0u);
   // K and Q of chunk c are there; rows of K past the sequence's end (the next
   // one's) become zero
@@ -930,7 +1011,7 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
     tc_fence_after_sync();
     // rows 0-31 of M end in column 31: 16 columns each for warps 2 and 6
     if (w != 4)
-      form_row(tm, g, quad >= 2, n, w == 5 || w == 7, w == 2, w == 6 ? 1 : 2, quad >= 2 ? mb : ab,
+      form_row(tm, g, quad >= 2, n, w == 5 || w == 7, w == 2, w == 6 ? 1 : 2, quad >= 2 ? mb : base + kOffT3,
                solver ? X + n * kPitchX : nullptr);
     tc_fence_before_sync();
     if (solver) {
@@ -939,10 +1020,10 @@ __device__ __forceinline__ void run_prep(ChunkSmem& cs, unsigned char* base, int
     }
     if (c + 1 < nchunk && !stage_in(c + 1)) ok = false;
     if (prep_failed(ok)) break;
-    solve64(X, ab, tb, g, p);
+    solve64(base, g, p);
     fence_proxy_async_smem();
     warp_arrive(&cs.t_ready);
-    prep_sync();  // X may be written again
+    prep_sync();  // X is written again once the next [K;Q] K^T is there, and so kt of this chunk
   }
 }
 
@@ -1163,7 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kGateWarp) {
       run_gates(a, cs, q, h, nchunk);
     } else {
-      run_issue(cs, base, nchunk);
+      run_issue<OF32>(cs, base, nchunk);
       drain(&cs.drain[2]);
     }
   }

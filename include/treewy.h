@@ -337,8 +337,13 @@ typedef struct treewy_seqs {
  * are.
  *
  * Long sequences of bf16 q, k and v with 16-byte rows run in chunks of 64
- * tokens on the tensor cores, f32 operands as two bf16 terms each (a result
- * is a few 2^-17 off); other calls run token by token in f32, and so do f32
+ * tokens on the tensor cores, f32 operands as bf16 terms.  For unit keys, the
+ * state and f32 outputs are then within 2^-14 of their largest value where
+ * 0 <= beta <= 1, and within 2^-11 where beta <= 2 and keys are much alike
+ * (512 tokens at a cosine of 0.99 without decay; errors of independent keys
+ * are 5e-6 in the norm); bf16 outputs are within four times that and their own
+ * rounding.  Other calls run token by token in f32 (1e-7 to 1e-6), as all do
+ * with TREEWY_FLAG_FORCE_GENERIC, and so do f32
  * outputs over a bf16 pool, where such differences would turn roundings of
  * the next call's state.  In a chunk a NaN or an infinity among a token's
  * inputs can reach the outputs of that sequence and head from up to 63 tokens
