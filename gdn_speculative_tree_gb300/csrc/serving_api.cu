@@ -63,14 +63,23 @@ treewy_status validate_seqs(const treewy_seqs* s) {
 }
 
 // Batches whose longest sequence has at least this many tokens run in chunks.
-// A chunk takes 13 (bf16 pool) to 17 us whatever its length; token by token it
+// A chunk takes 14 (bf16 pool) to 17 us whatever its length; token by token it
 // is 0.2 to 0.3 us a token (128 x 128 heads) while a head's rows have the SMs
-// to themselves, more when heads share them.  Chunks against tokens: 32 tokens
-// of 40 heads 13.3 and 13.2 us (16.7 and 13.4 us on an f32 pool), 40 tokens
-// 13.4 and 15.8 (16.7 and 15.9); 12 tokens of 80 heads 13.6 and 11.8 (16.8 and
-// 13.0), 16 tokens 13.9 and 14.8 (16.7 and 16.5); 10 tokens of 2048 heads 148
-// and 156 (186 and 132), 16 tokens 150 and 235 (187 and 211).
-int chunked_len(const treewy_seqs& s) { return int64_t(s.R) * s.H > 64 ? 13 : 33; }
+// to themselves, more when heads share them.  Chunks against tokens, us, on a
+// bf16 pool and on an f32 one:
+//   40 heads,   33 tokens   14.4 / 14.5   16.5 / 14.7
+//               40          14.4 / 15.6   16.5 / 15.8
+//               48          14.4 / 17.8   16.5 / 18.1
+//   80 heads,   12          14.4 / 11.5   16.5 / 12.8
+//               16          14.4 / 14.5   16.5 / 16.3
+//               20          14.4 / 18.6   16.5 / 19.1
+//   2048 heads, 10           164 / 154     208 / 137
+//               13           166 / 195     209 / 171
+//               16           166 / 234     209 / 215
+int chunked_len(const treewy_seqs& s) {
+  const bool sb = (s.flags & TREEWY_FLAG_STATE_BF16) != 0;
+  return int64_t(s.R) * s.H > 64 ? (sb ? 13 : 16) : (sb ? 33 : 43);
+}
 
 // Whether the chunked kernel takes the batch (s: strides resolved).  f32
 // outputs over a bf16 pool go token by token: a product of split operands is
