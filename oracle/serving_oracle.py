@@ -27,23 +27,18 @@ def extend(S, q, k, v, alpha, beta):
 def norm_rotate(x, norm, eps, weight=None, scale=1.0, rope=None, position=None, interleaved=False, repeat=1):
     """Rows x [T][heads][d] normed, weighted, scaled, rotated and repeated."""
     x = np.asarray(x, dtype=np.float64)
-    T, heads, d = x.shape
-    y = np.zeros_like(x)
-    for t in range(T):
-        for h in range(heads):
-            total = np.dot(x[t, h], x[t, h])
-            row = scale * x[t, h] / np.sqrt((total if norm == "l2" else total / d) + eps)
-            if weight is not None:
-                row = row * np.asarray(weight, dtype=np.float64)
-            if rope is not None:
-                r = rope.shape[1]
-                out = row.copy()
-                for i in range(r // 2):
-                    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + r // 2)
-                    c, s = float(rope[position[t], i]), float(rope[position[t], r // 2 + i])
-                    out[a], out[b] = row[a] * c - row[b] * s, row[b] * c + row[a] * s
-                row = out
-            y[t, h] = row
+    total = np.square(x).sum(axis=-1, keepdims=True)
+    y = scale * x / np.sqrt((total if norm == "l2" else total / x.shape[2]) + eps)
+    if weight is not None:
+        y = y * np.asarray(weight, dtype=np.float64)
+    if rope is not None:
+        r = rope.shape[1]
+        i = np.arange(r // 2)
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + r // 2)
+        table = np.asarray(rope, dtype=np.float64)[position][:, None]
+        c, s = table[..., :r // 2], table[..., r // 2:]
+        u, w = y[..., a], y[..., b]
+        y[..., a], y[..., b] = u * c - w * s, w * c + u * s
     return np.repeat(y, repeat, axis=1)
 
 
