@@ -440,6 +440,8 @@ def make_slots(*, state, src, dst, status, layers: Optional[int] = None) -> Tree
     per = 1
     for n in shape[1:]:
         per *= int(n)
+    if layers is not None and layers > 1 and state.stride(0) < int(shape[0]) * per:
+        raise ValueError("state: layers overlap")  # a stride of 0 would pass for dense layers
     _one_device((state, src, dst, status))
     a = TreewySlots()
     a.n, a.layers = int(src.numel()), 1 if layers is None else int(layers)
