@@ -80,6 +80,7 @@ class TreewyBatch(ctypes.Structure):
 
 
 class TreewySeqs(ctypes.Structure):
+    _device = None  # of the tensors it was made from
     _fields_ = [(f, ctypes.c_int32) for f in
                 ("R", "H", "Hk", "dk", "dv", "max_len", "qkv_dtype", "o_dtype")] + [
         (f, ctypes.c_int64) for f in ("T", "num_slots", "q_stride", "k_stride", "v_stride")] + [
@@ -89,6 +90,7 @@ class TreewySeqs(ctypes.Structure):
 
 
 class TreewyQk(ctypes.Structure):
+    _device = None  # of the tensors it was made from
     _fields_ = [("T", ctypes.c_int64)] + [(f, ctypes.c_int32) for f in
                 ("Hq", "Hk", "d", "dtype", "norm", "rope_dims", "interleaved", "q_repeat", "k_repeat")] + [
         (f, ctypes.c_float) for f in ("eps", "q_scale", "k_scale")] + [
@@ -98,6 +100,7 @@ class TreewyQk(ctypes.Structure):
 
 
 class TreewySlots(ctypes.Structure):
+    _device = None  # of the tensors it was made from
     _fields_ = [("n", ctypes.c_int32), ("layers", ctypes.c_int32)] + [
         (f, ctypes.c_int64) for f in ("num_slots", "slot_bytes", "layer_stride")] + [
         (f, ctypes.c_void_p) for f in ("state", "src", "dst", "status")]
@@ -166,6 +169,29 @@ def _current_stream_handle() -> int:
     return _current_raw_stream()
 
 
+_get_device = None
+
+
+def _current_device() -> int:
+    global _get_device
+    if _get_device is None:
+        import torch
+        # without the checks of torch.cuda.current_device, where this PyTorch has it
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _get_device()
+
+
+def _reachable(args) -> None:
+    """Refuses arguments described from tensors that a kernel on the current device cannot reach."""
+    device = args._device
+    if device is None:
+        return
+    if device < 0:
+        raise ValueError("the tensors are on the CPU")
+    if device != _current_device():
+        raise ValueError(f"the tensors are on device {device}, the current device is {_current_device()}")
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
         return _current_stream_handle()
@@ -227,16 +253,19 @@ def treewy_storeall_commit(batch: TreewyBatch, snapshots, accepted, stream=None)
 
 def treewy_extend(seqs: TreewySeqs, stream=None) -> None:
     """The gated delta rule over every sequence's new tokens, from and into its state slot."""
+    _reachable(seqs)
     _check(load().treewy_extend(ctypes.byref(seqs), _stream_handle(stream)))
 
 
 def treewy_qk_norm(qk: TreewyQk, stream=None) -> None:
     """Norm, weight, scale and rotation of every query and key head."""
+    _reachable(qk)
     _check(load().treewy_qk_norm(ctypes.byref(qk), _stream_handle(stream)))
 
 
 def treewy_copy_slots(slots: TreewySlots, stream=None) -> None:
     """Copy, fork, compact and clear slots of the state pools of all layers."""
+    _reachable(slots)
     _check(load().treewy_copy_slots(ctypes.byref(slots), _stream_handle(stream)))
 
 
@@ -310,10 +339,12 @@ def _need(x, name: str, dtype, shape=None) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _one_device(tensors) -> None:
+def _one_device(tensors) -> int:
+    """The device that all of the tensors are on (-1: the CPU)."""
     found = {x.get_device() for x in tensors if x is not None}
     if len(found) > 1:
         raise ValueError(f"tensors on several devices: {sorted(found)} (-1: the CPU)")
+    return found.pop()
 
 
 def _token_stride(x, name: str) -> int:
@@ -358,12 +389,12 @@ def make_seqs(*, seq_offset, q, k, v, alpha, beta, state, state_slot, o, status,
     _need(o, "o", o.dtype, (T, H, dv))
     _need(state, "state", state.dtype, (num_slots, H, dv, dk))
     keep = (seq_offset, q, k, v, alpha, beta, state, state_slot, fresh, o, status)
-    _one_device(keep)
+    device = _one_device(keep)
     if _dtype_code(state, "state") == DTYPE_BF16:
         flags |= FLAG_STATE_BF16
     s = TreewySeqs(R, H, Hk, dk, dv, int(max_len), _dtype_code(q, "q/k/v"), _dtype_code(o, "o"), T, num_slots,
                    *strides, *map(_ptr, keep), int(flags), 0)
-    s._keep = keep
+    s._keep, s._device = keep, device
     return s
 
 
@@ -414,7 +445,7 @@ def make_qk(*, q=None, k=None, q_out=None, k_out=None, norm: str = "l2", eps: fl
     if status is not None:
         _need(status, "status", torch.int32)
     keep = (q, k, q_out, k_out, q_weight, k_weight, rope, position, status)
-    _one_device(keep)
+    a._device = _one_device(keep)
     a.eps, a.q_scale, a.k_scale, a.interleaved = float(eps), float(q_scale), float(k_scale), int(interleaved)
     a.rope, a.position, a.status = _ptr(rope), _ptr(position), _ptr(status)
     a._keep = keep
@@ -442,13 +473,13 @@ def make_slots(*, state, src, dst, status, layers: Optional[int] = None) -> Tree
         per *= int(n)
     if layers is not None and layers > 1 and state.stride(0) < int(shape[0]) * per:
         raise ValueError("state: layers overlap")  # a stride of 0 would pass for dense layers
-    _one_device((state, src, dst, status))
+    device = _one_device((state, src, dst, status))
     a = TreewySlots()
     a.n, a.layers = int(src.numel()), 1 if layers is None else int(layers)
     a.num_slots, a.slot_bytes = int(shape[0]), per * state.element_size()
     a.layer_stride = int(state.stride(0)) * state.element_size() if layers is not None and layers > 1 else 0
     a.state, a.src, a.dst, a.status = _ptr(state), _ptr(src), _ptr(dst), _ptr(status)
-    a._keep = (state, src, dst, status)
+    a._keep, a._device = (state, src, dst, status), device
     return a
 
 
