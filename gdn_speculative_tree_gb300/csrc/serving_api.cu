@@ -82,12 +82,16 @@ int chunked_len(const treewy_seqs& s) {
 }
 
 // Whether the chunked kernel takes the batch (s: strides resolved).  f32
-// outputs over a bf16 pool go token by token: a product of split operands is
-// a few 2^-18 off, so that one value in 500 of the next call's state rounds to
-// the other side, 2^-8 away, and its f32 outputs (70 tokens, decays above
-// 0.97) differ by 7e-5 in the norm, where f32 sums throughout keep them within
-// 6e-5 (a flip in 10^4).  It costs time: 996 us for 4096 tokens of 32 heads of
-// 128, where chunks with bf16 outputs take 271 us.
+// outputs over a bf16 pool go token by token: chunks are 4e-6 to 5e-6 off, so
+// that one value in 500 of the state that a call stores rounds to the other
+// side, 2^-8 away (one in 10^4 with f32 sums), and the next call's f32 outputs
+// show it: the second of two calls of 70 tokens (decays above 0.97) is 6.3e-5
+// off in the norm, 2.3e-5 token by token; of 1000 tokens 2.1e-5 and 2.4e-6.
+// bf16 outputs do not show it beside their own 2^-9.  So the sequences that
+// gain are those whose calls all have f32 outputs: after a call with bf16
+// outputs that ran in chunks its roundings are in the state, unless that call
+// set TREEWY_FLAG_FORCE_GENERIC.  It costs time: 1010 us for 4096 tokens of 32
+// heads, where chunks with bf16 outputs take 290 us.
 bool use_chunks(const treewy_seqs& s) {
   const bool rounded_state = (s.flags & TREEWY_FLAG_STATE_BF16) != 0 && s.o_dtype == TREEWY_DTYPE_F32;
   auto rows_on16 = [](const void* p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; };

@@ -343,12 +343,16 @@ typedef struct treewy_seqs {
  * (512 tokens at a cosine of 0.99 without decay; errors of independent keys
  * are 5e-6 in the norm); bf16 outputs are within four times that and their own
  * rounding.  Other calls run token by token in f32 (1e-7 to 1e-6), as all do
- * with TREEWY_FLAG_FORCE_GENERIC, and so do f32
- * outputs over a bf16 pool, where such differences would turn roundings of
- * the next call's state.  In a chunk a NaN or an infinity among a token's
- * inputs can reach the outputs of that sequence and head from up to 63 tokens
- * before it on.  TREEWY_STATUS_TIMEOUT: a wait of the kernel gave up; the
- * sequence's outputs are partly written and its state may be too.
+ * with TREEWY_FLAG_FORCE_GENERIC.  So do calls with f32 outputs over a bf16
+ * pool: a difference that turns a rounding of the stored state shows in f32
+ * outputs of later calls.  It does so whichever call stored the state, so a
+ * sequence is as near as f32 sums only where all calls over it have f32
+ * outputs or that flag.
+ *
+ * In a chunk a NaN or an infinity among a token's inputs can reach the outputs
+ * of that sequence and head from up to 63 tokens before it on.
+ * TREEWY_STATUS_TIMEOUT: a wait of the kernel gave up; the sequence's outputs
+ * are partly written and its state may be too.
  */
 treewy_status treewy_extend(const treewy_seqs* seqs, cudaStream_t stream);
 
