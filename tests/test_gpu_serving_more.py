@@ -32,6 +32,20 @@ def test_extend_f32_rows_over_a_bf16_pool_strides(cuda_lib, n, pad, shift):
     Case([n, n], H=2, Hk=1, qkv="f32", pool="bf16", pad=pad, shift=shift, seed=pad + shift).run().check()
 
 
+# -------------------------------------------------- a step of prompts and single tokens as two calls
+
+@pytest.mark.parametrize("pool", ["f32", "bf16"])
+def test_extend_prompts_and_single_tokens_in_two_calls(cuda_lib, pool):
+    c = Case([200, 90, 1, 1, 0, 1], H=4, Hk=2, out="bf16", pool=pool, fresh=(1, 3), seed=35)
+    for lo, hi, most in ((0, 2, 200), (2, 6, 1)):
+        binding.treewy_extend(binding.make_seqs(
+            seq_offset=c.off[lo:hi + 1], q=c.q, k=c.k, v=c.v, alpha=c.alpha, beta=c.beta, state=c.pool,
+            state_slot=c.slot[lo:hi], fresh=c.fresh[lo:hi], o=c.o, status=c.status[lo:hi], max_len=most))
+    torch.cuda.synchronize()
+    c.check()
+    assert c.status.tolist() == [0] * 6
+
+
 # -------------------------------------------------- qk_norm: several parts of tokens per warp
 
 def norm_case(dtype, d, Hq, Hk, T, rope, interleaved, norm="rms", repeat=1, pad=0):
