@@ -7,6 +7,7 @@ particular libcudart on the loading machine.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -51,6 +52,27 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _without_ptxas(log: str) -> str:
+    """Warnings without what ptxas says of every kernel."""
+    return "".join(x for x in log.splitlines(True) if not re.match(r"ptxas info|\s+\d+ bytes stack frame", x))
+
+
+def check_launch_registers(src: str, log: str) -> None:
+    """``log``: what ptxas -v says of ``src``.  A kernel whose warps hand registers to one another (setmaxnreg) states
+    the registers per thread of its launch as kLaunchRegs; one that is compiled to another number would be refused at
+    its first launch, since an increase waits for registers that are not there."""
+    with open(src) as f:
+        stated = re.search(r"\bkLaunchRegs = (\d+)", f.read())
+    if stated is None:
+        return
+    kernel = os.path.basename(src)[:-3] + "_kernel"
+    used = {int(n) for name, n in re.findall(r"Compiling entry function '([^']*)'.*?Used (\d+) registers", log, re.S)
+            if kernel in name}
+    if used != {int(stated.group(1))}:
+        raise RuntimeError(f"{kernel} is compiled to {sorted(used)} registers per thread, not {stated.group(1)}: "
+                           "its split of registers between warps does not hold with this compiler")
+
+
 def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile (if needed) and return the path of libtreewy.so."""
     nvcc = nvcc_path()
@@ -63,13 +85,13 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         src, obj = pair
         if not force and not _stale(obj, [src] + hdrs + [__file__]):
             return ""
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
-        if ptxas_verbose:
-            cmd += ["-Xptxas", "-v"]
+        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-Xptxas", "-v", "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj + ".tmp"]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{res.stdout}\n{res.stderr}")
-        return res.stderr
+        check_launch_registers(src, res.stderr)
+        os.replace(obj + ".tmp", obj)
+        return res.stderr if ptxas_verbose else _without_ptxas(res.stderr)
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         logs = list(ex.map(compile_one, zip(srcs, objs)))
