@@ -446,8 +446,8 @@ typedef struct treewy_slots {
  * treewy_copy_slots -- copies block src[i] to block dst[i] in every layer's
  * pool, byte for byte; src[i] = -1 fills block dst[i] with zeros (a request's
  * states forked to samples of it, live slots moved into holes, slots
- * cleared).  A source may serve several moves; moves with src[i] = dst[i]
- * leave the block as it is.  Moves must not meet: where dst[i] is another
+ * cleared).  A source may serve several moves; a move with src[i] = dst[i]
+ * does nothing and meets no other one.  Moves must not meet: where dst[i] is another
  * move's destination too, or src[i] another move's destination,
  * TREEWY_STATUS_SLOT_CLASH is set in status[i] and move i is not made.  An
  * index outside the pool sets TREEWY_STATUS_BAD_SLOT and the move is not

@@ -55,6 +55,6 @@ def move_slots(pool, src, dst):
                     status[i] |= 128
         if not (-1 <= src[i] < slots and 0 <= dst[i] < slots):
             status[i] |= 8
-        if status[i] == 0:
+        if status[i] == 0 and src[i] != dst[i]:
             out[:, dst[i]] = pool[:, src[i]] if src[i] >= 0 else 0
     return out, status
