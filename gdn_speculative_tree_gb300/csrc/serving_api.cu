@@ -59,6 +59,8 @@ treewy_status validate_seqs(const treewy_seqs* s) {
   if (!aligned(s->q, e) || !aligned(s->k, e) || !aligned(s->v, e) || !aligned(s->o, eo) ||
       !aligned(s->alpha, 4) || !aligned(s->beta, 4))
     return fail(TREEWY_ERR_INVALID_ARG, "q, k, v, o, alpha and beta must be aligned to their elements");
+  if (!aligned(s->seq_offset, 4) || !aligned(s->state_slot, 4) || !aligned(s->status, 4))
+    return fail(TREEWY_ERR_INVALID_ARG, "seq_offset, state_slot and status must be aligned to their elements");
   return TREEWY_OK;
 }
 
@@ -161,8 +163,9 @@ treewy_status validate_qk(const treewy_qk* a) {
   if (a->Hq > 0 && (!a->q || !a->q_out)) return fail(TREEWY_ERR_INVALID_ARG, "q and q_out must be non-NULL");
   if (a->Hk > 0 && (!a->k || !a->k_out)) return fail(TREEWY_ERR_INVALID_ARG, "k and k_out must be non-NULL");
   if (!aligned(a->q, e) || !aligned(a->k, e) || !aligned(a->q_out, e) || !aligned(a->k_out, e) ||
-      !aligned(a->q_weight, 4) || !aligned(a->k_weight, 4) || !aligned(a->rope, 4))
-    return fail(TREEWY_ERR_INVALID_ARG, "rows, weights and table must be aligned to their elements");
+      !aligned(a->q_weight, 4) || !aligned(a->k_weight, 4) || !aligned(a->rope, 4) || !aligned(a->position, 4) ||
+      !aligned(a->status, 4))
+    return fail(TREEWY_ERR_INVALID_ARG, "rows, weights, table, position and status must be aligned to their elements");
   if (a->Hq > 0 && a->q_out == a->q &&
       (a->q_repeat != 1 || stride_or(a->q_stride, int64_t(a->Hq) * a->d) != int64_t(a->Hq) * a->d))
     return fail(TREEWY_ERR_INVALID_ARG, "q_out = q needs q_repeat = 1 and dense rows");
@@ -194,6 +197,8 @@ treewy_status validate_slots(const treewy_slots* a) {
   if (a->n == 0 || a->layers == 0) return TREEWY_OK;
   if (!a->state || !a->src || !a->dst || !a->status)
     return fail(TREEWY_ERR_INVALID_ARG, "state, src, dst and status must be non-NULL");
+  if (!aligned(a->src, 4) || !aligned(a->dst, 4) || !aligned(a->status, 4))
+    return fail(TREEWY_ERR_INVALID_ARG, "src, dst and status must be aligned to their elements");
   return TREEWY_OK;
 }
 

@@ -288,7 +288,7 @@ treewy_status treewy_selftest_wait_timeout(int32_t* status, uint32_t limit_us,
  *               zero state, which is then not read
  *   o           f32 or bf16 (o_dtype) [T][H][dv]
  *   status      int32 [R], bits OR-ed in
- * q, k, v and o are aligned to their element size only; rows and bases that
+ * Everything but the state is aligned to its element size only; rows and bases that
  * are multiples of 16 bytes take the wide loads.  o and status overlap nothing
  * else.
  */
