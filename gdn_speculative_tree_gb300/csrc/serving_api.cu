@@ -242,6 +242,9 @@ treewy_status treewy_copy_slots(const treewy_slots* slots, cudaStream_t stream) 
   treewy_status st = validate_slots(slots);
   if (st != TREEWY_OK || slots->n == 0 || slots->layers == 0) return st;
   const cudaError_t err = treewy::launch_copy_slots(*slots, stream);
+  if (err == cudaErrorNotSupported)
+    return fail(TREEWY_ERR_UNSUPPORTED, "%d moves in %d layers of %lld bytes each are too many for one call", slots->n,
+                slots->layers, (long long)slots->slot_bytes);
   return err == cudaSuccess ? TREEWY_OK : cuda_fail(err, "treewy_copy_slots launch");
 }
 

@@ -62,9 +62,9 @@ template <typename W>
 cudaError_t launch(const treewy_slots& a, int64_t layer_stride, cudaStream_t stream) {
   const int64_t words = a.slot_bytes / static_cast<int64_t>(sizeof(W));
   const int64_t pieces = (words + kThreads * kWords - 1) / (kThreads * kWords);
-  const int64_t grid = pieces * a.layers * a.n;
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_after(copy_slots_kernel<W>, dim3(static_cast<unsigned>(grid)), kThreads, stream, a, words,
+  const int64_t copies = static_cast<int64_t>(a.layers) * a.n;
+  if (pieces > 0x7fffffff / copies) return cudaErrorNotSupported;
+  return launch_after(copy_slots_kernel<W>, dim3(static_cast<unsigned>(pieces * copies)), kThreads, stream, a, words,
                       static_cast<int>(pieces), layer_stride);
 }
 

@@ -145,6 +145,7 @@ struct ExtendMaps {
 cudaError_t launch_extend_chunk(const treewy_seqs& s, const ExtendMaps& maps, cudaStream_t stream);
 
 cudaError_t launch_qk_norm(const treewy_qk& a, cudaStream_t stream);
+// cudaErrorNotSupported: more pieces of moves than a launch holds.
 cudaError_t launch_copy_slots(const treewy_slots& a, cudaStream_t stream);
 
 // One thread waiting for a barrier phase nothing completes (bounded).

@@ -26,3 +26,13 @@ def test_whole_numbers_are_aligned_to_their_elements(lib, make, call, fields):  
             setattr(a, field, FAKE + off)
             assert getattr(lib, call)(ctypes.byref(a), None) == INVALID, (field, off)
             assert "aligned" in binding.treewy_last_error()
+
+
+@pytest.mark.parametrize("n,layers,slot_bytes", [((1 << 31) - 1, (1 << 31) - 1, 1 << 20), (1 << 16, 1 << 16, 1 << 31),
+                                                 (1 << 15, 1 << 16, 1 << 10)])
+def test_more_moves_than_a_launch_holds(lib, n, layers, slot_bytes):  # noqa: F811
+    """Their number passes 2^31, and 2^63 in the first case: none of them may wrap to a smaller one."""
+    a = slots()
+    a.n, a.layers, a.num_slots, a.slot_bytes = n, layers, 2, slot_bytes
+    assert lib.treewy_copy_slots(ctypes.byref(a), None) == binding.TREEWY_ERR_UNSUPPORTED
+    assert "moves" in binding.treewy_last_error()
