@@ -20,7 +20,7 @@ own = False
 _TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 _E4M3 = torch.float8_e4m3fn
 _TOP = 448.0      # the largest e4m3 value
-_LEAST = -100     # the least exponent of a page's scale
+_LEAST = -40      # the least exponent of a page's scale
 
 
 # ------------------------------------------------------------------ cases
