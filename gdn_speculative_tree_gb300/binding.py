@@ -6,12 +6,14 @@ module raises instead of computing anything.
 
 Entry points keep the C names: ``treewy_verify``, ``treewy_commit``,
 ``treewy_storeall_verify``, ``treewy_storeall_commit``, ``treewy_extend``,
-``treewy_qk_norm``, ``treewy_copy_slots``, ``treewy_last_error`` and
+``treewy_qk_norm``, ``treewy_copy_slots``, ``treewy_attend``,
+``treewy_append``, ``treewy_add_norm``, ``treewy_last_error`` and
 ``treewy_version``.  ``TreewyBatch`` mirrors ``struct treewy_batch``;
 ``make_batch`` fills one from torch tensors (device memory and streams are
 PyTorch's; the library only receives raw pointers), as ``make_seqs``,
 ``make_qk`` and ``make_slots`` fill the arguments of the three calls around
-verification.
+verification, and ``make_cache``, ``make_attn``, ``make_append`` and
+``make_norm`` those of the softmax layers' calls.
 """
 from __future__ import annotations
 
@@ -35,6 +37,7 @@ STATUS_TIMEOUT = 16
 STATUS_COMMIT_REFUSED = 32
 STATUS_BAD_POSITION = 64
 STATUS_SLOT_CLASH = 128
+STATUS_BAD_PAGE = 256
 
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
@@ -106,10 +109,43 @@ class TreewySlots(ctypes.Structure):
         (f, ctypes.c_void_p) for f in ("state", "src", "dst", "status")]
 
 
+class TreewyCache(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("Hkv", "d", "page_len", "max_pages")] + [
+        ("num_pages", ctypes.c_int64)] + [
+        (f, ctypes.c_void_p) for f in ("k", "v", "k_scale", "v_scale", "page_table", "length")]
+
+
+class TreewyAttn(ctypes.Structure):
+    _device = None  # of the tensors it was made from
+    _fields_ = [(f, ctypes.c_int32) for f in ("R", "Hq", "max_nodes", "max_context", "qkv_dtype", "o_dtype")] + [
+        (f, ctypes.c_int64) for f in ("T", "q_stride", "k_stride", "v_stride")] + [
+        (f, ctypes.c_void_p) for f in ("node_offset", "parent", "q", "k", "v", "o", "status", "workspace")] + [
+        ("workspace_bytes", ctypes.c_uint64), ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+        ("cache", TreewyCache)]
+
+
+class TreewyAppendArgs(ctypes.Structure):
+    _device = None  # of the tensors it was made from
+    _fields_ = [("R", ctypes.c_int32), ("max_new", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_uint32)] + [
+        (f, ctypes.c_int64) for f in ("T", "k_stride", "v_stride")] + [
+        (f, ctypes.c_void_p) for f in ("node_offset", "parent", "accepted", "k", "v", "new_length", "status")] + [
+        ("cache", TreewyCache)]
+
+
+class TreewyNorm(ctypes.Structure):
+    _device = None  # of the tensors it was made from
+    _fields_ = [(f, ctypes.c_int64) for f in ("T", "x_stride", "residual_stride")] + [
+        (f, ctypes.c_int32) for f in ("n", "x_dtype", "residual_dtype", "group")] + [
+        ("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)] + [
+        (f, ctypes.c_void_p) for f in ("x", "residual", "residual_out", "weight", "y", "y8", "y8_scale")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 ENTRY_POINTS = ("treewy_verify", "treewy_commit", "treewy_commit_verify", "treewy_storeall_verify",
                 "treewy_storeall_commit", "treewy_extend", "treewy_qk_norm", "treewy_copy_slots",
+                "treewy_attend", "treewy_attend_workspace", "treewy_append", "treewy_add_norm",
                 "treewy_selftest_wait_timeout", "treewy_last_error", "treewy_version")
 
 
@@ -134,9 +170,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.treewy_extend.argtypes = [ctypes.POINTER(TreewySeqs), vp]
     lib.treewy_qk_norm.argtypes = [ctypes.POINTER(TreewyQk), vp]
     lib.treewy_copy_slots.argtypes = [ctypes.POINTER(TreewySlots), vp]
+    lib.treewy_attend.argtypes = [ctypes.POINTER(TreewyAttn), vp]
+    lib.treewy_attend_workspace.argtypes = [ctypes.POINTER(TreewyAttn), ctypes.POINTER(ctypes.c_uint64)]
+    lib.treewy_append.argtypes = [ctypes.POINTER(TreewyAppendArgs), vp]
+    lib.treewy_add_norm.argtypes = [ctypes.POINTER(TreewyNorm), vp]
     lib.treewy_selftest_wait_timeout.argtypes = [vp, ctypes.c_uint32, vp]
     for name in ("treewy_verify", "treewy_commit", "treewy_commit_verify", "treewy_storeall_verify",
                  "treewy_storeall_commit", "treewy_extend", "treewy_qk_norm", "treewy_copy_slots",
+                 "treewy_attend", "treewy_attend_workspace", "treewy_append", "treewy_add_norm",
                  "treewy_selftest_wait_timeout"):
         getattr(lib, name).restype = ctypes.c_int
     lib.treewy_last_error.argtypes = []
@@ -267,6 +308,31 @@ def treewy_copy_slots(slots: TreewySlots, stream=None) -> None:
     """Copy, fork, compact and clear slots of the state pools of all layers."""
     _reachable(slots)
     _check(load().treewy_copy_slots(ctypes.byref(slots), _stream_handle(stream)))
+
+
+def treewy_attend(attn: TreewyAttn, stream=None) -> None:
+    """Softmax attention of every draft node over its context in 8 bits and its path in the draft."""
+    _reachable(attn)
+    _check(load().treewy_attend(ctypes.byref(attn), _stream_handle(stream)))
+
+
+def treewy_append(args: TreewyAppendArgs, stream=None) -> None:
+    """Accepted (or all) rows of keys and values into the 8-bit pages."""
+    _reachable(args)
+    _check(load().treewy_append(ctypes.byref(args), _stream_handle(stream)))
+
+
+def treewy_add_norm(norm: TreewyNorm, stream=None) -> None:
+    """The residual's addition and the RMS norm, in 8 bits with scales where wanted."""
+    _reachable(norm)
+    _check(load().treewy_add_norm(ctypes.byref(norm), _stream_handle(stream)))
+
+
+def treewy_attend_workspace(attn: TreewyAttn) -> int:
+    """Bytes of workspace that a call with these sizes needs."""
+    n = ctypes.c_uint64(0)
+    _check(load().treewy_attend_workspace(ctypes.byref(attn), ctypes.byref(n)))
+    return n.value
 
 
 def make_batch(*, node_offset, parent, q, k, v, alpha, beta, state, state_slot, o, U, status,
@@ -480,6 +546,136 @@ def make_slots(*, state, src, dst, status, layers: Optional[int] = None) -> Tree
     a.layer_stride = int(state.stride(0)) * state.element_size() if layers is not None and layers > 1 else 0
     a.state, a.src, a.dst, a.status = _ptr(state), _ptr(src), _ptr(dst), _ptr(status)
     a._keep, a._device = (state, src, dst, status), device
+    return a
+
+
+def make_cache(*, k, v, k_scale, v_scale, page_table, length) -> TreewyCache:
+    """Fill a TreewyCache: k and v float8_e4m3fn [num_pages][Hkv][page_len][d],
+    scales f32 [num_pages][Hkv], page_table int32 [R][max_pages], length int32 [R].
+    """
+    import torch
+    if k.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k must be [num_pages][Hkv][page_len][d], page_table [R][max_pages]")
+    num_pages, Hkv, page_len, d = k.shape
+    _need(k, "k", torch.float8_e4m3fn)
+    _need(v, "v", torch.float8_e4m3fn, k.shape)
+    _need(k_scale, "k_scale", torch.float32, (num_pages, Hkv))
+    _need(v_scale, "v_scale", torch.float32, (num_pages, Hkv))
+    _need(page_table, "page_table", torch.int32)
+    _need(length, "length", torch.int32, (page_table.shape[0],))
+    keep = (k, v, k_scale, v_scale, page_table, length)
+    c = TreewyCache(Hkv, d, page_len, page_table.shape[1], num_pages, *map(_ptr, keep))
+    c._keep, c._device, c._R = keep, _one_device(keep), int(page_table.shape[0])
+    return c
+
+
+def _rows_of_cache(cache: TreewyCache, tensors, node_offset, status, others) -> tuple:
+    """What make_attn and make_append check alike; the tensors' strides and the device."""
+    import torch
+    strides = [_token_stride(x, n) for n, x in tensors]
+    T = tensors[0][1].shape[0]
+    for n, x in tensors:
+        if x.shape[0] != T or x.shape[2] != cache.d or x.dtype != tensors[0][1].dtype:
+            raise ValueError(f"{n} must have {T} rows of the cache's head size, and the rows one dtype")
+        if n != "q" and x.shape[1] != cache.Hkv:
+            raise ValueError(f"{n} must have the cache's {cache.Hkv} heads")
+    _need(node_offset, "node_offset", torch.int32, (cache._R + 1,))
+    _need(status, "status", torch.int32, (cache._R,))
+    device = _one_device([x for _, x in tensors] + [node_offset, status, *others])
+    if device != cache._device:
+        raise ValueError(f"the cache is on device {cache._device}, the rows on {device} (-1: the CPU)")
+    return T, strides, device
+
+
+def make_attn(*, cache: TreewyCache, node_offset, q, k, v, o, status, scale: float, max_nodes: int, max_context: int,
+              parent=None, workspace=None, flags: int = 0) -> TreewyAttn:
+    """Fill a TreewyAttn: q [T][Hq][d], k and v [T][Hkv][d] (strided token rows
+    allowed), o [T][Hq][d]; ``parent`` None: chains.  ``workspace`` is a uint8
+    tensor; without one, the structure gets its own, as large as it needs.
+    """
+    import torch
+    T, strides, device = _rows_of_cache(cache, (("q", q), ("k", k), ("v", v)), node_offset, status,
+                                        (o, parent, workspace))
+    Hq = int(q.shape[1])
+    _need(o, "o", o.dtype, (T, Hq, cache.d))
+    _need(parent, "parent", torch.int32, (T,))
+    _need(workspace, "workspace", torch.uint8)
+    a = TreewyAttn()
+    a.R, a.Hq, a.max_nodes, a.max_context = cache._R, Hq, int(max_nodes), int(max_context)
+    a.qkv_dtype, a.o_dtype, a.T = _dtype_code(q, "q/k/v"), _dtype_code(o, "o"), T
+    a.q_stride, a.k_stride, a.v_stride = strides
+    a.scale, a.flags, a.cache = float(scale), int(flags), cache
+    if workspace is None:
+        workspace = torch.empty(treewy_attend_workspace(a), dtype=torch.uint8, device=q.device)
+    a.node_offset, a.parent, a.q, a.k, a.v, a.o, a.status = map(_ptr, (node_offset, parent, q, k, v, o, status))
+    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+    a._keep, a._device = (cache._keep, node_offset, parent, q, k, v, o, status, workspace), device
+    return a
+
+
+def make_append(*, cache: TreewyCache, node_offset, k, v, status, max_new: int, parent=None, accepted=None,
+                new_length=None) -> TreewyAppendArgs:
+    """Fill a TreewyAppendArgs: k and v [T][Hkv][d] (strided token rows allowed);
+    ``accepted`` None: every row; ``new_length`` int32 [R], not the cache's own.
+    """
+    import torch
+    T, strides, device = _rows_of_cache(cache, (("k", k), ("v", v)), node_offset, status, (parent, accepted, new_length))
+    _need(parent, "parent", torch.int32, (T,))
+    _need(accepted, "accepted", torch.int32, (cache._R,))
+    _need(new_length, "new_length", torch.int32, (cache._R,))
+    a = TreewyAppendArgs()
+    a.R, a.max_new, a.kv_dtype, a.T = cache._R, int(max_new), _dtype_code(k, "k/v"), T
+    a.k_stride, a.v_stride = strides
+    a.cache = cache
+    a.node_offset, a.parent, a.accepted, a.k, a.v, a.new_length, a.status = map(
+        _ptr, (node_offset, parent, accepted, k, v, new_length, status))
+    a._keep, a._device = (cache._keep, node_offset, parent, accepted, k, v, new_length, status), device
+    return a
+
+
+def _row_stride(x, name: str) -> int:
+    """Elements between the rows of ``x`` [T][n], contiguous within a row."""
+    T, n = x.shape
+    if n > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    if T <= 1:
+        return n
+    if x.stride(0) < n:
+        raise ValueError(f"{name}: rows overlap")
+    return x.stride(0)
+
+
+def make_norm(*, x, residual=None, residual_out=None, weight=None, eps: float = 1e-6, y=None, y8=None, y8_scale=None,
+              group: int = 0) -> TreewyNorm:
+    """Fill a TreewyNorm: x [T][n] and residual [T][n] (strided rows allowed),
+    residual_out of the residual's type, y of x's, y8 float8_e4m3fn with
+    y8_scale [T][groups]; ``group`` columns to a scale, 0: the row.
+    """
+    import torch
+    if x.dim() != 2 or (residual is not None and residual.shape != x.shape):
+        raise ValueError("x and residual must be [T][n]")
+    T, n = x.shape
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if y8 is not None and y8_scale is None:
+        raise ValueError("y8_scale is needed with y8")
+    a = TreewyNorm()
+    a.T, a.n, a.group, a.eps = T, n, int(group), float(eps)
+    a.x_dtype, a.x_stride = _dtype_code(x, "x"), _row_stride(x, "x")
+    if residual is not None:
+        a.residual_dtype, a.residual_stride = _dtype_code(residual, "residual"), _row_stride(residual, "residual")
+        if residual_out is None:
+            raise ValueError("residual_out is needed with a residual")
+        _need(residual_out, "residual_out", residual.dtype, (T, n))
+    _need(weight, "weight", torch.float32, (n,))
+    _need(y, "y", x.dtype, (T, n))
+    _need(y8, "y8", torch.float8_e4m3fn, (T, n))
+    if y8 is not None:
+        _need(y8_scale, "y8_scale", torch.float32, (T, -(-n // group) if group else 1))
+    keep = (x, residual, residual_out, weight, y, y8, y8_scale)
+    a._device = _one_device(keep)
+    a.x, a.residual, a.residual_out, a.weight, a.y, a.y8, a.y8_scale = map(_ptr, keep)
+    a._keep = keep
     return a
 
 

@@ -43,10 +43,12 @@ cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& set) {
 // it touches memory, which holds it until that kernel is done.  A small call's
 // time between its neighbours is mostly that set-up.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
+cudaError_t launch_after_smem(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                              A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -54,6 +56,10 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, cuda
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
+  return launch_after_smem(kernel, grid, threads, 0, stream, args...);
 }
 
 // Tensor maps the tensor-core verify kernel reads through (built on the host
@@ -147,6 +153,14 @@ cudaError_t launch_extend_chunk(const treewy_seqs& s, const ExtendMaps& maps, cu
 cudaError_t launch_qk_norm(const treewy_qk& a, cudaStream_t stream);
 // cudaErrorNotSupported: more pieces of moves than a launch holds.
 cudaError_t launch_copy_slots(const treewy_slots& a, cudaStream_t stream);
+
+// Attention over 8-bit pages in f32 (attend_scan.cu), rows into those pages
+// (append.cu) and the norm in front of a projection (add_norm.cu).
+// cudaErrorNotSupported: more work than a launch holds.
+inline uint64_t attend_workspace(const treewy_attn&) { return 0; }
+cudaError_t launch_attend_scan(const treewy_attn& a, cudaStream_t stream);
+cudaError_t launch_append(const treewy_append_args& a, cudaStream_t stream);
+cudaError_t launch_add_norm(const treewy_norm& a, cudaStream_t stream);
 
 // One thread waiting for a barrier phase nothing completes (bounded).
 cudaError_t launch_wait_selftest(int32_t* status, uint32_t limit_us, cudaStream_t stream);

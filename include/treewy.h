@@ -22,7 +22,10 @@
  * Around it, for a server's pool of states: treewy_extend (the same rule over
  * a prompt's or a decode step's tokens), treewy_qk_norm (the normed q and k
  * that all of these read) and treewy_copy_slots (forking and compacting the
- * pool).
+ * pool).  In the softmax layers between the GDN ones, treewy_attend verifies a
+ * draft against a context kept in pages of 8 bits, treewy_append takes the
+ * accepted path (or a prompt) into it, and treewy_add_norm adds the residual
+ * and norms the rows of the next projection, in 8 bits where wanted.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -75,9 +78,13 @@ enum {
                                        it say why */
   TREEWY_STATUS_BAD_POSITION = 64,  /* treewy_qk_norm: a position outside the
                                        rotation table */
-  TREEWY_STATUS_SLOT_CLASH = 128    /* treewy_copy_slots: the move's destination
+  TREEWY_STATUS_SLOT_CLASH = 128,   /* treewy_copy_slots: the move's destination
                                        is written by another move too, or its
                                        source is another move's destination */
+  TREEWY_STATUS_BAD_PAGE = 256      /* treewy_attend, treewy_append: a page index
+                                       outside the pool, or a length that is
+                                       negative or above what the call or the
+                                       request's pages hold */
 };
 
 /* Element type of q, k and v. */
@@ -454,6 +461,204 @@ typedef struct treewy_slots {
  * made (it still counts as a destination or source of its other index).
  */
 treewy_status treewy_copy_slots(const treewy_slots* slots, cudaStream_t stream);
+
+/*
+ * One softmax layer's keys and values in 8 bits (treewy_attend, treewy_append):
+ * a pool of pages of page_len tokens, e4m3 codes with an f32 scale for each
+ * page and head, so that a key is k_scale times its code.
+ *
+ *   k, v        e4m3 [num_pages][Hkv][page_len][d], 16-byte aligned
+ *   k_scale, v_scale  f32 [num_pages][Hkv], positive; treewy_append makes them
+ *               powers of two, treewy_attend takes any in [2^-60, 2^60]
+ *   page_table  int32 [R][max_pages]: token t of request r is row t % page_len
+ *               of page page_table[r][t / page_len]; entries behind the
+ *               request's tokens are not read
+ *   length      int32 [R]: tokens in the cache
+ * page_len is 16, 32, 64 or 128, 1 <= d <= 256, num_pages * Hkv < 2^31.  Full
+ * pages may be shared by requests (a common prefix); a page that
+ * treewy_append writes to belongs to one request.  What a page holds behind
+ * its tokens may be anything.
+ */
+typedef struct treewy_cache {
+  int32_t Hkv;
+  int32_t d;
+  int32_t page_len;
+  int32_t max_pages;
+  int64_t num_pages;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  const int32_t* length;
+} treewy_cache;
+
+/*
+ * Draft trees in front of a softmax layer (treewy_attend).
+ *
+ * Sizes: R >= 0 requests, Hq >= 1 query heads, a multiple of Hkv (query head
+ * h reads key head h / (Hq / Hkv)), 1 <= max_nodes <= 64 a bound on every
+ * request's nodes, max_context >= 0 a bound on every length (both known to the
+ * host, which divides the work by them), T >= node_offset[R] rows.
+ *   node_offset int32 [R+1], as in treewy_batch; a lone token is a tree of one
+ *               node
+ *   parent      int32 [T] as in treewy_batch (-1: hangs off the context), or
+ *               NULL: every request's nodes are a chain
+ *   q           bf16|f32, token t's row of [Hq][d] at element t * q_stride
+ *   k, v        the same type, rows of [Hkv][d], the nodes' own keys and values
+ *               (normed and rotated; they enter the cache by treewy_append).
+ *               Strides 0 mean dense rows
+ *   o           bf16|f32 (o_dtype) [T][Hq][d]
+ *   status      int32 [R], bits OR-ed in
+ *   scale       factor of the scores, positive (1/sqrt(d))
+ *   workspace   workspace_bytes of device memory, 16-byte aligned, at least
+ *               what treewy_attend_workspace says; one call at a time uses it.
+ *               It needs no contents before a call and keeps none after it.
+ * Everything but the pages and the workspace is aligned to its element size;
+ * o and status overlap nothing else.
+ */
+typedef struct treewy_attn {
+  int32_t R;
+  int32_t Hq;
+  int32_t max_nodes;
+  int32_t max_context;
+  int32_t qkv_dtype;
+  int32_t o_dtype;
+  int64_t T;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* node_offset;
+  const int32_t* parent;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  int32_t* status;
+  void* workspace;
+  uint64_t workspace_bytes;
+  float scale;
+  uint32_t flags;                 /* TREEWY_FLAG_FORCE_GENERIC */
+  treewy_cache cache;
+} treewy_attn;
+
+/*
+ * treewy_attend -- softmax attention of every draft node over its request's
+ * context and its own path in the draft: for node n,
+ *   s_j = scale q_n . k_j,  o_n = sum_j e^{s_j} v_j / sum_j e^{s_j},
+ * j over the length[r] tokens in the cache, n's ancestors and n itself.  So no
+ * node is without a key.  The cache is not changed: as with treewy_verify and
+ * treewy_commit, what is accepted goes in afterwards.
+ *
+ * A node range outside [0, T) or a bad parent sets TREEWY_STATUS_BAD_TREE,
+ * more than max_nodes nodes TREEWY_STATUS_TOO_MANY_NODES, a page or length that
+ * does not hold TREEWY_STATUS_BAD_PAGE; that request's outputs stay as they are
+ * (with TREEWY_STATUS_TIMEOUT, some may be written).
+ *
+ * bf16 rows with bf16 outputs and d a multiple of 16 run on the tensor cores in
+ * 8-bit products, every f32 or bf16 operand as two e4m3 terms: a query, key or
+ * value of the draft is within 2^-17 of its row's largest, a weight of the
+ * softmax within 2^-8 of itself and 2^-14 of its row's largest.  Other calls
+ * run in f32.  A NaN (or an infinity, which counts as one) in a key reaches
+ * every node that sees it, in a value every such node's column.  Scores pass f32: where
+ * they overflow it, the node's outputs are NaN.
+ */
+treewy_status treewy_attend(const treewy_attn* attn, cudaStream_t stream);
+
+/* Bytes of workspace that treewy_attend needs for arguments of these sizes
+   (R, Hq, max_nodes, the types and the cache's sizes are read, no pointers):
+   on a card of any number of SMs, and for any contents. */
+treewy_status treewy_attend_workspace(const treewy_attn* attn, uint64_t* bytes);
+
+/*
+ * New keys and values for a cache (treewy_append).
+ *
+ * node_offset, T, strides: as in treewy_attn.  accepted NULL: every row of
+ * request r, in order, goes behind its length[r] tokens.  accepted int32 [R]:
+ * the rows on the path from the root to node accepted[r] do (-1: none), for
+ * trees of at most 64 nodes (parent NULL: chains).  max_new: a bound on every
+ * request's rows.  k, v: bf16|f32 (kv_dtype) rows of [Hkv][d].
+ *   new_length  int32 [R] or NULL: length[r] and the rows taken.  It is not
+ *               cache.length itself, which all layers of a step read.
+ */
+typedef struct treewy_append_args {
+  int32_t R;
+  int32_t max_new;
+  int32_t kv_dtype;
+  uint32_t reserved;
+  int64_t T;
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* node_offset;
+  const int32_t* parent;
+  const int32_t* accepted;
+  const void* k;
+  const void* v;
+  int32_t* new_length;
+  int32_t* status;
+  treewy_cache cache;
+} treewy_append_args;
+
+/*
+ * treewy_append -- rows into their pages, rounded to e4m3 in units of the
+ * page's scale (for each head; keys and values apart).
+ *
+ * A page's scale is the least power of two, 2^-40 at least, that brings what is
+ * written to it within 448, e4m3's largest value.  Where a page has tokens
+ * already, its scale only grows: then the codes of those tokens are divided by
+ * the same power of two, which is exact but for codes that leave e4m3's normal
+ * range.  A NaN or an infinity is stored as NaN and does not count for the
+ * scale.  Rows of a page behind its tokens stay as they are.
+ *
+ * A node range outside [0, T) or a bad parent sets TREEWY_STATUS_BAD_TREE,
+ * more than max_new rows TREEWY_STATUS_TOO_MANY_NODES, accepted[r] outside
+ * [-1, N_r) TREEWY_STATUS_BAD_ACCEPTED, a length that does not fit the pages or
+ * a page outside the pool TREEWY_STATUS_BAD_PAGE; nothing of that request is
+ * written.
+ */
+treewy_status treewy_append(const treewy_append_args* args, cudaStream_t stream);
+
+/*
+ * Rows for treewy_add_norm: T rows of n, 1 <= n <= 32768.
+ *   x             bf16|f32 (x_dtype), row t at element t * x_stride (0: dense)
+ *   residual      bf16|f32 (residual_dtype) or NULL, stride residual_stride
+ *   residual_out  the same type, dense rows, needed with a residual; it may be
+ *                 residual itself where that is dense
+ *   weight        f32 [n] or NULL (ones)
+ *   y             x's type, dense rows, or NULL; it may be x itself where that
+ *                 is dense
+ *   y8            e4m3, dense rows, or NULL
+ *   y8_scale      f32 [T][ceil(n / group)], needed with y8; group is 32, 64 or
+ *                 128 columns, or 0: one scale for a row
+ * Other overlaps are not allowed; everything is aligned to its element size.
+ */
+typedef struct treewy_norm {
+  int64_t T;
+  int64_t x_stride;
+  int64_t residual_stride;
+  int32_t n;
+  int32_t x_dtype;
+  int32_t residual_dtype;
+  int32_t group;
+  float eps;
+  uint32_t reserved;
+  const void* x;
+  const void* residual;
+  void* residual_out;
+  const float* weight;
+  void* y;
+  void* y8;
+  float* y8_scale;
+} treewy_norm;
+
+/*
+ * treewy_add_norm -- the residual's addition and the RMS norm in one pass:
+ *   z = x + residual,  y = w z / sqrt(mean of z^2 + eps),
+ * in f32; residual_out gets z, y and y8 the norm of z before its rounding.  A
+ * group's scale is its largest |y| / 448 (1 where that is 0), and y8 is y /
+ * scale rounded to e4m3; NaN stays NaN and does not count for the scale.
+ */
+treewy_status treewy_add_norm(const treewy_norm* norm, cudaStream_t stream);
 
 /* Message for the last non-OK return on the calling host thread ("" if none). */
 const char* treewy_last_error(void);
