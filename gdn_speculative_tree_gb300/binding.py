@@ -575,8 +575,10 @@ def _rows_of_cache(cache: TreewyCache, tensors, node_offset, status, others) -> 
     strides = [_token_stride(x, n) for n, x in tensors]
     T = tensors[0][1].shape[0]
     for n, x in tensors:
-        if x.shape[0] != T or x.shape[2] != cache.d or x.dtype != tensors[0][1].dtype:
-            raise ValueError(f"{n} must have {T} rows of the cache's head size, and the rows one dtype")
+        if x.dtype != tensors[0][1].dtype:
+            raise TypeError(f"{n} must have the other rows' dtype, {tensors[0][1].dtype}")
+        if x.shape[0] != T or x.shape[2] != cache.d:
+            raise ValueError(f"{n} must have {T} rows of the cache's head size {cache.d}")
         if n != "q" and x.shape[1] != cache.Hkv:
             raise ValueError(f"{n} must have the cache's {cache.Hkv} heads")
     _need(node_offset, "node_offset", torch.int32, (cache._R + 1,))

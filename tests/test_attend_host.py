@@ -193,7 +193,7 @@ def test_make_cache_refuses(name, change, error):
 
 
 @pytest.mark.parametrize("name,change,error", [
-    ("q", lambda x: x.half(), TypeError), ("q", lambda x: x[:-1], ValueError), ("q", lambda x: x.float(), ValueError),
+    ("q", lambda x: x.half(), TypeError), ("q", lambda x: x[:-1], ValueError), ("q", lambda x: x.float(), TypeError),
     ("k", lambda x: x[:, :1], ValueError), ("v", lambda x: x[:, :, :16], ValueError), ("o", lambda x: x[:-1], ValueError),
     ("o", lambda x: x.half(), TypeError), ("node_offset", lambda x: x[:-1], ValueError),
     ("status", lambda x: x.long(), TypeError), ("q", lambda x: x.transpose(1, 2), ValueError),
