@@ -164,7 +164,7 @@ treewy_status treewy_attend(const treewy_attn* attn, cudaStream_t stream) {
   a.q_stride = stride_or(a.q_stride, int64_t(a.Hq) * a.cache.d);
   a.k_stride = stride_or(a.k_stride, int64_t(a.cache.Hkv) * a.cache.d);
   a.v_stride = stride_or(a.v_stride, int64_t(a.cache.Hkv) * a.cache.d);
-  const cudaError_t err = treewy::launch_attend_scan(a, stream);
+  const cudaError_t err = treewy::attend_on_tensor_cores(a) ? treewy::launch_attend_tc(a, stream) : treewy::launch_attend_scan(a, stream);
   if (err == cudaErrorNotSupported)
     return fail(TREEWY_ERR_UNSUPPORTED, "%d requests of %d nodes and %d heads are too many for one call", a.R, a.max_nodes, a.Hq);
   return err == cudaSuccess ? TREEWY_OK : cuda_fail(err, "treewy_attend launch");

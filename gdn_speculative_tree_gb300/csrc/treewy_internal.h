@@ -2,6 +2,7 @@
 // translation units (launchers); not part of the public C ABI.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
@@ -154,10 +155,13 @@ cudaError_t launch_qk_norm(const treewy_qk& a, cudaStream_t stream);
 // cudaErrorNotSupported: more pieces of moves than a launch holds.
 cudaError_t launch_copy_slots(const treewy_slots& a, cudaStream_t stream);
 
-// Attention over 8-bit pages in f32 (attend_scan.cu), rows into those pages
-// (append.cu) and the norm in front of a projection (add_norm.cu).
-// cudaErrorNotSupported: more work than a launch holds.
-inline uint64_t attend_workspace(const treewy_attn&) { return 0; }
+// Attention over 8-bit pages on the tensor cores (attend_tc.cu; whether it takes
+// the call, from its sizes and types alone) and in f32 (attend_scan.cu), rows
+// into those pages (append.cu) and the norm in front of a projection
+// (add_norm.cu).  cudaErrorNotSupported: more work than a launch holds.
+bool attend_on_tensor_cores(const treewy_attn& a);
+uint64_t attend_workspace(const treewy_attn& a);
+cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream);
 cudaError_t launch_attend_scan(const treewy_attn& a, cudaStream_t stream);
 cudaError_t launch_append(const treewy_append_args& a, cudaStream_t stream);
 cudaError_t launch_add_norm(const treewy_norm& a, cudaStream_t stream);

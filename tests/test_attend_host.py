@@ -91,6 +91,7 @@ CACHE = [("cache.Hkv", 0, INVALID), ("cache.d", 0, INVALID), ("cache.d", 257, UN
     ("k_stride", -1, INVALID), ("v_stride", 1 << 40, UNSUPPORTED), ("q", None, INVALID), ("v", None, INVALID),
     ("o", None, INVALID), ("node_offset", None, INVALID), ("status", None, INVALID), ("q", FAKE + 1, INVALID),
     ("o", FAKE + 1, INVALID), ("parent", FAKE + 2, INVALID), ("node_offset", FAKE + 2, INVALID), ("status", FAKE + 1, INVALID),
+    ("workspace", None, INVALID), ("workspace", FAKE + 8, INVALID), ("workspace_bytes", 0, INVALID),
 ])
 def test_attend_refuses(lib, field, value, code):  # noqa: F811
     a = attn()
