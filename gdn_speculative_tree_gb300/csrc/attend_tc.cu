@@ -29,6 +29,12 @@
 //   warp 8      page table, scales and pages (TMA)
 //   warp 9      issues the products: S of the next tile before O of this one
 //
+// Drafts of at most 32 rows leave most lanes of a tile empty, and the softmax
+// of the rest to two warps (TMEM lanes belong to warps).  There (kSmall) Q's
+// rows are in shared memory four times, so that every quarter of the lanes has
+// all of S: each of the eight warps takes 16 tokens of every row, and the
+// weights go to shared memory instead of TMEM, as the product's left operand.
+//
 // Work: the items' tiles in a row, cut into equal pieces, one for each CTA; an
 // item that lies in several pieces is joined by attend_join_kernel.  Many
 // items of several row tiles each go to a CTA apiece instead, the row tiles
@@ -43,7 +49,7 @@ constexpr int kTile = 128;                      // tokens, and rows
 constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 1;
 constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kGroups = kTile / 16;             // the smallest page is 16 tokens
-constexpr int kMaxListed = 1024;                // requests whose tiles are put in a row
+constexpr int kMaxListed = 768;                 // requests whose tiles are put in a row
 constexpr int kMaxPieces = 152;                 // CTAs that share the row
 constexpr float kGrowth = 3.f, kBias = 5.f;     // 2^(kGrowth + kBias) <= 448
 constexpr float kLeast = 1e-37f;                // of a score's factor: -inf times it stays -inf
@@ -51,12 +57,15 @@ constexpr uint32_t kHalf = 128 * 128;           // bytes of 128 rows of 128
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 constexpr unsigned kFull = 0xffffffffu;
 
-template <int NH, int QR>
+// NH: halves of 128 columns of a head; kSmall: at most 32 rows.
+template <int NH, bool kSmall>
 struct Shape {
-  static constexpr uint32_t kQBytes = 2 * NH * QR * 128;
-  static constexpr uint32_t kStage = 2 * NH * kHalf;  // K, then V
-  static constexpr int kStages = NH == 2 ? (QR == 128 ? 2 : 3) : (QR == 128 ? 5 : 6);
-  static constexpr uint32_t kBytes = kQBytes + kStages * kStage + 1024;
+  static constexpr uint32_t kWBlock = 32 * 128;                      // a term of the weights of 32 rows
+  static constexpr uint32_t kWBytes = kSmall ? 4 * kWBlock : 0;      // two tiles, two terms
+  static constexpr uint32_t kQBytes = 2 * NH * kHalf;                // behind them: products read 128 rows of weights
+  static constexpr uint32_t kStage = 2 * NH * kHalf;                 // K, then V
+  static constexpr int kStages = NH == 2 ? 2 : 5;
+  static constexpr uint32_t kBytes = kWBytes + kQBytes + kStages * kStage + 1024;
 };
 
 struct Consts {
@@ -65,19 +74,23 @@ struct Consts {
 };
 
 struct AttendSmem {
-  Consts c[6];
-  uint64_t kfull[6], kfree[6], vfull[6], vfree[6], cfull[6];
+  Consts c[5];
+  uint64_t kfull[5], kfree[5], vfull[5], vfree[5], cfull[5];
   uint64_t sfull[2], pready[2], pvdone[2], qready, drain;
   uint64_t deadline;
   unsigned long long seen[kMaxNodes];  // the nodes that a node sees
   unsigned long long no_number;        // nodes with a value that is none
   float rowf[kTile];            // a row's unit of the queries, times the scores' factor
   float ks[kMaxNodes], lv[kMaxNodes], il[kMaxNodes];  // of the draft
-  float top[2][2][kTile];       // maxima (and sums) of the half rows; two sets in turn
+  float top[2][2 * kTile];      // maxima (and sums) of the parts of rows; two sets in turn
   int parent[kMaxNodes];
   int bad_tree;
   uint32_t tmem;
   int fail;
+  int scan[kThreads / 32];
+  // of every request, or of the CTA's own: tiles before it, rows, context
+  int base[kMaxListed + 1], lo[kMaxListed], len[kMaxListed];
+  uint8_t nodes[kMaxListed];
 };
 
 // A bounded wait: every wait of the CTA gives up at the same time.
@@ -171,12 +184,18 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
   return r;
 }
-// Two weights as hi + lo: f16 first, of which hi has the four leading bits and
-// lo the rest, rounded (2^-8 of the weight in all, 2^-9 where hi leaves e4m3's
-// normal range).
-__device__ __forceinline__ void weight_terms(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+// Eight values of a row of d bf16 at column c (zeros behind d).
+__device__ __forceinline__ uint4 load_row8(const uint16_t* row, int c, int d, bool wide) {
+  if (wide) return c < d ? __ldg(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
+  uint32_t u[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    u[e] = (c + 2 * e < d ? __ldg(row + c + 2 * e) : 0u) | (c + 2 * e + 1 < d ? static_cast<uint32_t>(__ldg(row + c + 2 * e + 1)) << 16 : 0u);
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Two values in f16 as hi + lo: hi the four leading bits, lo the next.
+__device__ __forceinline__ void split_f16x2(uint32_t h, uint32_t& hi, uint32_t& lo) {
   const uint32_t top = (h + 0x00400040u) & 0xff80ff80u;  // half a unit of the fourth bit up, the rest off
   uint32_t rest;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(top));
@@ -184,46 +203,43 @@ __device__ __forceinline__ void weight_terms(float x0, float x1, uint32_t& hi, u
   lo = e4m3x2_of_f16x2(rest);
 }
 
-// Eight values of a row of d bf16 at column c (zeros behind d).
-__device__ __forceinline__ void load_row8(const uint16_t* row, int c, int d, bool wide, float (&x)[8]) {
-  if (wide && c + 8 <= d) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + c));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(u[e] << 16);
-      x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = c + e < d ? bf16_bits_to_float(__ldg(row + c + e)) : 0.f;
-  }
+// Two weights as hi + lo: f16 first, of which hi has the four leading bits and
+// lo the rest, rounded (2^-8 of the weight in all, 2^-9 where hi leaves e4m3's
+// normal range).
+__device__ __forceinline__ void weight_terms(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+  split_f16x2(h, hi, lo);
 }
 
-// A row's terms, by one warp (lane: eight columns): codes of x 2^(7 - E), 2^E
-// the largest exponent of the row, and the unit 2^(E - 7).  What is not finite
-// becomes NaN.
-__device__ __forceinline__ float row_terms(const float (&x)[8], uint2& hi, uint2& lo) {
-  float top = 0.f;
+// A row's terms, by one warp (lane: eight columns, as bf16): codes of
+// x 2^(7 - E), 2^E the largest exponent of the row, and the unit 2^(E - 7).
+// What is not finite becomes NaN, or zero where `clear`; `none`: there is some.
+__device__ __forceinline__ float row_terms(uint4 x, bool clear, uint2& hi, uint2& lo, bool& none) {
+  uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  auto largest = [&] {
+    const uint32_t m = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu), __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
+    return __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+  };
+  uint32_t top = largest(), bad[4] = {0, 0, 0, 0};
+  none = top >= 0x7f80u;
+  if (none) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = fmaxf(top, size_of(x[e]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  const int E = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+    for (int e = 0; e < 4; ++e) {
+      bad[e] = ((u[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((u[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+      u[e] &= ~bad[e];
+    }
+    top = largest();
+  }
+  const int E = max(static_cast<int>(top >> 7) - 127, -100);
   const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - E) << 23);
   uint32_t h[4], l[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float y[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float v = x[2 * e + i];
-      y[i] = size_of(v) == fabsf(v) ? v * f : __uint_as_float(0x7fffffffu);
-    }
-    h[e] = e4m3x2(y[0], y[1]);
-    const uint32_t back = e4m3x2_to_f16x2(h[e]);
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
-    l[e] = e4m3x2(y[0] - b.x, y[1] - b.y);
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(__uint_as_float(u[e] & 0xffff0000u) * f), "f"(__uint_as_float(u[e] << 16) * f));
+    split_f16x2(y, h[e], l[e]);
+    if (!clear) h[e] |= (bad[e] & 0x7fu) | ((bad[e] >> 8) & 0x7f00u);
   }
   hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
@@ -259,92 +275,45 @@ __device__ __forceinline__ int row_tiles(const Params& p, int N) { return (N * p
 
 // Walks a CTA's segments; every role walks them for itself.
 struct Walk {
-  int64_t u, end;
-  int r;
-  __device__ bool next(const Params& p, const int64_t* base, Segment& s) {
-    const treewy_cache& c = p.a.cache;
+  int u, end, r;
+  __device__ bool next(const Params& p, const AttendSmem& cs, Segment& s) {
     if (u >= end) return false;
-    if (!p.listed) {
-      const int per = c.Hkv * p.tiles_m;
-      s.r = static_cast<int>(blockIdx.x / per);
-      s.h = static_cast<int>(blockIdx.x % per) / p.tiles_m;
-      s.m = static_cast<int>(blockIdx.x % per) % p.tiles_m;
-      const CacheRequest q = cache_request(c, p.a.node_offset, s.r, p.a.T, p.a.max_nodes, p.a.max_context);
-      s.lo = q.lo, s.N = q.N, s.len = q.len, s.t0 = 0, s.tiles = s.t1 = tiles_of(q.len);
-      u = end;
-      return true;
+    int k = 0;
+    if (p.listed) {
+      while (cs.base[r + 1] <= u) ++r;
+      k = s.r = r;
+    } else {
+      s.r = static_cast<int>(blockIdx.x / (p.a.cache.Hkv * p.tiles_m));
     }
-    while (base[r + 1] <= u) ++r;
-    const CacheRequest q = cache_request(c, p.a.node_offset, r, p.a.T, p.a.max_nodes, p.a.max_context);
-    s.r = r, s.lo = q.lo, s.N = q.N, s.len = q.len, s.tiles = tiles_of(q.len);
-    const int64_t in = u - base[r];
-    const int item = static_cast<int>(in / s.tiles), mt = row_tiles(p, q.N);
-    s.h = item / mt, s.m = item % mt;
-    s.t0 = static_cast<int>(in % s.tiles);
-    s.t1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.t0 + (end - u)));
+    s.lo = cs.lo[k], s.N = cs.nodes[k], s.len = cs.len[k], s.tiles = tiles_of(s.len);
+    if (p.listed) {
+      const int in = u - cs.base[r], item = in / s.tiles, mt = row_tiles(p, s.N);
+      s.h = item / mt, s.m = item % mt, s.t0 = in % s.tiles, s.t1 = min(s.tiles, s.t0 + (end - u));
+    } else {
+      const int item = static_cast<int>(blockIdx.x % (p.a.cache.Hkv * p.tiles_m));
+      s.h = item / p.tiles_m, s.m = item % p.tiles_m, s.t0 = 0, s.t1 = s.tiles;
+    }
     u += s.t1 - s.t0;
     return true;
   }
 };
 
-template <int NH, int QR>
+template <int NH, bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
-  after_previous();
-  using Sh = Shape<NH, QR>;
+  using Sh = Shape<NH, kSmall>;
   constexpr int S = Sh::kStages;
   extern __shared__ unsigned char raw_smem[];
   __shared__ AttendSmem cs;
-  __shared__ int64_t base[kMaxListed + 1];
-  unsigned char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  unsigned char* wts = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  unsigned char* smem = wts + Sh::kWBytes;
   unsigned char* ring = smem + Sh::kQBytes;
   const treewy_attn& a = p.a;
   const treewy_cache& c = a.cache;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, d = c.d, G = p.G;
 
-  // ---- this CTA's part
-  Walk begin = {0, 1, 0};
-  int64_t total = 1, pieces = 1;
-  if (p.listed) {
-    for (int r = t; r < a.R; r += kThreads) {
-      const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
-      if (q.err != 0 && blockIdx.x == 0) atomicOr(a.status + r, q.err);
-      base[r + 1] = q.N == 0 ? 0 : static_cast<int64_t>(c.Hkv) * row_tiles(p, q.N) * tiles_of(q.len);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      int64_t carry = 0;
-      for (int r0 = 0; r0 < a.R; r0 += 32) {
-        long long v = r0 + lane < a.R ? base[r0 + lane + 1] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(kFull, v, o);
-          if (lane >= o) v += y;
-        }
-        if (r0 + lane < a.R) base[r0 + lane + 1] = carry + v;
-        carry += __shfl_sync(kFull, v, 31);
-      }
-      if (lane == 0) base[0] = 0;
-    }
-    __syncthreads();
-    total = base[a.R];
-    pieces = min(static_cast<int64_t>(gridDim.x), total);  // none of them empty
-    begin.u = blockIdx.x * total / max(pieces, static_cast<int64_t>(1));
-    begin.end = (blockIdx.x + 1) * total / max(pieces, static_cast<int64_t>(1));
-    if (t == 0) {
-      p.record[8 * blockIdx.x] = 0;
-      p.part_bad[2 * blockIdx.x] = p.part_bad[2 * blockIdx.x + 1] = 1;
-    }
-    if (blockIdx.x >= pieces) return;
-  } else {
-    const int per = c.Hkv * p.tiles_m, r = static_cast<int>(blockIdx.x / per), item = static_cast<int>(blockIdx.x % per);
-    const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
-    if (q.err != 0 && item == 0 && t == 0) atomicOr(a.status + r, q.err);
-    if (item % p.tiles_m >= row_tiles(p, q.N)) return;
-  }
-
-  // ---- set-up
+  // ---- set-up, while the kernel before may still run
   if (t == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&cs.kfull[i], 1);
@@ -362,14 +331,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&cs.drain, 1);
     fence_mbarrier_init();
     cs.fail = 0;
-    // a second, and a hundred times what a tile takes
-    cs.deadline = globaltimer_ns() + 1000000000ull +
-                  100000ull * static_cast<uint64_t>(p.listed ? begin.end - begin.u : 1 + a.max_context / kTile);
+    cs.base[0] = 0;
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&cs.tmem, kTmemCols);
     tmem_relinquish();
   }
+  after_previous();
+
+  // ---- this CTA's part
+  Walk begin = {0, 1, 0};
+  int total = 1, pieces = 1;
+  bool none_here = false;
+  if (p.listed) {
+    int carry = 0;
+    for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+      const int r = r0 + t;
+      int v = 0;
+      if (r < a.R) {
+        const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
+        if (q.err != 0 && blockIdx.x == 0) atomicOr(a.status + r, q.err);
+        cs.lo[r] = q.lo, cs.nodes[r] = static_cast<uint8_t>(q.N), cs.len[r] = q.len;
+        v = q.N == 0 ? 0 : c.Hkv * row_tiles(p, q.N) * tiles_of(q.len);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += y;
+      }
+      if (lane == 31) cs.scan[warp] = v;
+      __syncthreads();
+      int before = carry;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const int x = cs.scan[w];
+        if (w < warp) before += x;
+        carry += x;
+      }
+      if (r < a.R) cs.base[r + 1] = before + v;
+      __syncthreads();
+    }
+    total = carry;
+    pieces = min(static_cast<int>(gridDim.x), total);  // none of them empty
+    none_here = static_cast<int>(blockIdx.x) >= pieces;
+    if (!none_here) {
+      begin.u = static_cast<int>(static_cast<int64_t>(blockIdx.x) * total / pieces);
+      begin.end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * total / pieces);
+      int lo = 0, hi = a.R;  // base[lo] <= u < base[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cs.base[mid] <= begin.u) lo = mid;
+        else hi = mid;
+      }
+      begin.r = lo;
+    }
+    if (t == 0) {
+      p.record[8 * blockIdx.x] = 0;
+      p.part_bad[2 * blockIdx.x] = p.part_bad[2 * blockIdx.x + 1] = 1;
+    }
+  } else {
+    const int per = c.Hkv * p.tiles_m, r = static_cast<int>(blockIdx.x / per), item = static_cast<int>(blockIdx.x % per);
+    const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
+    if (q.err != 0 && item == 0 && t == 0) atomicOr(a.status + r, q.err);
+    if (t == 0) cs.lo[0] = q.lo, cs.nodes[0] = static_cast<uint8_t>(q.N), cs.len[0] = q.len;
+    none_here = item % p.tiles_m >= row_tiles(p, q.N);
+  }
+  if (t == 0) {  // a second, and a hundred times what a tile takes
+    cs.deadline = globaltimer_ns() + 1000000000ull +
+                  100000ull * static_cast<uint64_t>(p.listed ? begin.end - begin.u : 1 + a.max_context / kTile);
+  }
+  if (none_here) begin.end = begin.u;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -385,12 +417,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- pages: lane i has the i-th of 32 pages of the context
     const int P = c.page_len, per = kTile / P;
     bool ok = true;
-    while (ok && walk.next(p, base, g)) {
+    while (ok && walk.next(p, cs, g)) {
       const int32_t* table = c.page_table + static_cast<int64_t>(g.r) * c.max_pages;
       const int pages = (g.len + P - 1) / P;
+      auto entry = [&](int i) { return i < pages ? __ldg(table + i) : -1; };
+      auto scale = [&](const float* x, int page) {
+        return page >= 0 && page < c.num_pages ? __ldg(x + static_cast<int64_t>(page) * c.Hkv + g.h) : 1.f;
+      };
       int first = -1;  // page index of lane 0's
-      int page = 0;
-      float ks = 0.f, vs = 1.f;
+      int page = 0, next = 0;
+      float ks = 0.f, vs = 1.f, next_ks = 0.f, next_vs = 1.f;
       for (int j = g.t0; j < g.t1; ++j, ++gt) {
         const int slot = gt % S;
         const uint32_t again = (gt / S + 1) & 1;
@@ -403,13 +439,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const int p0 = (j - 1) * per;  // the tile's first page
-        if (first < 0 || p0 >= first + 32) {
+        if (first < 0) {
           first = p0;
-          page = -1;
-          if (p0 + lane < pages) page = __ldg(table + p0 + lane);
-          const bool in = page >= 0 && page < c.num_pages;
-          ks = in ? __ldg(c.k_scale + static_cast<int64_t>(page) * c.Hkv + g.h) : 1.f;
-          vs = in ? __ldg(c.v_scale + static_cast<int64_t>(page) * c.Hkv + g.h) : 1.f;
+          page = entry(p0 + lane);
+          next = entry(p0 + 32 + lane);
+          ks = scale(c.k_scale, page), vs = scale(c.v_scale, page);
+        } else if (p0 >= first + 32) {  // the next 32, asked for ahead
+          first = p0;
+          page = next, ks = next_ks, vs = next_vs;
+          next = entry(p0 + 32 + lane);
         }
         const int src = p0 - first;  // the lane that has it
         const bool mine = lane >= src && lane < src + per && first + lane < pages;
@@ -430,6 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (gt >= S) ok = wait_warp(cs, &cs.vfree[slot], again);
         if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&cs.vfull[slot], bytes);
+        armed_v = gt + 1;
+        __syncwarp();
+        if (mine && in) {
+#pragma unroll
+          for (int x = 0; x < NH; ++x) tma_load_3d(stage + (NH + x) * kHalf + to, &vmap, &cs.vfull[slot], x * 128, 0, z);
+        }
+        __syncwarp();
         const int at = src + min(lane, kGroups - 1) * 16 / P;
         const float gk = __shfl_sync(kFull, ks, at), gv = __shfl_sync(kFull, vs, at);
         if (lane < kGroups) {
@@ -440,23 +486,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) cs.c[slot].bad = load != wanted;
         warp_arrive(&cs.cfull[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(&cs.vfull[slot], bytes);
-        armed_v = gt + 1;
-        __syncwarp();
-        if (mine && in) {
-#pragma unroll
-          for (int x = 0; x < NH; ++x) tma_load_3d(stage + (NH + x) * kHalf + to, &vmap, &cs.vfull[slot], x * 128, 0, z);
-        }
-        __syncwarp();
+        // the scales of the pages that were asked for with the last 32
+        if (src == (per == 32 ? 0 : per)) next_ks = scale(c.k_scale, next), next_vs = scale(c.v_scale, next);
       }
     }
   } else if (warp == kMmaWarp) {
     // ---- products
     const uint32_t id_s = idesc_f8(kTile, false), id_o = idesc_f8(d, true);
-    const uint32_t q0 = smem_addr(smem), r0 = smem_addr(ring);
+    const uint32_t q0 = smem_addr(smem), r0 = smem_addr(ring), w0 = smem_addr(wts);
     int seg = 0;
     bool ok = true;
-    while (ok && walk.next(p, base, g)) {
+    while (ok && walk.next(p, cs, g)) {
       ok = wait_warp(cs, &cs.qready, seg & 1);
       ++seg;
       auto scores = [&](int tile) {  // S of the CTA's tile number `tile`
@@ -475,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t b = smem_desc_sw128(k0 + x * kHalf + k * 32, 1024);
 #pragma unroll
               for (int term = 0; term < 2; ++term) {
-                mma_f8(s, smem_desc_sw128(q0 + (term * NH + x) * (QR * 128) + k * 32, 1024), b, id_s, acc);
+                mma_f8(s, smem_desc_sw128(q0 + (term * NH + x) * kHalf + k * 32, 1024), b, id_s, acc);
                 acc = 1;
               }
             }
@@ -490,10 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = g.t0; ok && j < g.t1; ++j, ++gt) {
         if (j + 1 < g.t1) ok = scores(gt + 1);
         const int slot = gt % S;
-        ok = ok && wait_warp(cs, &cs.pready[gt & 1], (gt >> 1) & 1) && wait_warp(cs, &cs.vfull[slot], (gt / S) & 1);
+        ok = ok && wait_warp(cs, &cs.vfull[slot], (gt / S) & 1) && wait_warp(cs, &cs.pready[gt & 1], (gt >> 1) & 1);
         if (!ok) break;
         tc_fence_after_sync();
-        const int n = j == 0 ? (g.N > 32 ? kTile : kTile / 2) : min(kTile, g.len - (j - 1) * kTile);
+        const int n = j == 0 ? (kSmall ? (g.N + 7) / 8 * 16 : g.N > 32 ? kTile : kTile / 2) : min(kTile, g.len - (j - 1) * kTile);
         if (elect_one()) {
           const uint32_t w = tmem + kColS + (gt & 1) * kTile, v0 = r0 + slot * Sh::kStage + NH * kHalf;
           uint32_t acc = j != g.t0;
@@ -503,7 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b = desc_mn(v0 + k * 4096);
 #pragma unroll
             for (int term = 0; term < 2; ++term) {
-              mma_f8_ts(tmem + kColO, w + term * 32 + k * 8, b, id_o, acc);
+              if constexpr (kSmall)
+                mma_f8(tmem + kColO, smem_desc_sw128(w0 + (2 * (gt & 1) + term) * Sh::kWBlock + k * 32, 1024), b, id_o, acc);
+              else
+                mma_f8_ts(tmem + kColO, w + term * 32 + k * 8, b, id_o, acc);
               acc = 1;
             }
           }
@@ -514,14 +557,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- softmax: warps w and w + 4 have the two halves of the tokens for rows 32 (w % 4) ..
-    const int part = warp & 3, hf = warp >> 2, row = part * 32 + lane;
+    // ---- softmax: warps w and w + 4 have lanes 32 (w % 4) ..; a thread has kCols tokens of a row
+    constexpr int kCols = kSmall ? 16 : 64, kNodes = kCols / 2;
+    const int part = warp & 3, hf = warp >> 2, row = kSmall ? lane : part * 32 + lane;
+    const int share = kSmall ? part * 2 + hf : hf, tok0 = share * kCols;  // which part of the row
     const uint32_t lanes = tmem + (static_cast<uint32_t>(part * 32) << 16);
     const int out_cols = (d / 16 + 1) / 2 * 16;  // O's columns of the first half
     const int col0 = hf ? out_cols : 0, col1 = hf ? d : out_cols;
+    const bool has_o = !kSmall || part == 0;  // O is in lanes 0-31 there
     auto all_sync = [] { named_bar_sync<1, kSoftThreads>(); };
-    auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(2 + part) : "memory"); };
-    while (walk.next(p, base, g)) {
+    auto row_sync = [&] {  // among the warps that share rows
+      if constexpr (kSmall) named_bar_sync<1, kSoftThreads>();
+      else asm volatile("bar.sync %0, 64;" ::"r"(2 + part) : "memory");
+    };
+    // `op` over the parts of this thread's row
+    auto over_row = [&](int set, float v, auto op) {
+      constexpr int kPitch = kSmall ? 32 : kTile;
+      cs.top[set][share * kPitch + row] = v;
+      row_sync();
+#pragma unroll
+      for (int i = 0; i < (kSmall ? 8 : 2); ++i) {
+        const float y = cs.top[set][i * kPitch + row];
+        v = i == 0 ? y : op(v, y);
+      }
+      return v;
+    };
+    while (walk.next(p, cs, g)) {
       // queries and tree
       const int row0 = g.m * kTile, rows = min(kTile, g.N * G - row0);
       if (t == 0) cs.bad_tree = 0, cs.no_number = 0;
@@ -532,66 +593,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (wrong) cs.bad_tree = 1;
         cs.parent[t] = wrong ? -1 : q;
       }
-      for (int i = warp; i < rows; i += kSoftWarps) {
-        const int node = (row0 + i) / G, head = g.h * G + (row0 + i) % G;
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(g.lo) + node) * a.q_stride +
-                            static_cast<int64_t>(head) * d;
-        float x[8];
-        uint2 hi, lo;
-        load_row8(q, 8 * lane, d, p.wide_q, x);
-        const float unit = row_terms(x, hi, lo);
-        if (8 * lane < NH * 128) {
-          *operand8(smem, i, lane, QR * 128) = hi;
-          *operand8(smem + NH * QR * 128, i, lane, QR * 128) = lo;
+      constexpr int kBatch = 8;  // rows of a warp that are loaded together
+      for (int i0 = warp; i0 < rows; i0 += kSoftWarps * kBatch) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int i = i0 + e * kSoftWarps, rr = row0 + i, node = rr / G;
+          if (i < rows)
+            x[e] = load_row8(static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(g.lo) + node) * a.q_stride +
+                                 static_cast<int64_t>(g.h * G + rr - node * G) * d,
+                             8 * lane, d, p.wide_q);
         }
-        if (lane == 0) cs.rowf[i] = unit * factor;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int i = i0 + e * kSoftWarps;
+          if (i >= rows) continue;
+          uint2 hi, lo;
+          bool none;
+          const float unit = row_terms(x[e], false, hi, lo, none);
+          if (8 * lane < NH * 128) {
+#pragma unroll
+            for (int copy = 0; copy < (kSmall ? 4 : 1); ++copy) {
+              *operand8(smem, 32 * copy + i, lane, kHalf) = hi;
+              *operand8(smem + NH * kHalf, 32 * copy + i, lane, kHalf) = lo;
+            }
+          }
+          if (lane == 0) cs.rowf[i] = unit * factor;
+        }
       }
       if (g.t0 == 0) {
         wait_warp(cs, &cs.cfull[gt % S], (gt / S) & 1);  // the stage is free
         unsigned char* stage = ring + (gt % S) * Sh::kStage;
-        for (int i = warp; i < 2 * kMaxNodes; i += kSoftWarps) {
-          const bool value = i >= kMaxNodes;
-          const int n = i & (kMaxNodes - 1), token = (n >> 5) * 64 + (n & 31);
-          uint2 hi = make_uint2(0, 0), lo = hi;
-          float unit = 1.f;
-          if (n < g.N) {
-            const uint16_t* q = value ? static_cast<const uint16_t*>(a.v) + (static_cast<int64_t>(g.lo) + n) * a.v_stride
-                                      : static_cast<const uint16_t*>(a.k) + (static_cast<int64_t>(g.lo) + n) * a.k_stride;
-            float x[8];
-            load_row8(q + static_cast<int64_t>(g.h) * d, 8 * lane, d, value ? p.wide_v : p.wide_k, x);
-            if (value) {  // NaN would reach the nodes that do not see it: weights of zero times it
-              bool none = false;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if (size_of(x[e]) != fabsf(x[e])) none = true, x[e] = 0.f;
-              }
-              if (none) atomicOr(&cs.no_number, 1ull << n);
+        for (int value = 0; value < 2; ++value) {
+          const uint16_t* from = static_cast<const uint16_t*>(value ? a.v : a.k) +
+                                 static_cast<int64_t>(g.lo) * (value ? a.v_stride : a.k_stride) + static_cast<int64_t>(g.h) * d;
+          uint4 x[kMaxNodes / kSoftWarps];
+#pragma unroll
+          for (int e = 0; e < kMaxNodes / kSoftWarps; ++e) {
+            const int n = warp + e * kSoftWarps;
+            x[e] = make_uint4(0, 0, 0, 0);
+            if (n < g.N) x[e] = load_row8(from + n * (value ? a.v_stride : a.k_stride), 8 * lane, d, value ? p.wide_v : p.wide_k);
+          }
+#pragma unroll
+          for (int e = 0; e < kMaxNodes / kSoftWarps; ++e) {
+            const int n = warp + e * kSoftWarps, token = n / kNodes * kCols + n % kNodes;
+            uint2 hi = make_uint2(0, 0), lo = hi;
+            float unit = 1.f;
+            bool none = false;
+            // a value that is no number would reach the nodes that do not see it: weights of zero times it
+            if (n < g.N) unit = row_terms(x[e], value != 0, hi, lo, none);
+            if (8 * lane < NH * 128) {
+              unsigned char* tile = stage + (value ? NH * kHalf : 0);
+              *operand8(tile, token, lane, kHalf) = hi;
+              *operand8(tile, token + kNodes, lane, kHalf) = lo;
             }
-            unit = row_terms(x, hi, lo);
-          }
-          if (8 * lane < NH * 128) {
-            unsigned char* tile = stage + (value ? NH * kHalf : 0);
-            *operand8(tile, token, lane, kHalf) = hi;
-            *operand8(tile, token + 32, lane, kHalf) = lo;
-          }
-          if (lane == 0) {
-            if (value) {
-              const float lv = log2f(unit);
-              cs.lv[n] = lv;
-              cs.il[n] = ex2(-lv);
-            } else {
-              cs.ks[n] = unit;
+            if (lane == 0) {
+              if (value) {
+                if (none) atomicOr(&cs.no_number, 1ull << n);
+                const float lv = log2f(unit);
+                cs.lv[n] = lv;
+                cs.il[n] = ex2(-lv);
+              } else {
+                cs.ks[n] = unit;
+              }
             }
           }
         }
       }
       fence_proxy_async_smem();
       all_sync();
-      if (t < g.N) {  // the nodes that node t sees
-        unsigned long long m = 0;
-        for (int q = t; q >= 0; q = cs.parent[q]) m |= 1ull << q;
-        cs.seen[t] = m;
-      }
       if (t == 0) {
         arrive(&cs.qready);
         if (g.t0 == 0) {
@@ -599,13 +670,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           arrive(&cs.vfull[gt % S]);
         }
       }
+      if (t < g.N) {  // the nodes that node t sees
+        unsigned long long m = 0;
+        for (int q = t; q >= 0; q = cs.parent[q]) m |= 1ull << q;
+        cs.seen[t] = m;
+      }
       all_sync();
 
       bool bad = cs.bad_tree != 0;
       const int bad_bit = bad ? TREEWY_STATUS_BAD_TREE : TREEWY_STATUS_BAD_PAGE;
-      const bool alive = part * 32 < rows;
+      const bool alive = kSmall || part * 32 < rows;
       const float rowf = row < rows ? cs.rowf[row] : 0.f;
-      const uint32_t seen = static_cast<uint32_t>(cs.seen[min(row0 + row, g.N * G - 1) / G] >> (32 * hf));
+      const int node = min(row0 + row, g.N * G - 1) / G;
+      const uint32_t seen = static_cast<uint32_t>(cs.seen[node] >> (kNodes * share));
       float m = -INFINITY, sum = 0.f;
       for (int j = g.t0; j < g.t1; ++j, ++gt) {
         const int slot = gt % S, b = gt & 1;
@@ -626,38 +703,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (alive) {
           const uint32_t sc = lanes + kColS + b * kTile;
-          uint32_t r[64];
+          uint32_t r[kCols];
           float* s = reinterpret_cast<float*>(r);
           if (ok) {
-            tmem_ld32(sc + hf * 64, r);
-            tmem_ld32(sc + hf * 64 + 32, r + 32);
-            tmem_wait32(r);
-            tmem_wait32(r + 32);
+            if constexpr (kSmall) {
+              uint32_t(&r16)[16] = *reinterpret_cast<uint32_t(*)[16]>(r);
+              tmem_ld16_async(sc + tok0, r16);
+              tmem_wait16(r16);
+            } else {
+              tmem_ld32(sc + tok0, r);
+              tmem_ld32(sc + tok0 + 32, r + 32);
+              tmem_wait32(r);
+              tmem_wait32(r + 32);
+            }
           }
           float top = -INFINITY;
           if (j == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float y = (s[i] + s[32 + i]) * (cs.ks[hf * 32 + i] * rowf) + cs.lv[hf * 32 + i];
+            for (int i = 0; i < kNodes; ++i) {
+              const int q = share * kNodes + i;
+              const float y = (s[i] + s[kNodes + i]) * (cs.ks[q] * rowf) + cs.lv[q];
               s[i] = (seen >> i) & 1 ? y : -INFINITY;
               top = fmaxf(top, s[i]);
             }
           } else {
             if (n < kTile) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) s[i] = hf * 64 + i < n ? s[i] : -INFINITY;
+              for (int i = 0; i < kCols; ++i) s[i] = tok0 + i < n ? s[i] : -INFINITY;
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kCols / 16; ++q) {
               float x = s[16 * q];
 #pragma unroll
               for (int i = 1; i < 16; ++i) x = fmaxf(x, s[16 * q + i]);
-              top = fmaxf(top, fmaf(x, fmaxf(cc.ks[hf * 4 + q] * rowf, kLeast), cc.lv[hf * 4 + q]));
+              const int at = share * (kCols / 16) + q;
+              top = fmaxf(top, fmaf(x, fmaxf(cc.ks[at] * rowf, kLeast), cc.lv[at]));
             }
           }
-          cs.top[b][hf][row] = top;
-          pair_sync();
-          top = fmaxf(top, cs.top[b][hf ^ 1][row]);
+          top = over_row(b, top, [](float x, float y) { return fmaxf(x, y); });
           if (j == g.t0) {
             m = top;
           } else {
@@ -666,49 +749,52 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float down = grown ? ex2(m - top) : 1.f;
               if (grown) m = top;
               sum *= down;
-              wait_warp(cs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
-              tc_fence_after_sync();
-              for (int x = col0; x < col1; x += 16) {
-                uint32_t o[16];
-                tmem_ld16_async(lanes + kColO + x, o);
-                tmem_wait16(o);
+              if (has_o) {
+                wait_warp(cs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
+                tc_fence_after_sync();
+                for (int x = col0; x < col1; x += 16) {
+                  uint32_t o[16];
+                  tmem_ld16_async(lanes + kColO + x, o);
+                  tmem_wait16(o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * down);
-                tmem_st16(lanes + kColO + x, o);
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * down);
+                  tmem_st16(lanes + kColO + x, o);
+                }
+                tmem_wait_st();
               }
-              tmem_wait_st();
             }
           }
           const float off = kBias - m;
-          uint32_t hi[16], lo[16];
+          uint32_t hi[kCols / 4], lo[kCols / 4];
           if (j == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < kNodes; ++i) {
               s[i] = ex2(s[i] + off);
-              sum = fmaf(s[i], cs.il[hf * 32 + i], sum);
+              sum = fmaf(s[i], cs.il[share * kNodes + i], sum);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kNodes / 4; ++i) {
               uint32_t h0, l0, h1, l1;
               weight_terms(s[4 * i], s[4 * i + 1], h0, l0);
               weight_terms(s[4 * i + 2], s[4 * i + 3], h1, l1);
-              hi[i] = hi[i + 8] = h0 | (h1 << 16);  // the value's two terms have one weight
-              lo[i] = lo[i + 8] = l0 | (l1 << 16);
+              hi[i] = hi[i + kNodes / 4] = h0 | (h1 << 16);  // the value's two terms have one weight
+              lo[i] = lo[i + kNodes / 4] = l0 | (l1 << 16);
             }
           } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float f = fmaxf(cc.ks[hf * 4 + q] * rowf, kLeast), e = cc.lv[hf * 4 + q] + off;
+            for (int q = 0; q < kCols / 16; ++q) {
+              const int at = share * (kCols / 16) + q;
+              const float f = fmaxf(cc.ks[at] * rowf, kLeast), e = cc.lv[at] + off;
               float part_sum = 0.f;
 #pragma unroll
               for (int i = 16 * q; i < 16 * q + 16; ++i) {
                 s[i] = ex2(fmaf(s[i], f, e));
                 part_sum += s[i];
               }
-              sum = fmaf(part_sum, cc.il[hf * 4 + q], sum);
+              sum = fmaf(part_sum, cc.il[at], sum);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kCols / 4; ++i) {
               uint32_t h0, l0, h1, l1;
               weight_terms(s[4 * i], s[4 * i + 1], h0, l0);
               weight_terms(s[4 * i + 2], s[4 * i + 3], h1, l1);
@@ -716,9 +802,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               lo[i] = l0 | (l1 << 16);
             }
           }
-          tmem_st16(sc + hf * 16, hi);
-          tmem_st16(sc + 32 + hf * 16, lo);
-          tmem_wait_st();
+          if constexpr (kSmall) {
+            unsigned char* w = wts + 2 * b * Sh::kWBlock + row * 128 + ((share ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(w) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(w + Sh::kWBlock) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            fence_proxy_async_smem();
+          } else {
+            tmem_st16(sc + hf * 16, hi);
+            tmem_st16(sc + 32 + hf * 16, lo);
+            tmem_wait_st();
+          }
           tc_fence_before_sync();
         }
         warp_arrive(&cs.pready[b]);
@@ -728,62 +821,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = g.t0 == 0 && g.t1 == g.tiles;
       const bool ok = wait_warp(cs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
       tc_fence_after_sync();
-      if (alive) {
-        cs.top[gt & 1][hf][row] = sum;  // not the set of the last tile, which the other warp may still read
-        pair_sync();
-        sum += cs.top[gt & 1][hf ^ 1][row];
+      // not the set of the last tile, which another warp may still read
+      if (alive) sum = over_row(gt & 1, sum, [](float x, float y) { return x + y; });
+      const float inv = 1.f / sum;
+      if (ok && alive && has_o) {
+        const int head = g.h * G + (row0 + row) % G;
+        const int64_t out = ((static_cast<int64_t>(g.lo) + node) * a.Hq + head) * d;
+        const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
+        float* po = p.part_o + (piece * p.rows_cap + row) * d;
+        const bool write = row < rows && !bad;
+        const unsigned long long none = g.t0 == 0 && write ? cs.no_number & cs.seen[node] : 0;
+        for (int x = col0; x < col1; x += 16) {
+          uint32_t o[16];
+          tmem_ld16_async(lanes + kColO + x, o);
+          tmem_wait16(o);
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * inv;
+          for (unsigned long long q = none; q != 0; q &= q - 1) {  // values of the node's path that are no numbers
+            const uint16_t* v = static_cast<const uint16_t*>(a.v) + (static_cast<int64_t>(g.lo) + __ffsll(q) - 1) * a.v_stride +
+                                static_cast<int64_t>(g.h) * d + x;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if ((v[i] & 0x7f80) == 0x7f80) y[i] = NAN;
+          }
+          uint32_t u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          const uint4 u0 = make_uint4(u[0], u[1], u[2], u[3]), u1 = make_uint4(u[4], u[5], u[6], u[7]);
+          if (!whole) {
+            if (!write) continue;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(po + x + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          } else if (!kSmall && p.wide_o) {  // by way of the queries' place, so that rows are written as such
+            unsigned char* to = smem + row * (NH * 256);
+            *reinterpret_cast<uint4*>(to + (((x >> 3) ^ (row & 7)) << 4)) = u0;
+            *reinterpret_cast<uint4*>(to + (((x >> 3) + 1 ^ (row & 7)) << 4)) = u1;
+          } else if (!write) {
+            continue;
+          } else if (p.wide_o) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + out + x);
+            to[0] = u0;
+            to[1] = u1;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) static_cast<__nv_bfloat16*>(a.o)[out + x + i] = __float2bfloat16_rn(y[i]);
+          }
+        }
+        if (write && !whole && hf == 0) p.part_lse[piece * p.rows_cap + row] = m + log2f(sum);
+        tc_fence_before_sync();
+      }
+      if (!kSmall && whole && p.wide_o) {
+        all_sync();
+        if (ok && !bad) {
+          for (int i = warp; i < rows; i += kSoftWarps) {
+            const int rr = row0 + i, at = rr / G;
+            uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) +
+                                                 ((static_cast<int64_t>(g.lo) + at) * a.Hq + g.h * G + rr - at * G) * d);
+            if (8 * lane < d) to[lane] = *reinterpret_cast<const uint4*>(smem + i * (NH * 256) + ((lane ^ (i & 7)) << 4));
+          }
+        }
       }
       if (ok) {
-        if (alive) {
-          const float inv = 1.f / sum;
-          const int node = (row0 + row) / G, head = g.h * G + (row0 + row) % G;
-          const int64_t out = ((static_cast<int64_t>(g.lo) + node) * a.Hq + head) * d;
-          const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
-          float* po = p.part_o + (piece * p.rows_cap + row) * d;
-          const bool write = row < rows && !bad;
-          const unsigned long long none = g.t0 == 0 && write ? cs.no_number & cs.seen[node] : 0;
-          for (int x = col0; x < col1; x += 16) {
-            uint32_t o[16];
-            tmem_ld16_async(lanes + kColO + x, o);
-            tmem_wait16(o);
-            float y[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * inv;
-            for (unsigned long long q = none; q != 0; q &= q - 1) {  // values of the node's path that are no numbers
-              const uint16_t* v = static_cast<const uint16_t*>(a.v) + (static_cast<int64_t>(g.lo) + __ffsll(q) - 1) * a.v_stride +
-                                  static_cast<int64_t>(g.h) * d + x;
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if ((v[i] & 0x7f80) == 0x7f80) y[i] = NAN;
-            }
-            if (!write) continue;
-            if (!whole) {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(po + x + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-            } else if (p.wide_o) {
-              uint32_t u[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-                u[i] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-              uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + out + x);
-              to[0] = make_uint4(u[0], u[1], u[2], u[3]);
-              to[1] = make_uint4(u[4], u[5], u[6], u[7]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) static_cast<__nv_bfloat16*>(a.o)[out + x + i] = __float2bfloat16_rn(y[i]);
-            }
-          }
-          if (write && !whole && hf == 0) p.part_lse[piece * p.rows_cap + row] = m + log2f(sum);
-          tc_fence_before_sync();
-        }
         if (t == 0 && bad) atomicOr(a.status + g.r, bad_bit);
         if (t == 0 && !whole) {
           if (g.t0 == 0) {
             // the piece in which the item's last tile lies
-            const int64_t last = walk.u + (g.tiles - g.t1) - 1;
+            const int64_t last = static_cast<int64_t>(walk.u) + (g.tiles - g.t1) - 1;
             int* rec = p.record + 8 * blockIdx.x;
             rec[1] = static_cast<int>(((last + 1) * pieces - 1) / total);
             rec[2] = g.r, rec[3] = g.h, rec[4] = g.m, rec[5] = rows;
@@ -799,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (cs.fail != 0) {
     if (t == 0) {  // some of these may be written
       walk = begin;
-      while (walk.next(p, base, g)) atomicOr(a.status + g.r, TREEWY_STATUS_TIMEOUT);
+      while (walk.next(p, cs, g)) atomicOr(a.status + g.r, TREEWY_STATUS_TIMEOUT);
     }
     // copies and products in flight end before the CTA does (a draft's tile among these may never be filled)
     if (warp == kLoadWarp) {
@@ -879,7 +987,8 @@ int row_tiles_of(const treewy_attn& a) {
 // context, or too few items to fill the SMs several times over.
 bool listed(const treewy_attn& a) {
   const int mt = row_tiles_of(a);
-  return a.R <= kMaxListed && (mt == 1 || static_cast<int64_t>(a.R) * a.cache.Hkv * mt <= 4 * kMaxPieces);
+  const int64_t items = static_cast<int64_t>(a.R) * a.cache.Hkv * mt;
+  return a.R <= kMaxListed && (mt == 1 || items <= 4 * kMaxPieces) && items * (2 + a.max_context / kTile) < (int64_t(1) << 31);
 }
 int rows_cap(const treewy_attn& a) {
   return static_cast<int>(std::min<int64_t>(kTile, static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv)));
@@ -897,14 +1006,14 @@ bool make_map(CUtensorMap* map, const void* codes, const treewy_cache& c) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NH, int QR>
+template <int NH, bool kSmall>
 cudaError_t launch(const Params& p, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(attend_tc_kernel<NH, QR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NH, QR>::kBytes);
+    return cudaFuncSetAttribute(attend_tc_kernel<NH, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NH, kSmall>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  return launch_after_smem(attend_tc_kernel<NH, QR>, dim3(grid), kThreads, Shape<NH, QR>::kBytes, stream, p, k, v);
+  return launch_after_smem(attend_tc_kernel<NH, kSmall>, dim3(grid), kThreads, Shape<NH, kSmall>::kBytes, stream, p, k, v);
 }
 
 }  // namespace
@@ -953,8 +1062,8 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
   if (c.num_pages == 0) c.num_pages = 1, c.k = c.v = const_cast<void*>(a.q);
   if (!make_map(&k, c.k, c) || !make_map(&v, c.v, c)) return cudaErrorUnknown;
   const bool two = a.cache.d > 128, small = static_cast<int64_t>(a.max_nodes) * p.G <= 32;
-  cudaError_t e = two ? (small ? launch<2, 32>(p, k, v, grid, stream) : launch<2, 128>(p, k, v, grid, stream))
-                      : (small ? launch<1, 32>(p, k, v, grid, stream) : launch<1, 128>(p, k, v, grid, stream));
+  cudaError_t e = two ? (small ? launch<2, true>(p, k, v, grid, stream) : launch<2, false>(p, k, v, grid, stream))
+                      : (small ? launch<1, true>(p, k, v, grid, stream) : launch<1, false>(p, k, v, grid, stream));
   if (e != cudaSuccess || !p.listed) return e;
   return launch_after(attend_join_kernel, dim3(p.rows_cap, grid), 256, stream, p);
 }
