@@ -1,0 +1,450 @@
+// attend_few.cu -- attention over pages of e4m3 keys and values and the
+// draft's own ones on the 5th-generation tensor cores, as attend_tc.cu, for
+// drafts of at most 32 rows (nodes times query heads of a key head): single
+// tokens and chains.
+//
+// Such a call reads its context at the rate of HBM or should.  Rows of 128
+// would be mostly empty, so the tile lies on its side: TMEM lanes are tokens,
+// and the columns are rows, hi and lo terms side by side:
+//
+//   S^T = K Q^T     M = 128 tokens, N = 2 NR, from the page as it is
+//   w               a thread has one token of NR / 2 rows; their terms go to
+//                   shared memory, a byte each
+//   O^T += V^T w^T  M = 128 columns of the head (V's rows run along the sum)
+//
+// A product of N = 16 takes an eighth of the time of one of 128, and the
+// softmax of a tile is spread over all 256 threads.
+//
+// The draft's keys and values are the terms' rows 0 .. 31 (hi) and 64 .. 95
+// (lo) of a tile: the keys' products are added up in S^T, and the weights of
+// the first quarter of the lanes stand for both tokens of a value.
+//
+//   warps 0-7   queries and draft to e4m3; softmax; outputs
+//   warp 8      page table, scales and pages (TMA)
+//   warp 9      issues the products: S of the next tile before O of this one
+#include "attend_tc.cuh"
+
+namespace treewy {
+namespace {
+
+constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 1;
+constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
+constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;
+
+// NH: halves of 128 columns of a head; NR: rows, 8, 16 or 32.
+template <int NH, int NR>
+struct Shape {
+  static constexpr uint32_t kRowBytes = 2 * NR * 128;                // hi and lo rows of 128 bytes
+  static constexpr uint32_t kWBytes = 2 * kRowBytes;                 // weights of two tiles
+  static constexpr uint32_t kQBytes = NH * kRowBytes;
+  static constexpr uint32_t kStage = 2 * NH * kHalf;                 // K, then V
+  static constexpr int kStages = NH == 2 ? (NR == 32 ? 2 : 3) : (NR == 32 ? 5 : 6);
+  static constexpr uint32_t kBytes = kWBytes + kQBytes + kStages * kStage + 1024;
+};
+
+template <int S>
+struct FewSmem {
+  RingSmem<S> ring;
+  uint64_t sfull[2], pready[2], pvdone[2], qready, drain;
+  alignas(16) float top[2][4][kFewRows];  // maxima (and sums) of the quarters of rows; two sets in turn
+  uint32_t seen[kFewRows];      // the nodes that a row sees
+  uint32_t tmem;
+  DraftSmem draft;
+  PlanSmem plan;
+};
+
+// N TMEM columns of this thread's lane; complete after ld_wait.
+template <int N>
+__device__ __forceinline__ void ld_cols(uint32_t at, uint32_t* r) {
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+  } else if constexpr (N == 8) {
+    tmem_ld8_async(at, *reinterpret_cast<uint32_t(*)[8]>(r));
+  } else {
+    tmem_ld16_async(at, *reinterpret_cast<uint32_t(*)[16]>(r));
+  }
+}
+template <int N>
+__device__ __forceinline__ void ld_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+template <int N>
+__device__ __forceinline__ void st_cols(uint32_t at, const uint32_t* r) {
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+  } else if constexpr (N == 8) {
+    tmem_st8(at, r);
+  } else {
+    tmem_st16(at, r);
+  }
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int NH, int NR>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_few_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+  using Sh = Shape<NH, NR>;
+  constexpr int S = Sh::kStages, NT = NR / 2;  // rows of a thread
+  extern __shared__ unsigned char raw_smem[];
+  __shared__ FewSmem<S> cs;
+  RingSmem<S>& rs = cs.ring;
+  DraftSmem& ds = cs.draft;
+  unsigned char* wts = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  unsigned char* qs = wts + Sh::kWBytes;
+  unsigned char* ring = qs + Sh::kQBytes;
+  const treewy_attn& a = p.a;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, d = a.cache.d, G = p.G;
+
+  // ---- set-up, while the kernel before may still run
+  if (t == 0) {
+    init_ring(rs);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&cs.sfull[i], 1);
+      mbar_init(&cs.pready[i], kSoftWarps);
+      mbar_init(&cs.pvdone[i], 1);
+    }
+    mbar_init(&cs.qready, 1);
+    mbar_init(&cs.drain, 1);
+    fence_mbarrier_init();
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&cs.tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  after_previous();
+  const Part mine = make_plan<kThreads>(p, cs.plan, rs);
+  const uint32_t tmem = cs.tmem;
+
+  Walk walk = mine.walk;
+  Segment g;
+  int2 armed = make_int2(0, 0);
+  int gt = 0;  // tiles so far
+
+  if (warp == kLoadWarp) {
+    armed = load_pages<NH, S>(p, cs, rs, walk, ring, kmap, vmap);
+  } else if (warp == kMmaWarp) {
+    // ---- products
+    const uint32_t id_s = idesc_f8(2 * NR, false, false), id_o = idesc_f8(2 * NR, true, false);
+    const uint32_t q0 = smem_addr(qs), r0 = smem_addr(ring), w0 = smem_addr(wts);
+    int seg = 0;
+    bool ok = true;
+#pragma unroll 1
+    while (ok && walk.next(p, cs.plan, g)) {
+      ok = wait_warp(rs, &cs.qready, seg & 1);
+      ++seg;
+      // S of the next tile, then O of the last
+#pragma unroll 1
+      for (int j = g.t0 - 1; ok && j < g.t1; ++j) {
+        if (j + 1 < g.t1) {
+          const int tile = gt + (j >= g.t0 ? 1 : 0), slot = tile % S;
+          ok = wait_warp(rs, &rs.kfull[slot], (tile / S) & 1);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+            const uint32_t s = tmem + kColS + (tile & 1) * (2 * NR);
+            uint32_t acc = 0, k0 = r0 + slot * Sh::kStage;
+#pragma unroll 1
+            for (int term = 0; term < (j + 1 == 0 ? 2 : 1); ++term, k0 += 64 * 128) {  // the draft's lo rows
+#pragma unroll
+              for (int x = 0; x < NH; ++x) {
+                const int steps = (min(128, d - 128 * x) + 31) / 32;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (k >= steps) continue;
+                  mma_f8(s, smem_desc_sw128(k0 + x * kHalf + k * 32, 1024), smem_desc_sw128(q0 + x * Sh::kRowBytes + k * 32, 1024), id_s, acc);
+                  acc = 1;
+                }
+              }
+            }
+            mma_commit(&cs.sfull[tile & 1]);
+            mma_commit(&rs.kfree[slot]);
+          }
+          __syncwarp();
+        }
+        if (j < g.t0) continue;
+        const int slot = gt % S;
+        ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1) && wait_warp(rs, &cs.pready[gt & 1], (gt >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after_sync();
+        // 32 tokens each: the draft's are the first and the third
+        const int n = min(kTile, g.len - (j - 1) * kTile), steps = j == 0 ? 5 : (1 << ((n + 31) / 32)) - 1;
+        if (elect_one()) {
+          const uint32_t w = w0 + (gt & 1) * Sh::kRowBytes, v0 = r0 + slot * Sh::kStage + NH * kHalf;
+#pragma unroll
+          for (int x = 0; x < NH; ++x) {
+            uint32_t acc = j != g.t0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (((steps >> k) & 1) == 0) continue;
+              mma_f8(tmem + kColO + x * (2 * NR), desc_mn(v0 + x * kHalf + k * 4096), smem_desc_sw128(w + k * 32, 1024), id_o, acc);
+              acc = 1;
+            }
+          }
+          mma_commit(&rs.vfree[slot]);
+          mma_commit(&cs.pvdone[gt & 1]);
+        }
+        __syncwarp();
+        ++gt;
+      }
+    }
+  } else {
+    // ---- softmax: warps w and w + 4 have the tokens 32 (w % 4) .., each of them half of the rows
+    const int quarter = warp & 3, hf = warp >> 2, row0 = hf * NT, token = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const float factor = a.scale * 1.4426950408889634f;  // scores in powers of two
+    auto all_sync = [] { named_bar_sync<1, kSoftThreads>(); };
+#pragma unroll 1
+    while (walk.next(p, cs.plan, g)) {
+      // queries and tree
+      const int rows = g.N * G;
+      if (t == 0) ds.bad_tree = 0, ds.no_number = 0;
+      if (g.t0 == 0) wait_warp(rs, &rs.cfull[gt % S], (gt / S) & 1);  // the stage is free
+      all_sync();
+      load_tree(p, ds, g, t);
+      unsigned char* draft = ring + (gt % S) * Sh::kStage;
+      fill_rows<NH, kSoftWarps>(p, ds, g, rows, NR, factor, 32, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
+        unsigned char* tile = kind == 0 ? qs : kind == 1 ? draft : draft + NH * kHalf;
+        const uint32_t block = kind == 0 ? Sh::kRowBytes : kHalf;
+        *operand8(tile, i, ln, block) = hi;
+        *operand8(tile, i + (kind == 0 ? NR : 64), ln, block) = lo;
+      });
+      fence_proxy_async_smem();
+      all_sync();
+      if (t == 0) {
+        arrive(&cs.qready);
+        if (g.t0 == 0) {
+          arrive(&rs.kfull[gt % S]);
+          arrive(&rs.vfull[gt % S]);
+        }
+      }
+      see(ds, g, t);
+      all_sync();
+      if (t < NR) cs.seen[t] = static_cast<uint32_t>(ds.seen[min(t, rows - 1) / G]);
+
+      const bool bad_tree = ds.bad_tree != 0;
+      bool bad = bad_tree;
+      float m[NT], sum[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) m[i] = -INFINITY, sum[i] = 0.f;
+      if (g.t0 == 0) all_sync();
+#pragma unroll 1
+      for (int j = g.t0; j < g.t1; ++j, ++gt) {
+        const int slot = gt % S, b = gt & 1;
+        const Consts& cc = rs.c[slot];
+        // after a wait that gave up a warp still comes by every barrier of threads
+        bool ok = wait_warp(rs, &cs.sfull[b], (gt >> 1) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
+        tc_fence_after_sync();
+        bad |= cc.bad != 0;
+        const int n = j == 0 ? g.N : min(kTile, g.len - (j - 1) * kTile);
+        if (j != 0 && n < kTile && ok) ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1);
+        if (j != 0 && n < kTile && ok) {  // values behind the context: anything, so none
+          const int end = (n + 31) & ~31;
+          unsigned char* v = ring + slot * Sh::kStage + NH * kHalf;
+#pragma unroll 1
+          for (int i = n * 8 + t; i < end * 8; i += kSoftThreads)
+#pragma unroll
+            for (int x = 0; x < NH; ++x) *reinterpret_cast<uint4*>(v + x * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
+        }
+        uint32_t r[2 * NT];
+        if (ok) {
+          ld_cols<NT>(lanes + kColS + b * (2 * NR) + row0, r);
+          ld_cols<NT>(lanes + kColS + b * (2 * NR) + NR + row0, r + NT);
+          ld_wait<2 * NT>(r);
+        }
+        const bool draft_tile = j == 0;
+        const float ks = draft_tile ? ds.ks[lane] : cc.ks[token >> 4], lv = draft_tile ? ds.lv[lane] : cc.lv[token >> 4];
+        const float il = draft_tile ? (token < n ? ds.il[lane] : 0.f) : cc.il[token >> 4];
+        float s[NT], top[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float x = __uint_as_float(r[i]) + __uint_as_float(r[NT + i]);
+          const float y = fmaf(x, fmaxf(ks * ds.rowf[row0 + i], kLeast), lv);
+          const bool live = token < n && (!draft_tile || ((cs.seen[row0 + i] >> lane) & 1));
+          s[i] = live ? y : -INFINITY;
+          top[i] = warp_max(s[i]);
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < NT; i += 4) *reinterpret_cast<float4*>(&cs.top[b][quarter][row0 + i]) = make_float4(top[i], top[i + 1], top[i + 2], top[i + 3]);
+        }
+        all_sync();
+        bool grown = false;
+        float down[NT];
+#pragma unroll
+        for (int i = 0; i < NT; i += 4) {
+          float4 x = *reinterpret_cast<const float4*>(&cs.top[b][0][row0 + i]);
+#pragma unroll
+          for (int q = 1; q < 4; ++q) {
+            const float4 y = *reinterpret_cast<const float4*>(&cs.top[b][q][row0 + i]);
+            x = make_float4(fmaxf(x.x, y.x), fmaxf(x.y, y.y), fmaxf(x.z, y.z), fmaxf(x.w, y.w));
+          }
+          const float z[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool more = j == g.t0 || z[e] > m[i + e] + kGrowth;
+            down[i + e] = 1.f;
+            if (more) {
+              down[i + e] = ex2(m[i + e] - z[e]);
+              m[i + e] = z[e];
+              grown = true;
+            }
+          }
+        }
+        if (grown && j != g.t0) {  // the same in all warps that have these rows
+          wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int x = 0; x < 2 * NH; ++x) {  // halves of the head's columns, terms
+            uint32_t o[NT];
+            ld_cols<NT>(lanes + kColO + x * NR + row0, o);
+            ld_wait<NT>(o);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * down[i]);
+            st_cols<NT>(lanes + kColO + x * NR + row0, o);
+          }
+          tmem_wait_st();
+#pragma unroll
+          for (int i = 0; i < NT; ++i) sum[i] *= down[i];
+        }
+        unsigned char* w = wts + b * Sh::kRowBytes;
+#pragma unroll
+        for (int i = 0; i < NT; i += 2) {
+          const float w0 = ex2(s[i] + (kBias - m[i])), w1 = ex2(s[i + 1] + (kBias - m[i + 1]));
+          sum[i] = fmaf(w0, il, sum[i]);
+          sum[i + 1] = fmaf(w1, il, sum[i + 1]);
+          uint32_t hi, lo;
+          weight_terms(w0, w1, hi, lo);
+          if (!draft_tile || quarter == 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = row0 + i + e;
+              unsigned char* at = w + row * 128 + (((token >> 4) ^ (row & 7)) << 4) + (token & 15);
+              at[0] = static_cast<unsigned char>(hi >> (8 * e));
+              at[NR * 128] = static_cast<unsigned char>(lo >> (8 * e));
+              if (draft_tile) {  // a value's two terms have one weight
+                at = w + row * 128 + ((((token + 64) >> 4) ^ (row & 7)) << 4) + (token & 15);
+                at[0] = static_cast<unsigned char>(hi >> (8 * e));
+                at[NR * 128] = static_cast<unsigned char>(lo >> (8 * e));
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        warp_arrive(&cs.pready[b]);
+      }
+
+      // ---- outputs
+      const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+      const bool ok = wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
+      tc_fence_after_sync();
+      // not the set of the last tile, which another warp may still read
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(kFull, sum[i], o);
+        if (lane == 0) cs.top[gt & 1][quarter][row0 + i] = sum[i];
+      }
+      all_sync();
+      if (ok && !bad) {
+        const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          sum[i] = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sum[i] += cs.top[gt & 1][q][row0 + i];
+        }
+#pragma unroll 1
+        for (int x = 0; x < NH; ++x) {
+          uint32_t o[2 * NT];
+          ld_cols<NT>(lanes + kColO + x * (2 * NR) + row0, o);
+          ld_cols<NT>(lanes + kColO + x * (2 * NR) + NR + row0, o + NT);
+          ld_wait<2 * NT>(o);
+          const int col = x * 128 + token;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const int row = row0 + i, node = row / G;
+            if (row >= rows || col >= d) continue;
+            float y = (__uint_as_float(o[i]) + __uint_as_float(o[NT + i])) * (1.f / sum[i]);
+            if (g.t0 == 0 && ds.no_number != 0) {  // values of the node's path that are no numbers
+              for (unsigned long long q = ds.no_number & ds.seen[node]; q != 0; q &= q - 1) {
+                const uint16_t v = static_cast<const uint16_t*>(a.v)[(static_cast<int64_t>(g.lo) + __ffsll(q) - 1) * a.v_stride +
+                                                                    static_cast<int64_t>(g.h) * d + col];
+                if ((v & 0x7f80) == 0x7f80) y = NAN;
+              }
+            }
+            if (whole)
+              static_cast<__nv_bfloat16*>(a.o)[((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + row - node * G) * d + col] =
+                  __float2bfloat16_rn(y);
+            else
+              p.part_o[(piece * p.rows_cap + row) * d + col] = y;
+          }
+        }
+        if (!whole && quarter == 0 && lane == 0) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            if (row0 + i < rows) p.part_lse[piece * p.rows_cap + row0 + i] = m[i] + log2f(sum[i]);
+        }
+        tc_fence_before_sync();
+      }
+      if (ok && t == 0) report(p, mine, walk, g, rows, bad_tree, bad);
+    }
+  }
+
+  __syncthreads();
+  if (rs.fail != 0) {
+    if (t == 0) {  // some of these may be written
+      walk = mine.walk;
+      while (walk.next(p, cs.plan, g)) atomicOr(a.status + g.r, TREEWY_STATUS_TIMEOUT);
+    }
+    if (warp == kLoadWarp) drain_copies(rs, armed);
+    if (warp == kMmaWarp) {
+      if (elect_one()) mma_commit(&cs.drain);
+      __syncwarp();
+      mbar_wait_for(&cs.drain, 0, 100000000ull);
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int NH, int NR>
+cudaError_t launch(const Params& p, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(attend_few_kernel<NH, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NH, NR>::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_after_smem(attend_few_kernel<NH, NR>, dim3(grid), kThreads, Shape<NH, NR>::kBytes, stream, p, k, v);
+}
+
+template <int NH>
+cudaError_t by_rows(const Params& p, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, cudaStream_t stream) {
+  const int rows = p.a.max_nodes * p.G;
+  return rows <= 8 ? launch<NH, 8>(p, k, v, grid, stream) : rows <= 16 ? launch<NH, 16>(p, k, v, grid, stream) : launch<NH, 32>(p, k, v, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_few(const Params& p, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, cudaStream_t stream) {
+  return p.a.cache.d > 128 ? by_rows<2>(p, k, v, grid, stream) : by_rows<1>(p, k, v, grid, stream);
+}
+
+}  // namespace treewy

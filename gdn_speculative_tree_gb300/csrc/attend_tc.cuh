@@ -1,0 +1,570 @@
+// attend_tc.cuh -- what the tensor-core kernels of treewy_attend share: e4m3
+// operands and their terms, the plan of the work, and the loading warp.
+//
+// The pages are the products' operands as they are: an e4m3 operand costs no
+// conversion, and an f32 or bf16 one becomes two e4m3 terms x = hi + lo.  hi
+// has four significant bits, lo the next four and a sign, so that a bf16 value
+// in units of its row's power of two is exact but for the smallest of the row.
+// Both terms' products go into f32 at twice the rate of one product in bf16.
+//
+// A tile is 128 tokens.  The weights of the softmax are
+//
+//   w = 2^(s + log2(the page's value scale) - m + 5)
+//
+// with one reference m per row for the running maximum of s + log2(scale): they
+// have the size of what they contribute, however far the pages' scales lie
+// apart.  m follows the maximum only when that has grown by more than 2^3 (the
+// output and the sum are then brought down): weights stay within 2^8, and
+// their terms' last step, 2^-9, within 2^-14 of the row's largest weight.
+//
+// Work: the items (request, key head, 128 rows at most) are runs of tiles, the
+// draft's own keys first; all runs in a row are cut into equal pieces, one for
+// each CTA, and an item that lies in several pieces is joined by
+// attend_join_kernel.  Many items of several row tiles each go to a CTA apiece
+// instead, the row tiles of one context side by side, so that L2 serves it to
+// all of them.
+#pragma once
+#include "cache_device.cuh"
+#include "treewy_internal.h"
+
+namespace treewy {
+
+constexpr int kTile = 128;                      // tokens, and rows at most
+constexpr int kGroups = kTile / 16;             // the smallest page is 16 tokens
+constexpr int kMaxListed = 768;                 // requests whose tiles are put in a row
+constexpr int kMaxPieces = 152;                 // CTAs that share the row
+constexpr float kGrowth = 3.f, kBias = 5.f;     // 2^(kGrowth + kBias) <= 448
+constexpr float kLeast = 1e-37f;                // of a score's factor: -inf times it stays -inf
+constexpr uint32_t kHalf = 128 * 128;           // bytes of 128 rows of 128
+constexpr unsigned kFull = 0xffffffffu;
+
+struct Consts {
+  float ks[kGroups], lv[kGroups], il[kGroups];  // key scale, log2 of the value scale, 1 / value scale
+  int bad;
+};
+
+// What every request, or the CTA's own one, brings.
+struct PlanSmem {
+  int scan[32];
+  int base[kMaxListed + 1], lo[kMaxListed], len[kMaxListed];  // tiles before it, rows, context
+  uint8_t nodes[kMaxListed];
+};
+
+template <int S>
+struct RingSmem {
+  Consts c[S];
+  uint64_t kfull[S], kfree[S], vfull[S], vfree[S], cfull[S];
+  uint64_t deadline;
+  int fail;
+};
+
+// The draft of the CTA's item.
+struct DraftSmem {
+  unsigned long long seen[kMaxNodes];  // the nodes that a node sees
+  unsigned long long no_number;        // nodes with a value that is none
+  float rowf[kTile];                   // a row's unit of the queries, times the scores' factor
+  float ks[kMaxNodes], lv[kMaxNodes], il[kMaxNodes];
+  int parent[kMaxNodes];
+  int bad_tree;
+};
+
+// A bounded wait: every wait of the CTA gives up at the same time.
+template <typename Smem>
+__device__ __forceinline__ bool wait(Smem& s, uint64_t* bar, uint32_t parity) {
+  while (!mbar_try_wait(bar, parity & 1u)) {
+    if (*reinterpret_cast<volatile int*>(&s.fail) != 0 || globaltimer_ns() > s.deadline) {
+      *reinterpret_cast<volatile int*>(&s.fail) = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// The same for a converged warp, whose lanes agree.
+template <typename Smem>
+__device__ __forceinline__ bool wait_warp(Smem& s, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(s, bar, parity));
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(bar);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// e4m3 x e4m3 -> f32, A in shared memory or in TMEM (four codes per column).
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A, B e4m3 (0), D f32, M = 128; `a_mn`, `b_mn`: the operand's rows run along the sum.
+__device__ __forceinline__ uint32_t idesc_f8(uint32_t N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | (8u << 24);
+}
+// V: rows of 128 bytes along the sum, 128-byte swizzle, blocks of 128 columns kHalf bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  uint64_t d = smem_desc_sw128(addr, 1024);
+  d &= ~(static_cast<uint64_t>(0x3FFFu) << 16);
+  return d | (static_cast<uint64_t>(kHalf >> 4) << 16);
+}
+
+// 32 TMEM columns of this thread's lane; complete after tmem_wait32.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::
+          "r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+// Eight values of a row of d bf16 at column c (zeros behind d).
+// (one by one where rows do not start on 16 bytes)
+static __device__ __noinline__ uint4 load_row8_odd(const uint16_t* row, int c, int d) {
+  uint32_t u[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    u[e] = (c + 2 * e < d ? __ldg(row + c + 2 * e) : 0u) | (c + 2 * e + 1 < d ? static_cast<uint32_t>(__ldg(row + c + 2 * e + 1)) << 16 : 0u);
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ uint4 load_row8(const uint16_t* row, int c, int d, bool wide) {
+  if (!wide) return load_row8_odd(row, c, d);
+  return c < d ? __ldg(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
+}
+
+// Two values in f16 as hi + lo: hi the four leading bits, lo the next.
+__device__ __forceinline__ void split_f16x2(uint32_t h, uint32_t& hi, uint32_t& lo) {
+  const uint32_t top = (h + 0x00400040u) & 0xff80ff80u;  // half a unit of the fourth bit up, the rest off
+  uint32_t rest;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(top));
+  hi = e4m3x2_of_f16x2(top);
+  lo = e4m3x2_of_f16x2(rest);
+}
+
+// Two weights as hi + lo: f16 first, of which hi has the four leading bits and
+// lo the rest, rounded (2^-8 of the weight in all, 2^-9 where hi leaves e4m3's
+// normal range).
+__device__ __forceinline__ void weight_terms(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+  split_f16x2(h, hi, lo);
+}
+
+// The largest of a row's |bf16|, by one warp (lane: eight of them).
+__device__ __forceinline__ uint32_t row_largest(const uint4& x) {
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  return __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+}
+// What is not finite out of eight values; its places (all bits of a value).
+static __device__ __noinline__ void take_out(uint4& x, uint4& bad) {
+  auto one = [](uint32_t& u) {
+    const uint32_t b = ((u & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((u & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+    u &= ~b;
+    return b;
+  };
+  bad = make_uint4(one(x.x), one(x.y), one(x.z), one(x.w));
+}
+
+// A row's terms, by one warp (lane: eight columns, as bf16): codes of
+// x 2^(7 - E), 2^E the largest exponent of the row, and the unit 2^(E - 7).
+// What is not finite becomes NaN, or zero where `clear`; `none`: there is some.
+__device__ __forceinline__ float row_terms(uint4 x, bool clear, uint2& hi, uint2& lo, bool& none) {
+  uint32_t top = row_largest(x);
+  uint4 bad = make_uint4(0, 0, 0, 0);
+  none = top >= 0x7f80u;
+  if (none) {
+    take_out(x, bad);
+    top = row_largest(x);
+  }
+  const int E = max(static_cast<int>(top >> 7) - 127, -100);
+  const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - E) << 23);
+  uint32_t h[4], l[4];
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, b[4] = {bad.x, bad.y, bad.z, bad.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(__uint_as_float(u[e] & 0xffff0000u) * f), "f"(__uint_as_float(u[e] << 16) * f));
+    split_f16x2(y, h[e], l[e]);
+    if (!clear) h[e] |= (b[e] & 0x7fu) | ((b[e] >> 8) & 0x7f00u);
+  }
+  hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+  return __uint_as_float(static_cast<uint32_t>(127 - 7 + E) << 23);
+}
+
+// Columns 8 lane .. 8 lane + 7 of row `row` of an operand of 128-byte rows
+// (128-byte swizzle), blocks of 128 columns `block` bytes apart.
+__device__ __forceinline__ uint2* operand8(unsigned char* tile, int row, int lane, uint32_t block) {
+  return reinterpret_cast<uint2*>(tile + (lane >> 4) * block + row * 128 + (((lane & 15) >> 1) ^ (row & 7)) * 16 + (lane & 1) * 8);
+}
+
+struct Params {
+  treewy_attn a;
+  int G, tiles_m;        // query heads per key head; row tiles of the largest draft
+  int listed;            // tiles in a row (1) or an item per CTA (0)
+  int rows_cap;          // rows of a partial result
+  int wide_q, wide_k, wide_v, wide_o;  // rows start on 16 bytes
+  float* part_o;         // [kMaxPieces][2][rows_cap][d]
+  float* part_lse;       // [kMaxPieces][2][rows_cap]
+  int* record;           // [kMaxPieces][8]: the item that begins in a piece and ends in a later one
+  int* part_bad;         // [kMaxPieces][2]
+};
+
+// The tiles of one item that a CTA takes.
+struct Segment {
+  int r, h, m, t0, t1, tiles;
+  int lo, N, len;
+};
+
+__device__ __forceinline__ int tiles_of(int len) { return 1 + (len + kTile - 1) / kTile; }
+__device__ __forceinline__ int row_tiles(const Params& p, int N) { return (N * p.G + kTile - 1) / kTile; }
+
+// Walks a CTA's segments; every role walks them for itself.
+struct Walk {
+  int u, end, r;
+  __device__ bool next(const Params& p, const PlanSmem& cs, Segment& s) {
+    if (u >= end) return false;
+    int k = 0;
+    if (p.listed) {
+      while (cs.base[r + 1] <= u) ++r;
+      k = s.r = r;
+    } else {
+      s.r = static_cast<int>(blockIdx.x / (p.a.cache.Hkv * p.tiles_m));
+    }
+    s.lo = cs.lo[k], s.N = cs.nodes[k], s.len = cs.len[k], s.tiles = tiles_of(s.len);
+    if (p.listed) {
+      const int in = u - cs.base[r], item = in / s.tiles, mt = row_tiles(p, s.N);
+      s.h = item / mt, s.m = item % mt, s.t0 = in % s.tiles, s.t1 = min(s.tiles, s.t0 + (end - u));
+    } else {
+      const int item = static_cast<int>(blockIdx.x % (p.a.cache.Hkv * p.tiles_m));
+      s.h = item / p.tiles_m, s.m = item % p.tiles_m, s.t0 = 0, s.t1 = s.tiles;
+    }
+    u += s.t1 - s.t0;
+    return true;
+  }
+};
+
+
+// Where a CTA's part begins and ends.
+struct Part {
+  Walk walk;
+  int total, pieces;
+};
+
+// All threads call it (THREADS of them, after the barriers' set-up); ends with
+// a __syncthreads.
+template <int THREADS, int S>
+__device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSmem<S>& ring) {
+  const treewy_attn& a = p.a;
+  const treewy_cache& c = a.cache;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  Part part = {{0, 0, 0}, 1, 1};
+  if (p.listed) {
+    int carry = 0;
+    if (t == 0) cs.base[0] = 0;
+#pragma unroll 1
+    for (int r0 = 0; r0 < a.R; r0 += THREADS) {
+      const int r = r0 + t;
+      int v = 0;
+      if (r < a.R) {
+        const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
+        if (q.err != 0 && blockIdx.x == 0) atomicOr(a.status + r, q.err);
+        cs.lo[r] = q.lo, cs.nodes[r] = static_cast<uint8_t>(q.N), cs.len[r] = q.len;
+        v = q.N == 0 ? 0 : c.Hkv * row_tiles(p, q.N) * tiles_of(q.len);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += y;
+      }
+      if (lane == 31) cs.scan[warp] = v;
+      __syncthreads();
+      int before = carry;
+#pragma unroll 1
+      for (int w = 0; w < THREADS / 32; ++w) {
+        const int x = cs.scan[w];
+        if (w < warp) before += x;
+        carry += x;
+      }
+      if (r < a.R) cs.base[r + 1] = before + v;
+      __syncthreads();
+    }
+    part.total = carry;
+    part.pieces = min(static_cast<int>(gridDim.x), carry);  // none of them empty
+    if (static_cast<int>(blockIdx.x) < part.pieces) {
+      part.walk.u = static_cast<int>(static_cast<int64_t>(blockIdx.x) * carry / part.pieces);
+      part.walk.end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * carry / part.pieces);
+      int lo = 0, hi = a.R;  // base[lo] <= u < base[hi]
+#pragma unroll 1
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cs.base[mid] <= part.walk.u) lo = mid;
+        else hi = mid;
+      }
+      part.walk.r = lo;
+    }
+    if (t == 0) {
+      p.record[8 * blockIdx.x] = 0;
+      p.part_bad[2 * blockIdx.x] = p.part_bad[2 * blockIdx.x + 1] = 1;
+    }
+  } else {
+    const int per = c.Hkv * p.tiles_m, r = static_cast<int>(blockIdx.x / per), item = static_cast<int>(blockIdx.x % per);
+    const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
+    if (q.err != 0 && item == 0 && t == 0) atomicOr(a.status + r, q.err);
+    if (t == 0) cs.lo[0] = q.lo, cs.nodes[0] = static_cast<uint8_t>(q.N), cs.len[0] = q.len;
+    if (item % p.tiles_m < row_tiles(p, q.N)) part.walk.end = 1;
+  }
+  if (t == 0) {  // a second, and a hundred times what a tile takes
+    ring.fail = 0;
+    ring.deadline = globaltimer_ns() + 1000000000ull +
+                    100000ull * static_cast<uint64_t>(p.listed ? part.walk.end - part.walk.u : 1 + a.max_context / kTile);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  return part;
+}
+
+// The loading warp: pages of every tile of the CTA's segments into the ring's
+// stages (K's halves of 128 columns, then V's), their scales beside them.
+// Lane i has the i-th of 32 pages of the context, and the next 32's, asked for
+// ahead.  Returns the tiles up to which copies have been started.
+template <int NH, int S, typename Cs>
+__device__ __forceinline__ int2 load_pages(const Params& p, Cs& cs, RingSmem<S>& rs, Walk walk, unsigned char* ring, const CUtensorMap& kmap,
+                                           const CUtensorMap& vmap) {
+  const treewy_cache& c = p.a.cache;
+  constexpr uint32_t kStage = 2 * NH * kHalf;
+  const int lane = threadIdx.x & 31, P = c.page_len, per = kTile / P;
+  int gt = 0;
+  int2 armed = make_int2(0, 0);
+  Segment g;
+#pragma unroll 1
+  while (walk.next(p, cs.plan, g)) {
+    const int32_t* table = c.page_table + static_cast<int64_t>(g.r) * c.max_pages;
+    const int pages = (g.len + P - 1) / P;
+    auto entry = [&](int i) { return i < pages ? __ldg(table + i) : -1; };
+    auto scale = [&](const float* x, int page) {
+      return page >= 0 && page < c.num_pages ? __ldg(x + static_cast<int64_t>(page) * c.Hkv + g.h) : 1.f;
+    };
+    int first = -1;  // page index of lane 0's
+    int page = 0, next = 0;
+    float ks = 0.f, vs = 1.f, next_ks = 0.f, next_vs = 1.f;
+#pragma unroll 1
+    for (int j = g.t0; j < g.t1; ++j, ++gt) {
+      const int slot = gt % S;
+      const uint32_t again = (gt / S + 1) & 1;
+      unsigned char* stage = ring + slot * kStage;
+      if (j == 0) {  // the draft's tile: the softmax warps fill it
+        if (gt >= S && !(wait_warp(rs, &rs.kfree[slot], again) && wait_warp(rs, &rs.vfree[slot], again))) return armed;
+        if (lane < kGroups) rs.c[slot].ks[lane] = 1.f, rs.c[slot].lv[lane] = rs.c[slot].il[lane] = 0.f;
+        if (lane == 0) rs.c[slot].bad = 0;
+        warp_arrive(&rs.cfull[slot]);
+        continue;
+      }
+      const int p0 = (j - 1) * per;  // the tile's first page
+      if (first < 0 || p0 >= first + 32) {
+        page = first < 0 ? entry(p0 + lane) : next;
+        next = entry(p0 + 32 + lane);
+        if (first < 0) next_ks = scale(c.k_scale, page), next_vs = scale(c.v_scale, page);
+        ks = next_ks, vs = next_vs;
+        first = p0;
+      }
+      const int src = p0 - first;  // the lane that has it
+      const bool mine = lane >= src && lane < src + per && first + lane < pages;
+      const bool in = page >= 0 && page < c.num_pages;
+      const unsigned load = __ballot_sync(kFull, mine && in), wanted = __ballot_sync(kFull, mine);
+      const uint32_t bytes = __popc(load) * P * 128u * NH, to = (lane - src) * P * 128;
+      const int z = page * c.Hkv + g.h;
+#pragma unroll
+      for (int value = 0; value < 2; ++value) {
+        uint64_t* full = value ? &rs.vfull[slot] : &rs.kfull[slot];
+        if (gt >= S && !wait_warp(rs, value ? &rs.vfree[slot] : &rs.kfree[slot], again)) return armed;
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        (value ? armed.y : armed.x) = gt + 1;
+        __syncwarp();
+        if (mine && in) {
+#pragma unroll
+          for (int x = 0; x < NH; ++x) tma_load_3d(stage + (value * NH + x) * kHalf + to, value ? &vmap : &kmap, full, x * 128, 0, z);
+        }
+        __syncwarp();
+      }
+      const int at = src + min(lane, kGroups - 1) * 16 / P;
+      const float gk = __shfl_sync(kFull, ks, at), gv = __shfl_sync(kFull, vs, at);
+      if (lane < kGroups) {
+        const float lv = log2f(gv);
+        rs.c[slot].ks[lane] = gk;
+        rs.c[slot].lv[lane] = lv;
+        rs.c[slot].il[lane] = ex2(-lv);
+      }
+      if (lane == 0) rs.c[slot].bad = load != wanted;
+      warp_arrive(&rs.cfull[slot]);
+      if (src == per) next_ks = scale(c.k_scale, next), next_vs = scale(c.v_scale, next);
+    }
+  }
+  return armed;
+}
+
+// At the end of a CTA whose waits have given up: what is in flight ends first
+// (a draft's tile among the last ones may never be filled).
+template <int S>
+__device__ __forceinline__ void drain_copies(RingSmem<S>& rs, int2 armed) {
+  for (int i = 0; i < S; ++i) {
+    if (armed.x > i) mbar_wait_for(&rs.kfull[(armed.x - 1 - i) % S], ((armed.x - 1 - i) / S) & 1, 20000000ull);
+    if (armed.y > i) mbar_wait_for(&rs.vfull[(armed.y - 1 - i) % S], ((armed.y - 1 - i) / S) & 1, 20000000ull);
+  }
+}
+
+// A segment's queries, and the draft's keys and values where it has them, as
+// terms: by WARPS warps, four rows each at a time.
+// place(kind, i, ..) writes row i of the queries (kind 0; zeros from `rows` to
+// `padded`), keys (1) or values (2; zeros up to zero_to).
+template <int NH, int WARPS, typename Place>
+__device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, int padded, float factor, int zero_to,
+                                          Place place) {
+  const treewy_attn& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.cache.d, G = p.G, row0 = g.m * kTile;
+  const int nodes = g.t0 == 0 ? g.N : 0, keys = padded, values = keys + nodes;  // a row's number, by kind
+  const int jobs = values + (g.t0 == 0 ? zero_to : 0);
+#pragma unroll 1
+  for (int j0 = warp; j0 < jobs; j0 += 4 * WARPS) {
+    uint4 x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + e * WARPS;
+      x[e] = make_uint4(0, 0, 0, 0);
+      const uint16_t* from = nullptr;
+      int wide = p.wide_q;
+      if (j < rows) {
+        const int rr = row0 + j, node = rr / G;
+        from = static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(g.lo) + node) * a.q_stride + static_cast<int64_t>(g.h * G + rr - node * G) * d;
+      } else if (j >= keys && j < values) {
+        from = static_cast<const uint16_t*>(a.k) + (static_cast<int64_t>(g.lo) + j - keys) * a.k_stride + static_cast<int64_t>(g.h) * d;
+        wide = p.wide_k;
+      } else if (j >= values && j < values + nodes) {
+        from = static_cast<const uint16_t*>(a.v) + (static_cast<int64_t>(g.lo) + j - values) * a.v_stride + static_cast<int64_t>(g.h) * d;
+        wide = p.wide_v;
+      }
+      if (from != nullptr) x[e] = load_row8(from, 8 * lane, d, wide);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + e * WARPS;
+      if (j >= jobs) continue;
+      const int kind = j < keys ? 0 : j < values ? 1 : 2, i = j - (kind == 0 ? 0 : kind == 1 ? keys : values);
+      uint2 hi, lo;
+      bool none;
+      // a value that is no number would reach the nodes that do not see it: weights of zero times it
+      const float unit = row_terms(x[e], kind == 2, hi, lo, none);
+      if (8 * lane < NH * 128) place(kind, i, lane, hi, lo);
+      if (lane == 0) {
+        if (kind == 0) ds.rowf[i] = unit * factor;
+        else if (kind == 1) ds.ks[i] = unit;
+        else {
+          if (none) atomicOr(&ds.no_number, 1ull << i);
+          const float lv = log2f(unit);
+          ds.lv[i] = lv;
+          ds.il[i] = ex2(-lv);
+        }
+      }
+    }
+  }
+}
+
+// Parents of the segment's nodes; who sees whom.
+__device__ __forceinline__ void load_tree(const Params& p, DraftSmem& ds, const Segment& g, int t) {
+  if (t >= g.N) return;
+  const int q = p.a.parent != nullptr ? __ldg(p.a.parent + g.lo + t) : t - 1;
+  const bool wrong = q < -1 || q >= t;
+  if (wrong) ds.bad_tree = 1;
+  ds.parent[t] = wrong ? -1 : q;
+}
+__device__ __forceinline__ void see(DraftSmem& ds, const Segment& g, int t) {
+  if (t >= g.N) return;
+  unsigned long long m = 0;
+#pragma unroll 1
+  for (int q = t; q >= 0; q = ds.parent[q]) m |= 1ull << q;
+  ds.seen[t] = m;
+}
+
+// What one thread says of a finished segment: the status, and where it is a
+// part of an item, what the joining kernel needs.
+__device__ __forceinline__ void report(const Params& p, const Part& part, const Walk& walk, const Segment& g, int rows, bool bad_tree, bool bad) {
+  if (bad) atomicOr(p.a.status + g.r, bad_tree ? TREEWY_STATUS_BAD_TREE : TREEWY_STATUS_BAD_PAGE);
+  if (g.t0 == 0 && g.t1 == g.tiles) return;
+  if (g.t0 == 0) {
+    // the piece in which the item's last tile lies
+    const int64_t last = static_cast<int64_t>(walk.u) + (g.tiles - g.t1) - 1;
+    int* rec = p.record + 8 * blockIdx.x;
+    rec[1] = static_cast<int>(((last + 1) * part.pieces - 1) / part.total);
+    rec[2] = g.r, rec[3] = g.h, rec[4] = g.m, rec[5] = rows;
+    rec[0] = 1;
+  }
+  p.part_bad[2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)] = bad;
+}
+
+template <int S>
+__device__ __forceinline__ void init_ring(RingSmem<S>& rs) {
+  for (int i = 0; i < S; ++i) {
+    mbar_init(&rs.kfull[i], 1);
+    mbar_init(&rs.kfree[i], 1);
+    mbar_init(&rs.vfull[i], 1);
+    mbar_init(&rs.vfree[i], 1);
+    mbar_init(&rs.cfull[i], 1);
+  }
+}
+
+// Drafts of at most kFewRows rows (nodes times query heads of a key head) are
+// another kernel's (attend_few.cu).
+constexpr int kFewRows = 32;
+cudaError_t launch_attend_few(const Params& p, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, cudaStream_t stream);
+
+}  // namespace treewy
