@@ -47,6 +47,7 @@ struct FewSmem {
   RingSmem<S> ring;
   uint64_t sfull[2], pready[2], pvdone[2], qready, drain;
   alignas(16) float top[2][4][kFewRows];  // maxima (and sums) of the quarters of rows; two sets in turn
+  float ref[kFewRows];          // the rows' references
   uint32_t seen[kFewRows];      // the nodes that a row sees
   uint32_t tmem;
   DraftSmem draft;
@@ -216,7 +217,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       all_sync();
       load_tree(p, ds, g, t);
       unsigned char* draft = ring + (gt % S) * Sh::kStage;
-      fill_rows<NH, kSoftWarps>(p, ds, g, rows, NR, factor, 32, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
+      zero_rows<kSoftThreads>(qs, NH, Sh::kRowBytes, rows, NR);
+      zero_rows<kSoftThreads>(qs, NH, Sh::kRowBytes, NR + rows, 2 * NR);
+      if (t >= rows && t < NR) ds.rowf[t] = 0.f;
+      if (g.t0 == 0) {  // what the draft's tile has behind its values
+        zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, g.N, 32);
+        zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, 64 + g.N, 96);
+        if (t >= g.N && t < 32) ds.ks[t] = 1.f, ds.lv[t] = ds.il[t] = 0.f;
+      }
+      fill_rows<NH, kSoftWarps, 2>(p, ds, g, rows, factor, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
         unsigned char* tile = kind == 0 ? qs : kind == 1 ? draft : draft + NH * kHalf;
         const uint32_t block = kind == 0 ? Sh::kRowBytes : kHalf;
         *operand8(tile, i, ln, block) = hi;
@@ -283,7 +292,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         all_sync();
         bool grown = false;
-        float down[NT];
 #pragma unroll
         for (int i = 0; i < NT; i += 4) {
           float4 x = *reinterpret_cast<const float4*>(&cs.top[b][0][row0 + i]);
@@ -292,33 +300,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float4 y = *reinterpret_cast<const float4*>(&cs.top[b][q][row0 + i]);
             x = make_float4(fmaxf(x.x, y.x), fmaxf(x.y, y.y), fmaxf(x.z, y.z), fmaxf(x.w, y.w));
           }
-          const float z[4] = {x.x, x.y, x.z, x.w};
+          top[i] = x.x, top[i + 1] = x.y, top[i + 2] = x.z, top[i + 3] = x.w;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool more = j == g.t0 || z[e] > m[i + e] + kGrowth;
-            down[i + e] = 1.f;
-            if (more) {
-              down[i + e] = ex2(m[i + e] - z[e]);
-              m[i + e] = z[e];
-              grown = true;
-            }
-          }
+          for (int e = 0; e < 4; ++e) grown |= top[i + e] > m[i + e] + kGrowth;
         }
-        if (grown && j != g.t0) {  // the same in all warps that have these rows
+        if (j == g.t0) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) m[i] = top[i];
+        } else if (grown) {  // the same in all warps that have these rows
           wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
           tc_fence_after_sync();
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const bool more = top[i] > m[i] + kGrowth;
+            const float down = more ? ex2(m[i] - top[i]) : 1.f;
+            if (more) m[i] = top[i];
+            sum[i] *= down;
+            top[i] = down;
+          }
 #pragma unroll 1
           for (int x = 0; x < 2 * NH; ++x) {  // halves of the head's columns, terms
             uint32_t o[NT];
             ld_cols<NT>(lanes + kColO + x * NR + row0, o);
             ld_wait<NT>(o);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * down[i]);
+            for (int i = 0; i < NT; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * top[i]);
             st_cols<NT>(lanes + kColO + x * NR + row0, o);
           }
           tmem_wait_st();
-#pragma unroll
-          for (int i = 0; i < NT; ++i) sum[i] *= down[i];
         }
         unsigned char* w = wts + b * Sh::kRowBytes;
 #pragma unroll
@@ -357,47 +366,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < NT; ++i) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(kFull, sum[i], o);
-        if (lane == 0) cs.top[gt & 1][quarter][row0 + i] = sum[i];
+        if (lane == 0) {
+          cs.top[gt & 1][quarter][row0 + i] = sum[i];
+          if (quarter == 0) cs.ref[row0 + i] = m[i];
+        }
       }
       all_sync();
       if (ok && !bad) {
+        // row by row: little code, which a CTA meets for the first time here, costs less than many loads at once
         const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          sum[i] = 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) sum[i] += cs.top[gt & 1][q][row0 + i];
-        }
+        const unsigned long long none = g.t0 == 0 ? ds.no_number : 0;
+        int node = row0 / G, head = row0 - node * G;
 #pragma unroll 1
-        for (int x = 0; x < NH; ++x) {
-          uint32_t o[2 * NT];
-          ld_cols<NT>(lanes + kColO + x * (2 * NR) + row0, o);
-          ld_cols<NT>(lanes + kColO + x * (2 * NR) + NR + row0, o + NT);
-          ld_wait<2 * NT>(o);
-          const int col = x * 128 + token;
+        for (int row = row0; row < min(rows, row0 + NT); ++row, ++head) {
+          if (head == G) head = 0, ++node;
+          float total = 0.f;
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const int row = row0 + i, node = row / G;
-            if (row >= rows || col >= d) continue;
-            float y = (__uint_as_float(o[i]) + __uint_as_float(o[NT + i])) * (1.f / sum[i]);
-            if (g.t0 == 0 && ds.no_number != 0) {  // values of the node's path that are no numbers
-              for (unsigned long long q = ds.no_number & ds.seen[node]; q != 0; q &= q - 1) {
+          for (int q = 0; q < 4; ++q) total += cs.top[gt & 1][q][row];
+          const float inv = 1.f / total;
+          const int64_t out = ((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + head) * d;
+          uint32_t o[2 * NH];
+#pragma unroll
+          for (int x = 0; x < 2 * NH; ++x)
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o[x]) : "r"(lanes + kColO + x * NR + row) : "memory");
+          ld_wait<2 * NH>(o);
+#pragma unroll
+          for (int x = 0; x < NH; ++x) {
+            const int col = x * 128 + token;
+            float y = (__uint_as_float(o[2 * x]) + __uint_as_float(o[2 * x + 1])) * inv;
+            if (col >= d) continue;
+            if (none != 0) {  // values of the node's path that are no numbers
+#pragma unroll 1
+              for (unsigned long long q = none & ds.seen[node]; q != 0; q &= q - 1) {
                 const uint16_t v = static_cast<const uint16_t*>(a.v)[(static_cast<int64_t>(g.lo) + __ffsll(q) - 1) * a.v_stride +
                                                                     static_cast<int64_t>(g.h) * d + col];
                 if ((v & 0x7f80) == 0x7f80) y = NAN;
               }
             }
-            if (whole)
-              static_cast<__nv_bfloat16*>(a.o)[((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + row - node * G) * d + col] =
-                  __float2bfloat16_rn(y);
-            else
-              p.part_o[(piece * p.rows_cap + row) * d + col] = y;
+            if (whole) static_cast<__nv_bfloat16*>(a.o)[out + col] = __float2bfloat16_rn(y);
+            else p.part_o[(piece * p.rows_cap + row) * d + col] = y;
           }
-        }
-        if (!whole && quarter == 0 && lane == 0) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-            if (row0 + i < rows) p.part_lse[piece * p.rows_cap + row0 + i] = m[i] + log2f(sum[i]);
+          if (!whole && quarter == 0 && lane == 0) p.part_lse[piece * p.rows_cap + row] = cs.ref[row] + log2f(total);
         }
         tc_fence_before_sync();
       }

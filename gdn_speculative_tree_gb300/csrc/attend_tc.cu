@@ -181,7 +181,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       all_sync();
       load_tree(p, ds, g, t);
       unsigned char* draft = ring + (gt % S) * Sh::kStage;
-      fill_rows<NH, kSoftWarps>(p, ds, g, rows, rows, factor, kMaxNodes, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
+      if (g.t0 == 0) {  // what the draft's tile has behind its values
+        const int last = g.N % kNodes;
+        if (last != 0) {
+          const int at = g.N / kNodes * kCols;
+          zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, at + last, at + kNodes);
+          zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, at + kNodes + last, at + kCols);
+        }
+        zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, (g.N + kNodes - 1) / kNodes * kCols, kTile);
+        if (t >= g.N && t < kMaxNodes) ds.ks[t] = 1.f, ds.lv[t] = ds.il[t] = 0.f;
+      }
+      fill_rows<NH, kSoftWarps, 4>(p, ds, g, rows, factor, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
         unsigned char* tile = kind == 0 ? smem : kind == 1 ? draft : draft + NH * kHalf;
         const int token = i / kNodes * kCols + i % kNodes;
         *operand8(tile, kind == 0 ? i : token, ln, kHalf) = hi;
@@ -424,29 +434,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Params p) {
   after_previous();
   __shared__ float acc[8][256], wsum[8];
-  __shared__ int refused;
   const int w = blockIdx.y, row = blockIdx.x, t = threadIdx.x, warp = t >> 5, lane = t & 31, d = p.a.cache.d;
-  const int* rec = p.record + 8 * w;
-  if (rec[0] == 0 || row >= rec[5]) return;
-  const int parts = rec[1] - w + 1;
-  if (t == 0) refused = 0;
-  __syncthreads();
+  const int4 rec = *reinterpret_cast<const int4*>(p.record + 8 * w);
+  if (rec.x == 0 || row >= rec.z) return;
+  const int4 item = *reinterpret_cast<const int4*>(p.record + 8 * w + 4);
+  const int parts = rec.y - w + 1;
+  auto part_of = [&](int i) { return (2 * static_cast<int64_t>(w + i) + (i == 0 ? 1 : 0)) * p.rows_cap + row; };
   float top = -INFINITY;
-  auto piece_of = [&](int i) { return 2 * static_cast<int64_t>(w + i) + (i == 0 ? 1 : 0); };
-  for (int i = t; i < parts; i += 256)
-    if (p.part_bad[piece_of(i)] != 0) refused = 1;
-  for (int i = lane; i < parts; i += 32) {
-    const float lse = p.part_lse[piece_of(i) * p.rows_cap + row];
-    top = lse > top || lse != lse ? lse : top;
-  }
+#pragma unroll 1
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_lse[part_of(i)]);  // NaN comes by way of the weights
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+  if (top == INFINITY) return;  // a part was refused
   float sum = 0.f, y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = 0.f;
 #pragma unroll 4
   for (int i = warp; i < parts; i += 8) {
-    const int64_t at = piece_of(i) * p.rows_cap + row;
+    const int64_t at = part_of(i);
     const float f = exp2f(p.part_lse[at] - top);
     sum += f;
     if (8 * lane < d) {
@@ -460,13 +465,13 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   for (int e = 0; e < 8; ++e) acc[warp][8 * lane + e] = y[e];
   if (lane == 0) wsum[warp] = sum;
   __syncthreads();
-  if (refused || t >= d) return;
+  if (t >= d) return;
   float z = 0.f, n = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) z += acc[i][t], n += wsum[i];
-  const int rr = rec[4] * kTile + row;
-  const int64_t node = static_cast<int64_t>(__ldg(p.a.node_offset + rec[2])) + rr / p.G;
-  static_cast<__nv_bfloat16*>(p.a.o)[(node * p.a.Hq + rec[3] * p.G + rr % p.G) * d + t] = __float2bfloat16_rn(z / n);
+  const int rr = item.y * kTile + row, node = rr / p.G;
+  static_cast<__nv_bfloat16*>(p.a.o)[((static_cast<int64_t>(item.z) + node) * p.a.Hq + item.x * p.G + rr - node * p.G) * d + t] =
+      __float2bfloat16_rn(z / n);
 }
 
 int row_tiles_of(const treewy_attn& a) {
@@ -514,7 +519,7 @@ bool attend_on_tensor_cores(const treewy_attn& a) {
 
 uint64_t attend_workspace(const treewy_attn& a) {
   if (a.R == 0 || !attend_on_tensor_cores(a) || !listed(a)) return 0;
-  return static_cast<uint64_t>(kMaxPieces) * (2ull * rows_cap(a) * (a.cache.d + 1) * 4 + 8 * 4 + 2 * 4);
+  return static_cast<uint64_t>(kMaxPieces) * (2ull * rows_cap(a) * (a.cache.d + 1) * 4 + 8 * 4);
 }
 
 cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
@@ -529,9 +534,8 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
   if (p.listed) {
     const size_t rows = static_cast<size_t>(kMaxPieces) * 2 * p.rows_cap;
     p.part_o = static_cast<float*>(a.workspace);
-    p.part_lse = p.part_o + rows * a.cache.d;
-    p.record = reinterpret_cast<int*>(p.part_lse + rows);
-    p.part_bad = p.record + 8 * kMaxPieces;
+    p.record = reinterpret_cast<int*>(p.part_o + rows * a.cache.d);
+    p.part_lse = reinterpret_cast<float*>(p.record + 8 * kMaxPieces);
   }
   unsigned grid;
   if (p.listed) {

@@ -254,9 +254,8 @@ struct Params {
   int rows_cap;          // rows of a partial result
   int wide_q, wide_k, wide_v, wide_o;  // rows start on 16 bytes
   float* part_o;         // [kMaxPieces][2][rows_cap][d]
-  float* part_lse;       // [kMaxPieces][2][rows_cap]
+  float* part_lse;       // [kMaxPieces][2][rows_cap]; infinity: refused
   int* record;           // [kMaxPieces][8]: the item that begins in a piece and ends in a later one
-  int* part_bad;         // [kMaxPieces][2]
 };
 
 // The tiles of one item that a CTA takes.
@@ -297,8 +296,13 @@ struct Walk {
 // Where a CTA's part begins and ends.
 struct Part {
   Walk walk;
-  int total, pieces;
+  int each, more;  // tiles of a piece; how many pieces have one more
 };
+// The piece that a tile lies in.
+__device__ __forceinline__ int piece_of(const Part& p, int u) {
+  const int big = p.more * (p.each + 1);
+  return u < big ? u / (p.each + 1) : p.more + (u - big) / p.each;
+}
 
 // All threads call it (THREADS of them, after the barriers' set-up); ends with
 // a __syncthreads.
@@ -307,7 +311,7 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
   const treewy_attn& a = p.a;
   const treewy_cache& c = a.cache;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  Part part = {{0, 0, 0}, 1, 1};
+  Part part = {{0, 0, 0}, 1, 0};
   if (p.listed) {
     int carry = 0;
     if (t == 0) cs.base[0] = 0;
@@ -329,8 +333,9 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
       if (lane == 31) cs.scan[warp] = v;
       __syncthreads();
       int before = carry;
+      const int used = min(THREADS / 32, (a.R - r0 + 31) / 32);
 #pragma unroll 1
-      for (int w = 0; w < THREADS / 32; ++w) {
+      for (int w = 0; w < used; ++w) {
         const int x = cs.scan[w];
         if (w < warp) before += x;
         carry += x;
@@ -338,11 +343,11 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
       if (r < a.R) cs.base[r + 1] = before + v;
       __syncthreads();
     }
-    part.total = carry;
-    part.pieces = min(static_cast<int>(gridDim.x), carry);  // none of them empty
-    if (static_cast<int>(blockIdx.x) < part.pieces) {
-      part.walk.u = static_cast<int>(static_cast<int64_t>(blockIdx.x) * carry / part.pieces);
-      part.walk.end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * carry / part.pieces);
+    const int pieces = min(static_cast<int>(gridDim.x), carry), w = blockIdx.x;  // none of them empty
+    if (w < pieces) {
+      part.each = carry / pieces, part.more = carry - part.each * pieces;
+      part.walk.u = w * part.each + min(w, part.more);
+      part.walk.end = part.walk.u + part.each + (w < part.more ? 1 : 0);
       int lo = 0, hi = a.R;  // base[lo] <= u < base[hi]
 #pragma unroll 1
       while (hi - lo > 1) {
@@ -352,10 +357,10 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
       }
       part.walk.r = lo;
     }
-    if (t == 0) {
-      p.record[8 * blockIdx.x] = 0;
-      p.part_bad[2 * blockIdx.x] = p.part_bad[2 * blockIdx.x + 1] = 1;
-    }
+    // until it is written: no item begins here and ends elsewhere, and no part is any good
+    if (t == 0) p.record[8 * blockIdx.x] = 0;
+#pragma unroll 1
+    for (int i = t; i < 2 * p.rows_cap; i += THREADS) p.part_lse[2 * static_cast<int64_t>(blockIdx.x) * p.rows_cap + i] = INFINITY;
   } else {
     const int per = c.Hkv * p.tiles_m, r = static_cast<int>(blockIdx.x / per), item = static_cast<int>(blockIdx.x % per);
     const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
@@ -464,42 +469,38 @@ __device__ __forceinline__ void drain_copies(RingSmem<S>& rs, int2 armed) {
 }
 
 // A segment's queries, and the draft's keys and values where it has them, as
-// terms: by WARPS warps, four rows each at a time.
-// place(kind, i, ..) writes row i of the queries (kind 0; zeros from `rows` to
-// `padded`), keys (1) or values (2; zeros up to zero_to).
-template <int NH, int WARPS, typename Place>
-__device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, int padded, float factor, int zero_to,
-                                          Place place) {
+// terms: by WARPS warps, BATCH rows each at a time.
+// place(kind, i, ..) writes row i of the queries (kind 0), keys (1) or values (2).
+template <int NH, int WARPS, int BATCH, typename Place>
+__device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, float factor, Place place) {
   const treewy_attn& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.cache.d, G = p.G, row0 = g.m * kTile;
-  const int nodes = g.t0 == 0 ? g.N : 0, keys = padded, values = keys + nodes;  // a row's number, by kind
-  const int jobs = values + (g.t0 == 0 ? zero_to : 0);
+  const int nodes = g.t0 == 0 ? g.N : 0, values = rows + nodes, jobs = values + nodes;
 #pragma unroll 1
-  for (int j0 = warp; j0 < jobs; j0 += 4 * WARPS) {
-    uint4 x[4];
+  for (int j0 = warp; j0 < jobs; j0 += BATCH * WARPS) {
+    uint4 x[BATCH];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = j0 + e * WARPS;
-      x[e] = make_uint4(0, 0, 0, 0);
-      const uint16_t* from = nullptr;
-      int wide = p.wide_q;
-      if (j < rows) {
-        const int rr = row0 + j, node = rr / G;
-        from = static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(g.lo) + node) * a.q_stride + static_cast<int64_t>(g.h * G + rr - node * G) * d;
-      } else if (j >= keys && j < values) {
-        from = static_cast<const uint16_t*>(a.k) + (static_cast<int64_t>(g.lo) + j - keys) * a.k_stride + static_cast<int64_t>(g.h) * d;
-        wide = p.wide_k;
-      } else if (j >= values && j < values + nodes) {
-        from = static_cast<const uint16_t*>(a.v) + (static_cast<int64_t>(g.lo) + j - values) * a.v_stride + static_cast<int64_t>(g.h) * d;
-        wide = p.wide_v;
-      }
-      if (from != nullptr) x[e] = load_row8(from, 8 * lane, d, wide);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < BATCH; ++e) {
       const int j = j0 + e * WARPS;
       if (j >= jobs) continue;
-      const int kind = j < keys ? 0 : j < values ? 1 : 2, i = j - (kind == 0 ? 0 : kind == 1 ? keys : values);
+      const void* from = a.q;
+      int64_t token = g.lo, stride = a.q_stride;
+      int head, wide = p.wide_q;
+      if (j < rows) {
+        const int rr = row0 + j, node = rr / G;
+        token += node, head = g.h * G + rr - node * G;
+      } else {
+        const bool value = j >= values;
+        token += j - (value ? values : rows), head = g.h;
+        from = value ? a.v : a.k, stride = value ? a.v_stride : a.k_stride, wide = value ? p.wide_v : p.wide_k;
+      }
+      x[e] = load_row8(static_cast<const uint16_t*>(from) + token * stride + static_cast<int64_t>(head) * d, 8 * lane, d, wide);
+    }
+#pragma unroll
+    for (int e = 0; e < BATCH; ++e) {
+      const int j = j0 + e * WARPS;
+      if (j >= jobs) continue;
+      const int kind = j < rows ? 0 : j < values ? 1 : 2, i = j - (kind == 0 ? 0 : kind == 1 ? rows : values);
       uint2 hi, lo;
       bool none;
       // a value that is no number would reach the nodes that do not see it: weights of zero times it
@@ -517,6 +518,14 @@ __device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const 
       }
     }
   }
+}
+
+// Zeros in the 128-byte rows [lo, hi) of `blocks` blocks of 128 rows, by THREADS threads.
+template <int THREADS>
+__device__ __forceinline__ void zero_rows(unsigned char* tile, int blocks, uint32_t block, int lo, int hi) {
+  for (int x = 0; x < blocks; ++x)
+#pragma unroll 1
+    for (int i = lo * 8 + threadIdx.x; i < hi * 8; i += THREADS) *reinterpret_cast<uint4*>(tile + x * block + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // Parents of the segment's nodes; who sees whom.
@@ -539,16 +548,10 @@ __device__ __forceinline__ void see(DraftSmem& ds, const Segment& g, int t) {
 // part of an item, what the joining kernel needs.
 __device__ __forceinline__ void report(const Params& p, const Part& part, const Walk& walk, const Segment& g, int rows, bool bad_tree, bool bad) {
   if (bad) atomicOr(p.a.status + g.r, bad_tree ? TREEWY_STATUS_BAD_TREE : TREEWY_STATUS_BAD_PAGE);
-  if (g.t0 == 0 && g.t1 == g.tiles) return;
-  if (g.t0 == 0) {
-    // the piece in which the item's last tile lies
-    const int64_t last = static_cast<int64_t>(walk.u) + (g.tiles - g.t1) - 1;
-    int* rec = p.record + 8 * blockIdx.x;
-    rec[1] = static_cast<int>(((last + 1) * part.pieces - 1) / part.total);
-    rec[2] = g.r, rec[3] = g.h, rec[4] = g.m, rec[5] = rows;
-    rec[0] = 1;
-  }
-  p.part_bad[2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)] = bad;
+  if (g.t0 != 0 || g.t1 == g.tiles) return;
+  int4* rec = reinterpret_cast<int4*>(p.record + 8 * blockIdx.x);
+  rec[1] = make_int4(g.h, g.m, g.lo, 0);
+  rec[0] = make_int4(1, piece_of(part, walk.u + (g.tiles - g.t1) - 1), rows, 0);  // the piece of the item's last tile
 }
 
 template <int S>
