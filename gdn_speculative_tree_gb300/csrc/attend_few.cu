@@ -5,7 +5,7 @@
 //
 // Such a call reads its context at the rate of HBM or should.  Rows of 128
 // would be mostly empty, so the tile lies on its side: TMEM lanes are tokens,
-// and the columns are rows, hi and lo terms side by side:
+// and the columns are rows (of the queries, hi and lo terms side by side):
 //
 //   S^T = K Q^T     M = 128 tokens, N = 2 NR, from the page as it is
 //   w               a thread has one token of NR / 2 rows; their terms go to
@@ -20,14 +20,14 @@
 // the first quarter of the lanes stand for both tokens of a value.
 //
 //   warps 0-7   queries and draft to e4m3; softmax; outputs
-//   warp 8      page table, scales and pages (TMA)
-//   warp 9      issues the products: S of the next tile before O of this one
+//   warps 8, 9  page table, scales and pages (TMA): keys, and values
+//   warp 10     issues the products: S of the next tile before O of this one
 #include "attend_tc.cuh"
 
 namespace treewy {
 namespace {
 
-constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 1;
+constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;
 constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;
 
@@ -35,7 +35,9 @@ constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;
 template <int NH, int NR>
 struct Shape {
   static constexpr uint32_t kRowBytes = 2 * NR * 128;                // hi and lo rows of 128 bytes
-  static constexpr uint32_t kWBytes = 2 * kRowBytes;                 // weights of two tiles
+  static constexpr int kCols = NR < 16 ? 16 : NR;                    // of a product of the weights, 16 at least
+  static constexpr uint32_t kWBlock = kCols * 128;                   // a term of a tile's weights
+  static constexpr uint32_t kWBytes = 4 * kWBlock;                   // of two tiles
   static constexpr uint32_t kQBytes = NH * kRowBytes;
   static constexpr uint32_t kStage = 2 * NH * kHalf;                 // K, then V
   static constexpr int kStages = NH == 2 ? (NR == 32 ? 2 : 3) : (NR == 32 ? 5 : 6);
@@ -132,14 +134,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   Walk walk = mine.walk;
   Segment g;
-  int2 armed = make_int2(0, 0);
+  int armed = 0;
   int gt = 0;  // tiles so far
 
   if (warp == kLoadWarp) {
-    armed = load_pages<NH, S>(p, cs, rs, walk, ring, kmap, vmap);
+    armed = load_pages<false, NH, S>(p, cs, rs, walk, ring, kmap);
+  } else if (warp == kLoadWarp + 1) {
+    armed = load_pages<true, NH, S>(p, cs, rs, walk, ring, vmap);
   } else if (warp == kMmaWarp) {
     // ---- products
-    const uint32_t id_s = idesc_f8(2 * NR, false, false), id_o = idesc_f8(2 * NR, true, false);
+    const uint32_t id_s = idesc_f8(2 * NR, false, false), id_o = idesc_f8(Sh::kCols, true, false);
     const uint32_t q0 = smem_addr(qs), r0 = smem_addr(ring), w0 = smem_addr(wts);
     int seg = 0;
     bool ok = true;
@@ -184,14 +188,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 32 tokens each: the draft's are the first and the third
         const int n = min(kTile, g.len - (j - 1) * kTile), steps = j == 0 ? 5 : (1 << ((n + 31) / 32)) - 1;
         if (elect_one()) {
-          const uint32_t w = w0 + (gt & 1) * Sh::kRowBytes, v0 = r0 + slot * Sh::kStage + NH * kHalf;
+          const uint32_t w = w0 + (gt & 1) * (2 * Sh::kWBlock), v0 = r0 + slot * Sh::kStage + NH * kHalf;
 #pragma unroll
           for (int x = 0; x < NH; ++x) {
             uint32_t acc = j != g.t0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (((steps >> k) & 1) == 0) continue;
-              mma_f8(tmem + kColO + x * (2 * NR), desc_mn(v0 + x * kHalf + k * 4096), smem_desc_sw128(w + k * 32, 1024), id_o, acc);
+              const uint64_t v = desc_mn(v0 + x * kHalf + k * 4096);
+              mma_f8(tmem + kColO + x * Sh::kCols, v, smem_desc_sw128(w + k * 32, 1024), id_o | kBE5m2, acc);
+              mma_f8(tmem + kColO + x * Sh::kCols, v, smem_desc_sw128(w + Sh::kWBlock + k * 32, 1024), id_o, 1);
               acc = 1;
             }
           }
@@ -319,17 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             top[i] = down;
           }
 #pragma unroll 1
-          for (int x = 0; x < 2 * NH; ++x) {  // halves of the head's columns, terms
+          for (int x = 0; x < NH; ++x) {  // halves of the head's columns
             uint32_t o[NT];
-            ld_cols<NT>(lanes + kColO + x * NR + row0, o);
+            ld_cols<NT>(lanes + kColO + x * Sh::kCols + row0, o);
             ld_wait<NT>(o);
 #pragma unroll
             for (int i = 0; i < NT; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * top[i]);
-            st_cols<NT>(lanes + kColO + x * NR + row0, o);
+            st_cols<NT>(lanes + kColO + x * Sh::kCols + row0, o);
           }
           tmem_wait_st();
         }
-        unsigned char* w = wts + b * Sh::kRowBytes;
+        unsigned char* w = wts + b * (2 * Sh::kWBlock);
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {
           const float w0 = ex2(s[i] + (kBias - m[i])), w1 = ex2(s[i + 1] + (kBias - m[i + 1]));
@@ -342,12 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 2; ++e) {
               const int row = row0 + i + e;
               unsigned char* at = w + row * 128 + (((token >> 4) ^ (row & 7)) << 4) + (token & 15);
-              at[0] = static_cast<unsigned char>(hi >> (8 * e));
-              at[NR * 128] = static_cast<unsigned char>(lo >> (8 * e));
+              at[0] = static_cast<unsigned char>(hi >> (16 * e + 8));
+              at[Sh::kWBlock] = static_cast<unsigned char>(lo >> (8 * e));
               if (draft_tile) {  // a value's two terms have one weight
                 at = w + row * 128 + ((((token + 64) >> 4) ^ (row & 7)) << 4) + (token & 15);
-                at[0] = static_cast<unsigned char>(hi >> (8 * e));
-                at[NR * 128] = static_cast<unsigned char>(lo >> (8 * e));
+                at[0] = static_cast<unsigned char>(hi >> (16 * e + 8));
+                at[Sh::kWBlock] = static_cast<unsigned char>(lo >> (8 * e));
               }
             }
           }
@@ -385,15 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 4; ++q) total += cs.top[gt & 1][q][row];
           const float inv = 1.f / total;
           const int64_t out = ((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + head) * d;
-          uint32_t o[2 * NH];
+          uint32_t o[NH];
 #pragma unroll
-          for (int x = 0; x < 2 * NH; ++x)
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o[x]) : "r"(lanes + kColO + x * NR + row) : "memory");
-          ld_wait<2 * NH>(o);
+          for (int x = 0; x < NH; ++x)
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o[x]) : "r"(lanes + kColO + x * Sh::kCols + row) : "memory");
+          ld_wait<NH>(o);
 #pragma unroll
           for (int x = 0; x < NH; ++x) {
             const int col = x * 128 + token;
-            float y = (__uint_as_float(o[2 * x]) + __uint_as_float(o[2 * x + 1])) * inv;
+            float y = __uint_as_float(o[x]) * inv;
             if (col >= d) continue;
             if (none != 0) {  // values of the node's path that are no numbers
 #pragma unroll 1
@@ -420,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       walk = mine.walk;
       while (walk.next(p, cs.plan, g)) atomicOr(a.status + g.r, TREEWY_STATUS_TIMEOUT);
     }
-    if (warp == kLoadWarp) drain_copies(rs, armed);
+    if (warp == kLoadWarp) drain_copies(rs.kfull, armed);
+    if (warp == kLoadWarp + 1) drain_copies(rs.vfull, armed);
     if (warp == kMmaWarp) {
       if (elect_one()) mma_commit(&cs.drain);
       __syncwarp();

@@ -15,14 +15,14 @@
 // the ancestors are a mask of bits.
 //
 //   softmax warps  queries and draft to e4m3; softmax; outputs
-//   loading warp   page table, scales and pages (TMA)
+//   loading warps  page table, scales and pages (TMA): keys, and values
 //   issuing warp   the products: S of the next tile before O of this one
 #include "attend_tc.cuh"
 
 namespace treewy {
 namespace {
 
-constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 1;
+constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;
 constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kParts = kSoftWarps / 4, kCols = kTile / kParts, kNodes = kCols / 2;  // of a row, by warp
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
@@ -84,11 +84,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   Walk walk = mine.walk;
   Segment g;
-  int2 armed = make_int2(0, 0);
+  int armed = 0;
   int gt = 0;  // tiles so far
 
   if (warp == kLoadWarp) {
-    armed = load_pages<NH, S>(p, cs, rs, walk, ring, kmap, vmap);
+    armed = load_pages<false, NH, S>(p, cs, rs, walk, ring, kmap);
+  } else if (warp == kLoadWarp + 1) {
+    armed = load_pages<true, NH, S>(p, cs, rs, walk, ring, vmap);
   } else if (warp == kMmaWarp) {
     // ---- products
     const uint32_t id_s = idesc_f8(kTile, false, false), id_o = idesc_f8(d, false, true);
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b = desc_mn(v0 + k * 4096);
 #pragma unroll
             for (int term = 0; term < 2; ++term) {
-              mma_f8_ts(tmem + kColO, w + term * 32 + k * 8, b, id_o, acc);
+              mma_f8_ts(tmem + kColO, w + term * 32 + k * 8, b, term == 0 ? id_o | kAE5m2 : id_o, acc);
               acc = 1;
             }
           }
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_st();
             }
           }
-          uint32_t hi[kCols / 4], lo[kCols / 4];
+          uint32_t hi[kCols / 4], lo[kCols / 4];  // four codes each
 #pragma unroll
           for (int q = 0; q < kCols / 16; ++q) {
             const float e = cc.lv[share * (kCols / 16) + q] + (kBias - m);
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t h0, l0, h1, l1;
               weight_terms(s[4 * i], s[4 * i + 1], h0, l0);
               weight_terms(s[4 * i + 2], s[4 * i + 3], h1, l1);
-              hi[i] = h0 | (h1 << 16);
+              hi[i] = __byte_perm(h0, h1, 0x7531);
               lo[i] = l0 | (l1 << 16);
             }
           }
@@ -414,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       walk = mine.walk;
       while (walk.next(p, cs.plan, g)) atomicOr(a.status + g.r, TREEWY_STATUS_TIMEOUT);
     }
-    if (warp == kLoadWarp) drain_copies(rs, armed);
+    if (warp == kLoadWarp) drain_copies(rs.kfull, armed);
+    if (warp == kLoadWarp + 1) drain_copies(rs.vfull, armed);
     if (warp == kMmaWarp) {
       if (elect_one()) mma_commit(&cs.drain);
       __syncwarp();

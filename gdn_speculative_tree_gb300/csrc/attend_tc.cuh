@@ -2,20 +2,25 @@
 // operands and their terms, the plan of the work, and the loading warp.
 //
 // The pages are the products' operands as they are: an e4m3 operand costs no
-// conversion, and an f32 or bf16 one becomes two e4m3 terms x = hi + lo.  hi
-// has four significant bits, lo the next four and a sign, so that a bf16 value
-// in units of its row's power of two is exact but for the smallest of the row.
-// Both terms' products go into f32 at twice the rate of one product in bf16.
+// conversion, and an f32 or bf16 one becomes two 8-bit terms x = hi + lo, whose
+// products go into one f32 sum at twice the rate of a product in bf16.
+// Queries, and the draft's keys and values, are two e4m3 terms in units of
+// their row's power of two: hi has four significant bits, lo the next four and
+// a sign, so that a bf16 value is exact but for the smallest of its row.
 //
 // A tile is 128 tokens.  The weights of the softmax are
 //
-//   w = 2^(s + log2(the page's value scale) - m + 5)
+//   w = 2^(s + log2(the page's value scale) - m + 6)
 //
 // with one reference m per row for the running maximum of s + log2(scale): they
 // have the size of what they contribute, however far the pages' scales lie
-// apart.  m follows the maximum only when that has grown by more than 2^3 (the
-// output and the sum are then brought down): weights stay within 2^8, and
-// their terms' last step, 2^-9, within 2^-14 of the row's largest weight.
+// apart.  m follows the maximum only when that has grown by more than 2^5 (the
+// output and the sum are then brought down), so weights stay within 2^11.
+// Their hi is e5m2 (three significant bits, down to 2^-16) and lo e4m3: 2^-8 of
+// a weight or 2^-16 of its row's largest, and 2^-3 of a weight down to 2^-22 of
+// the largest: hundreds of thousands of tokens that weigh next to nothing each
+// still count.  (Two e4m3 terms are as exact above, but drop what is below
+// 2^-15 of the largest.)
 //
 // Work: the items (request, key head, 128 rows at most) are runs of tiles, the
 // draft's own keys first; all runs in a row are cut into equal pieces, one for
@@ -33,7 +38,7 @@ constexpr int kTile = 128;                      // tokens, and rows at most
 constexpr int kGroups = kTile / 16;             // the smallest page is 16 tokens
 constexpr int kMaxListed = 768;                 // requests whose tiles are put in a row
 constexpr int kMaxPieces = 152;                 // CTAs that share the row
-constexpr float kGrowth = 3.f, kBias = 5.f;     // 2^(kGrowth + kBias) <= 448
+constexpr float kGrowth = 5.f, kBias = 6.f;     // lo is at most 2^-3 of a weight: 2^(kGrowth + kBias - 3) <= 448
 constexpr float kLeast = 1e-37f;                // of a score's factor: -inf times it stays -inf
 constexpr uint32_t kHalf = 128 * 128;           // bytes of 128 rows of 128
 constexpr unsigned kFull = 0xffffffffu;
@@ -110,10 +115,11 @@ __device__ __forceinline__ void mma_f8_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// A, B e4m3 (0), D f32, M = 128; `a_mn`, `b_mn`: the operand's rows run along the sum.
+// D f32, M = 128, e4m3 operands; `a_mn`, `b_mn`: the operand's rows run along the sum.
 __device__ __forceinline__ uint32_t idesc_f8(uint32_t N, bool a_mn, bool b_mn) {
   return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | (8u << 24);
 }
+constexpr uint32_t kAE5m2 = 1u << 7, kBE5m2 = 1u << 10;  // that operand is e5m2
 // V: rows of 128 bytes along the sum, 128-byte swizzle, blocks of 128 columns kHalf bytes apart.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
   uint64_t d = smem_desc_sw128(addr, 1024);
@@ -181,22 +187,15 @@ __device__ __forceinline__ uint4 load_row8(const uint16_t* row, int c, int d, bo
   return c < d ? __ldg(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
 }
 
-// Two values in f16 as hi + lo: hi the four leading bits, lo the next.
-__device__ __forceinline__ void split_f16x2(uint32_t h, uint32_t& hi, uint32_t& lo) {
-  const uint32_t top = (h + 0x00400040u) & 0xff80ff80u;  // half a unit of the fourth bit up, the rest off
-  uint32_t rest;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(top));
-  hi = e4m3x2_of_f16x2(top);
-  lo = e4m3x2_of_f16x2(rest);
-}
-
-// Two weights as hi + lo: f16 first, of which hi has the four leading bits and
-// lo the rest, rounded (2^-8 of the weight in all, 2^-9 where hi leaves e4m3's
-// normal range).
+// Two weights as hi + lo: of their f16, hi is the upper byte after rounding
+// (e5m2 is f16 without its last eight bits), lo the rest in e4m3.  `hi` has the
+// bytes in places 1 and 3.
 __device__ __forceinline__ void weight_terms(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  uint32_t h;
+  uint32_t h, rest;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
-  split_f16x2(h, hi, lo);
+  hi = h + 0x00800080u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(hi & 0xff00ff00u));
+  lo = e4m3x2_of_f16x2(rest);
 }
 
 // The largest of a row's |bf16|, by one warp (lane: eight of them).
@@ -215,9 +214,9 @@ static __device__ __noinline__ void take_out(uint4& x, uint4& bad) {
 }
 
 // A row's terms, by one warp (lane: eight columns, as bf16): codes of
-// x 2^(7 - E), 2^E the largest exponent of the row, and the unit 2^(E - 7).
-// What is not finite becomes NaN, or zero where `clear`; `none`: there is some.
-__device__ __forceinline__ float row_terms(uint4 x, bool clear, uint2& hi, uint2& lo, bool& none) {
+// x 2^(7 - E), 2^E the largest exponent of the row; returns E - 7.  What is not
+// finite becomes NaN, or zero where `clear`; `none`: there is some.
+__device__ __forceinline__ int row_terms(uint4 x, bool clear, uint2& hi, uint2& lo, bool& none) {
   uint32_t top = row_largest(x);
   uint4 bad = make_uint4(0, 0, 0, 0);
   none = top >= 0x7f80u;
@@ -228,18 +227,27 @@ __device__ __forceinline__ float row_terms(uint4 x, bool clear, uint2& hi, uint2
   const int E = max(static_cast<int>(top >> 7) - 127, -100);
   const float f = __uint_as_float(static_cast<uint32_t>(127 + 7 - E) << 23);
   uint32_t h[4], l[4];
-  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, b[4] = {bad.x, bad.y, bad.z, bad.w};
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    uint32_t y;
+    uint32_t y, rest;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(__uint_as_float(u[e] & 0xffff0000u) * f), "f"(__uint_as_float(u[e] << 16) * f));
-    split_f16x2(y, h[e], l[e]);
-    if (!clear) h[e] |= (b[e] & 0x7fu) | ((b[e] >> 8) & 0x7f00u);
+    const uint32_t four = (y + 0x00400040u) & 0xff80ff80u;  // half a unit of the fourth bit up, the rest off
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(y), "r"(four));
+    h[e] = e4m3x2_of_f16x2(four);
+    l[e] = e4m3x2_of_f16x2(rest);
   }
   hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-  return __uint_as_float(static_cast<uint32_t>(127 - 7 + E) << 23);
+  if (none && !clear) {
+    auto codes = [](uint32_t a, uint32_t b) {
+      return (a & 0x7fu) | ((a >> 8) & 0x7f00u) | ((b & 0x7fu) << 16) | ((b << 8) & 0x7f000000u);
+    };
+    hi.x |= codes(bad.x, bad.y), hi.y |= codes(bad.z, bad.w);
+  }
+  return E - 7;
 }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // Columns 8 lane .. 8 lane + 7 of row `row` of an operand of 128-byte rows
 // (128-byte swizzle), blocks of 128 columns `block` bytes apart.
@@ -379,18 +387,20 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
   return part;
 }
 
-// The loading warp: pages of every tile of the CTA's segments into the ring's
-// stages (K's halves of 128 columns, then V's), their scales beside them.
-// Lane i has the i-th of 32 pages of the context, and the next 32's, asked for
-// ahead.  Returns the tiles up to which copies have been started.
-template <int NH, int S, typename Cs>
-__device__ __forceinline__ int2 load_pages(const Params& p, Cs& cs, RingSmem<S>& rs, Walk walk, unsigned char* ring, const CUtensorMap& kmap,
-                                           const CUtensorMap& vmap) {
+// A loading warp: the keys (or the values, with the pages' scales) of every
+// tile of the CTA's segments into the ring's stages (K's halves of 128 columns,
+// then V's).  Lane i has the i-th of 32 pages of the context, and the next
+// 32's, asked for ahead.  Returns the tiles up to which copies have been
+// started.
+template <bool kValues, int NH, int S, typename Cs>
+__device__ __forceinline__ int load_pages(const Params& p, Cs& cs, RingSmem<S>& rs, Walk walk, unsigned char* ring, const CUtensorMap& map) {
   const treewy_cache& c = p.a.cache;
   constexpr uint32_t kStage = 2 * NH * kHalf;
   const int lane = threadIdx.x & 31, P = c.page_len, per = kTile / P;
-  int gt = 0;
-  int2 armed = make_int2(0, 0);
+  uint64_t* const full = kValues ? rs.vfull : rs.kfull;
+  uint64_t* const free = kValues ? rs.vfree : rs.kfree;
+  int armed = 0, gt = 0, slot = 0;
+  uint32_t again = 1;  // parity of the stage's use before
   Segment g;
 #pragma unroll 1
   while (walk.next(p, cs.plan, g)) {
@@ -400,59 +410,60 @@ __device__ __forceinline__ int2 load_pages(const Params& p, Cs& cs, RingSmem<S>&
     auto scale = [&](const float* x, int page) {
       return page >= 0 && page < c.num_pages ? __ldg(x + static_cast<int64_t>(page) * c.Hkv + g.h) : 1.f;
     };
-    int first = -1;  // page index of lane 0's
+    int src = 32, p0 = (g.t0 - 1) * per;  // the lane that has the tile's first page; its number
     int page = 0, next = 0;
     float ks = 0.f, vs = 1.f, next_ks = 0.f, next_vs = 1.f;
+    bool begun = false;
 #pragma unroll 1
     for (int j = g.t0; j < g.t1; ++j, ++gt) {
-      const int slot = gt % S;
-      const uint32_t again = (gt / S + 1) & 1;
-      unsigned char* stage = ring + slot * kStage;
+      if (gt >= S && !wait_warp(rs, &free[slot], again)) return armed;
       if (j == 0) {  // the draft's tile: the softmax warps fill it
-        if (gt >= S && !(wait_warp(rs, &rs.kfree[slot], again) && wait_warp(rs, &rs.vfree[slot], again))) return armed;
-        if (lane < kGroups) rs.c[slot].ks[lane] = 1.f, rs.c[slot].lv[lane] = rs.c[slot].il[lane] = 0.f;
-        if (lane == 0) rs.c[slot].bad = 0;
-        warp_arrive(&rs.cfull[slot]);
-        continue;
-      }
-      const int p0 = (j - 1) * per;  // the tile's first page
-      if (first < 0 || p0 >= first + 32) {
-        page = first < 0 ? entry(p0 + lane) : next;
-        next = entry(p0 + 32 + lane);
-        if (first < 0) next_ks = scale(c.k_scale, page), next_vs = scale(c.v_scale, page);
-        ks = next_ks, vs = next_vs;
-        first = p0;
-      }
-      const int src = p0 - first;  // the lane that has it
-      const bool mine = lane >= src && lane < src + per && first + lane < pages;
-      const bool in = page >= 0 && page < c.num_pages;
-      const unsigned load = __ballot_sync(kFull, mine && in), wanted = __ballot_sync(kFull, mine);
-      const uint32_t bytes = __popc(load) * P * 128u * NH, to = (lane - src) * P * 128;
-      const int z = page * c.Hkv + g.h;
-#pragma unroll
-      for (int value = 0; value < 2; ++value) {
-        uint64_t* full = value ? &rs.vfull[slot] : &rs.kfull[slot];
-        if (gt >= S && !wait_warp(rs, value ? &rs.vfree[slot] : &rs.kfree[slot], again)) return armed;
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-        (value ? armed.y : armed.x) = gt + 1;
+        if constexpr (kValues) {
+          if (gt >= S && !wait_warp(rs, &rs.kfree[slot], again)) return armed;
+          if (lane < kGroups) rs.c[slot].ks[lane] = 1.f, rs.c[slot].lv[lane] = rs.c[slot].il[lane] = 0.f;
+          if (lane == 0) rs.c[slot].bad = 0;
+          warp_arrive(&rs.cfull[slot]);
+        }
+      } else {
+        if (src == 32) {
+          page = begun ? next : entry(p0 + lane);
+          next = entry(p0 + 32 + lane);
+          if constexpr (kValues) {
+            if (!begun) next_ks = scale(c.k_scale, page), next_vs = scale(c.v_scale, page);
+            ks = next_ks, vs = next_vs;
+          }
+          begun = true, src = 0;
+        }
+        const bool mine = lane >= src && lane < src + per && p0 + lane - src < pages;
+        const bool in = mine && page >= 0 && page < c.num_pages;
+        const unsigned load = __ballot_sync(kFull, in);
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(load) * P * 128u * NH);
+        armed = gt + 1;
         __syncwarp();
-        if (mine && in) {
+        if (in) {
+          unsigned char* to = ring + slot * kStage + (kValues ? NH * kHalf : 0) + (lane - src) * P * 128;
 #pragma unroll
-          for (int x = 0; x < NH; ++x) tma_load_3d(stage + (value * NH + x) * kHalf + to, value ? &vmap : &kmap, full, x * 128, 0, z);
+          for (int x = 0; x < NH; ++x) tma_load_3d(to + x * kHalf, &map, &full[slot], x * 128, 0, page * c.Hkv + g.h);
         }
         __syncwarp();
+        if constexpr (kValues) {
+          const int at = src + min(lane, kGroups - 1) * 16 / P;
+          const float gk = __shfl_sync(kFull, ks, at), gv = __shfl_sync(kFull, vs, at);
+          const bool bad = __any_sync(kFull, mine && !in);
+          if (lane < kGroups) {
+            const float lv = log2f(gv);
+            rs.c[slot].ks[lane] = gk;
+            rs.c[slot].lv[lane] = lv;
+            rs.c[slot].il[lane] = ex2(-lv);
+          }
+          if (lane == 0) rs.c[slot].bad = bad;
+          warp_arrive(&rs.cfull[slot]);
+          if (src == per) next_ks = scale(c.k_scale, next), next_vs = scale(c.v_scale, next);
+        }
+        src += per;
       }
-      const int at = src + min(lane, kGroups - 1) * 16 / P;
-      const float gk = __shfl_sync(kFull, ks, at), gv = __shfl_sync(kFull, vs, at);
-      if (lane < kGroups) {
-        const float lv = log2f(gv);
-        rs.c[slot].ks[lane] = gk;
-        rs.c[slot].lv[lane] = lv;
-        rs.c[slot].il[lane] = ex2(-lv);
-      }
-      if (lane == 0) rs.c[slot].bad = load != wanted;
-      warp_arrive(&rs.cfull[slot]);
-      if (src == per) next_ks = scale(c.k_scale, next), next_vs = scale(c.v_scale, next);
+      p0 += per;
+      if (++slot == S) slot = 0, again ^= 1;
     }
   }
   return armed;
@@ -461,59 +472,71 @@ __device__ __forceinline__ int2 load_pages(const Params& p, Cs& cs, RingSmem<S>&
 // At the end of a CTA whose waits have given up: what is in flight ends first
 // (a draft's tile among the last ones may never be filled).
 template <int S>
-__device__ __forceinline__ void drain_copies(RingSmem<S>& rs, int2 armed) {
-  for (int i = 0; i < S; ++i) {
-    if (armed.x > i) mbar_wait_for(&rs.kfull[(armed.x - 1 - i) % S], ((armed.x - 1 - i) / S) & 1, 20000000ull);
-    if (armed.y > i) mbar_wait_for(&rs.vfull[(armed.y - 1 - i) % S], ((armed.y - 1 - i) / S) & 1, 20000000ull);
-  }
+__device__ __forceinline__ void drain_copies(uint64_t (&full)[S], int armed) {
+  for (int i = 0; i < S && i < armed; ++i) mbar_wait_for(&full[(armed - 1 - i) % S], ((armed - 1 - i) / S) & 1, 20000000ull);
 }
 
 // A segment's queries, and the draft's keys and values where it has them, as
-// terms: by WARPS warps, BATCH rows each at a time.
-// place(kind, i, ..) writes row i of the queries (kind 0), keys (1) or values (2).
+// terms, by WARPS warps; BATCH queries, and half as many nodes, are loaded
+// together.  place(kind, i, ..) writes row i of the queries (kind 0), keys (1)
+// or values (2).
 template <int NH, int WARPS, int BATCH, typename Place>
 __device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, float factor, Place place) {
   const treewy_attn& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.cache.d, G = p.G, row0 = g.m * kTile;
-  const int nodes = g.t0 == 0 ? g.N : 0, values = rows + nodes, jobs = values + nodes;
+  const bool inside = 8 * lane < NH * 128;
+  const int each = (rows + WARPS - 1) / WARPS, begin = warp * each, end = min(rows, begin + each);
+  int head = (row0 + begin) % G;
+  const uint16_t* q = static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(g.lo) + (row0 + begin) / G) * a.q_stride +
+                      static_cast<int64_t>(g.h * G) * d;
 #pragma unroll 1
-  for (int j0 = warp; j0 < jobs; j0 += BATCH * WARPS) {
+  for (int i0 = begin; i0 < end; i0 += BATCH) {
     uint4 x[BATCH];
 #pragma unroll
     for (int e = 0; e < BATCH; ++e) {
-      const int j = j0 + e * WARPS;
-      if (j >= jobs) continue;
-      const void* from = a.q;
-      int64_t token = g.lo, stride = a.q_stride;
-      int head, wide = p.wide_q;
-      if (j < rows) {
-        const int rr = row0 + j, node = rr / G;
-        token += node, head = g.h * G + rr - node * G;
-      } else {
-        const bool value = j >= values;
-        token += j - (value ? values : rows), head = g.h;
-        from = value ? a.v : a.k, stride = value ? a.v_stride : a.k_stride, wide = value ? p.wide_v : p.wide_k;
-      }
-      x[e] = load_row8(static_cast<const uint16_t*>(from) + token * stride + static_cast<int64_t>(head) * d, 8 * lane, d, wide);
+      if (i0 + e >= end) continue;
+      x[e] = load_row8(q + head * d, 8 * lane, d, p.wide_q);
+      if (++head == G) head = 0, q += a.q_stride;
     }
 #pragma unroll
     for (int e = 0; e < BATCH; ++e) {
-      const int j = j0 + e * WARPS;
-      if (j >= jobs) continue;
-      const int kind = j < rows ? 0 : j < values ? 1 : 2, i = j - (kind == 0 ? 0 : kind == 1 ? rows : values);
+      if (i0 + e >= end) continue;
+      uint2 hi, lo;
+      bool none;
+      const float unit = pow2(row_terms(x[e], false, hi, lo, none));
+      if (inside) place(0, i0 + e, lane, hi, lo);
+      if (lane == 0) ds.rowf[i0 + e] = unit * factor;
+    }
+  }
+  if (g.t0 != 0) return;
+  const uint16_t* k = static_cast<const uint16_t*>(a.k) + (static_cast<int64_t>(g.lo) + warp) * a.k_stride + static_cast<int64_t>(g.h) * d;
+  const uint16_t* v = static_cast<const uint16_t*>(a.v) + (static_cast<int64_t>(g.lo) + warp) * a.v_stride + static_cast<int64_t>(g.h) * d;
+#pragma unroll 1
+  for (int n0 = warp; n0 < g.N; n0 += BATCH / 2 * WARPS) {
+    uint4 x[BATCH];
+#pragma unroll
+    for (int e = 0; e < BATCH; e += 2) {
+      if (n0 + e / 2 * WARPS >= g.N) continue;
+      x[e] = load_row8(k, 8 * lane, d, p.wide_k);
+      x[e + 1] = load_row8(v, 8 * lane, d, p.wide_v);
+      k += WARPS * a.k_stride, v += WARPS * a.v_stride;
+    }
+#pragma unroll
+    for (int e = 0; e < BATCH; ++e) {
+      const int n = n0 + e / 2 * WARPS;
+      if (n >= g.N) continue;
       uint2 hi, lo;
       bool none;
       // a value that is no number would reach the nodes that do not see it: weights of zero times it
-      const float unit = row_terms(x[e], kind == 2, hi, lo, none);
-      if (8 * lane < NH * 128) place(kind, i, lane, hi, lo);
+      const int unit = row_terms(x[e], e & 1, hi, lo, none);
+      if (inside) place(1 + (e & 1), n, lane, hi, lo);
       if (lane == 0) {
-        if (kind == 0) ds.rowf[i] = unit * factor;
-        else if (kind == 1) ds.ks[i] = unit;
-        else {
-          if (none) atomicOr(&ds.no_number, 1ull << i);
-          const float lv = log2f(unit);
-          ds.lv[i] = lv;
-          ds.il[i] = ex2(-lv);
+        if (e & 1) {
+          if (none) atomicOr(&ds.no_number, 1ull << n);
+          ds.lv[n] = static_cast<float>(unit);
+          ds.il[n] = pow2(-unit);
+        } else {
+          ds.ks[n] = pow2(unit);
         }
       }
     }

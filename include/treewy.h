@@ -556,9 +556,9 @@ typedef struct treewy_attn {
  * (with TREEWY_STATUS_TIMEOUT, some may be written).
  *
  * bf16 rows with bf16 outputs and d a multiple of 16 run on the tensor cores in
- * 8-bit products, every f32 or bf16 operand as two e4m3 terms: a query, key or
+ * 8-bit products, every f32 or bf16 operand as two 8-bit terms: a query, key or
  * value of the draft is within 2^-17 of its row's largest, a weight of the
- * softmax within 2^-8 of itself and 2^-14 of its row's largest.  Other calls
+ * softmax within 2^-8 of itself or 2^-16 of its row's largest.  Other calls
  * run in f32.  A NaN (or an infinity, which counts as one) in a key reaches
  * every node that sees it, in a value every such node's column.  Scores pass f32: where
  * they overflow it, the node's outputs are NaN.

@@ -134,12 +134,12 @@ class Attend:
                 top = np.abs(values[h // G]).max()
                 tol = 2 * score + n * 2.0 ** -24
                 if self.tensor:
-                    # queries, and the draft's keys, to 2^-17 of a row's largest; weights to 2^-8 of themselves and 2^-14
+                    # queries, and the draft's keys, to 2^-17 of a row's largest; weights to 2^-8 of themselves or 2^-16
                     # of the largest of their row; the draft's values to 2^-17 of a row's largest
                     lengths = np.abs(keys[h // G]).sum(1).max() * np.abs(q[at][:, h]).max()
                     lengths += np.abs(q[at][:, h]).sum(1).max() * np.abs(keys[h // G]).max()
                     s = q[at][:, h] @ keys[h // G].T * self.scale
-                    flat = np.minimum(1.0, n * 2.0 ** -14 / np.exp(s - s.max(1, keepdims=True)).sum(1).min())
+                    flat = np.minimum(1.0, n * 2.0 ** -16 / np.exp(s - s.max(1, keepdims=True)).sum(1).min())
                     tol += 2 * self.scale * 2.0 ** -17 * lengths + 2.0 ** -8 + flat + 2.0 ** -17
                 err = np.abs(o[at][:, h] - want[:, h])
                 half = 2.0 ** -8 if self.o.dtype == torch.bfloat16 else 2.0 ** -24

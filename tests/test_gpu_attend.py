@@ -94,8 +94,32 @@ def test_small_values_beside_large_ones_that_are_not_seen(cuda_lib, flags):
     keep = np.r_[0:64, 128:512]
     from oracle import attend_oracle as orc
     small = orc.attend(f64(a.q), f64(a.k), f64(a.v), a.parents[0], ck[:, keep], cv[:, keep], a.scale)
-    # weights to 2^-8 of themselves and 2^-14 of the row's largest (448 tokens), scores and outputs as ever
-    assert np.abs(want - small).max() <= (2.0 ** -7 + 448 * 2.0 ** -14) * np.abs(cv[:, keep]).max()
+    # weights to 2^-8 of themselves or 2^-16 of the row's largest (448 tokens), scores and outputs as ever
+    assert np.abs(want - small).max() <= (2.0 ** -7 + 448 * 2.0 ** -16) * np.abs(cv[:, keep]).max()
+
+
+@pytest.mark.parametrize("Hq", [4, 40])
+@pytest.mark.parametrize("flags", [0, GENERIC])
+def test_many_tokens_that_weigh_next_to_nothing(cuda_lib, flags, Hq):
+    """One token with a weight of 1 and 100,000 of 2^-17 each: together they count for 0.76, and their values are alike."""
+    n = 100000
+    a = Attend([n], [1], Hq=Hq, Hkv=1, d=64, page=128, kind="chain", flags=flags, seed=21)
+    a.q.zero_()
+    a.q[..., 0] = 8.0
+    a.k.zero_()
+    a.v.fill_(-1.0)
+    a.cache.k.view(torch.uint8).zero_()
+    a.cache.v.copy_(torch.ones_like(a.cache.v, dtype=torch.float32))
+    a.cache.ks.fill_(1.0)
+    a.cache.vs.fill_(1.0)
+    a.scale = 1.0
+    # 17 ln 2 = 8 * 1.473 in the lone token's favour; its key is bf16, so the weight is that of the key as stored
+    a.k[..., 0] = 17 * np.log(2) / 8
+    w = np.exp(-8 * float(a.k[0, 0, 0]))
+    a.run()
+    want = (n * w - 1) / (n * w + 1)
+    # weights as small as these to 2^-3 of themselves at worst; of equal ones the error is the same for all
+    assert np.abs(f64(a.o) - want).max() <= (2.0 ** -3 * n * w / (n * w + 1) * 2 if flags == 0 else 1e-3) + 2.0 ** -8
 
 
 @pytest.mark.parametrize("flags", [0, GENERIC])
