@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, 64 + g.N, 96);
         if (t >= g.N && t < 32) ds.ks[t] = 1.f, ds.lv[t] = ds.il[t] = 0.f;
       }
-      fill_rows<NH, kSoftWarps, 2>(p, ds, g, rows, factor, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
+      fill_rows<NH, kSoftWarps, 4>(p, ds, g, rows, factor, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
         unsigned char* tile = kind == 0 ? qs : kind == 1 ? draft : draft + NH * kHalf;
         const uint32_t block = kind == 0 ? Sh::kRowBytes : kHalf;
         *operand8(tile, i, ln, block) = hi;

@@ -41,6 +41,7 @@ struct AttendSmem {
   uint64_t sfull[2], pready[2], pvdone[2], qready, drain;
   float top[2][kParts * kTile];  // maxima (and sums) of the parts of rows; two sets in turn
   uint32_t tmem;
+  Segment segment;               // the softmax warps' current one
   DraftSmem draft;
   PlanSmem plan;
 };
@@ -177,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     while (walk.next(p, cs.plan, g)) {
       // queries and tree
-      const int row0 = g.m * kTile, rows = min(kTile, g.N * G - row0);
-      if (t == 0) ds.bad_tree = 0, ds.no_number = 0;
+      const int rows = min(kTile, g.N * G - g.m * kTile);
+      if (t == 0) ds.bad_tree = 0, ds.no_number = 0, cs.segment = g;
       if (g.t0 == 0) wait_warp(rs, &rs.cfull[gt % S], (gt / S) & 1);  // the stage is free
       all_sync();
       load_tree(p, ds, g, t);
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, (g.N + kNodes - 1) / kNodes * kCols, kTile);
         if (t >= g.N && t < kMaxNodes) ds.ks[t] = 1.f, ds.lv[t] = ds.il[t] = 0.f;
       }
-      fill_rows<NH, kSoftWarps, 4>(p, ds, g, rows, factor, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
+      fill_rows<NH, kSoftWarps, 8>(p, ds, g, rows, factor, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
         unsigned char* tile = kind == 0 ? smem : kind == 1 ? draft : draft + NH * kHalf;
         const int token = i / kNodes * kCols + i % kNodes;
         *operand8(tile, kind == 0 ? i : token, ln, kHalf) = hi;
@@ -214,17 +215,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool bad_tree = ds.bad_tree != 0, alive = quarter * 32 < rows;
       bool bad = bad_tree;
       const float rowf = row < rows ? ds.rowf[row] : 0.f;
-      const int node = min(row0 + row, g.N * G - 1) / G;
       float m = -INFINITY, sum = 0.f;
+      const int t0 = g.t0, t1 = g.t1, len = g.len;
 #pragma unroll 1
-      for (int j = g.t0; j < g.t1; ++j, ++gt) {
+      for (int j = t0; j < t1; ++j, ++gt) {
         const int slot = gt % S, b = gt & 1;
         const Consts& cc = rs.c[slot];
         // after a wait that gave up a warp still comes by every barrier of threads
         bool ok = wait_warp(rs, &cs.sfull[b], (gt >> 1) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
         tc_fence_after_sync();
         bad |= cc.bad != 0;
-        const int n = j == 0 ? kTile : min(kTile, g.len - (j - 1) * kTile);
+        const int n = j == 0 ? kTile : min(kTile, len - (j - 1) * kTile);
         if (n < kTile && ok) ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1);
         if (n < kTile && ok) {  // values behind the context: anything, so none
           const int end = (n + 31) & ~31;
@@ -248,7 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float rf = rowf;
           if (j == 0) {  // scores here; the loading warp's constants of the tile are 1 and 0
             rf = 1.f;
-            const uint32_t seen = static_cast<uint32_t>(ds.seen[node] >> (kNodes * share));
+            const Segment& now = cs.segment;
+            const uint32_t seen =
+                static_cast<uint32_t>(ds.seen[min(now.m * kTile + row, now.N * G - 1) / G] >> (kNodes * share));
 #pragma unroll
             for (int i = 0; i < kNodes; ++i) {
               const int q = share * kNodes + i;
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             top = fmaxf(top, fmaf(x, f[q], cc.lv[share * (kCols / 16) + q]));
           }
           top = over_row(b, top, [](float x, float y) { return fmaxf(x, y); });
-          if (j == g.t0) {
+          if (j == t0) {
             m = top;
           } else {
             const bool grown = top > m + kGrowth;
@@ -279,18 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum *= down;
               wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
               tc_fence_after_sync();
-              int x = col0;
 #pragma unroll 1
-              for (; x + 32 <= col1; x += 32) {
-                uint32_t o[32];
-                tmem_ld32(lanes + kColO + x, o);
-                tmem_wait32(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * down);
-                tmem_st16(lanes + kColO + x, o);
-                tmem_st16(lanes + kColO + x + 16, o + 16);
-              }
-              if (x < col1) {
+              for (int x = col0; x < col1; x += 16) {
                 uint32_t o[16];
                 tmem_ld16_async(lanes + kColO + x, o);
                 tmem_wait16(o);
@@ -301,32 +294,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_st();
             }
           }
-          uint32_t hi[kCols / 4], lo[kCols / 4];  // four codes each
 #pragma unroll
           for (int q = 0; q < kCols / 16; ++q) {
             const float e = cc.lv[share * (kCols / 16) + q] + (kBias - m);
             float part_sum = 0.f;
+            uint32_t hi[4], lo[4];  // four codes each
 #pragma unroll
-            for (int i = 16 * q; i < 16 * q + 16; ++i) {
-              s[i] = ex2(fmaf(s[i], f[q], e));
-              part_sum += s[i];
-            }
-            sum = fmaf(part_sum, cc.il[share * (kCols / 16) + q], sum);
+            for (int i = 0; i < 4; ++i) {
+              float* w = s + 16 * q + 4 * i;
 #pragma unroll
-            for (int i = 4 * q; i < 4 * q + 4; ++i) {
+              for (int k = 0; k < 4; ++k) {
+                w[k] = ex2(fmaf(w[k], f[q], e));
+                part_sum += w[k];
+              }
               uint32_t h0, l0, h1, l1;
-              weight_terms(s[4 * i], s[4 * i + 1], h0, l0);
-              weight_terms(s[4 * i + 2], s[4 * i + 3], h1, l1);
+              weight_terms(w[0], w[1], h0, l0);
+              weight_terms(w[2], w[3], h1, l1);
               hi[i] = __byte_perm(h0, h1, 0x7531);
               lo[i] = l0 | (l1 << 16);
             }
-          }
-          if constexpr (kCols == 64) {
-            tmem_st16(sc + share * 16, hi);
-            tmem_st16(sc + 32 + share * 16, lo);
-          } else {
-            tmem_st8(sc + share * 8, hi);
-            tmem_st8(sc + 32 + share * 8, lo);
+            sum = fmaf(part_sum, cc.il[share * (kCols / 16) + q], sum);
+            tmem_st4(sc + share * (kCols / 4) + 4 * q, hi);
+            tmem_st4(sc + 32 + share * (kCols / 4) + 4 * q, lo);
           }
           if (j == 0) {
 #pragma unroll
@@ -339,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- outputs
+      g = cs.segment;
+      const int row0 = g.m * kTile, node = min(row0 + row, g.N * G - 1) / G;
       const bool whole = g.t0 == 0 && g.t1 == g.tiles;
       const bool ok = wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
       tc_fence_after_sync();
@@ -397,12 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (whole && p.wide_o) {
         all_sync();
         if (ok && !bad) {
+          constexpr int kEach = kTile / kSoftWarps;
+          int head = (row0 + warp * kEach) % G;
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.o) + ((static_cast<int64_t>(g.lo) + (row0 + warp * kEach) / G) * a.Hq + g.h * G) * d;
 #pragma unroll 4
-          for (int i = warp; i < rows; i += kSoftWarps) {
-            const int rr = row0 + i, at = rr / G;
-            uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) +
-                                                 ((static_cast<int64_t>(g.lo) + at) * a.Hq + g.h * G + rr - at * G) * d);
-            if (8 * lane < d) to[lane] = *reinterpret_cast<const uint4*>(smem + i * (NH * 256) + ((lane ^ (i & 7)) << 4));
+          for (int i = warp * kEach; i < min(rows, warp * kEach + kEach); ++i) {
+            if (8 * lane < d)
+              reinterpret_cast<uint4*>(to + head * d)[lane] = *reinterpret_cast<const uint4*>(smem + i * (NH * 256) + ((lane ^ (i & 7)) << 4));
+            if (++head == G) head = 0, to += static_cast<int64_t>(a.Hq) * d;
           }
         }
       }

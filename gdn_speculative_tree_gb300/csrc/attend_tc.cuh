@@ -153,6 +153,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t* r) {
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+__device__ __forceinline__ void tmem_st4(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::
@@ -175,15 +179,14 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
 }
 // Eight values of a row of d bf16 at column c (zeros behind d).
 // (one by one where rows do not start on 16 bytes)
-static __device__ __noinline__ uint4 load_row8_odd(const uint16_t* row, int c, int d) {
+__device__ __forceinline__ uint4 load_row8_odd(const uint16_t* row, int c, int d) {
   uint32_t u[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     u[e] = (c + 2 * e < d ? __ldg(row + c + 2 * e) : 0u) | (c + 2 * e + 1 < d ? static_cast<uint32_t>(__ldg(row + c + 2 * e + 1)) << 16 : 0u);
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ uint4 load_row8(const uint16_t* row, int c, int d, bool wide) {
-  if (!wide) return load_row8_odd(row, c, d);
+__device__ __forceinline__ uint4 load_row8(const uint16_t* row, int c, int d) {
   return c < d ? __ldg(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
 }
 
@@ -204,7 +207,7 @@ __device__ __forceinline__ uint32_t row_largest(const uint4& x) {
   return __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
 }
 // What is not finite out of eight values; its places (all bits of a value).
-static __device__ __noinline__ void take_out(uint4& x, uint4& bad) {
+__device__ __forceinline__ void take_out(uint4& x, uint4& bad) {
   auto one = [](uint32_t& u) {
     const uint32_t b = ((u & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((u & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
     u &= ~b;
@@ -477,67 +480,74 @@ __device__ __forceinline__ void drain_copies(uint64_t (&full)[S], int armed) {
 }
 
 // A segment's queries, and the draft's keys and values where it has them, as
-// terms, by WARPS warps; BATCH queries, and half as many nodes, are loaded
-// together.  place(kind, i, ..) writes row i of the queries (kind 0), keys (1)
-// or values (2).
-template <int NH, int WARPS, int BATCH, typename Place>
+// terms, by WARPS warps.  ROWS of a warp's rows are loaded at once, and
+// converted two at a time: little code, which a CTA meets for the first time
+// here.
+// place(kind, i, ..) writes row i of the queries (kind 0), keys (1) or values (2).
+template <int NH, int WARPS, int ROWS, typename Place>
 __device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, float factor, Place place) {
   const treewy_attn& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.cache.d, G = p.G, row0 = g.m * kTile;
-  const bool inside = 8 * lane < NH * 128;
-  const int each = (rows + WARPS - 1) / WARPS, begin = warp * each, end = min(rows, begin + each);
-  int head = (row0 + begin) % G;
-  const uint16_t* q = static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(g.lo) + (row0 + begin) / G) * a.q_stride +
-                      static_cast<int64_t>(g.h * G) * d;
+  const int each = (rows + WARPS - 1) / WARPS, begin = warp * each;
 #pragma unroll 1
-  for (int i0 = begin; i0 < end; i0 += BATCH) {
-    uint4 x[BATCH];
-#pragma unroll
-    for (int e = 0; e < BATCH; ++e) {
-      if (i0 + e >= end) continue;
-      x[e] = load_row8(q + head * d, 8 * lane, d, p.wide_q);
-      if (++head == G) head = 0, q += a.q_stride;
-    }
-#pragma unroll
-    for (int e = 0; e < BATCH; ++e) {
-      if (i0 + e >= end) continue;
-      uint2 hi, lo;
-      bool none;
-      const float unit = pow2(row_terms(x[e], false, hi, lo, none));
-      if (inside) place(0, i0 + e, lane, hi, lo);
-      if (lane == 0) ds.rowf[i0 + e] = unit * factor;
-    }
-  }
-  if (g.t0 != 0) return;
-  const uint16_t* k = static_cast<const uint16_t*>(a.k) + (static_cast<int64_t>(g.lo) + warp) * a.k_stride + static_cast<int64_t>(g.h) * d;
-  const uint16_t* v = static_cast<const uint16_t*>(a.v) + (static_cast<int64_t>(g.lo) + warp) * a.v_stride + static_cast<int64_t>(g.h) * d;
+  for (int pass = 0; pass < (g.t0 == 0 ? 2 : 1); ++pass) {
+    const bool nodes = pass == 1, wide = nodes ? p.wide_k && p.wide_v : p.wide_q;
+    const int count = nodes ? (g.N > warp ? 2 * ((g.N - warp + WARPS - 1) / WARPS) : 0) : min(rows, begin + each) - begin;
+    // rows alternate between two places (heads of a token, or keys and values), each a step on
+    int head = nodes ? 0 : (row0 + begin) % G;
+    const int64_t token = static_cast<int64_t>(g.lo) + (nodes ? warp : (row0 + begin) / G);
+    const uint16_t* from = static_cast<const uint16_t*>(nodes ? a.k : a.q) + token * (nodes ? a.k_stride : a.q_stride) +
+                           static_cast<int64_t>(nodes ? g.h : g.h * G) * d;
+    const uint16_t* values = static_cast<const uint16_t*>(a.v) + token * a.v_stride + static_cast<int64_t>(g.h) * d;
+    auto next = [&] {
+      const uint16_t* at = nodes ? (head == 0 ? from : values) : from + head * d;
+      if (++head == (nodes ? 2 : G)) {
+        head = 0;
+        from += nodes ? WARPS * a.k_stride : a.q_stride;
+        values += WARPS * a.v_stride;
+      }
+      return at;
+    };
+    const int batch = wide ? ROWS : 1;
 #pragma unroll 1
-  for (int n0 = warp; n0 < g.N; n0 += BATCH / 2 * WARPS) {
-    uint4 x[BATCH];
+    for (int b0 = 0; b0 < count; b0 += batch) {
+      uint4 x[ROWS];
+      const int many = min(batch, count - b0);
+      if (wide) {
 #pragma unroll
-    for (int e = 0; e < BATCH; e += 2) {
-      if (n0 + e / 2 * WARPS >= g.N) continue;
-      x[e] = load_row8(k, 8 * lane, d, p.wide_k);
-      x[e + 1] = load_row8(v, 8 * lane, d, p.wide_v);
-      k += WARPS * a.k_stride, v += WARPS * a.v_stride;
-    }
+        for (int e = 0; e < ROWS; ++e)
+          if (e < many) x[e] = load_row8(next(), 8 * lane, d);
+      } else {
+        x[0] = load_row8_odd(next(), 8 * lane, d);
+      }
+      constexpr int kStep = ROWS < 2 ? ROWS : 2;
+#pragma unroll 1
+      for (int e0 = 0; e0 < many; e0 += kStep) {
 #pragma unroll
-    for (int e = 0; e < BATCH; ++e) {
-      const int n = n0 + e / 2 * WARPS;
-      if (n >= g.N) continue;
-      uint2 hi, lo;
-      bool none;
-      // a value that is no number would reach the nodes that do not see it: weights of zero times it
-      const int unit = row_terms(x[e], e & 1, hi, lo, none);
-      if (inside) place(1 + (e & 1), n, lane, hi, lo);
-      if (lane == 0) {
-        if (e & 1) {
-          if (none) atomicOr(&ds.no_number, 1ull << n);
-          ds.lv[n] = static_cast<float>(unit);
-          ds.il[n] = pow2(-unit);
-        } else {
-          ds.ks[n] = pow2(unit);
+        for (int e = 0; e < kStep; ++e) {
+          if (e0 + e >= many) continue;
+          const int k = b0 + e0 + e;
+          const bool value = nodes && (k & 1);
+          const int i = nodes ? warp + k / 2 * WARPS : begin + k;
+          uint2 hi, lo;
+          bool none;
+          // a value that is no number would reach the nodes that do not see it: weights of zero times it
+          const int unit = row_terms(x[e], value, hi, lo, none);
+          if (8 * lane < NH * 128) place(nodes ? (value ? 2 : 1) : 0, i, lane, hi, lo);
+          if (lane == 0) {
+            if (!nodes) {
+              ds.rowf[i] = pow2(unit) * factor;
+            } else if (value) {
+              if (none) atomicOr(&ds.no_number, 1ull << i);
+              ds.lv[i] = static_cast<float>(unit);
+              ds.il[i] = pow2(-unit);
+            } else {
+              ds.ks[i] = pow2(unit);
+            }
+          }
         }
+#pragma unroll
+        for (int e = 0; e + kStep < ROWS; ++e) x[e] = x[e + kStep];
       }
     }
   }
