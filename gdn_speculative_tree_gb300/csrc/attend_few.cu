@@ -138,9 +138,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int gt = 0;  // tiles so far
 
   if (warp == kLoadWarp) {
-    armed = load_pages<false, NH, S>(p, cs, rs, walk, ring, kmap);
+    armed = load_pages<false, NH, S>(p, cs, rs, walk, ring, kmap, [](const Segment&) { return true; },
+                                     [](const Segment&, int, int, uint32_t) { return true; });
   } else if (warp == kLoadWarp + 1) {
-    armed = load_pages<true, NH, S>(p, cs, rs, walk, ring, vmap);
+    // the softmax warps fill the draft's tile once both its stages are free
+    armed = load_pages<true, NH, S>(p, cs, rs, walk, ring, vmap, [](const Segment&) { return true; },
+                                    [&](const Segment&, int tile, int slot, uint32_t again) {
+                                      return tile < S || wait_warp(rs, &rs.kfree[slot], again);
+                                    });
   } else if (warp == kMmaWarp) {
     // ---- products
     const uint32_t id_s = idesc_f8(2 * NR, false, false), id_o = idesc_f8(Sh::kCols, true, false);
@@ -367,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = g.t0 == 0 && g.t1 == g.tiles;
       const bool ok = wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
       tc_fence_after_sync();
+      const unsigned long long none = g.t0 == 0 ? ds.no_number : 0;  // before the next segment's
       // not the set of the last tile, which another warp may still read
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
@@ -381,7 +387,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && !bad) {
         // row by row: little code, which a CTA meets for the first time here, costs less than many loads at once
         const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
-        const unsigned long long none = g.t0 == 0 ? ds.no_number : 0;
         int node = row0 / G, head = row0 - node * G;
 #pragma unroll 1
         for (int row = row0; row < min(rows, row0 + NT); ++row, ++head) {

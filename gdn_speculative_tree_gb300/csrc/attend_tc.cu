@@ -3,29 +3,88 @@
 // rows and outputs, head sizes that are multiples of 16, and drafts of more
 // than 32 rows; and what joins the pieces of an item.
 //
+// attend_split_kernel makes the terms of all queries and of the drafts' keys and
+// values, once for every tile that reads them; attend_tc_kernel then loads them
+// as it loads pages.
+//
 // A tile is 128 rows, (node, query head) pairs that share a key head, times
-// 128 tokens.  TMEM lanes are rows, so that a softmax thread owns a part of a
-// row:
+// 128 tokens.  TMEM lanes are rows:
 //
 //   S = Q K^T          Q's terms and K in shared memory, S in TMEM, twice
 //   w                  two terms, back in TMEM in the place of S
 //   O += w V           V in shared memory as it is stored (rows along the sum)
 //
-// The draft's keys and values take two tokens of its tile each, one per term;
-// the ancestors are a mask of bits.
+// Two sets of eight warps take tiles in turn, so that one's loads and waits fall
+// into the other's arithmetic; a thread has half a row of its set's tile.  The
+// sets share the rows' references: a tile's weights wait for the maxima of the
+// tile before it, not for its weights.  The first reference is the larger
+// maximum of a segment's first two tiles, the draft's own one being small.
 //
-//   softmax warps  queries and draft to e4m3; softmax; outputs
-//   loading warps  page table, scales and pages (TMA): keys, and values
-//   issuing warp   the products: S of the next tile before O of this one
+// The draft's keys and values take two tokens of its tile each, one per term
+// (n and 64 + n); the ancestors are a mask of bits.
+//
+//   warps 0-15   softmax, outputs
+//   warps 16, 17 page table, scales, pages and terms (TMA): keys, and values
+//   warp 18      issues the products: S of the next tile before O of this one
 #include "attend_tc.cuh"
 
 namespace treewy {
 namespace {
 
-constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;
+constexpr int kSets = 2, kSetWarps = 8, kSoftWarps = kSets * kSetWarps, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;
 constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
-constexpr int kParts = kSoftWarps / 4, kCols = kTile / kParts, kNodes = kCols / 2;  // of a row, by warp
+constexpr int kParts = kSoftWarps / 4;  // warps that share 32 rows
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
+
+// Terms of every row: a warp takes a row, (head, token) and whether it is a
+// query, a key or a value.  Units are the exponents of a row's power of two,
+// kNone above them where a value's row has something that is no number.
+constexpr int kNone = 1024, kSplitThreads = 256;
+__global__ void __launch_bounds__(kSplitThreads) attend_split_kernel(const __grid_constant__ Params p) {
+  after_previous();
+  const treewy_attn& a = p.a;
+  const int lane = threadIdx.x & 31, d = a.cache.d, G = p.G, Hkv = a.cache.Hkv;
+  const int64_t T = a.T, queries = T * a.Hq, rows = queries + 2 * T * Hkv;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kSplitThreads / 32);
+  constexpr int kBatch = 4;
+#pragma unroll 1
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (kSplitThreads / 32) + (threadIdx.x >> 5); r0 < rows; r0 += kBatch * step) {
+    uint4 x[kBatch];
+    int64_t to[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int64_t r = r0 + e * step;
+      if (r >= rows) continue;
+      // rows as they are stored, token by token
+      const int kind = r < queries ? 0 : r < queries + T * Hkv ? 1 : 2, heads = kind == 0 ? a.Hq : Hkv;
+      const int64_t i = r - (kind == 0 ? 0 : kind == 1 ? queries : queries + T * Hkv), token = i / heads;
+      const int head = static_cast<int>(i - token * heads);
+      const uint16_t* from = static_cast<const uint16_t*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                             token * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + static_cast<int64_t>(head) * d;
+      const bool wide = kind == 0 ? p.wide_q : kind == 1 ? p.wide_k : p.wide_v;
+      x[e] = wide ? load_row8(from, 8 * lane, d) : load_row8_odd(from, 8 * lane, d);
+      const int g = kind == 0 ? G : 1;
+      to[e] = (head / g * T + token) * g + head % g;
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int64_t r = r0 + e * step;
+      if (r >= rows) continue;
+      const int kind = r < queries ? 0 : r < queries + T * Hkv ? 1 : 2;
+      uint2 hi, lo;
+      bool none;
+      // a value that is no number would reach the nodes that do not see it: weights of zero times it
+      int unit = row_terms(x[e], kind == 2, hi, lo, none);
+      if (kind == 2 && none) unit += kNone;
+      uint8_t* terms = (kind == 0 ? p.q_terms : kind == 1 ? p.k_terms : p.v_terms) + to[e] * d + 8 * lane;
+      if (8 * lane < d) {
+        *reinterpret_cast<uint2*>(terms) = hi;
+        *reinterpret_cast<uint2*>(terms + (kind == 0 ? queries : T * Hkv) * d) = lo;
+      }
+      if (lane == 0) (kind == 0 ? p.q_units : kind == 1 ? p.k_units : p.v_units)[to[e]] = static_cast<int16_t>(unit);
+    }
+  }
+}
 
 // NH: halves of 128 columns of a head.
 template <int NH>
@@ -38,18 +97,22 @@ struct Shape {
 template <int S>
 struct AttendSmem {
   RingSmem<S> ring;
-  uint64_t sfull[2], pready[2], pvdone[2], qready, drain;
-  float top[2][kParts * kTile];  // maxima (and sums) of the parts of rows; two sets in turn
+  uint64_t sfull[2], mdone[2], pready[2], pvdone[2], qfull, qfree, drain;
+  float ref[kTile], first[kSets][kTile], half[kSets][2][kTile], sum[kParts][kTile];  // of the rows
   uint32_t tmem;
+  int bad;                       // a page of the segment's
   Segment segment;               // the softmax warps' current one
   DraftSmem draft;
   PlanSmem plan;
 };
 
+struct Maps {
+  CUtensorMap k, v;              // pages
+  CUtensorMap q_terms, k_terms, v_terms;
+};
+
 template <int NH>
-__global__ void __launch_bounds__(kThreads, 1)
-    attend_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap) {
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using Sh = Shape<NH>;
   constexpr int S = Sh::kStages;
   extern __shared__ unsigned char raw_smem[];
@@ -66,14 +129,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     init_ring(rs);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cs.sfull[i], 1);
-      mbar_init(&cs.pready[i], kSoftWarps);
+      mbar_init(&cs.mdone[i], kSetWarps);
+      mbar_init(&cs.pready[i], kSetWarps);
       mbar_init(&cs.pvdone[i], 1);
     }
-    mbar_init(&cs.qready, 1);
+    mbar_init(&cs.qfull, 1);
+    mbar_init(&cs.qfree, kSoftWarps);
     mbar_init(&cs.drain, 1);
     fence_mbarrier_init();
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
+    prefetch_tensormap(&maps.k);
+    prefetch_tensormap(&maps.v);
+    prefetch_tensormap(&maps.q_terms);
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&cs.tmem, kTmemCols);
@@ -86,12 +152,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk walk = mine.walk;
   Segment g;
   int armed = 0;
+  int queries = 0;  // segments whose queries have been sent for
   int gt = 0;  // tiles so far
 
   if (warp == kLoadWarp) {
-    armed = load_pages<false, NH, S>(p, cs, rs, walk, ring, kmap);
+    armed = load_pages<false, NH, S>(
+        p, cs, rs, walk, ring, maps.k,
+        [&](const Segment& s) {
+          if (queries > 0 && !wait_warp(rs, &cs.qfree, (queries - 1) & 1)) return false;
+          ++queries;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&cs.qfull, 2 * NH * kHalf);
+            const int row = static_cast<int>((static_cast<int64_t>(s.h) * a.T + s.lo) * G + s.m * kTile);
+#pragma unroll
+            for (int x = 0; x < 2 * NH; ++x) tma_load_3d(smem + x * kHalf, &maps.q_terms, &cs.qfull, x % NH * 128, row, x / NH);
+          }
+          __syncwarp();
+          return true;
+        },
+        [&](const Segment& s, int tile, int slot, uint32_t) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&rs.kfull[slot], NH * kHalf);
+            for (int x = 0; x < 2 * NH; ++x)
+              tma_load_3d(ring + slot * Sh::kStage + x % NH * kHalf + x / NH * (kHalf / 2), &maps.k_terms, &rs.kfull[slot], x % NH * 128,
+                          static_cast<int>(s.h * a.T + s.lo), x / NH);
+          }
+          __syncwarp();
+          return true;
+        });
   } else if (warp == kLoadWarp + 1) {
-    armed = load_pages<true, NH, S>(p, cs, rs, walk, ring, vmap);
+    armed = load_pages<true, NH, S>(
+        p, cs, rs, walk, ring, maps.v, [](const Segment&) { return true; },
+        [&](const Segment& s, int tile, int slot, uint32_t) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&rs.vfull[slot], NH * kHalf);
+            for (int x = 0; x < 2 * NH; ++x)
+              tma_load_3d(ring + slot * Sh::kStage + (NH + x % NH) * kHalf + x / NH * (kHalf / 2), &maps.v_terms, &rs.vfull[slot],
+                          x % NH * 128, static_cast<int>(s.h * a.T + s.lo), x / NH);
+          }
+          __syncwarp();
+          return true;
+        });
   } else if (warp == kMmaWarp) {
     // ---- products
     const uint32_t id_s = idesc_f8(kTile, false, false), id_o = idesc_f8(d, false, true);
@@ -100,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next(p, cs.plan, g)) {
-      ok = wait_warp(rs, &cs.qready, seg & 1);
+      ok = wait_warp(rs, &cs.qfull, seg & 1);
       ++seg;
       // S of the next tile, then O of the last
 #pragma unroll 1
@@ -147,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b = desc_mn(v0 + k * 4096);
 #pragma unroll
             for (int term = 0; term < 2; ++term) {
-              mma_f8_ts(tmem + kColO, w + term * 32 + k * 8, b, term == 0 ? id_o | kAE5m2 : id_o, acc);
+              mma_f8_ts(tmem + kColO, w + k / 2 * 64 + k % 2 * 16 + term * 8, b, term == 0 ? id_o | kAE5m2 : id_o, acc);
               acc = 1;
             }
           }
@@ -159,189 +260,223 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- softmax: warp w has lanes 32 (w % 4) .. and of their rows the tokens from kCols (w / 4)
-    const int quarter = warp & 3, share = warp >> 2, row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int per = (d / 16 + kParts - 1) / kParts * 16;  // O's columns of a warp
-    const int col0 = min(d, share * per), col1 = min(d, col0 + per);
+    // ---- softmax: a warp has lanes 32 (w % 4) .. and half of the tokens, of its set's tiles (even or odd ones)
+    const int quarter = warp & 3, hf = (warp >> 2) & 1, set = warp >> 3, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16), sc = lanes + kColS + set * kTile;
     const float factor = a.scale * 1.4426950408889634f;  // scores in powers of two
     auto all_sync = [] { named_bar_sync<1, kSoftThreads>(); };
-    // `op` over the parts of this thread's row
-    auto over_row = [&](int set, float v, auto op) {
-      cs.top[set][share * kTile + row] = v;
-      asm volatile("bar.sync %0, %1;" ::"r"(2 + quarter), "n"(32 * kParts) : "memory");
-      v = cs.top[set][row];
-#pragma unroll
-      for (int i = 1; i < kParts; ++i) v = op(v, cs.top[set][i * kTile + row]);
-      return v;
-    };
+    auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3) + 4 * set) : "memory"); };
 #pragma unroll 1
     while (walk.next(p, cs.plan, g)) {
-      // queries and tree
+      // tree and units
       const int rows = min(kTile, g.N * G - g.m * kTile);
-      if (t == 0) ds.bad_tree = 0, ds.no_number = 0, cs.segment = g;
-      if (g.t0 == 0) wait_warp(rs, &rs.cfull[gt % S], (gt / S) & 1);  // the stage is free
+      if (t == 0) ds.bad_tree = 0, ds.no_number = 0, cs.bad = 0, cs.segment = g;
       all_sync();
       load_tree(p, ds, g, t);
-      unsigned char* draft = ring + (gt % S) * Sh::kStage;
-      if (g.t0 == 0) {  // what the draft's tile has behind its values
-        const int last = g.N % kNodes;
-        if (last != 0) {
-          const int at = g.N / kNodes * kCols;
-          zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, at + last, at + kNodes);
-          zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, at + kNodes + last, at + kCols);
-        }
-        zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, (g.N + kNodes - 1) / kNodes * kCols, kTile);
-        if (t >= g.N && t < kMaxNodes) ds.ks[t] = 1.f, ds.lv[t] = ds.il[t] = 0.f;
+      if (t < kMaxNodes) {
+        const bool in = t < g.N;
+        const int64_t at = static_cast<int64_t>(g.h) * a.T + g.lo + t;
+        int v = in ? p.v_units[at] : 0;
+        ds.ks[t] = in ? pow2(p.k_units[at]) : 1.f;
+        if (v >= kNone / 2) v -= kNone, atomicOr(&ds.no_number, 1ull << t);
+        ds.lv[t] = static_cast<float>(v);
+        ds.il[t] = in ? pow2(-v) : 0.f;
       }
-      fill_rows<NH, kSoftWarps, 8>(p, ds, g, rows, factor, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
-        unsigned char* tile = kind == 0 ? smem : kind == 1 ? draft : draft + NH * kHalf;
-        const int token = i / kNodes * kCols + i % kNodes;
-        *operand8(tile, kind == 0 ? i : token, ln, kHalf) = hi;
-        *operand8(kind == 0 ? smem + NH * kHalf : tile, kind == 0 ? i : token + kNodes, ln, kHalf) = lo;
-      });
-      fence_proxy_async_smem();
+      float rowf = 0.f;
+      if (row < rows) rowf = pow2(p.q_units[(static_cast<int64_t>(g.h) * a.T + g.lo) * G + g.m * kTile + row]) * factor;
       all_sync();
-      if (t == 0) {
-        arrive(&cs.qready);
-        if (g.t0 == 0) {
-          arrive(&rs.kfull[gt % S]);
-          arrive(&rs.vfull[gt % S]);
-        }
-      }
       see(ds, g, t);
       all_sync();
 
       const bool bad_tree = ds.bad_tree != 0, alive = quarter * 32 < rows;
-      bool bad = bad_tree;
-      const float rowf = row < rows ? ds.rowf[row] : 0.f;
       float m = -INFINITY, sum = 0.f;
       const int t0 = g.t0, t1 = g.t1, len = g.len;
 #pragma unroll 1
       for (int j = t0; j < t1; ++j, ++gt) {
-        const int slot = gt % S, b = gt & 1;
+        const int slot = gt % S;
         const Consts& cc = rs.c[slot];
+        if ((gt & 1) != set) continue;
         // after a wait that gave up a warp still comes by every barrier of threads
-        bool ok = wait_warp(rs, &cs.sfull[b], (gt >> 1) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
+        bool ok = wait_warp(rs, &cs.sfull[set], (gt >> 1) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
         tc_fence_after_sync();
-        bad |= cc.bad != 0;
+        if (cc.bad != 0) cs.bad = 1;
         const int n = j == 0 ? kTile : min(kTile, len - (j - 1) * kTile);
         if (n < kTile && ok) ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1);
         if (n < kTile && ok) {  // values behind the context: anything, so none
-          const int end = (n + 31) & ~31;
           unsigned char* v = ring + slot * Sh::kStage + NH * kHalf;
 #pragma unroll 1
-          for (int i = n * 8 + t; i < end * 8; i += kSoftThreads)
+          for (int i = n * 8 + (t & 255); i < ((n + 31) & ~31) * 8; i += 32 * kSetWarps)
 #pragma unroll
             for (int x = 0; x < NH; ++x) *reinterpret_cast<uint4*>(v + x * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
-        if (alive) {
-          const uint32_t sc = lanes + kColS + b * kTile;
-          uint32_t r[kCols];
-          float* s = reinterpret_cast<float*>(r);
-          if (ok) {
-#pragma unroll
-            for (int x = 0; x < kCols; x += 32) tmem_ld32(sc + share * kCols + x, r + x);
-#pragma unroll
-            for (int x = 0; x < kCols; x += 32) tmem_wait32(r + x);
-          }
-          float rf = rowf;
-          if (j == 0) {  // scores here; the loading warp's constants of the tile are 1 and 0
-            rf = 1.f;
-            const Segment& now = cs.segment;
-            const uint32_t seen =
-                static_cast<uint32_t>(ds.seen[min(now.m * kTile + row, now.N * G - 1) / G] >> (kNodes * share));
-#pragma unroll
-            for (int i = 0; i < kNodes; ++i) {
-              const int q = share * kNodes + i;
-              const float y = (s[i] + s[kNodes + i]) * (ds.ks[q] * rowf) + ds.lv[q];
-              s[i] = s[kNodes + i] = (seen >> i) & 1 ? y : -INFINITY;
-            }
-          } else if (n < kTile) {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) s[i] = share * kCols + i < n ? s[i] : -INFINITY;
-          }
-          float f[kCols / 16], top = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < kCols / 16; ++q) {
-            float x = s[16 * q];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) x = fmaxf(x, s[16 * q + i]);
-            f[q] = fmaxf(cc.ks[share * (kCols / 16) + q] * rf, kLeast);
-            top = fmaxf(top, fmaf(x, f[q], cc.lv[share * (kCols / 16) + q]));
-          }
-          top = over_row(b, top, [](float x, float y) { return fmaxf(x, y); });
-          if (j == t0) {
-            m = top;
-          } else {
-            const bool grown = top > m + kGrowth;
-            if (__any_sync(kFull, grown)) {
-              const float down = grown ? ex2(m - top) : 1.f;
-              if (grown) m = top;
-              sum *= down;
-              wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
-              tc_fence_after_sync();
+        // the tile's maxima
+        float top = -INFINITY, rf = rowf;
+        if (alive && j == 0) {  // the draft's scores go back in the place of the products; the tile's constants are 1 and 0
+          rf = 1.f;
+          const Segment& now = cs.segment;
+          const uint32_t seen = static_cast<uint32_t>(ds.seen[min(now.m * kTile + row, now.N * G - 1) / G] >> (32 * hf));
 #pragma unroll 1
-              for (int x = col0; x < col1; x += 16) {
-                uint32_t o[16];
-                tmem_ld16_async(lanes + kColO + x, o);
-                tmem_wait16(o);
+          for (int x = 32 * hf; x < 32 * hf + 32; x += 16) {
+            uint32_t r[2][16];
+            tmem_ld16_async(sc + x, r[0]);
+            tmem_ld16_async(sc + 64 + x, r[1]);
+            tmem_wait16(r[0]);
+            tmem_wait16(r[1]);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * down);
-                tmem_st16(lanes + kColO + x, o);
-              }
-              tmem_wait_st();
+            for (int i = 0; i < 16; ++i) {
+              const float y = (__uint_as_float(r[0][i]) + __uint_as_float(r[1][i])) * (ds.ks[x + i] * rowf) + ds.lv[x + i];
+              const float s = (seen >> (x + i - 32 * hf)) & 1 ? y : -INFINITY;
+              top = fmaxf(top, s);
+              r[0][i] = __float_as_uint(s);
             }
-          }
-#pragma unroll
-          for (int q = 0; q < kCols / 16; ++q) {
-            const float e = cc.lv[share * (kCols / 16) + q] + (kBias - m);
-            float part_sum = 0.f;
-            uint32_t hi[4], lo[4];  // four codes each
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float* w = s + 16 * q + 4 * i;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                w[k] = ex2(fmaf(w[k], f[q], e));
-                part_sum += w[k];
-              }
-              uint32_t h0, l0, h1, l1;
-              weight_terms(w[0], w[1], h0, l0);
-              weight_terms(w[2], w[3], h1, l1);
-              hi[i] = __byte_perm(h0, h1, 0x7531);
-              lo[i] = l0 | (l1 << 16);
-            }
-            sum = fmaf(part_sum, cc.il[share * (kCols / 16) + q], sum);
-            tmem_st4(sc + share * (kCols / 4) + 4 * q, hi);
-            tmem_st4(sc + 32 + share * (kCols / 4) + 4 * q, lo);
-          }
-          if (j == 0) {
-#pragma unroll
-            for (int i = 0; i < kNodes; ++i) sum = fmaf(s[i], ds.il[share * kNodes + i], sum);
+            tmem_st16(sc + x, r[0]);
+            tmem_st16(sc + 64 + x, r[0]);
           }
           tmem_wait_st();
           tc_fence_before_sync();
+        } else if (alive) {
+#pragma unroll 1
+          for (int x = 64 * hf; x < 64 * hf + 64; x += 32) {
+            uint32_t r[32];
+            float* s = reinterpret_cast<float*>(r);
+            tmem_ld32(sc + x, r);
+            tmem_wait32(r);
+            if (n < kTile) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] = x + i < n ? s[i] : -INFINITY;
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = fmaxf(fmaxf(s[16 * q + i], s[16 * q + 4 + i]), fmaxf(s[16 * q + 8 + i], s[16 * q + 12 + i]));
+              const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+              top = fmaxf(top, fmaf(z, fmaxf(cc.ks[x / 16 + q] * rowf, kLeast), cc.lv[x / 16 + q]));
+            }
+          }
         }
-        warp_arrive(&cs.pready[b]);
+        // the rows' references, in the order of the tiles; both halves of a row have read the last one before it moves on
+        const bool start = j - t0 < 2;
+        float now = m;
+        if (!start) {
+          wait_warp(rs, &cs.mdone[set ^ 1], ((gt - 1) >> 1) & 1);
+          now = cs.ref[row];
+        }
+        cs.half[set][hf][row] = top;
+        pair_sync();
+        top = fmaxf(top, cs.half[set][hf ^ 1][row]);
+        bool grown = false;
+        float down = 1.f;
+        if (start) {  // the larger of the first two
+          if (hf == 0) cs.first[set][row] = top;
+          warp_arrive(&cs.mdone[set]);
+          if (t1 - t0 > 1) {
+            const int other = j == t0 ? gt + 1 : gt - 1;
+            wait_warp(rs, &cs.mdone[set ^ 1], (other >> 1) & 1);
+            top = fmaxf(top, cs.first[set ^ 1][row]);
+          }
+          m = top;
+          if (hf == 0 && j == t0) cs.ref[row] = top;  // the other set has it too, and reads this two tiles later
+        } else {
+          if (now != m) sum *= ex2(m - now), m = now;
+          grown = top > m + kGrowth;
+          if (grown) {
+            down = ex2(m - top);
+            sum *= down;
+            m = top;
+            if (hf == 0) cs.ref[row] = top;
+          }
+          warp_arrive(&cs.mdone[set]);
+        }
+        if (alive && __any_sync(kFull, grown)) {
+          wait_warp(rs, &cs.pvdone[set ^ 1], ((gt - 1) >> 1) & 1);
+          tc_fence_after_sync();
+          const int mid = (d / 16 + 1) / 2 * 16;
+#pragma unroll 1
+          for (int x = hf ? mid : 0; x < (hf ? d : mid); x += 16) {
+            uint32_t o[16];
+            tmem_ld16_async(lanes + kColO + x, o);
+            tmem_wait16(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * down);
+            tmem_st16(lanes + kColO + x, o);
+          }
+          tmem_wait_st();
+        }
+        if (alive) {
+          if (j == 0) tc_fence_after_sync();  // the other half's scores of the draft
+          // weights, 32 tokens at a time; their terms take the place of products that have been read
+#pragma unroll 1
+          for (int y = 0; y < 2; ++y) {
+            const int at = 64 * hf + 32 * y;
+            uint32_t r[32];
+            float* s = reinterpret_cast<float*>(r);
+            tmem_ld32(sc + at, r);
+            tmem_wait32(r);
+            if (n < kTile) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] = at + i < n ? s[i] : -INFINITY;
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float f = fmaxf(cc.ks[at / 16 + q] * rf, kLeast), e = cc.lv[at / 16 + q] + (kBias - m);
+              float part[4] = {0.f, 0.f, 0.f, 0.f};
+              uint32_t hi[4], lo[4];  // four codes each
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float* w = s + 16 * q + 4 * i;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  w[k] = ex2(fmaf(w[k], f, e));
+                  part[k] += w[k];
+                }
+                uint32_t h0, l0, h1, l1;
+                weight_terms(w[0], w[1], h0, l0);
+                weight_terms(w[2], w[3], h1, l1);
+                hi[i] = __byte_perm(h0, h1, 0x7531);
+                lo[i] = l0 | (l1 << 16);
+              }
+              sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), cc.il[at / 16 + q], sum);
+              tmem_st4(sc + 64 * hf + 16 * y + 4 * q, hi);
+              tmem_st4(sc + 64 * hf + 16 * y + 8 + 4 * q, lo);
+            }
+            if (j == 0 && hf == 0) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum = fmaf(s[i], ds.il[at + i], sum);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before_sync();
+        warp_arrive(&cs.pready[set]);
       }
 
       // ---- outputs
       g = cs.segment;
-      const int row0 = g.m * kTile, node = min(row0 + row, g.N * G - 1) / G;
+      const int row0 = g.m * kTile, node = min(row0 + row, g.N * G - 1) / G, part = set * 2 + hf;
+      const int per = (d / 16 + kParts - 1) / kParts * 16, col0 = min(d, part * per), col1 = min(d, col0 + per);  // O's columns of a warp
       const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-      const bool ok = wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
+      // the last two tiles in their order: a set that did not take the last one may come here two phases early
+      bool ok = gt < 2 || wait_warp(rs, &cs.pvdone[gt & 1], ((gt - 2) >> 1) & 1);
+      ok = wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1) && ok;
       tc_fence_after_sync();
-      // not the set of the last tile, which another warp may still read
-      if (alive) sum = over_row(gt & 1, sum, [](float x, float y) { return x + y; });
+      const unsigned long long no_number = ds.no_number;  // before the next segment's
+      cs.sum[part][row] = m == -INFINITY ? 0.f : sum * ex2(m - cs.ref[row]);  // a set may have had no tile
+      all_sync();
+      m = cs.ref[row];
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) sum += cs.sum[i][row];
+      const bool bad = bad_tree || cs.bad != 0;
       const float inv = 1.f / sum;
       if (ok && alive) {
         const int64_t out = ((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + (row0 + row) % G) * d;
         const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
         float* po = p.part_o + (piece * p.rows_cap + row) * d;
-        const bool write = row < rows && !bad;
-        const unsigned long long none = g.t0 == 0 && write ? ds.no_number & ds.seen[node] : 0;
+        const bool write = row < min(kTile, g.N * G - row0) && !bad;
+        const unsigned long long none = g.t0 == 0 && write ? no_number & ds.seen[node] : 0;
 #pragma unroll 1
         for (int x = col0; x < col1; x += 16) {
           uint32_t o[16];
@@ -382,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i) static_cast<__nv_bfloat16*>(a.o)[out + x + i] = __float2bfloat16_rn(y[i]);
           }
         }
-        if (write && !whole && share == 0) p.part_lse[piece * p.rows_cap + row] = m + log2f(sum);
+        if (write && !whole && part == 0) p.part_lse[piece * p.rows_cap + row] = m + log2f(sum);
         tc_fence_before_sync();
       }
       if (whole && p.wide_o) {
@@ -392,14 +527,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           int head = (row0 + warp * kEach) % G;
           __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.o) + ((static_cast<int64_t>(g.lo) + (row0 + warp * kEach) / G) * a.Hq + g.h * G) * d;
 #pragma unroll 4
-          for (int i = warp * kEach; i < min(rows, warp * kEach + kEach); ++i) {
+          for (int i = warp * kEach; i < min(min(kTile, g.N * G - row0), warp * kEach + kEach); ++i) {
             if (8 * lane < d)
               reinterpret_cast<uint4*>(to + head * d)[lane] = *reinterpret_cast<const uint4*>(smem + i * (NH * 256) + ((lane ^ (i & 7)) << 4));
             if (++head == G) head = 0, to += static_cast<int64_t>(a.Hq) * d;
           }
         }
       }
-      if (ok && t == 0) report(p, mine, walk, g, rows, bad_tree, bad);
+      if (ok && t == 0) report(p, mine, walk, g, min(kTile, g.N * G - row0), bad_tree, bad);
+      fence_proxy_async_smem();  // the queries' place is read from and written to here
+      warp_arrive(&cs.qfree);
     }
   }
 
@@ -409,7 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       walk = mine.walk;
       while (walk.next(p, cs.plan, g)) atomicOr(a.status + g.r, TREEWY_STATUS_TIMEOUT);
     }
-    if (warp == kLoadWarp) drain_copies(rs.kfull, armed);
+    if (warp == kLoadWarp) {
+      drain_copies(rs.kfull, armed);
+      if (queries > 0) mbar_wait_for(&cs.qfull, (queries - 1) & 1, 20000000ull);
+    }
     if (warp == kLoadWarp + 1) drain_copies(rs.vfull, armed);
     if (warp == kMmaWarp) {
       if (elect_one()) mma_commit(&cs.drain);
@@ -484,26 +624,48 @@ int rows_cap(const treewy_attn& a) {
   return static_cast<int>(std::min<int64_t>(kTile, static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv)));
 }
 
-bool make_map(CUtensorMap* map, const void* codes, const treewy_cache& c) {
+bool make_map(CUtensorMap* map, const void* codes, int d, int rows, int64_t blocks, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (enc == nullptr) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page_len),
-                              static_cast<cuuint64_t>(c.num_pages * c.Hkv)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.d) * c.page_len};
-  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(c.page_len), 1}, ones[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(d) * static_cast<cuuint64_t>(rows)};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool few_rows(const treewy_attn& a) { return static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv) <= kFewRows; }
+// A 16-byte aligned address beside p, for a map that nothing is read through.
+void* any16(const void* p) { return reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15)); }
+uint64_t up256(uint64_t n) { return (n + 255) & ~uint64_t(255); }
+
+// Where things are in the workspace: the parts of items in several pieces, then the terms.
+struct Workspace {
+  uint64_t record, lse, q_terms, k_terms, v_terms, q_units, k_units, v_units, end;
+  explicit Workspace(const treewy_attn& a) {
+    const uint64_t rows = listed(a) ? static_cast<uint64_t>(kMaxPieces) * 2 * rows_cap(a) : 0;
+    const uint64_t T = few_rows(a) ? 0 : static_cast<uint64_t>(std::max<int64_t>(a.T, 1)), q = T * a.Hq, kv = T * a.cache.Hkv, d = a.cache.d;
+    record = up256(rows * d * 4);
+    lse = record + (rows > 0 ? kMaxPieces * 8 * 4 : 0);
+    q_terms = up256(lse + rows * 4);
+    k_terms = up256(q_terms + 2 * q * d);
+    v_terms = up256(k_terms + 2 * kv * d);
+    q_units = up256(v_terms + 2 * kv * d);
+    k_units = up256(q_units + 2 * q);
+    v_units = up256(k_units + 2 * kv);
+    end = v_units + 2 * kv;
+  }
+};
+
 template <int NH>
-cudaError_t launch(const Params& p, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, cudaStream_t stream) {
+cudaError_t launch(const Params& p, const Maps& maps, unsigned grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {
     return cudaFuncSetAttribute(attend_tc_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NH>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  return launch_after_smem(attend_tc_kernel<NH>, dim3(grid), kThreads, Shape<NH>::kBytes, stream, p, k, v);
+  return launch_after_smem(attend_tc_kernel<NH>, dim3(grid), kThreads, Shape<NH>::kBytes, stream, p, maps);
 }
 
 }  // namespace
@@ -513,10 +675,7 @@ bool attend_on_tensor_cores(const treewy_attn& a) {
          (a.flags & TREEWY_FLAG_FORCE_GENERIC) == 0;
 }
 
-uint64_t attend_workspace(const treewy_attn& a) {
-  if (a.R == 0 || !attend_on_tensor_cores(a) || !listed(a)) return 0;
-  return static_cast<uint64_t>(kMaxPieces) * (2ull * rows_cap(a) * (a.cache.d + 1) * 4 + 8 * 4);
-}
+uint64_t attend_workspace(const treewy_attn& a) { return a.R == 0 || !attend_on_tensor_cores(a) ? 0 : Workspace(a).end; }
 
 cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
   Params p = {};
@@ -527,12 +686,15 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
   p.rows_cap = rows_cap(a);
   auto wide = [](const void* x, int64_t stride) { return reinterpret_cast<uintptr_t>(x) % 16 == 0 && stride % 8 == 0 ? 1 : 0; };
   p.wide_q = wide(a.q, a.q_stride), p.wide_k = wide(a.k, a.k_stride), p.wide_v = wide(a.v, a.v_stride), p.wide_o = wide(a.o, 0);
-  if (p.listed) {
-    const size_t rows = static_cast<size_t>(kMaxPieces) * 2 * p.rows_cap;
-    p.part_o = static_cast<float*>(a.workspace);
-    p.record = reinterpret_cast<int*>(p.part_o + rows * a.cache.d);
-    p.part_lse = reinterpret_cast<float*>(p.record + 8 * kMaxPieces);
-  }
+  const Workspace at(a);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.record = reinterpret_cast<int*>(ws + at.record);
+  p.part_lse = reinterpret_cast<float*>(ws + at.lse);
+  p.q_terms = ws + at.q_terms, p.k_terms = ws + at.k_terms, p.v_terms = ws + at.v_terms;
+  p.q_units = reinterpret_cast<int16_t*>(ws + at.q_units);
+  p.k_units = reinterpret_cast<int16_t*>(ws + at.k_units);
+  p.v_units = reinterpret_cast<int16_t*>(ws + at.v_units);
   unsigned grid;
   if (p.listed) {
     int dev = 0, sms = 0;
@@ -545,15 +707,32 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
     if (items > 0x7fffffff / a.R) return cudaErrorNotSupported;
     grid = static_cast<unsigned>(items * a.R);
   }
-  CUtensorMap k, v;
+  const bool few = few_rows(a);
+  const int64_t T = std::max<int64_t>(a.T, 1);
+  if (!few && T * a.Hq > 0x7fffffff) return cudaErrorNotSupported;
+  Maps maps;
   // a cache without pages has none to read: its requests are short or refused
-  treewy_cache c = a.cache;
-  if (c.num_pages == 0) c.num_pages = 1, c.k = c.v = const_cast<void*>(a.q);
-  if (!make_map(&k, c.k, c) || !make_map(&v, c.v, c)) return cudaErrorUnknown;
-  const bool few = static_cast<int64_t>(a.max_nodes) * p.G <= kFewRows;
-  const cudaError_t e = few                ? launch_attend_few(p, k, v, grid, stream)
-                        : a.cache.d > 128 ? launch<2>(p, k, v, grid, stream)
-                                          : launch<1>(p, k, v, grid, stream);
+  const treewy_cache& c = a.cache;
+  const int64_t blocks = std::max<int64_t>(c.num_pages, 1) * c.Hkv;
+  const void* any = c.num_pages > 0 ? nullptr : a.node_offset;
+  if (!make_map(&maps.k, any ? any16(any) : c.k, c.d, c.page_len, blocks, c.page_len) ||
+      !make_map(&maps.v, any ? any16(any) : c.v, c.d, c.page_len, blocks, c.page_len))
+    return cudaErrorUnknown;
+  cudaError_t e;
+  if (few) {
+    e = launch_attend_few(p, maps.k, maps.v, grid, stream);
+  } else {
+    if (!make_map(&maps.q_terms, p.q_terms, c.d, static_cast<int>(T * a.Hq), 2, kTile) ||
+        !make_map(&maps.k_terms, p.k_terms, c.d, static_cast<int>(T * c.Hkv), 2, kMaxNodes) ||
+        !make_map(&maps.v_terms, p.v_terms, c.d, static_cast<int>(T * c.Hkv), 2, kMaxNodes))
+      return cudaErrorUnknown;
+    const int64_t rows = a.T * (a.Hq + 2 * static_cast<int64_t>(c.Hkv)), ctas = std::min<int64_t>((rows + 31) / 32, 8 * kMaxPieces);
+    if (ctas > 0) {
+      e = launch_after(attend_split_kernel, dim3(static_cast<unsigned>(ctas)), kSplitThreads, stream, p);
+      if (e != cudaSuccess) return e;
+    }
+    e = c.d > 128 ? launch<2>(p, maps, grid, stream) : launch<1>(p, maps, grid, stream);
+  }
   if (e != cudaSuccess || !p.listed) return e;
   return launch_after(attend_join_kernel, dim3(p.rows_cap, grid), 256, stream, p);
 }

@@ -267,6 +267,9 @@ struct Params {
   float* part_o;         // [kMaxPieces][2][rows_cap][d]
   float* part_lse;       // [kMaxPieces][2][rows_cap]; infinity: refused
   int* record;           // [kMaxPieces][8]: the item that begins in a piece and ends in a later one
+  // of attend_split_kernel: terms e4m3 [2][Hkv][T][G][d] (G = 1: keys and values), and their units' exponents
+  uint8_t *q_terms, *k_terms, *v_terms;
+  int16_t *q_units, *k_units, *v_units;
 };
 
 // The tiles of one item that a CTA takes.
@@ -393,10 +396,12 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
 // A loading warp: the keys (or the values, with the pages' scales) of every
 // tile of the CTA's segments into the ring's stages (K's halves of 128 columns,
 // then V's).  Lane i has the i-th of 32 pages of the context, and the next
-// 32's, asked for ahead.  Returns the tiles up to which copies have been
-// started.
-template <bool kValues, int NH, int S, typename Cs>
-__device__ __forceinline__ int load_pages(const Params& p, Cs& cs, RingSmem<S>& rs, Walk walk, unsigned char* ring, const CUtensorMap& map) {
+// 32's, asked for ahead.  begin(g) comes before a segment's tiles, draft(g, gt,
+// slot, again) in the place of the draft's; false: a wait of theirs gave up.
+// Returns the tiles up to which copies have been started.
+template <bool kValues, int NH, int S, typename Cs, typename Begin, typename Draft>
+__device__ __forceinline__ int load_pages(const Params& p, Cs& cs, RingSmem<S>& rs, Walk walk, unsigned char* ring, const CUtensorMap& map,
+                                          Begin begin, Draft draft) {
   const treewy_cache& c = p.a.cache;
   constexpr uint32_t kStage = 2 * NH * kHalf;
   const int lane = threadIdx.x & 31, P = c.page_len, per = kTile / P;
@@ -407,6 +412,7 @@ __device__ __forceinline__ int load_pages(const Params& p, Cs& cs, RingSmem<S>& 
   Segment g;
 #pragma unroll 1
   while (walk.next(p, cs.plan, g)) {
+    if (!begin(g)) return armed;
     const int32_t* table = c.page_table + static_cast<int64_t>(g.r) * c.max_pages;
     const int pages = (g.len + P - 1) / P;
     auto entry = [&](int i) { return i < pages ? __ldg(table + i) : -1; };
@@ -420,9 +426,9 @@ __device__ __forceinline__ int load_pages(const Params& p, Cs& cs, RingSmem<S>& 
 #pragma unroll 1
     for (int j = g.t0; j < g.t1; ++j, ++gt) {
       if (gt >= S && !wait_warp(rs, &free[slot], again)) return armed;
-      if (j == 0) {  // the draft's tile: the softmax warps fill it
+      if (j == 0) {
+        if (!draft(g, gt, slot, again)) return armed;
         if constexpr (kValues) {
-          if (gt >= S && !wait_warp(rs, &rs.kfree[slot], again)) return armed;
           if (lane < kGroups) rs.c[slot].ks[lane] = 1.f, rs.c[slot].lv[lane] = rs.c[slot].il[lane] = 0.f;
           if (lane == 0) rs.c[slot].bad = 0;
           warp_arrive(&rs.cfull[slot]);

@@ -566,8 +566,8 @@ typedef struct treewy_attn {
 treewy_status treewy_attend(const treewy_attn* attn, cudaStream_t stream);
 
 /* Bytes of workspace that treewy_attend needs for arguments of these sizes
-   (R, Hq, max_nodes, the types and the cache's sizes are read, no pointers):
-   on a card of any number of SMs, and for any contents. */
+   (R, T, Hq, max_nodes, max_context, the types, flags and the cache's sizes are
+   read, no pointers): on a card of any number of SMs, and for any contents. */
 treewy_status treewy_attend_workspace(const treewy_attn* attn, uint64_t* bytes);
 
 /*
