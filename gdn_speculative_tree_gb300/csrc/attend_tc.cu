@@ -36,52 +36,48 @@ constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kParts = kSoftWarps / 4;  // warps that share 32 rows
 constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
 
-// Terms of every row: a warp takes a row, (head, token) and whether it is a
-// query, a key or a value.  Units are the exponents of a row's power of two,
-// kNone above them where a value's row has something that is no number.
-constexpr int kNone = 1024, kSplitThreads = 256;
-__global__ void __launch_bounds__(kSplitThreads) attend_split_kernel(const __grid_constant__ Params p) {
+// Terms of every row: a warp takes four rows of a token (its query heads, then
+// key heads, keys and values) at a time.  Units are the exponents of a row's
+// power of two, kNone above them where a value's row has something that is no
+// number.  Bound by HBM: every row is read and written once.
+constexpr int kNone = 1024, kSplitThreads = 256, kSplitRows = 4;
+__global__ void __launch_bounds__(kSplitThreads) attend_split_kernel(const __grid_constant__ Params p, int groups) {
   after_previous();
   const treewy_attn& a = p.a;
-  const int lane = threadIdx.x & 31, d = a.cache.d, G = p.G, Hkv = a.cache.Hkv;
-  const int64_t T = a.T, queries = T * a.Hq, rows = queries + 2 * T * Hkv;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kSplitThreads / 32);
-  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 31, d = a.cache.d, G = p.G, Hkv = a.cache.Hkv, heads = a.Hq + 2 * Hkv;
+  const unsigned T = static_cast<unsigned>(a.T), jobs = T * groups;
 #pragma unroll 1
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (kSplitThreads / 32) + (threadIdx.x >> 5); r0 < rows; r0 += kBatch * step) {
-    uint4 x[kBatch];
-    int64_t to[kBatch];
+  for (unsigned job = blockIdx.x * (kSplitThreads / 32) + (threadIdx.x >> 5); job < jobs; job += gridDim.x * (kSplitThreads / 32)) {
+    const unsigned token = job / groups;
+    const int first = static_cast<int>(job - token * groups) * kSplitRows;
+    uint4 x[kSplitRows];
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int64_t r = r0 + e * step;
-      if (r >= rows) continue;
-      // rows as they are stored, token by token
-      const int kind = r < queries ? 0 : r < queries + T * Hkv ? 1 : 2, heads = kind == 0 ? a.Hq : Hkv;
-      const int64_t i = r - (kind == 0 ? 0 : kind == 1 ? queries : queries + T * Hkv), token = i / heads;
-      const int head = static_cast<int>(i - token * heads);
+    for (int e = 0; e < kSplitRows; ++e) {
+      const int head = first + e;
+      if (head >= heads) continue;
+      const int kind = head < a.Hq ? 0 : head < a.Hq + Hkv ? 1 : 2, h = head - (kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + Hkv);
       const uint16_t* from = static_cast<const uint16_t*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                             token * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + static_cast<int64_t>(head) * d;
+                             token * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + static_cast<int64_t>(h) * d;
       const bool wide = kind == 0 ? p.wide_q : kind == 1 ? p.wide_k : p.wide_v;
       x[e] = wide ? load_row8(from, 8 * lane, d) : load_row8_odd(from, 8 * lane, d);
-      const int g = kind == 0 ? G : 1;
-      to[e] = (head / g * T + token) * g + head % g;
     }
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int64_t r = r0 + e * step;
-      if (r >= rows) continue;
-      const int kind = r < queries ? 0 : r < queries + T * Hkv ? 1 : 2;
+    for (int e = 0; e < kSplitRows; ++e) {
+      const int head = first + e;
+      if (head >= heads) continue;
+      const int kind = head < a.Hq ? 0 : head < a.Hq + Hkv ? 1 : 2, h = head - (kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + Hkv);
+      const unsigned g = kind == 0 ? G : 1, hk = h / g, to = (hk * T + token) * g + (h - hk * g);
       uint2 hi, lo;
       bool none;
       // a value that is no number would reach the nodes that do not see it: weights of zero times it
       int unit = row_terms(x[e], kind == 2, hi, lo, none);
       if (kind == 2 && none) unit += kNone;
-      uint8_t* terms = (kind == 0 ? p.q_terms : kind == 1 ? p.k_terms : p.v_terms) + to[e] * d + 8 * lane;
+      uint8_t* terms = (kind == 0 ? p.q_terms : kind == 1 ? p.k_terms : p.v_terms) + static_cast<int64_t>(to) * d + 8 * lane;
       if (8 * lane < d) {
         *reinterpret_cast<uint2*>(terms) = hi;
-        *reinterpret_cast<uint2*>(terms + (kind == 0 ? queries : T * Hkv) * d) = lo;
+        *reinterpret_cast<uint2*>(terms + static_cast<int64_t>(T) * (kind == 0 ? a.Hq : Hkv) * d) = lo;
       }
-      if (lane == 0) (kind == 0 ? p.q_units : kind == 1 ? p.k_units : p.v_units)[to[e]] = static_cast<int16_t>(unit);
+      if (lane == 0) (kind == 0 ? p.q_units : kind == 1 ? p.k_units : p.v_units)[to] = static_cast<int16_t>(unit);
     }
   }
 }
@@ -422,15 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               const float f = fmaxf(cc.ks[at / 16 + q] * rf, kLeast), e = cc.lv[at / 16 + q] + (kBias - m);
-              float part[4] = {0.f, 0.f, 0.f, 0.f};
+              float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
               uint32_t hi[4], lo[4];  // four codes each
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 float* w = s + 16 * q + 4 * i;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  w[k] = ex2(fmaf(w[k], f, e));
-                  part[k] += w[k];
+                for (int k = 0; k < 4; k += 2) {
+                  const float2 y = fma2(make_float2(w[k], w[k + 1]), make_float2(f, f), make_float2(e, e));
+                  w[k] = ex2(y.x), w[k + 1] = ex2(y.y);
+                  part[k / 2] = add2(part[k / 2], make_float2(w[k], w[k + 1]));
                 }
                 uint32_t h0, l0, h1, l1;
                 weight_terms(w[0], w[1], h0, l0);
@@ -438,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 hi[i] = __byte_perm(h0, h1, 0x7531);
                 lo[i] = l0 | (l1 << 16);
               }
-              sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), cc.il[at / 16 + q], sum);
+              sum = fmaf((part[0].x + part[0].y) + (part[1].x + part[1].y), cc.il[at / 16 + q], sum);
               tmem_st4(sc + 64 * hf + 16 * y + 4 * q, hi);
               tmem_st4(sc + 64 * hf + 16 * y + 8 + 4 * q, lo);
             }
@@ -709,7 +706,7 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
   }
   const bool few = few_rows(a);
   const int64_t T = std::max<int64_t>(a.T, 1);
-  if (!few && T * a.Hq > 0x7fffffff) return cudaErrorNotSupported;
+  if (!few && T * (a.Hq + 2 * static_cast<int64_t>(a.cache.Hkv)) > 0x7fffffff) return cudaErrorNotSupported;
   Maps maps;
   // a cache without pages has none to read: its requests are short or refused
   const treewy_cache& c = a.cache;
@@ -726,9 +723,10 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
         !make_map(&maps.k_terms, p.k_terms, c.d, static_cast<int>(T * c.Hkv), 2, kMaxNodes) ||
         !make_map(&maps.v_terms, p.v_terms, c.d, static_cast<int>(T * c.Hkv), 2, kMaxNodes))
       return cudaErrorUnknown;
-    const int64_t rows = a.T * (a.Hq + 2 * static_cast<int64_t>(c.Hkv)), ctas = std::min<int64_t>((rows + 31) / 32, 8 * kMaxPieces);
-    if (ctas > 0) {
-      e = launch_after(attend_split_kernel, dim3(static_cast<unsigned>(ctas)), kSplitThreads, stream, p);
+    const int groups = (a.Hq + 2 * c.Hkv + kSplitRows - 1) / kSplitRows;
+    if (a.T > 0) {
+      const int64_t ctas = std::min<int64_t>((a.T * groups + 7) / 8, 16 * kMaxPieces);
+      e = launch_after(attend_split_kernel, dim3(static_cast<unsigned>(ctas)), kSplitThreads, stream, p, groups);
       if (e != cudaSuccess) return e;
     }
     e = c.d > 128 ? launch<2>(p, maps, grid, stream) : launch<1>(p, maps, grid, stream);
