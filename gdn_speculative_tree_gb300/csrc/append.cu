@@ -20,24 +20,6 @@ __device__ __forceinline__ float to_f32(T x) {
   else return x;
 }
 
-// Eight values of a row, in f32.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(u[e] << 16);
-      x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
-}
-
 // x in units of a scale, as e4m3; what is not finite becomes NaN.
 struct Quantizer {
   float scale, inv;
@@ -49,19 +31,71 @@ struct Quantizer {
   __device__ uint32_t pair(float a, float b) const { return e4m3x2(unit(a), unit(b)); }
 };
 
-template <typename T, int VEC>
-__global__ void __launch_bounds__(256) append_kernel(const treewy_append_args a, int pages) {
+// Eight neighbouring values of a row, as they are stored.
+template <typename T>
+struct Piece {
+  uint4 w[sizeof(T) / 2];
+  __device__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) {
+          x[2 * e] = __uint_as_float(u[e] << 16);
+          x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+        } else {
+          x[4 * i + e] = __uint_as_float(u[e]);
+        }
+      }
+    }
+  }
+  __device__ float largest() const {
+    float x[8], top = 0.f;
+    values(x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, size_of(x[e]));
+    return top;
+  }
+  __device__ uint2 codes(const Quantizer& z) const {
+    float x[8];
+    values(x);
+    return make_uint2(z.pair(x[0], x[1]) | (z.pair(x[2], x[3]) << 16), z.pair(x[4], x[5]) | (z.pair(x[6], x[7]) << 16));
+  }
+};
+
+// Four codes times f (2^-n), rounded again where they leave e4m3's normal range.
+__device__ __forceinline__ uint32_t again(uint32_t w, float f) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t h = e4m3x2_to_f16x2((w >> (16 * i)) & 0xffffu);
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    out |= e4m3x2(y.x * f, y.y * f) << (16 * i);
+  }
+  return out;
+}
+
+// HOLD: pieces of eight values that a thread keeps from the search for the
+// largest to the writing, what is behind them is read twice; 0: one value at a
+// time, read twice (odd sizes).
+template <typename T, int HOLD>
+__global__ void __launch_bounds__(256, HOLD == 8 && sizeof(T) == 2 ? 3 : 1) append_kernel(const treewy_append_args a, int pages) {
   after_previous();
   __shared__ int parent[kMaxNodes], path[kMaxNodes], count;
   __shared__ float part[8];
   const treewy_cache& c = a.cache;
-  const int t = threadIdx.x, P = c.page_len, d = c.d;
-  // pages of one head are neighbours, then keys and values, heads, requests
-  const int i = static_cast<int>(blockIdx.x % pages);
-  unsigned rest = blockIdx.x / pages;
+  const int t = threadIdx.x, P = c.page_len, d = c.d, threads = blockDim.x;
+  // heads are neighbours as they are in a row, then keys and values, pages, requests
+  const int h = static_cast<int>(blockIdx.x % c.Hkv);
+  unsigned rest = blockIdx.x / c.Hkv;
   const bool values = rest & 1;
   rest >>= 1;
-  const int h = static_cast<int>(rest % c.Hkv), r = static_cast<int>(rest / c.Hkv);
+  const int i = static_cast<int>(rest % pages), r = static_cast<int>(rest / pages);
   const bool first_cta = i == 0 && h == 0 && !values && t == 0;
   CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_new, INT32_MAX);
   int m = q.N;  // rows that are taken
@@ -80,13 +114,39 @@ __global__ void __launch_bounds__(256) append_kernel(const treewy_append_args a,
       m = count;
     }
   }
+  // what goes into this CTA's page
   const int first = q.len / P;
+  const int64_t begin = static_cast<int64_t>(first + i) * P, after = static_cast<int64_t>(q.len) + m;
+  const int lo = max(0, static_cast<int>(q.len - begin));  // tokens that it holds already
+  const int hi = static_cast<int>(min(static_cast<int64_t>(P), after - begin));
+  const bool mine = q.err == 0 && m > 0 && begin < after;
+  const int j0 = static_cast<int>(begin + lo - q.len);       // the first new one
+  const T* rows = static_cast<const T*>(values ? a.v : a.k) + static_cast<int64_t>(h) * d;
+  const int64_t stride = values ? a.v_stride : a.k_stride;
+  auto row_of = [&](int s) {  // of the page's row s
+    const int j = j0 + s - lo;
+    return rows + (static_cast<int64_t>(q.lo) + (a.accepted != nullptr ? path[j] : j)) * stride;
+  };
+  // a thread's pieces: its first row and column, and the way to the next ones
+  const int per = HOLD > 0 ? d / 8 : d, row0 = t / per, col0 = t - row0 * per, down = threads / per, right = threads - down * per;
+  Piece<T> x[HOLD > 0 ? HOLD : 1];
+  float top = 0.f;
+  if (mine) {
+    if constexpr (HOLD > 0) {  // on their way while the pages are looked at
+      int s = lo + row0, col = col0;
+#pragma unroll
+      for (int e = 0; e < HOLD; ++e) {
+        if (s < hi) x[e].load(row_of(s) + 8 * col);
+        s += down, col += right;
+        if (col >= per) col -= per, ++s;
+      }
+    }
+  }
   if (q.err == 0 && m > 0) {
-    const int64_t after = static_cast<int64_t>(q.len) + m;
     bool bad = after > static_cast<int64_t>(c.max_pages) * P || after > INT32_MAX;
     if (!bad) {
       const int last = static_cast<int>((after - 1) / P);
-      for (int p = first + t; p <= last; p += blockDim.x) {
+      for (int p = first + t; p <= last; p += threads) {
         const int page = __ldg(c.page_table + static_cast<int64_t>(r) * c.max_pages + p);
         bad |= page < 0 || page >= c.num_pages;
       }
@@ -97,63 +157,96 @@ __global__ void __launch_bounds__(256) append_kernel(const treewy_append_args a,
     if (first_cta) atomicOr(a.status + r, q.err);
     return;
   }
-  if (first_cta && a.new_length != nullptr) a.new_length[r] = q.len + m;
-  const int64_t begin = static_cast<int64_t>(first + i) * P;  // the page's first token
-  if (begin >= static_cast<int64_t>(q.len) + m) return;
-  const int lo = max(0, static_cast<int>(q.len - begin));       // tokens that it holds already
-  const int hi = static_cast<int>(min(static_cast<int64_t>(P), static_cast<int64_t>(q.len) + m - begin));
-  const int j0 = static_cast<int>(begin + lo - q.len);            // the first new one
+  if (first_cta && a.new_length != nullptr) a.new_length[r] = static_cast<int>(after);
+  if (!mine) return;
   const int page = __ldg(c.page_table + static_cast<int64_t>(r) * c.max_pages + first + i);
   const int64_t block = static_cast<int64_t>(page) * c.Hkv + h;
   uint8_t* codes = static_cast<uint8_t*>(values ? c.v : c.k) + block * P * d;
   float* scale = (values ? c.v_scale : c.k_scale) + block;
-  const T* rows = static_cast<const T*>(values ? a.v : a.k) + static_cast<int64_t>(h) * d;
-  const int64_t stride = values ? a.v_stride : a.k_stride;
-  auto row_of = [&](int s) {  // of the page's row s
-    const int j = j0 + s - lo;
-    return rows + (static_cast<int64_t>(q.lo) + (a.accepted != nullptr ? path[j] : j)) * stride;
-  };
-  const int per = d / VEC, total = (hi - lo) * per;
-  float top = 0.f;
-  for (int x = t; x < total; x += blockDim.x) {
-    const T* p = row_of(lo + x / per) + (x % per) * VEC;
-    if constexpr (VEC == 8) {
-      float f[8];
-      load8(p, f);
+  const float was = lo > 0 ? *scale : 0.f;
+  {
+    int s = lo + row0, col = col0;
+    if constexpr (HOLD > 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, size_of(f[e]));
+      for (int e = 0; e < HOLD; ++e) {
+        if (s < hi) top = fmaxf(top, x[e].largest());
+        s += down, col += right;
+        if (col >= per) col -= per, ++s;
+      }
+#pragma unroll 2
+      while (s < hi) {
+        Piece<T> y;
+        y.load(row_of(s) + 8 * col);
+        top = fmaxf(top, y.largest());
+        s += down, col += right;
+        if (col >= per) col -= per, ++s;
+      }
     } else {
-      top = fmaxf(top, size_of(to_f32(__ldg(p))));
+      while (s < hi) {
+        top = fmaxf(top, size_of(to_f32(__ldg(row_of(s) + col))));
+        s += down, col += right;
+        if (col >= per) col -= per, ++s;
+      }
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if ((t & 31) == 0) part[t >> 5] = top;
-  const float was = lo > 0 ? *scale : 0.f;
   __syncthreads();  // and every thread has read the scale
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) top = fmaxf(top, part[w]);
+  for (int w = 0; w < threads >> 5; ++w) top = fmaxf(top, part[w]);
   float now = was;
   if (lo == 0) now = scale_for(top);
   else if (!(top <= 448.f * was)) now = fmaxf(was, scale_for(top));
   if (t == 0) *scale = now;
   const Quantizer z{now, 1.f / now, (__float_as_uint(now) & 0x7fffffu) == 0};
-  for (int x = t; x < total; x += blockDim.x) {
-    const int s = lo + x / per, col = (x % per) * VEC;
-    const T* p = row_of(s) + col;
-    if constexpr (VEC == 8) {
-      float f[8];
-      load8(p, f);
-      const uint2 w = make_uint2(z.pair(f[0], f[1]) | (z.pair(f[2], f[3]) << 16), z.pair(f[4], f[5]) | (z.pair(f[6], f[7]) << 16));
-      *reinterpret_cast<uint2*>(codes + s * d + col) = w;
+  {
+    int s = lo + row0, col = col0;
+    if constexpr (HOLD > 0) {
+#pragma unroll
+      for (int e = 0; e < HOLD; ++e) {
+        if (s < hi) *reinterpret_cast<uint2*>(codes + s * d + 8 * col) = x[e].codes(z);
+        s += down, col += right;
+        if (col >= per) col -= per, ++s;
+      }
+#pragma unroll 2
+      while (s < hi) {
+        Piece<T> y;
+        y.load(row_of(s) + 8 * col);
+        *reinterpret_cast<uint2*>(codes + s * d + 8 * col) = y.codes(z);
+        s += down, col += right;
+        if (col >= per) col -= per, ++s;
+      }
     } else {
-      codes[s * d + col] = static_cast<uint8_t>(z.pair(to_f32(__ldg(p)), 0.f));
+      while (s < hi) {
+        codes[s * d + col] = static_cast<uint8_t>(z.pair(to_f32(__ldg(row_of(s) + col)), 0.f));
+        s += down, col += right;
+        if (col >= per) col -= per, ++s;
+      }
     }
   }
   if (now != was && lo > 0) {  // the scale has grown: the older tokens anew
     const float f = was / now;
-    for (int x = t; x < lo * d; x += blockDim.x)
-      codes[x] = static_cast<uint8_t>(e4m3x2(e4m3_to_float(codes[x]) * f, 0.f));
+    if constexpr (HOLD > 0) {
+      for (int k = t; k < lo * d / 8; k += threads) {
+        uint2* at = reinterpret_cast<uint2*>(codes) + k;
+        const uint2 old = *at;
+        *at = make_uint2(again(old.x, f), again(old.y, f));
+      }
+    } else {
+      for (int k = t; k < lo * d; k += threads) codes[k] = static_cast<uint8_t>(e4m3x2(e4m3_to_float(codes[k]) * f, 0.f));
+    }
   }
+}
+
+template <typename T>
+cudaError_t launch(const treewy_append_args& a, bool wide, dim3 grid, int pages, cudaStream_t stream) {
+  if (!wide) return launch_after(append_kernel<T, 0>, grid, 256, stream, a, pages);
+  // paths are short whatever the trees' bound is
+  const int rows = std::min(a.max_new, a.cache.page_len), pieces = (a.accepted != nullptr ? std::min(rows, 8) : rows) * (a.cache.d / 8);
+  // CTAs of two warps where a page gets little; of eight, with most of a page in registers, where it gets much
+  if (pieces <= 64) return launch_after(append_kernel<T, 1>, grid, 64, stream, a, pages);
+  if (pieces <= 512) return launch_after(append_kernel<T, 4>, grid, 128, stream, a, pages);
+  return launch_after(append_kernel<T, 8>, grid, 256, stream, a, pages);
 }
 
 }  // namespace
@@ -170,11 +263,7 @@ cudaError_t launch_append(const treewy_append_args& a, cudaStream_t stream) {
                         static_cast<uintptr_t>(a.cache.d * size);
   const bool wide = all % 16 == 0 && a.cache.d % 8 == 0;
   const int np = static_cast<int>(pages);
-  if (size == 2)
-    return wide ? launch_after(append_kernel<uint16_t, 8>, grid, 256, stream, a, np)
-                : launch_after(append_kernel<uint16_t, 1>, grid, 256, stream, a, np);
-  return wide ? launch_after(append_kernel<float, 8>, grid, 256, stream, a, np)
-              : launch_after(append_kernel<float, 1>, grid, 256, stream, a, np);
+  return size == 2 ? launch<uint16_t>(a, wide, grid, np, stream) : launch<float>(a, wide, grid, np, stream);
 }
 
 }  // namespace treewy

@@ -21,15 +21,16 @@
 //
 //   warps 0-7   queries and draft to e4m3; softmax; outputs
 //   warps 8, 9  page table, scales and pages (TMA): keys, and values
-//   warp 10     issues the products: S of the next tile before O of this one
+//   warps 10, 11  issue the products, S up to four tiles ahead of O
 #include "attend_tc.cuh"
 
 namespace treewy {
 namespace {
 
-constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;
-constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
-constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;
+constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;  // and the next one
+constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 2);
+constexpr int kAhead = 4;  // tiles of S
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
 // NH: halves of 128 columns of a head; NR: rows, 8, 16 or 32.
 template <int NH, int NR>
@@ -47,9 +48,10 @@ struct Shape {
 template <int S>
 struct FewSmem {
   RingSmem<S> ring;
-  uint64_t sfull[2], pready[2], pvdone[2], qready, drain;
+  uint64_t sfull[kAhead], sread[kAhead], pready[2], pvdone[2], qready, drain[2];
   alignas(16) float top[2][4][kFewRows];  // maxima (and sums) of the quarters of rows; two sets in turn
-  float ref[kFewRows];          // the rows' references
+  float ref[kFewRows], inv[kFewRows];  // the rows' references, and one over their sums
+  int64_t out[kFewRows];        // where a row's output begins
   uint32_t seen[kFewRows];      // the nodes that a row sees
   uint32_t tmem;
   DraftSmem draft;
@@ -94,6 +96,36 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// Sums over a warp of N values that every lane has: lane l gets that of value
+// l / (32 / N), in a few exchanges of ever fewer values.
+template <int N>
+__device__ __forceinline__ float sum_lanes(float (&v)[N], int lane) {
+  int bit = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1, bit >>= 1) {
+    const bool upper = lane & bit;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float other = __shfl_xor_sync(kFull, upper ? v[i] : v[n + i], bit);
+      v[i] = (upper ? v[n + i] : v[i]) + other;
+    }
+  }
+#pragma unroll
+  for (; bit > 0; bit >>= 1) v[0] += __shfl_xor_sync(kFull, v[0], bit);
+  return v[0];
+}
+
+// An output of a node that sees values that are no numbers, among them perhaps this column's.
+static __device__ __noinline__ float with_none(const Params& p, const DraftSmem& ds, const Segment& g, int node, int col, unsigned long long none,
+                                               float y) {
+  for (unsigned long long q = none & ds.seen[node]; q != 0; q &= q - 1) {
+    const uint16_t v = static_cast<const uint16_t*>(p.a.v)[(static_cast<int64_t>(g.lo) + __ffsll(q) - 1) * p.a.v_stride +
+                                                          static_cast<int64_t>(g.h) * p.a.cache.d + col];
+    if ((v & 0x7f80) == 0x7f80) y = NAN;
+  }
+  return y;
+}
+
 template <int NH, int NR>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_few_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
@@ -113,13 +145,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- set-up, while the kernel before may still run
   if (t == 0) {
     init_ring(rs);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAhead; ++i) {
       mbar_init(&cs.sfull[i], 1);
+      mbar_init(&cs.sread[i], kSoftWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&cs.pready[i], kSoftWarps);
       mbar_init(&cs.pvdone[i], 1);
     }
     mbar_init(&cs.qready, 1);
-    mbar_init(&cs.drain, 1);
+    mbar_init(&cs.drain[0], 1);
+    mbar_init(&cs.drain[1], 1);
     fence_mbarrier_init();
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
@@ -147,45 +183,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       return tile < S || wait_warp(rs, &rs.kfree[slot], again);
                                     });
   } else if (warp == kMmaWarp) {
-    // ---- products
-    const uint32_t id_s = idesc_f8(2 * NR, false, false), id_o = idesc_f8(Sh::kCols, true, false);
-    const uint32_t q0 = smem_addr(qs), r0 = smem_addr(ring), w0 = smem_addr(wts);
+    // ---- S^T = K Q^T
+    const uint32_t id_s = idesc_f8(2 * NR, false, false), q0 = smem_addr(qs), r0 = smem_addr(ring);
     int seg = 0;
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next(p, cs.plan, g)) {
       ok = wait_warp(rs, &cs.qready, seg & 1);
       ++seg;
-      // S of the next tile, then O of the last
 #pragma unroll 1
-      for (int j = g.t0 - 1; ok && j < g.t1; ++j) {
-        if (j + 1 < g.t1) {
-          const int tile = gt + (j >= g.t0 ? 1 : 0), slot = tile % S;
-          ok = wait_warp(rs, &rs.kfull[slot], (tile / S) & 1);
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (elect_one()) {
-            const uint32_t s = tmem + kColS + (tile & 1) * (2 * NR);
-            uint32_t acc = 0, k0 = r0 + slot * Sh::kStage;
+      for (int j = g.t0; ok && j < g.t1; ++j, ++gt) {
+        const int slot = gt % S, b = gt % kAhead;
+        ok = (gt < kAhead || wait_warp(rs, &cs.sread[b], (gt / kAhead - 1) & 1)) && wait_warp(rs, &rs.kfull[slot], (gt / S) & 1);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          uint32_t acc = 0, k0 = r0 + slot * Sh::kStage;
 #pragma unroll 1
-            for (int term = 0; term < (j + 1 == 0 ? 2 : 1); ++term, k0 += 64 * 128) {  // the draft's lo rows
+          for (int term = 0; term < (j == 0 ? 2 : 1); ++term, k0 += 64 * 128) {  // the draft's lo rows
 #pragma unroll
-              for (int x = 0; x < NH; ++x) {
-                const int steps = (min(128, d - 128 * x) + 31) / 32;
+            for (int x = 0; x < NH; ++x) {
+              const int steps = (min(128, d - 128 * x) + 31) / 32;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (k >= steps) continue;
-                  mma_f8(s, smem_desc_sw128(k0 + x * kHalf + k * 32, 1024), smem_desc_sw128(q0 + x * Sh::kRowBytes + k * 32, 1024), id_s, acc);
-                  acc = 1;
-                }
+              for (int k = 0; k < 4; ++k) {
+                if (k >= steps) continue;
+                mma_f8(tmem + kColS + b * (2 * NR), smem_desc_sw128(k0 + x * kHalf + k * 32, 1024),
+                       smem_desc_sw128(q0 + x * Sh::kRowBytes + k * 32, 1024), id_s, acc);
+                acc = 1;
               }
             }
-            mma_commit(&cs.sfull[tile & 1]);
-            mma_commit(&rs.kfree[slot]);
           }
-          __syncwarp();
+          mma_commit(&cs.sfull[b]);
+          mma_commit(&rs.kfree[slot]);
         }
-        if (j < g.t0) continue;
+        __syncwarp();
+      }
+    }
+  } else if (warp == kMmaWarp + 1) {
+    // ---- O^T += V^T w^T
+    const uint32_t id_o = idesc_f8(Sh::kCols, true, false), r0 = smem_addr(ring), w0 = smem_addr(wts);
+    bool ok = true;
+#pragma unroll 1
+    while (ok && walk.next(p, cs.plan, g)) {
+#pragma unroll 1
+      for (int j = g.t0; ok && j < g.t1; ++j, ++gt) {
         const int slot = gt % S;
         ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1) && wait_warp(rs, &cs.pready[gt & 1], (gt >> 1) & 1);
         if (!ok) break;
@@ -210,7 +251,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&cs.pvdone[gt & 1]);
         }
         __syncwarp();
-        ++gt;
       }
     }
   } else {
@@ -266,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = gt % S, b = gt & 1;
         const Consts& cc = rs.c[slot];
         // after a wait that gave up a warp still comes by every barrier of threads
-        bool ok = wait_warp(rs, &cs.sfull[b], (gt >> 1) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
+        bool ok = wait_warp(rs, &cs.sfull[gt % kAhead], (gt / kAhead) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
         tc_fence_after_sync();
         bad |= cc.bad != 0;
         const int n = j == 0 ? g.N : min(kTile, g.len - (j - 1) * kTile);
@@ -281,10 +321,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t r[2 * NT];
         if (ok) {
-          ld_cols<NT>(lanes + kColS + b * (2 * NR) + row0, r);
-          ld_cols<NT>(lanes + kColS + b * (2 * NR) + NR + row0, r + NT);
+          const uint32_t sc = lanes + kColS + gt % kAhead * (2 * NR) + row0;
+          ld_cols<NT>(sc, r);
+          ld_cols<NT>(sc + NR, r + NT);
           ld_wait<2 * NT>(r);
+          tc_fence_before_sync();
         }
+        warp_arrive(&cs.sread[gt % kAhead]);
         const bool draft_tile = j == 0;
         const float ks = draft_tile ? ds.ks[lane] : cc.ks[token >> 4], lv = draft_tile ? ds.lv[lane] : cc.lv[token >> 4];
         const float il = draft_tile ? (token < n ? ds.il[lane] : 0.f) : cc.il[token >> 4];
@@ -319,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < NT; ++i) m[i] = top[i];
         } else if (grown) {  // the same in all warps that have these rows
-          wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
+          if (gt >= 2) wait_warp(rs, &cs.pvdone[b], ((gt - 2) >> 1) & 1);  // in their order
+          wait_warp(rs, &cs.pvdone[b ^ 1], ((gt - 1) >> 1) & 1);
           tc_fence_after_sync();
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
@@ -340,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
+        if (gt >= 2) wait_warp(rs, &cs.pvdone[b], ((gt - 2) >> 1) & 1);  // read no more
         unsigned char* w = wts + b * (2 * Sh::kWBlock);
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {
@@ -370,54 +415,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- outputs
       const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-      const bool ok = wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1);
+      bool ok = gt < 2 || wait_warp(rs, &cs.pvdone[gt & 1], ((gt - 2) >> 1) & 1);
+      ok = wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1) && ok;
       tc_fence_after_sync();
       const unsigned long long none = g.t0 == 0 ? ds.no_number : 0;  // before the next segment's
       // not the set of the last tile, which another warp may still read
+      const float part = sum_lanes<NT>(sum, lane);  // of row row0 + lane / (32 / NT)
+      if (lane % (32 / NT) == 0) cs.top[gt & 1][quarter][row0 + lane / (32 / NT)] = part;
+      if (quarter == 0 && lane == 0) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+        for (int i = 0; i < NT; ++i) cs.ref[row0 + i] = m[i];
+      }
+      all_sync();
+      const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
+      if (t < NR) {
+        float total = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(kFull, sum[i], o);
-        if (lane == 0) {
-          cs.top[gt & 1][quarter][row0 + i] = sum[i];
-          if (quarter == 0) cs.ref[row0 + i] = m[i];
-        }
+        for (int q = 0; q < 4; ++q) total += cs.top[gt & 1][q][t];
+        cs.inv[t] = 1.f / total;
+        const int node = t / G;
+        cs.out[t] = whole ? ((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + t - node * G) * d : (piece * p.rows_cap + t) * d;
+        if (!whole && ok && !bad && t < rows) p.part_lse[piece * p.rows_cap + t] = cs.ref[t] + log2f(total);
       }
       all_sync();
       if (ok && !bad) {
-        // row by row: little code, which a CTA meets for the first time here, costs less than many loads at once
-        const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
-        int node = row0 / G, head = row0 - node * G;
 #pragma unroll 1
-        for (int row = row0; row < min(rows, row0 + NT); ++row, ++head) {
-          if (head == G) head = 0, ++node;
-          float total = 0.f;
+        for (int x = 0; x < NH; ++x) {
+          uint32_t o[NT];
+          ld_cols<NT>(lanes + kColO + x * Sh::kCols + row0, o);
+          ld_wait<NT>(o);
+          const int col = x * 128 + token;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) total += cs.top[gt & 1][q][row];
-          const float inv = 1.f / total;
-          const int64_t out = ((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + head) * d;
-          uint32_t o[NH];
-#pragma unroll
-          for (int x = 0; x < NH; ++x)
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o[x]) : "r"(lanes + kColO + x * Sh::kCols + row) : "memory");
-          ld_wait<NH>(o);
-#pragma unroll
-          for (int x = 0; x < NH; ++x) {
-            const int col = x * 128 + token;
-            float y = __uint_as_float(o[x]) * inv;
-            if (col >= d) continue;
-            if (none != 0) {  // values of the node's path that are no numbers
-#pragma unroll 1
-              for (unsigned long long q = none & ds.seen[node]; q != 0; q &= q - 1) {
-                const uint16_t v = static_cast<const uint16_t*>(a.v)[(static_cast<int64_t>(g.lo) + __ffsll(q) - 1) * a.v_stride +
-                                                                    static_cast<int64_t>(g.h) * d + col];
-                if ((v & 0x7f80) == 0x7f80) y = NAN;
-              }
-            }
-            if (whole) static_cast<__nv_bfloat16*>(a.o)[out + col] = __float2bfloat16_rn(y);
-            else p.part_o[(piece * p.rows_cap + row) * d + col] = y;
+          for (int i = 0; i < NT; ++i) {
+            const int row = row0 + i;
+            if (row >= rows || col >= d) continue;
+            float y = __uint_as_float(o[i]) * cs.inv[row];
+            if (none != 0) y = with_none(p, ds, g, row / G, col, none, y);
+            if (whole) static_cast<__nv_bfloat16*>(a.o)[cs.out[row] + col] = __float2bfloat16_rn(y);
+            else p.part_o[cs.out[row] + col] = y;
           }
-          if (!whole && quarter == 0 && lane == 0) p.part_lse[piece * p.rows_cap + row] = cs.ref[row] + log2f(total);
         }
         tc_fence_before_sync();
       }
@@ -433,10 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kLoadWarp) drain_copies(rs.kfull, armed);
     if (warp == kLoadWarp + 1) drain_copies(rs.vfull, armed);
-    if (warp == kMmaWarp) {
-      if (elect_one()) mma_commit(&cs.drain);
+    if (warp >= kMmaWarp) {
+      uint64_t* drain = &cs.drain[warp - kMmaWarp];
+      if (elect_one()) mma_commit(drain);
       __syncwarp();
-      mbar_wait_for(&cs.drain, 0, 100000000ull);
+      mbar_wait_for(drain, 0, 100000000ull);
     }
   }
   __syncthreads();

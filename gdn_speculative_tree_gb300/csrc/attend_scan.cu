@@ -1,108 +1,145 @@
 // attend_scan.cu -- attention over pages of e4m3 keys and values and the
 // draft's own ones, in f32 on the CUDA cores (treewy_attend for f32 rows or
-// outputs and for head sizes that the tensor-core kernel does not take).
+// outputs and for head sizes that the tensor-core kernels do not take).
 //
 // One pass over the tokens with the running maximum and sum of the softmax: a
-// CTA holds 16 (node, query head) rows that share a key head, and takes 32
-// tokens at a time, the context's and then the draft's, through one tile in
-// shared memory (keys, then values).
+// cluster of eight CTAs holds 16 (node, query head) rows that share a key head;
+// its CTAs take tiles of 32 tokens in turn, the context's and then the
+// draft's, through one tile in shared memory (keys, then values), and read
+// each other's maxima, sums and outputs at the end.
+//
+// Bound by the loads from shared memory of the two products: 128 bits for
+// four products each.
+#include <cooperative_groups.h>
+
 #include "cache_device.cuh"
 #include "treewy_internal.h"
 
 namespace treewy {
 namespace {
 
-constexpr int kRows = 16, kTile = 32, kThreads = 128;
+namespace cg = cooperative_groups;
+
+constexpr int kRows = 16, kTile = 32, kThreads = 128, kRanks = 8, kMaxPad = 256;
 constexpr unsigned kFull = 0xffffffffu;
 
-__global__ void __launch_bounds__(kThreads) attend_scan_kernel(const treewy_attn a, int blocks) {
+struct Shared {
+  int parent[kMaxNodes];
+  unsigned long long seen[kMaxNodes];
+  int page_of[2];
+  float top[kRows], sum[kRows];
+  int bad;
+};
+
+__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
+    attend_scan_kernel(const __grid_constant__ treewy_attn a, int blocks) {
   after_previous();
-  extern __shared__ float smem[];
-  __shared__ int parent[kMaxNodes];
-  __shared__ unsigned long long seen[kMaxNodes];
-  __shared__ int page_of[2];
+  extern __shared__ float4 raw_smem[];
+  __shared__ Shared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
   const treewy_cache& c = a.cache;
-  const int t = threadIdx.x, d = c.d, P = c.page_len, pitch = d + 1;
-  const int block = static_cast<int>(blockIdx.x % blocks);
-  const unsigned rest = blockIdx.x / blocks;
+  // columns in fours, the last ones filled up with zeros; rows of the tile four floats further apart
+  const int t = threadIdx.x, d = c.d, P = c.page_len, pad = (d + 3) & ~3, pitch = pad + 4;
+  const unsigned item = blockIdx.x / kRanks;
+  const int block = static_cast<int>(item % blocks);
+  const unsigned rest = item / blocks;
   const int h = static_cast<int>(rest % c.Hkv), r = static_cast<int>(rest / c.Hkv);
   const int G = a.Hq / c.Hkv;
+  // the same in all of the cluster: it leaves as one
   CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
-  if (q.err == 0 && !load_parents(parent, a.parent, q.lo, q.N)) q.err = TREEWY_STATUS_BAD_TREE;
+  if (q.err == 0 && !load_parents(sh.parent, a.parent, q.lo, q.N)) q.err = TREEWY_STATUS_BAD_TREE;
   if (q.err != 0) {
-    if (block == 0 && h == 0 && t == 0) atomicOr(a.status + r, q.err);
+    if (block == 0 && h == 0 && rank == 0 && t == 0) atomicOr(a.status + r, q.err);
     return;
   }
   const int row0 = block * kRows, live = min(kRows, q.N * G - row0);
   if (live <= 0) return;
   if (t < q.N) {  // the nodes that node t sees
     unsigned long long m = 0;
-    for (int p = t; p >= 0; p = parent[p]) m |= 1ull << p;
-    seen[t] = m;
+    for (int p = t; p >= 0; p = sh.parent[p]) m |= 1ull << p;
+    sh.seen[t] = m;
   }
-  float* qs = smem;                    // [kRows][d]
-  float* tile = qs + kRows * d;        // [kTile][pitch]
-  float* weight = tile + kTile * pitch;  // [kRows][kTile]
+  if (t == 0) sh.bad = 0;
+  float* qs = reinterpret_cast<float*>(raw_smem);  // [kRows][pad], the outputs at the end
+  float* tile = qs + kRows * pad;                  // [kTile][pitch]
+  float* weight = tile + kTile * pitch;            // [kRows][kTile]
   const bool bf16 = a.qkv_dtype == TREEWY_DTYPE_BF16;
-  for (int x = t; x < kRows * d; x += kThreads) {
-    const int row = row0 + x / d;
-    qs[x] = x / d < live ? load_qkv(a.q, (static_cast<int64_t>(q.lo) + row / G) * a.q_stride +
-                                             (static_cast<int64_t>(h) * G + row % G) * d + x % d, bf16)
-                         : 0.f;
+  for (int x = t; x < kRows * pad; x += kThreads) {
+    const int i = x / pad, col = x % pad, rr = row0 + i;
+    qs[x] = i < live && col < d ? load_qkv(a.q, (static_cast<int64_t>(q.lo) + rr / G) * a.q_stride +
+                                                    (static_cast<int64_t>(h) * G + rr % G) * d + col, bf16)
+                                : 0.f;
   }
   const int row = t / 8, sub = t % 8;  // eight threads per row
   const int node = min(row0 + row, q.N * G - 1) / G;
-  float acc[32], top = -INFINITY, sum = 0.f;
+  float4 acc[kMaxPad / 32];
+  float top = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-  const int total = q.len + q.N;
-  for (int t0 = 0; t0 < total; ) {
-    // tokens of the context, or of the draft: a tile has one kind
-    const bool context = t0 < q.len;
-    const int n = min(kTile, (context ? q.len : total) - t0);
+  for (int e = 0; e < kMaxPad / 32; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int context_tiles = (q.len + kTile - 1) / kTile, tiles = context_tiles + (q.N + kTile - 1) / kTile;
+  for (int j = rank; j < tiles; j += kRanks) {
+    const bool context = j < context_tiles;
+    const int t0 = (context ? j : j - context_tiles) * kTile, n = min(kTile, (context ? q.len : q.N) - t0);
     __syncthreads();  // the tile and the weights are free
     if (context) {
-      const int p0 = t0 / P;
-      if (t < 2) {
-        page_of[t] = -1;
-        if (p0 + t <= (t0 + n - 1) / P) page_of[t] = __ldg(c.page_table + static_cast<int64_t>(r) * c.max_pages + p0 + t);
+      const int p0 = t0 / P, count = (t0 + n - 1) / P - p0 + 1;
+      if (t < count) {
+        const int page = __ldg(c.page_table + static_cast<int64_t>(r) * c.max_pages + p0 + t);
+        const bool in = page >= 0 && page < c.num_pages;
+        if (!in) sh.bad = 1;
+        sh.page_of[t] = in ? page : 0;
       }
       __syncthreads();
-      bool bad = false;
-      for (int i = 0; i <= (t0 + n - 1) / P - p0; ++i) bad |= page_of[i] < 0 || page_of[i] >= c.num_pages;
-      if (bad) {
-        if (block == 0 && h == 0 && t == 0) atomicOr(a.status + r, TREEWY_STATUS_BAD_PAGE);
-        return;
-      }
+      if (sh.bad != 0) break;  // nothing of the request is written
     }
     auto load = [&](bool values) {
-      for (int x = t; x < n * d; x += kThreads) {
-        const int j = x / d, col = x % d;
-        float f;
-        if (context) {
-          const int at = t0 + j;
-          const int64_t b = static_cast<int64_t>(page_of[at / P - t0 / P]) * c.Hkv + h;
+      if (context && d % 16 == 0) {
+        for (int x = t; x < n * (d / 16); x += kThreads) {
+          const int i = x / (d / 16), col = x % (d / 16) * 16, at = t0 + i;
+          const int64_t b = static_cast<int64_t>(sh.page_of[at / P - t0 / P]) * c.Hkv + h;
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(values ? c.v : c.k) + (b * P + at % P) * d + col));
+          const float f = __ldg((values ? c.v_scale : c.k_scale) + b);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t h0 = e4m3x2_to_f16x2(u[e] & 0xffffu), h1 = e4m3x2_to_f16x2(u[e] >> 16);
+            const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)), y1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+            *reinterpret_cast<float4*>(tile + i * pitch + col + 4 * e) = make_float4(y0.x * f, y0.y * f, y1.x * f, y1.y * f);
+          }
+        }
+        return;
+      }
+      for (int x = t; x < n * pad; x += kThreads) {
+        const int i = x / pad, col = x % pad, at = t0 + i;
+        float f = 0.f;
+        if (col < d && context) {
+          const int64_t b = static_cast<int64_t>(sh.page_of[at / P - t0 / P]) * c.Hkv + h;
           f = e4m3_to_float(__ldg(static_cast<const uint8_t*>(values ? c.v : c.k) + (b * P + at % P) * d + col)) *
               __ldg((values ? c.v_scale : c.k_scale) + b);
-        } else {
-          f = load_qkv(values ? a.v : a.k, (static_cast<int64_t>(q.lo) + t0 - q.len + j) * (values ? a.v_stride : a.k_stride) +
+        } else if (col < d) {
+          f = load_qkv(values ? a.v : a.k, (static_cast<int64_t>(q.lo) + at) * (values ? a.v_stride : a.k_stride) +
                                                static_cast<int64_t>(h) * d + col, bf16);
         }
-        tile[j * pitch + col] = f;
+        tile[i * pitch + col] = f;
       }
     };
     load(false);
     __syncthreads();
-    float s[4], high = -INFINITY;
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, high = -INFINITY;  // tokens sub, sub + 8, ..
+    for (int x = 0; x < pad; x += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(qs + row * pad + x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 v = *reinterpret_cast<const float4*>(tile + (sub + 8 * e) * pitch + x);
+        s[e] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, s[e]))));
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int j = sub + 8 * e;
-      s[e] = -INFINITY;
-      if (j < n && (context || ((seen[node] >> (t0 - q.len + j)) & 1))) {
-        float dot = 0.f;
-        for (int x = 0; x < d; ++x) dot = fmaf(qs[row * d + x], tile[j * pitch + x], dot);
-        s[e] = dot * a.scale;
-      }
+      const int i = sub + 8 * e;
+      const bool sees = i < n && (context || ((sh.seen[node] >> (t0 + i)) & 1));
+      s[e] = sees ? s[e] * a.scale : -INFINITY;
       high = fmaxf(high, s[e]);
     }
 #pragma unroll
@@ -120,51 +157,80 @@ __global__ void __launch_bounds__(kThreads) attend_scan_kernel(const treewy_attn
     top = now;
     sum = sum * keep + part;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) acc[e] *= keep;
+    for (int e = 0; e < kMaxPad / 32; ++e) acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
     __syncthreads();
     load(true);
     __syncthreads();
-    for (int j = 0; j < n; ++j) {
-      const float w = weight[row * kTile + j];
+    for (int i = 0; i < n; ++i) {
+      const float w = weight[row * kTile + i];
       // what a node does not see adds nothing to it, whatever it is
-      if (!context && !((seen[node] >> (t0 - q.len + j)) & 1)) continue;
+      if (!context && !((sh.seen[node] >> (t0 + i)) & 1)) continue;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int col = sub + 8 * e;
-        if (col < d) acc[e] = fmaf(w, tile[j * pitch + col], acc[e]);
+      for (int e = 0; e < kMaxPad / 32; ++e) {
+        const int col = 4 * sub + 32 * e;
+        if (col < pad) {
+          const float4 v = *reinterpret_cast<const float4*>(tile + i * pitch + col);
+          acc[e] = make_float4(fmaf(w, v.x, acc[e].x), fmaf(w, v.y, acc[e].y), fmaf(w, v.z, acc[e].z), fmaf(w, v.w, acc[e].w));
+        }
       }
     }
-    t0 += n;
   }
+  // the ranks' parts; one that had no tile, or whose tiles no row saw, has the maximum -infinity and zeros
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if (row >= live) return;
-  const int64_t out = ((static_cast<int64_t>(q.lo) + (row0 + row) / G) * a.Hq + static_cast<int64_t>(h) * G + (row0 + row) % G) * d;
+  __syncthreads();
+  if (sub == 0) sh.top[row] = top, sh.sum[row] = sum;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    const int col = sub + 8 * e;
-    if (col >= d) continue;
-    const float y = acc[e] / sum;
-    if (a.o_dtype == TREEWY_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.o)[out + col] = __float2bfloat16_rn(y);
-    else static_cast<float*>(a.o)[out + col] = y;
+  for (int e = 0; e < kMaxPad / 32; ++e)
+    if (4 * sub + 32 * e < pad) *reinterpret_cast<float4*>(qs + row * pad + 4 * sub + 32 * e) = acc[e];
+  cluster.sync();
+  bool bad = false;
+  for (int k = 0; k < kRanks; ++k) bad |= cluster.map_shared_rank(&sh, k)->bad != 0;
+  if (bad && rank == 0 && t == 0) atomicOr(a.status + r, TREEWY_STATUS_BAD_PAGE);
+  for (int i = rank; !bad && i < live; i += kRanks) {
+    float high = -INFINITY, total = 0.f, f[kRanks];
+#pragma unroll
+    for (int k = 0; k < kRanks; ++k) {
+      f[k] = cluster.map_shared_rank(&sh, k)->top[i];
+      high = fmaxf(high, f[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kRanks; ++k) {
+      const float part = cluster.map_shared_rank(&sh, k)->sum[i];
+      // a sum that is no number comes through whatever its maximum is
+      f[k] = f[k] == -INFINITY ? (part == 0.f ? 0.f : part) : expf(f[k] - high);
+      total = fmaf(f[k], part, total);
+    }
+    const int rr = row0 + i;
+    const int64_t out = ((static_cast<int64_t>(q.lo) + rr / G) * a.Hq + static_cast<int64_t>(h) * G + rr % G) * d;
+    for (int col = t; col < d; col += kThreads) {
+      float y = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRanks; ++k) {
+        const float* part = cluster.map_shared_rank(qs, k) + i * pad + col;
+        if (f[k] != 0.f) y = fmaf(f[k], *part, y);
+      }
+      y /= total;
+      if (a.o_dtype == TREEWY_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.o)[out + col] = __float2bfloat16_rn(y);
+      else static_cast<float*>(a.o)[out + col] = y;
+    }
   }
+  cluster.sync();  // the others may still read here
 }
 
 }  // namespace
 
 cudaError_t launch_attend_scan(const treewy_attn& a, cudaStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv) + kRows - 1) / kRows;
-  const int64_t ctas = blocks * a.cache.Hkv;
+  const int64_t ctas = blocks * a.cache.Hkv * kRanks;
   if (ctas > 0x7fffffff / a.R) return cudaErrorNotSupported;
-  const int d = a.cache.d;
-  const size_t bytes = sizeof(float) * (kRows * d + kTile * (d + 1) + kRows * kTile);
+  auto bytes = [](int pad) { return sizeof(float) * (kRows * pad + kTile * (pad + 4) + kRows * kTile); };
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(attend_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                sizeof(float) * (kRows * 256 + kTile * 257 + kRows * kTile));
+  cudaError_t e = once_per_device(done, [&] {
+    return cudaFuncSetAttribute(attend_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes(kMaxPad)));
   });
   if (e != cudaSuccess) return e;
-  return launch_after_smem(attend_scan_kernel, dim3(static_cast<unsigned>(ctas * a.R)), kThreads, bytes, stream, a,
+  return launch_after_smem(attend_scan_kernel, dim3(static_cast<unsigned>(ctas * a.R)), kThreads, bytes((a.cache.d + 3) & ~3), stream, a,
                            static_cast<int>(blocks));
 }
 

@@ -562,13 +562,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 }
 
 // An item that lies in several pieces: its parts' outputs, each normed with
-// its own sum, by the weights 2^lse.  A CTA per row: eight warps take the
-// parts in turn, a lane eight columns.
-__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Params p) {
+// its own sum, by the weights 2^lse.  A CTA takes eight rows, a warp each, a
+// lane eight columns; or one row (`many`: few items, of many parts each), whose
+// parts the warps share.
+constexpr int kJoinRows = 8;
+__global__ void __launch_bounds__(32 * kJoinRows) attend_join_kernel(const __grid_constant__ Params p, int many) {
   after_previous();
-  __shared__ float acc[8][256], wsum[8];
-  const int w = blockIdx.y, row = blockIdx.x, t = threadIdx.x, warp = t >> 5, lane = t & 31, d = p.a.cache.d;
+  __shared__ float acc[kJoinRows][256], wsum[kJoinRows];
+  const int w = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31, d = p.a.cache.d;
   const int4 rec = *reinterpret_cast<const int4*>(p.record + 8 * w);
+  const int row = many ? blockIdx.x : blockIdx.x * kJoinRows + warp;
   if (rec.x == 0 || row >= rec.z) return;
   const int4 item = *reinterpret_cast<const int4*>(p.record + 8 * w + 4);
   const int parts = rec.y - w + 1;
@@ -578,12 +581,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_lse[part_of(i)]);  // NaN comes by way of the weights
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  if (top == INFINITY) return;  // a part was refused
+  if (top == INFINITY) return;  // a part was refused, in all of its rows
   float sum = 0.f, y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = 0.f;
 #pragma unroll 4
-  for (int i = warp; i < parts; i += 8) {
+  for (int i = many ? warp : 0; i < parts; i += many ? kJoinRows : 1) {
     const int64_t at = part_of(i);
     const float f = exp2f(p.part_lse[at] - top);
     sum += f;
@@ -594,17 +597,25 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
       y[4] = fmaf(f, v.x, y[4]); y[5] = fmaf(f, v.y, y[5]); y[6] = fmaf(f, v.z, y[6]); y[7] = fmaf(f, v.w, y[7]);
     }
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[warp][8 * lane + e] = y[e];
-  if (lane == 0) wsum[warp] = sum;
-  __syncthreads();
-  if (t >= d) return;
-  float z = 0.f, n = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) z += acc[i][t], n += wsum[i];
   const int rr = item.y * kTile + row, node = rr / p.G;
-  static_cast<__nv_bfloat16*>(p.a.o)[((static_cast<int64_t>(item.z) + node) * p.a.Hq + item.x * p.G + rr - node * p.G) * d + t] =
-      __float2bfloat16_rn(z / n);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.o) +
+                       ((static_cast<int64_t>(item.z) + node) * p.a.Hq + item.x * p.G + rr - node * p.G) * d;
+  if (many) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[warp][8 * lane + e] = y[e];
+    if (lane == 0) wsum[warp] = sum;
+    __syncthreads();
+    if (t < d) {
+      float z = 0.f, n = 0.f;
+#pragma unroll
+      for (int i = 0; i < kJoinRows; ++i) z += acc[i][t], n += wsum[i];
+      out[t] = __float2bfloat16_rn(z / n);
+    }
+  } else if (8 * lane < d) {
+    const float inv = 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[8 * lane + e] = __float2bfloat16_rn(y[e] * inv);
+  }
 }
 
 int row_tiles_of(const treewy_attn& a) {
@@ -732,7 +743,8 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
     e = c.d > 128 ? launch<2>(p, maps, grid, stream) : launch<1>(p, maps, grid, stream);
   }
   if (e != cudaSuccess || !p.listed) return e;
-  return launch_after(attend_join_kernel, dim3(p.rows_cap, grid), 256, stream, p);
+  const int many = static_cast<int64_t>(a.R) * c.Hkv * p.tiles_m * 8 <= kMaxPieces ? 1 : 0;
+  return launch_after(attend_join_kernel, dim3(many ? p.rows_cap : (p.rows_cap + kJoinRows - 1) / kJoinRows, grid), 32 * kJoinRows, stream, p, many);
 }
 
 }  // namespace treewy
