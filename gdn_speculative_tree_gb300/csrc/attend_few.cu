@@ -19,16 +19,23 @@
 // (lo) of a tile: the keys' products are added up in S^T, and the weights of
 // the first quarter of the lanes stand for both tokens of a value.
 //
-//   warps 0-7   queries and draft to e4m3; softmax; outputs
-//   warps 8, 9  page table, scales and pages (TMA): keys, and values
+// A context's tiles are few where there are many heads, so that what comes
+// before and after them counts: four warps of their own make the next item's
+// queries and draft while the softmax goes through this one's tiles, and write
+// the last one's outputs (queries, drafts and O are there twice).
+//
+//   warps 0-7     softmax
+//   warps 8, 9    page table, scales and pages (TMA): keys, and values
 //   warps 10, 11  issue the products, S up to four tiles ahead of O
+//   warps 12-15   queries and draft to e4m3; outputs
 #include "attend_tc.cuh"
 
 namespace treewy {
 namespace {
 
 constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;  // and the next one
-constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 2);
+constexpr int kSideWarp = kMmaWarp + 2, kSideWarps = 4, kSideThreads = 32 * kSideWarps;
+constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kSideWarp + kSideWarps);
 constexpr int kAhead = 4;  // tiles of S
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
@@ -39,22 +46,33 @@ struct Shape {
   static constexpr int kCols = NR < 16 ? 16 : NR;                    // of a product of the weights, 16 at least
   static constexpr uint32_t kWBlock = kCols * 128;                   // a term of a tile's weights
   static constexpr uint32_t kWBytes = 4 * kWBlock;                   // of two tiles
-  static constexpr uint32_t kQBytes = NH * kRowBytes;
+  static constexpr uint32_t kQBytes = NH * kRowBytes;                // of an item; two of them
   static constexpr uint32_t kStage = 2 * NH * kHalf;                 // K, then V
-  static constexpr int kStages = NH == 2 ? (NR == 32 ? 2 : 3) : (NR == 32 ? 5 : 6);
-  static constexpr uint32_t kBytes = kWBytes + kQBytes + kStages * kStage + 1024;
+  static constexpr int kStages = NH == 2 ? (NR == 8 ? 3 : 2) : (NR == 32 ? 5 : 6);
+  static constexpr uint32_t kBytes = kWBytes + 2 * kQBytes + kStages * kStage + 1024;
+};
+
+// What belongs to an item: two of them in turn.
+struct ItemSmem {
+  DraftSmem draft;
+  alignas(16) float sum[4][kFewRows];  // of the quarters of the lanes
+  float ref[kFewRows], inv[kFewRows];  // the rows' references, and one over their sums
+  int64_t out[kFewRows];               // where a row's output begins
+  uint32_t seen[kFewRows];             // the nodes that a row sees
+  int bad;                             // a page of it
 };
 
 template <int S>
 struct FewSmem {
   RingSmem<S> ring;
-  uint64_t sfull[kAhead], sread[kAhead], pready[2], pvdone[2], qready, drain[2];
-  alignas(16) float top[2][4][kFewRows];  // maxima (and sums) of the quarters of rows; two sets in turn
-  float ref[kFewRows], inv[kFewRows];  // the rows' references, and one over their sums
-  int64_t out[kFewRows];        // where a row's output begins
-  uint32_t seen[kFewRows];      // the nodes that a row sees
+  uint64_t sfull[kAhead], sread[kAhead], pready[2], pvdone[2], drain[2];
+  // A stage is there for an item's draft (or it has none).  The loading warp is ahead of who fills them by its stages at
+  // most, so that with eight barriers none is two phases on before it is waited for.
+  uint64_t place[8];
+  uint64_t ready[2], free[2], done[2], odone[2], ofree[2];  // items: made, their place free, their softmax done, O, O written
+  alignas(16) float top[2][4][kFewRows];  // maxima of the quarters of rows; two sets in turn
   uint32_t tmem;
-  DraftSmem draft;
+  ItemSmem item[2];
   PlanSmem plan;
 };
 
@@ -135,10 +153,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char raw_smem[];
   __shared__ FewSmem<S> cs;
   RingSmem<S>& rs = cs.ring;
-  DraftSmem& ds = cs.draft;
   unsigned char* wts = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   unsigned char* qs = wts + Sh::kWBytes;
-  unsigned char* ring = qs + Sh::kQBytes;
+  unsigned char* ring = qs + 2 * Sh::kQBytes;
   const treewy_attn& a = p.a;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, d = a.cache.d, G = p.G;
 
@@ -149,13 +166,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&cs.sfull[i], 1);
       mbar_init(&cs.sread[i], kSoftWarps);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&cs.place[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&cs.pready[i], kSoftWarps);
       mbar_init(&cs.pvdone[i], 1);
+      mbar_init(&cs.ready[i], kSideWarps);
+      mbar_init(&cs.free[i], kSoftWarps);
+      mbar_init(&cs.done[i], kSoftWarps);
+      mbar_init(&cs.odone[i], 1);
+      mbar_init(&cs.ofree[i], kSideWarps);
+      mbar_init(&cs.drain[i], 1);
     }
-    mbar_init(&cs.qready, 1);
-    mbar_init(&cs.drain[0], 1);
-    mbar_init(&cs.drain[1], 1);
     fence_mbarrier_init();
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
@@ -171,26 +192,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk walk = mine.walk;
   Segment g;
   int armed = 0;
-  int gt = 0;  // tiles so far
+  int gt = 0;   // tiles so far
+  int seg = 0;  // items, or parts of them, so far: the k-th uses place k & 1 for the k / 2-th time
 
   if (warp == kLoadWarp) {
     armed = load_pages<false, NH, S>(p, cs, rs, walk, ring, kmap, [](const Segment&) { return true; },
                                      [](const Segment&, int, int, uint32_t) { return true; });
   } else if (warp == kLoadWarp + 1) {
-    // the softmax warps fill the draft's tile once both its stages are free
-    armed = load_pages<true, NH, S>(p, cs, rs, walk, ring, vmap, [](const Segment&) { return true; },
-                                    [&](const Segment&, int tile, int slot, uint32_t again) {
-                                      return tile < S || wait_warp(rs, &rs.kfree[slot], again);
-                                    });
+    // the draft's tile is filled by other warps, once both its stages are free
+    static_assert(S < 8, "drafts whose stage is there and that are not filled yet");
+    armed = load_pages<true, NH, S>(
+        p, cs, rs, walk, ring, vmap,
+        [&](const Segment& s) {
+          if (s.t0 != 0) warp_arrive(&cs.place[seg & 7]);
+          ++seg;
+          return true;
+        },
+        [&](const Segment&, int tile, int slot, uint32_t again) {
+          if (tile >= S && !wait_warp(rs, &rs.kfree[slot], again)) return false;
+          warp_arrive(&cs.place[(seg - 1) & 7]);
+          return true;
+        });
   } else if (warp == kMmaWarp) {
     // ---- S^T = K Q^T
-    const uint32_t id_s = idesc_f8(2 * NR, false, false), q0 = smem_addr(qs), r0 = smem_addr(ring);
-    int seg = 0;
+    const uint32_t id_s = idesc_f8(2 * NR, false, false), r0 = smem_addr(ring);
     bool ok = true;
 #pragma unroll 1
-    while (ok && walk.next(p, cs.plan, g)) {
-      ok = wait_warp(rs, &cs.qready, seg & 1);
-      ++seg;
+    for (; ok && walk.next(p, cs.plan, g); ++seg) {
+      const uint32_t q0 = smem_addr(qs) + (seg & 1) * Sh::kQBytes;
+      ok = wait_warp(rs, &cs.ready[seg & 1], (seg >> 1) & 1);
 #pragma unroll 1
       for (int j = g.t0; ok && j < g.t1; ++j, ++gt) {
         const int slot = gt % S, b = gt % kAhead;
@@ -224,7 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t id_o = idesc_f8(Sh::kCols, true, false), r0 = smem_addr(ring), w0 = smem_addr(wts);
     bool ok = true;
 #pragma unroll 1
-    while (ok && walk.next(p, cs.plan, g)) {
+    for (; ok && walk.next(p, cs.plan, g); ++seg) {
+      const uint32_t o0 = tmem + kColO + (seg & 1) * (NH * Sh::kCols);
+      ok = seg < 2 || wait_warp(rs, &cs.ofree[seg & 1], ((seg >> 1) - 1) & 1);
 #pragma unroll 1
       for (int j = g.t0; ok && j < g.t1; ++j, ++gt) {
         const int slot = gt % S;
@@ -242,80 +274,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               if (((steps >> k) & 1) == 0) continue;
               const uint64_t v = desc_mn(v0 + x * kHalf + k * 4096);
-              mma_f8(tmem + kColO + x * Sh::kCols, v, smem_desc_sw128(w + k * 32, 1024), id_o | kBE5m2, acc);
-              mma_f8(tmem + kColO + x * Sh::kCols, v, smem_desc_sw128(w + Sh::kWBlock + k * 32, 1024), id_o, 1);
+              mma_f8(o0 + x * Sh::kCols, v, smem_desc_sw128(w + k * 32, 1024), id_o | kBE5m2, acc);
+              mma_f8(o0 + x * Sh::kCols, v, smem_desc_sw128(w + Sh::kWBlock + k * 32, 1024), id_o, 1);
               acc = 1;
             }
           }
           mma_commit(&rs.vfree[slot]);
           mma_commit(&cs.pvdone[gt & 1]);
+          if (j + 1 == g.t1) mma_commit(&cs.odone[seg & 1]);
         }
         __syncwarp();
       }
     }
-  } else {
+  } else if (warp < kSoftWarps) {
     // ---- softmax: warps w and w + 4 have the tokens 32 (w % 4) .., each of them half of the rows
     const int quarter = warp & 3, hf = warp >> 2, row0 = hf * NT, token = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const float factor = a.scale * 1.4426950408889634f;  // scores in powers of two
     auto all_sync = [] { named_bar_sync<1, kSoftThreads>(); };
 #pragma unroll 1
-    while (walk.next(p, cs.plan, g)) {
-      // queries and tree
-      const int rows = g.N * G;
-      if (t == 0) ds.bad_tree = 0, ds.no_number = 0;
-      if (g.t0 == 0) wait_warp(rs, &rs.cfull[gt % S], (gt / S) & 1);  // the stage is free
-      all_sync();
-      load_tree(p, ds, g, t);
-      unsigned char* draft = ring + (gt % S) * Sh::kStage;
-      zero_rows<kSoftThreads>(qs, NH, Sh::kRowBytes, rows, NR);
-      zero_rows<kSoftThreads>(qs, NH, Sh::kRowBytes, NR + rows, 2 * NR);
-      if (t >= rows && t < NR) ds.rowf[t] = 0.f;
-      if (g.t0 == 0) {  // what the draft's tile has behind its values
-        zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, g.N, 32);
-        zero_rows<kSoftThreads>(draft + NH * kHalf, NH, kHalf, 64 + g.N, 96);
-        if (t >= g.N && t < 32) ds.ks[t] = 1.f, ds.lv[t] = ds.il[t] = 0.f;
-      }
-      fill_rows<NH, kSoftWarps, 4>(p, ds, g, rows, factor, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
-        unsigned char* tile = kind == 0 ? qs : kind == 1 ? draft : draft + NH * kHalf;
-        const uint32_t block = kind == 0 ? Sh::kRowBytes : kHalf;
-        *operand8(tile, i, ln, block) = hi;
-        *operand8(tile, i + (kind == 0 ? NR : 64), ln, block) = lo;
-      });
-      fence_proxy_async_smem();
-      all_sync();
-      if (t == 0) {
-        arrive(&cs.qready);
-        if (g.t0 == 0) {
-          arrive(&rs.kfull[gt % S]);
-          arrive(&rs.vfull[gt % S]);
-        }
-      }
-      see(ds, g, t);
-      all_sync();
-      if (t < NR) cs.seen[t] = static_cast<uint32_t>(ds.seen[min(t, rows - 1) / G]);
-
-      const bool bad_tree = ds.bad_tree != 0;
-      bool bad = bad_tree;
+    for (; walk.next(p, cs.plan, g); ++seg) {
+      ItemSmem& it = cs.item[seg & 1];
+      const DraftSmem& ds = it.draft;
+      const uint32_t o0 = lanes + kColO + (seg & 1) * (NH * Sh::kCols) + row0;
+      wait_warp(rs, &cs.ready[seg & 1], (seg >> 1) & 1);
       float m[NT], sum[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) m[i] = -INFINITY, sum[i] = 0.f;
-      if (g.t0 == 0) all_sync();
+      const int t0 = g.t0, t1 = g.t1, N = g.N, len = g.len;
 #pragma unroll 1
-      for (int j = g.t0; j < g.t1; ++j, ++gt) {
+      for (int j = t0; j < t1; ++j, ++gt) {
         const int slot = gt % S, b = gt & 1;
         const Consts& cc = rs.c[slot];
         // after a wait that gave up a warp still comes by every barrier of threads
         bool ok = wait_warp(rs, &cs.sfull[gt % kAhead], (gt / kAhead) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
         tc_fence_after_sync();
-        bad |= cc.bad != 0;
-        const int n = j == 0 ? g.N : min(kTile, g.len - (j - 1) * kTile);
-        if (j != 0 && n < kTile && ok) ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1);
-        if (j != 0 && n < kTile && ok) {  // values behind the context: anything, so none
-          const int end = (n + 31) & ~31;
+        if (cc.bad != 0) it.bad = 1;
+        const bool draft_tile = j == 0;
+        const int n = draft_tile ? N : min(kTile, len - (j - 1) * kTile);
+        if (!draft_tile && n < kTile && ok) ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1);
+        if (!draft_tile && n < kTile && ok) {  // values behind the context: anything, so none
           unsigned char* v = ring + slot * Sh::kStage + NH * kHalf;
 #pragma unroll 1
-          for (int i = n * 8 + t; i < end * 8; i += kSoftThreads)
+          for (int i = n * 8 + t; i < ((n + 31) & ~31) * 8; i += kSoftThreads)
 #pragma unroll
             for (int x = 0; x < NH; ++x) *reinterpret_cast<uint4*>(v + x * kHalf + i * 16) = make_uint4(0, 0, 0, 0);
         }
@@ -328,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before_sync();
         }
         warp_arrive(&cs.sread[gt % kAhead]);
-        const bool draft_tile = j == 0;
         const float ks = draft_tile ? ds.ks[lane] : cc.ks[token >> 4], lv = draft_tile ? ds.lv[lane] : cc.lv[token >> 4];
         const float il = draft_tile ? (token < n ? ds.il[lane] : 0.f) : cc.il[token >> 4];
         float s[NT], top[NT];
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < NT; ++i) {
           const float x = __uint_as_float(r[i]) + __uint_as_float(r[NT + i]);
           const float y = fmaf(x, fmaxf(ks * ds.rowf[row0 + i], kLeast), lv);
-          const bool live = token < n && (!draft_tile || ((cs.seen[row0 + i] >> lane) & 1));
+          const bool live = token < n && (!draft_tile || ((it.seen[row0 + i] >> lane) & 1));
           s[i] = live ? y : -INFINITY;
           top[i] = warp_max(s[i]);
         }
@@ -358,11 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) grown |= top[i + e] > m[i + e] + kGrowth;
         }
-        if (j == g.t0) {
+        if (gt >= 2) wait_warp(rs, &cs.pvdone[b], ((gt - 2) >> 1) & 1);  // the weights' place is read no more
+        if (j == t0) {
 #pragma unroll
           for (int i = 0; i < NT; ++i) m[i] = top[i];
         } else if (grown) {  // the same in all warps that have these rows
-          if (gt >= 2) wait_warp(rs, &cs.pvdone[b], ((gt - 2) >> 1) & 1);  // in their order
           wait_warp(rs, &cs.pvdone[b ^ 1], ((gt - 1) >> 1) & 1);
           tc_fence_after_sync();
 #pragma unroll
@@ -376,15 +375,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int x = 0; x < NH; ++x) {  // halves of the head's columns
             uint32_t o[NT];
-            ld_cols<NT>(lanes + kColO + x * Sh::kCols + row0, o);
+            ld_cols<NT>(o0 + x * Sh::kCols, o);
             ld_wait<NT>(o);
 #pragma unroll
             for (int i = 0; i < NT; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * top[i]);
-            st_cols<NT>(lanes + kColO + x * Sh::kCols + row0, o);
+            st_cols<NT>(o0 + x * Sh::kCols, o);
           }
           tmem_wait_st();
         }
-        if (gt >= 2) wait_warp(rs, &cs.pvdone[b], ((gt - 2) >> 1) & 1);  // read no more
         unsigned char* w = wts + b * (2 * Sh::kWBlock);
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {
@@ -412,52 +410,108 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
         warp_arrive(&cs.pready[b]);
       }
-
-      // ---- outputs
-      const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-      bool ok = gt < 2 || wait_warp(rs, &cs.pvdone[gt & 1], ((gt - 2) >> 1) & 1);
-      ok = wait_warp(rs, &cs.pvdone[(gt - 1) & 1], ((gt - 1) >> 1) & 1) && ok;
-      tc_fence_after_sync();
-      const unsigned long long none = g.t0 == 0 ? ds.no_number : 0;  // before the next segment's
-      // not the set of the last tile, which another warp may still read
       const float part = sum_lanes<NT>(sum, lane);  // of row row0 + lane / (32 / NT)
-      if (lane % (32 / NT) == 0) cs.top[gt & 1][quarter][row0 + lane / (32 / NT)] = part;
+      if (lane % (32 / NT) == 0) it.sum[quarter][row0 + lane / (32 / NT)] = part;
       if (quarter == 0 && lane == 0) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) cs.ref[row0 + i] = m[i];
+        for (int i = 0; i < NT; ++i) it.ref[row0 + i] = m[i];
       }
-      all_sync();
-      const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
-      if (t < NR) {
-        float total = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) total += cs.top[gt & 1][q][t];
-        cs.inv[t] = 1.f / total;
-        const int node = t / G;
-        cs.out[t] = whole ? ((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + t - node * G) * d : (piece * p.rows_cap + t) * d;
-        if (!whole && ok && !bad && t < rows) p.part_lse[piece * p.rows_cap + t] = cs.ref[t] + log2f(total);
-      }
-      all_sync();
-      if (ok && !bad) {
+      warp_arrive(&cs.done[seg & 1]);
+      if (lane == 0) arrive(&cs.free[seg & 1]);
+    }
+  } else {
+    // ---- the next item's queries and draft, the last one's outputs
+    const int quarter = warp & 3, u = t - 32 * kSideWarp;
+    const float factor = a.scale * 1.4426950408889634f;  // scores in powers of two
+    auto side_sync = [] { named_bar_sync<2, kSideThreads>(); };
+    Walk behind = walk;
+    int tiles = 0;  // up to the item that is made
+    bool more = true;
 #pragma unroll 1
-        for (int x = 0; x < NH; ++x) {
-          uint32_t o[NT];
-          ld_cols<NT>(lanes + kColO + x * Sh::kCols + row0, o);
-          ld_wait<NT>(o);
-          const int col = x * 128 + token;
+    for (;; ++seg) {
+      more = more && walk.next(p, cs.plan, g);
+      if (more) {
+        ItemSmem& it = cs.item[seg & 1];
+        DraftSmem& ds = it.draft;
+        const int rows = g.N * G;
+        if (seg >= 2) wait_warp(rs, &cs.free[seg & 1], ((seg >> 1) - 1) & 1);
+        if (u == 0) ds.bad_tree = 0, ds.no_number = 0, it.bad = 0;
+        const int slot = tiles % S;
+        wait_warp(rs, &cs.place[seg & 7], (seg >> 3) & 1);
+        side_sync();
+        load_tree(p, ds, g, u);
+        unsigned char *q = qs + (seg & 1) * Sh::kQBytes, *draft = ring + slot * Sh::kStage;
+        zero_rows<kSideThreads>(q, NH, Sh::kRowBytes, rows, NR, u);
+        zero_rows<kSideThreads>(q, NH, Sh::kRowBytes, NR + rows, 2 * NR, u);
+        if (u >= rows && u < NR) ds.rowf[u] = 0.f;
+        if (g.t0 == 0) {  // what the draft's tile has behind its values
+          zero_rows<kSideThreads>(draft + NH * kHalf, NH, kHalf, g.N, 32, u);
+          zero_rows<kSideThreads>(draft + NH * kHalf, NH, kHalf, 64 + g.N, 96, u);
+          if (u >= g.N && u < 32) ds.ks[u] = 1.f, ds.lv[u] = ds.il[u] = 0.f;
+        }
+        fill_rows<NH, kSideWarps, 4>(p, ds, g, rows, factor, warp - kSideWarp, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
+          unsigned char* tile = kind == 0 ? q : kind == 1 ? draft : draft + NH * kHalf;
+          const uint32_t block = kind == 0 ? Sh::kRowBytes : kHalf;
+          *operand8(tile, i, ln, block) = hi;
+          *operand8(tile, i + (kind == 0 ? NR : 64), ln, block) = lo;
+        });
+        fence_proxy_async_smem();
+        side_sync();
+        see(ds, g, u);
+        side_sync();
+        if (u < NR) it.seen[u] = static_cast<uint32_t>(ds.seen[min(u, rows - 1) / G]);
+        if (g.t0 == 0 && u == 0) {
+          arrive(&rs.kfull[slot]);
+          arrive(&rs.vfull[slot]);
+        }
+        warp_arrive(&cs.ready[seg & 1]);
+        tiles += g.t1 - g.t0;
+      }
+      if (seg == 0) continue;
+      if (!behind.next(p, cs.plan, g)) break;
+      // ---- outputs of the one before
+      const int k = seg - 1;
+      ItemSmem& it = cs.item[k & 1];
+      const int rows = g.N * G;
+      const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+      bool ok = wait_warp(rs, &cs.done[k & 1], (k >> 1) & 1);
+      ok = wait_warp(rs, &cs.odone[k & 1], (k >> 1) & 1) && ok;
+      tc_fence_after_sync();
+      const bool bad_tree = it.draft.bad_tree != 0, bad = bad_tree || it.bad != 0;
+      const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (g.t0 == 0 ? 1 : 0);
+      if (u < NR) {
+        const float total = it.sum[0][u] + it.sum[1][u] + it.sum[2][u] + it.sum[3][u];
+        const int node = u / G;
+        it.inv[u] = 1.f / total;
+        it.out[u] = whole ? ((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + u - node * G) * d : (piece * p.rows_cap + u) * d;
+        if (!whole && ok && !bad && u < rows) p.part_lse[piece * p.rows_cap + u] = it.ref[u] + log2f(total);
+      }
+      side_sync();
+      if (ok && !bad) {
+        const unsigned long long none = g.t0 == 0 ? it.draft.no_number : 0;
+        constexpr int kStep = NR < 8 ? NR : 8;
+#pragma unroll 1
+        for (int x = 0; x < NH * (NR / kStep); ++x) {
+          const int half = x / (NR / kStep), r0 = x % (NR / kStep) * kStep, col = half * 128 + quarter * 32 + lane;
+          if (r0 >= rows) continue;
+          uint32_t o[kStep];
+          ld_cols<kStep>(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kColO + ((k & 1) * NH + half) * Sh::kCols + r0, o);
+          ld_wait<kStep>(o);
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const int row = row0 + i;
+          for (int i = 0; i < kStep; ++i) {
+            const int row = r0 + i;
             if (row >= rows || col >= d) continue;
-            float y = __uint_as_float(o[i]) * cs.inv[row];
-            if (none != 0) y = with_none(p, ds, g, row / G, col, none, y);
-            if (whole) static_cast<__nv_bfloat16*>(a.o)[cs.out[row] + col] = __float2bfloat16_rn(y);
-            else p.part_o[cs.out[row] + col] = y;
+            float y = __uint_as_float(o[i]) * it.inv[row];
+            if (none != 0) y = with_none(p, it.draft, g, row / G, col, none, y);
+            if (whole) static_cast<__nv_bfloat16*>(a.o)[it.out[row] + col] = __float2bfloat16_rn(y);
+            else p.part_o[it.out[row] + col] = y;
           }
         }
         tc_fence_before_sync();
       }
-      if (ok && t == 0) report(p, mine, walk, g, rows, bad_tree, bad);
+      if (ok && u == 0) report(p, mine, behind, g, rows, bad_tree, bad);
+      side_sync();  // before this place is made anew
+      warp_arrive(&cs.ofree[k & 1]);
     }
   }
 
@@ -469,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kLoadWarp) drain_copies(rs.kfull, armed);
     if (warp == kLoadWarp + 1) drain_copies(rs.vfull, armed);
-    if (warp >= kMmaWarp) {
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       uint64_t* drain = &cs.drain[warp - kMmaWarp];
       if (elect_one()) mma_commit(drain);
       __syncwarp();

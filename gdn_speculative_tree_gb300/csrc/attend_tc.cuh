@@ -36,7 +36,7 @@ namespace treewy {
 
 constexpr int kTile = 128;                      // tokens, and rows at most
 constexpr int kGroups = kTile / 16;             // the smallest page is 16 tokens
-constexpr int kMaxListed = 768;                 // requests whose tiles are put in a row
+constexpr int kMaxListed = 640;                 // requests whose tiles are put in a row
 constexpr int kMaxPieces = 152;                 // CTAs that share the row
 constexpr float kGrowth = 5.f, kBias = 6.f;     // lo is at most 2^-3 of a weight: 2^(kGrowth + kBias - 3) <= 448
 constexpr float kLeast = 1e-37f;                // of a score's factor: -inf times it stays -inf
@@ -494,14 +494,14 @@ __device__ __forceinline__ void drain_copies(uint64_t (&full)[S], int armed) {
 }
 
 // A segment's queries, and the draft's keys and values where it has them, as
-// terms, by WARPS warps.  ROWS of a warp's rows are loaded at once, and
+// terms, by WARPS warps (this one's number: `warp`).  ROWS of a warp's rows are loaded at once, and
 // converted two at a time: little code, which a CTA meets for the first time
 // here.
 // place(kind, i, ..) writes row i of the queries (kind 0), keys (1) or values (2).
 template <int NH, int WARPS, int ROWS, typename Place>
-__device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, float factor, Place place) {
+__device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, float factor, int warp, Place place) {
   const treewy_attn& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.cache.d, G = p.G, row0 = g.m * kTile;
+  const int lane = threadIdx.x & 31, d = a.cache.d, G = p.G, row0 = g.m * kTile;
   const int each = (rows + WARPS - 1) / WARPS, begin = warp * each;
 #pragma unroll 1
   for (int pass = 0; pass < (g.t0 == 0 ? 2 : 1); ++pass) {
@@ -567,12 +567,12 @@ __device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const 
   }
 }
 
-// Zeros in the 128-byte rows [lo, hi) of `blocks` blocks of 128 rows, by THREADS threads.
+// Zeros in the 128-byte rows [lo, hi) of `blocks` blocks, by THREADS threads (this one: t).
 template <int THREADS>
-__device__ __forceinline__ void zero_rows(unsigned char* tile, int blocks, uint32_t block, int lo, int hi) {
+__device__ __forceinline__ void zero_rows(unsigned char* tile, int blocks, uint32_t block, int lo, int hi, int t) {
   for (int x = 0; x < blocks; ++x)
 #pragma unroll 1
-    for (int i = lo * 8 + threadIdx.x; i < hi * 8; i += THREADS) *reinterpret_cast<uint4*>(tile + x * block + i * 16) = make_uint4(0, 0, 0, 0);
+    for (int i = lo * 8 + t; i < hi * 8; i += THREADS) *reinterpret_cast<uint4*>(tile + x * block + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // Parents of the segment's nodes; who sees whom.
