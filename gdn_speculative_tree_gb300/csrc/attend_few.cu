@@ -8,12 +8,12 @@
 // and the columns are rows (of the queries, hi and lo terms side by side):
 //
 //   S^T = K Q^T     M = 128 tokens, N = 2 NR, from the page as it is
-//   w               a thread has one token of NR / 2 rows; their terms go to
+//   w               a thread has one token of 4 or 8 rows; their terms go to
 //                   shared memory, a byte each
 //   O^T += V^T w^T  M = 128 columns of the head (V's rows run along the sum)
 //
 // A product of N = 16 takes an eighth of the time of one of 128, and the
-// softmax of a tile is spread over all 256 threads.
+// softmax of a tile is spread over 256 or 512 threads.
 //
 // The draft's keys and values are the terms' rows 0 .. 31 (hi) and 64 .. 95
 // (lo) of a tile: the keys' products are added up in S^T, and the weights of
@@ -24,24 +24,25 @@
 // queries and draft while the softmax goes through this one's tiles, and write
 // the last one's outputs (queries, drafts and O are there twice).
 //
-//   warps 0-7     softmax
-//   warps 8, 9    page table, scales and pages (TMA): keys, and values
-//   warps 10, 11  issue the products, S up to four tiles ahead of O
-//   warps 12-15   queries and draft to e4m3; outputs
+//   8 or 16 warps  softmax
+//   two            page table, scales and pages (TMA): keys, and values
+//   two            issue the products, S up to four tiles ahead of O
+//   four           queries and draft to e4m3; outputs
 #include "attend_tc.cuh"
 
 namespace treewy {
 namespace {
 
-constexpr int kSoftWarps = 8, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;  // and the next one
-constexpr int kSideWarp = kMmaWarp + 2, kSideWarps = 4, kSideThreads = 32 * kSideWarps;
-constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kSideWarp + kSideWarps);
+constexpr int kSideWarps = 4, kSideThreads = 32 * kSideWarps;
 constexpr int kAhead = 4;  // tiles of S
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
 // NH: halves of 128 columns of a head; NR: rows, 8, 16 or 32.
 template <int NH, int NR>
 struct Shape {
+  static constexpr int kGroups = NR == 8 ? 2 : 4, kRowsOf = NR / kGroups;   // of warps that share a tile's tokens; rows of a thread
+  static constexpr int kSoftWarps = 4 * kGroups, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2, kSideWarp = kMmaWarp + 2;
+  static constexpr int kThreads = 32 * (kSideWarp + kSideWarps);
   static constexpr uint32_t kRowBytes = 2 * NR * 128;                // hi and lo rows of 128 bytes
   static constexpr int kCols = NR < 16 ? 16 : NR;                    // of a product of the weights, 16 at least
   static constexpr uint32_t kWBlock = kCols * 128;                   // a term of a tile's weights
@@ -145,11 +146,12 @@ static __device__ __noinline__ float with_none(const Params& p, const DraftSmem&
 }
 
 template <int NH, int NR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
     attend_few_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
   using Sh = Shape<NH, NR>;
-  constexpr int S = Sh::kStages, NT = NR / 2;  // rows of a thread
+  constexpr int S = Sh::kStages, NT = Sh::kRowsOf, kThreads = Sh::kThreads, kSoftWarps = Sh::kSoftWarps, kSoftThreads = 32 * kSoftWarps;
+  constexpr int kLoadWarp = Sh::kLoadWarp, kMmaWarp = Sh::kMmaWarp, kSideWarp = Sh::kSideWarp;
   extern __shared__ unsigned char raw_smem[];
   __shared__ FewSmem<S> cs;
   RingSmem<S>& rs = cs.ring;
@@ -287,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kSoftWarps) {
-    // ---- softmax: warps w and w + 4 have the tokens 32 (w % 4) .., each of them half of the rows
-    const int quarter = warp & 3, hf = warp >> 2, row0 = hf * NT, token = quarter * 32 + lane;
+    // ---- softmax: a warp has the tokens 32 (w % 4) .. of a part of the rows
+    const int quarter = warp & 3, row0 = (warp >> 2) * NT, token = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     auto all_sync = [] { named_bar_sync<1, kSoftThreads>(); };
 #pragma unroll 1
@@ -544,7 +546,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& k, const CUtensorMap& v, 
     return cudaFuncSetAttribute(attend_few_kernel<NH, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NH, NR>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  return launch_after_smem(attend_few_kernel<NH, NR>, dim3(grid), kThreads, Shape<NH, NR>::kBytes, stream, p, k, v);
+  return launch_after_smem(attend_few_kernel<NH, NR>, dim3(grid), Shape<NH, NR>::kThreads, Shape<NH, NR>::kBytes, stream, p, k, v);
 }
 
 template <int NH>

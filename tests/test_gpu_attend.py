@@ -62,18 +62,18 @@ def test_many_requests(cuda_lib, nodes, max_nodes):
     assert not a.status.any()
 
 
-@pytest.mark.parametrize("d,page,nodes", [(128, 16, 4), (128, 64, 1), (256, 64, 1), (256, 32, 8), (64, 128, 2), (128, 32, 16), (256, 64, 12)])
+@pytest.mark.parametrize("d,page,nodes", [(128, 16, 4), (256, 64, 1), (256, 32, 8), (128, 32, 16)])
 def test_several_items_of_many_tiles_to_a_piece(cuda_lib, d, page, nodes):
     """Pieces of the work that hold the end of one item, two or three whole ones and the beginning of another."""
     r = np.random.RandomState(d + nodes)
-    R = 64
+    R = 130
     lengths = np.where(r.rand(R) < 0.1, r.randint(0, 100, R), r.randint(700, 1500, R))
-    a = Attend(lengths, r.randint(1, nodes + 1, R), Hq=32, Hkv=8, d=d, page=page, max_nodes=nodes, seed=nodes)
+    a = Attend(lengths, r.randint(1, nodes + 1, R), Hq=16, Hkv=4, d=d, page=page, max_nodes=nodes, seed=nodes, quick=True)
     for _ in range(3):
         a.run()
-    a.check(range(0, R, 13))
+    a.check([0, 50, 129])
     assert not a.status.any()
-    b = Attend(lengths, a.nodes, Hq=32, Hkv=8, d=d, page=page, max_nodes=nodes, seed=nodes, flags=GENERIC).run()
+    b = Attend(lengths, a.nodes, Hq=16, Hkv=4, d=d, page=page, max_nodes=nodes, seed=nodes, flags=GENERIC, quick=True).run()
     # weights to 2^-8, a bf16 output's own rounding on both sides
     assert (a.o.float() - b.o.float()).abs().max() <= 2 * 2.0 ** -7 * b.o.float().abs().max()
 
