@@ -1,10 +1,14 @@
-"""One GDN layer of a server, from a prompt to a verified draft.
+"""One GDN layer of a server, from a prompt to a verified draft; and the softmax
+layer of a hybrid behind it.
 
 Requests bring prompts; their queries and keys are normed, their states made
 from the prompts, each request's state is forked to two samples, a draft tree
 is verified for every sample and the accepted node committed, and the next
-token is taken in without a draft.  Everything runs on one stream, without the
-host waiting for the device until the end.
+token is taken in without a draft.  The softmax layer norms the residual
+stream's rows into 8 bits, takes the prompts' keys and values into pages of 8
+bits, verifies the same tree against them and takes the accepted path.
+Everything runs on one stream, without the host waiting for the device until
+the end.
 
     python examples/serve_round.py [--requests 4] [--prompt 300] [--heads 8]
 """
@@ -84,6 +88,70 @@ class Layer:
         return o, status
 
 
+class SoftmaxLayer:
+    """A softmax layer's heads and its 8-bit pages of keys and values, one row of the page table per request."""
+
+    def __init__(self, Hq: int, Hkv: int, requests: int, most: int, d: int = 128, page: int = 64, seed: int = 0):
+        self.Hq, self.Hkv, self.d, self.most, self.scale = Hq, Hkv, d, most, d ** -0.5
+        self.g = torch.Generator(device="cuda").manual_seed(seed + 100)
+        width = -(-most // page)
+        codes = torch.zeros(2, requests * width, Hkv, page, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        scales = torch.ones(2, requests * width, Hkv, device="cuda")
+        table = torch.randperm(requests * width, generator=self.g, device="cuda").to(torch.int32).view(requests, width)
+        self.length, self.after = (torch.zeros(requests, dtype=torch.int32, device="cuda") for _ in range(2))
+        self.status = torch.zeros(requests, dtype=torch.int32, device="cuda")
+        self.cache = binding.make_cache(k=codes[0], v=codes[1], k_scale=scales[0], v_scale=scales[1], page_table=table,
+                                        length=self.length)
+
+    def project(self, T: int, hidden: int = 256):
+        """T tokens: the residual stream's rows normed into 8 bits for the projection, whose rows (random here) come back."""
+        x, residual = (torch.randn(T, hidden, generator=self.g, device="cuda").bfloat16() for _ in range(2))
+        rows = torch.empty(T, hidden, device="cuda", dtype=torch.float8_e4m3fn)
+        scales = torch.empty(T, hidden // 128, device="cuda")
+        binding.treewy_add_norm(binding.make_norm(x=x, residual=residual, residual_out=residual, y8=rows, y8_scale=scales,
+                                                  group=128))
+        wide = torch.randn(T, (self.Hq + 2 * self.Hkv) * self.d, generator=self.g, device="cuda").bfloat16()
+        q, k, v = wide.split([self.Hq * self.d, self.Hkv * self.d, self.Hkv * self.d], dim=1)
+        q, k, v = q.view(T, self.Hq, self.d), k.view(T, self.Hkv, self.d), v.view(T, self.Hkv, self.d)
+        qo, ko = (torch.empty(x.shape, device="cuda", dtype=x.dtype) for x in (q, k))
+        binding.treewy_qk_norm(binding.make_qk(q=q, k=k, q_out=qo, k_out=ko, norm="rms"))
+        return qo, ko, v
+
+    def append(self, off, k, v, most: int, parent=None, accepted=None):
+        binding.treewy_append(binding.make_append(cache=self.cache, node_offset=off, parent=parent, accepted=accepted, k=k, v=v,
+                                                  new_length=self.after, status=self.status, max_new=most))
+        self.length.copy_(self.after)
+
+    def attend(self, off, parent, q, k, v, most: int):
+        o = torch.empty(q.shape, device="cuda", dtype=q.dtype)
+        binding.treewy_attend(binding.make_attn(cache=self.cache, node_offset=off, parent=parent, q=q, k=k, v=v, o=o,
+                                                status=self.status, scale=self.scale, max_nodes=most, max_context=self.most))
+        return o
+
+
+def softmax_round(requests: int = 4, prompt: int = 300, heads: int = 8, seed: int = 0):
+    """Prompts, a verified tree with its accepted path, and a single token; returns the layer and its outputs by step."""
+    tree = workloads.complete_binary_parents(4)
+    lengths = [max(1, prompt - 37 * r) for r in range(requests)]
+    layer = SoftmaxLayer(heads, max(1, heads // 4), requests, max(lengths) + len(tree) + 1, seed=seed)
+
+    def offsets(n):
+        return torch.tensor([0] + list(torch.tensor(n).cumsum(0)), dtype=torch.int32, device="cuda")
+
+    _, k, v = layer.project(sum(lengths))
+    layer.append(offsets(lengths), k, v, max(lengths))
+    out, off, N = {}, offsets([len(tree)] * requests), len(tree)
+    parent = torch.as_tensor(tree, dtype=torch.int32).repeat(requests).cuda()
+    q, k, v = layer.project(requests * N)
+    out["draft"] = layer.attend(off, parent, q, k, v, N)
+    accepted = torch.randint(-1, N, (requests,), generator=layer.g, device="cuda", dtype=torch.int32)
+    layer.append(off, k, v, N, parent, accepted)
+    q, k, v = layer.project(requests)
+    out["token"] = layer.attend(offsets([1] * requests), None, q, k, v, 1)
+    layer.append(offsets([1] * requests), k, v, 1)
+    return layer, out
+
+
 def run(requests: int = 4, prompt: int = 300, heads: int = 8, seed: int = 0):
     """One round; returns the layer, its outputs by step and every status word."""
     layer = Layer(heads, max(1, heads // 2), 2 * requests, seed=seed)
@@ -115,6 +183,11 @@ def main() -> None:
     assert not status.any().item(), status.tolist()
     for step, o in out.items():
         print(f"{step:7s} {tuple(o.shape)} rms {o.float().square().mean().sqrt().item():.4f}")
+    softmax, out = softmax_round(a.requests, a.prompt, a.heads)
+    torch.cuda.synchronize()
+    assert not softmax.status.any().item(), softmax.status.tolist()
+    for step, o in out.items():
+        print(f"softmax layer, {step:7s} {tuple(o.shape)} rms {o.float().square().mean().sqrt().item():.4f}")
     print(f"states  {tuple(layer.pool.shape)} rms {layer.pool.square().mean().sqrt().item():.4f}")
 
 

@@ -54,7 +54,20 @@ struct Piece {
       }
     }
   }
-  __device__ float largest() const {
+  // |values| as whole numbers, which order them: the largest so far of two in a word (bf16), or of one.
+  __device__ uint32_t largest(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 2) m = __vmaxu2(m, u[e] & 0x7fff7fffu);
+        else m = max(m, u[e] & 0x7fffffffu);
+      }
+    }
+    return m;
+  }
+  __device__ float largest_finite() const {
     float x[8], top = 0.f;
     values(x);
 #pragma unroll
@@ -65,6 +78,13 @@ struct Piece {
     float x[8];
     values(x);
     return make_uint2(z.pair(x[0], x[1]) | (z.pair(x[2], x[3]) << 16), z.pair(x[4], x[5]) | (z.pair(x[6], x[7]) << 16));
+  }
+  // The same where all are finite and 1 / scale is exact.
+  __device__ uint2 codes(float inv) const {
+    float x[8];
+    values(x);
+    return make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | (e4m3x2(x[2] * inv, x[3] * inv) << 16),
+                      e4m3x2(x[4] * inv, x[5] * inv) | (e4m3x2(x[6] * inv, x[7] * inv) << 16));
   }
 };
 
@@ -84,10 +104,10 @@ __device__ __forceinline__ uint32_t again(uint32_t w, float f) {
 // largest to the writing, what is behind them is read twice; 0: one value at a
 // time, read twice (odd sizes).
 template <typename T, int HOLD>
-__global__ void __launch_bounds__(256, HOLD == 8 && sizeof(T) == 2 ? 3 : 1) append_kernel(const treewy_append_args a, int pages) {
+__global__ void __launch_bounds__(256) append_kernel(const treewy_append_args a, int pages) {
   after_previous();
   __shared__ int parent[kMaxNodes], path[kMaxNodes], count;
-  __shared__ float part[8];
+  __shared__ uint32_t part[8];
   const treewy_cache& c = a.cache;
   const int t = threadIdx.x, P = c.page_len, d = c.d, threads = blockDim.x;
   // heads are neighbours as they are in a row, then keys and values, pages, requests
@@ -116,30 +136,27 @@ __global__ void __launch_bounds__(256, HOLD == 8 && sizeof(T) == 2 ? 3 : 1) appe
   }
   // what goes into this CTA's page
   const int first = q.len / P;
-  const int64_t begin = static_cast<int64_t>(first + i) * P, after = static_cast<int64_t>(q.len) + m;
+  const int64_t begin = (static_cast<int64_t>(first) + i) * P, after = static_cast<int64_t>(q.len) + m;
   const int lo = max(0, static_cast<int>(q.len - begin));  // tokens that it holds already
-  const int hi = static_cast<int>(min(static_cast<int64_t>(P), after - begin));
-  const bool mine = q.err == 0 && m > 0 && begin < after;
-  const int j0 = static_cast<int>(begin + lo - q.len);       // the first new one
+  const int hi = q.err == 0 && m > 0 && begin < after ? static_cast<int>(min(static_cast<int64_t>(P), after - begin)) : 0;  // and with the new ones
+  const int j0 = static_cast<int>(begin + lo - q.len);       // the first of them
   const T* rows = static_cast<const T*>(values ? a.v : a.k) + static_cast<int64_t>(h) * d;
   const int64_t stride = values ? a.v_stride : a.k_stride;
-  auto row_of = [&](int s) {  // of the page's row s
-    const int j = j0 + s - lo;
+  const int32_t* table = c.page_table + static_cast<int64_t>(r) * c.max_pages;
+  auto row_of = [&](int row) {  // of the page
+    const int j = j0 + row - lo;
     return rows + (static_cast<int64_t>(q.lo) + (a.accepted != nullptr ? path[j] : j)) * stride;
   };
   // a thread's pieces: its first row and column, and the way to the next ones
   const int per = HOLD > 0 ? d / 8 : d, row0 = t / per, col0 = t - row0 * per, down = threads / per, right = threads - down * per;
   Piece<T> x[HOLD > 0 ? HOLD : 1];
-  float top = 0.f;
-  if (mine) {
-    if constexpr (HOLD > 0) {  // on their way while the pages are looked at
-      int s = lo + row0, col = col0;
+  if constexpr (HOLD > 0) {  // on their way while the pages are looked at
+    int row = lo + row0, col = col0;
 #pragma unroll
-      for (int e = 0; e < HOLD; ++e) {
-        if (s < hi) x[e].load(row_of(s) + 8 * col);
-        s += down, col += right;
-        if (col >= per) col -= per, ++s;
-      }
+    for (int e = 0; e < HOLD; ++e) {
+      if (row < hi) x[e].load(row_of(row) + 8 * col);
+      row += down, col += right;
+      if (col >= per) col -= per, ++row;
     }
   }
   if (q.err == 0 && m > 0) {
@@ -147,7 +164,7 @@ __global__ void __launch_bounds__(256, HOLD == 8 && sizeof(T) == 2 ? 3 : 1) appe
     if (!bad) {
       const int last = static_cast<int>((after - 1) / P);
       for (int p = first + t; p <= last; p += threads) {
-        const int page = __ldg(c.page_table + static_cast<int64_t>(r) * c.max_pages + p);
+        const int page = __ldg(table + p);
         bad |= page < 0 || page >= c.num_pages;
       }
     }
@@ -158,71 +175,72 @@ __global__ void __launch_bounds__(256, HOLD == 8 && sizeof(T) == 2 ? 3 : 1) appe
     return;
   }
   if (first_cta && a.new_length != nullptr) a.new_length[r] = static_cast<int>(after);
-  if (!mine) return;
-  const int page = __ldg(c.page_table + static_cast<int64_t>(r) * c.max_pages + first + i);
+  if (hi == 0) return;
+  const int page = __ldg(table + first + i);
   const int64_t block = static_cast<int64_t>(page) * c.Hkv + h;
   uint8_t* codes = static_cast<uint8_t*>(values ? c.v : c.k) + block * P * d;
   float* scale = (values ? c.v_scale : c.k_scale) + block;
   const float was = lo > 0 ? *scale : 0.f;
-  {
-    int s = lo + row0, col = col0;
+  int row = 0, col = 0;
+  auto step = [&] {
+    row += down, col += right;
+    if (col >= per) col -= per, ++row;
+  };
+  // f(piece, where it goes) for all of the thread's, those in the registers first
+  auto pieces = [&](auto f) {
+    row = lo + row0, col = col0;
     if constexpr (HOLD > 0) {
 #pragma unroll
       for (int e = 0; e < HOLD; ++e) {
-        if (s < hi) top = fmaxf(top, x[e].largest());
-        s += down, col += right;
-        if (col >= per) col -= per, ++s;
+        if (row < hi) f(x[e], codes + row * d + 8 * col);
+        step();
       }
-#pragma unroll 2
-      while (s < hi) {
+#pragma unroll 1
+      for (; row < hi; step()) {
         Piece<T> y;
-        y.load(row_of(s) + 8 * col);
-        top = fmaxf(top, y.largest());
-        s += down, col += right;
-        if (col >= per) col -= per, ++s;
-      }
-    } else {
-      while (s < hi) {
-        top = fmaxf(top, size_of(to_f32(__ldg(row_of(s) + col))));
-        s += down, col += right;
-        if (col >= per) col -= per, ++s;
+        y.load(row_of(row) + 8 * col);
+        f(y, codes + row * d + 8 * col);
       }
     }
+  };
+  auto over_cta = [&](uint32_t m, uint32_t* to) {  // the largest of a word of every thread
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((t & 31) == 0) to[t >> 5] = m;
+    __syncthreads();
+    for (int w = 0; w < threads >> 5; ++w) m = max(m, to[w]);
+    return m;
+  };
+  float top;
+  bool plain = false;  // all values are finite
+  if constexpr (HOLD > 0) {
+    uint32_t m = 0;
+    pieces([&](const Piece<T>& y, uint8_t*) { m = y.largest(m); });
+    if constexpr (sizeof(T) == 2) m = max(m & 0xffffu, m >> 16) << 16;
+    m = over_cta(m, part);  // and every thread has read the scale
+    plain = m < 0x7f800000u;
+    top = __uint_as_float(m);
+    if (!plain) {
+      top = 0.f;
+      pieces([&](const Piece<T>& y, uint8_t*) { top = fmaxf(top, y.largest_finite()); });
+      __syncthreads();  // the words of the first search have been read
+      top = __uint_as_float(over_cta(__float_as_uint(top), part));
+    }
+  } else {
+    top = 0.f;
+    for (row = lo + row0, col = col0; row < hi; step()) top = fmaxf(top, size_of(to_f32(__ldg(row_of(row) + col))));
+    top = __uint_as_float(over_cta(__float_as_uint(top), part));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((t & 31) == 0) part[t >> 5] = top;
-  __syncthreads();  // and every thread has read the scale
-  for (int w = 0; w < threads >> 5; ++w) top = fmaxf(top, part[w]);
   float now = was;
   if (lo == 0) now = scale_for(top);
   else if (!(top <= 448.f * was)) now = fmaxf(was, scale_for(top));
   if (t == 0) *scale = now;
   const Quantizer z{now, 1.f / now, (__float_as_uint(now) & 0x7fffffu) == 0};
-  {
-    int s = lo + row0, col = col0;
-    if constexpr (HOLD > 0) {
-#pragma unroll
-      for (int e = 0; e < HOLD; ++e) {
-        if (s < hi) *reinterpret_cast<uint2*>(codes + s * d + 8 * col) = x[e].codes(z);
-        s += down, col += right;
-        if (col >= per) col -= per, ++s;
-      }
-#pragma unroll 2
-      while (s < hi) {
-        Piece<T> y;
-        y.load(row_of(s) + 8 * col);
-        *reinterpret_cast<uint2*>(codes + s * d + 8 * col) = y.codes(z);
-        s += down, col += right;
-        if (col >= per) col -= per, ++s;
-      }
-    } else {
-      while (s < hi) {
-        codes[s * d + col] = static_cast<uint8_t>(z.pair(to_f32(__ldg(row_of(s) + col)), 0.f));
-        s += down, col += right;
-        if (col >= per) col -= per, ++s;
-      }
-    }
+  if constexpr (HOLD > 0) {
+    if (plain && z.exact) pieces([&](const Piece<T>& y, uint8_t* at) { *reinterpret_cast<uint2*>(at) = y.codes(z.inv); });
+    else pieces([&](const Piece<T>& y, uint8_t* at) { *reinterpret_cast<uint2*>(at) = y.codes(z); });
+  } else {
+    for (row = lo + row0, col = col0; row < hi; step())
+      codes[row * d + col] = static_cast<uint8_t>(z.pair(to_f32(__ldg(row_of(row) + col)), 0.f));
   }
   if (now != was && lo > 0) {  // the scale has grown: the older tokens anew
     const float f = was / now;
@@ -239,31 +257,29 @@ __global__ void __launch_bounds__(256, HOLD == 8 && sizeof(T) == 2 ? 3 : 1) appe
 }
 
 template <typename T>
-cudaError_t launch(const treewy_append_args& a, bool wide, dim3 grid, int pages, cudaStream_t stream) {
-  if (!wide) return launch_after(append_kernel<T, 0>, grid, 256, stream, a, pages);
+cudaError_t launch(const treewy_append_args& a, cudaStream_t stream) {
+  const int P = a.cache.page_len;
+  const int64_t pages = (static_cast<int64_t>(a.max_new) + P - 2) / P + 1;  // that max_new rows can touch
+  const int64_t ctas = pages * 2 * a.cache.Hkv;
+  if (ctas > 0x7fffffff / a.R) return cudaErrorNotSupported;
+  const dim3 grid(static_cast<unsigned>(ctas * a.R));
+  const int np = static_cast<int>(pages);
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                        static_cast<uintptr_t>(a.k_stride * sizeof(T)) | static_cast<uintptr_t>(a.v_stride * sizeof(T)) |
+                        static_cast<uintptr_t>(a.cache.d * sizeof(T));
+  if (all % 16 != 0 || a.cache.d % 8 != 0) return launch_after(append_kernel<T, 0>, grid, 256, stream, a, np);
   // paths are short whatever the trees' bound is
-  const int rows = std::min(a.max_new, a.cache.page_len), pieces = (a.accepted != nullptr ? std::min(rows, 8) : rows) * (a.cache.d / 8);
+  const int rows = std::min(a.max_new, P), pieces = (a.accepted != nullptr ? std::min(rows, 8) : rows) * (a.cache.d / 8);
   // CTAs of two warps where a page gets little; of eight, with most of a page in registers, where it gets much
-  if (pieces <= 64) return launch_after(append_kernel<T, 1>, grid, 64, stream, a, pages);
-  if (pieces <= 512) return launch_after(append_kernel<T, 4>, grid, 128, stream, a, pages);
-  return launch_after(append_kernel<T, 8>, grid, 256, stream, a, pages);
+  if (pieces <= 64) return launch_after(append_kernel<T, 1>, grid, 64, stream, a, np);
+  if (pieces <= 512) return launch_after(append_kernel<T, 4>, grid, 128, stream, a, np);
+  return launch_after(append_kernel<T, 8>, grid, 256, stream, a, np);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const treewy_append_args& a, cudaStream_t stream) {
-  const int P = a.cache.page_len;
-  const int64_t pages = (static_cast<int64_t>(a.max_new) + P - 2) / P + 1;
-  const int64_t ctas = pages * 2 * a.cache.Hkv;
-  if (ctas > 0x7fffffff / a.R) return cudaErrorNotSupported;
-  const dim3 grid(static_cast<unsigned>(ctas * a.R));
-  const int size = a.kv_dtype == TREEWY_DTYPE_BF16 ? 2 : 4;
-  const uintptr_t all = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
-                        static_cast<uintptr_t>(a.k_stride * size) | static_cast<uintptr_t>(a.v_stride * size) |
-                        static_cast<uintptr_t>(a.cache.d * size);
-  const bool wide = all % 16 == 0 && a.cache.d % 8 == 0;
-  const int np = static_cast<int>(pages);
-  return size == 2 ? launch<uint16_t>(a, wide, grid, np, stream) : launch<float>(a, wide, grid, np, stream);
+  return a.kv_dtype == TREEWY_DTYPE_BF16 ? launch<uint16_t>(a, stream) : launch<float>(a, stream);
 }
 
 }  // namespace treewy

@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) attend_join_kernel(const __gri
   float sum = 0.f, y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = many ? warp : 0; i < parts; i += many ? kJoinRows : 1) {
     const int64_t at = part_of(i);
     const float f = exp2f(p.part_lse[at] - top);

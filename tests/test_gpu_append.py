@@ -177,3 +177,14 @@ def test_graph_replays_with_other_lengths(cuda_lib):
 def test_no_rows(cuda_lib):
     Append([10, 20], [0, 0], seed=10).run()
     Append([10, 20], [3, 2], accepted=[-1, -1], seed=10).run()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,page,rows,R", [(256, 64, 600, 12), (64, 128, 1500, 40), (256, 16, 300, 30), (128, 64, 63, 600)])
+def test_many_pages_one_after_the_other(cuda_lib, d, page, rows, R, dtype):
+    """Prompts of several groups of pages, some of them short: CTAs that take more than one page."""
+    r = np.random.RandomState(d + rows)
+    lengths = r.randint(0, 3 * page, R)
+    nodes = np.where(r.rand(R) < 0.3, r.randint(0, page, R), r.randint(rows // 2, rows + 1, R))
+    a = Append(lengths, nodes, Hkv=2, d=d, page=page, dtype=dtype, seed=11, max_new=rows).run()
+    assert not a.status.any()
