@@ -59,6 +59,7 @@ treewy_status validate_attn_sizes(const treewy_attn* a) {
   if (a->max_nodes < 1 || a->max_nodes > TREEWY_MAX_NODES)
     return fail(a->max_nodes < 1 ? TREEWY_ERR_INVALID_ARG : TREEWY_ERR_UNSUPPORTED, "max_nodes = %d outside [1, %d]",
                 a->max_nodes, TREEWY_MAX_NODES);
+  if (a->T < 0 || a->T > kMax31) return fail(TREEWY_ERR_INVALID_ARG, "T = %lld outside [0, 2^31)", (long long)a->T);
   if (a->max_context < 0) return fail(TREEWY_ERR_INVALID_ARG, "max_context = %d is negative", a->max_context);
   if (!known(a->qkv_dtype) || !known(a->o_dtype))
     return fail(TREEWY_ERR_INVALID_ARG, "qkv_dtype = %d, o_dtype = %d: not TREEWY_DTYPE_BF16/F32", a->qkv_dtype, a->o_dtype);
@@ -71,7 +72,6 @@ treewy_status validate_attn(const treewy_attn* a) {
   treewy_status st = validate_attn_sizes(a);
   if (st != TREEWY_OK) return st;
   const treewy_cache& c = a->cache;
-  if (a->T < 0 || a->T > kMax31) return fail(TREEWY_ERR_INVALID_ARG, "T = %lld outside [0, 2^31)", (long long)a->T);
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return fail(TREEWY_ERR_INVALID_ARG, "scale must be positive and finite");
   for (auto [stride, heads] : {std::pair<int64_t, int64_t>{a->q_stride, a->Hq}, {a->k_stride, c.Hkv}, {a->v_stride, c.Hkv}})
     if ((st = validate_stride(stride, heads * c.d)) != TREEWY_OK) return st;

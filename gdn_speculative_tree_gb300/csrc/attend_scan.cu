@@ -77,7 +77,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
   float top = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int e = 0; e < kMaxPad / 32; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int context_tiles = (q.len + kTile - 1) / kTile, tiles = context_tiles + (q.N + kTile - 1) / kTile;
+  const int context_tiles = q.len / kTile + (q.len % kTile != 0), tiles = context_tiles + (q.N + kTile - 1) / kTile;
   for (int j = rank; j < tiles; j += kRanks) {
     const bool context = j < context_tiles;
     const int t0 = (context ? j : j - context_tiles) * kTile, n = min(kTile, (context ? q.len : q.N) - t0);

@@ -286,7 +286,7 @@ struct Segment {
   int lo, N, len;
 };
 
-__device__ __forceinline__ int tiles_of(int len) { return 1 + (len + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(int len) { return 1 + len / kTile + (len % kTile != 0); }
 __device__ __forceinline__ int row_tiles(const Params& p, int N) { return (N * p.G + kTile - 1) / kTile; }
 
 // Walks a CTA's segments; every role walks them for itself.
@@ -393,7 +393,7 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
   if (t == 0) {  // a second, and a hundred times what a tile takes
     ring.fail = 0;
     ring.deadline = globaltimer_ns() + 1000000000ull +
-                    100000ull * static_cast<uint64_t>(p.listed ? part.walk.end - part.walk.u : 1 + a.max_context / kTile);
+                    100000ull * static_cast<uint64_t>(p.listed ? part.walk.end - part.walk.u : tiles_of(cs.len[0]));
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -416,13 +416,14 @@ __device__ __forceinline__ int load_pages(const Params& p, Cs& cs, RingSmem<S>& 
   uint64_t* const full = kValues ? rs.vfull : rs.kfull;
   uint64_t* const free = kValues ? rs.vfree : rs.kfree;
   int armed = 0, gt = 0, slot = 0;
+  asm volatile("fence.proxy.async.global;" ::: "memory");  // pages and terms that an earlier kernel wrote
   uint32_t again = 1;  // parity of the stage's use before
   Segment g;
 #pragma unroll 1
   while (walk.next(p, cs.plan, g)) {
     if (!begin(g)) return armed;
     const int32_t* table = c.page_table + static_cast<int64_t>(g.r) * c.max_pages;
-    const int pages = (g.len + P - 1) / P;
+    const int pages = g.len / P + (g.len % P != 0);
     auto entry = [&](int i) { return i < pages ? __ldg(table + i) : -1; };
     auto scale = [&](const float* x, int page) {
       return page >= 0 && page < c.num_pages ? __ldg(x + static_cast<int64_t>(page) * c.Hkv + g.h) : 1.f;

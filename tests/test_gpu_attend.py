@@ -38,6 +38,12 @@ def test_sizes_beside_the_tensor_cores(cuda_lib, d):
     Attend([40, 0, 200], [3, 9, 1], Hq=6, Hkv=2, d=d, page=32, seed=d).run().check()
 
 
+@pytest.mark.parametrize("d", [16, 32, 48, 112, 144, 208, 240])
+@pytest.mark.parametrize("Hq,Hkv,nodes", [(3, 3, [1, 5, 2]), (48, 1, [5, 1, 3]), (40, 2, [1, 1, 1]), (64, 32, [9, 0, 30])])
+def test_every_head_size_and_many_heads(cuda_lib, d, Hq, Hkv, nodes):
+    Attend([130, 7, 64], nodes, Hq=Hq, Hkv=Hkv, d=d, page=16, seed=d + Hq).run().check()
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (1, 0), (0, 1), (256, 3)])
 @pytest.mark.parametrize("d", [64, 256])
 def test_strided_and_unaligned_rows(cuda_lib, d, pad, shift):
@@ -285,6 +291,24 @@ def test_graph_on_another_stream_with_other_contents(cuda_lib, flags):
     torch.cuda.synchronize()
     a.check()
     assert not a.status.any()
+
+
+def test_bounds_as_large_as_they_go(cuda_lib):
+    """The largest bound on the contexts, and the largest on the nodes, for small ones; a table of one empty page each."""
+    for kw in (dict(Hq=4, Hkv=2), dict(Hq=32, Hkv=2), dict(Hq=4, Hkv=2, flags=GENERIC)):
+        Attend([33, 200, 0], [2, 1, 3], d=64, page=32, max_context=(1 << 31) - 1, max_nodes=64, seed=22, **kw).run().check()
+        a = Attend([0, 0], [3, 1], d=64, page=32, max_context=(1 << 31) - 1, seed=23, **kw)
+        a.cache.table = a.cache.table[:, :0].contiguous()
+        a.run().check()
+
+
+@pytest.mark.parametrize("Hq", [4, 64])
+def test_no_rows_at_all(cuda_lib, Hq):
+    """Requests without a node, with contexts; and one whose length is refused all the same."""
+    a = Attend([100, 20], [0, 0], Hq=Hq, Hkv=2, d=64, page=32, max_nodes=4)
+    a.cache.length[1] = -5
+    a.run()
+    assert a.status.tolist() == [0, binding.STATUS_BAD_PAGE]
 
 
 def test_two_calls_at_once(cuda_lib):
