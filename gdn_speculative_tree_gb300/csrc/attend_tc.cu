@@ -10,7 +10,8 @@
 // A tile is 128 rows, (node, query head) pairs that share a key head, times
 // 128 tokens.  TMEM lanes are rows:
 //
-//   S = Q K^T          Q's terms and K in shared memory, S in TMEM, twice
+//   S = Q K^T          Q's terms and K in shared memory, S in TMEM, twice (three
+//                      times for heads of up to 128, where O leaves room)
 //   w                  two terms, back in TMEM in the place of S
 //   O += w V           V in shared memory as it is stored (rows along the sum)
 //
@@ -25,7 +26,7 @@
 //
 //   warps 0-15   softmax, outputs
 //   warps 16, 17 page table, scales, pages and terms (TMA): keys, and values
-//   warp 18      issues the products: S of the next tile before O of this one
+//   warp 18      issues the products: S of the next tiles before O of this one
 #include "attend_tc.cuh"
 
 namespace treewy {
@@ -34,7 +35,7 @@ namespace {
 constexpr int kSets = 2, kSetWarps = 8, kSoftWarps = kSets * kSetWarps, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2;
 constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kParts = kSoftWarps / 4;  // warps that share 32 rows
-constexpr uint32_t kColO = 0, kColS = 256, kTmemCols = 512;
+constexpr uint32_t kColO = 0, kTmemCols = 512;
 
 // Terms of every row: a warp takes four rows of a token (its query heads, then
 // key heads, keys and values) at a time.  Units are the exponents of a row's
@@ -87,13 +88,15 @@ template <int NH>
 struct Shape {
   static constexpr uint32_t kQBytes = 2 * NH * kHalf, kStage = 2 * NH * kHalf;  // hi and lo; K and V
   static constexpr int kStages = NH == 2 ? 2 : 5;
+  static constexpr int kScores = NH == 2 ? 2 : 3;      // tiles of S
+  static constexpr uint32_t kColS = kTmemCols - kScores * kTile;
   static constexpr uint32_t kBytes = kQBytes + kStages * kStage + 1024;
 };
 
 template <int S>
 struct AttendSmem {
   RingSmem<S> ring;
-  uint64_t sfull[2], mdone[2], pready[2], pvdone[2], qfull, qfree, drain;
+  uint64_t sfull[3], mdone[2], pready[2], pvdone[2], qfull, qfree, drain;
   float ref[kTile], first[kSets][kTile], half[kSets][2][kTile], sum[kParts][kTile];  // of the rows
   uint32_t tmem;
   int bad;                       // a page of the segment's
@@ -110,7 +113,7 @@ struct Maps {
 template <int NH>
 __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using Sh = Shape<NH>;
-  constexpr int S = Sh::kStages;
+  constexpr int S = Sh::kStages, B = Sh::kScores;
   extern __shared__ unsigned char raw_smem[];
   __shared__ AttendSmem<S> cs;
   RingSmem<S>& rs = cs.ring;
@@ -123,8 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   // ---- set-up, while the kernel before may still run
   if (t == 0) {
     init_ring(rs);
+    for (int i = 0; i < 3; ++i) mbar_init(&cs.sfull[i], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&cs.sfull[i], 1);
       mbar_init(&cs.mdone[i], kSetWarps);
       mbar_init(&cs.pready[i], kSetWarps);
       mbar_init(&cs.pvdone[i], 1);
@@ -193,22 +196,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     // ---- products
     const uint32_t id_s = idesc_f8(kTile, false, false), id_o = idesc_f8(d, false, true);
     const uint32_t q0 = smem_addr(smem), r0 = smem_addr(ring);
-    int seg = 0;
+    int seg = 0, tile = 0;  // tile: whose S is next
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next(p, cs.plan, g)) {
       ok = wait_warp(rs, &cs.qfull, seg & 1);
       ++seg;
-      // S of the next tile, then O of the last
+      // S of B - 1 tiles ahead, then O of this one
+      const int end = gt + g.t1 - g.t0;
 #pragma unroll 1
-      for (int j = g.t0 - 1; ok && j < g.t1; ++j) {
-        if (j + 1 < g.t1) {
-          const int tile = gt + (j >= g.t0 ? 1 : 0), slot = tile % S;
+      for (int j = g.t0 - (B - 1); ok && j < g.t1; ++j) {
+        if (tile < end) {
+          const int slot = tile % S;
           ok = wait_warp(rs, &rs.kfull[slot], (tile / S) & 1);
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one()) {
-            const uint32_t s = tmem + kColS + (tile & 1) * kTile, k0 = r0 + slot * Sh::kStage;
+            const uint32_t s = tmem + Sh::kColS + tile % B * kTile, k0 = r0 + slot * Sh::kStage;
             uint32_t acc = 0;
 #pragma unroll
             for (int x = 0; x < NH; ++x) {
@@ -224,10 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 }
               }
             }
-            mma_commit(&cs.sfull[tile & 1]);
+            mma_commit(&cs.sfull[tile % B]);
             mma_commit(&rs.kfree[slot]);
           }
           __syncwarp();
+          ++tile;
         }
         if (j < g.t0) continue;
         const int slot = gt % S;
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         tc_fence_after_sync();
         const int n = j == 0 ? kTile : min(kTile, g.len - (j - 1) * kTile);
         if (elect_one()) {
-          const uint32_t w = tmem + kColS + (gt & 1) * kTile, v0 = r0 + slot * Sh::kStage + NH * kHalf;
+          const uint32_t w = tmem + Sh::kColS + gt % B * kTile, v0 = r0 + slot * Sh::kStage + NH * kHalf;
           uint32_t acc = j != g.t0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   } else {
     // ---- softmax: a warp has lanes 32 (w % 4) .. and half of the tokens, of its set's tiles (even or odd ones)
     const int quarter = warp & 3, hf = (warp >> 2) & 1, set = warp >> 3, row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16), sc = lanes + kColS + set * kTile;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float factor = a.scale * 1.4426950408889634f;  // scores in powers of two
     auto all_sync = [] { named_bar_sync<1, kSoftThreads>(); };
     auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3) + 4 * set) : "memory"); };
@@ -293,7 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         const Consts& cc = rs.c[slot];
         if ((gt & 1) != set) continue;
         // after a wait that gave up a warp still comes by every barrier of threads
-        bool ok = wait_warp(rs, &cs.sfull[set], (gt >> 1) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
+        const uint32_t sc = lanes + Sh::kColS + gt % B * kTile;
+        bool ok = wait_warp(rs, &cs.sfull[gt % B], (gt / B) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
+        // the set's last product, so that none of its phases is missed (with two tiles of S, S itself came behind it)
+        if (B > 2 && gt >= 2) wait_warp(rs, &cs.pvdone[set], ((gt - 2) >> 1) & 1);
         tc_fence_after_sync();
         if (cc.bad != 0) cs.bad = 1;
         const int n = j == 0 ? kTile : min(kTile, len - (j - 1) * kTile);
