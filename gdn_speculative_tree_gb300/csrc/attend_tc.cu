@@ -99,7 +99,7 @@ struct AttendSmem {
   uint64_t sfull[3], mdone[2], pready[2], pvdone[2], qfull, qfree, drain;
   float ref[kTile], first[kSets][kTile], half[kSets][2][kTile], sum[kParts][kTile];  // of the rows
   uint32_t tmem;
-  int bad;                       // a page of the segment's
+  int bad[2];                    // a page of the segment's: two in turn, as warps still read the last one's
   Segment segment;               // the softmax warps' current one
   DraftSmem draft;
   PlanSmem plan;
@@ -266,12 +266,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float factor = a.scale * 1.4426950408889634f;  // scores in powers of two
     auto all_sync = [] { named_bar_sync<1, kSoftThreads>(); };
+    int turn = 0;
     auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(2 + (warp & 3) + 4 * set) : "memory"); };
 #pragma unroll 1
-    while (walk.next(p, cs.plan, g)) {
+    for (; walk.next(p, cs.plan, g); turn ^= 1) {
       // tree and units
       const int rows = min(kTile, g.N * G - g.m * kTile);
-      if (t == 0) ds.bad_tree = 0, ds.no_number = 0, cs.bad = 0, cs.segment = g;
+      if (t == 0) ds.bad_tree = 0, ds.no_number = 0, cs.bad[turn] = 0, cs.segment = g;
       all_sync();
       load_tree(p, ds, g, t);
       if (t < kMaxNodes) {
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         // the set's last product, so that none of its phases is missed (with two tiles of S, S itself came behind it)
         if (B > 2 && gt >= 2) wait_warp(rs, &cs.pvdone[set], ((gt - 2) >> 1) & 1);
         tc_fence_after_sync();
-        if (cc.bad != 0) cs.bad = 1;
+        if (cc.bad != 0) cs.bad[turn] = 1;
         const int n = j == 0 ? kTile : min(kTile, len - (j - 1) * kTile);
         if (n < kTile && ok) ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1);
         if (n < kTile && ok) {  // values behind the context: anything, so none
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       sum = 0.f;
 #pragma unroll
       for (int i = 0; i < kParts; ++i) sum += cs.sum[i][row];
-      const bool bad = bad_tree || cs.bad != 0;
+      const bool bad = bad_tree || cs.bad[turn] != 0;
       const float inv = 1.f / sum;
       if (ok && alive) {
         const int64_t out = ((static_cast<int64_t>(g.lo) + node) * a.Hq + g.h * G + (row0 + row) % G) * d;
