@@ -75,9 +75,10 @@ __device__ __forceinline__ float reduce_row(float v, float* part, Op op) {
   return v;
 }
 
-// A group's scale from its largest value, and what to multiply by.
+// A group's scale from its largest value, and what to multiply by: at least
+// 2^-126, one over which is finite (zeros beside tiny values stay zeros).
 __device__ __forceinline__ float2 scale_of(float top) {
-  const float s = top > 0.f ? top / 448.f : 1.f;
+  const float s = top > 0.f ? fmaxf(top / 448.f, 1.17549435e-38f) : 1.f;
   return make_float2(s, 1.f / s);
 }
 

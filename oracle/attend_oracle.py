@@ -114,8 +114,8 @@ def add_norm(x, residual, weight, eps: float):
 
 
 def group_scales(y, group: int) -> np.ndarray:
-    """Each row's scales: the largest |y| of every group of columns (0: the row) over 448, 1 where that is 0."""
+    """Each row's scales: the largest |y| of every group of columns (0: the row) over 448, 2^-126 at least, 1 where that is 0."""
     n = y.shape[1]
     group = group or n
     top = np.stack([np.abs(y[:, i:i + group]).max(axis=1) for i in range(0, n, group)], axis=1)
-    return np.where(top > 0, top / E4M3_MAX, 1.0)
+    return np.where(top > 0, np.maximum(top / E4M3_MAX, 2.0 ** -126), 1.0)

@@ -142,3 +142,20 @@ def test_same_bits_in_a_graph_on_another_stream(cuda_lib):
     torch.cuda.synchronize()
     for a, b in ((out, o2), (y, y2), (y8, z2), (s, s2)):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("n", [64, 61])
+def test_zeros_beside_the_smallest_numbers(cuda_lib, n, group):
+    """One over a scale below 2^-128 would be infinite, and zeros times it no numbers."""
+    x = torch.zeros(5, n)
+    x[:, ::2] = torch.arange(1, (n + 1) // 2 + 1) * 2.0 ** -149 * torch.tensor([[1.0], [5.0], [100.0], [-3.0], [0.0]])
+    x = x.cuda()
+    m = -(-n // group) if group else 1
+    y8, s = torch.full((5, n), -7.0, device="cuda").to(E4M3), torch.full((5, m), -7.0, device="cuda")
+    binding.treewy_add_norm(binding.make_norm(x=x, y8=y8, y8_scale=s, group=group))
+    ref = orc.add_norm(f64(x), None, None, 1e-6)[1]
+    scale = np.repeat(f64(s), group or n, axis=1)[:, :n]
+    assert (f64(s)[:4] == 2.0 ** -126).all() and (f64(s)[4] == 1).all()
+    # y in f32 is off by a step of 2^-149 or 2^-21 of it, its code by half a step of e4m3
+    assert (np.abs(f64(y8) * scale - ref) <= 2.0 ** -148 + 2.0 ** -21 * np.abs(ref) + np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 * scale)).all()
