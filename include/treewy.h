@@ -557,7 +557,7 @@ typedef struct treewy_attn {
  *
  * bf16 rows with bf16 outputs and d a multiple of 16 run on the tensor cores in
  * 8-bit products, every f32 or bf16 operand as two 8-bit terms: a query, key or
- * value of the draft is within 2^-17 of its row's largest, a weight of the
+ * value of the draft is within 2^-17 of its row's largest (or 2^-117), a weight of the
  * softmax within 2^-8 of itself or 2^-16 of its row's largest.  Other calls
  * run in f32.  A NaN (or an infinity, which counts as one) in a key reaches
  * every node that sees it, in a value every such node's column.  Scores pass f32: where
@@ -601,7 +601,8 @@ typedef struct treewy_append_args {
 
 /*
  * treewy_append -- rows into their pages, rounded to e4m3 in units of the
- * page's scale (for each head; keys and values apart).
+ * page's scale (for each head; keys and values apart).  Values up to 2^68 give
+ * scales that treewy_attend takes.
  *
  * A page's scale is the least power of two, 2^-40 at least, that brings what is
  * written to it within 448, e4m3's largest value.  Where a page has tokens
@@ -655,8 +656,9 @@ typedef struct treewy_norm {
  * treewy_add_norm -- the residual's addition and the RMS norm in one pass:
  *   z = x + residual,  y = w z / sqrt(mean of z^2 + eps),
  * in f32; residual_out gets z, y and y8 the norm of z before its rounding.  A
- * group's scale is its largest |y| / 448 (1 where that is 0), and y8 is y /
- * scale rounded to e4m3; NaN stays NaN and does not count for the scale.
+ * group's scale is its largest |y| / 448, 2^-126 at least (1 where all are 0),
+ * and y8 is y / scale rounded to e4m3; NaN stays NaN and does not count for the
+ * scale.
  */
 treewy_status treewy_add_norm(const treewy_norm* norm, cudaStream_t stream);
 
