@@ -134,15 +134,66 @@ __device__ __forceinline__ float sum_lanes(float (&v)[N], int lane) {
   return v[0];
 }
 
-// An output of a node that sees values that are no numbers, among them perhaps this column's.
-static __device__ __noinline__ float with_none(const Params& p, const DraftSmem& ds, const Segment& g, int node, int col, unsigned long long none,
-                                               float y) {
-  for (unsigned long long q = none & ds.seen[node]; q != 0; q &= q - 1) {
-    const uint16_t v = static_cast<const uint16_t*>(p.a.v)[(static_cast<int64_t>(g.lo) + __ffsll(q) - 1) * p.a.v_stride +
-                                                          static_cast<int64_t>(g.h) * p.a.cache.d + col];
-    if ((v & 0x7f80) == 0x7f80) y = NAN;
+// A part of an item's queries, and of the draft's keys and values where it has
+// them, as terms: by one of the four warps (number w).  All of its rows, or the
+// first eight, are loaded at once, and converted two at a time: little code,
+// which a CTA meets for the first time here.
+// place(kind, i, ..) writes row i of the queries (kind 0), keys (1) or values (2).
+template <int NR, typename Place>
+__device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, float factor, int w, Place place) {
+  constexpr int kBatch = 8;
+  const treewy_attn& a = p.a;
+  const int lane = threadIdx.x & 31, d = a.cache.d, G = p.G;
+  const int total = rows + (g.t0 == 0 ? 2 * g.N : 0), each = (total + kSideWarps - 1) / kSideWarps, end = min(total, (w + 1) * each);
+  const bool wide = p.wide_q && p.wide_k && p.wide_v;
+  const int batch = wide ? kBatch : 1;
+#pragma unroll 1
+  for (int b0 = w * each; b0 < end; b0 += batch) {
+    const int many = min(batch, end - b0);
+    // lane i finds the i-th row
+    const int e = min(b0 + (lane & (kBatch - 1)), total - 1), n = e - rows, in = e < rows ? e / G : n >> 1;
+    const int64_t token = static_cast<int64_t>(g.lo) + in;
+    const uint16_t* row = e < rows ? static_cast<const uint16_t*>(a.q) + token * a.q_stride + (static_cast<int64_t>(g.h) * G + e - in * G) * d
+                                   : static_cast<const uint16_t*>(n & 1 ? a.v : a.k) + token * (n & 1 ? a.v_stride : a.k_stride) +
+                                         static_cast<int64_t>(g.h) * d;
+    const unsigned long long at = reinterpret_cast<unsigned long long>(row);
+    uint4 x[kBatch];
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(__shfl_sync(kFull, at, i));
+        if (i < many) x[i] = load_row8(from, 8 * lane, d);
+      }
+    } else {
+      x[0] = load_row8_odd(reinterpret_cast<const uint16_t*>(__shfl_sync(kFull, at, 0)), 8 * lane, d);
+    }
+#pragma unroll 1
+    for (int e0 = 0; e0 < many; e0 += 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (e0 + i >= many) continue;
+        const int r = b0 + e0 + i, kind = r < rows ? 0 : 1 + ((r - rows) & 1), to = kind == 0 ? r : (r - rows) >> 1;
+        uint2 hi, lo;
+        bool none;
+        // a value that is no number would reach the nodes that do not see it: weights of zero times it
+        const int unit = row_terms(x[i], kind == 2, hi, lo, none);
+        place(kind, to, hi, lo);
+        if (lane == 0) {
+          if (kind == 0) {
+            ds.rowf[to] = pow2(unit) * factor;
+          } else if (kind == 1) {
+            ds.ks[to] = pow2(unit);
+          } else {
+            if (none) atomicOr(&ds.no_number, 1ull << to);
+            ds.lv[to] = static_cast<float>(unit);
+            ds.il[to] = pow2(-unit);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i + 2 < kBatch; ++i) x[i] = x[i + 2];
+    }
   }
-  return y;
 }
 
 template <int NH, int NR>
@@ -162,48 +213,50 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, d = a.cache.d, G = p.G;
 
   // ---- set-up, while the kernel before may still run
-  if (t == 0) {
-    init_ring(rs);
-    for (int i = 0; i < kAhead; ++i) {
-      mbar_init(&cs.sfull[i], 1);
-      mbar_init(&cs.sread[i], kSoftWarps);
+  if (warp == 0) {
+    init_ring(rs, lane);
+    if (lane < 8) mbar_init(&cs.place[lane], 1);
+    if (lane < kAhead) {
+      mbar_init(&cs.sfull[lane], 1);
+      mbar_init(&cs.sread[lane], kSoftWarps);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&cs.place[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&cs.pready[i], kSoftWarps);
-      mbar_init(&cs.pvdone[i], 1);
-      mbar_init(&cs.ready[i], kSideWarps);
-      mbar_init(&cs.free[i], kSoftWarps);
-      mbar_init(&cs.done[i], kSoftWarps);
-      mbar_init(&cs.odone[i], 1);
-      mbar_init(&cs.ofree[i], kSideWarps);
-      mbar_init(&cs.drain[i], 1);
+    if (lane < 2) {
+      mbar_init(&cs.pready[lane], kSoftWarps);
+      mbar_init(&cs.pvdone[lane], 1);
+      mbar_init(&cs.ready[lane], kSideWarps);
+      mbar_init(&cs.free[lane], kSoftWarps);
+      mbar_init(&cs.done[lane], kSoftWarps);
+      mbar_init(&cs.odone[lane], 1);
+      mbar_init(&cs.ofree[lane], kSideWarps);
+      mbar_init(&cs.drain[lane], 1);
     }
     fence_mbarrier_init();
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
+    if (lane == 0) {
+      prefetch_tensormap(&kmap);
+      prefetch_tensormap(&vmap);
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&cs.tmem, kTmemCols);
     tmem_relinquish();
   }
   after_previous();
-  const Part mine = make_plan<kThreads>(p, cs.plan, rs);
+  const Part<false> mine = make_plan<kThreads, false>(p, cs.plan, rs);
   const uint32_t tmem = cs.tmem;
 
-  Walk walk = mine.walk;
+  Walk<false> walk = mine.walk;
   Segment g;
   int armed = 0;
   int gt = 0;   // tiles so far
   int seg = 0;  // items, or parts of them, so far: the k-th uses place k & 1 for the k / 2-th time
 
   if (warp == kLoadWarp) {
-    armed = load_pages<false, NH, S>(p, cs, rs, walk, ring, kmap, [](const Segment&) { return true; },
+    armed = load_pages<false, NH>(p, cs, rs, walk, ring, kmap, [](const Segment&) { return true; },
                                      [](const Segment&, int, int, uint32_t) { return true; });
   } else if (warp == kLoadWarp + 1) {
     // the draft's tile is filled by other warps, once both its stages are free
     static_assert(S < 8, "drafts whose stage is there and that are not filled yet");
-    armed = load_pages<true, NH, S>(
+    armed = load_pages<true, NH>(
         p, cs, rs, walk, ring, vmap,
         [&](const Segment& s) {
           if (s.t0 != 0) warp_arrive(&cs.place[seg & 7]);
@@ -426,7 +479,7 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
     const int quarter = warp & 3, u = t - 32 * kSideWarp;
     const float factor = a.scale * 1.4426950408889634f;  // scores in powers of two
     auto side_sync = [] { named_bar_sync<2, kSideThreads>(); };
-    Walk behind = walk;
+    Walk<false> behind = walk;
     int tiles = 0;  // up to the item that is made
     bool more = true;
 #pragma unroll 1
@@ -435,33 +488,48 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
       if (more) {
         ItemSmem& it = cs.item[seg & 1];
         DraftSmem& ds = it.draft;
-        const int rows = g.N * G;
+        const int rows = g.N * G, slot = tiles % S;
+        unsigned char *q = qs + (seg & 1) * Sh::kQBytes, *draft = ring + slot * Sh::kStage;
+        const int parent = u < g.N ? (a.parent != nullptr ? __ldg(a.parent + g.lo + u) : u - 1) : -1;
         if (seg >= 2) wait_warp(rs, &cs.free[seg & 1], ((seg >> 1) - 1) & 1);
         if (u == 0) ds.bad_tree = 0, ds.no_number = 0, it.bad = 0;
-        const int slot = tiles % S;
-        wait_warp(rs, &cs.place[seg & 7], (seg >> 3) & 1);
-        side_sync();
-        load_tree(p, ds, g, u);
-        unsigned char *q = qs + (seg & 1) * Sh::kQBytes, *draft = ring + slot * Sh::kStage;
         zero_rows<kSideThreads>(q, NH, Sh::kRowBytes, rows, NR, u);
         zero_rows<kSideThreads>(q, NH, Sh::kRowBytes, NR + rows, 2 * NR, u);
         if (u >= rows && u < NR) ds.rowf[u] = 0.f;
+        side_sync();
+        if (u < g.N) {
+          const bool wrong = parent < -1 || parent >= u;
+          if (wrong) ds.bad_tree = 1;
+          ds.parent[u] = wrong ? -1 : parent;
+        }
+        bool placed = false;
+        auto stage_is_there = [&] {
+          if (!placed) wait_warp(rs, &cs.place[seg & 7], (seg >> 3) & 1);
+          placed = true;
+        };
+        fill_rows<NR>(p, ds, g, rows, factor, warp - kSideWarp, [&](int kind, int i, uint2 hi, uint2 lo) {
+          if (kind != 0) stage_is_there();
+          unsigned char* tile = kind == 0 ? q : kind == 1 ? draft : draft + NH * kHalf;
+          const uint32_t block = kind == 0 ? Sh::kRowBytes : kHalf;
+          if (8 * lane < NH * 128) {
+            *operand8(tile, i, lane, block) = hi;
+            *operand8(tile, i + (kind == 0 ? NR : 64), lane, block) = lo;
+          }
+        });
+        stage_is_there();
         if (g.t0 == 0) {  // what the draft's tile has behind its values
           zero_rows<kSideThreads>(draft + NH * kHalf, NH, kHalf, g.N, 32, u);
           zero_rows<kSideThreads>(draft + NH * kHalf, NH, kHalf, 64 + g.N, 96, u);
           if (u >= g.N && u < 32) ds.ks[u] = 1.f, ds.lv[u] = ds.il[u] = 0.f;
         }
-        fill_rows<NH, kSideWarps, 4>(p, ds, g, rows, factor, warp - kSideWarp, [&](int kind, int i, int ln, uint2 hi, uint2 lo) {
-          unsigned char* tile = kind == 0 ? q : kind == 1 ? draft : draft + NH * kHalf;
-          const uint32_t block = kind == 0 ? Sh::kRowBytes : kHalf;
-          *operand8(tile, i, ln, block) = hi;
-          *operand8(tile, i + (kind == 0 ? NR : 64), ln, block) = lo;
-        });
         fence_proxy_async_smem();
         side_sync();
-        see(ds, g, u);
-        side_sync();
-        if (u < NR) it.seen[u] = static_cast<uint32_t>(ds.seen[min(u, rows - 1) / G]);
+        if (u < NR) {
+          uint32_t m = 0;
+#pragma unroll 1
+          for (int n = min(u, rows - 1) / G; n >= 0; n = ds.parent[n]) m |= 1u << n;
+          it.seen[u] = m;
+        }
         if (g.t0 == 0 && u == 0) {
           arrive(&rs.kfull[slot]);
           arrive(&rs.vfull[slot]);
@@ -490,23 +558,34 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
       }
       side_sync();
       if (ok && !bad) {
-        const unsigned long long none = g.t0 == 0 ? it.draft.no_number : 0;
-        constexpr int kStep = NR < 8 ? NR : 8;
 #pragma unroll 1
-        for (int x = 0; x < NH * (NR / kStep); ++x) {
-          const int half = x / (NR / kStep), r0 = x % (NR / kStep) * kStep, col = half * 128 + quarter * 32 + lane;
+        for (int x = 0; x < NH * (NR / 8); ++x) {
+          const int half = x / (NR / 8), r0 = x % (NR / 8) * 8, col = half * 128 + quarter * 32 + lane;
           if (r0 >= rows) continue;
-          uint32_t o[kStep];
-          ld_cols<kStep>(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kColO + ((k & 1) * NH + half) * Sh::kCols + r0, o);
-          ld_wait<kStep>(o);
+          uint32_t o[8];
+          ld_cols<8>(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + kColO + ((k & 1) * NH + half) * Sh::kCols + r0, o);
+          ld_wait<8>(o);
 #pragma unroll
-          for (int i = 0; i < kStep; ++i) {
-            const int row = r0 + i;
-            if (row >= rows || col >= d) continue;
-            float y = __uint_as_float(o[i]) * it.inv[row];
-            if (none != 0) y = with_none(p, it.draft, g, row / G, col, none, y);
-            if (whole) static_cast<__nv_bfloat16*>(a.o)[it.out[row] + col] = __float2bfloat16_rn(y);
-            else p.part_o[it.out[row] + col] = y;
+          for (int i = 0; i < 8; ++i) {
+            if (r0 + i >= rows || col >= d) continue;
+            const float y = __uint_as_float(o[i]) * it.inv[r0 + i];
+            if (whole) static_cast<__nv_bfloat16*>(a.o)[it.out[r0 + i] + col] = __float2bfloat16_rn(y);
+            else p.part_o[it.out[r0 + i] + col] = y;
+          }
+        }
+        if (g.t0 == 0 && it.draft.no_number != 0) {  // values of the rows' paths that are no numbers
+#pragma unroll 1
+          for (int x = 0; x < rows * NH; ++x) {
+            const int row = x / NH, col = x % NH * 128 + quarter * 32 + lane;
+            if (col >= d) continue;
+#pragma unroll 1
+            for (uint32_t n = it.seen[row] & static_cast<uint32_t>(it.draft.no_number); n != 0; n &= n - 1) {
+              const uint16_t v = static_cast<const uint16_t*>(a.v)[(static_cast<int64_t>(g.lo) + __ffs(n) - 1) * a.v_stride +
+                                                                   static_cast<int64_t>(g.h) * d + col];
+              if ((v & 0x7f80) != 0x7f80) continue;
+              if (whole) static_cast<__nv_bfloat16*>(a.o)[it.out[row] + col] = __float2bfloat16_rn(NAN);
+              else p.part_o[it.out[row] + col] = NAN;
+            }
           }
         }
         tc_fence_before_sync();

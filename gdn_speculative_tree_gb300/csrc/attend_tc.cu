@@ -124,38 +124,42 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, d = a.cache.d, G = p.G;
 
   // ---- set-up, while the kernel before may still run
-  if (t == 0) {
-    init_ring(rs);
-    for (int i = 0; i < 3; ++i) mbar_init(&cs.sfull[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&cs.mdone[i], kSetWarps);
-      mbar_init(&cs.pready[i], kSetWarps);
-      mbar_init(&cs.pvdone[i], 1);
+  if (warp == 0) {
+    init_ring(rs, lane);
+    if (lane < 3) mbar_init(&cs.sfull[lane], 1);
+    if (lane < 2) {
+      mbar_init(&cs.mdone[lane], kSetWarps);
+      mbar_init(&cs.pready[lane], kSetWarps);
+      mbar_init(&cs.pvdone[lane], 1);
     }
-    mbar_init(&cs.qfull, 1);
-    mbar_init(&cs.qfree, kSoftWarps);
-    mbar_init(&cs.drain, 1);
+    if (lane == 0) {
+      mbar_init(&cs.qfull, 1);
+      mbar_init(&cs.qfree, kSoftWarps);
+      mbar_init(&cs.drain, 1);
+    }
     fence_mbarrier_init();
-    prefetch_tensormap(&maps.k);
-    prefetch_tensormap(&maps.v);
-    prefetch_tensormap(&maps.q_terms);
+    if (lane == 0) {
+      prefetch_tensormap(&maps.k);
+      prefetch_tensormap(&maps.v);
+      prefetch_tensormap(&maps.q_terms);
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&cs.tmem, kTmemCols);
     tmem_relinquish();
   }
   after_previous();
-  const Part mine = make_plan<kThreads>(p, cs.plan, rs);
+  const Part<true> mine = make_plan<kThreads, true>(p, cs.plan, rs);
   const uint32_t tmem = cs.tmem;
 
-  Walk walk = mine.walk;
+  Walk<true> walk = mine.walk;
   Segment g;
   int armed = 0;
   int queries = 0;  // segments whose queries have been sent for
   int gt = 0;  // tiles so far
 
   if (warp == kLoadWarp) {
-    armed = load_pages<false, NH, S>(
+    armed = load_pages<false, NH>(
         p, cs, rs, walk, ring, maps.k,
         [&](const Segment& s) {
           if (queries > 0 && !wait_warp(rs, &cs.qfree, (queries - 1) & 1)) return false;
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           return true;
         });
   } else if (warp == kLoadWarp + 1) {
-    armed = load_pages<true, NH, S>(
+    armed = load_pages<true, NH>(
         p, cs, rs, walk, ring, maps.v, [](const Segment&) { return true; },
         [&](const Segment& s, int tile, int slot, uint32_t) {
           if (lane == 0) {

@@ -289,51 +289,48 @@ struct Segment {
 __device__ __forceinline__ int tiles_of(int len) { return 1 + len / kTile + (len % kTile != 0); }
 __device__ __forceinline__ int row_tiles(const Params& p, int N) { return (N * p.G + kTile - 1) / kTile; }
 
-// Walks a CTA's segments; every role walks them for itself.
+// Walks a CTA's segments; every role walks them for itself.  kTilesOfRows: a
+// context may have several row tiles.
+template <bool kTilesOfRows>
 struct Walk {
-  int u, end, r;
-  __device__ bool next(const Params& p, const PlanSmem& cs, Segment& s) {
+  int u, end, r, item, t;  // tile, the end of the part; request, item (head, row tile) and tile of the next segment
+  __device__ __forceinline__ bool next(const Params& p, const PlanSmem& cs, Segment& s) {
     if (u >= end) return false;
-    int k = 0;
     if (p.listed) {
-      while (cs.base[r + 1] <= u) ++r;
-      k = s.r = r;
-    } else {
-      s.r = static_cast<int>(blockIdx.x / (p.a.cache.Hkv * p.tiles_m));
+      while (cs.base[r + 1] <= u) ++r, item = 0;
     }
-    s.lo = cs.lo[k], s.N = cs.nodes[k], s.len = cs.len[k], s.tiles = tiles_of(s.len);
-    if (p.listed) {
-      const int in = u - cs.base[r], item = in / s.tiles, mt = row_tiles(p, s.N);
-      s.h = item / mt, s.m = item % mt, s.t0 = in % s.tiles, s.t1 = min(s.tiles, s.t0 + (end - u));
-    } else {
-      const int item = static_cast<int>(blockIdx.x % (p.a.cache.Hkv * p.tiles_m));
-      s.h = item / p.tiles_m, s.m = item % p.tiles_m, s.t0 = 0, s.t1 = s.tiles;
-    }
-    u += s.t1 - s.t0;
+    const int k = p.listed ? r : 0;
+    s.r = r, s.lo = cs.lo[k], s.N = cs.nodes[k], s.len = cs.len[k], s.tiles = tiles_of(s.len);
+    const int mt = !kTilesOfRows ? 1 : p.listed ? row_tiles(p, s.N) : p.tiles_m;
+    s.h = kTilesOfRows ? item / mt : item;
+    s.m = item - s.h * mt;
+    s.t0 = t, s.t1 = p.listed ? min(s.tiles, t + (end - u)) : s.tiles;
+    u += s.t1 - s.t0, ++item, t = 0;
     return true;
   }
 };
 
-
 // Where a CTA's part begins and ends.
+template <bool kTilesOfRows>
 struct Part {
-  Walk walk;
+  Walk<kTilesOfRows> walk;
   int each, more;  // tiles of a piece; how many pieces have one more
 };
 // The piece that a tile lies in.
-__device__ __forceinline__ int piece_of(const Part& p, int u) {
+template <bool M>
+__device__ __forceinline__ int piece_of(const Part<M>& p, int u) {
   const int big = p.more * (p.each + 1);
   return u < big ? u / (p.each + 1) : p.more + (u - big) / p.each;
 }
 
 // All threads call it (THREADS of them, after the barriers' set-up); ends with
 // a __syncthreads.
-template <int THREADS, int S>
-__device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSmem<S>& ring) {
+template <int THREADS, bool kTilesOfRows, int S>
+__device__ __forceinline__ Part<kTilesOfRows> make_plan(const Params& p, PlanSmem& cs, RingSmem<S>& ring) {
   const treewy_attn& a = p.a;
   const treewy_cache& c = a.cache;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  Part part = {{0, 0, 0}, 1, 0};
+  Part<kTilesOfRows> part = {{0, 0, 0, 0, 0}, 1, 0};
   if (p.listed) {
     int carry = 0;
     if (t == 0) cs.base[0] = 0;
@@ -378,6 +375,8 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
         else hi = mid;
       }
       part.walk.r = lo;
+      const int in = part.walk.u - cs.base[lo], tiles = tiles_of(cs.len[lo]);
+      part.walk.item = in / tiles, part.walk.t = in - part.walk.item * tiles;
     }
     // until it is written: no item begins here and ends elsewhere, and no part is any good
     if (t == 0) p.record[8 * blockIdx.x] = 0;
@@ -388,6 +387,7 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
     const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
     if (q.err != 0 && item == 0 && t == 0) atomicOr(a.status + r, q.err);
     if (t == 0) cs.lo[0] = q.lo, cs.nodes[0] = static_cast<uint8_t>(q.N), cs.len[0] = q.len;
+    part.walk.r = r, part.walk.item = item;
     if (item % p.tiles_m < row_tiles(p, q.N)) part.walk.end = 1;
   }
   if (t == 0) {  // a second, and a hundred times what a tile takes
@@ -407,8 +407,8 @@ __device__ __forceinline__ Part make_plan(const Params& p, PlanSmem& cs, RingSme
 // 32's, asked for ahead.  begin(g) comes before a segment's tiles, draft(g, gt,
 // slot, again) in the place of the draft's; false: a wait of theirs gave up.
 // Returns the tiles up to which copies have been started.
-template <bool kValues, int NH, int S, typename Cs, typename Begin, typename Draft>
-__device__ __forceinline__ int load_pages(const Params& p, Cs& cs, RingSmem<S>& rs, Walk walk, unsigned char* ring, const CUtensorMap& map,
+template <bool kValues, int NH, bool M, int S, typename Cs, typename Begin, typename Draft>
+__device__ __forceinline__ int load_pages(const Params& p, Cs& cs, RingSmem<S>& rs, Walk<M> walk, unsigned char* ring, const CUtensorMap& map,
                                           Begin begin, Draft draft) {
   const treewy_cache& c = p.a.cache;
   constexpr uint32_t kStage = 2 * NH * kHalf;
@@ -494,80 +494,6 @@ __device__ __forceinline__ void drain_copies(uint64_t (&full)[S], int armed) {
   for (int i = 0; i < S && i < armed; ++i) mbar_wait_for(&full[(armed - 1 - i) % S], ((armed - 1 - i) / S) & 1, 20000000ull);
 }
 
-// A segment's queries, and the draft's keys and values where it has them, as
-// terms, by WARPS warps (this one's number: `warp`).  ROWS of a warp's rows are loaded at once, and
-// converted two at a time: little code, which a CTA meets for the first time
-// here.
-// place(kind, i, ..) writes row i of the queries (kind 0), keys (1) or values (2).
-template <int NH, int WARPS, int ROWS, typename Place>
-__device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const Segment& g, int rows, float factor, int warp, Place place) {
-  const treewy_attn& a = p.a;
-  const int lane = threadIdx.x & 31, d = a.cache.d, G = p.G, row0 = g.m * kTile;
-  const int each = (rows + WARPS - 1) / WARPS, begin = warp * each;
-#pragma unroll 1
-  for (int pass = 0; pass < (g.t0 == 0 ? 2 : 1); ++pass) {
-    const bool nodes = pass == 1, wide = nodes ? p.wide_k && p.wide_v : p.wide_q;
-    const int count = nodes ? (g.N > warp ? 2 * ((g.N - warp + WARPS - 1) / WARPS) : 0) : min(rows, begin + each) - begin;
-    // rows alternate between two places (heads of a token, or keys and values), each a step on
-    int head = nodes ? 0 : (row0 + begin) % G;
-    const int64_t token = static_cast<int64_t>(g.lo) + (nodes ? warp : (row0 + begin) / G);
-    const uint16_t* from = static_cast<const uint16_t*>(nodes ? a.k : a.q) + token * (nodes ? a.k_stride : a.q_stride) +
-                           static_cast<int64_t>(nodes ? g.h : g.h * G) * d;
-    const uint16_t* values = static_cast<const uint16_t*>(a.v) + token * a.v_stride + static_cast<int64_t>(g.h) * d;
-    auto next = [&] {
-      const uint16_t* at = nodes ? (head == 0 ? from : values) : from + head * d;
-      if (++head == (nodes ? 2 : G)) {
-        head = 0;
-        from += nodes ? WARPS * a.k_stride : a.q_stride;
-        values += WARPS * a.v_stride;
-      }
-      return at;
-    };
-    const int batch = wide ? ROWS : 1;
-#pragma unroll 1
-    for (int b0 = 0; b0 < count; b0 += batch) {
-      uint4 x[ROWS];
-      const int many = min(batch, count - b0);
-      if (wide) {
-#pragma unroll
-        for (int e = 0; e < ROWS; ++e)
-          if (e < many) x[e] = load_row8(next(), 8 * lane, d);
-      } else {
-        x[0] = load_row8_odd(next(), 8 * lane, d);
-      }
-      constexpr int kStep = ROWS < 2 ? ROWS : 2;
-#pragma unroll 1
-      for (int e0 = 0; e0 < many; e0 += kStep) {
-#pragma unroll
-        for (int e = 0; e < kStep; ++e) {
-          if (e0 + e >= many) continue;
-          const int k = b0 + e0 + e;
-          const bool value = nodes && (k & 1);
-          const int i = nodes ? warp + k / 2 * WARPS : begin + k;
-          uint2 hi, lo;
-          bool none;
-          // a value that is no number would reach the nodes that do not see it: weights of zero times it
-          const int unit = row_terms(x[e], value, hi, lo, none);
-          if (8 * lane < NH * 128) place(nodes ? (value ? 2 : 1) : 0, i, lane, hi, lo);
-          if (lane == 0) {
-            if (!nodes) {
-              ds.rowf[i] = pow2(unit) * factor;
-            } else if (value) {
-              if (none) atomicOr(&ds.no_number, 1ull << i);
-              ds.lv[i] = static_cast<float>(unit);
-              ds.il[i] = pow2(-unit);
-            } else {
-              ds.ks[i] = pow2(unit);
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e + kStep < ROWS; ++e) x[e] = x[e + kStep];
-      }
-    }
-  }
-}
-
 // Zeros in the 128-byte rows [lo, hi) of `blocks` blocks, by THREADS threads (this one: t).
 template <int THREADS>
 __device__ __forceinline__ void zero_rows(unsigned char* tile, int blocks, uint32_t block, int lo, int hi, int t) {
@@ -594,7 +520,8 @@ __device__ __forceinline__ void see(DraftSmem& ds, const Segment& g, int t) {
 
 // What one thread says of a finished segment: the status, and where it is a
 // part of an item, what the joining kernel needs.
-__device__ __forceinline__ void report(const Params& p, const Part& part, const Walk& walk, const Segment& g, int rows, bool bad_tree, bool bad) {
+template <bool M>
+__device__ __forceinline__ void report(const Params& p, const Part<M>& part, const Walk<M>& walk, const Segment& g, int rows, bool bad_tree, bool bad) {
   if (bad) atomicOr(p.a.status + g.r, bad_tree ? TREEWY_STATUS_BAD_TREE : TREEWY_STATUS_BAD_PAGE);
   if (g.t0 != 0 || g.t1 == g.tiles) return;
   int4* rec = reinterpret_cast<int4*>(p.record + 8 * blockIdx.x);
@@ -602,15 +529,15 @@ __device__ __forceinline__ void report(const Params& p, const Part& part, const 
   rec[0] = make_int4(1, piece_of(part, walk.u + (g.tiles - g.t1) - 1), rows, 0);  // the piece of the item's last tile
 }
 
+// By the lanes of a warp.
 template <int S>
-__device__ __forceinline__ void init_ring(RingSmem<S>& rs) {
-  for (int i = 0; i < S; ++i) {
-    mbar_init(&rs.kfull[i], 1);
-    mbar_init(&rs.kfree[i], 1);
-    mbar_init(&rs.vfull[i], 1);
-    mbar_init(&rs.vfree[i], 1);
-    mbar_init(&rs.cfull[i], 1);
-  }
+__device__ __forceinline__ void init_ring(RingSmem<S>& rs, int lane) {
+  if (lane >= S) return;
+  mbar_init(&rs.kfull[lane], 1);
+  mbar_init(&rs.kfree[lane], 1);
+  mbar_init(&rs.vfull[lane], 1);
+  mbar_init(&rs.vfree[lane], 1);
+  mbar_init(&rs.cfull[lane], 1);
 }
 
 // Drafts of at most kFewRows rows (nodes times query heads of a key head) are
