@@ -136,7 +136,7 @@ __device__ __forceinline__ float sum_lanes(float (&v)[N], int lane) {
 
 // A part of an item's queries, and of the draft's keys and values where it has
 // them, as terms: by one of the four warps (number w).  All of its rows, or the
-// first eight, are loaded at once, and converted two at a time: little code,
+// first eight, are loaded at once, and converted one at a time: little code,
 // which a CTA meets for the first time here.
 // place(kind, i, ..) writes row i of the queries (kind 0), keys (1) or values (2).
 template <int NR, typename Place>
@@ -168,30 +168,26 @@ __device__ __forceinline__ void fill_rows(const Params& p, DraftSmem& ds, const 
       x[0] = load_row8_odd(reinterpret_cast<const uint16_t*>(__shfl_sync(kFull, at, 0)), 8 * lane, d);
     }
 #pragma unroll 1
-    for (int e0 = 0; e0 < many; e0 += 2) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (e0 + i >= many) continue;
-        const int r = b0 + e0 + i, kind = r < rows ? 0 : 1 + ((r - rows) & 1), to = kind == 0 ? r : (r - rows) >> 1;
-        uint2 hi, lo;
-        bool none;
-        // a value that is no number would reach the nodes that do not see it: weights of zero times it
-        const int unit = row_terms(x[i], kind == 2, hi, lo, none);
-        place(kind, to, hi, lo);
-        if (lane == 0) {
-          if (kind == 0) {
-            ds.rowf[to] = pow2(unit) * factor;
-          } else if (kind == 1) {
-            ds.ks[to] = pow2(unit);
-          } else {
-            if (none) atomicOr(&ds.no_number, 1ull << to);
-            ds.lv[to] = static_cast<float>(unit);
-            ds.il[to] = pow2(-unit);
-          }
+    for (int e0 = 0; e0 < many; ++e0) {
+      const int r = b0 + e0, kind = r < rows ? 0 : 1 + ((r - rows) & 1), to = kind == 0 ? r : (r - rows) >> 1;
+      uint2 hi, lo;
+      bool none;
+      // a value that is no number would reach the nodes that do not see it: weights of zero times it
+      const int unit = row_terms(x[0], kind == 2, hi, lo, none);
+      place(kind, to, hi, lo);
+      if (lane == 0) {
+        if (kind == 0) {
+          ds.rowf[to] = pow2(unit) * factor;
+        } else if (kind == 1) {
+          ds.ks[to] = pow2(unit);
+        } else {
+          if (none) atomicOr(&ds.no_number, 1ull << to);
+          ds.lv[to] = static_cast<float>(unit);
+          ds.il[to] = pow2(-unit);
         }
       }
 #pragma unroll
-      for (int i = 0; i + 2 < kBatch; ++i) x[i] = x[i + 2];
+      for (int i = 0; i + 1 < kBatch; ++i) x[i] = x[i + 1];
     }
   }
 }

@@ -497,6 +497,7 @@ __device__ __forceinline__ void drain_copies(uint64_t (&full)[S], int armed) {
 // Zeros in the 128-byte rows [lo, hi) of `blocks` blocks, by THREADS threads (this one: t).
 template <int THREADS>
 __device__ __forceinline__ void zero_rows(unsigned char* tile, int blocks, uint32_t block, int lo, int hi, int t) {
+#pragma unroll 1
   for (int x = 0; x < blocks; ++x)
 #pragma unroll 1
     for (int i = lo * 8 + t; i < hi * 8; i += THREADS) *reinterpret_cast<uint4*>(tile + x * block + i * 16) = make_uint4(0, 0, 0, 0);
