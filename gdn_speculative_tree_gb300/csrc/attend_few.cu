@@ -26,7 +26,7 @@
 //
 //   8 or 16 warps  softmax
 //   two            page table, scales and pages (TMA): keys, and values
-//   two            issue the products, S up to four tiles ahead of O
+//   two            issue the products, S two or up to four tiles ahead of O
 //   four           queries and draft to e4m3; outputs
 #include "attend_tc.cuh"
 
@@ -34,7 +34,6 @@ namespace treewy {
 namespace {
 
 constexpr int kSideWarps = 4, kSideThreads = 32 * kSideWarps;
-constexpr int kAhead = 4;  // tiles of S
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
 // NH: halves of 128 columns of a head; NR: rows, 8, 16 or 32.
@@ -50,6 +49,13 @@ struct Shape {
   static constexpr uint32_t kQBytes = NH * kRowBytes;                // of an item; two of them
   static constexpr uint32_t kStage = 2 * NH * kHalf;                 // K, then V
   static constexpr int kStages = NH == 2 ? (NR == 8 ? 3 : 2) : (NR == 32 ? 5 : 6);
+  // What the softmax waits for besides S costs it most where tiles are small (a wait, met by all of its warps, is some 200
+  // cycles of a tile's 2,200 for heads of up to 128).  There S comes behind the products that free the weights' place, and
+  // behind the tile's constants, so that it stands for both: drafts of 4 nodes 94 us against 106 with waits of their own.
+  // For heads of 256 the stages are few: S up to four tiles ahead frees K's sooner (one long context 56 us against 58),
+  // and with two stages the constants would hold S up (drafts of 4: 138 us against 148).
+  static constexpr bool kInOrder = NH == 1, kWithConsts = kStages > 2;
+  static constexpr int kAhead = kInOrder ? 2 : 4;                    // tiles of S
   static constexpr uint32_t kBytes = kWBytes + 2 * kQBytes + kStages * kStage + 1024;
 };
 
@@ -63,7 +69,7 @@ struct ItemSmem {
   int bad;                             // a page of it
 };
 
-template <int S>
+template <int S, int kAhead>
 struct FewSmem {
   RingSmem<S> ring;
   uint64_t sfull[kAhead], sread[kAhead], pready[2], pvdone[2], drain[2];
@@ -197,10 +203,10 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
     attend_few_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
   using Sh = Shape<NH, NR>;
-  constexpr int S = Sh::kStages, NT = Sh::kRowsOf, kThreads = Sh::kThreads, kSoftWarps = Sh::kSoftWarps, kSoftThreads = 32 * kSoftWarps;
+  constexpr int S = Sh::kStages, kAhead = Sh::kAhead, NT = Sh::kRowsOf, kThreads = Sh::kThreads, kSoftWarps = Sh::kSoftWarps, kSoftThreads = 32 * kSoftWarps;
   constexpr int kLoadWarp = Sh::kLoadWarp, kMmaWarp = Sh::kMmaWarp, kSideWarp = Sh::kSideWarp;
   extern __shared__ unsigned char raw_smem[];
-  __shared__ FewSmem<S> cs;
+  __shared__ FewSmem<S, kAhead> cs;
   RingSmem<S>& rs = cs.ring;
   unsigned char* wts = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   unsigned char* qs = wts + Sh::kWBytes;
@@ -244,6 +250,11 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
   Segment g;
   int armed = 0;
   int gt = 0;   // tiles so far
+  int slot = 0;      // their stage
+  uint32_t use = 0;  // and the parity of its use
+  auto next_stage = [&] {
+    if (++slot == S) slot = 0, use ^= 1;
+  };
   int seg = 0;  // items, or parts of them, so far: the k-th uses place k & 1 for the k / 2-th time
 
   if (warp == kLoadWarp) {
@@ -274,8 +285,11 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
       ok = wait_warp(rs, &cs.ready[seg & 1], (seg >> 1) & 1);
 #pragma unroll 1
       for (int j = g.t0; ok && j < g.t1; ++j, ++gt) {
-        const int slot = gt % S, b = gt % kAhead;
-        ok = (gt < kAhead || wait_warp(rs, &cs.sread[b], (gt / kAhead - 1) & 1)) && wait_warp(rs, &rs.kfull[slot], (gt / S) & 1);
+        const int b = gt % kAhead;
+        if constexpr (Sh::kInOrder) ok = gt < 2 || wait_warp(rs, &cs.pvdone[b], ((gt - 2) >> 1) & 1);
+        else ok = gt < kAhead || wait_warp(rs, &cs.sread[b], (gt / kAhead - 1) & 1);
+        if constexpr (Sh::kWithConsts) ok = ok && wait_warp(rs, &rs.cfull[slot], use);
+        ok = ok && wait_warp(rs, &rs.kfull[slot], use);
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
@@ -298,6 +312,7 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
           mma_commit(&rs.kfree[slot]);
         }
         __syncwarp();
+        next_stage();
       }
     }
   } else if (warp == kMmaWarp + 1) {
@@ -310,8 +325,7 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
       ok = seg < 2 || wait_warp(rs, &cs.ofree[seg & 1], ((seg >> 1) - 1) & 1);
 #pragma unroll 1
       for (int j = g.t0; ok && j < g.t1; ++j, ++gt) {
-        const int slot = gt % S;
-        ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1) && wait_warp(rs, &cs.pready[gt & 1], (gt >> 1) & 1);
+        ok = wait_warp(rs, &rs.vfull[slot], use) && wait_warp(rs, &cs.pready[gt & 1], (gt >> 1) & 1);
         if (!ok) break;
         tc_fence_after_sync();
         // 32 tokens each: the draft's are the first and the third
@@ -335,6 +349,7 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
           if (j + 1 == g.t1) mma_commit(&cs.odone[seg & 1]);
         }
         __syncwarp();
+        next_stage();
       }
     }
   } else if (warp < kSoftWarps) {
@@ -353,16 +368,17 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
       for (int i = 0; i < NT; ++i) m[i] = -INFINITY, sum[i] = 0.f;
       const int t0 = g.t0, t1 = g.t1, N = g.N, len = g.len;
 #pragma unroll 1
-      for (int j = t0; j < t1; ++j, ++gt) {
-        const int slot = gt % S, b = gt & 1;
+      for (int j = t0; j < t1; ++j, ++gt, next_stage()) {
+        const int b = gt & 1;
         const Consts& cc = rs.c[slot];
         // after a wait that gave up a warp still comes by every barrier of threads
-        bool ok = wait_warp(rs, &cs.sfull[gt % kAhead], (gt / kAhead) & 1) && wait_warp(rs, &rs.cfull[slot], (gt / S) & 1);
+        bool ok = wait_warp(rs, &cs.sfull[gt % kAhead], (gt / kAhead) & 1);
+        if constexpr (!Sh::kWithConsts) ok = wait_warp(rs, &rs.cfull[slot], use) && ok;
         tc_fence_after_sync();
         if (cc.bad != 0) it.bad = 1;
         const bool draft_tile = j == 0;
         const int n = draft_tile ? N : min(kTile, len - (j - 1) * kTile);
-        if (!draft_tile && n < kTile && ok) ok = wait_warp(rs, &rs.vfull[slot], (gt / S) & 1);
+        if (!draft_tile && n < kTile && ok) ok = wait_warp(rs, &rs.vfull[slot], use);
         if (!draft_tile && n < kTile && ok) {  // values behind the context: anything, so none
           unsigned char* v = ring + slot * Sh::kStage + NH * kHalf;
 #pragma unroll 1
@@ -378,7 +394,7 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
           ld_wait<2 * NT>(r);
           tc_fence_before_sync();
         }
-        warp_arrive(&cs.sread[gt % kAhead]);
+        if constexpr (!Sh::kInOrder) warp_arrive(&cs.sread[gt % kAhead]);
         const float ks = draft_tile ? ds.ks[lane] : cc.ks[token >> 4], lv = draft_tile ? ds.lv[lane] : cc.lv[token >> 4];
         const float il = draft_tile ? (token < n ? ds.il[lane] : 0.f) : cc.il[token >> 4];
         float s[NT], top[NT];
@@ -408,7 +424,9 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) grown |= top[i + e] > m[i + e] + kGrowth;
         }
-        if (gt >= 2) wait_warp(rs, &cs.pvdone[b], ((gt - 2) >> 1) & 1);  // the weights' place is read no more
+        // the weights' place is read no more
+        if constexpr (!Sh::kInOrder)
+          if (gt >= 2) wait_warp(rs, &cs.pvdone[b], ((gt - 2) >> 1) & 1);
         if (j == t0) {
 #pragma unroll
           for (int i = 0; i < NT; ++i) m[i] = top[i];
@@ -484,8 +502,8 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
       if (more) {
         ItemSmem& it = cs.item[seg & 1];
         DraftSmem& ds = it.draft;
-        const int rows = g.N * G, slot = tiles % S;
-        unsigned char *q = qs + (seg & 1) * Sh::kQBytes, *draft = ring + slot * Sh::kStage;
+        const int rows = g.N * G, at = tiles % S;
+        unsigned char *q = qs + (seg & 1) * Sh::kQBytes, *draft = ring + at * Sh::kStage;
         const int parent = u < g.N ? (a.parent != nullptr ? __ldg(a.parent + g.lo + u) : u - 1) : -1;
         if (seg >= 2) wait_warp(rs, &cs.free[seg & 1], ((seg >> 1) - 1) & 1);
         if (u == 0) ds.bad_tree = 0, ds.no_number = 0, it.bad = 0;
@@ -527,8 +545,8 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
           it.seen[u] = m;
         }
         if (g.t0 == 0 && u == 0) {
-          arrive(&rs.kfull[slot]);
-          arrive(&rs.vfull[slot]);
+          arrive(&rs.kfull[at]);
+          arrive(&rs.vfull[at]);
         }
         warp_arrive(&cs.ready[seg & 1]);
         tiles += g.t1 - g.t0;
