@@ -5,8 +5,8 @@
 // One pass over the tokens with the running maximum and sum of the softmax: a
 // cluster of eight CTAs holds 16 (node, query head) rows that share a key head;
 // its CTAs take tiles of 32 tokens in turn, the context's and then the
-// draft's, through one tile in shared memory (keys, then values), and read
-// each other's maxima, sums and outputs at the end.
+// draft's, through shared memory (keys and values, asked for together), and
+// read each other's maxima, sums and outputs at the end.
 //
 // Bound by the loads from shared memory of the two products: 128 bits for
 // four products each.
@@ -31,8 +31,25 @@ struct Shared {
   int bad;
 };
 
+// Sixteen codes times a scale.
+__device__ __forceinline__ void sixteen(float* to, const uint4& w, float f) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t h0 = e4m3x2_to_f16x2(u[e] & 0xffffu), h1 = e4m3x2_to_f16x2(u[e] >> 16);
+    const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)), y1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+    *reinterpret_cast<float4*>(to + 4 * e) = make_float4(y0.x * f, y0.y * f, y1.x * f, y1.y * f);
+  }
+}
+// Four values of a row that start on four elements.
+__device__ __forceinline__ float4 load4(const void* p, int64_t at, bool bf16) {
+  if (!bf16) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at));
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+
 __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
-    attend_scan_kernel(const __grid_constant__ treewy_attn a, int blocks) {
+    attend_scan_kernel(const __grid_constant__ treewy_attn a, int blocks, int fours) {
   after_previous();
   extern __shared__ float4 raw_smem[];
   __shared__ Shared sh;
@@ -62,14 +79,24 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
   }
   if (t == 0) sh.bad = 0;
   float* qs = reinterpret_cast<float*>(raw_smem);  // [kRows][pad], the outputs at the end
-  float* tile = qs + kRows * pad;                  // [kTile][pitch]
-  float* weight = tile + kTile * pitch;            // [kRows][kTile]
+  float* tile = qs + kRows * pad;                  // [2][kTile][pitch]: keys, values
+  float* weight = tile + 2 * kTile * pitch;        // [kRows][kTile]
   const bool bf16 = a.qkv_dtype == TREEWY_DTYPE_BF16;
-  for (int x = t; x < kRows * pad; x += kThreads) {
-    const int i = x / pad, col = x % pad, rr = row0 + i;
-    qs[x] = i < live && col < d ? load_qkv(a.q, (static_cast<int64_t>(q.lo) + rr / G) * a.q_stride +
-                                                    (static_cast<int64_t>(h) * G + rr % G) * d + col, bf16)
-                                : 0.f;
+  if (fours) {
+#pragma unroll 4
+    for (int x = t; x < kRows * (pad / 4); x += kThreads) {
+      const int i = x / (pad / 4), col = x % (pad / 4) * 4, rr = row0 + i;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < live) y = load4(a.q, (static_cast<int64_t>(q.lo) + rr / G) * a.q_stride + (static_cast<int64_t>(h) * G + rr % G) * d + col, bf16);
+      *reinterpret_cast<float4*>(qs + i * pad + col) = y;
+    }
+  } else {
+    for (int x = t; x < kRows * pad; x += kThreads) {
+      const int i = x / pad, col = x % pad, rr = row0 + i;
+      qs[x] = i < live && col < d ? load_qkv(a.q, (static_cast<int64_t>(q.lo) + rr / G) * a.q_stride +
+                                                      (static_cast<int64_t>(h) * G + rr % G) * d + col, bf16)
+                                  : 0.f;
+    }
   }
   const int row = t / 8, sub = t % 8;  // eight threads per row
   const int node = min(row0 + row, q.N * G - 1) / G;
@@ -93,38 +120,44 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
       __syncthreads();
       if (sh.bad != 0) break;  // nothing of the request is written
     }
-    auto load = [&](bool values) {
-      if (context && d % 16 == 0) {
-        for (int x = t; x < n * (d / 16); x += kThreads) {
-          const int i = x / (d / 16), col = x % (d / 16) * 16, at = t0 + i;
-          const int64_t b = static_cast<int64_t>(sh.page_of[at / P - t0 / P]) * c.Hkv + h;
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(values ? c.v : c.k) + (b * P + at % P) * d + col));
-          const float f = __ldg((values ? c.v_scale : c.k_scale) + b);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t h0 = e4m3x2_to_f16x2(u[e] & 0xffffu), h1 = e4m3x2_to_f16x2(u[e] >> 16);
-            const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)), y1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-            *reinterpret_cast<float4*>(tile + i * pitch + col + 4 * e) = make_float4(y0.x * f, y0.y * f, y1.x * f, y1.y * f);
-          }
-        }
-        return;
+    float* value = tile + kTile * pitch;
+    if (context && d % 16 == 0) {
+#pragma unroll 2
+      for (int x = t; x < n * (d / 16); x += kThreads) {
+        const int i = x / (d / 16), col = x % (d / 16) * 16, at = t0 + i;
+        const int64_t b = static_cast<int64_t>(sh.page_of[at / P - t0 / P]) * c.Hkv + h, from = (b * P + at % P) * d + col;
+        const uint4 wk = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.k) + from));
+        const uint4 wv = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.v) + from));
+        const float fk = __ldg(c.k_scale + b), fv = __ldg(c.v_scale + b);
+        sixteen(tile + i * pitch + col, wk, fk);
+        sixteen(value + i * pitch + col, wv, fv);
       }
+    } else if (!context && fours) {
+#pragma unroll 4
+      for (int x = t; x < n * (d / 4); x += kThreads) {
+        const int i = x / (d / 4), col = x % (d / 4) * 4;
+        const int64_t token = static_cast<int64_t>(q.lo) + t0 + i, head = static_cast<int64_t>(h) * d + col;
+        const float4 k = load4(a.k, token * a.k_stride + head, bf16), v = load4(a.v, token * a.v_stride + head, bf16);
+        *reinterpret_cast<float4*>(tile + i * pitch + col) = k;
+        *reinterpret_cast<float4*>(value + i * pitch + col) = v;
+      }
+    } else {
       for (int x = t; x < n * pad; x += kThreads) {
         const int i = x / pad, col = x % pad, at = t0 + i;
-        float f = 0.f;
+        float k = 0.f, v = 0.f;
         if (col < d && context) {
-          const int64_t b = static_cast<int64_t>(sh.page_of[at / P - t0 / P]) * c.Hkv + h;
-          f = e4m3_to_float(__ldg(static_cast<const uint8_t*>(values ? c.v : c.k) + (b * P + at % P) * d + col)) *
-              __ldg((values ? c.v_scale : c.k_scale) + b);
+          const int64_t b = static_cast<int64_t>(sh.page_of[at / P - t0 / P]) * c.Hkv + h, from = (b * P + at % P) * d + col;
+          k = e4m3_to_float(__ldg(static_cast<const uint8_t*>(c.k) + from)) * __ldg(c.k_scale + b);
+          v = e4m3_to_float(__ldg(static_cast<const uint8_t*>(c.v) + from)) * __ldg(c.v_scale + b);
         } else if (col < d) {
-          f = load_qkv(values ? a.v : a.k, (static_cast<int64_t>(q.lo) + at) * (values ? a.v_stride : a.k_stride) +
-                                               static_cast<int64_t>(h) * d + col, bf16);
+          const int64_t token = static_cast<int64_t>(q.lo) + at, head = static_cast<int64_t>(h) * d + col;
+          k = load_qkv(a.k, token * a.k_stride + head, bf16);
+          v = load_qkv(a.v, token * a.v_stride + head, bf16);
         }
-        tile[i * pitch + col] = f;
+        tile[i * pitch + col] = k;
+        value[i * pitch + col] = v;
       }
-    };
-    load(false);
+    }
     __syncthreads();
     float s[4] = {0.f, 0.f, 0.f, 0.f}, high = -INFINITY;  // tokens sub, sub + 8, ..
     for (int x = 0; x < pad; x += 4) {
@@ -158,9 +191,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
     sum = sum * keep + part;
 #pragma unroll
     for (int e = 0; e < kMaxPad / 32; ++e) acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
-    __syncthreads();
-    load(true);
-    __syncthreads();
+    __syncwarp();  // a row's weights are its own warp's
     for (int i = 0; i < n; ++i) {
       const float w = weight[row * kTile + i];
       // what a node does not see adds nothing to it, whatever it is
@@ -169,7 +200,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
       for (int e = 0; e < kMaxPad / 32; ++e) {
         const int col = 4 * sub + 32 * e;
         if (col < pad) {
-          const float4 v = *reinterpret_cast<const float4*>(tile + i * pitch + col);
+          const float4 v = *reinterpret_cast<const float4*>(value + i * pitch + col);
           acc[e] = make_float4(fmaf(w, v.x, acc[e].x), fmaf(w, v.y, acc[e].y), fmaf(w, v.z, acc[e].z), fmaf(w, v.w, acc[e].w));
         }
       }
@@ -224,14 +255,18 @@ cudaError_t launch_attend_scan(const treewy_attn& a, cudaStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv) + kRows - 1) / kRows;
   const int64_t ctas = blocks * a.cache.Hkv * kRanks;
   if (ctas > 0x7fffffff / a.R) return cudaErrorNotSupported;
-  auto bytes = [](int pad) { return sizeof(float) * (kRows * pad + kTile * (pad + 4) + kRows * kTile); };
+  auto bytes = [](int pad) { return sizeof(float) * (kRows * pad + 2 * kTile * (pad + 4) + kRows * kTile); };
   static std::atomic<uint64_t> done{0};
   cudaError_t e = once_per_device(done, [&] {
     return cudaFuncSetAttribute(attend_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes(kMaxPad)));
   });
   if (e != cudaSuccess) return e;
+  // rows that can be read in fours
+  const uintptr_t e4 = a.qkv_dtype == TREEWY_DTYPE_BF16 ? 8 : 16;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+  const int fours = all % e4 == 0 && a.cache.d % 4 == 0 && a.q_stride % 4 == 0 && a.k_stride % 4 == 0 && a.v_stride % 4 == 0 ? 1 : 0;
   return launch_after_smem(attend_scan_kernel, dim3(static_cast<unsigned>(ctas * a.R)), kThreads, bytes((a.cache.d + 3) & ~3), stream, a,
-                           static_cast<int>(blocks));
+                           static_cast<int>(blocks), fours);
 }
 
 }  // namespace treewy
