@@ -105,18 +105,23 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
 #pragma unroll
   for (int e = 0; e < kMaxPad / 32; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int context_tiles = q.len / kTile + (q.len % kTile != 0), tiles = context_tiles + (q.N + kTile - 1) / kTile;
+  // thread t's page of a tile of the context, asked for a tile ahead (a page has 16 tokens at least: two to a tile at most)
+  auto page_of = [&](int j) {
+    const int64_t token = static_cast<int64_t>(j) * kTile + t * P;
+    return t < 2 && j < context_tiles && t * P < kTile && token < q.len ? __ldg(c.page_table + static_cast<int64_t>(r) * c.max_pages + token / P) : 0;
+  };
+  int page = page_of(rank);
   for (int j = rank; j < tiles; j += kRanks) {
     const bool context = j < context_tiles;
     const int t0 = (context ? j : j - context_tiles) * kTile, n = min(kTile, (context ? q.len : q.N) - t0);
     __syncthreads();  // the tile and the weights are free
     if (context) {
-      const int p0 = t0 / P, count = (t0 + n - 1) / P - p0 + 1;
-      if (t < count) {
-        const int page = __ldg(c.page_table + static_cast<int64_t>(r) * c.max_pages + p0 + t);
+      if (t < 2) {
         const bool in = page >= 0 && page < c.num_pages;
-        if (!in) sh.bad = 1;
+        if (!in && t * P < n) sh.bad = 1;
         sh.page_of[t] = in ? page : 0;
       }
+      page = page_of(j + kRanks);
       __syncthreads();
       if (sh.bad != 0) break;  // nothing of the request is written
     }
@@ -160,6 +165,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
     }
     __syncthreads();
     float s[4] = {0.f, 0.f, 0.f, 0.f}, high = -INFINITY;  // tokens sub, sub + 8, ..
+#pragma unroll 2
     for (int x = 0; x < pad; x += 4) {
       const float4 u = *reinterpret_cast<const float4*>(qs + row * pad + x);
 #pragma unroll
@@ -192,10 +198,8 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
 #pragma unroll
     for (int e = 0; e < kMaxPad / 32; ++e) acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
     __syncwarp();  // a row's weights are its own warp's
-    for (int i = 0; i < n; ++i) {
+    auto add = [&](int i) {
       const float w = weight[row * kTile + i];
-      // what a node does not see adds nothing to it, whatever it is
-      if (!context && !((sh.seen[node] >> (t0 + i)) & 1)) continue;
 #pragma unroll
       for (int e = 0; e < kMaxPad / 32; ++e) {
         const int col = 4 * sub + 32 * e;
@@ -204,6 +208,13 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
           acc[e] = make_float4(fmaf(w, v.x, acc[e].x), fmaf(w, v.y, acc[e].y), fmaf(w, v.z, acc[e].z), fmaf(w, v.w, acc[e].w));
         }
       }
+    };
+    if (context) {
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) add(i);
+    } else {  // what a node does not see adds nothing to it, whatever it is
+      for (int i = 0; i < n; ++i)
+        if ((sh.seen[node] >> (t0 + i)) & 1) add(i);
     }
   }
   // the ranks' parts; one that had no tile, or whose tiles no row saw, has the maximum -infinity and zeros
