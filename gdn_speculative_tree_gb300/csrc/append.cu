@@ -8,6 +8,11 @@
 // shorter significand, and a scale that grows while a page fills only lowers
 // the exponents of the codes that are there: nothing is rounded twice but what
 // leaves e4m3's normal range.
+//
+// Bound by HBM where there is much to do: 187 MB of prompts in 41.5 us
+// (4.5 TB/s), and short of it by the two steps of every CTA, the loads and,
+// behind a barrier, the writing; by the launch (4.3 us for 64 single tokens)
+// where there is little.
 #include "cache_device.cuh"
 #include "treewy_internal.h"
 
@@ -104,10 +109,11 @@ __device__ __forceinline__ uint32_t again(uint32_t w, float f) {
 // largest to the writing, what is behind them is read twice; 0: one value at a
 // time, read twice (odd sizes).
 template <typename T, int HOLD>
-__global__ void __launch_bounds__(256) append_kernel(const treewy_append_args a, int pages) {
+// Two CTAs of 512 (64 registers a thread for bf16): 41.5 us for the prompts of pages of 64 tokens, 47.6 with 128 registers.
+__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1) append_kernel(const treewy_append_args a, int pages) {
   after_previous();
   __shared__ int parent[kMaxNodes], path[kMaxNodes], count;
-  __shared__ uint32_t part[8];
+  __shared__ uint32_t part[16];
   const treewy_cache& c = a.cache;
   const int t = threadIdx.x, P = c.page_len, d = c.d, threads = blockDim.x;
   // heads are neighbours as they are in a row, then keys and values, pages, requests
@@ -256,6 +262,8 @@ __global__ void __launch_bounds__(256) append_kernel(const treewy_append_args a,
   }
 }
 
+constexpr int kHold = 8;
+
 template <typename T>
 cudaError_t launch(const treewy_append_args& a, cudaStream_t stream) {
   const int P = a.cache.page_len;
@@ -270,10 +278,13 @@ cudaError_t launch(const treewy_append_args& a, cudaStream_t stream) {
   if (all % 16 != 0 || a.cache.d % 8 != 0) return launch_after(append_kernel<T, 0>, grid, 256, stream, a, np);
   // paths are short whatever the trees' bound is
   const int rows = std::min(a.max_new, P), pieces = (a.accepted != nullptr ? std::min(rows, 8) : rows) * (a.cache.d / 8);
-  // CTAs of two warps where a page gets little; of eight, with most of a page in registers, where it gets much
+  // a single token's page: 640 requests 4.8 us, 6.7 with eight pieces a thread
   if (pieces <= 64) return launch_after(append_kernel<T, 1>, grid, 64, stream, a, np);
-  if (pieces <= 512) return launch_after(append_kernel<T, 4>, grid, 128, stream, a, np);
-  return launch_after(append_kernel<T, 8>, grid, 256, stream, a, np);
+  // As few threads as hold the page: 16 prompts of 3500 to 4096 tokens with pages of 32 tokens, heads of 256, take 39 us with
+  // 128 threads of eight pieces, 47 with 256 of four, 81 with 512 of two; pages of 128, whose second half 256 threads would
+  // read twice, 45 us against 54; the paths of 256 trees 6.4 us with 64 threads, 7.7 with 128, 12.3 with 256.
+  const unsigned threads = pieces <= 512 ? 64 : pieces <= 1024 ? 128 : pieces <= 2048 ? 256 : 512;
+  return launch_after(append_kernel<T, kHold>, grid, threads, stream, a, np);
 }
 
 }  // namespace
