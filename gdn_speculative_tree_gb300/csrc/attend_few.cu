@@ -1,6 +1,6 @@
 // attend_few.cu -- attention over pages of e4m3 keys and values and the
 // draft's own ones on the 5th-generation tensor cores, as attend_tc.cu, for
-// drafts of at most 32 rows (nodes times query heads of a key head): single
+// drafts of at most 16 rows (nodes times query heads of a key head): single
 // tokens and chains.
 //
 // Such a call reads its context at the rate of HBM or should.  Rows of 128
@@ -8,16 +8,16 @@
 // and the columns are rows (of the queries, hi and lo terms side by side):
 //
 //   S^T = K Q^T     M = 128 tokens, N = 2 NR, from the page as it is
-//   w               a thread has one token of 4 or 8 rows; their terms go to
+//   w               a thread has one token of four rows; their terms go to
 //                   shared memory, a byte each
 //   O^T += V^T w^T  M = 128 columns of the head (V's rows run along the sum)
 //
 // A product of N = 16 takes an eighth of the time of one of 128, and the
 // softmax of a tile is spread over 256 or 512 threads.
 //
-// The draft's keys and values are the terms' rows 0 .. 31 (hi) and 64 .. 95
+// The draft's keys and values are the terms' rows 0 .. 15 (hi) and 64 .. 79
 // (lo) of a tile: the keys' products are added up in S^T, and the weights of
-// the first quarter of the lanes stand for both tokens of a value.
+// the first lanes stand for both tokens of a value.
 //
 // A context's tiles are few where there are many heads, so that what comes
 // before and after them counts: four warps of their own make the next item's
@@ -36,19 +36,19 @@ namespace {
 constexpr int kSideWarps = 4, kSideThreads = 32 * kSideWarps;
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 
-// NH: halves of 128 columns of a head; NR: rows, 8, 16 or 32.
+// NH: halves of 128 columns of a head; NR: rows, 8 or 16.
 template <int NH, int NR>
 struct Shape {
-  static constexpr int kGroups = NR == 8 ? 2 : 4, kRowsOf = NR / kGroups;   // of warps that share a tile's tokens; rows of a thread
+  static constexpr int kRowsOf = 4, kGroups = NR / kRowsOf;          // rows of a thread; of warps that share a tile's tokens
   static constexpr int kSoftWarps = 4 * kGroups, kLoadWarp = kSoftWarps, kMmaWarp = kLoadWarp + 2, kSideWarp = kMmaWarp + 2;
   static constexpr int kThreads = 32 * (kSideWarp + kSideWarps);
   static constexpr uint32_t kRowBytes = 2 * NR * 128;                // hi and lo rows of 128 bytes
-  static constexpr int kCols = NR < 16 ? 16 : NR;                    // of a product of the weights, 16 at least
+  static constexpr int kCols = 16;                                   // of a product of the weights, 16 at least
   static constexpr uint32_t kWBlock = kCols * 128;                   // a term of a tile's weights
   static constexpr uint32_t kWBytes = 4 * kWBlock;                   // of two tiles
   static constexpr uint32_t kQBytes = NH * kRowBytes;                // of an item; two of them
   static constexpr uint32_t kStage = 2 * NH * kHalf;                 // K, then V
-  static constexpr int kStages = NH == 2 ? (NR == 8 ? 3 : 2) : (NR == 32 ? 5 : 6);
+  static constexpr int kStages = NH == 2 ? (NR == 8 ? 3 : 2) : 6;
   // What the softmax waits for besides S costs it most where tiles are small (a wait, met by all of its warps, is some 200
   // cycles of a tile's 2,200 for heads of up to 128).  There S comes behind the products that free the weights' place, and
   // behind the tile's constants, so that it stands for both: drafts of 4 nodes 94 us against 106 with waits of their own.
@@ -83,18 +83,17 @@ struct FewSmem {
   PlanSmem plan;
 };
 
-// N TMEM columns of this thread's lane; complete after ld_wait.
+// 4 or 8 TMEM columns of this thread's lane; complete after ld_wait.
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t at, uint32_t* r) {
+  static_assert(N == 4 || N == 8, "columns");
   if constexpr (N == 4) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(at)
                  : "memory");
-  } else if constexpr (N == 8) {
-    tmem_ld8_async(at, *reinterpret_cast<uint32_t(*)[8]>(r));
   } else {
-    tmem_ld16_async(at, *reinterpret_cast<uint32_t(*)[16]>(r));
+    tmem_ld8_async(at, *reinterpret_cast<uint32_t(*)[8]>(r));
   }
 }
 template <int N>
@@ -102,17 +101,6 @@ __device__ __forceinline__ void ld_wait(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-template <int N>
-__device__ __forceinline__ void st_cols(uint32_t at, const uint32_t* r) {
-  if constexpr (N == 4) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
-  } else if constexpr (N == 8) {
-    tmem_st8(at, r);
-  } else {
-    tmem_st16(at, r);
-  }
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -448,7 +436,7 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
             ld_wait<NT>(o);
 #pragma unroll
             for (int i = 0; i < NT; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * top[i]);
-            st_cols<NT>(o0 + x * Sh::kCols, o);
+            tmem_st4(o0 + x * Sh::kCols, o);
           }
           tmem_wait_st();
         }
@@ -645,7 +633,8 @@ cudaError_t launch(const Params& p, const CUtensorMap& k, const CUtensorMap& v, 
 template <int NH>
 cudaError_t by_rows(const Params& p, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, cudaStream_t stream) {
   const int rows = p.a.max_nodes * p.G;
-  return rows <= 8 ? launch<NH, 8>(p, k, v, grid, stream) : rows <= 16 ? launch<NH, 16>(p, k, v, grid, stream) : launch<NH, 32>(p, k, v, grid, stream);
+  // 64 single tokens of eight heads a key head: 64 us with 8 rows, 67 with 16
+  return rows <= 8 ? launch<NH, 8>(p, k, v, grid, stream) : launch<NH, 16>(p, k, v, grid, stream);
 }
 
 }  // namespace

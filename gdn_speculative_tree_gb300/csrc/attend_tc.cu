@@ -1,7 +1,7 @@
 // attend_tc.cu -- attention over pages of e4m3 keys and values and the draft's
 // own ones on the 5th-generation tensor cores (tcgen05, TMEM, TMA), for bf16
 // rows and outputs, head sizes that are multiples of 16, and drafts of more
-// than 32 rows; and what joins the pieces of an item.
+// than 16 rows; and what joins the pieces of an item.
 //
 // attend_split_kernel makes the terms of all queries and of the drafts' keys and
 // values, once for every tile that reads them; attend_tc_kernel then loads them
@@ -109,6 +109,22 @@ struct Maps {
   CUtensorMap k, v;              // pages
   CUtensorMap q_terms, k_terms, v_terms;
 };
+
+// Parents of the segment's nodes; who sees whom.
+__device__ __forceinline__ void load_tree(const Params& p, DraftSmem& ds, const Segment& g, int t) {
+  if (t >= g.N) return;
+  const int q = p.a.parent != nullptr ? __ldg(p.a.parent + g.lo + t) : t - 1;
+  const bool wrong = q < -1 || q >= t;
+  if (wrong) ds.bad_tree = 1;
+  ds.parent[t] = wrong ? -1 : q;
+}
+__device__ __forceinline__ void see(DraftSmem& ds, const Segment& g, int t) {
+  if (t >= g.N) return;
+  unsigned long long m = 0;
+#pragma unroll 1
+  for (int q = t; q >= 0; q = ds.parent[q]) m |= 1ull << q;
+  ds.seen[t] = m;
+}
 
 template <int NH>
 __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
@@ -634,12 +650,18 @@ __global__ void __launch_bounds__(32 * kJoinRows) attend_join_kernel(const __gri
 int row_tiles_of(const treewy_attn& a) {
   return static_cast<int>((static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv) + kTile - 1) / kTile);
 }
-// Whether the tiles are put in a row: where there is one row tile to a
-// context, or too few items to fill the SMs several times over.
+bool few_rows(const treewy_attn& a) { return static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv) <= kFewRows; }
+// Whether the tiles are put in a row.  For few rows always: 64 drafts of 4 nodes
+// on 8 key heads 94 us (an item per CTA: 114), 64 tokens 64 us (69).  Otherwise
+// where there are few items, for which a CTA apiece would leave SMs idle, and
+// fewer where they are row tiles of one context, which L2 then serves to
+// neighbours: 64-node trees of 4 row tiles 61 us with 64 items (72), 83 with
+// 128 (75), 146 with 256 (114); 16-node trees of one row tile 57 us with 128
+// (61), 94 with 256 (96), 164 with 512 (150).
 bool listed(const treewy_attn& a) {
   const int mt = row_tiles_of(a);
   const int64_t items = static_cast<int64_t>(a.R) * a.cache.Hkv * mt;
-  return a.R <= kMaxListed && (mt == 1 || items <= 4 * kMaxPieces) && items * (2 + a.max_context / kTile) < (int64_t(1) << 31);
+  return a.R <= kMaxListed && (few_rows(a) || items * mt <= 2 * kMaxPieces) && items * (2 + a.max_context / kTile) < (int64_t(1) << 31);
 }
 int rows_cap(const treewy_attn& a) {
   return static_cast<int>(std::min<int64_t>(kTile, static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv)));
@@ -656,7 +678,6 @@ bool make_map(CUtensorMap* map, const void* codes, int d, int rows, int64_t bloc
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool few_rows(const treewy_attn& a) { return static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv) <= kFewRows; }
 // A 16-byte aligned address beside p, for a map that nothing is read through.
 void* any16(const void* p) { return reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15)); }
 uint64_t up256(uint64_t n) { return (n + 255) & ~uint64_t(255); }
@@ -756,7 +777,9 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
     e = c.d > 128 ? launch<2>(p, maps, grid, stream) : launch<1>(p, maps, grid, stream);
   }
   if (e != cudaSuccess || !p.listed) return e;
-  const int many = static_cast<int64_t>(a.R) * c.Hkv * p.tiles_m * 8 <= kMaxPieces ? 1 : 0;
+  // 256K tokens of one request in 57 us, 71 by eight rows to a CTA; 64 tokens of eight rows 62.5 us against 64; but 64-node
+  // trees of 8 requests 78 us against 61
+  const int many = p.rows_cap <= 8 || static_cast<int64_t>(a.R) * c.Hkv * p.tiles_m * 8 <= kMaxPieces ? 1 : 0;
   return launch_after(attend_join_kernel, dim3(many ? p.rows_cap : (p.rows_cap + kJoinRows - 1) / kJoinRows, grid), 32 * kJoinRows, stream, p, many);
 }
 

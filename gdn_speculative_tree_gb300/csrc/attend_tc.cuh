@@ -43,6 +43,12 @@ constexpr float kLeast = 1e-37f;                // of a score's factor: -inf tim
 constexpr uint32_t kHalf = 128 * 128;           // bytes of 128 rows of 128
 constexpr unsigned kFull = 0xffffffffu;
 
+// Drafts of at most kFewRows rows (nodes times query heads of a key head) are
+// another kernel's (attend_few.cu): 64 of them, contexts of 1000 to 4000, take
+// 94 us there at 16 rows (146 in attend_tc_kernel), 140 at 20 (137), and with
+// places for 32 of them it took 162 at 32 rows (150).
+constexpr int kFewRows = 16;
+
 struct Consts {
   float ks[kGroups], lv[kGroups], il[kGroups];  // key scale, log2 of the value scale, 1 / value scale
   int bad;
@@ -67,7 +73,7 @@ struct RingSmem {
 struct DraftSmem {
   unsigned long long seen[kMaxNodes];  // the nodes that a node sees
   unsigned long long no_number;        // nodes with a value that is none
-  float rowf[kTile];                   // a row's unit of the queries, times the scores' factor
+  float rowf[kFewRows];                // (few rows) a row's unit of the queries, times the scores' factor
   float ks[kMaxNodes], lv[kMaxNodes], il[kMaxNodes];
   int parent[kMaxNodes];
   int bad_tree;
@@ -146,11 +152,6 @@ __device__ __forceinline__ void tmem_wait32(uint32_t* r) {
                  "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
                  "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 __device__ __forceinline__ void tmem_st4(uint32_t at, const uint32_t* r) {
@@ -503,22 +504,6 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int blocks, uint3
     for (int i = lo * 8 + t; i < hi * 8; i += THREADS) *reinterpret_cast<uint4*>(tile + x * block + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// Parents of the segment's nodes; who sees whom.
-__device__ __forceinline__ void load_tree(const Params& p, DraftSmem& ds, const Segment& g, int t) {
-  if (t >= g.N) return;
-  const int q = p.a.parent != nullptr ? __ldg(p.a.parent + g.lo + t) : t - 1;
-  const bool wrong = q < -1 || q >= t;
-  if (wrong) ds.bad_tree = 1;
-  ds.parent[t] = wrong ? -1 : q;
-}
-__device__ __forceinline__ void see(DraftSmem& ds, const Segment& g, int t) {
-  if (t >= g.N) return;
-  unsigned long long m = 0;
-#pragma unroll 1
-  for (int q = t; q >= 0; q = ds.parent[q]) m |= 1ull << q;
-  ds.seen[t] = m;
-}
-
 // What one thread says of a finished segment: the status, and where it is a
 // part of an item, what the joining kernel needs.
 template <bool M>
@@ -541,9 +526,6 @@ __device__ __forceinline__ void init_ring(RingSmem<S>& rs, int lane) {
   mbar_init(&rs.cfull[lane], 1);
 }
 
-// Drafts of at most kFewRows rows (nodes times query heads of a key head) are
-// another kernel's (attend_few.cu).
-constexpr int kFewRows = 32;
 cudaError_t launch_attend_few(const Params& p, const CUtensorMap& k, const CUtensorMap& v, unsigned grid, cudaStream_t stream);
 
 }  // namespace treewy
