@@ -24,6 +24,16 @@
 // The draft's keys and values take two tokens of its tile each, one per term
 // (n and 64 + n); the ancestors are a mask of bits.
 //
+// Bound by the way of a tile through its set where the tensor pipe could take
+// twice as many (48 % busy): S, maxima, the reference, weights, O, and only then
+// the next S in its place, O taking all of TMEM that S does not for heads of
+// 256.  A tile's two products are 2,048 cycles, and a set takes 6,500 for one,
+// 3,100 of them waiting for S.  256 trees of 16 to 64 nodes over 500 to 4000
+// tokens: 490 us, 777 TFLOP/s (counted once, not by term); all of 64 nodes over
+// 4000: 951 us, 1,138 TFLOP/s, 0.58 of a dense bf16 product's rate; with heads
+// of 128, whose softmax is as long, 790 us, 685 TFLOP/s (828 us with two tiles
+// of S).
+//
 //   warps 0-15   softmax, outputs
 //   warps 16, 17 page table, scales, pages and terms (TMA): keys, and values
 //   warp 18      issues the products: S of the next tiles before O of this one
@@ -40,7 +50,8 @@ constexpr uint32_t kColO = 0, kTmemCols = 512;
 // Terms of every row: a warp takes four rows of a token (its query heads, then
 // key heads, keys and values) at a time.  Units are the exponents of a row's
 // power of two, kNone above them where a value's row has something that is no
-// number.  Bound by HBM: every row is read and written once.
+// number.  Bound by HBM: every row is read and written once (the wide trees'
+// 210 MB in 47 us), where every CTA would convert them for its own tile.
 constexpr int kNone = 1024, kSplitThreads = 256, kSplitRows = 4;
 __global__ void __launch_bounds__(kSplitThreads) attend_split_kernel(const __grid_constant__ Params p, int groups) {
   after_previous();
@@ -592,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 
 // An item that lies in several pieces: its parts' outputs, each normed with
 // its own sum, by the weights 2^lse.  A CTA takes eight rows, a warp each, a
-// lane eight columns; or one row (`many`: few items, of many parts each), whose
-// parts the warps share.
+// lane eight columns; or one row (`many`), whose parts the warps share.  Bound
+// by three loads in a row (the item, its parts' sums, their outputs): 5 us.
 constexpr int kJoinRows = 8;
 __global__ void __launch_bounds__(32 * kJoinRows) attend_join_kernel(const __grid_constant__ Params p, int many) {
   after_previous();
