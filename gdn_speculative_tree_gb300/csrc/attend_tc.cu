@@ -52,12 +52,28 @@ constexpr uint32_t kColO = 0, kTmemCols = 512;
 // power of two, kNone above them where a value's row has something that is no
 // number.  Bound by HBM: every row is read and written once (the wide trees'
 // 210 MB in 47 us), where every CTA would convert them for its own tile.
-constexpr int kNone = 1024, kSplitThreads = 256, kSplitRows = 4;
+//
+// Its first CTA also finds the order in which the requests are begun where an
+// item is a CTA's: the longest context first, so that the last CTAs are short
+// (256 trees 490 us in their own order; 100 of them 221).
+constexpr int kNone = 1024, kSplitThreads = 256, kSplitRows = 4, kMaxOrdered = 1024;
 __global__ void __launch_bounds__(kSplitThreads) attend_split_kernel(const __grid_constant__ Params p, int groups) {
   after_previous();
   const treewy_attn& a = p.a;
   const int lane = threadIdx.x & 31, d = a.cache.d, G = p.G, Hkv = a.cache.Hkv, heads = a.Hq + 2 * Hkv;
   const unsigned T = static_cast<unsigned>(a.T), jobs = T * groups;
+  if (p.order != nullptr && blockIdx.x == 0) {
+    __shared__ int length[kMaxOrdered];
+    for (int r = threadIdx.x; r < a.R; r += kSplitThreads) length[r] = __ldg(a.cache.length + r);
+    __syncthreads();
+    for (int r = threadIdx.x; r < a.R; r += kSplitThreads) {
+      const int mine = length[r];
+      int before = 0;
+#pragma unroll 8
+      for (int s = 0; s < a.R; ++s) before += length[s] > mine || (length[s] == mine && s < r);
+      p.order[before] = r;
+    }
+  }
 #pragma unroll 1
   for (unsigned job = blockIdx.x * (kSplitThreads / 32) + (threadIdx.x >> 5); job < jobs; job += gridDim.x * (kSplitThreads / 32)) {
     const unsigned token = job / groups;
@@ -693,9 +709,13 @@ bool make_map(CUtensorMap* map, const void* codes, int d, int rows, int64_t bloc
 void* any16(const void* p) { return reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15)); }
 uint64_t up256(uint64_t n) { return (n + 255) & ~uint64_t(255); }
 
+// Whether the longest contexts are begun first: where an item is a CTA's, up to a number of requests behind which the last
+// CTAs matter little.
+bool ordered(const treewy_attn& a) { return !few_rows(a) && !listed(a) && a.R <= kMaxOrdered; }
+
 // Where things are in the workspace: the parts of items in several pieces, then the terms.
 struct Workspace {
-  uint64_t record, lse, q_terms, k_terms, v_terms, q_units, k_units, v_units, end;
+  uint64_t record, lse, q_terms, k_terms, v_terms, q_units, k_units, v_units, order, end;
   explicit Workspace(const treewy_attn& a) {
     const uint64_t rows = listed(a) ? static_cast<uint64_t>(kMaxPieces) * 2 * rows_cap(a) : 0;
     const uint64_t T = few_rows(a) ? 0 : static_cast<uint64_t>(std::max<int64_t>(a.T, 1)), q = T * a.Hq, kv = T * a.cache.Hkv, d = a.cache.d;
@@ -707,7 +727,8 @@ struct Workspace {
     q_units = up256(v_terms + 2 * kv * d);
     k_units = up256(q_units + 2 * q);
     v_units = up256(k_units + 2 * kv);
-    end = v_units + 2 * kv;
+    order = up256(v_units + 2 * kv);
+    end = order + (ordered(a) ? 4 * static_cast<uint64_t>(a.R) : 0);
   }
 };
 
@@ -748,6 +769,7 @@ cudaError_t launch_attend_tc(const treewy_attn& a, cudaStream_t stream) {
   p.q_units = reinterpret_cast<int16_t*>(ws + at.q_units);
   p.k_units = reinterpret_cast<int16_t*>(ws + at.k_units);
   p.v_units = reinterpret_cast<int16_t*>(ws + at.v_units);
+  if (ordered(a) && a.T > 0) p.order = reinterpret_cast<int*>(ws + at.order);  // without rows nothing writes it
   unsigned grid;
   if (p.listed) {
     int dev = 0, sms = 0;

@@ -279,6 +279,7 @@ struct Params {
   // of attend_split_kernel: terms e4m3 [2][Hkv][T][G][d] (G = 1: keys and values), and their units' exponents
   uint8_t *q_terms, *k_terms, *v_terms;
   int16_t *q_units, *k_units, *v_units;
+  int* order;            // requests as they are begun where an item is a CTA's, or NULL: in their own order
 };
 
 // The tiles of one item that a CTA takes.
@@ -384,7 +385,9 @@ __device__ __forceinline__ Part<kTilesOfRows> make_plan(const Params& p, PlanSme
 #pragma unroll 1
     for (int i = t; i < 2 * p.rows_cap; i += THREADS) p.part_lse[2 * static_cast<int64_t>(blockIdx.x) * p.rows_cap + i] = INFINITY;
   } else {
-    const int per = c.Hkv * p.tiles_m, r = static_cast<int>(blockIdx.x / per), item = static_cast<int>(blockIdx.x % per);
+    const int per = c.Hkv * p.tiles_m, item = static_cast<int>(blockIdx.x % per);
+    int r = static_cast<int>(blockIdx.x / per);
+    if (p.order != nullptr) r = min(max(__ldcg(p.order + r), 0), a.R - 1);
     const CacheRequest q = cache_request(c, a.node_offset, r, a.T, a.max_nodes, a.max_context);
     if (q.err != 0 && item == 0 && t == 0) atomicOr(a.status + r, q.err);
     if (t == 0) cs.lo[0] = q.lo, cs.nodes[0] = static_cast<uint8_t>(q.N), cs.len[0] = q.len;
