@@ -29,9 +29,9 @@
 // the next S in its place, O taking all of TMEM that S does not for heads of
 // 256.  A tile's two products are 2,048 cycles, and a set takes 6,500 for one,
 // 3,100 of them waiting for S.  256 trees of 16 to 64 nodes over 500 to 4000
-// tokens: 490 us, 777 TFLOP/s (counted once, not by term); all of 64 nodes over
-// 4000: 951 us, 1,138 TFLOP/s, 0.58 of a dense bf16 product's rate; with heads
-// of 128, whose softmax is as long, 790 us, 685 TFLOP/s (828 us with two tiles
+// tokens: 470 us, 811 TFLOP/s (counted once, not by term); all of 64 nodes over
+// 4000: 952 us, 1,137 TFLOP/s, 0.58 of a dense bf16 product's rate; with heads
+// of 128, whose softmax is as long, 787 us, 688 TFLOP/s (828 us with two tiles
 // of S).
 //
 //   warps 0-15   softmax, outputs
@@ -55,7 +55,7 @@ constexpr uint32_t kColO = 0, kTmemCols = 512;
 //
 // Its first CTA also finds the order in which the requests are begun where an
 // item is a CTA's: the longest context first, so that the last CTAs are short
-// (256 trees 490 us in their own order; 100 of them 221).
+// (256 trees 470 us, 490 in their own order; 100 of them 183 and 221).
 constexpr int kNone = 1024, kSplitThreads = 256, kSplitRows = 4, kMaxOrdered = 1024;
 __global__ void __launch_bounds__(kSplitThreads) attend_split_kernel(const __grid_constant__ Params p, int groups) {
   after_previous();
@@ -682,13 +682,14 @@ bool few_rows(const treewy_attn& a) { return static_cast<int64_t>(a.max_nodes) *
 // on 8 key heads 94 us (an item per CTA: 114), 64 tokens 64 us (69).  Otherwise
 // where there are few items, for which a CTA apiece would leave SMs idle, and
 // fewer where they are row tiles of one context, which L2 then serves to
-// neighbours: 64-node trees of 4 row tiles 61 us with 64 items (72), 83 with
-// 128 (75), 146 with 256 (114); 16-node trees of one row tile 57 us with 128
-// (61), 94 with 256 (96), 164 with 512 (150).
+// neighbours.  16-node trees of one row tile: 57 us with 128 items (61), 70 with
+// 160 (61), 94 with 256 (76); 64-node trees of 4 row tiles: 64 us with 72 items
+// (73), 76 with 96 (75), 83 with 128 (75).
 bool listed(const treewy_attn& a) {
   const int mt = row_tiles_of(a);
   const int64_t items = static_cast<int64_t>(a.R) * a.cache.Hkv * mt;
-  return a.R <= kMaxListed && (few_rows(a) || items * mt <= 2 * kMaxPieces) && items * (2 + a.max_context / kTile) < (int64_t(1) << 31);
+  return a.R <= kMaxListed && (few_rows(a) || items <= (mt == 1 ? kMaxPieces : kMaxPieces / 2)) &&
+         items * (2 + a.max_context / kTile) < (int64_t(1) << 31);
 }
 int rows_cap(const treewy_attn& a) {
   return static_cast<int>(std::min<int64_t>(kTile, static_cast<int64_t>(a.max_nodes) * (a.Hq / a.cache.Hkv)));

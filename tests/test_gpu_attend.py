@@ -86,7 +86,8 @@ def test_several_items_of_many_tiles_to_a_piece(cuda_lib, d, page, nodes):
 
 @pytest.mark.parametrize("d", [128, 256])
 @pytest.mark.parametrize("nodes,Hq,Hkv,R", [(2, 8, 2, 130), (9, 1, 1, 330), (4, 12, 3, 100), (16, 2, 2, 200), (17, 1, 1, 304), (17, 1, 1, 305),
-                                            (6, 12, 3, 100), (40, 16, 2, 16), (40, 16, 2, 17), (17, 1, 1, 1024), (17, 1, 1, 1025)])
+                                            (6, 12, 3, 100), (40, 16, 2, 16), (40, 16, 2, 17), (17, 1, 1, 1024), (17, 1, 1, 1025), (17, 1, 1, 152), (17, 1, 1, 153),
+                                            (40, 16, 2, 12), (40, 16, 2, 13)])
 def test_on_both_sides_of_every_choice(cuda_lib, d, nodes, Hq, Hkv, R):
     """8, 9, 16, 17 and more rows; tiles in a row, several items to a piece, or an item to a CTA, the
     longest first or in order."""
