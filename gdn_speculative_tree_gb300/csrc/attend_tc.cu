@@ -422,11 +422,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         bool grown = false;
         float down = 1.f;
         if (start) {  // the larger of the first two
+          // The second tile's set waits for the first one's maxima before it says that its own are there: the other way
+          // round the first set could go on to its next phase, of the same parity as the one before, past a warp that
+          // has yet to look.
+          if (j != t0) wait_warp(rs, &cs.mdone[set ^ 1], ((gt - 1) >> 1) & 1);
           if (hf == 0) cs.first[set][row] = top;
           warp_arrive(&cs.mdone[set]);
           if (t1 - t0 > 1) {
-            const int other = j == t0 ? gt + 1 : gt - 1;
-            wait_warp(rs, &cs.mdone[set ^ 1], (other >> 1) & 1);
+            if (j == t0) wait_warp(rs, &cs.mdone[set ^ 1], ((gt + 1) >> 1) & 1);
             top = fmaxf(top, cs.first[set ^ 1][row]);
           }
           m = top;
