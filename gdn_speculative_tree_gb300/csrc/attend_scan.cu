@@ -44,11 +44,19 @@ __device__ __forceinline__ void sixteen(float* to, const uint4& w, float f) {
     *reinterpret_cast<float4*>(to + 4 * e) = make_float4(y0.x * f, y0.y * f, y1.x * f, y1.y * f);
   }
 }
-// Four values of a row that start on four elements.
+// x, or NaN where it is not finite: an infinity counts as no number whatever it is multiplied by.
+__device__ __forceinline__ float number(float x) { return fabsf(x) <= 3.4028234664e38f ? x : NAN; }
+// A value of a row; four that start on four elements.
+__device__ __forceinline__ float load1(const void* p, int64_t at, bool bf16) { return number(load_qkv(p, at, bf16)); }
 __device__ __forceinline__ float4 load4(const void* p, int64_t at, bool bf16) {
-  if (!bf16) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at));
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at));
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  float4 x;
+  if (bf16) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at));
+    x = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  } else {
+    x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at));
+  }
+  return make_float4(number(x.x), number(x.y), number(x.z), number(x.w));
 }
 
 __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
@@ -96,8 +104,8 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
   } else {
     for (int x = t; x < kRows * pad; x += kThreads) {
       const int i = x / pad, col = x % pad, rr = row0 + i;
-      qs[x] = i < live && col < d ? load_qkv(a.q, (static_cast<int64_t>(q.lo) + rr / G) * a.q_stride +
-                                                      (static_cast<int64_t>(h) * G + rr % G) * d + col, bf16)
+      qs[x] = i < live && col < d ? load1(a.q, (static_cast<int64_t>(q.lo) + rr / G) * a.q_stride +
+                                                   (static_cast<int64_t>(h) * G + rr % G) * d + col, bf16)
                                   : 0.f;
     }
   }
@@ -159,8 +167,8 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
           v = e4m3_to_float(__ldg(static_cast<const uint8_t*>(c.v) + from)) * __ldg(c.v_scale + b);
         } else if (col < d) {
           const int64_t token = static_cast<int64_t>(q.lo) + at, head = static_cast<int64_t>(h) * d + col;
-          k = load_qkv(a.k, token * a.k_stride + head, bf16);
-          v = load_qkv(a.v, token * a.v_stride + head, bf16);
+          k = load1(a.k, token * a.k_stride + head, bf16);
+          v = load1(a.v, token * a.v_stride + head, bf16);
         }
         tile[i * pitch + col] = k;
         value[i * pitch + col] = v;
@@ -181,7 +189,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
     for (int e = 0; e < 4; ++e) {
       const int i = sub + 8 * e;
       const bool sees = i < n && (context || ((sh.seen[node] >> (t0 + i)) & 1));
-      s[e] = sees ? s[e] * a.scale : -INFINITY;
+      s[e] = sees ? number(s[e] * a.scale) : -INFINITY;  // so that -infinity is what is not seen, and no score that has passed f32
       high = fmaxf(high, s[e]);
     }
 #pragma unroll

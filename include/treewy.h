@@ -560,8 +560,9 @@ typedef struct treewy_attn {
  * value of the draft is within 2^-17 of its row's largest (or 2^-117), a weight of the
  * softmax within 2^-8 of itself or 2^-16 of its row's largest.  Other calls
  * run in f32.  A NaN (or an infinity, which counts as one) in a key reaches
- * every node that sees it, in a value every such node's column.  Scores pass f32: where
- * they overflow it, the node's outputs are NaN.
+ * every node that sees it, in a value every such node's column, in a query its
+ * own row.  Where a score overflows f32, the node's outputs are NaN (on the
+ * tensor cores one that overflows below counts for nothing).
  */
 treewy_status treewy_attend(const treewy_attn* attn, cudaStream_t stream);
 
