@@ -261,7 +261,7 @@ __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
 #pragma unroll
       for (int k = 0; k < kRanks; ++k) {
         const float* part = cluster.map_shared_rank(qs, k) + i * pad + col;
-        if (f[k] != 0.f) y = fmaf(f[k], *part, y);
+        y = fmaf(f[k], *part, y);  // a part without weight too: it has zeros, or values that are no numbers
       }
       y /= total;
       if (a.o_dtype == TREEWY_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.o)[out + col] = __float2bfloat16_rn(y);

@@ -57,3 +57,25 @@ def test_two_tokens_of_which_one_score_passes_f32(cuda_lib):
     a.q[..., 0], a.k[0, 0, 0] = 1e25, -1e25
     a.run()
     assert torch.isnan(a.o).all()
+
+
+@pytest.mark.parametrize("flags", [0, GENERIC])
+@pytest.mark.parametrize("Hq", [4, 40])
+@pytest.mark.parametrize("token", [5, 64, 200])
+def test_a_value_that_is_no_number_beside_far_larger_weights(cuda_lib, flags, Hq, token):
+    """It reaches its column, however little its token weighs: that of a tile far below the others', and none at all in f32."""
+    a = Attend([256], [1], Hq=Hq, Hkv=1, d=64, page=16, flags=flags, seed=33)
+    a.cache.k.view(torch.uint8).zero_()
+    a.cache.k.view(torch.uint8)[:, :, :, 0] = 0x38           # 1
+    a.q.zero_()
+    a.q[..., 0] = 100.0
+    a.k.zero_()
+    a.cache.ks.fill_(1.0)
+    a.scale = 1.0
+    for p in range(16):                                       # scores of 1,600 down to 100, and of 0 for the draft's own
+        a.cache.ks[int(a.cache.table_np[0, p])] = float((p + 5) % 16 + 1)
+    a.cache.v.view(torch.uint8)[int(a.cache.table_np[0, token // 16]), 0, token % 16, 9] = 127
+    a.run()
+    want = torch.zeros_like(a.o, dtype=torch.bool)
+    want[..., 9] = True
+    assert torch.equal(torch.isnan(a.o.float()), want)
