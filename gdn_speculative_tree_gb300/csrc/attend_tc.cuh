@@ -244,9 +244,8 @@ __device__ __forceinline__ int row_terms(uint4 x, bool clear, uint2& hi, uint2& 
   for (int e = 0; e < 4; ++e) {
     uint32_t y, rest;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(__uint_as_float(u[e] & 0xffff0000u) * f), "f"(__uint_as_float(u[e] << 16) * f));
-    const uint32_t four = (y + 0x00400040u) & 0xff80ff80u;  // half a unit of the fourth bit up, the rest off
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(y), "r"(four));
-    h[e] = e4m3x2_of_f16x2(four);
+    h[e] = e4m3x2_of_f16x2(y);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(y), "r"(e4m3x2_to_f16x2(h[e])));  // exactly; of the code, which has fewer bits where y is small
     l[e] = e4m3x2_of_f16x2(rest);
   }
   hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
