@@ -335,8 +335,8 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               if (((steps >> k) & 1) == 0) continue;
               const uint64_t v = desc_mn(v0 + x * kHalf + k * 4096);
-              mma_f8(o0 + x * Sh::kCols, v, smem_desc_sw128(w + k * 32, 1024), id_o | kBE5m2, acc);
-              mma_f8(o0 + x * Sh::kCols, v, smem_desc_sw128(w + Sh::kWBlock + k * 32, 1024), id_o, 1);
+              mma_f8(o0 + x * Sh::kCols, v, smem_desc_sw128(w + k * 32, 1024), id_o, acc);
+              mma_f8(o0 + x * Sh::kCols, v, smem_desc_sw128(w + Sh::kWBlock + k * 32, 1024), id_o | kBE5m2, 1);
               acc = 1;
             }
           }
@@ -461,12 +461,12 @@ __global__ void __launch_bounds__(Shape<NH, NR>::kThreads, 1)
             for (int e = 0; e < 2; ++e) {
               const int row = row0 + i + e;
               unsigned char* at = w + row * 128 + (((token >> 4) ^ (row & 7)) << 4) + (token & 15);
-              at[0] = static_cast<unsigned char>(hi >> (16 * e + 8));
-              at[Sh::kWBlock] = static_cast<unsigned char>(lo >> (8 * e));
+              at[0] = static_cast<unsigned char>(hi >> (8 * e));
+              at[Sh::kWBlock] = static_cast<unsigned char>(lo >> (16 * e + 8));
               if (draft_tile) {  // a value's two terms have one weight
                 at = w + row * 128 + ((((token + 64) >> 4) ^ (row & 7)) << 4) + (token & 15);
-                at[0] = static_cast<unsigned char>(hi >> (16 * e + 8));
-                at[Sh::kWBlock] = static_cast<unsigned char>(lo >> (8 * e));
+                at[0] = static_cast<unsigned char>(hi >> (8 * e));
+                at[Sh::kWBlock] = static_cast<unsigned char>(lo >> (16 * e + 8));
               }
             }
           }

@@ -18,8 +18,8 @@
 // Two sets of eight warps take tiles in turn, so that one's loads and waits fall
 // into the other's arithmetic; a thread has half a row of its set's tile.  The
 // sets share the rows' references: a tile's weights wait for the maxima of the
-// tile before it, not for its weights.  The first reference is the larger
-// maximum of a segment's first two tiles, the draft's own one being small.
+// tile before it, not for its weights.  The first reference comes from a
+// segment's first two tiles, the draft's own one being small.
 //
 // The draft's keys and values take two tokens of its tile each, one per term
 // (n and 64 + n); the ancestors are a mask of bits.
@@ -46,6 +46,12 @@ constexpr int kSets = 2, kSetWarps = 8, kSoftWarps = kSets * kSetWarps, kLoadWar
 constexpr int kSoftThreads = 32 * kSoftWarps, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kParts = kSoftWarps / 4;  // warps that share 32 rows
 constexpr uint32_t kColO = 0, kTmemCols = 512;
+// The first reference is the largest of a segment's first two tiles where a token stands out there: where some 16 tokens
+// in a row have none within 2^-kFar of it.  Then the others need the weights' bits, and few rows see a larger one later.
+// Elsewhere it is 2^kRoom above, so that a maximum that grows brings the output down less often: that waits for the tile
+// before.  Wide trees 470 us; 478 and 519 with kFar = 6 and 4, 527 without room for any row; with room for all of them
+// (471) the outputs of 32,000 tokens beside a first one of a third of the weight are more than 0.008 off.
+constexpr float kFar = 8.f, kRoom = 4.f;
 
 // Terms of every row: a warp takes four rows of a token (its query heads, then
 // key heads, keys and values) at a time.  Units are the exponents of a row's
@@ -124,7 +130,7 @@ template <int S>
 struct AttendSmem {
   RingSmem<S> ring;
   uint64_t sfull[3], mdone[2], pready[2], pvdone[2], qfull, qfree, drain;
-  float ref[kTile], first[kSets][kTile], half[kSets][2][kTile], sum[kParts][kTile];  // of the rows
+  float ref[kTile], first[kSets][kTile], half[kSets][2][kTile], low[kSets][2][kTile], sum[kParts][kTile];  // of the rows
   uint32_t tmem;
   int bad[2];                    // a page of the segment's: two in turn, as warps still read the last one's
   Segment segment;               // the softmax warps' current one
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             const uint64_t b = desc_mn(v0 + k * 4096);
 #pragma unroll
             for (int term = 0; term < 2; ++term) {
-              mma_f8_ts(tmem + kColO, w + k / 2 * 64 + k % 2 * 16 + term * 8, b, term == 0 ? id_o | kAE5m2 : id_o, acc);
+              mma_f8_ts(tmem + kColO, w + k / 2 * 64 + k % 2 * 16 + term * 8, b, term == 0 ? id_o : id_o | kAE5m2, acc);
               acc = 1;
             }
           }
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           fence_proxy_async_smem();
         }
         // the tile's maxima
-        float top = -INFINITY, rf = rowf;
+        float top = -INFINITY, low = INFINITY, rf = rowf;  // low: of the context's maxima by 16 tokens
         if (alive && j == 0) {  // the draft's scores go back in the place of the products; the tile's constants are 1 and 0
           rf = 1.f;
           const Segment& now = cs.segment;
@@ -405,7 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
               for (int i = 0; i < 4; ++i)
                 y[i] = fmaxf(fmaxf(s[16 * q + i], s[16 * q + 4 + i]), fmaxf(s[16 * q + 8 + i], s[16 * q + 12 + i]));
               const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-              top = fmaxf(top, fmaf(z, fmaxf(cc.ks[x / 16 + q] * rowf, kLeast), cc.lv[x / 16 + q]));
+              const float high = fmaf(z, fmaxf(cc.ks[x / 16 + q] * rowf, kLeast), cc.lv[x / 16 + q]);
+              top = fmaxf(top, high);
+              if (x + 16 * q + 16 <= n) low = fminf(low, high);
             }
           }
         }
@@ -417,8 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           now = cs.ref[row];
         }
         cs.half[set][hf][row] = top;
+        if (start) cs.low[set][hf][row] = low;
         pair_sync();
         top = fmaxf(top, cs.half[set][hf ^ 1][row]);
+        if (start) low = fminf(low, cs.low[set][hf ^ 1][row]);
         bool grown = false;
         float down = 1.f;
         if (start) {  // the larger of the first two
@@ -431,9 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           if (t1 - t0 > 1) {
             if (j == t0) wait_warp(rs, &cs.mdone[set ^ 1], ((gt + 1) >> 1) & 1);
             top = fmaxf(top, cs.first[set ^ 1][row]);
+            low = fminf(low, fminf(cs.low[set ^ 1][0][row], cs.low[set ^ 1][1][row]));
           }
-          m = top;
-          if (hf == 0 && j == t0) cs.ref[row] = top;  // the other set has it too, and reads this two tiles later
+          m = top - low > kFar ? top : top + kRoom;
+          if (hf == 0 && j == t0) cs.ref[row] = m;  // the other set has it too, and reads this two tiles later
         } else {
           if (now != m) sum *= ex2(m - now), m = now;
           grown = top > m + kGrowth;
@@ -491,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 uint32_t h0, l0, h1, l1;
                 weight_terms(w[0], w[1], h0, l0);
                 weight_terms(w[2], w[3], h1, l1);
-                hi[i] = __byte_perm(h0, h1, 0x7531);
-                lo[i] = l0 | (l1 << 16);
+                hi[i] = h0 | (h1 << 16);
+                lo[i] = __byte_perm(l0, l1, 0x7531);
               }
               sum = fmaf((part[0].x + part[0].y) + (part[1].x + part[1].y), cc.il[at / 16 + q], sum);
               tmem_st4(sc + 64 * hf + 16 * y + 4 * q, hi);

@@ -10,17 +10,19 @@
 //
 // A tile is 128 tokens.  The weights of the softmax are
 //
-//   w = 2^(s + log2(the page's value scale) - m + 6)
+//   w = 2^(s + log2(the page's value scale) - m + 7.75)
 //
 // with one reference m per row for the running maximum of s + log2(scale): they
 // have the size of what they contribute, however far the pages' scales lie
-// apart.  m follows the maximum only when that has grown by more than 2^5 (the
-// output and the sum are then brought down), so weights stay within 2^11.
-// Their hi is e5m2 (three significant bits, down to 2^-16) and lo e4m3: 2^-8 of
-// a weight or 2^-16 of its row's largest, and 2^-3 of a weight down to 2^-22 of
-// the largest: hundreds of thousands of tokens that weigh next to nothing each
-// still count.  (Two e4m3 terms are as exact above, but drop what is below
-// 2^-15 of the largest.)
+// apart.  m follows the maximum only when that has grown by more than 2 (the
+// output and the sum are then brought down), so weights stay within 2^8.75 =
+// 431, e4m3's 448.  Their hi is e4m3 (four significant bits, steps of 2^-9 below
+// 2^-6) and lo e5m2 (three, down to 2^-16): a weight is off by 2^-8 of itself or by
+// 2^-14, which is 2^-21 of a row's largest (2^-17 where attend_tc_kernel leaves
+// room above it), and a smaller one than that by 2^-3 of itself or 2^-17.  So
+// tokens beside one that has most of the weight are about as exact as bf16 would
+// have them.  (hi in e5m2 and lo in e4m3 ends at 2^-10, with weights of up to 2^11:
+// 2^-16 of the largest with the headroom of 2^5 that brings the output down least.)
 //
 // Work: the items (request, key head, 128 rows at most) are runs of tiles, the
 // draft's own keys first; all runs in a row are cut into equal pieces, one for
@@ -38,7 +40,7 @@ constexpr int kTile = 128;                      // tokens, and rows at most
 constexpr int kGroups = kTile / 16;             // the smallest page is 16 tokens
 constexpr int kMaxListed = 640;                 // requests whose tiles are put in a row
 constexpr int kMaxPieces = 152;                 // CTAs that share the row
-constexpr float kGrowth = 5.f, kBias = 6.f;     // lo is at most 2^-3 of a weight: 2^(kGrowth + kBias - 3) <= 448
+constexpr float kGrowth = 1.f, kBias = 7.75f;   // weights are within e4m3: 2^(kGrowth + kBias) <= 448
 constexpr float kLeast = 1e-37f;                // of a score's factor: -inf times it stays -inf
 constexpr uint32_t kHalf = 128 * 128;           // bytes of 128 rows of 128
 constexpr unsigned kFull = 0xffffffffu;
@@ -199,15 +201,15 @@ __device__ __forceinline__ uint4 load_row8(const uint16_t* row, int c, int d) {
   return c < d ? __ldg(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
 }
 
-// Two weights as hi + lo: of their f16, hi is the upper byte after rounding
-// (e5m2 is f16 without its last eight bits), lo the rest in e4m3.  `hi` has the
-// bytes in places 1 and 3.
+// Two weights as hi + lo: of their f16, hi is the e4m3 nearest to it, and lo the
+// upper byte of the rest (e5m2 is f16 without its last eight bits) after rounding.
+// `lo` has the bytes in places 1 and 3.
 __device__ __forceinline__ void weight_terms(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   uint32_t h, rest;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
-  hi = h + 0x00800080u;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(hi & 0xff00ff00u));
-  lo = e4m3x2_of_f16x2(rest);
+  hi = e4m3x2_of_f16x2(h);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(e4m3x2_to_f16x2(hi)));
+  lo = rest + 0x00800080u;
 }
 
 // The largest of a row's |bf16|, by one warp (lane: eight of them).

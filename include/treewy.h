@@ -557,12 +557,15 @@ typedef struct treewy_attn {
  *
  * bf16 rows with bf16 outputs and d a multiple of 16 run on the tensor cores in
  * 8-bit products, every f32 or bf16 operand as two 8-bit terms: a query, key or
- * value of the draft is within 2^-17 of its row's largest (or 2^-117), a weight of the
- * softmax within 2^-8 of itself or 2^-16 of its row's largest.  Other calls
- * run in f32.  A NaN (or an infinity, which counts as one) in a key reaches
- * every node that sees it, in a value every such node's column, in a query its
- * own row.  Where a score overflows f32, the node's outputs are NaN (on the
- * tensor cores one that overflows below counts for nothing).
+ * value of the draft is within 2^-17 of its row's largest (or 2^-117), a weight
+ * of the softmax within 2^-8 of itself or 2^-17 of its row's largest (2^-21
+ * where that stands out from the others, or with at most 16 rows: nodes times
+ * query heads of a key head).  Other calls run in f32.
+ *
+ * A NaN (or an infinity, which counts as one) in a key reaches every node that
+ * sees it, in a value every such node's column, in a query its own row.  Where a
+ * score overflows f32, the node's outputs are NaN (on the tensor cores one that
+ * overflows below counts for nothing).
  */
 treewy_status treewy_attend(const treewy_attn* attn, cudaStream_t stream);
 

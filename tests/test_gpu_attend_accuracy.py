@@ -1,11 +1,90 @@
-"""treewy_attend where errors hide behind a bound for each element."""
+"""treewy_attend where errors hide behind a bound for each element: long contexts, of which a part could be lost, and tokens
+beside one that has most of the weight.  Bounds are of the norm of a row's output, or of values that mark their tile."""
 import numpy as np
 import pytest
 import torch
 
-from tests.cache_helpers import Attend, f64
+from gdn_speculative_tree_gb300 import binding
+from oracle import attend_oracle as orc
+from tests.cache_helpers import E4M3, TYPES, Attend, f64
 
 pytestmark = pytest.mark.gpu
+
+GENERIC = binding.FLAG_FORCE_GENERIC
+
+
+class Shared:
+    """R requests of N nodes (chains) over the pages of one context: keys and values are e4m3 numbers, the scales 1."""
+
+    def __init__(self, keys, values, *, R, N, G, page=64, scale=None, out="bf16", flags=0, seed=0):
+        n, Hkv, d = keys.shape
+        g = torch.Generator().manual_seed(seed)
+        pages = -(-n // page)
+        self.n, self.R, self.N, self.G, self.scale = n, R, N, G, d ** -0.5 if scale is None else scale
+        self.k8, self.v8 = keys.to(E4M3), values.to(E4M3)
+
+        def paged(x):
+            room = torch.full((pages * page, Hkv, d), 127, dtype=torch.uint8)  # NaN behind the tokens
+            room[:n] = x.view(torch.uint8)
+            return room.view(pages, page, Hkv, d).transpose(1, 2).contiguous().cuda().view(E4M3)
+
+        one = torch.ones(pages, Hkv, device="cuda")
+        table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(R, 1)
+        self.cache = binding.make_cache(k=paged(self.k8), v=paged(self.v8), k_scale=one, v_scale=one.clone(), page_table=table,
+                                        length=torch.full((R,), n, dtype=torch.int32, device="cuda"))
+        T = R * N
+        self.off = torch.arange(0, T + 1, N, dtype=torch.int32, device="cuda")
+        self.q = torch.randn(T, Hkv * G, d, generator=g).bfloat16().cuda()
+        self.k, self.v = (torch.randn(T, Hkv, d, generator=g).bfloat16().cuda() for _ in range(2))
+        self.o = torch.full((T, Hkv * G, d), -7.0, dtype=TYPES[out], device="cuda")
+        self.status, self.flags = torch.zeros(R, dtype=torch.int32, device="cuda"), flags
+
+    def run(self):
+        call = binding.make_attn(cache=self.cache, node_offset=self.off, q=self.q, k=self.k, v=self.v, o=self.o, status=self.status,
+                                 scale=self.scale, max_nodes=self.N, max_context=self.n, flags=self.flags)
+        binding.treewy_attend(call)
+        torch.cuda.synchronize()
+        assert not self.status.any()
+        return self
+
+    def want(self, r):
+        at = slice(r * self.N, (r + 1) * self.N)
+        keys, values = (f64(x.float()).swapaxes(0, 1) for x in (self.k8, self.v8))
+        return orc.attend(f64(self.q[at]), f64(self.k[at]), f64(self.v[at]), np.arange(self.N) - 1, keys, values, self.scale)
+
+    def off_by(self, requests):
+        """The largest error of a row's output, relative to the row's norm."""
+        worst = 0.0
+        for r in requests:
+            want, got = self.want(r), f64(self.o[r * self.N:(r + 1) * self.N])
+            worst = max(worst, (np.linalg.norm(got - want, axis=2) / np.linalg.norm(want, axis=2)).max())
+        return worst
+
+
+# A weight is within 2^-8 of itself, an output's rounding 2^-8 of it: the errors of independent tokens add up as their values
+# do, so that in the norm the output is off by no more than the two together, and by some 2^-24 of a score on the CUDA cores.
+NORM = {0: 2.0 ** -7, GENERIC: 2.0 ** -8 + 1e-4}
+
+
+@pytest.mark.parametrize("flags", [0, GENERIC])
+@pytest.mark.parametrize("share", [0.3, 0.6])
+@pytest.mark.parametrize("n", [2000, 8000, 32000])
+@pytest.mark.parametrize("R,N,G", [(152, 1, 8), (152, 4, 4), (160, 5, 4)])
+def test_tokens_beside_a_dominating_one(cuda_lib, R, N, G, n, share, flags):
+    """A first token that has a share of every row's weight and next to no value: the outputs are the other tokens', each of
+    which weighs 2^-11 to 2^-16 of it.  As many requests as leave each context in one piece."""
+    torch.manual_seed(n)
+    d = 128
+    keys, values = torch.randn(n, 1, d), torch.randn(n, 1, d)
+    keys[:, 0, 0] = 0.0
+    keys[0] = 0.0
+    # the others' scores have the variance |q|^2 / d = 1: e^0.5 on the average; q is 4 in the first column
+    keys[0, 0, 0] = np.log(n * np.exp(0.5) * share / (1 - share)) * d ** 0.5 / 4
+    values[0] *= 0.01
+    a = Shared(keys, values, R=R, N=N, G=G, flags=flags, seed=n)
+    a.q[..., 0] = 4.0
+    a.k[..., 0] = 0.0
+    assert a.run().off_by([0, 70, R - 1]) <= NORM[flags]
 
 
 @pytest.mark.parametrize("Hq", [8, 32])
