@@ -67,6 +67,38 @@ NORM = {0: 2.0 ** -7, GENERIC: 2.0 ** -8 + 1e-4}
 
 
 @pytest.mark.parametrize("flags", [0, GENERIC])
+@pytest.mark.parametrize("R,N,G", [(1, 1, 8), (3, 4, 2), (1, 9, 8), (160, 1, 2), (160, 5, 4)])
+@pytest.mark.parametrize("n,page,d", [(9001, 16, 128), (5000, 64, 256), (4999, 128, 64)])
+def test_every_tile_of_a_long_context_counts(cuda_lib, n, page, d, R, N, G, flags):
+    """All scores alike, and the values of every tile of 128 tokens a number in a column of its own: the column of a tile
+    that is left out, taken twice or cut short shows it."""
+    keys, values = torch.randn(n, 1, d), torch.zeros(n, 1, d)
+    tile = torch.arange(n) // 128
+    values[torch.arange(n), 0, tile % d] = 1.0
+    a = Shared(keys, values, R=R, N=N, G=G, page=page, flags=flags)
+    a.q.zero_()
+    a.v.zero_()
+    a.run()
+    seen = np.bincount(tile.numpy() % d, minlength=d)[:d]
+    node = np.arange(N)[None, :, None, None]
+    want = np.broadcast_to(seen / (n + node + 1.0), (R, N, G, d))
+    # equal weights: 2^-8 of each and of the output's rounding
+    assert (np.abs(f64(a.o).reshape(want.shape) - want) <= 2 * 2.0 ** -8 * want).all()
+
+
+@pytest.mark.parametrize("flags", [0, GENERIC])
+@pytest.mark.parametrize("R,N,G", [(1, 1, 8), (2, 9, 8), (3, 4, 2), (160, 1, 2), (160, 5, 4)])
+@pytest.mark.parametrize("n,page", [(9001, 16), (5000, 64)])
+def test_long_contexts_in_the_norm(cuda_lib, n, page, R, N, G, flags):
+    """Random tokens: a lost tile of n / 128 would be some sqrt(128 / n) of the output, 0.12 to 0.16."""
+    torch.manual_seed(n)
+    a = Shared(torch.randn(n, 1, 128), torch.randn(n, 1, 128), R=R, N=N, G=G, page=page, flags=flags, seed=n + 1)
+    assert a.run().off_by(range(0, R, 53)) <= NORM[flags]
+    a.k8, a.v8 = (torch.cat([x.view(torch.uint8)[:1280], x.view(torch.uint8)[1408:]]).view(E4M3) for x in (a.k8, a.v8))
+    assert a.off_by([0]) > 4 * NORM[flags]  # a definition that leaves a tile out is seen
+
+
+@pytest.mark.parametrize("flags", [0, GENERIC])
 @pytest.mark.parametrize("share", [0.3, 0.6])
 @pytest.mark.parametrize("n", [2000, 8000, 32000])
 @pytest.mark.parametrize("R,N,G", [(152, 1, 8), (152, 4, 4), (160, 5, 4)])
@@ -81,7 +113,7 @@ def test_tokens_beside_a_dominating_one(cuda_lib, R, N, G, n, share, flags):
     # the others' scores have the variance |q|^2 / d = 1: e^0.5 on the average; q is 4 in the first column
     keys[0, 0, 0] = np.log(n * np.exp(0.5) * share / (1 - share)) * d ** 0.5 / 4
     values[0] *= 0.01
-    a = Shared(keys, values, R=R, N=N, G=G, flags=flags, seed=n)
+    a = Shared(keys, values, R=R, N=N, G=G, flags=flags, seed=n + 1)
     a.q[..., 0] = 4.0
     a.k[..., 0] = 0.0
     assert a.run().off_by([0, 70, R - 1]) <= NORM[flags]
