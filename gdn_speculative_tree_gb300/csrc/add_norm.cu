@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kPlainThreads) add_norm_plain_kernel(const tre
   const bool xb = a.x_dtype == TREEWY_DTYPE_BF16, rb = a.residual_dtype == TREEWY_DTYPE_BF16;
   float sum = 0.f;
   for (int i = t; i < n; i += kPlainThreads) {
-    float v = load_qkv(a.x, row * a.x_stride + i, xb);
+    const int64_t from = row * a.x_stride + i;  // plain loads: y may be x
+    float v = xb ? load1<uint16_t>(a.x, from) : load1<float>(a.x, from);
     if (a.residual != nullptr) {
       const int64_t at = row * a.residual_stride + i;
       v += rb ? load1<uint16_t>(a.residual, at) : load1<float>(a.residual, at);
