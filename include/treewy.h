@@ -659,10 +659,12 @@ typedef struct treewy_norm {
 /*
  * treewy_add_norm -- the residual's addition and the RMS norm in one pass:
  *   z = x + residual,  y = w z / sqrt(mean of z^2 + eps),
- * in f32; residual_out gets z, y and y8 the norm of z before its rounding.  A
- * group's scale is its largest |y| / 448, 2^-126 at least (1 where all are 0),
- * and y8 is y / scale rounded to e4m3; NaN stays NaN and does not count for the
- * scale.
+ * in f32 (so a row whose squares pass f32 is normed to zeros); residual_out gets
+ * z, y and y8 the norm of z before its rounding.  A group's scale is its largest
+ * |y| / 448, 2^-126 at least (1 where all are 0), and y8 is y times 1 / scale in
+ * f32 rounded to e4m3: where y / scale is within 2^-22 of the middle between two
+ * codes, either one.  NaN stays NaN and does not count for the scale; an infinite
+ * y makes the scale infinite, its own code NaN and the group's others 0.
  */
 treewy_status treewy_add_norm(const treewy_norm* norm, cudaStream_t stream);
 
