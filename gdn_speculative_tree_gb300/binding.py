@@ -117,6 +117,8 @@ class TreewyCache(ctypes.Structure):
 
 class TreewyAttn(ctypes.Structure):
     _device = None  # of the tensors it was made from
+    _own = None     # workspaces that the binding made, by the stream whose memory each is
+    _stream = None  # of the one in the fields
     _fields_ = [(f, ctypes.c_int32) for f in ("R", "Hq", "max_nodes", "max_context", "qkv_dtype", "o_dtype")] + [
         (f, ctypes.c_int64) for f in ("T", "q_stride", "k_stride", "v_stride")] + [
         (f, ctypes.c_void_p) for f in ("node_offset", "parent", "q", "k", "v", "o", "status", "workspace")] + [
@@ -241,6 +243,19 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream
 
 
+def _own_workspace(attn, handle: int) -> None:
+    """The structure's own workspace for calls on this stream, from this stream's memory: when it is given back, nobody gets
+    it before what the stream has been told until then is done."""
+    import torch
+    if handle not in attn._own:
+        made = next(iter(attn._own.values()))
+        stream = (torch.cuda.default_stream(made.device) if handle == 0
+                  else torch.cuda.ExternalStream(handle, device=made.device))
+        with torch.cuda.stream(stream):
+            attn._own[handle] = torch.empty_like(made)
+    attn._stream, attn.workspace = handle, attn._own[handle].data_ptr()
+
+
 def _ptr(x) -> Optional[int]:
     if x is None:
         return None
@@ -313,7 +328,10 @@ def treewy_copy_slots(slots: TreewySlots, stream=None) -> None:
 def treewy_attend(attn: TreewyAttn, stream=None) -> None:
     """Softmax attention of every draft node over its context in 8 bits and its path in the draft."""
     _reachable(attn)
-    _check(load().treewy_attend(ctypes.byref(attn), _stream_handle(stream)))
+    handle = _stream_handle(stream)
+    if attn._own is not None and handle != attn._stream:
+        _own_workspace(attn, handle)
+    _check(load().treewy_attend(ctypes.byref(attn), handle))
 
 
 def treewy_append(args: TreewyAppendArgs, stream=None) -> None:
@@ -593,7 +611,9 @@ def make_attn(*, cache: TreewyCache, node_offset, q, k, v, o, status, scale: flo
               parent=None, workspace=None, flags: int = 0) -> TreewyAttn:
     """Fill a TreewyAttn: q [T][Hq][d], k and v [T][Hkv][d] (strided token rows
     allowed), o [T][Hq][d]; ``parent`` None: chains.  ``workspace`` is a uint8
-    tensor; without one, the structure gets its own, as large as it needs.
+    tensor; without one, the structure gets its own, as large as it needs, and
+    another for each further stream that it is called on.  A captured call needs
+    the structure for as long as the graph is replayed.
     """
     import torch
     T, strides, device = _rows_of_cache(cache, (("q", q), ("k", k), ("v", v)), node_offset, status,
@@ -609,6 +629,9 @@ def make_attn(*, cache: TreewyCache, node_offset, q, k, v, o, status, scale: flo
     a.scale, a.flags, a.cache = float(scale), int(flags), cache
     if workspace is None:
         workspace = torch.empty(treewy_attend_workspace(a), dtype=torch.uint8, device=q.device)
+        if q.is_cuda and workspace.numel() > 0:
+            a._stream = torch.cuda.current_stream(q.device).cuda_stream
+            a._own = {a._stream: workspace}
     a.node_offset, a.parent, a.q, a.k, a.v, a.o, a.status = map(_ptr, (node_offset, parent, q, k, v, o, status))
     a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
     a._keep, a._device = (cache._keep, node_offset, parent, q, k, v, o, status, workspace), device
