@@ -6,7 +6,8 @@ from the prompts, each request's state is forked to two samples, a draft tree
 is verified for every sample and the accepted node committed, and the next
 token is taken in without a draft.  The softmax layer norms the residual
 stream's rows into 8 bits, takes the prompts' keys and values into pages of 8
-bits, verifies the same tree against them and takes the accepted path.
+bits, verifies the same tree against them and takes the accepted path.  (What a
+prompt's own tokens attend to is left to the server's prompt attention.)
 Everything runs on one stream, without the host waiting for the device until
 the end.
 

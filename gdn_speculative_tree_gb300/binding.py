@@ -613,7 +613,8 @@ def make_attn(*, cache: TreewyCache, node_offset, q, k, v, o, status, scale: flo
     allowed), o [T][Hq][d]; ``parent`` None: chains.  ``workspace`` is a uint8
     tensor; without one, the structure gets its own, as large as it needs, and
     another for each further stream that it is called on.  A captured call needs
-    the structure for as long as the graph is replayed.
+    the structure for as long as the graph is replayed, and one replay at a time
+    uses its workspace.
     """
     import torch
     T, strides, device = _rows_of_cache(cache, (("q", q), ("k", k), ("v", v)), node_offset, status,

@@ -26,7 +26,7 @@
 //
 // Bound by HBM with long contexts: 64 tokens on 8 key heads of 128 over 8000
 // tokens 165 us, 6.4 TB/s or 0.94 of a copy; 64 tokens on 2 key heads of 256
-// over 2000 to 8000, 62.5 us (5.3 TB/s, the joining 5 of it); 256K tokens of one
+// over 2000 to 8000, 62 us (5.3 TB/s, the joining 5 of it); 256K tokens of one
 // request 57 us (4.7 TB/s).  With 16 rows by the softmax: drafts of 4 nodes over
 // 1000 to 4000 tokens of 8 heads of 128, 94 us (3.6 TB/s), a tile a chain of
 // 2,200 cycles (S, maxima, a barrier, weights).  A lone request: the launches

@@ -9,10 +9,10 @@
 // read each other's maxima, sums and outputs at the end.
 //
 // Bound by a tile's chain of loads and barriers in small calls (7 trees of 1 to
-// 15 nodes, 5 heads of 80, contexts of up to 700: 22 us; 32 with keys and values
+// 15 nodes, 5 heads of 80, contexts of up to 700: 23 us; 32 with keys and values
 // loaded one after the other), and by the loads from shared memory of the two
 // products, 128 bits for four products each, in large ones (64 requests, 16
-// heads of 128, 500 to 4000 tokens: 987 us).
+// heads of 128, 500 to 4000 tokens: 900 us).
 #include <cooperative_groups.h>
 
 #include "cache_device.cuh"

@@ -47,7 +47,7 @@ constexpr unsigned kFull = 0xffffffffu;
 
 // Drafts of at most kFewRows rows (nodes times query heads of a key head) are
 // another kernel's (attend_few.cu): 64 of them, contexts of 1000 to 4000, take
-// 94 us there at 16 rows (146 in attend_tc_kernel), 140 at 20 (137), and with
+// 94 us there at 16 rows (146 in attend_tc_kernel), 140 at 20 (131), and with
 // places for 32 of them it took 162 at 32 rows (133).
 constexpr int kFewRows = 16;
 

@@ -476,8 +476,9 @@ treewy_status treewy_copy_slots(const treewy_slots* slots, cudaStream_t stream);
  *   length      int32 [R]: tokens in the cache
  * page_len is 16, 32, 64 or 128, 1 <= d <= 256, num_pages * Hkv < 2^31.  Full
  * pages may be shared by requests (a common prefix); a page that
- * treewy_append writes to belongs to one request.  What a page holds behind
- * its tokens may be anything.
+ * treewy_append writes to belongs to one request and stands in its table once
+ * (to fork a context whose last page is partly filled, copy that page first).
+ * What a page holds behind its tokens may be anything.
  */
 typedef struct treewy_cache {
   int32_t Hkv;
