@@ -155,3 +155,21 @@ def test_small_values_of_a_row_to_what_its_terms_hold(cuda_lib, Hq):
     got = np.log(o / (1 - o))
     want = scale * np.take_along_axis(k[:, 1, 0] - k[:, 0, 0], column, axis=1)
     assert np.abs(got - want).max() <= 0.5 + 0.125
+
+
+@pytest.mark.parametrize("flags", [0, GENERIC])
+@pytest.mark.parametrize("R,G,n,octaves", [(1, 8, 100000, 17), (1, 32, 100000, 17), (160, 8, 16000, 14), (160, 32, 16000, 14),
+                                           (160, 8, 6000, 12.3), (160, 32, 6000, 12.3)])
+def test_alike_tokens_that_weigh_next_to_nothing_each(cuda_lib, R, G, n, octaves, flags):
+    """A first token with a weight of 1 and n of 2^-octaves each, which together count for about as much; values of -1 and 1.
+    The contexts are cut into pieces (one request) or not.  Alike weights are off alike: 2^-8 of n w moves the output
+    (n w - 1) / (n w + 1) by 2 n w / (n w + 1)^2, half at most, of that; and the output is rounded.  (In the piece that has
+    the first token, those of 2^-17 are within 2^-4 of themselves; it has a hundredth of them.)"""
+    keys, values = torch.zeros(n, 1, 64), torch.ones(n, 1, 64)
+    keys[0, 0, 0], values[0] = 1.0, -1.0
+    a = Shared(keys, values, R=R, N=1, G=G, scale=1.0, flags=flags)
+    a.q.zero_(), a.k.zero_(), a.v.fill_(1.0)
+    a.q[..., 0] = octaves * np.log(2)
+    nw = n * np.exp(-float(a.q[0, 0, 0]))
+    a.run()
+    assert np.abs(f64(a.o) - (nw - 1) / (nw + 1)).max() <= 2.0 ** -9 + 2.0 ** -11 + 2.0 ** -8 * abs((nw - 1) / (nw + 1)) + 2.0 ** -12
